@@ -35,6 +35,7 @@ MOE_GEMM_FWD, MOE_GEMM_DGRAD, MOE_GEMM_WGRAD = 0, 1, 2
 MOE_EPI_NONE, MOE_EPI_SWIGLU, MOE_EPI_SWIGLU_BWD, MOE_EPI_NONE_F32 = 0, 1, 2, 3
 MOE_B_GNK, MOE_B_NGK, MOE_B_SF_TILE224 = 0, 1, 2
 MOE_SF_ATOMS, MOE_SF_TILE224, MOE_SF_CANONICAL, MOE_SF_TILE224_AND_ATOMS = 0, 1, 2, 3
+MOE_TYPE_BF16, MOE_TYPE_F32 = 0, 1
 MOE_GEMM_KERNEL_AUTO, MOE_GEMM_KERNEL_1SM, MOE_GEMM_KERNEL_1SM_N128 = 0, 1, 2
 MOE_GEMM_KERNEL_PAIR, MOE_GEMM_KERNEL_PAIR_N128 = 3, 4
 (MOE_OP_ROUTE_TOPK, MOE_OP_PERMUTE, MOE_OP_GROUP_QUANTIZE, MOE_OP_GATHER_QUANTIZE, MOE_OP_GROUPED_GEMM,
@@ -51,15 +52,31 @@ EXPORTS = [
     "moe_selftest_bounded_wait", "moe_workspace_size", "mxfp8_scale_layout", "grouped_gemm_mxfp8_ex",
     "grouped_gemm_mxfp8_swiglu_quant_ex", "grouped_gemm_nvfp4_ex", "moe_hbm_fill", "mxfp8_gather_quantize_ex",
     "mxfp8_swiglu_bwd_quantize_ex", "mxfp8_group_quantize_ex",
+    "rmsnorm_residual_fwd", "rmsnorm_bwd_workspace_size", "rmsnorm_residual_bwd",
+    "adamw_plan_bytes", "adamw_plan_encode", "adamw_step",
 ]
 
 _vp, _i32, _i64, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t
+_f32 = ctypes.c_float
 
 
 class GemmOpts(ctypes.Structure):
     """moe_gemm_opts_t (include/moe.h): per-call grouped-GEMM kernel choice."""
     _fields_ = [("kernel", ctypes.c_int), ("band", ctypes.c_int), ("register_stores", ctypes.c_int),
                 ("wgrad_rows_lo", ctypes.c_int), ("wgrad_rows_hi", ctypes.c_int)]
+
+
+class AdamWTensor(ctypes.Structure):
+    """moe_adamw_tensor_t (include/moe.h)."""
+    _fields_ = [("p", _vp), ("g", _vp), ("m", _vp), ("v", _vp), ("m_scale", _vp), ("v_scale", _vp), ("copy", _vp),
+                ("n", _i64), ("rng_base", _i64), ("weight_decay", _f32)]
+
+
+class AdamWOpts(ctypes.Structure):
+    """moe_adamw_opts_t (include/moe.h)."""
+    _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
+                ("eps", ctypes.c_double), ("step", _i64), ("step_dev", _vp), ("lr_dev", _vp), ("grad_scale", _vp),
+                ("seed", ctypes.c_uint32)]
 
 
 _GEMM_KERNELS = {"auto": MOE_GEMM_KERNEL_AUTO, "1sm": MOE_GEMM_KERNEL_1SM, "1sm_n128": MOE_GEMM_KERNEL_1SM_N128,
@@ -122,6 +139,14 @@ _SIGS = {
                                         _vp, _vp]),
     "mxfp8_swiglu_bwd_quantize_ex": (_i32, [_vp, _vp, _i32, _vp, _i32, _i64, _vp, _vp, _vp, _vp, _vp, _i32, _vp,
                                             _vp]),
+    "rmsnorm_residual_fwd": (_i32, [_vp, _i32, _i64, _vp, _i32, _i64, _vp, _i32, _f32, _i64, _i32, _vp, _i64, _vp,
+                                    _i32, _i64, _vp, _vp, _vp, _i32, _vp]),
+    "rmsnorm_bwd_workspace_size": (_sz, [_i64, _i32]),
+    "rmsnorm_residual_bwd": (_i32, [_vp, _i32, _i64, _vp, _i32, _i64, _vp, _i32, _vp, _vp, _i64, _i64, _i32, _vp,
+                                    _i64, _vp, _vp, _sz, _vp]),
+    "adamw_plan_bytes": (_sz, [_i32]),
+    "adamw_plan_encode": (_i32, [_vp, _i32, _i32, _i32, _i32, _vp, ctypes.POINTER(_i64)]),
+    "adamw_step": (_i32, [_vp, _i32, _i64, _i32, _i32, _i32, _vp, _vp]),
 }
 
 
@@ -574,3 +599,194 @@ def moe_selftest_bounded_wait(timeout_ns, err, completed, stream=None):
     _check("moe_selftest_bounded_wait", lib.moe_selftest_bounded_wait(int(timeout_ns), _p(err), _p(completed),
                                                                       _stream(stream)))
 
+
+
+# --------------------------------------------- dense operators (norm, AdamW) --
+# These take any strided rows (unit stride inside a row) on the current
+# device; a tensor that does not fit the call is refused with
+# MOE_ERR_INVALID_ARG before anything is launched.
+
+_TYPES = {torch.bfloat16: MOE_TYPE_BF16, torch.float32: MOE_TYPE_F32}
+
+
+def _need(fn, ok):
+    if not ok:
+        raise MoEError(fn, MOE_ERR_INVALID_ARG)
+
+
+def _rows(fn, t, m=None, n=None, types=_TYPES):
+    """(pointer, type code, row stride) of a [m, n] matrix on the current
+    device; (None, 0, 0) for None."""
+    if t is None:
+        return None, 0, 0
+    _need(fn, t.dim() == 2 and t.is_cuda and t.dtype in types and t.get_device() == torch.cuda.current_device())
+    rows, cols = t.shape
+    _need(fn, (m is None or rows == m) and (n is None or cols == n))
+    ld = t.stride(0) if rows > 1 else max(t.stride(0), cols)
+    _need(fn, (cols == 1 or t.stride(1) == 1) and ld >= cols)
+    return t.data_ptr(), _TYPES[t.dtype], ld
+
+
+def _flat(fn, t, n, types):
+    """Pointer of a contiguous tensor of n elements on the current device."""
+    if t is None:
+        return None
+    _need(fn, t.is_cuda and t.dtype in types and t.numel() == n and t.is_contiguous() and
+          t.get_device() == torch.cuda.current_device())
+    return t.data_ptr()
+
+
+def _new(shape, dtype, like, stream):
+    """An uninitialised tensor that belongs to the stream it is used on."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=like.device)
+
+
+def rmsnorm_residual_fwd(x, w, residual=None, eps=1e-6, y=None, r=None, rstd=None, codes=None, scales=None,
+                         want_y=True, want_r=True, want_codes=False, sf_layout=MOE_SF_ATOMS, y_dtype=torch.bfloat16,
+                         stream=None):
+    """r = x + residual, y = r / sqrt(mean r^2 + eps) * w, and y's MXFP8
+    codes and scales.  See include/moe.h.  Outputs that are wanted and not
+    given are allocated; r is only written when there is a residual.
+    Returns (y, r, rstd, codes, scales), None for what is not produced."""
+    fn = "rmsnorm_residual_fwd"
+    px, tx, ldx = _rows(fn, x)
+    M, N = x.shape
+    pres, tres, ldres = _rows(fn, residual, M, N)
+    if residual is None:
+        tres = tx if r is None else _TYPES.get(r.dtype, -1)
+    elif r is None and want_r:
+        r = _new((M, N), residual.dtype, x, stream)
+    _need(fn, w.dtype in _TYPES)
+    pw = _flat(fn, w, N, _TYPES)
+    if y is None and want_y:
+        y = _new((M, N), y_dtype, x, stream)
+    if rstd is None:
+        rstd = _new((M,), torch.float32, x, stream)
+    if want_codes and codes is None:
+        rows = (M + 127) // 128 * 128 if sf_layout == MOE_SF_ATOMS else M
+        codes = _new((rows, N), torch.uint8, x, stream)
+        scales = _new((rows * (N // 32),), torch.uint8, x, stream) if scales is None else scales
+    pr, tr, ldr = _rows(fn, r, M, N)
+    _need(fn, r is None or tr == tres)
+    py, ty, ldy = _rows(fn, y, M, N)
+    pc = ps = None
+    if codes is not None or scales is not None:
+        rows = (M + 127) // 128 * 128 if sf_layout == MOE_SF_ATOMS else M
+        _need(fn, codes is not None and scales is not None)
+        pc = _flat(fn, codes, rows * N, (torch.uint8, torch.float8_e4m3fn))
+        ps = _flat(fn, scales, rows * (N // 32), (torch.uint8,))
+    _check(fn, lib.rmsnorm_residual_fwd(px, tx, ldx, pres, tres, ldres, pw, _TYPES[w.dtype], eps, M, N, pr, ldr, py,
+                                        ty, ldy, _flat(fn, rstd, M, (torch.float32,)), pc, ps, int(sf_layout),
+                                        _stream(stream)))
+    return y, r, rstd, codes, scales
+
+
+def rmsnorm_bwd_workspace_size(M: int, N: int) -> int:
+    v = int(lib.rmsnorm_bwd_workspace_size(int(M), int(N)))
+    return -1 if v == ctypes.c_size_t(-1).value else v
+
+
+def rmsnorm_residual_bwd(dy, r, w, rstd, dres=None, want_dw=True, dx=None, dw=None, ws=None, stream=None):
+    """Gradients of rmsnorm_residual_fwd: dx (of x and of the residual; + dres)
+    and dw (fp32).  See include/moe.h.  Returns (dx, dw)."""
+    fn = "rmsnorm_residual_bwd"
+    pr, tr, ldr = _rows(fn, r)
+    M, N = r.shape
+    pdy, tdy, lddy = _rows(fn, dy, M, N)
+    pdr, tdr, lddr = _rows(fn, dres, M, N)
+    _need(fn, dres is None or tdr == tr)
+    _need(fn, w.dtype in _TYPES)
+    if dx is None:
+        dx = _new((M, N), r.dtype, r, stream)
+    if want_dw and dw is None:
+        dw = _new((N,), torch.float32, r, stream)
+    if dw is not None and ws is None:
+        ws = _new((max(rmsnorm_bwd_workspace_size(M, N), 0),), torch.uint8, r, stream)
+    pdx, tdx, lddx = _rows(fn, dx, M, N)
+    _need(fn, tdx == tr)
+    nws = ws.numel() * ws.element_size() if ws is not None else 0
+    _check(fn, lib.rmsnorm_residual_bwd(pdy, tdy, lddy, pr, tr, ldr, _flat(fn, w, N, _TYPES), _TYPES[w.dtype],
+                                        _flat(fn, rstd, M, (torch.float32,)), pdr, lddr, M, N, pdx, lddx,
+                                        _flat(fn, dw, N, (torch.float32,)), _p(ws), nws, _stream(stream)))
+    return dx, dw
+
+
+class AdamWPlan:
+    """The device table of one AdamW step over a list of tensors (adamw_plan)
+    and the references that keep the tensors alive."""
+
+    def __init__(self, table, tensors, tiles, p_type, g_type, state_bits, kept):
+        self.table, self.tensors, self.tiles = table, tensors, tiles
+        self.p_type, self.g_type, self.state_bits = p_type, g_type, state_bits
+        self.kept = kept
+
+
+def adamw_plan(params, grads, ms, vs, m_scales=None, v_scales=None, copies=None, weight_decay=0.0, rng_base=None,
+               stream=None):
+    """Builds the table that adamw_step runs over (include/moe.h).  Lists of
+    contiguous tensors of equal sizes: params, grads (each list of one dtype,
+    float32 or bfloat16), first and second moments (float32; or 8 bits:
+    uint8 / float8_e4m3fn with m_scales and v_scales, float32 of ceil(n/256)),
+    optional bfloat16 copies of the params.  weight_decay: one number, or one per tensor.
+    rng_base: first counter of each tensor's rounding (8 bits; multiples of
+    256), by default one tensor after the other."""
+    fn = "adamw_plan_encode"
+    n = len(params)
+    _need(fn, n >= 1 and len(grads) == len(ms) == len(vs) == n)
+    bits = 32 if ms[0].dtype == torch.float32 else 8
+    _need(fn, (bits == 8) == (m_scales is not None) == (v_scales is not None))
+    state = (torch.float32,) if bits == 32 else (torch.uint8, torch.float8_e4m3fn)
+    pt, gt = params[0].dtype, grads[0].dtype
+    _need(fn, pt in _TYPES and gt in _TYPES)
+    for opt in (m_scales, v_scales, copies, rng_base):
+        _need(fn, opt is None or len(opt) == n)
+    wd = [float(weight_decay)] * n if isinstance(weight_decay, (int, float)) else [float(v) for v in weight_decay]
+    _need(fn, len(wd) == n)
+    arr = (AdamWTensor * n)()
+    counter = 0
+    for i in range(n):
+        e, k = arr[i], params[i].numel()
+        e.p, e.g = _flat(fn, params[i], k, (pt,)), _flat(fn, grads[i], k, (gt,))
+        e.m, e.v = _flat(fn, ms[i], k, state), _flat(fn, vs[i], k, state)
+        if bits == 8:
+            e.m_scale = _flat(fn, m_scales[i], (k + 255) // 256, (torch.float32,))
+            e.v_scale = _flat(fn, v_scales[i], (k + 255) // 256, (torch.float32,))
+        if copies is not None:
+            e.copy = _flat(fn, copies[i], k, (torch.bfloat16,))
+        e.n, e.weight_decay = k, wd[i]
+        e.rng_base = counter if rng_base is None else int(rng_base[i])
+        counter += (k + 255) // 256 * 256
+    size = int(lib.adamw_plan_bytes(n))
+    host = torch.zeros((size + 7) // 8, dtype=torch.int64)
+    tiles = _i64(0)
+    _check(fn, lib.adamw_plan_encode(ctypes.cast(arr, _vp), n, _TYPES[pt], _TYPES[gt], bits, host.data_ptr(),
+                                     ctypes.byref(tiles)))
+    table = _new(host.shape, torch.int64, params[0], stream)
+    with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream()):
+        table.copy_(host)
+    return AdamWPlan(table, n, tiles.value, _TYPES[pt], _TYPES[gt], bits,
+                     (params, grads, ms, vs, m_scales, v_scales, copies))
+
+
+def adamw_step(plan, lr, betas=(0.9, 0.999), eps=1e-8, step=1, grad_scale=None, seed=0, stream=None):
+    """One AdamW step over a plan's tensors, in place.  step: the number of
+    this step (from 1), or an int32 device tensor with the steps taken so far,
+    which the call counts up.  lr: a number or a float32 device tensor.
+    grad_scale: float32 device tensor, a factor of every gradient; when it is
+    not finite the call changes nothing.  seed: of the 8-bit rounding."""
+    fn = "adamw_step"
+    o = AdamWOpts(0.0, betas[0], betas[1], eps, 0, None, None, _flat(fn, grad_scale, 1, (torch.float32,)),
+                  int(seed) & 0xFFFFFFFF)
+    if isinstance(lr, torch.Tensor):
+        o.lr_dev = _flat(fn, lr, 1, (torch.float32,))
+    else:
+        o.lr = lr
+    if isinstance(step, torch.Tensor):
+        o.step_dev = _flat(fn, step, 1, (torch.int32,))
+    else:
+        o.step = step
+    _check(fn, lib.adamw_step(plan.table.data_ptr(), plan.tensors, plan.tiles, plan.p_type, plan.g_type,
+                              plan.state_bits, ctypes.byref(o), _stream(stream)))

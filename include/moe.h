@@ -806,6 +806,114 @@ MOE_API moe_status_t moe_selftest_bounded_wait(uint64_t timeout_ns, int32_t* err
  */
 MOE_API moe_status_t moe_hbm_fill(void* dst, size_t bytes, uint32_t value, int method, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Dense operators beside the MoE layer: the norm in front of it and the
+ * optimizer step of the weights it trains.  (The pages have no counterpart:
+ * these complete a training step around the pages' layer.)
+ *
+ * Row strides (ld*) are in elements; a stride may be larger than the row.
+ * Any stride and any element-aligned address is taken; rows whose start is a
+ * multiple of 16 bytes (address and stride) are moved in 16-byte vectors, others
+ * element by element.
+ * ------------------------------------------------------------------------ */
+typedef enum { MOE_TYPE_BF16 = 0, MOE_TYPE_F32 = 1 } moe_type_t;
+
+/*
+ * rmsnorm_residual_fwd -- r = x + res, rstd = 1 / sqrt(mean_j r_j^2 + eps),
+ * y_j = r_j rstd w_j, over M rows of N columns (1 <= N <= 32768).
+ *   x [M, N] x_type; res [M, N] res_type or NULL (r = x); w [N] w_type.
+ *   r    [M, N] res_type or NULL: the sum, for the next residual addition
+ *        and the backward pass (res_type is also r's type when res is NULL).
+ *        r may be res itself (same address and stride).
+ *   y    [M, N] y_type or NULL.
+ *   rstd [M] fp32 or NULL.
+ *   codes, scales: MXFP8 of y along its rows (both or neither).  sf_layout
+ *        MOE_SF_ATOMS (N % 128 == 0): codes [ceil128(M), N], scales
+ *        ceil128(M) * N / 32 bytes in the atom layout; the rows from M on get
+ *        zero codes and scale bytes, so the pair is an operand of
+ *        grouped_gemm_mxfp8 as it is.  MOE_SF_CANONICAL (N % 32 == 0): codes
+ *        [M, N], scales [M, N / 32].  codes 16-byte aligned.
+ * The sum, the norm and y are fp32 until stored: the norm is that of the
+ * unrounded sum, and the codes are those of the unrounded y (the scale rule
+ * above, applied to fp32 values).  M = 0 does nothing.
+ */
+MOE_API moe_status_t rmsnorm_residual_fwd(const void* x, int x_type, int64_t ldx, const void* res, int res_type,
+                                          int64_t ldres, const void* w, int w_type, float eps, int64_t M, int N,
+                                          void* r, int64_t ldr, void* y, int y_type, int64_t ldy, float* rstd,
+                                          uint8_t* codes, uint8_t* scales, int sf_layout, void* stream);
+
+/*
+ * rmsnorm_residual_bwd -- with xhat = r rstd and t = dy w:
+ *   dx = rstd (t - xhat mean_j(t_j xhat_j)) + dres,   dw = sum over rows of dy xhat.
+ * dx is the gradient of x and of res alike.  r [M, N] r_type and rstd [M] are
+ * the forward call's; dres [M, N] r_type (the gradient that reaches r from
+ * the residual stream) or NULL; dx [M, N] r_type, may be dres itself; dw [N]
+ * fp32 or NULL.  dw needs a workspace of rmsnorm_bwd_workspace_size(M, N)
+ * bytes (16-byte aligned) and is the same on every run (fixed order of
+ * addition).  M = 0 writes zeros to dw.
+ */
+MOE_API size_t rmsnorm_bwd_workspace_size(int64_t M, int N);
+MOE_API moe_status_t rmsnorm_residual_bwd(const void* dy, int dy_type, int64_t lddy, const void* r, int r_type,
+                                          int64_t ldr, const void* w, int w_type, const float* rstd,
+                                          const void* dres, int64_t lddres, int64_t M, int N, void* dx,
+                                          int64_t lddx, float* dw, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * AdamW over many tensors in one launch.
+ *   g <- grad_scale g
+ *   m <- b1 m + (1 - b1) g,   v <- b2 v + (1 - b2) g^2
+ *   p <- p (1 - lr wd) - lr / (1 - b1^t) m / (sqrt(v / (1 - b2^t)) + eps)
+ * p is fp32 or bf16 (p_type), g fp32 or bf16 (g_type), the same for all
+ * tensors of a plan; copy (may be NULL) is a bf16 copy of p that the step
+ * writes too, for fp32 masters.
+ * state_bits 32: m and v are fp32 [n].
+ * state_bits 8: m and v are E4M3 codes [n] with fp32 scales m_scale, v_scale
+ *   [ceil(n / 256)], one per 256 elements; m = code * scale and
+ *   v = (code * scale)^2.  scale = (block's largest magnitude) / 448 (a block
+ *   with none above 1e-35 is zero).  Codes are rounded down or up at random,
+ *   keeping the mean: b = mix(lo32(c) + mix(hi32(c) ^ mix(seed ^ mix(t))))
+ *   for the counter c = rng_base + index, the low 16 bits of b for m, the
+ *   high 16 for v, with mix(x): x = (x ^ x >> 16) * 0x9E3779B1,
+ *   x = (x ^ x >> 15) * 0x85EBCA77, x ^ x >> 16.  A v that is not zero is
+ *   never rounded to zero.  All zero bytes are a fresh state.
+ * The update itself uses m and v before that rounding.
+ *
+ * adamw_plan_encode (host only) writes the device table of `tensors` tensors
+ * into HOST memory of adamw_plan_bytes(tensors) bytes and its number of
+ * tiles into *tiles; the caller copies the table once to 16-byte aligned
+ * device memory and passes that to every adamw_step until an address
+ * changes.  A plan serves one step at a time (no overlapping calls).
+ */
+typedef struct {
+    void* p;
+    const void* g;
+    void* m;
+    void* v;
+    float* m_scale;       /* 8-bit states, else NULL */
+    float* v_scale;
+    void* copy;           /* bf16 [n] or NULL */
+    int64_t n;            /* elements, >= 0 */
+    int64_t rng_base;     /* 8-bit states: first counter value, a multiple of 256 */
+    float weight_decay;
+} moe_adamw_tensor_t;
+
+typedef struct {
+    double lr, beta1, beta2, eps;
+    int64_t step;             /* t >= 1, the number of this step (when step_dev is NULL) */
+    int32_t* step_dev;        /* device: steps taken so far; t = *step_dev + 1, and the call
+                                 stores t back (so a captured graph counts on) */
+    const float* lr_dev;      /* device: learning rate instead of lr, or NULL */
+    const float* grad_scale;  /* device: factor of every gradient, or NULL (1); when it is not
+                                 finite the call changes nothing, the step count included */
+    uint32_t seed;            /* of the 8-bit rounding */
+} moe_adamw_opts_t;
+
+MOE_API size_t adamw_plan_bytes(int tensors);
+MOE_API moe_status_t adamw_plan_encode(const moe_adamw_tensor_t* t, int tensors, int p_type, int g_type,
+                                       int state_bits, void* plan, int64_t* tiles);
+MOE_API moe_status_t adamw_step(void* plan, int tensors, int64_t tiles, int p_type, int g_type, int state_bits,
+                                const moe_adamw_opts_t* opts, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
