@@ -13,6 +13,7 @@ static std::mutex g_mu;
 cudaError_t gemm_set_attributes();   // gemm.cu
 cudaError_t quant_set_attributes();  // quant.cu
 cudaError_t gemm_init_driver();      // gemm.cu
+cudaError_t dense_set_attributes();  // dense.cu
 void route_scratch_forget(int device);  // route.cu
 
 int device_sm_count() {
@@ -69,6 +70,7 @@ extern "C" moe_status_t moe_init(int device) {
     if (gemm_init_driver() != cudaSuccess) return MOE_ERR_CUDA;
     if (gemm_set_attributes() != cudaSuccess) return MOE_ERR_CUDA;
     if (quant_set_attributes() != cudaSuccess) return MOE_ERR_CUDA;
+    if (dense_set_attributes() != cudaSuccess) return MOE_ERR_CUDA;
     g_sm_count[device] = sms;
     g_init[device] = true;
     return MOE_OK;

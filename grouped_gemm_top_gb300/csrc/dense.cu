@@ -1,0 +1,708 @@
+// Dense bf16 matrix products with fused epilogues: the gated feed-forward
+// projections, the linear layer, and their backward passes.
+//
+// One kernel serves the three products of a layer y = x W (x [M, K], W [K, N],
+// both row-major as they lie in memory):
+//   forward            D[M, N] = x W        A = x  (K-major),  B = W  (N-major)
+//   input gradient     D[M, K] = dy W^T     A = dy (K-major),  B = W  (K-major)
+//   weight gradient    D[K, N] = x^T dy     A = x  (M-major),  B = dy (N-major)
+// ("X-major": X is the contiguous axis.)  The tensor core takes either order
+// of both operands, so nothing is transposed or copied beforehand.
+//
+// Tile: 256 x 256 of D per CTA pair (tcgen05.mma.cta_group::2, M = 256,
+// N = 256), 64 deep per pipeline stage; CTA r of the pair holds 128 of the
+// A rows and 128 of the B rows, 32 KB per stage.  Two accumulators of 256
+// TMEM columns, so that the epilogue of one tile runs under the next tile's
+// products.  Per k-step the pair reads 64 KB for 256 x 256 x 64 products,
+// which two SMs take 256 cycles over: half the operand traffic per SM of a
+// 128 x 256 tile on one SM.
+//
+// Warps: 0 TMA, 1 MMA (of the leader CTA), 4-11 epilogue.  All waits are
+// bounded, as in the grouped GEMM kernels.
+
+#include <algorithm>
+
+#include "gemm_common.cuh"
+
+namespace moe {
+
+bool make_bf16_map(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, int64_t ld, int box_rows);  // gemm.cu
+
+namespace dense {
+
+using namespace gg;
+
+constexpr int TM = 256, TN = 256, TK = 64;      // the pair's tile and the k-step
+constexpr int HALF_BYTES = 128 * TK * 2;        // one CTA's rows of an operand per stage
+constexpr int STAGES = 6;
+constexpr int NACC = 2;
+constexpr int OFF_A = 0;
+constexpr int OFF_B = OFF_A + STAGES * HALF_BYTES;
+constexpr int OFF_BAR = OFF_B + STAGES * HALF_BYTES;      // full[S], empty[S], tfull[A], tempty[A], drain
+constexpr int NBAR = 2 * STAGES + 2 * NACC + 1;
+constexpr int OFF_MISC = OFF_BAR + 8 * NBAR;
+constexpr int SMEM_BYTES = OFF_MISC + 16 + 1024;
+static_assert(SMEM_BYTES <= 232448, "shared memory budget");
+
+// What the epilogue makes of the product v:
+//   EPI_LINEAR  z = v + bias; y = act(z) + residual (bf16; z stored when asked for)
+//   EPI_F32     y = v (fp32)
+//   EPI_GLU     columns [0, 128) of the tile are gate, [128, 256) up:
+//               h = act(gate) * up; a = [gate | up] stored when asked for
+enum { EPI_LINEAR = 0, EPI_F32 = 1, EPI_GLU = 2 };
+
+struct Params {
+    int64_t M;              // rows and columns of D (GLU: N = f)
+    int N;
+    int64_t K;
+    int64_t m_tiles;
+    int n_tiles, nk, band;
+    int up;                 // GLU: column of W where the up half begins
+    int act;
+    void* y;                // bf16, EPI_F32: fp32
+    int64_t ldy;
+    __nv_bfloat16* z;       // EPI_LINEAR: z, EPI_GLU: a; may be NULL
+    int64_t ldz;
+    const __nv_bfloat16* bias;
+    const __nv_bfloat16* res;
+    int64_t ldres;
+    int32_t* err;
+    uint64_t timeout_ns;
+};
+
+// Instruction descriptor: bf16 A and B, fp32 D, M = 256 over the pair,
+// N = 256; bits 15 and 16 say that A and B lie M- and N-major.
+template <bool A_MN, bool B_MN>
+__device__ __forceinline__ constexpr uint32_t make_idesc_pair() {
+    return (1u << 4) | (1u << 7) | (1u << 10) | (A_MN ? 1u << 15 : 0u) | (B_MN ? 1u << 16 : 0u) |
+           ((uint32_t)(TN >> 3) << 17) | ((uint32_t)(TM >> 4) << 24);
+}
+
+// Shared-memory descriptor of an operand that lies M- or N-major, 128-byte
+// swizzle: rows of 64 elements (128 bytes) of the M/N axis, one row per k;
+// 8 k-rows are 1024 bytes apart (stride offset), the next 64 elements of the
+// M/N axis `block` bytes further (leading offset).
+__device__ __forceinline__ uint64_t desc_mn_sw128(uint32_t saddr, uint32_t block) {
+    uint64_t d = 0;
+    d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);
+    d |= (uint64_t)(block >> 4) << 16;
+    d |= (uint64_t)(1024 >> 4) << 32;
+    d |= (uint64_t)1 << 46;
+    d |= (uint64_t)2 << 61;
+    return d;
+}
+template <bool MN>
+__device__ __forceinline__ uint64_t operand_desc(uint32_t saddr) {
+    if constexpr (MN) return desc_mn_sw128(saddr, 64 * TK * 2);
+    else return desc_sw128(saddr);
+}
+// 16 deeper along k: 32 bytes inside the rows, or 16 rows of 128 bytes
+template <bool MN>
+__device__ __forceinline__ constexpr uint64_t k16_step() {
+    return MN ? (16 * 128) >> 4 : 32 >> 4;
+}
+
+__device__ __forceinline__ void tc_mma2_bf16(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                             uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+__device__ __forceinline__ float act_of(float z, int act) {
+    if (act == MOE_ACT_SILU) return z * fast_sigmoid(z);
+    if (act == MOE_ACT_GELU) return 0.5f * z * (1.f + erff(z * 0.70710678118654752f));
+    if (act == MOE_ACT_RELU) return z < 0.f ? 0.f : z;
+    return z;
+}
+// d act(z) / dz
+__device__ __forceinline__ float act_slope(float z, int act) {
+    if (act == MOE_ACT_SILU) {
+        const float s = fast_sigmoid(z);
+        return s * (1.f + z * (1.f - s));
+    }
+    if (act == MOE_ACT_GELU)
+        return 0.5f * (1.f + erff(z * 0.70710678118654752f)) + z * __expf(-0.5f * z * z) * 0.39894228040143268f;
+    if (act == MOE_ACT_RELU) return z > 0.f ? 1.f : 0.f;
+    return 1.f;
+}
+
+// 32 columns of one row from / to memory; `n` of them exist.  Rows start at
+// multiples of 16 bytes and columns at multiples of 32.
+__device__ __forceinline__ void load32(const __nv_bfloat16* p, int n, float* f) {
+    if (n >= 32) {
+        load_row32(p, f);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) f[i] = i < n ? __bfloat162float(p[i]) : 0.f;
+    }
+}
+__device__ __forceinline__ void store32(__nv_bfloat16* p, int n, const float* f) {
+    if (n >= 32) {
+        store_row32(p, f);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            if (i < n) p[i] = __float2bfloat16_rn(f[i]);
+    }
+}
+__device__ __forceinline__ void store32(float* p, int n, const float* f) {
+    if (n >= 32) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            reinterpret_cast<float4*>(p)[i] = make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            if (i < n) p[i] = f[i];
+    }
+}
+
+// z -> y for 32 columns of a row, in place.
+__device__ __forceinline__ void linear32(const Params& p, int64_t row, int col, int n, float* v) {
+    if (p.bias != nullptr) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] += i < n ? __bfloat162float(p.bias[col + i]) : 0.f;
+    }
+    if (p.z != nullptr) store32(p.z + row * p.ldz + col, n, v);
+    if (p.act != MOE_ACT_NONE) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = act_of(v[i], p.act);
+    }
+    if (p.res != nullptr) {
+        float r[32];
+        load32(p.res + row * p.ldres + col, n, r);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] += r[i];
+    }
+}
+
+struct Tile {
+    int64_t mt;
+    int nt;
+};
+__device__ __forceinline__ Tile get_tile(const Params& p, int64_t t) {
+    Tile r;
+    band_decode(t, p.m_tiles, p.n_tiles, p.band, r.mt, r.nt);
+    return r;
+}
+
+template <bool A_MN, bool B_MN, int EPI>
+__global__ void __launch_bounds__(THREADS, 1)
+    k_dense_pair(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, const Params p) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_ctarank();
+    const bool leader = rank == 0;
+    const int64_t pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
+    const int64_t total = p.m_tiles * p.n_tiles;
+
+    const uint32_t bar0 = smem_u32(smem + OFF_BAR);
+    auto full_bar = [&](int s) { return bar0 + 8u * s; };
+    auto empty_bar = [&](int s) { return bar0 + 8u * (STAGES + s); };
+    auto tfull_bar = [&](int a) { return bar0 + 8u * (2 * STAGES + a); };
+    auto tempty_bar = [&](int a) { return bar0 + 8u * (2 * STAGES + NACC + a); };
+    const uint32_t drain_bar = bar0 + 8u * (2 * STAGES + 2 * NACC);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + OFF_MISC);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + OFF_MISC + 4);
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < STAGES; ++s) {
+            mbar_init(full_bar(s), 1);
+            mbar_init(empty_bar(s), 1);
+        }
+        for (int a = 0; a < NACC; ++a) {
+            mbar_init(tfull_bar(a), 1);
+            mbar_init(tempty_bar(a), 2 * EPI_WARPS);
+        }
+        mbar_init(drain_bar, 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        *abort_flag = 0;
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
+                     "r"(TMEM_COLS));
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();      // the peer's barriers are initialised and TMEM is allocated
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_slot;
+
+    if (warp == 0 && lane == 0) {
+        // ------------------------------------------------ TMA producer ----
+        uint32_t leader_full[STAGES];
+        for (int s = 0; s < STAGES; ++s) leader_full[s] = mapa(full_bar(s), 0);
+        int pend[STAGES];
+        for (int s = 0; s < STAGES; ++s) pend[s] = -1;
+        int stage = 0;
+        uint32_t phase = 0;
+        bool aborted = false;
+        for (int64_t t = pair; t < total && !aborted; t += npairs) {
+            const Tile ti = get_tile(p, t);
+            const int am = (int)(ti.mt * TM) + 128 * (int)rank;
+            const int bn = EPI == EPI_GLU ? ti.nt * 128 + p.up * (int)rank : ti.nt * TN + 128 * (int)rank;
+            for (int ks = 0; ks < p.nk; ++ks) {
+                if (!mbar_wait_cluster(empty_bar(stage), phase ^ 1u, p, abort_flag)) {
+                    aborted = true;
+                    break;
+                }
+                const int k = ks * TK;
+                // both CTAs' bytes complete on the leader's full barrier
+                const uint32_t fb = leader_full[stage];
+                if (leader) mbar_expect_tx(full_bar(stage), 4 * HALF_BYTES);
+                const uint32_t sa = smem_u32(smem + OFF_A + stage * HALF_BYTES);
+                const uint32_t sb = smem_u32(smem + OFF_B + stage * HALF_BYTES);
+                if constexpr (A_MN) {
+                    tma2_load_2d(sa, &tmA, am, k, fb);
+                    tma2_load_2d(sa + HALF_BYTES / 2, &tmA, am + 64, k, fb);
+                } else {
+                    tma2_load_2d(sa, &tmA, k, am, fb);
+                }
+                if constexpr (B_MN) {
+                    tma2_load_2d(sb, &tmB, bn, k, fb);
+                    tma2_load_2d(sb + HALF_BYTES / 2, &tmB, bn + 64, k, fb);
+                } else {
+                    tma2_load_2d(sb, &tmB, k, bn, fb);
+                }
+                pend[stage] = (int)phase;
+                if (++stage == STAGES) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+            }
+        }
+        if (aborted && leader) {
+            // the leader's full barriers count both CTAs' bytes; the follower
+            // leaves only after the closing cluster barrier, i.e. after this
+            Params q = p;
+            q.timeout_ns = 200000000ull;
+            volatile int no_abort = 0;
+            for (int s = 0; s < STAGES; ++s)
+                if (pend[s] >= 0) mbar_wait_cluster(full_bar(s), (uint32_t)pend[s], q, &no_abort);
+        }
+    } else if (warp == 1 && lane == 0 && leader) {
+        // ---------------------------------------- MMA issuer (leader) ----
+        int stage = 0, acc = 0;
+        uint32_t phase = 0, acc_phase = 0;
+        bool aborted = false, issued = false;
+        for (int64_t t = pair; t < total && !aborted; t += npairs) {
+            if (!mbar_wait_cluster(tempty_bar(acc), acc_phase ^ 1u, p, abort_flag)) break;
+            tc_fence_after();
+            const uint32_t d_tmem = tmem_base + (uint32_t)(acc * TN);
+            for (int ks = 0; ks < p.nk; ++ks) {
+                if (!mbar_wait_cluster(full_bar(stage), phase, p, abort_flag)) {
+                    aborted = true;
+                    break;
+                }
+                tc_fence_after();
+                const uint64_t adesc = operand_desc<A_MN>(smem_u32(smem + OFF_A + stage * HALF_BYTES));
+                const uint64_t bdesc = operand_desc<B_MN>(smem_u32(smem + OFF_B + stage * HALF_BYTES));
+#pragma unroll
+                for (int kk = 0; kk < TK / 16; ++kk)
+                    tc_mma2_bf16(d_tmem, adesc + k16_step<A_MN>() * kk, bdesc + k16_step<B_MN>() * kk,
+                                 make_idesc_pair<A_MN, B_MN>(), (ks | kk) != 0 ? 1u : 0u);
+                issued = true;
+                tc_commit_both(empty_bar(stage));
+                if (++stage == STAGES) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+            }
+            if (aborted) break;
+            tc_commit_both(tfull_bar(acc));
+            if (++acc == NACC) {
+                acc = 0;
+                acc_phase ^= 1u;
+            }
+        }
+        if (issued) {
+            tc_commit_local2(drain_bar);
+            Params q = p;
+            q.timeout_ns = 200000000ull;
+            volatile int no_abort = 0;
+            mbar_wait(drain_bar, 0, q, &no_abort);
+        }
+    } else if (warp >= 4) {
+        // ----------------------------------------------------- epilogue ----
+        const int ew = warp - 4;
+        const int quarter = ew & 3, half = ew >> 2;
+        int acc = 0;
+        uint32_t acc_phase = 0;
+        const uint32_t lane_base = tmem_base + ((uint32_t)(quarter * 32) << 16);
+        for (int64_t t = pair; t < total; t += npairs) {
+            const Tile ti = get_tile(p, t);
+            const int64_t row = ti.mt * TM + 128 * rank + quarter * 32 + lane;
+            if (!mbar_wait_cluster(tfull_bar(acc), acc_phase, p, abort_flag)) break;
+            tc_fence_after();
+            const uint32_t tacc = lane_base + (uint32_t)(acc * TN);
+            if constexpr (EPI == EPI_GLU) {
+                for (int c = 0; c < 2; ++c) {
+                    float g[32], u[32];
+                    const int c32 = half * 64 + 32 * c;
+                    tmem_ld32(tacc + c32, g);
+                    tmem_ld32(tacc + 128 + c32, u);
+                    const int col = ti.nt * 128 + c32;
+                    const int n = p.N - col;
+                    if (row < p.M && n > 0) {
+                        if (p.z != nullptr) {
+                            store32(p.z + row * p.ldz + col, n, g);
+                            store32(p.z + row * p.ldz + p.N + col, n, u);
+                        }
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) u[i] *= act_of(g[i], p.act);
+                        store32(static_cast<__nv_bfloat16*>(p.y) + row * p.ldy + col, n, u);
+                    }
+                }
+            } else {
+                for (int c = 0; c < 4; ++c) {
+                    float v[32];
+                    const int c32 = half * 128 + 32 * c;
+                    tmem_ld32(tacc + c32, v);
+                    const int col = ti.nt * TN + c32;
+                    const int n = p.N - col;
+                    if (row < p.M && n > 0) {
+                        if constexpr (EPI == EPI_F32) {
+                            store32(static_cast<float*>(p.y) + row * p.ldy + col, n, v);
+                        } else {
+                            linear32(p, row, col, n, v);
+                            store32(static_cast<__nv_bfloat16*>(p.y) + row * p.ldy + col, n, v);
+                        }
+                    }
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_remote(mapa(tempty_bar(acc), 0));
+            if (++acc == NACC) {
+                acc = 0;
+                acc_phase ^= 1u;
+            }
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();      // both CTAs are done with TMEM and with each other's barriers
+    tc_fence_after();
+    if (warp == 1) {
+        __syncwarp();
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(TMEM_COLS));
+    }
+}
+
+// ------------------------------------------------- elementwise backward ----
+
+// da = [dh * up * act'(gate) | dh * act(gate)] from a = [gate | up].  Bound by
+// its 10 bytes per element of h; each product is rounded to bf16 once, as the
+// operand of the two GEMMs that follow.
+__global__ void __launch_bounds__(256) k_glu_bwd(const __nv_bfloat16* __restrict__ dh, int64_t lddh,
+                                                 const __nv_bfloat16* __restrict__ a, int64_t lda, int64_t M, int f,
+                                                 int act, __nv_bfloat16* __restrict__ da, int64_t ldda) {
+    const int nvec = f / 8;
+    const int64_t n = M * nvec, stride = (int64_t)gridDim.x * blockDim.x;
+    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += stride) {
+        const int64_t row = i / nvec;
+        const int c = (int)(i - row * nvec) * 8;
+        float d[8], g[8], u[8];
+        unpack8(*reinterpret_cast<const uint4*>(dh + row * lddh + c), d);
+        unpack8(*reinterpret_cast<const uint4*>(a + row * lda + c), g);
+        unpack8(*reinterpret_cast<const uint4*>(a + row * lda + f + c), u);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float gj = g[j];
+            g[j] = d[j] * u[j] * act_slope(gj, act);
+            u[j] = d[j] * act_of(gj, act);
+        }
+        *reinterpret_cast<uint4*>(da + row * ldda + c) = pack8(g);
+        *reinterpret_cast<uint4*>(da + row * ldda + f + c) = pack8(u);
+    }
+}
+
+// dz = dy * act'(z) (bf16, when act is not MOE_ACT_NONE) and the column sums of the
+// unrounded dz over this CTA's rows, one row of partial sums per blockIdx.y.
+// A thread owns 8 columns; the CTA's 8 groups of 32 threads take every
+// eighth row and are added in order at the end.
+__global__ void __launch_bounds__(256) k_act_bwd(const __nv_bfloat16* __restrict__ dy, int64_t lddy,
+                                                 const __nv_bfloat16* __restrict__ z, int64_t ldz, int64_t M, int N,
+                                                 int act, __nv_bfloat16* __restrict__ dz, int64_t lddz,
+                                                 float* __restrict__ part) {
+    __shared__ float s_sum[8][257];
+    const int lane = threadIdx.x & 31, grp = threadIdx.x >> 5;
+    const int c = blockIdx.x * 256 + lane * 8;
+    const int n = N - c < 0 ? 0 : (N - c > 8 ? 8 : N - c);
+    float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    const int64_t step = (int64_t)gridDim.y * 8;
+    if (n > 0) {
+        for (int64_t row = (int64_t)blockIdx.y * 8 + grp; row < M; row += step) {
+            float d[8], v[8];
+            if (n == 8) {
+                unpack8(*reinterpret_cast<const uint4*>(dy + row * lddy + c), d);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) d[j] = j < n ? __bfloat162float(dy[row * lddy + c + j]) : 0.f;
+            }
+            if (act != MOE_ACT_NONE) {
+                if (n == 8) {
+                    unpack8(*reinterpret_cast<const uint4*>(z + row * ldz + c), v);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) v[j] = j < n ? __bfloat162float(z[row * ldz + c + j]) : 0.f;
+                }
+#pragma unroll
+                for (int j = 0; j < 8; ++j) d[j] *= act_slope(v[j], act);
+                if (n == 8) {
+                    *reinterpret_cast<uint4*>(dz + row * lddz + c) = pack8(d);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        if (j < n) dz[row * lddz + c + j] = __float2bfloat16_rn(d[j]);
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) sum[j] += d[j];
+        }
+    }
+    if (part == nullptr) return;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) s_sum[grp][lane * 8 + j] = sum[j];
+    __syncthreads();
+    const int col = blockIdx.x * 256 + threadIdx.x;
+    if (col < N) {
+        float t = 0.f;
+#pragma unroll
+        for (int g = 0; g < 8; ++g) t += s_sum[g][threadIdx.x];
+        part[(int64_t)blockIdx.y * N + col] = t;
+    }
+}
+
+// ----------------------------------------------------------------- host ----
+
+static int g_max_clusters = 0;
+
+static cudaLaunchConfig_t launch_cfg(int clusters, cudaStream_t stream, cudaLaunchAttribute* attr) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2 * clusters, 1, 1);
+    cfg.blockDim = dim3(THREADS, 1, 1);
+    cfg.dynamicSmemBytes = SMEM_BYTES;
+    cfg.stream = stream;
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cfg;
+}
+
+// the products that are built: forward (plain and GLU), input gradient, weight gradient (bf16, fp32)
+#define MOE_DENSE_INSTANCES(X) \
+    X(false, true, EPI_LINEAR) X(false, true, EPI_GLU) X(false, false, EPI_LINEAR) X(true, true, EPI_LINEAR) \
+    X(true, true, EPI_F32)
+
+static cudaError_t set_attributes() {
+#define X(A, B, E)                                                                                                  \
+    {                                                                                                               \
+        cudaError_t e = cudaFuncSetAttribute(k_dense_pair<A, B, E>, cudaFuncAttributeMaxDynamicSharedMemorySize,    \
+                                             SMEM_BYTES);                                                           \
+        if (e != cudaSuccess) return e;                                                                             \
+    }
+    MOE_DENSE_INSTANCES(X)
+#undef X
+    cudaLaunchAttribute attr[1];
+    cudaLaunchConfig_t cfg = launch_cfg(1024, nullptr, attr);
+    return cudaOccupancyMaxActiveClusters(&g_max_clusters, k_dense_pair<false, true, EPI_LINEAR>, &cfg);
+}
+
+// One matrix operand as it lies in memory: [rows, cols], rows of ld elements.
+struct Mat {
+    const void* p;
+    int64_t rows, cols, ld;
+};
+
+template <bool A_MN, bool B_MN, int EPI>
+static moe_status_t product(const Mat& a, const Mat& b, Params p, cudaStream_t s) {
+    CUtensorMap tmA, tmB;
+    MOE_REQUIRE(make_bf16_map(&tmA, a.p, a.rows, a.cols, a.ld, A_MN ? TK : 128) &&
+                    make_bf16_map(&tmB, b.p, b.rows, b.cols, b.ld, B_MN ? TK : 128),
+                MOE_ERR_CUDA);
+    p.m_tiles = (p.M + TM - 1) / TM;
+    p.n_tiles = EPI == EPI_GLU ? (p.N + 127) / 128 : (p.N + TN - 1) / TN;
+    p.nk = (int)((p.K + TK - 1) / TK);
+    p.band = 8;
+    p.timeout_ns = 2000000000ull;
+    const int clusters = (int)std::min<int64_t>(p.m_tiles * p.n_tiles, g_max_clusters);
+    MOE_REQUIRE(clusters > 0, MOE_ERR_NOT_INITIALIZED);
+    cudaLaunchAttribute attr[1];
+    cudaLaunchConfig_t cfg = launch_cfg(clusters, s, attr);
+    if (cudaLaunchKernelEx(&cfg, k_dense_pair<A_MN, B_MN, EPI>, tmA, tmB, p) != cudaSuccess) return MOE_ERR_CUDA;
+    MOE_CHECK_LAUNCH();
+    return MOE_OK;
+}
+
+static bool act_ok(int a) { return a >= MOE_ACT_NONE && a <= MOE_ACT_SILU; }
+// sizes the tensor maps and the tile counts hold
+static bool size_ok(int64_t v) { return v >= 1 && v <= 0x7FFFFF00LL; }
+static bool row_ok(const void* p, int64_t ld) { return moe_aligned16(p) && ld % 8 == 0; }
+
+constexpr int kActRows = 256;      // rows of partial sums of k_act_bwd at most
+static int act_parts(int64_t M) { return (int)std::min<int64_t>((M + 31) / 32, kActRows); }
+
+}  // namespace dense
+
+cudaError_t dense_set_attributes() { return dense::set_attributes(); }
+void launch_column_sum(const float* part, int P, int N, float* out, cudaStream_t s);      // norm.cu
+
+}  // namespace moe
+
+using namespace moe;
+using namespace moe::dense;
+
+extern "C" moe_status_t linear_fwd(const void* x, int64_t ldx, const void* w, int64_t ldw, const void* bias, int act,
+                                   const void* res, int64_t ldres, int64_t M, int N, int64_t K, void* y, int64_t ldy,
+                                   void* z, int64_t ldz, int32_t* err, void* stream) {
+    MOE_REQUIRE(M >= 0 && N >= 1 && K >= 1 && act_ok(act), MOE_ERR_INVALID_ARG);
+    MOE_REQUIRE(ldx >= K && ldw >= N && ldy >= N && (!res || ldres >= N) && (!z || ldz >= N), MOE_ERR_INVALID_ARG);
+    MOE_REQUIRE(M <= 0x7FFFFF00LL && size_ok(N) && size_ok(K), MOE_ERR_UNSUPPORTED);
+    if (M == 0) return MOE_OK;
+    MOE_REQUIRE(x && w && y, MOE_ERR_INVALID_ARG);
+    MOE_REQUIRE(row_ok(x, ldx) && row_ok(w, ldw) && row_ok(y, ldy) && (!res || row_ok(res, ldres)) &&
+                    (!z || row_ok(z, ldz)) && reinterpret_cast<uintptr_t>(bias) % 2 == 0,
+                MOE_ERR_ALIGNMENT);
+    MOE_REQUIRE(device_initialized(), MOE_ERR_NOT_INITIALIZED);
+    dense::Params p{};
+    p.M = M, p.N = N, p.K = K, p.act = act;
+    p.y = y, p.ldy = ldy, p.z = static_cast<__nv_bfloat16*>(z), p.ldz = ldz;
+    p.bias = static_cast<const __nv_bfloat16*>(bias);
+    p.res = static_cast<const __nv_bfloat16*>(res), p.ldres = ldres;
+    p.err = err;
+    return product<false, true, EPI_LINEAR>({x, M, K, ldx}, {w, K, N, ldw}, p, (cudaStream_t)stream);
+}
+
+// D[M, N] = dy W^T and D = x^T dy with plain stores
+static moe_status_t input_grad(const void* dy, int64_t lddy, const void* w, int64_t ldw, int64_t M, int N, int64_t K,
+                               void* dx, int64_t lddx, int32_t* err, cudaStream_t s) {
+    dense::Params p{};
+    p.M = M, p.N = (int)K, p.K = N, p.act = MOE_ACT_NONE, p.y = dx, p.ldy = lddx, p.err = err;
+    return product<false, false, EPI_LINEAR>({dy, M, N, lddy}, {w, K, N, ldw}, p, s);
+}
+static moe_status_t weight_grad(const void* x, int64_t ldx, const void* dy, int64_t lddy, int64_t M, int N, int64_t K,
+                                void* dw, int dw_type, int64_t lddw, int32_t* err, cudaStream_t s) {
+    if (M == 0) {
+        const size_t e = dw_type == MOE_TYPE_F32 ? 4 : 2;
+        return cudaMemset2DAsync(dw, lddw * e, 0, N * e, K, s) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+    }
+    dense::Params p{};
+    p.M = K, p.N = N, p.K = M, p.act = MOE_ACT_NONE, p.y = dw, p.ldy = lddw, p.err = err;
+    if (dw_type == MOE_TYPE_F32) return product<true, true, EPI_F32>({x, M, K, ldx}, {dy, M, N, lddy}, p, s);
+    return product<true, true, EPI_LINEAR>({x, M, K, ldx}, {dy, M, N, lddy}, p, s);
+}
+
+static size_t dz_bytes(int64_t M, int N) { return ((size_t)M * ((N + 7) / 8 * 8) * 2 + 255) / 256 * 256; }
+
+extern "C" size_t linear_bwd_workspace_size(int64_t M, int N) {
+    if (M < 0 || M > 0x7FFFFF00LL || !size_ok(N)) return (size_t)-1;
+    return dz_bytes(M, N) + (size_t)act_parts(M) * N * sizeof(float);
+}
+
+extern "C" moe_status_t linear_bwd(const void* dy, int64_t lddy, const void* x, int64_t ldx, const void* w, int64_t ldw,
+                                   const void* z, int64_t ldz, int act, int64_t M, int N, int64_t K, void* dx,
+                                   int64_t lddx, void* dw, int dw_type, int64_t lddw, float* dbias, void* ws,
+                                   size_t ws_bytes, int32_t* err, void* stream) {
+    MOE_REQUIRE(M >= 0 && N >= 1 && K >= 1 && act_ok(act), MOE_ERR_INVALID_ARG);
+    MOE_REQUIRE(dw_type == MOE_TYPE_BF16 || dw_type == MOE_TYPE_F32, MOE_ERR_INVALID_ARG);
+    const bool with_z = act != MOE_ACT_NONE;
+    MOE_REQUIRE(lddy >= N && (!with_z || ldz >= N) && (!dx || (ldw >= N && lddx >= K)) &&
+                    (!dw || (ldx >= K && lddw >= N)),
+                MOE_ERR_INVALID_ARG);
+    MOE_REQUIRE(M <= 0x7FFFFF00LL && size_ok(N) && size_ok(K), MOE_ERR_UNSUPPORTED);
+    MOE_REQUIRE(dx || dw || dbias, MOE_ERR_INVALID_ARG);
+    MOE_REQUIRE(M == 0 || (dy && (!with_z || z) && (!dx || w) && (!dw || x)), MOE_ERR_INVALID_ARG);
+    MOE_REQUIRE(row_ok(dy, lddy) && (!with_z || row_ok(z, ldz)) && (!dx || (row_ok(w, ldw) && row_ok(dx, lddx))) &&
+                    (!dw || (row_ok(x, ldx) && row_ok(dw, lddw))) && reinterpret_cast<uintptr_t>(dbias) % 4 == 0 &&
+                    moe_aligned16(ws),
+                MOE_ERR_ALIGNMENT);
+    const bool need_ws = M > 0 && (dbias || (with_z && (dx || dw)));
+    MOE_REQUIRE(!need_ws || (ws && ws_bytes >= linear_bwd_workspace_size(M, N)), MOE_ERR_WORKSPACE);
+    MOE_REQUIRE(device_initialized(), MOE_ERR_NOT_INITIALIZED);
+    cudaStream_t s = (cudaStream_t)stream;
+    const void* g = dy;
+    int64_t ldg = lddy;
+    float* part = need_ws && dbias ? reinterpret_cast<float*>(static_cast<char*>(ws) + dz_bytes(M, N)) : nullptr;
+    if (need_ws) {
+        __nv_bfloat16* dz = static_cast<__nv_bfloat16*>(ws);
+        const int64_t lddz = (N + 7) / 8 * 8;
+        k_act_bwd<<<dim3((N + 255) / 256, act_parts(M)), 256, 0, s>>>(
+            static_cast<const __nv_bfloat16*>(dy), lddy, static_cast<const __nv_bfloat16*>(z), ldz, M, N, act, dz,
+            lddz, part);
+        MOE_CHECK_LAUNCH();
+        if (with_z) g = dz, ldg = lddz;
+    }
+    if (dbias) {
+        launch_column_sum(part, M > 0 ? act_parts(M) : 0, N, dbias, s);
+        MOE_CHECK_LAUNCH();
+    }
+    if (dx && M > 0) {
+        const moe_status_t st = input_grad(g, ldg, w, ldw, M, N, K, dx, lddx, err, s);
+        if (st != MOE_OK) return st;
+    }
+    if (dw) return weight_grad(x, ldx, g, ldg, M, N, K, dw, dw_type, lddw, err, s);
+    return MOE_OK;
+}
+
+extern "C" moe_status_t gated_ffn_fwd(const void* x, int64_t ldx, const void* w1, int64_t ldw, int act, int64_t M,
+                                      int f, int64_t d, void* h, int64_t ldh, void* a, int64_t lda, int32_t* err,
+                                      void* stream) {
+    MOE_REQUIRE(M >= 0 && f >= 1 && d >= 1 && act_ok(act), MOE_ERR_INVALID_ARG);
+    MOE_REQUIRE(ldx >= d && ldw >= 2 * (int64_t)f && ldh >= f && (!a || lda >= 2 * (int64_t)f), MOE_ERR_INVALID_ARG);
+    MOE_REQUIRE(f % 8 == 0 && M <= 0x7FFFFF00LL && f <= 0x3FFFFF00 && size_ok(d), MOE_ERR_UNSUPPORTED);
+    if (M == 0) return MOE_OK;
+    MOE_REQUIRE(x && w1 && h, MOE_ERR_INVALID_ARG);
+    MOE_REQUIRE(row_ok(x, ldx) && row_ok(w1, ldw) && row_ok(h, ldh) && (!a || row_ok(a, lda)), MOE_ERR_ALIGNMENT);
+    MOE_REQUIRE(device_initialized(), MOE_ERR_NOT_INITIALIZED);
+    dense::Params p{};
+    p.M = M, p.N = f, p.K = d, p.act = act, p.up = f;
+    p.y = h, p.ldy = ldh, p.z = static_cast<__nv_bfloat16*>(a), p.ldz = lda;
+    p.err = err;
+    return product<false, true, EPI_GLU>({x, M, d, ldx}, {w1, d, 2 * (int64_t)f, ldw}, p, (cudaStream_t)stream);
+}
+
+extern "C" moe_status_t gated_ffn_bwd(const void* dh, int64_t lddh, const void* a, int64_t lda, const void* x,
+                                      int64_t ldx, const void* w1, int64_t ldw, int act, int64_t M, int f, int64_t d,
+                                      void* da, int64_t ldda, void* dx, int64_t lddx, void* dw1, int dw_type,
+                                      int64_t lddw, int32_t* err, void* stream) {
+    MOE_REQUIRE(M >= 0 && f >= 1 && d >= 1 && act_ok(act), MOE_ERR_INVALID_ARG);
+    MOE_REQUIRE(dw_type == MOE_TYPE_BF16 || dw_type == MOE_TYPE_F32, MOE_ERR_INVALID_ARG);
+    const int64_t f2 = 2 * (int64_t)f;
+    MOE_REQUIRE(lddh >= f && lda >= f2 && ldda >= f2 && (!dx || (ldw >= f2 && lddx >= d)) &&
+                    (!dw1 || (ldx >= d && lddw >= f2)),
+                MOE_ERR_INVALID_ARG);
+    MOE_REQUIRE(f % 8 == 0 && M <= 0x7FFFFF00LL && f <= 0x3FFFFF00 && size_ok(d), MOE_ERR_UNSUPPORTED);
+    MOE_REQUIRE(M == 0 || (dh && a && da && (!dx || w1) && (!dw1 || x)), MOE_ERR_INVALID_ARG);
+    MOE_REQUIRE(row_ok(dh, lddh) && row_ok(a, lda) && row_ok(da, ldda) &&
+                    (!dx || (row_ok(w1, ldw) && row_ok(dx, lddx))) &&
+                    (!dw1 || (row_ok(x, ldx) && row_ok(dw1, lddw))),
+                MOE_ERR_ALIGNMENT);
+    MOE_REQUIRE(device_initialized(), MOE_ERR_NOT_INITIALIZED);
+    const int sms = device_sm_count();
+    MOE_REQUIRE(sms > 0, MOE_ERR_NOT_INITIALIZED);
+    cudaStream_t s = (cudaStream_t)stream;
+    if (M > 0) {
+        const int64_t n = M * (f / 8);
+        k_glu_bwd<<<(unsigned)std::min<int64_t>((n + 255) / 256, (int64_t)sms * 8), 256, 0, s>>>(
+            static_cast<const __nv_bfloat16*>(dh), lddh, static_cast<const __nv_bfloat16*>(a), lda, M, f, act,
+            static_cast<__nv_bfloat16*>(da), ldda);
+        MOE_CHECK_LAUNCH();
+    }
+    if (dx && M > 0) {
+        const moe_status_t st = input_grad(da, ldda, w1, ldw, M, 2 * f, d, dx, lddx, err, s);
+        if (st != MOE_OK) return st;
+    }
+    if (dw1) return weight_grad(x, ldx, da, ldda, M, 2 * f, d, dw1, dw_type, lddw, err, s);
+    return MOE_OK;
+}

@@ -584,6 +584,19 @@ static bool make_d_map(CUtensorMap* m, void* base, int64_t rows, int N) {
     return r == CUDA_SUCCESS;
 }
 
+// bf16 matrix [rows, cols] with rows of ld elements (16-byte aligned), boxes
+// of 64 columns x box_rows rows, 128-byte swizzle; what a box holds outside
+// the matrix is zero.
+bool make_bf16_map(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, int64_t ld, int box_rows) {
+    cuuint64_t gdim[2] = {(cuuint64_t)cols, (cuuint64_t)rows}, gstr[1] = {(cuuint64_t)ld * 2};
+    cuuint32_t box[2] = {64, (cuuint32_t)box_rows}, estr[2] = {1, 1};
+    if (g_encode == nullptr) return false;
+    CUresult r = g_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), gdim, gstr, box, estr,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS;
+}
+
 // rank-2/3 uint8 tensor map, 128x128 boxes, 128-byte swizzle
 static bool make_map(CUtensorMap* m, const void* base, int rank, const uint64_t* dims, const uint64_t* strides_bytes,
                      int box_rows = 128) {

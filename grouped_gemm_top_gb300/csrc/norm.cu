@@ -380,6 +380,12 @@ static void launch_bwd(const BwdParams& p, const Shape& s, int groups, cudaStrea
 }
 
 }  // namespace norm
+
+// out[c] = sum over the P rows of part [P, N], in a fixed order; zeros for P = 0
+void launch_column_sum(const float* part, int P, int N, float* out, cudaStream_t s) {
+    norm::k_dw_sum<<<(N + 31) / 32, 1024, 0, s>>>(part, P, N, out);
+}
+
 }  // namespace moe
 
 extern "C" moe_status_t rmsnorm_residual_fwd(const void* x, int x_type, int64_t ldx, const void* res, int res_type,
@@ -471,7 +477,7 @@ extern "C" moe_status_t rmsnorm_residual_bwd(const void* dy, int dy_type, int64_
         MOE_CHECK_LAUNCH();
     }
     if (dw) {
-        k_dw_sum<<<(N + 31) / 32, 1024, 0, st>>>(static_cast<const float*>(ws), M > 0 ? groups : 0, N, dw);
+        launch_column_sum(static_cast<const float*>(ws), M > 0 ? groups : 0, N, dw, st);
         MOE_CHECK_LAUNCH();
     }
     return MOE_OK;

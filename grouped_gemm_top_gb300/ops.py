@@ -36,6 +36,7 @@ MOE_EPI_NONE, MOE_EPI_SWIGLU, MOE_EPI_SWIGLU_BWD, MOE_EPI_NONE_F32 = 0, 1, 2, 3
 MOE_B_GNK, MOE_B_NGK, MOE_B_SF_TILE224 = 0, 1, 2
 MOE_SF_ATOMS, MOE_SF_TILE224, MOE_SF_CANONICAL, MOE_SF_TILE224_AND_ATOMS = 0, 1, 2, 3
 MOE_TYPE_BF16, MOE_TYPE_F32 = 0, 1
+MOE_ACT_NONE, MOE_ACT_RELU, MOE_ACT_GELU, MOE_ACT_SILU = range(4)
 MOE_GEMM_KERNEL_AUTO, MOE_GEMM_KERNEL_1SM, MOE_GEMM_KERNEL_1SM_N128 = 0, 1, 2
 MOE_GEMM_KERNEL_PAIR, MOE_GEMM_KERNEL_PAIR_N128 = 3, 4
 (MOE_OP_ROUTE_TOPK, MOE_OP_PERMUTE, MOE_OP_GROUP_QUANTIZE, MOE_OP_GATHER_QUANTIZE, MOE_OP_GROUPED_GEMM,
@@ -54,6 +55,7 @@ EXPORTS = [
     "mxfp8_swiglu_bwd_quantize_ex", "mxfp8_group_quantize_ex",
     "rmsnorm_residual_fwd", "rmsnorm_bwd_workspace_size", "rmsnorm_residual_bwd",
     "adamw_plan_bytes", "adamw_plan_encode", "adamw_step",
+    "linear_fwd", "linear_bwd_workspace_size", "linear_bwd", "gated_ffn_fwd", "gated_ffn_bwd",
 ]
 
 _vp, _i32, _i64, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t
@@ -144,6 +146,14 @@ _SIGS = {
     "rmsnorm_bwd_workspace_size": (_sz, [_i64, _i32]),
     "rmsnorm_residual_bwd": (_i32, [_vp, _i32, _i64, _vp, _i32, _i64, _vp, _i32, _vp, _vp, _i64, _i64, _i32, _vp,
                                     _i64, _vp, _vp, _sz, _vp]),
+    "linear_fwd": (_i32, [_vp, _i64, _vp, _i64, _vp, _i32, _vp, _i64, _i64, _i32, _i64, _vp, _i64, _vp, _i64, _vp,
+                          _vp]),
+    "linear_bwd_workspace_size": (_sz, [_i64, _i32]),
+    "linear_bwd": (_i32, [_vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _i32, _i64, _i32, _i64, _vp, _i64, _vp, _i32,
+                          _i64, _vp, _vp, _sz, _vp, _vp]),
+    "gated_ffn_fwd": (_i32, [_vp, _i64, _vp, _i64, _i32, _i64, _i32, _i64, _vp, _i64, _vp, _i64, _vp, _vp]),
+    "gated_ffn_bwd": (_i32, [_vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _i32, _i64, _i32, _i64, _vp, _i64, _vp,
+                             _i64, _vp, _i32, _i64, _vp, _vp]),
     "adamw_plan_bytes": (_sz, [_i32]),
     "adamw_plan_encode": (_i32, [_vp, _i32, _i32, _i32, _i32, _vp, ctypes.POINTER(_i64)]),
     "adamw_step": (_i32, [_vp, _i32, _i64, _i32, _i32, _i32, _vp, _vp]),
@@ -712,6 +722,120 @@ def rmsnorm_residual_bwd(dy, r, w, rstd, dres=None, want_dw=True, dx=None, dw=No
                                         _flat(fn, rstd, M, (torch.float32,)), pdr, lddr, M, N, pdx, lddx,
                                         _flat(fn, dw, N, (torch.float32,)), _p(ws), nws, _stream(stream)))
     return dx, dw
+
+
+_BF16 = (torch.bfloat16,)
+_ACTS = {"none": MOE_ACT_NONE, "relu": MOE_ACT_RELU, "gelu": MOE_ACT_GELU, "silu": MOE_ACT_SILU}
+
+
+def _act(fn, act):
+    a = _ACTS.get(act, act)
+    _need(fn, isinstance(a, int))
+    return a
+
+
+def _new_rows(m, n, dtype, like, stream):
+    """An uninitialised [m, n] whose rows start at multiples of 16 bytes."""
+    t = _new((m, (n + 7) // 8 * 8), dtype, like, stream)
+    return t if n % 8 == 0 else t[:, :n]
+
+
+def linear_fwd(x, w, bias=None, act="none", residual=None, y=None, z=None, want_z=False, err=None, stream=None):
+    """z = x w + bias, y = act(z) + residual (bf16; act "none", "relu", "gelu"
+    or "silu").  See include/moe.h.  Rows of every matrix start at multiples of 16 bytes.
+    Returns y, or (y, z) when z is asked for."""
+    fn = "linear_fwd"
+    px, _, ldx = _rows(fn, x, types=_BF16)
+    M, K = x.shape
+    pw, _, ldw = _rows(fn, w, K, types=_BF16)
+    N = w.shape[1]
+    y = y if y is not None else _new_rows(M, N, torch.bfloat16, x, stream)
+    if want_z and z is None:
+        z = _new_rows(M, N, torch.bfloat16, x, stream)
+    pr, _, ldr = _rows(fn, residual, M, N, _BF16)
+    py, _, ldy = _rows(fn, y, M, N, _BF16)
+    pz, _, ldz = _rows(fn, z, M, N, _BF16)
+    _check(fn, lib.linear_fwd(px, ldx, pw, ldw, _flat(fn, bias, N, _BF16), _act(fn, act), pr, ldr, M, N, K, py, ldy,
+                              pz, ldz, _p(err), _stream(stream)))
+    return y if z is None else (y, z)
+
+
+def linear_bwd_workspace_size(M: int, N: int) -> int:
+    v = int(lib.linear_bwd_workspace_size(int(M), int(N)))
+    return -1 if v == ctypes.c_size_t(-1).value else v
+
+
+def linear_bwd(dy, x, w, z=None, act="none", want_dx=True, want_dw=True, want_dbias=False, dx=None, dw=None,
+               dbias=None, dw_dtype=torch.bfloat16, ws=None, err=None, stream=None):
+    """Gradients of linear_fwd: dx, dw (bfloat16 or float32) and dbias
+    (float32), those that are wanted or given.  See include/moe.h.  Returns
+    (dx, dw, dbias)."""
+    fn = "linear_bwd"
+    act = _act(fn, act)
+    pdy, _, lddy = _rows(fn, dy, types=_BF16)
+    M, N = dy.shape
+    px, _, ldx = _rows(fn, x, M, types=_BF16)
+    K = x.shape[1]
+    pw, _, ldw = _rows(fn, w, K, N, _BF16)
+    pz, _, ldz = _rows(fn, z, M, N, _BF16)
+    if want_dx and dx is None:
+        dx = _new_rows(M, K, torch.bfloat16, x, stream)
+    if want_dw and dw is None:
+        dw = _new_rows(K, N, dw_dtype, x, stream)
+    if want_dbias and dbias is None:
+        dbias = _new((N,), torch.float32, x, stream)
+    if ws is None and (dbias is not None or act != MOE_ACT_NONE):
+        ws = _new((max(linear_bwd_workspace_size(M, N), 0),), torch.uint8, x, stream)
+    pdx, _, lddx = _rows(fn, dx, M, K, _BF16)
+    pdw, tdw, lddw = _rows(fn, dw, K, N)
+    nws = ws.numel() * ws.element_size() if ws is not None else 0
+    _check(fn, lib.linear_bwd(pdy, lddy, px, ldx, pw, ldw, pz, ldz, act, M, N, K, pdx, lddx, pdw, tdw, lddw,
+                              _flat(fn, dbias, N, (torch.float32,)), _p(ws), nws, _p(err), _stream(stream)))
+    return dx, dw, dbias
+
+
+def gated_ffn_fwd(x, w1, act="silu", h=None, a=None, want_a=False, err=None, stream=None):
+    """[gate | up] = x w1, h = act(gate) * up in one kernel (bf16).  See
+    include/moe.h.  Returns h, or (h, a) when a = [gate | up] is asked for."""
+    fn = "gated_ffn_fwd"
+    px, _, ldx = _rows(fn, x, types=_BF16)
+    M, d = x.shape
+    pw, _, ldw = _rows(fn, w1, d, types=_BF16)
+    _need(fn, w1.shape[1] % 2 == 0)
+    f = w1.shape[1] // 2
+    h = h if h is not None else _new_rows(M, f, torch.bfloat16, x, stream)
+    if want_a and a is None:
+        a = _new_rows(M, 2 * f, torch.bfloat16, x, stream)
+    ph, _, ldh = _rows(fn, h, M, f, _BF16)
+    pa, _, lda = _rows(fn, a, M, 2 * f, _BF16)
+    _check(fn, lib.gated_ffn_fwd(px, ldx, pw, ldw, _act(fn, act), M, f, d, ph, ldh, pa, lda, _p(err),
+                                 _stream(stream)))
+    return h if a is None else (h, a)
+
+
+def gated_ffn_bwd(dh, a, x, w1, act="silu", want_dx=True, want_dw=True, dx=None, dw1=None, da=None,
+                  dw_dtype=torch.bfloat16, err=None, stream=None):
+    """Gradients of gated_ffn_fwd from the kept a: dx and dw1 (bfloat16 or
+    float32); da [M, 2f] is written on the way (may be a itself).  See
+    include/moe.h.  Returns (dx, dw1)."""
+    fn = "gated_ffn_bwd"
+    pdh, _, lddh = _rows(fn, dh, types=_BF16)
+    M, f = dh.shape
+    pa, _, lda = _rows(fn, a, M, 2 * f, _BF16)
+    px, _, ldx = _rows(fn, x, M, types=_BF16)
+    d = x.shape[1]
+    pw, _, ldw = _rows(fn, w1, d, 2 * f, _BF16)
+    da = da if da is not None else _new_rows(M, 2 * f, torch.bfloat16, x, stream)
+    if want_dx and dx is None:
+        dx = _new_rows(M, d, torch.bfloat16, x, stream)
+    if want_dw and dw1 is None:
+        dw1 = _new_rows(d, 2 * f, dw_dtype, x, stream)
+    pda, _, ldda = _rows(fn, da, M, 2 * f, _BF16)
+    pdx, _, lddx = _rows(fn, dx, M, d, _BF16)
+    pdw, tdw, lddw = _rows(fn, dw1, d, 2 * f)
+    _check(fn, lib.gated_ffn_bwd(pdh, lddh, pa, lda, px, ldx, pw, ldw, _act(fn, act), M, f, d, pda, ldda, pdx, lddx,
+                                 pdw, tdw, lddw, _p(err), _stream(stream)))
+    return dx, dw1
 
 
 class AdamWPlan:

@@ -807,18 +807,20 @@ MOE_API moe_status_t moe_selftest_bounded_wait(uint64_t timeout_ns, int32_t* err
 MOE_API moe_status_t moe_hbm_fill(void* dst, size_t bytes, uint32_t value, int method, void* stream);
 
 /* ------------------------------------------------------------------------
- * Dense operators beside the MoE layer: the norm in front of it and the
- * optimizer step of the weights it trains.  (The pages have no counterpart:
- * these complete a training step around the pages' layer.)
+ * Dense operators beside the MoE layer: the norm in front of it, bf16
+ * feed-forward and linear layers next to it, and the optimizer step of the
+ * weights.  (The pages have no counterpart: these complete a training step
+ * around the pages' layer.)
  *
  * Row strides (ld*) are in elements; a stride may be larger than the row.
- * Any stride and any element-aligned address is taken; rows whose start is a
- * multiple of 16 bytes (address and stride) are moved in 16-byte vectors, others
- * element by element.
  * ------------------------------------------------------------------------ */
 typedef enum { MOE_TYPE_BF16 = 0, MOE_TYPE_F32 = 1 } moe_type_t;
 
 /*
+ * The norm takes any stride and any element-aligned address; rows whose start
+ * is a multiple of 16 bytes (address and stride) are moved in 16-byte vectors,
+ * others element by element.
+ *
  * rmsnorm_residual_fwd -- r = x + res, rstd = 1 / sqrt(mean_j r_j^2 + eps),
  * y_j = r_j rstd w_j, over M rows of N columns (1 <= N <= 32768).
  *   x [M, N] x_type; res [M, N] res_type or NULL (r = x); w [N] w_type.
@@ -857,6 +859,64 @@ MOE_API moe_status_t rmsnorm_residual_bwd(const void* dy, int dy_type, int64_t l
                                           int64_t ldr, const void* w, int w_type, const float* rstd,
                                           const void* dres, int64_t lddres, int64_t M, int N, void* dx,
                                           int64_t lddx, float* dw, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Dense bf16 layers on the tensor cores, fp32 accumulation.  All matrices are
+ * row-major bf16 with rows that start at multiples of 16 bytes (base address
+ * 16-byte aligned, strides multiples of 8 elements; the TMA's rule); the
+ * sizes M, N and K themselves are free.  What lies between a row's end
+ * and the next row's start is neither used nor written.  err (may be NULL)
+ * receives MOE_ERR_DEVICE_TIMEOUT if a bounded wait inside a kernel gives up.
+ */
+typedef enum { MOE_ACT_NONE = 0, MOE_ACT_RELU = 1, MOE_ACT_GELU = 2, MOE_ACT_SILU = 3 } moe_act_t;  /* GELU: z Phi(z) */
+
+/*
+ * linear_fwd -- z = x w + bias, y = act(z) + res.
+ *   x [M, K], w [K, N], bias [N] bf16 or NULL, res [M, N] or NULL (may be y
+ *   itself), y [M, N], z [M, N] or NULL (kept for the backward pass).
+ * Everything between the product and the stores is fp32; y and z are each
+ * rounded once.  M = 0 does nothing.
+ */
+MOE_API moe_status_t linear_fwd(const void* x, int64_t ldx, const void* w, int64_t ldw, const void* bias, int act,
+                                const void* res, int64_t ldres, int64_t M, int N, int64_t K, void* y, int64_t ldy,
+                                void* z, int64_t ldz, int32_t* err, void* stream);
+
+/*
+ * linear_bwd -- dz = dy act'(z), dx = dz w^T, dw = x^T dz, dbias = sum of dz's
+ * rows.  (The gradient of res is dy itself.)  z is the forward call's, NULL
+ * with MOE_ACT_NONE.  dx [M, K], dw [K, N] (dw_type) and dbias [N] fp32 may
+ * each be NULL.  dz is rounded to bf16, the operand type of the two products,
+ * once; dbias is the sum of the unrounded dz, in a fixed order.  ws: at least
+ * linear_bwd_workspace_size(M, N) bytes, 16-byte aligned, unless act is
+ * MOE_ACT_NONE and dbias NULL.  M = 0 writes zeros to dw and dbias.
+ */
+MOE_API size_t linear_bwd_workspace_size(int64_t M, int N);
+MOE_API moe_status_t linear_bwd(const void* dy, int64_t lddy, const void* x, int64_t ldx, const void* w, int64_t ldw,
+                                const void* z, int64_t ldz, int act, int64_t M, int N, int64_t K, void* dx,
+                                int64_t lddx, void* dw, int dw_type, int64_t lddw, float* dbias, void* ws,
+                                size_t ws_bytes, int32_t* err, void* stream);
+
+/*
+ * gated_ffn_fwd -- [gate | up] = x w1, h = act(gate) * up in one kernel.
+ *   x [M, d], w1 [d, 2f] (columns [gate | up], f % 8 == 0: both halves start
+ *   at a multiple of 16 bytes), h [M, f], a [M, 2f] = [gate | up] or NULL (kept for the
+ *   backward pass).  h is that of the unrounded gate and up.  M = 0 does
+ *   nothing.
+ */
+MOE_API moe_status_t gated_ffn_fwd(const void* x, int64_t ldx, const void* w1, int64_t ldw, int act, int64_t M,
+                                   int f, int64_t d, void* h, int64_t ldh, void* a, int64_t lda, int32_t* err,
+                                   void* stream);
+
+/*
+ * gated_ffn_bwd -- da = [dh up act'(gate) | dh act(gate)] from the forward
+ * call's a, dx = da w1^T, dw1 = x^T da.  da [M, 2f] is written (bf16, the
+ * operand type of the two products) and may be a itself; dx [M, d] and dw1 [d, 2f] (dw_type) may each
+ * be NULL.  M = 0 writes zeros to dw1.
+ */
+MOE_API moe_status_t gated_ffn_bwd(const void* dh, int64_t lddh, const void* a, int64_t lda, const void* x,
+                                   int64_t ldx, const void* w1, int64_t ldw, int act, int64_t M, int f, int64_t d,
+                                   void* da, int64_t ldda, void* dx, int64_t lddx, void* dw1, int dw_type,
+                                   int64_t lddw, int32_t* err, void* stream);
 
 /*
  * AdamW over many tensors in one launch.

@@ -101,3 +101,64 @@ def test_adamw(ops):
         assert step(**k) == inv, k
     for k in (dict(plan=ctypes.c_void_p(4104)), dict(step_dev=4097), dict(lr_dev=4098), dict(grad_scale=4097)):
         assert step(**k) == ali, k
+
+
+def lin_fwd(ops, **k):
+    a = dict(x=P, ldx=64, w=P, ldw=48, bias=P, act=1, res=P, ldres=48, M=16, N=48, K=64, y=P, ldy=48, z=P, ldz=48)
+    a.update(k)
+    return ops.lib.linear_fwd(*a.values(), NULL, NULL)
+
+
+def lin_bwd(ops, **k):
+    a = dict(dy=P, lddy=48, x=P, ldx=64, w=P, ldw=48, z=P, ldz=48, act=3, M=16, N=48, K=64, dx=P, lddx=64, dw=P, dwt=0,
+             lddw=48, db=P, ws=P, wsb=1 << 30)
+    a.update(k)
+    return ops.lib.linear_bwd(*a.values(), NULL, NULL)
+
+
+def ffn_fwd(ops, **k):
+    a = dict(x=P, ldx=64, w=P, ldw=48, act=3, M=16, f=24, d=64, h=P, ldh=24, a=P, lda=48)
+    a.update(k)
+    return ops.lib.gated_ffn_fwd(*a.values(), NULL, NULL)
+
+
+def ffn_bwd(ops, **k):
+    a = dict(dh=P, lddh=24, a=P, lda=48, x=P, ldx=64, w=P, ldw=48, act=3, M=16, f=24, d=64, da=P, ldda=48, dx=P, lddx=64,
+             dw=P, dwt=1, lddw=48)
+    a.update(k)
+    return ops.lib.gated_ffn_bwd(*a.values(), NULL, NULL)
+
+
+@pytest.mark.parametrize("call,invalid,unaligned,unsupported", [
+    (lin_fwd, [dict(x=NULL), dict(w=NULL), dict(y=NULL), dict(M=-1), dict(N=0), dict(K=0), dict(act=4), dict(act=-1),
+               dict(ldx=63), dict(ldw=47), dict(ldy=47), dict(ldz=47), dict(ldres=47)],
+     [dict(x=ODD), dict(w=ODD), dict(y=ODD), dict(z=ODD), dict(res=ODD), dict(bias=ODD), dict(ldx=65), dict(ldw=49),
+      dict(ldy=49), dict(ldz=49), dict(ldres=49), dict(N=41, ldy=41)], [dict(M=1 << 31)]),
+    (lin_bwd, [dict(dy=NULL), dict(x=NULL), dict(w=NULL), dict(z=NULL), dict(M=-1), dict(act=4), dict(dwt=2), dict(lddy=47),
+               dict(ldx=63), dict(ldw=47), dict(ldz=47), dict(lddx=63), dict(lddw=47), dict(dx=NULL, dw=NULL, db=NULL)],
+     [dict(dy=ODD), dict(x=ODD), dict(w=ODD), dict(z=ODD), dict(dx=ODD), dict(dw=ODD), dict(db=ODD), dict(ws=ODD),
+      dict(lddy=49), dict(lddx=65)], [dict(M=1 << 31)]),
+    (ffn_fwd, [dict(x=NULL), dict(w=NULL), dict(h=NULL), dict(M=-1), dict(f=0), dict(d=0), dict(act=9), dict(ldx=63),
+               dict(ldw=47), dict(ldh=23), dict(lda=47)],
+     [dict(x=ODD), dict(w=ODD), dict(h=ODD), dict(a=ODD), dict(ldh=25), dict(lda=50)], [dict(f=20), dict(M=1 << 31)]),
+    (ffn_bwd, [dict(dh=NULL), dict(a=NULL), dict(x=NULL), dict(w=NULL), dict(da=NULL), dict(M=-1), dict(dwt=-1), dict(lddh=23),
+               dict(lda=47), dict(ldda=47), dict(ldx=63), dict(ldw=47), dict(lddx=63), dict(lddw=47)],
+     [dict(dh=ODD), dict(a=ODD), dict(da=ODD), dict(x=ODD), dict(w=ODD), dict(dx=ODD), dict(dw=ODD), dict(lddw=49)],
+     [dict(f=20), dict(M=1 << 31)]),
+])
+def test_dense_layers(ops, call, invalid, unaligned, unsupported):
+    for k in invalid:
+        assert call(ops, **k) == ops.MOE_ERR_INVALID_ARG, k
+    for k in unaligned:
+        assert call(ops, **k) == ops.MOE_ERR_ALIGNMENT, k
+    for k in unsupported:
+        assert call(ops, **k) == ops.MOE_ERR_UNSUPPORTED, k
+
+
+def test_dense_workspace_and_no_rows(ops):
+    assert lin_bwd(ops, ws=NULL) == ops.MOE_ERR_WORKSPACE
+    assert lin_bwd(ops, wsb=ops.linear_bwd_workspace_size(16, 48) - 1) == ops.MOE_ERR_WORKSPACE
+    assert ops.linear_bwd_workspace_size(16, 48) == 16 * 48 * 2 + 48 * 4
+    assert ops.linear_bwd_workspace_size(-1, 48) == -1 and ops.linear_bwd_workspace_size(16, 0) == -1
+    assert lin_fwd(ops, M=0, x=NULL, y=NULL, z=NULL, res=NULL) == ops.MOE_OK
+    assert ffn_fwd(ops, M=0, x=NULL, h=NULL, a=NULL) == ops.MOE_OK
