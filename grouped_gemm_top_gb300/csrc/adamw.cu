@@ -19,6 +19,10 @@
 // step and the seed: the same inputs give the same codes).  A v that is not
 // zero is never rounded to zero, which would let m / (sqrt(v) + eps) explode.
 //
+// m, v and the 8-bit rounding are a stated sequence of single fp32 operations
+// (products and sums rounded one by one), so that states, which feed the next
+// step, are the same bits wherever they are computed.
+//
 // The pass is bound by its traffic: p, g, m, v read and p, m, v written once.
 #include <math.h>
 
@@ -109,14 +113,51 @@ __device__ __forceinline__ void store(T* p, int n, bool vec, const float* f) {
     }
 }
 
-// E4M3 codes <-> fp32.  Two codes to two fp16 and on; exact.
-__device__ __forceinline__ void e4m3x2_to_f32(uint32_t two, float& lo, float& hi) {
-    uint32_t h;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)two));
-    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, h;\n\t}"
-        : "=f"(lo), "=f"(hi)
-        : "r"(h));
+// Two fp32 at a time (the packed forms take one issue slot for two results;
+// each is rounded as the single form rounds it).
+struct F2 {
+    uint64_t v;
+    __device__ __forceinline__ F2() {}
+    __device__ __forceinline__ F2(float a, float b) { asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b)); }
+    __device__ __forceinline__ explicit F2(float a) : F2(a, a) {}
+    __device__ __forceinline__ void get(float& a, float& b) const { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+};
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
 }
+// The sum stays two single additions: a packed product whose only use is a
+// packed sum is contracted into a fused multiply-add, which rounds once where
+// the states' arithmetic rounds twice.
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+    float x0, x1, y0, y1;
+    a.get(x0, x1);
+    b.get(y0, y1);
+    return F2(__fadd_rn(x0, y0), __fadd_rn(x1, y1));
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
+}
+__device__ __forceinline__ float rcp_approx(float x) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+// E4M3 codes to fp32 times 2^-120, in integer arithmetic (the conversion
+// instructions run at a quarter of its rate): the code's exponent and
+// mantissa moved into those of an fp32, exact, subnormal codes included.
+// (Code 0x7F is written only where the block's scale is not finite.)
+template <bool SIGNED>
+__device__ __forceinline__ float e4m3_bits(uint32_t w, int i) {      // byte i of w
+    uint32_t f = (i == 3 ? w >> 4 : w << (20 - 8 * i)) & 0x07F00000u;
+    if (SIGNED) f |= (w << (24 - 8 * i)) & 0x80000000u;
+    return __uint_as_float(f);
+}
+template <bool SIGNED>
 __device__ __forceinline__ void load_codes(const uint8_t* p, int n, bool vec, float* f) {
     uint32_t w[2] = {0u, 0u};
     if (vec && n >= 8) {
@@ -128,13 +169,9 @@ __device__ __forceinline__ void load_codes(const uint8_t* p, int n, bool vec, fl
             if (i < n) w[i >> 2] |= (uint32_t)p[i] << (8 * (i & 3));
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) e4m3x2_to_f32((w[i >> 1] >> (16 * (i & 1))) & 0xFFFFu, f[2 * i], f[2 * i + 1]);
+    for (int i = 0; i < 8; ++i) f[i] = e4m3_bits<SIGNED>(w[i >> 2], i & 3);
 }
-__device__ __forceinline__ void store_codes(uint8_t* p, int n, bool vec, const float* f) {
-    uint32_t w[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-        w[i] = cvt_e4m3x2(f[4 * i], f[4 * i + 1]) | (cvt_e4m3x2(f[4 * i + 2], f[4 * i + 3]) << 16);
+__device__ __forceinline__ void store_codes(uint8_t* p, int n, bool vec, const uint32_t* w) {
     if (vec && n >= 8) {
         *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
     } else {
@@ -144,13 +181,22 @@ __device__ __forceinline__ void store_codes(uint8_t* p, int n, bool vec, const f
     }
 }
 
-// 0 <= x (up to about 448) to a multiple of its E4M3 step, down or up as the
-// 16 dither bits say.  Steps: 2^(exponent - 3), 2^-9 below 2^-6.
-__device__ __forceinline__ float dithered(float x, uint32_t bits16) {
-    const int e = max((int)(__float_as_uint(x) >> 23) - 127 - 3, -9);
-    const float step = __uint_as_float((uint32_t)(e + 127) << 23), inv = __uint_as_float((uint32_t)(127 - e) << 23);
-    const float k = floorf(fmaf(x, inv, (float)bits16 * (1.f / 65536.f)));
-    return fminf(k * step, 448.f);
+// |x| (up to 448) rounded to E4M3 as 16 dither bits say,
+//   floor(|x| / step + dither / 2^16) * step,  step = 2^(exponent - 3), 2^-9 below 2^-6.
+// The dither is added to the fp32 pattern right below the three mantissa
+// bits that stay; what is above bit 20 then is the code, but for the
+// exponent's offset (120 of 8).  Below 2^-6 the same with |x| + 2^-6, whose
+// last bit that stays is worth 2^-9 and whose code is 8 higher.
+// `dither20` are the bits in place (16 bits from bit 4 on); the code is
+// returned in bits 24..30, with noise below.
+__device__ __forceinline__ uint32_t e4m3_code(float x, uint32_t dither20) {
+    const bool sub = fabsf(x) < 0.015625f;
+    const uint32_t bits = __float_as_uint(fabsf(x) + (sub ? 0.015625f : 0.f));
+    return (bits + dither20 - (sub ? 968u << 20 : 960u << 20)) << 4;
+}
+// the top bytes of four words
+__device__ __forceinline__ uint32_t top_bytes(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    return __byte_perm(__byte_perm(a, b, 0x0073), __byte_perm(c, d, 0x0073), 0x5410);
 }
 
 // Largest of a block's values (>= 0, or NaN), over its warp.
@@ -164,15 +210,14 @@ __device__ __forceinline__ float block_top(const float* f) {
 // 1e-35 (whose inverse scale fp32 does not hold) is zero.
 __device__ __forceinline__ void block_scale(float top, float& scale, float& inv) {
     const bool some = !(top <= 1e-35f);      // NaN too
-    scale = some ? __fdiv_rn(top, 448.f) : 0.f;
-    inv = some ? __fdiv_rn(448.f, top) : 0.f;
+    scale = some ? __fmul_rn(top, 1.f / 448.f) : 0.f;
+    inv = some ? __fmul_rn(__frcp_rn(top), 448.f) : 0.f;
 }
 
 template <typename PT, typename GT, int BITS>
-__global__ void __launch_bounds__(kThreads) k_adamw(const Params p) {
+__global__ void __launch_bounds__(kThreads, BITS == 8 ? 5 : 2) k_adamw(const Params p) {
     __shared__ float s_h[4];
     __shared__ uint32_t s_key;
-    __shared__ int s_last;
     if (threadIdx.x == 0) {
         float i1 = p.inv_bc1, i2 = p.inv_bc2;
         uint32_t key = p.key;
@@ -182,13 +227,13 @@ __global__ void __launch_bounds__(kThreads) k_adamw(const Params p) {
             i2 = 1.f / -expm1f((float)t * p.ln_b2);
             key = mix(p.seed ^ mix((uint32_t)t));
         }
-        s_h[0] = i1, s_h[1] = i2;
+        s_h[0] = i1, s_h[1] = sqrtf(i2);
         s_h[2] = p.lr_dev ? *p.lr_dev : p.lr;
         s_h[3] = p.grad_scale ? *p.grad_scale : 1.f;
         s_key = key;
     }
     __syncthreads();
-    const float lr = s_h[2], gs = s_h[3], inv_bc2 = s_h[1], lr1 = lr * s_h[0];
+    const float lr = s_h[2], gs = s_h[3], root2 = s_h[1], lr1 = lr * s_h[0];
     const uint32_t key = s_key;
     const bool skip = !(fabsf(gs) <= 3.402823466e38f);      // NaN or infinite: the step is not taken
     // the CTA's share of the tiles, in order
@@ -215,33 +260,40 @@ __global__ void __launch_bounds__(kThreads) k_adamw(const Params p) {
         const int n = left >= 8 ? 8 : (left > 0 ? (int)left : 0);
         if (BITS == 32 && n == 0) continue;      // 8 bits: the warp works together
         const bool vec = e.vec != 0;
-        float g[8], w[8], m[8], v[8];
+        float g[8], w[8], m[8], v[8], u[8];
         load(static_cast<const GT*>(e.g) + at, n, vec, g);
         load(static_cast<PT*>(e.p) + at, n, vec, w);
         if (BITS == 32) {
             load(static_cast<float*>(e.m) + at, n, vec, m);
             load(static_cast<float*>(e.v) + at, n, vec, v);
         } else {
-            load_codes(static_cast<uint8_t*>(e.m) + at, n, vec, m);
-            load_codes(static_cast<uint8_t*>(e.v) + at, n, vec, v);
+            load_codes<true>(static_cast<uint8_t*>(e.m) + at, n, vec, m);
+            load_codes<false>(static_cast<uint8_t*>(e.v) + at, n, vec, v);
             // the warp's block: its first element exists or the whole warp is past the end
             const int64_t b = (at - 8 * (int)(threadIdx.x & 31)) / kBlock;
             const bool some = b * kBlock < e.n;
-            const float sm = some ? e.ms[b] : 0.f, sv = some ? e.vs[b] : 0.f;
+            const F2 sm(some ? e.ms[b] : 0.f), sv(some ? e.vs[b] : 0.f), up(__uint_as_float((120u + 127u) << 23));
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                m[i] *= sm;
-                v[i] *= sv;
-                v[i] *= v[i];
+            for (int i = 0; i < 8; i += 2) {
+                mul2(mul2(F2(m[i], m[i + 1]), up), sm).get(m[i], m[i + 1]);
+                const F2 r = mul2(mul2(F2(v[i], v[i + 1]), up), sv);
+                mul2(r, r).get(v[i], v[i + 1]);
             }
         }
-        const float decay = 1.f - lr * e.wd;
+        const F2 decay(1.f - lr * e.wd);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float gi = g[i] * gs;
-            m[i] = p.b1 * m[i] + p.c1 * gi;
-            v[i] = p.b2 * v[i] + p.c2 * gi * gi;
-            w[i] = w[i] * decay - __fdividef(lr1 * m[i], sqrtf(v[i] * inv_bc2) + p.eps);
+        for (int i = 0; i < 8; i += 2) {
+            const F2 g2 = mul2(F2(g[i], g[i + 1]), F2(gs));
+            const F2 m2 = add2(mul2(F2(p.b1), F2(m[i], m[i + 1])), mul2(F2(p.c1), g2));
+            const F2 v2 = add2(mul2(F2(p.b2), F2(v[i], v[i + 1])), mul2(mul2(F2(p.c2), g2), g2));
+            m2.get(m[i], m[i + 1]);
+            v2.get(v[i], v[i + 1]);
+            u[i] = sqrtf(v[i]);
+            u[i + 1] = sqrtf(v[i + 1]);
+            float d0, d1;
+            fma2(F2(u[i], u[i + 1]), F2(root2), F2(p.eps)).get(d0, d1);
+            const F2 q = mul2(mul2(m2, F2(-lr1)), F2(rcp_approx(d0), rcp_approx(d1)));
+            fma2(F2(w[i], w[i + 1]), decay, q).get(w[i], w[i + 1]);
         }
         store(static_cast<PT*>(e.p) + at, n, vec, w);
         if (e.copy != nullptr) store(e.copy + at, n, vec, w);
@@ -250,28 +302,46 @@ __global__ void __launch_bounds__(kThreads) k_adamw(const Params p) {
             store(static_cast<float*>(e.v) + at, n, vec, v);
         } else {
             const int64_t b = (at - 8 * (int)(threadIdx.x & 31)) / kBlock;
+            if (n < 8) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                m[i] = i < n ? m[i] : 0.f;
-                v[i] = i < n ? sqrtf(v[i]) : 0.f;
+                for (int i = 0; i < 8; ++i) {
+                    m[i] = i < n ? m[i] : 0.f;
+                    u[i] = i < n ? u[i] : 0.f;
+                }
             }
-            float sm, im, sv, iv;
+            float sm, im, su, iu;
             block_scale(block_top(m), sm, im);
-            block_scale(block_top(v), sv, iv);
+            block_scale(block_top(u), su, iu);
             const uint64_t c = (uint64_t)(e.rng + at);     // blocks start at multiples of 256 of the counter
-            const uint32_t hi = mix((uint32_t)(c >> 32) ^ key);
+            const uint32_t lo = (uint32_t)c + mix((uint32_t)(c >> 32) ^ key);
+            uint32_t cm[8], cu[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const uint32_t bits = mix((uint32_t)c + (uint32_t)i + hi);
-                m[i] = copysignf(dithered(fabsf(m[i]) * im, bits & 0xFFFFu), m[i]);
-                const float q = dithered(v[i] * iv, bits >> 16);
-                v[i] = v[i] > 0.f && q == 0.f ? 0.001953125f : q;
+            for (int i = 0; i < 8; i += 2) {
+                mul2(F2(m[i], m[i + 1]), F2(im)).get(m[i], m[i + 1]);
+                mul2(F2(u[i], u[i + 1]), F2(iu)).get(u[i], u[i + 1]);
+#pragma unroll
+                for (int j = i; j < i + 2; ++j) {
+                    const uint32_t bits = mix(lo + (uint32_t)j);
+                    cm[j] = e4m3_code(m[j], (bits << 4) & 0xFFFF0u);
+                    const uint32_t k = e4m3_code(u[j], (bits >> 12) & 0xFFFF0u);
+                    cu[j] = u[j] > 0.f ? max(k, 1u << 24) : k;      // not zero: never rounded to zero
+                }
             }
-            store_codes(static_cast<uint8_t*>(e.m) + at, n, vec, m);
-            store_codes(static_cast<uint8_t*>(e.v) + at, n, vec, v);
+            uint32_t wm[2], wu[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                uint32_t sign[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) sign[i] = __float_as_uint(m[4 * j + i]);
+                wm[j] = top_bytes(cm[4 * j], cm[4 * j + 1], cm[4 * j + 2], cm[4 * j + 3]) |
+                        (top_bytes(sign[0], sign[1], sign[2], sign[3]) & 0x80808080u);
+                wu[j] = top_bytes(cu[4 * j], cu[4 * j + 1], cu[4 * j + 2], cu[4 * j + 3]);
+            }
+            store_codes(static_cast<uint8_t*>(e.m) + at, n, vec, wm);
+            store_codes(static_cast<uint8_t*>(e.v) + at, n, vec, wu);
             if ((threadIdx.x & 31) == 0 && n > 0) {
                 e.ms[b] = sm;
-                e.vs[b] = sv;
+                e.vs[b] = su;
             }
         }
     }
@@ -279,8 +349,7 @@ __global__ void __launch_bounds__(kThreads) k_adamw(const Params p) {
         // the last CTA to come here counts the step: every CTA has read it by then
         if (threadIdx.x == 0) {
             __threadfence();
-            s_last = atomicAdd(p.ticket, 1u) == gridDim.x - 1;
-            if (s_last) {
+            if (atomicAdd(p.ticket, 1u) == gridDim.x - 1) {
                 *p.ticket = 0u;
                 if (!skip) *p.step_dev += 1;
             }

@@ -616,7 +616,21 @@ def moe_selftest_bounded_wait(timeout_ns, err, completed, stream=None):
 # device; a tensor that does not fit the call is refused with
 # MOE_ERR_INVALID_ARG before anything is launched.
 
+# These calls also serve steps of a few microseconds: the current device and
+# stream come from torch's own C entry points, without the Python objects
+# around them.
+
 _TYPES = {torch.bfloat16: MOE_TYPE_BF16, torch.float32: MOE_TYPE_F32}
+_F32, _I32, _U8 = (torch.float32,), (torch.int32,), (torch.uint8,)
+_E4M3 = (torch.uint8, torch.float8_e4m3fn)
+
+
+def _device():
+    return torch._C._cuda_getDevice()
+
+
+def _raw_stream(device):
+    return torch._C._cuda_getCurrentRawStream(device)
 
 
 def _need(fn, ok):
@@ -629,21 +643,31 @@ def _rows(fn, t, m=None, n=None, types=_TYPES):
     device; (None, 0, 0) for None."""
     if t is None:
         return None, 0, 0
-    _need(fn, t.dim() == 2 and t.is_cuda and t.dtype in types and t.get_device() == torch.cuda.current_device())
-    rows, cols = t.shape
-    _need(fn, (m is None or rows == m) and (n is None or cols == n))
-    ld = t.stride(0) if rows > 1 else max(t.stride(0), cols)
-    _need(fn, (cols == 1 or t.stride(1) == 1) and ld >= cols)
-    return t.data_ptr(), _TYPES[t.dtype], ld
+    shape, dtype = t.shape, t.dtype
+    # (a tensor in host memory has device -1)
+    if len(shape) != 2 or dtype not in types or t.get_device() != _device():
+        raise MoEError(fn, MOE_ERR_INVALID_ARG)
+    rows, cols = shape
+    ld, step = t.stride()
+    if rows <= 1 and ld < cols:
+        ld = cols
+    if (m is not None and rows != m) or (n is not None and cols != n) or (step != 1 and cols != 1) or ld < cols:
+        raise MoEError(fn, MOE_ERR_INVALID_ARG)
+    return t.data_ptr(), _TYPES[dtype], ld
 
 
 def _flat(fn, t, n, types):
     """Pointer of a contiguous tensor of n elements on the current device."""
     if t is None:
         return None
-    _need(fn, t.is_cuda and t.dtype in types and t.numel() == n and t.is_contiguous() and
-          t.get_device() == torch.cuda.current_device())
+    if t.dtype not in types or t.numel() != n or t.get_device() != _device() or not t.is_contiguous():
+        raise MoEError(fn, MOE_ERR_INVALID_ARG)
     return t.data_ptr()
+
+
+def _handle(stream):
+    """The stream's handle; of the current stream for None."""
+    return _raw_stream(_device()) if stream is None else stream.cuda_stream
 
 
 def _new(shape, dtype, like, stream):
@@ -669,7 +693,6 @@ def rmsnorm_residual_fwd(x, w, residual=None, eps=1e-6, y=None, r=None, rstd=Non
         tres = tx if r is None else _TYPES.get(r.dtype, -1)
     elif r is None and want_r:
         r = _new((M, N), residual.dtype, x, stream)
-    _need(fn, w.dtype in _TYPES)
     pw = _flat(fn, w, N, _TYPES)
     if y is None and want_y:
         y = _new((M, N), y_dtype, x, stream)
@@ -686,11 +709,11 @@ def rmsnorm_residual_fwd(x, w, residual=None, eps=1e-6, y=None, r=None, rstd=Non
     if codes is not None or scales is not None:
         rows = (M + 127) // 128 * 128 if sf_layout == MOE_SF_ATOMS else M
         _need(fn, codes is not None and scales is not None)
-        pc = _flat(fn, codes, rows * N, (torch.uint8, torch.float8_e4m3fn))
-        ps = _flat(fn, scales, rows * (N // 32), (torch.uint8,))
+        pc = _flat(fn, codes, rows * N, _E4M3)
+        ps = _flat(fn, scales, rows * (N // 32), _U8)
     _check(fn, lib.rmsnorm_residual_fwd(px, tx, ldx, pres, tres, ldres, pw, _TYPES[w.dtype], eps, M, N, pr, ldr, py,
-                                        ty, ldy, _flat(fn, rstd, M, (torch.float32,)), pc, ps, int(sf_layout),
-                                        _stream(stream)))
+                                        ty, ldy, _flat(fn, rstd, M, _F32), pc, ps, int(sf_layout),
+                                        _handle(stream)))
     return y, r, rstd, codes, scales
 
 
@@ -719,8 +742,8 @@ def rmsnorm_residual_bwd(dy, r, w, rstd, dres=None, want_dw=True, dx=None, dw=No
     _need(fn, tdx == tr)
     nws = ws.numel() * ws.element_size() if ws is not None else 0
     _check(fn, lib.rmsnorm_residual_bwd(pdy, tdy, lddy, pr, tr, ldr, _flat(fn, w, N, _TYPES), _TYPES[w.dtype],
-                                        _flat(fn, rstd, M, (torch.float32,)), pdr, lddr, M, N, pdx, lddx,
-                                        _flat(fn, dw, N, (torch.float32,)), _p(ws), nws, _stream(stream)))
+                                        _flat(fn, rstd, M, _F32), pdr, lddr, M, N, pdx, lddx,
+                                        _flat(fn, dw, N, _F32), _p(ws), nws, _handle(stream)))
     return dx, dw
 
 
@@ -756,7 +779,7 @@ def linear_fwd(x, w, bias=None, act="none", residual=None, y=None, z=None, want_
     py, _, ldy = _rows(fn, y, M, N, _BF16)
     pz, _, ldz = _rows(fn, z, M, N, _BF16)
     _check(fn, lib.linear_fwd(px, ldx, pw, ldw, _flat(fn, bias, N, _BF16), _act(fn, act), pr, ldr, M, N, K, py, ldy,
-                              pz, ldz, _p(err), _stream(stream)))
+                              pz, ldz, _p(err), _handle(stream)))
     return y if z is None else (y, z)
 
 
@@ -790,7 +813,7 @@ def linear_bwd(dy, x, w, z=None, act="none", want_dx=True, want_dw=True, want_db
     pdw, tdw, lddw = _rows(fn, dw, K, N)
     nws = ws.numel() * ws.element_size() if ws is not None else 0
     _check(fn, lib.linear_bwd(pdy, lddy, px, ldx, pw, ldw, pz, ldz, act, M, N, K, pdx, lddx, pdw, tdw, lddw,
-                              _flat(fn, dbias, N, (torch.float32,)), _p(ws), nws, _p(err), _stream(stream)))
+                              _flat(fn, dbias, N, _F32), _p(ws), nws, _p(err), _handle(stream)))
     return dx, dw, dbias
 
 
@@ -809,7 +832,7 @@ def gated_ffn_fwd(x, w1, act="silu", h=None, a=None, want_a=False, err=None, str
     ph, _, ldh = _rows(fn, h, M, f, _BF16)
     pa, _, lda = _rows(fn, a, M, 2 * f, _BF16)
     _check(fn, lib.gated_ffn_fwd(px, ldx, pw, ldw, _act(fn, act), M, f, d, ph, ldh, pa, lda, _p(err),
-                                 _stream(stream)))
+                                 _handle(stream)))
     return h if a is None else (h, a)
 
 
@@ -834,7 +857,7 @@ def gated_ffn_bwd(dh, a, x, w1, act="silu", want_dx=True, want_dw=True, dx=None,
     pdx, _, lddx = _rows(fn, dx, M, d, _BF16)
     pdw, tdw, lddw = _rows(fn, dw1, d, 2 * f)
     _check(fn, lib.gated_ffn_bwd(pdh, lddh, pa, lda, px, ldx, pw, ldw, _act(fn, act), M, f, d, pda, ldda, pdx, lddx,
-                                 pdw, tdw, lddw, _p(err), _stream(stream)))
+                                 pdw, tdw, lddw, _p(err), _handle(stream)))
     return dx, dw1
 
 
@@ -846,6 +869,8 @@ class AdamWPlan:
         self.table, self.tensors, self.tiles = table, tensors, tiles
         self.p_type, self.g_type, self.state_bits = p_type, g_type, state_bits
         self.kept = kept
+        self.address, self.opts = table.data_ptr(), AdamWOpts()
+        self.opts_ref = ctypes.byref(self.opts)      # filled in by each adamw_step
 
 
 def adamw_plan(params, grads, ms, vs, m_scales=None, v_scales=None, copies=None, weight_decay=0.0, rng_base=None,
@@ -862,7 +887,7 @@ def adamw_plan(params, grads, ms, vs, m_scales=None, v_scales=None, copies=None,
     _need(fn, n >= 1 and len(grads) == len(ms) == len(vs) == n)
     bits = 32 if ms[0].dtype == torch.float32 else 8
     _need(fn, (bits == 8) == (m_scales is not None) == (v_scales is not None))
-    state = (torch.float32,) if bits == 32 else (torch.uint8, torch.float8_e4m3fn)
+    state = _F32 if bits == 32 else _E4M3
     pt, gt = params[0].dtype, grads[0].dtype
     _need(fn, pt in _TYPES and gt in _TYPES)
     for opt in (m_scales, v_scales, copies, rng_base):
@@ -876,8 +901,8 @@ def adamw_plan(params, grads, ms, vs, m_scales=None, v_scales=None, copies=None,
         e.p, e.g = _flat(fn, params[i], k, (pt,)), _flat(fn, grads[i], k, (gt,))
         e.m, e.v = _flat(fn, ms[i], k, state), _flat(fn, vs[i], k, state)
         if bits == 8:
-            e.m_scale = _flat(fn, m_scales[i], (k + 255) // 256, (torch.float32,))
-            e.v_scale = _flat(fn, v_scales[i], (k + 255) // 256, (torch.float32,))
+            e.m_scale = _flat(fn, m_scales[i], (k + 255) // 256, _F32)
+            e.v_scale = _flat(fn, v_scales[i], (k + 255) // 256, _F32)
         if copies is not None:
             e.copy = _flat(fn, copies[i], k, (torch.bfloat16,))
         e.n, e.weight_decay = k, wd[i]
@@ -902,15 +927,11 @@ def adamw_step(plan, lr, betas=(0.9, 0.999), eps=1e-8, step=1, grad_scale=None, 
     grad_scale: float32 device tensor, a factor of every gradient; when it is
     not finite the call changes nothing.  seed: of the 8-bit rounding."""
     fn = "adamw_step"
-    o = AdamWOpts(0.0, betas[0], betas[1], eps, 0, None, None, _flat(fn, grad_scale, 1, (torch.float32,)),
-                  int(seed) & 0xFFFFFFFF)
-    if isinstance(lr, torch.Tensor):
-        o.lr_dev = _flat(fn, lr, 1, (torch.float32,))
-    else:
-        o.lr = lr
-    if isinstance(step, torch.Tensor):
-        o.step_dev = _flat(fn, step, 1, (torch.int32,))
-    else:
-        o.step = step
-    _check(fn, lib.adamw_step(plan.table.data_ptr(), plan.tensors, plan.tiles, plan.p_type, plan.g_type,
-                              plan.state_bits, ctypes.byref(o), _stream(stream)))
+    o = plan.opts
+    o.beta1, o.beta2 = betas
+    o.eps, o.seed = eps, seed & 0xFFFFFFFF
+    o.lr, o.lr_dev = (0.0, _flat(fn, lr, 1, _F32)) if isinstance(lr, torch.Tensor) else (lr, None)
+    o.step, o.step_dev = (0, _flat(fn, step, 1, _I32)) if isinstance(step, torch.Tensor) else (step, None)
+    o.grad_scale = _flat(fn, grad_scale, 1, _F32)
+    _check(fn, lib.adamw_step(plan.address, plan.tensors, plan.tiles, plan.p_type, plan.g_type, plan.state_bits,
+                              plan.opts_ref, _handle(stream)))
