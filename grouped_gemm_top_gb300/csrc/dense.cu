@@ -396,6 +396,260 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
 }
 
+// ------------------------------------------------------- few rows ----
+//
+// With few rows of x the product is the reading of W, and 256 x 256 tiles
+// would leave most SMs without one.  Here the roles are swapped: W is the A
+// operand (128 of its columns, or rows for the input gradient, are the M of
+// the MMA) and up to 128 rows of x are its N, so a tile costs what the rows
+// cost.  The contraction is split over the S CTAs of a cluster; each leaves
+// its fp32 partial tile in its shared memory, and after a cluster barrier
+// each CTA adds every S-th row over all of them, in rank order, and runs the
+// epilogue on it (no workspace, no atomics, the same bits on every run).
+// About 96 KB of shared memory per CTA, so that two share an SM and one's
+// reduction runs under the other's loads.
+namespace few {
+
+constexpr int ROWS = 128;                       // most rows of x per tile
+constexpr int W_BYTES = 128 * TK * 2;
+constexpr int SMEM_TILES = 98304;               // pipeline stages, then the partial tile
+constexpr int MAX_STAGES = 5;
+constexpr int OFF_BAR = SMEM_TILES;             // full[S], empty[S], done
+constexpr int OFF_MISC = OFF_BAR + 8 * (2 * MAX_STAGES + 1);
+constexpr int SMEM_BYTES = OFF_MISC + 16 + 1024;
+constexpr int THREADS = 128;
+
+struct Split {
+    int rows;          // rows of x per tile, padded to 16
+    int stages;
+    int splits;        // CTAs of a cluster
+    uint32_t tmem_cols;
+};
+
+__device__ __forceinline__ void ld_cluster_v4(uint32_t addr, float* v) {
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3])
+                 : "r"(addr));
+}
+// 32 lanes x 16 columns
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float* v) {
+    uint32_t r[16];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// 4 columns of a row; `n` of them exist, columns start at multiples of 4
+__device__ __forceinline__ void load4(const __nv_bfloat16* p, int n, float* f) {
+    if (n >= 4) {
+        const uint2 q = *reinterpret_cast<const uint2*>(p);
+        f[0] = __uint_as_float(q.x << 16), f[1] = __uint_as_float(q.x & 0xFFFF0000u);
+        f[2] = __uint_as_float(q.y << 16), f[3] = __uint_as_float(q.y & 0xFFFF0000u);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f[i] = i < n ? __bfloat162float(p[i]) : 0.f;
+    }
+}
+__device__ __forceinline__ void store4(__nv_bfloat16* p, int n, const float* f) {
+    if (n >= 4) {
+        *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]));
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (i < n) p[i] = __float2bfloat16_rn(f[i]);
+    }
+}
+
+// tmW: W, boxes of 64 columns x 64 k (W_MN) or 64 k x 128 rows; tmX: x, boxes
+// of 64 k x s.rows rows.
+template <bool W_MN, int EPI>
+__global__ void __launch_bounds__(THREADS, 2)
+    k_dense_few(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX, const Params p,
+                const Split s) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = s.splits > 1 ? cluster_ctarank() : 0;
+    const int64_t tile = blockIdx.x / s.splits;
+    const int nt = (int)(tile % p.n_tiles);
+    const int64_t m0 = (tile / p.n_tiles) * s.rows;
+    const int m = (int)min((int64_t)s.rows, p.M - m0);
+    const int k0 = (int)((int64_t)p.nk * rank / s.splits), k1 = (int)((int64_t)p.nk * (rank + 1) / s.splits);
+    const int stage_bytes = W_BYTES + s.rows * TK * 2;
+
+    const uint32_t bar0 = smem_u32(smem + OFF_BAR);
+    auto full_bar = [&](int i) { return bar0 + 8u * i; };
+    auto empty_bar = [&](int i) { return bar0 + 8u * (MAX_STAGES + i); };
+    const uint32_t done_bar = bar0 + 8u * (2 * MAX_STAGES);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + OFF_MISC);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + OFF_MISC + 4);
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < s.stages; ++i) {
+            mbar_init(full_bar(i), 1);
+            mbar_init(empty_bar(i), 1);
+        }
+        mbar_init(done_bar, 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        *abort_flag = 0;
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
+                     "r"(s.tmem_cols));
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+
+    if (warp == 0 && lane == 0) {
+        // ------------------------------------------------ TMA producer ----
+        int stage = 0, issued = 0;
+        uint32_t phase = 0;
+        bool aborted = false;
+        for (int k = k0; k < k1; ++k) {
+            if (!mbar_wait(empty_bar(stage), phase ^ 1u, p, abort_flag)) {
+                aborted = true;
+                break;
+            }
+            const uint32_t fb = full_bar(stage);
+            const uint32_t sw = smem_u32(smem + stage * stage_bytes), sx = sw + W_BYTES;
+            mbar_expect_tx(fb, stage_bytes);
+            if constexpr (W_MN) {
+                const int c = EPI == EPI_GLU ? nt * 64 : nt * 128;
+                tma_load_2d(sw, &tmW, c, k * TK, fb);
+                tma_load_2d(sw + W_BYTES / 2, &tmW, EPI == EPI_GLU ? c + p.up : c + 64, k * TK, fb);
+            } else {
+                tma_load_2d(sw, &tmW, k * TK, nt * 128, fb);
+            }
+            tma_load_2d(sx, &tmX, k * TK, (int)m0, fb);
+            ++issued;
+            if (++stage == s.stages) {
+                stage = 0;
+                phase ^= 1u;
+            }
+        }
+        if (aborted) {      // wait (bounded) for the copies in flight
+            Params q = p;
+            q.timeout_ns = 200000000ull;
+            volatile int no_abort = 0;
+            for (int i = issued - min(issued, s.stages); i < issued; ++i)
+                mbar_wait(full_bar(i % s.stages), (uint32_t)(i / s.stages) & 1u, q, &no_abort);
+        }
+    } else if (warp == 1 && lane == 0) {
+        // -------------------------------------------------- MMA issuer ----
+        // bf16 A and B, fp32 D, M = 128, N = s.rows, A along M (W_MN) or K
+        const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | (W_MN ? 1u << 15 : 0u) |
+                               ((uint32_t)(s.rows >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
+        int stage = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        for (int k = k0; k < k1; ++k) {
+            if (!mbar_wait(full_bar(stage), phase, p, abort_flag)) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            const uint32_t sw = smem_u32(smem + stage * stage_bytes);
+            const uint64_t wdesc = operand_desc<W_MN>(sw), xdesc = desc_sw128(sw + W_BYTES);
+#pragma unroll
+            for (int kk = 0; kk < TK / 16; ++kk)
+                tc_mma_bf16(tmem, wdesc + k16_step<W_MN>() * kk, xdesc + k16_step<false>() * kk, idesc,
+                            (k != k0 || kk != 0) ? 1u : 0u);
+            tc_commit(empty_bar(stage));
+            if (++stage == s.stages) {
+                stage = 0;
+                phase ^= 1u;
+            }
+        }
+        (void)ok;
+        tc_commit(done_bar);
+    }
+    __syncwarp();
+    // every product of this CTA is done (and every stage read), or the CTA gives up
+    const bool ready = mbar_wait(done_bar, 0, p, abort_flag);
+    __syncthreads();      // the aborting producer's copies have landed
+    tc_fence_after();
+    float* part = reinterpret_cast<float*>(smem);          // [rows of x][128]
+    if (ready) {
+        for (int c = 0; c < m; c += 16) {
+            float v[16];
+            tmem_ld16(tmem + ((uint32_t)(warp * 32) << 16) + (uint32_t)c, v);
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                if (c + i < m) part[(c + i) * 128 + warp * 32 + lane] = v[i];
+        }
+    }
+    tc_fence_before();
+    if (s.splits > 1) cluster_sync();
+    else __syncthreads();
+    // rows rank, rank + splits, ... of the tile: 32 threads take a row, 4 columns each
+    const uint32_t part_addr = smem_u32(part);
+    for (int r = (int)rank + s.splits * warp; r < m; r += s.splits * (THREADS / 32)) {
+        float v[4] = {0.f, 0.f, 0.f, 0.f};
+        const uint32_t at = part_addr + (uint32_t)(r * 128 + lane * 4) * 4u;
+        if (s.splits == 1) {
+            const float4 q = *reinterpret_cast<const float4*>(part + r * 128 + lane * 4);
+            v[0] = q.x, v[1] = q.y, v[2] = q.z, v[3] = q.w;
+        } else {
+            for (int c = 0; c < s.splits; ++c) {
+                float q[4];
+                ld_cluster_v4(mapa(at, (uint32_t)c), q);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[i] += q[i];
+            }
+        }
+        const int64_t row = m0 + r;
+        if constexpr (EPI == EPI_GLU) {
+            float u[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) u[i] = __shfl_down_sync(0xFFFFFFFFu, v[i], 16);      // lanes 16..31 hold up
+            const int col = nt * 64 + lane * 4, n = p.N - col;
+            if (lane < 16 && n > 0) {
+                if (p.z != nullptr) {
+                    store4(p.z + row * p.ldz + col, n, v);
+                    store4(p.z + row * p.ldz + p.N + col, n, u);
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) u[i] *= act_of(v[i], p.act);
+                store4(static_cast<__nv_bfloat16*>(p.y) + row * p.ldy + col, n, u);
+            }
+        } else {
+            const int col = nt * 128 + lane * 4, n = p.N - col;
+            if (n > 0) {
+                if (p.bias != nullptr) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) v[i] += i < n ? __bfloat162float(p.bias[col + i]) : 0.f;
+                }
+                if (p.z != nullptr) store4(p.z + row * p.ldz + col, n, v);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[i] = act_of(v[i], p.act);
+                if (p.res != nullptr) {
+                    float q[4];
+                    load4(p.res + row * p.ldres + col, n, q);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) v[i] += q[i];
+                }
+                store4(static_cast<__nv_bfloat16*>(p.y) + row * p.ldy + col, n, v);
+            }
+        }
+    }
+    if (s.splits > 1) cluster_sync();      // nobody leaves while its partial tile is read
+    else __syncthreads();
+    if (warp == 1) {
+        __syncwarp();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(s.tmem_cols));
+    }
+}
+
+}  // namespace few
+
 // ------------------------------------------------- elementwise backward ----
 
 // da = [dh * up * act'(gate) | dh * act(gate)] from a = [gate | up].  Bound by
@@ -514,6 +768,12 @@ static cudaError_t set_attributes() {
     }
     MOE_DENSE_INSTANCES(X)
 #undef X
+    const cudaError_t es[] = {
+        cudaFuncSetAttribute(few::k_dense_few<true, EPI_LINEAR>, cudaFuncAttributeMaxDynamicSharedMemorySize, few::SMEM_BYTES),
+        cudaFuncSetAttribute(few::k_dense_few<true, EPI_GLU>, cudaFuncAttributeMaxDynamicSharedMemorySize, few::SMEM_BYTES),
+        cudaFuncSetAttribute(few::k_dense_few<false, EPI_LINEAR>, cudaFuncAttributeMaxDynamicSharedMemorySize, few::SMEM_BYTES)};
+    for (cudaError_t e : es)
+        if (e != cudaSuccess) return e;
     cudaLaunchAttribute attr[1];
     cudaLaunchConfig_t cfg = launch_cfg(1024, nullptr, attr);
     return cudaOccupancyMaxActiveClusters(&g_max_clusters, k_dense_pair<false, true, EPI_LINEAR>, &cfg);
@@ -544,6 +804,47 @@ static moe_status_t product(const Mat& a, const Mat& b, Params p, cudaStream_t s
     MOE_CHECK_LAUNCH();
     return MOE_OK;
 }
+
+// Few rows: see k_dense_few.  The product D[M, N] = x op(W), W's columns
+// (W_MN) or rows in tiles of 128 (GLU: 64 gate and 64 up columns).
+template <bool W_MN, int EPI>
+static moe_status_t product_few(const Mat& x, const Mat& w, Params p, cudaStream_t st) {
+    few::Split s{};
+    const int rows = (int)std::min<int64_t>(p.M, few::ROWS);
+    s.rows = (rows + 15) / 16 * 16;
+    s.stages = std::min(few::MAX_STAGES, few::SMEM_TILES / (few::W_BYTES + s.rows * TK * 2));
+    s.tmem_cols = s.rows <= 32 ? 32 : (s.rows <= 64 ? 64 : 128);
+    p.n_tiles = EPI == EPI_GLU ? (p.N + 63) / 64 : (p.N + 127) / 128;
+    p.m_tiles = (p.M + s.rows - 1) / s.rows;
+    p.nk = (int)((p.K + TK - 1) / TK);
+    p.timeout_ns = 2000000000ull;
+    const int64_t tiles = p.m_tiles * p.n_tiles;
+    const int sms = device_sm_count();
+    s.splits = 1;
+    while (s.splits < 8 && tiles * s.splits * 2 <= 2 * sms && p.nk >= 8 * s.splits) s.splits *= 2;
+    MOE_REQUIRE(tiles * s.splits <= 0x7FFFFFFFLL, MOE_ERR_UNSUPPORTED);
+    CUtensorMap tmW, tmX;
+    MOE_REQUIRE(make_bf16_map(&tmW, w.p, w.rows, w.cols, w.ld, W_MN ? TK : 128) &&
+                    make_bf16_map(&tmX, x.p, x.rows, x.cols, x.ld, s.rows),
+                MOE_ERR_CUDA);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(tiles * s.splits), 1, 1);
+    cfg.blockDim = dim3(few::THREADS, 1, 1);
+    cfg.dynamicSmemBytes = few::SMEM_BYTES;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = s.splits;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, few::k_dense_few<W_MN, EPI>, tmW, tmX, p, s) != cudaSuccess) return MOE_ERR_CUDA;
+    MOE_CHECK_LAUNCH();
+    return MOE_OK;
+}
+
+static bool few_rows(int64_t M) { return M <= few::ROWS; }
 
 static bool act_ok(int a) { return a >= MOE_ACT_NONE && a <= MOE_ACT_SILU; }
 // sizes the tensor maps and the tile counts hold
@@ -581,6 +882,7 @@ extern "C" moe_status_t linear_fwd(const void* x, int64_t ldx, const void* w, in
     p.bias = static_cast<const __nv_bfloat16*>(bias);
     p.res = static_cast<const __nv_bfloat16*>(res), p.ldres = ldres;
     p.err = err;
+    if (few_rows(M)) return product_few<true, EPI_LINEAR>({x, M, K, ldx}, {w, K, N, ldw}, p, (cudaStream_t)stream);
     return product<false, true, EPI_LINEAR>({x, M, K, ldx}, {w, K, N, ldw}, p, (cudaStream_t)stream);
 }
 
@@ -589,6 +891,7 @@ static moe_status_t input_grad(const void* dy, int64_t lddy, const void* w, int6
                                void* dx, int64_t lddx, int32_t* err, cudaStream_t s) {
     dense::Params p{};
     p.M = M, p.N = (int)K, p.K = N, p.act = MOE_ACT_NONE, p.y = dx, p.ldy = lddx, p.err = err;
+    if (few_rows(M)) return product_few<false, EPI_LINEAR>({dy, M, N, lddy}, {w, K, N, ldw}, p, s);
     return product<false, false, EPI_LINEAR>({dy, M, N, lddy}, {w, K, N, ldw}, p, s);
 }
 static moe_status_t weight_grad(const void* x, int64_t ldx, const void* dy, int64_t lddy, int64_t M, int N, int64_t K,
@@ -669,6 +972,8 @@ extern "C" moe_status_t gated_ffn_fwd(const void* x, int64_t ldx, const void* w1
     p.M = M, p.N = f, p.K = d, p.act = act, p.up = f;
     p.y = h, p.ldy = ldh, p.z = static_cast<__nv_bfloat16*>(a), p.ldz = lda;
     p.err = err;
+    if (few_rows(M))
+        return product_few<true, EPI_GLU>({x, M, d, ldx}, {w1, d, 2 * (int64_t)f, ldw}, p, (cudaStream_t)stream);
     return product<false, true, EPI_GLU>({x, M, d, ldx}, {w1, d, 2 * (int64_t)f, ldw}, p, (cudaStream_t)stream);
 }
 
