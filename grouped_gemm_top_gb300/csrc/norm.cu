@@ -13,7 +13,7 @@
 // unrounded y, so each output is rounded once.
 #include <algorithm>
 
-#include "common.cuh"
+#include "gemm_common.cuh"
 
 namespace moe {
 namespace norm {
@@ -122,6 +122,51 @@ struct FwdParams {
     bool block_row, vec_x, vec_res, vec_w, vec_r, vec_y;
 };
 
+// Padding row of the codes: zero codes and scale bytes.
+template <int VPT>
+__device__ __forceinline__ void pad_row(const FwdParams& p, int64_t row, int t, int tpr) {
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) {
+        const int c = (t + v * tpr) * kVec;
+        if (c >= p.N) continue;
+        *reinterpret_cast<uint2*>(p.codes + row * p.N + c) = make_uint2(0, 0);
+        if ((c & 31) == 0) p.scales[sf_atom_offset(row, c >> 5, p.rows)] = 0;
+    }
+}
+
+// Everything that is written of 8 columns from c on (`in`: they exist, n of
+// them): r, y, and codes with their scale.  All lanes of a warp call it.
+template <typename RT>
+__device__ __forceinline__ void fwd_outputs(const FwdParams& p, int64_t row, int c, bool in, int n, float rstd,
+                                            const float* f, const float* w) {
+    float y[kVec];
+    if (in) {
+        if (p.r != nullptr) store8(static_cast<RT*>(p.r) + row * p.ldr + c, n, p.vec_r, f);
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) y[i] = f[i] * rstd * w[i];
+        if (p.y != nullptr) store8(p.y, p.y_type, row * p.ldy + c, n, p.vec_y, y);
+    }
+    if (p.codes != nullptr) {       // N % 32 == 0: the four lanes of a block are in or out together
+        float m = 0.f;
+        if (in) {
+#pragma unroll
+            for (int i = 0; i < kVec; ++i) m = fmaxf(m, fabsf(y[i]));
+        }
+        m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+        m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+        if (in) {
+            const uint32_t b = e8m0_byte_f32(m);
+            const float inv = e8m0_inv_scale(b);
+            uint32_t q[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) q[i] = cvt_e4m3x2(y[2 * i] * inv, y[2 * i + 1] * inv);
+            *reinterpret_cast<uint2*>(p.codes + row * p.N + c) = make_uint2(q[0] | (q[1] << 16), q[2] | (q[3] << 16));
+            if ((c & 31) == 0)
+                p.scales[p.sf_canonical ? row * (p.N >> 5) + (c >> 5) : sf_atom_offset(row, c >> 5, p.rows)] = (uint8_t)b;
+        }
+    }
+}
+
 // A row's thread t owns the vectors t, t + T, ... (T threads per row): the
 // lanes of a warp read consecutive 16 bytes, and an MXFP8 block of 32 columns
 // is four neighbouring lanes.
@@ -135,14 +180,8 @@ __global__ void __launch_bounds__(MAXT) k_rms_fwd(const FwdParams p) {
     const int64_t row = p.block_row ? (int64_t)blockIdx.x
                                     : (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
     if (row >= p.rows) return;          // whole warps only (block_row: never)
-    if (row >= p.M) {                   // padding row of the codes
-#pragma unroll
-        for (int v = 0; v < VPT; ++v) {
-            const int c = (t + v * tpr) * kVec;
-            if (c >= p.N) continue;
-            *reinterpret_cast<uint2*>(p.codes + row * p.N + c) = make_uint2(0, 0);
-            if ((c & 31) == 0) p.scales[sf_atom_offset(row, c >> 5, p.rows)] = 0;
-        }
+    if (row >= p.M) {
+        pad_row<VPT>(p, row, t, tpr);
         return;
     }
     const XT* x = static_cast<const XT*>(p.x) + row * p.ldx;
@@ -181,36 +220,98 @@ __global__ void __launch_bounds__(MAXT) k_rms_fwd(const FwdParams p) {
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
         const int c = (t + v * tpr) * kVec;
-        const bool in = c < p.N;
-        const int n = p.N - c;
-        float y[kVec];
-        if (in) {
-            if (p.r != nullptr) store8(static_cast<RT*>(p.r) + row * p.ldr + c, n, p.vec_r, f[v]);
-            float w[kVec];
-            load8(p.w, p.w_type, c, n, p.vec_w, w);
+        float w[kVec];
+        if (c < p.N) load8(p.w, p.w_type, c, p.N - c, p.vec_w, w);
+        fwd_outputs<RT>(p, row, c, c < p.N, p.N - c, rstd, f[v], w);
+    }
+}
+
+// ---- long runs of aligned rows: a ring of rows in shared memory ----
+//
+// The kernels above load a row, wait for it, and compute while nothing of
+// that CTA is on its way; their registers allow too few CTAs to cover that
+// (62 % of the copy bandwidth at 24,576 x 7,168).  Here a CTA takes every G-th
+// row, and bulk copies bring the next rows into a ring of stages while it
+// works on one.  A thread reads its part of a stage into registers before the
+// row's barrier, so the stage is refilled right after it.
+
+constexpr int kMaxStages = 4;
+constexpr int kRingBytes = 200 * 1024;      // of all CTAs of an SM
+
+// Wait for a stage's bytes, bounded (about 2^16 polls of up to 50 us).
+__device__ __forceinline__ bool ring_wait(uint32_t bar, uint32_t parity) {
+    for (int i = 0; i < (1 << 16); ++i)
+        if (gg::mbar_try_wait(bar, parity)) return true;
+    return false;
+}
+
+template <typename XT, typename RT, int VPT>
+__global__ void __launch_bounds__(512) k_rms_fwd_ring(const FwdParams p, int stages, int stage_bytes) {
+    extern __shared__ __align__(128) uint8_t s_rows[];
+    __shared__ __align__(8) uint64_t s_bar[kMaxStages];
+    __shared__ float s_part[64];
+    const int t = (int)threadIdx.x, T = (int)blockDim.x;
+    const uint32_t xb = (uint32_t)p.N * sizeof(XT), rb = p.res != nullptr ? (uint32_t)p.N * sizeof(RT) : 0u;
+    const int64_t G = gridDim.x;
+    auto issue = [&](int st, int64_t row) {
+        const uint32_t bar = gg::smem_u32(&s_bar[st]), dst = gg::smem_u32(s_rows + st * stage_bytes);
+        gg::mbar_expect_tx(bar, xb + rb);
+        gg::bulk_load(dst, static_cast<const XT*>(p.x) + row * p.ldx, xb, bar);
+        if (rb != 0u) gg::bulk_load(dst + xb, static_cast<const RT*>(p.res) + row * p.ldres, rb, bar);
+    };
+    if (t == 0) {
+        for (int i = 0; i < stages; ++i) gg::mbar_init(gg::smem_u32(&s_bar[i]), 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        for (int i = 0; i < stages; ++i)
+            if (blockIdx.x + i * G < p.M) issue(i, blockIdx.x + i * G);
+    }
+    float w[VPT][kVec];
 #pragma unroll
-            for (int i = 0; i < kVec; ++i) y[i] = f[v][i] * rstd * w[i];
-            if (p.y != nullptr) store8(p.y, p.y_type, row * p.ldy + c, n, p.vec_y, y);
+    for (int v = 0; v < VPT; ++v) {
+        const int c = (t + v * T) * kVec;
+        if (c < p.N) load8(p.w, p.w_type, c, kVec, p.vec_w, w[v]);
+    }
+    __syncthreads();
+    int st = 0, half = 0;
+    uint32_t phase = 0;
+    for (int64_t row = blockIdx.x; row < p.rows; row += G) {
+        if (row >= p.M) {
+            pad_row<VPT>(p, row, t, T);
+            continue;
         }
-        if (p.codes != nullptr) {       // N % 32 == 0: the four lanes of a block are in or out together
-            float m = 0.f;
-            if (in) {
+        const bool ok = ring_wait(gg::smem_u32(&s_bar[st]), phase);
+        const XT* x = reinterpret_cast<const XT*>(s_rows + st * stage_bytes);
+        const RT* res = reinterpret_cast<const RT*>(s_rows + st * stage_bytes + xb);
+        float f[VPT][kVec];
+        float ss = ok ? 0.f : __uint_as_float(0x7FC00000u);      // bytes that never came: the row is NaN
 #pragma unroll
-                for (int i = 0; i < kVec; ++i) m = fmaxf(m, fabsf(y[i]));
-            }
-            m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
-            m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
-            if (in) {
-                const uint32_t b = e8m0_byte_f32(m);
-                const float inv = e8m0_inv_scale(b);
-                uint32_t q[4];
+        for (int v = 0; v < VPT; ++v) {
+            const int c = (t + v * T) * kVec;
+            if (c < p.N) {
+                load8(x + c, kVec, true, f[v]);
+                if (rb != 0u) {
+                    float a[kVec];
+                    load8(res + c, kVec, true, a);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) q[i] = cvt_e4m3x2(y[2 * i] * inv, y[2 * i + 1] * inv);
-                *reinterpret_cast<uint2*>(p.codes + row * p.N + c) = make_uint2(q[0] | (q[1] << 16), q[2] | (q[3] << 16));
-                if ((c & 31) == 0)
-                    p.scales[p.sf_canonical ? row * (p.N >> 5) + (c >> 5) : sf_atom_offset(row, c >> 5, p.rows)] =
-                        (uint8_t)b;
+                    for (int i = 0; i < kVec; ++i) f[v][i] += a[i];
+                }
+#pragma unroll
+                for (int i = 0; i < kVec; ++i) ss = fmaf(f[v][i], f[v][i], ss);
             }
+        }
+        ss = row_sum(ss, true, s_part, half);
+        half ^= 1;
+        if (t == 0 && row + stages * G < p.M) issue(st, row + stages * G);
+        if (++st == stages) {
+            st = 0;
+            phase ^= 1u;
+        }
+        const float rstd = 1.f / sqrtf(ss / (float)p.N + p.eps);
+        if (t == 0 && p.rstd != nullptr) p.rstd[row] = rstd;
+#pragma unroll
+        for (int v = 0; v < VPT; ++v) {
+            const int c = (t + v * T) * kVec;
+            fwd_outputs<RT>(p, row, c, c < p.N, kVec, rstd, f[v], w[v]);
         }
     }
 }
@@ -306,6 +407,88 @@ __global__ void __launch_bounds__(MAXT) k_rms_bwd(const BwdParams p) {
     }
 }
 
+// The backward pass on a ring of rows (dy, r, dres); see k_rms_fwd_ring.
+template <typename YT, typename RT, int VPT>
+__global__ void __launch_bounds__(512) k_rms_bwd_ring(const BwdParams p, int stages, int stage_bytes) {
+    extern __shared__ __align__(128) uint8_t s_rows[];
+    __shared__ __align__(8) uint64_t s_bar[kMaxStages];
+    __shared__ float s_part[64];
+    const int t = (int)threadIdx.x, T = (int)blockDim.x;
+    const uint32_t yb = (uint32_t)p.N * sizeof(YT), rb = (uint32_t)p.N * sizeof(RT);
+    const bool with_dres = p.dres != nullptr;
+    const int64_t G = gridDim.x;
+    auto issue = [&](int st, int64_t row) {
+        const uint32_t bar = gg::smem_u32(&s_bar[st]), dst = gg::smem_u32(s_rows + st * stage_bytes);
+        gg::mbar_expect_tx(bar, yb + rb + (with_dres ? rb : 0u));
+        gg::bulk_load(dst, static_cast<const YT*>(p.dy) + row * p.lddy, yb, bar);
+        gg::bulk_load(dst + yb, static_cast<const RT*>(p.r) + row * p.ldr, rb, bar);
+        if (with_dres) gg::bulk_load(dst + yb + rb, static_cast<const RT*>(p.dres) + row * p.lddres, rb, bar);
+    };
+    if (t == 0) {
+        for (int i = 0; i < stages; ++i) gg::mbar_init(gg::smem_u32(&s_bar[i]), 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        for (int i = 0; i < stages; ++i)
+            if (blockIdx.x + i * G < p.M) issue(i, blockIdx.x + i * G);
+    }
+    float w[VPT][kVec], dw[VPT][kVec];
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) {
+        const int c = (t + v * T) * kVec;
+        if (c < p.N) load8(p.w, p.w_type, c, kVec, p.vec_w, w[v]);
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) dw[v][i] = 0.f;
+    }
+    __syncthreads();
+    int st = 0, half = 0;
+    uint32_t phase = 0;
+    for (int64_t row = blockIdx.x; row < p.M; row += G) {
+        const float rstd = p.rstd[row];
+        const bool ok = ring_wait(gg::smem_u32(&s_bar[st]), phase);
+        const uint8_t* s = s_rows + st * stage_bytes;
+        float tv[VPT][kVec], xh[VPT][kVec], a[VPT][kVec];
+        float dot = ok ? 0.f : __uint_as_float(0x7FC00000u);      // bytes that never came: the row is NaN
+#pragma unroll
+        for (int v = 0; v < VPT; ++v) {
+            const int c = (t + v * T) * kVec;
+            if (c < p.N) {
+                load8(reinterpret_cast<const YT*>(s) + c, kVec, true, tv[v]);
+                load8(reinterpret_cast<const RT*>(s + yb) + c, kVec, true, xh[v]);
+                if (with_dres) load8(reinterpret_cast<const RT*>(s + yb + rb) + c, kVec, true, a[v]);
+#pragma unroll
+                for (int i = 0; i < kVec; ++i) {
+                    xh[v][i] *= rstd;
+                    dw[v][i] = fmaf(tv[v][i], xh[v][i], dw[v][i]);
+                    tv[v][i] *= w[v][i];
+                    dot = fmaf(tv[v][i], xh[v][i], dot);
+                }
+            }
+        }
+        const float mean = row_sum(dot, true, s_part, half) / (float)p.N;
+        half ^= 1;
+        if (t == 0 && row + stages * G < p.M) issue(st, row + stages * G);
+        if (++st == stages) {
+            st = 0;
+            phase ^= 1u;
+        }
+#pragma unroll
+        for (int v = 0; v < VPT; ++v) {
+            const int c = (t + v * T) * kVec;
+            if (c >= p.N) continue;
+            float d[kVec];
+#pragma unroll
+            for (int i = 0; i < kVec; ++i) d[i] = rstd * (tv[v][i] - xh[v][i] * mean) + (with_dres ? a[v][i] : 0.f);
+            store8(static_cast<RT*>(p.dx) + row * p.lddx + c, kVec, p.vec_dx, d);
+        }
+    }
+    if (p.part != nullptr) {
+#pragma unroll
+        for (int v = 0; v < VPT; ++v) {
+            const int c = (t + v * T) * kVec;
+            if (c < p.N) store8(p.part + (int64_t)blockIdx.x * p.N + c, kVec, true, dw[v]);
+        }
+    }
+}
+
 // Column sums of partial sums [P, N]: a CTA owns 32 columns, its warps every
 // 32nd row, and one warp adds the 32 results in order.  P = 0 writes zeros.
 __global__ void __launch_bounds__(1024) k_dw_sum(const float* __restrict__ part, int P, int N, float* __restrict__ dw) {
@@ -313,8 +496,10 @@ __global__ void __launch_bounds__(1024) k_dw_sum(const float* __restrict__ part,
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int c = blockIdx.x * 32 + lane;
     float a = 0.f;
-    if (c < N)
+    if (c < N) {
+#pragma unroll 8
         for (int r = warp; r < P; r += 32) a += part[(int64_t)r * N + c];
+    }
     s[warp][lane] = a;
     __syncthreads();
     // warp w adds column w of the 32 x 32 sums
@@ -334,6 +519,27 @@ static Shape shape_of(int N) {
     return {true, 4, (nvec + 127) / 128 * 32, 1};
 }
 
+// The ring kernels' launch: CTAs of an SM, stages, threads.
+struct Ring {
+    bool use;
+    int vpt, threads, ctas, stages, stage_bytes;
+};
+// `row_bytes`: what a stage holds.  Rows of 1,025 to 16,384 columns, at least
+// two stages, and enough rows that every CTA has some to run ahead on.
+static Ring ring_of(int64_t M, int N, size_t row_bytes, bool aligned, int sms) {
+    Ring r{};
+    const int nvec = N / kVec;
+    if (!aligned || N % kVec != 0 || N <= 1024 || N > 16384) return r;
+    r.vpt = N <= 8192 ? 2 : 4;
+    r.threads = (nvec + 32 * r.vpt - 1) / (32 * r.vpt) * 32;
+    r.stage_bytes = (int)((row_bytes + 127) / 128 * 128);
+    r.ctas = std::max(1, std::min(4, 1024 / r.threads));
+    while (r.ctas > 1 && kRingBytes / r.ctas < 2 * r.stage_bytes) --r.ctas;
+    r.stages = std::min(kMaxStages, kRingBytes / r.ctas / r.stage_bytes);
+    r.use = r.stages >= 2 && M >= 2 * (int64_t)sms;
+    return r;
+}
+
 static int esize(int type) { return type == MOE_TYPE_F32 ? 4 : 2; }
 static bool type_ok(int t) { return t == MOE_TYPE_BF16 || t == MOE_TYPE_F32; }
 // 16-byte loads of 8 elements: the base and every row's start are aligned
@@ -351,7 +557,16 @@ static int partials(int64_t M, int N) {
 }
 
 template <typename XT, typename RT>
-static void launch_fwd(const FwdParams& p, const Shape& s, cudaStream_t st) {
+static void launch_fwd(const FwdParams& p, const Shape& s, const Ring& q, int sms, cudaStream_t st) {
+    if (q.use) {
+        const unsigned g = (unsigned)std::min<int64_t>(p.rows, (int64_t)sms * q.ctas);
+        const size_t bytes = (size_t)q.stages * q.stage_bytes;
+        if (q.vpt == 2)
+            k_rms_fwd_ring<XT, RT, 2><<<g, q.threads, bytes, st>>>(p, q.stages, q.stage_bytes);
+        else
+            k_rms_fwd_ring<XT, RT, 4><<<g, q.threads, bytes, st>>>(p, q.stages, q.stage_bytes);
+        return;
+    }
     const unsigned grid = (unsigned)((p.rows + s.rows_per_cta - 1) / s.rows_per_cta);
     if (s.vpt == 1)
         k_rms_fwd<XT, RT, 1, 128><<<grid, s.threads, 0, st>>>(p);
@@ -365,7 +580,15 @@ static void launch_fwd(const FwdParams& p, const Shape& s, cudaStream_t st) {
         k_rms_fwd<XT, RT, 4, 1024><<<grid, s.threads, 0, st>>>(p);
 }
 template <typename YT, typename RT>
-static void launch_bwd(const BwdParams& p, const Shape& s, int groups, cudaStream_t st) {
+static void launch_bwd(const BwdParams& p, const Shape& s, const Ring& q, int groups, cudaStream_t st) {
+    if (q.use) {
+        const size_t bytes = (size_t)q.stages * q.stage_bytes;
+        if (q.vpt == 2)
+            k_rms_bwd_ring<YT, RT, 2><<<groups, q.threads, bytes, st>>>(p, q.stages, q.stage_bytes);
+        else
+            k_rms_bwd_ring<YT, RT, 4><<<groups, q.threads, bytes, st>>>(p, q.stages, q.stage_bytes);
+        return;
+    }
     const unsigned grid = (unsigned)(groups / s.rows_per_cta);
     if (s.vpt == 1)
         k_rms_bwd<YT, RT, 1, 128><<<grid, s.threads, 0, st>>>(p);
@@ -379,7 +602,27 @@ static void launch_bwd(const BwdParams& p, const Shape& s, int groups, cudaStrea
         k_rms_bwd<YT, RT, 4, 1024><<<grid, s.threads, 0, st>>>(p);
 }
 
+template <typename XT, typename RT>
+static cudaError_t set_ring() {
+    const void* ks[] = {(const void*)k_rms_fwd_ring<XT, RT, 2>, (const void*)k_rms_fwd_ring<XT, RT, 4>,
+                        (const void*)k_rms_bwd_ring<XT, RT, 2>, (const void*)k_rms_bwd_ring<XT, RT, 4>};
+    for (const void* k : ks) {
+        const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes);
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
+}
+
 }  // namespace norm
+
+cudaError_t norm_set_attributes() {
+    using namespace norm;
+    const cudaError_t es[] = {set_ring<__nv_bfloat16, __nv_bfloat16>(), set_ring<__nv_bfloat16, float>(),
+                              set_ring<float, __nv_bfloat16>(), set_ring<float, float>()};
+    for (cudaError_t e : es)
+        if (e != cudaSuccess) return e;
+    return cudaSuccess;
+}
 
 // out[c] = sum over the P rows of part [P, N], in a fixed order; zeros for P = 0
 void launch_column_sum(const float* part, int P, int N, float* out, cudaStream_t s) {
@@ -420,15 +663,18 @@ extern "C" moe_status_t rmsnorm_residual_fwd(const void* x, int x_type, int64_t 
     p.block_row = s.block_row;
     p.vec_x = vec_ok(x, ldx, x_type), p.vec_res = vec_ok(res, ldres, res_type), p.vec_w = moe_aligned16(w);
     p.vec_r = vec_ok(r, ldr, res_type), p.vec_y = vec_ok(y, ldy, y_type);
+    const int sms = device_sm_count();
+    const Ring q = ring_of(M, N, (size_t)N * (esize(x_type) + (res ? esize(res_type) : 0)),
+                           p.vec_x && (!res || p.vec_res), sms);
     cudaStream_t st = (cudaStream_t)stream;
     if (x_type == MOE_TYPE_BF16 && res_type == MOE_TYPE_BF16)
-        launch_fwd<__nv_bfloat16, __nv_bfloat16>(p, s, st);
+        launch_fwd<__nv_bfloat16, __nv_bfloat16>(p, s, q, sms, st);
     else if (x_type == MOE_TYPE_BF16)
-        launch_fwd<__nv_bfloat16, float>(p, s, st);
+        launch_fwd<__nv_bfloat16, float>(p, s, q, sms, st);
     else if (res_type == MOE_TYPE_BF16)
-        launch_fwd<float, __nv_bfloat16>(p, s, st);
+        launch_fwd<float, __nv_bfloat16>(p, s, q, sms, st);
     else
-        launch_fwd<float, float>(p, s, st);
+        launch_fwd<float, float>(p, s, q, sms, st);
     MOE_CHECK_LAUNCH();
     return MOE_OK;
 }
@@ -454,7 +700,7 @@ extern "C" moe_status_t rmsnorm_residual_bwd(const void* dy, int dy_type, int64_
                     moe_aligned16(ws),
                 MOE_ERR_ALIGNMENT);
     const Shape s = shape_of(N);
-    const int groups = partials(M, N);
+    int groups = partials(M, N);
     MOE_REQUIRE(!dw || M == 0 || (ws && ws_bytes >= rmsnorm_bwd_workspace_size(M, N)), MOE_ERR_WORKSPACE);
     MOE_REQUIRE(device_initialized(), MOE_ERR_NOT_INITIALIZED);
     cudaStream_t st = (cudaStream_t)stream;
@@ -466,14 +712,18 @@ extern "C" moe_status_t rmsnorm_residual_bwd(const void* dy, int dy_type, int64_
         p.block_row = s.block_row;
         p.vec_dy = vec_ok(dy, lddy, dy_type), p.vec_r = vec_ok(r, ldr, r_type), p.vec_w = moe_aligned16(w);
         p.vec_dres = vec_ok(dres, lddres, r_type), p.vec_dx = vec_ok(dx, lddx, r_type);
+        const int sms = device_sm_count();
+        const Ring q = ring_of(M, N, (size_t)N * (esize(dy_type) + (dres ? 2 : 1) * esize(r_type)),
+                               p.vec_dy && p.vec_r && (!dres || p.vec_dres), sms);
+        if (q.use) groups = (int)std::min<int64_t>(groups, (int64_t)sms * q.ctas);
         if (dy_type == MOE_TYPE_BF16 && r_type == MOE_TYPE_BF16)
-            launch_bwd<__nv_bfloat16, __nv_bfloat16>(p, s, groups, st);
+            launch_bwd<__nv_bfloat16, __nv_bfloat16>(p, s, q, groups, st);
         else if (dy_type == MOE_TYPE_BF16)
-            launch_bwd<__nv_bfloat16, float>(p, s, groups, st);
+            launch_bwd<__nv_bfloat16, float>(p, s, q, groups, st);
         else if (r_type == MOE_TYPE_BF16)
-            launch_bwd<float, __nv_bfloat16>(p, s, groups, st);
+            launch_bwd<float, __nv_bfloat16>(p, s, q, groups, st);
         else
-            launch_bwd<float, float>(p, s, groups, st);
+            launch_bwd<float, float>(p, s, q, groups, st);
         MOE_CHECK_LAUNCH();
     }
     if (dw) {

@@ -269,3 +269,43 @@ def test_refusals(ops):
     refused(bad, ops.rmsnorm_residual_bwd, x, x, w, rstd[:3])
     small = torch.empty((64,), dtype=torch.uint8, device="cuda")
     refused(ops.MOE_ERR_WORKSPACE, ops.rmsnorm_residual_bwd, x, x, w, rstd, ws=small)
+
+
+@pytest.mark.parametrize("m,n", [(304, 1032), (700, 4096), (931, 7168), (2500, 2000), (305, 8200), (400, 16384)])
+@pytest.mark.parametrize("xt,rt,res", [(torch.bfloat16, torch.bfloat16, True), (torch.bfloat16, torch.float32, True),
+                                       (torch.float32, torch.bfloat16, True), (torch.float32, torch.float32, False)])
+def test_many_rows(ops, m, n, xt, rt, res):
+    """Rows that come through the ring of stages, several to a CTA: forward
+    (in place too) and backward."""
+    x, w, dy = mat(m, n, 1, xt, ld=n + 8), mat(1, n, 3)[0], mat(m, n, 4, xt)
+    rs = mat(m, n, 2, rt, 3.0, ld=n + 16) if res else None
+    wr, wrstd, wy = D.rmsnorm_residual(f64(x), f64(rs) if res else None, f64(w), EPS)
+    y, r, rstd, _, _ = ops.rmsnorm_residual_fwd(x, w, rs, EPS, y_dtype=xt)
+    check_rows(y, wy, xt, "y")
+    check_rows(rstd[:, None], wrstd[:, None], torch.float32, "rstd")
+    if res:
+        check_rows(r, wr, rt, "r")
+        y2, r2, _, _, _ = ops.rmsnorm_residual_fwd(x, w, rs, EPS, y=x, r=rs)
+        assert torch.equal(y2, y) and torch.equal(r2, r)
+    else:
+        r = x
+    dr = mat(m, n, 5, r.dtype) if res else None
+    dx, dw = ops.rmsnorm_residual_bwd(dy, r, w, rstd, dr)
+    drn = f64(dr) if res else None
+    want, wdw = D.rmsnorm_residual_bwd(f64(dy), f64(r), f64(w), f64(rstd), drn)
+    assert np.all(np.abs(f64(dx) - want) <= bwd_tol(f64(dy), f64(r), f64(w), f64(rstd), drn, r.dtype, want) + 1e-30)
+    size = np.sum(np.abs(f64(dy) * f64(r) * f64(rstd)[:, None]), axis=0)
+    # a CTA adds m / 152 rows one after the other at most (one CTA per SM), then up to 608 partial sums
+    assert np.all(np.abs(f64(dw) - wdw) <= size * (m / 152 + 40) * 2.0 ** -24 + 1e-30)
+    if res:
+        assert torch.equal(ops.rmsnorm_residual_bwd(dy, r, w, rstd, dr, dx=dr)[0], dx)
+
+
+@pytest.mark.parametrize("m,n,layout", [(400, 1152, "atoms"), (1000, 7168, "atoms"), (500, 2080, "canonical")])
+def test_mxfp8_output_of_many_rows(ops, m, n, layout):
+    layout = ops.MOE_SF_ATOMS if layout == "atoms" else ops.MOE_SF_CANONICAL
+    x, res, w = mat(m, n, 1), mat(m, n, 2), mat(1, n, 3)[0]
+    y, _, _, codes, scales = ops.rmsnorm_residual_fwd(x, w, res, EPS, want_codes=True, sf_layout=layout)
+    wy = D.rmsnorm_residual(f64(x), f64(res), f64(w), EPS)[2]
+    check_rows(y, wy, torch.bfloat16, "y")
+    check_mx(ops, codes, scales, wy, m, n, layout)
