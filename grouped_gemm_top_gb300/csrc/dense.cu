@@ -9,13 +9,15 @@
 // ("X-major": X is the contiguous axis.)  The tensor core takes either order
 // of both operands, so nothing is transposed or copied beforehand.
 //
-// Tile: 256 x 256 of D per CTA pair (tcgen05.mma.cta_group::2, M = 256,
-// N = 256), 64 deep per pipeline stage; CTA r of the pair holds 128 of the
-// A rows and 128 of the B rows, 32 KB per stage.  Two accumulators of 256
-// TMEM columns, so that the epilogue of one tile runs under the next tile's
-// products.  Per k-step the pair reads 64 KB for 256 x 256 x 64 products,
-// which two SMs take 256 cycles over: half the operand traffic per SM of a
-// 128 x 256 tile on one SM.
+// Tile: 256 x bn of D per CTA pair (tcgen05.mma.cta_group::2, M = 256,
+// N = bn <= 256), 64 deep per pipeline stage; CTA r of the pair holds 128 of
+// the A rows and bn / 2 of the B rows, 32 KB per stage.  Two accumulators of
+// 256 TMEM columns, so that the epilogue of one tile runs under the next
+// tile's products.  Per k-step the pair reads 64 KB for 256 x 256 x 64
+// products: half the operand traffic per SM of a 128 x 256 tile on one SM.
+// D leaves through shared memory: each epilogue warp stages 32 rows x 32
+// columns and one TMA store writes them, clipped at D's edges, which
+// leaves whole lines to the memory system and the warp free.
 //
 // Warps: 0 TMA, 1 MMA (of the leader CTA), 4-11 epilogue.  All waits are
 // bounded, as in the grouped GEMM kernels.
@@ -26,19 +28,24 @@
 
 namespace moe {
 
-bool make_bf16_map(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, int64_t ld, int box_rows);  // gemm.cu
+// gemm.cu
+bool make_bf16_map(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, int64_t ld, int box_rows);
+bool make_store_map(CUtensorMap* m, void* base, int64_t rows, int64_t cols, int64_t ld, bool f32);
 
 namespace dense {
 
 using namespace gg;
 
-constexpr int TM = 256, TN = 256, TK = 64;      // the pair's tile and the k-step
+constexpr int TM = 256, TK = 64;                // rows of the pair's tile, the k-step
+constexpr int ACC_COLS = 256;                   // TMEM columns of an accumulator
 constexpr int HALF_BYTES = 128 * TK * 2;        // one CTA's rows of an operand per stage
 constexpr int STAGES = 6;
 constexpr int NACC = 2;
 constexpr int OFF_A = 0;
 constexpr int OFF_B = OFF_A + STAGES * HALF_BYTES;
-constexpr int OFF_BAR = OFF_B + STAGES * HALF_BYTES;      // full[S], empty[S], tfull[A], tempty[A], drain
+constexpr int OFF_EPI = OFF_B + STAGES * HALF_BYTES;      // staging, 4 KB per epilogue warp
+constexpr int EPI_STAGE = 4096;
+constexpr int OFF_BAR = OFF_EPI + EPI_WARPS * EPI_STAGE;      // full[S], empty[S], tfull[A], tempty[A], drain
 constexpr int NBAR = 2 * STAGES + 2 * NACC + 1;
 constexpr int OFF_MISC = OFF_BAR + 8 * NBAR;
 constexpr int SMEM_BYTES = OFF_MISC + 16 + 1024;
@@ -47,7 +54,7 @@ static_assert(SMEM_BYTES <= 232448, "shared memory budget");
 // What the epilogue makes of the product v:
 //   EPI_LINEAR  z = v + bias; y = act(z) + residual (bf16; z stored when asked for)
 //   EPI_F32     y = v (fp32)
-//   EPI_GLU     columns [0, 128) of the tile are gate, [128, 256) up:
+//   EPI_GLU     columns [0, bn / 2) of the tile are gate, [bn / 2, bn) up:
 //               h = act(gate) * up; a = [gate | up] stored when asked for
 enum { EPI_LINEAR = 0, EPI_F32 = 1, EPI_GLU = 2 };
 
@@ -57,6 +64,7 @@ struct Params {
     int64_t K;
     int64_t m_tiles;
     int n_tiles, nk, band;
+    int bn;                 // columns of the pair's tile
     int up;                 // GLU: column of W where the up half begins
     int act;
     void* y;                // bf16, EPI_F32: fp32
@@ -71,11 +79,11 @@ struct Params {
 };
 
 // Instruction descriptor: bf16 A and B, fp32 D, M = 256 over the pair,
-// N = 256; bits 15 and 16 say that A and B lie M- and N-major.
+// N = bn; bits 15 and 16 say that A and B lie M- and N-major.
 template <bool A_MN, bool B_MN>
-__device__ __forceinline__ constexpr uint32_t make_idesc_pair() {
+__device__ __forceinline__ uint32_t make_idesc_pair(int bn) {
     return (1u << 4) | (1u << 7) | (1u << 10) | (A_MN ? 1u << 15 : 0u) | (B_MN ? 1u << 16 : 0u) |
-           ((uint32_t)(TN >> 3) << 17) | ((uint32_t)(TM >> 4) << 24);
+           ((uint32_t)(bn >> 3) << 17) | ((uint32_t)(TM >> 4) << 24);
 }
 
 // Shared-memory descriptor of an operand that lies M- or N-major, 128-byte
@@ -140,45 +148,57 @@ __device__ __forceinline__ void load32(const __nv_bfloat16* p, int n, float* f) 
         for (int i = 0; i < 32; ++i) f[i] = i < n ? __bfloat162float(p[i]) : 0.f;
     }
 }
-__device__ __forceinline__ void store32(__nv_bfloat16* p, int n, const float* f) {
-    if (n >= 32) {
-        store_row32(p, f);
-    } else {
+// The columns of a row from `p` on, n < 32 of them, element by element.
+template <typename T>
+__device__ __forceinline__ void store_edge(T* p, int n, const float* v) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i)
-            if (i < n) p[i] = __float2bfloat16_rn(f[i]);
-    }
-}
-__device__ __forceinline__ void store32(float* p, int n, const float* f) {
-    if (n >= 32) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            reinterpret_cast<float4*>(p)[i] = make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 32; ++i)
-            if (i < n) p[i] = f[i];
+    for (int i = 0; i < 32; ++i) {
+        if (i < n) {
+            if constexpr (sizeof(T) == 4) p[i] = v[i];
+            else p[i] = __float2bfloat16_rn(v[i]);
+        }
     }
 }
 
-// z -> y for 32 columns of a row, in place.
-__device__ __forceinline__ void linear32(const Params& p, int64_t row, int col, int n, float* v) {
-    if (p.bias != nullptr) {
-#pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] += i < n ? __bfloat162float(p.bias[col + i]) : 0.f;
+// A warp's way out: 32 rows (one per lane) x 32 columns staged in the warp's
+// 4 KB and written by a TMA store (bf16: two boxes of 2 KB that alternate,
+// 64-byte swizzle; fp32: one of 4 KB, 128-byte swizzle; either way the
+// row-per-lane stores to shared memory meet no bank twice).
+struct Out {
+    uint32_t buf;
+    int lane;
+    uint32_t boxes;
+    __device__ __forceinline__ void send(const CUtensorMap* map, uint32_t b, int col, int64_t row0) {
+        fence_proxy_async_shared();
+        __syncwarp();
+        if (lane == 0) {
+            tma_store_2d(map, b, col, (int)row0);
+            bulk_commit_group();
+        }
     }
-    if (p.z != nullptr) store32(p.z + row * p.ldz + col, n, v);
-    if (p.act != MOE_ACT_NONE) {
+    __device__ __forceinline__ void bf16(const CUtensorMap* map, int col, int64_t row0, const float* v) {
+        const uint32_t b = buf + (boxes++ & 1u) * 2048u;
+        if (lane == 0) bulk_wait_group_read1();      // the box before the last one has been read
+        __syncwarp();
+        const uint32_t row = b + 64u * lane, sw = (uint32_t)(lane >> 1) & 3u;
 #pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] = act_of(v[i], p.act);
+        for (int c = 0; c < 4; ++c)
+            st_shared_v4(row + (((uint32_t)c ^ sw) << 4), pack_bf16x2(v[8 * c], v[8 * c + 1]),
+                         pack_bf16x2(v[8 * c + 2], v[8 * c + 3]), pack_bf16x2(v[8 * c + 4], v[8 * c + 5]),
+                         pack_bf16x2(v[8 * c + 6], v[8 * c + 7]));
+        send(map, b, col, row0);
     }
-    if (p.res != nullptr) {
-        float r[32];
-        load32(p.res + row * p.ldres + col, n, r);
+    __device__ __forceinline__ void f32(const CUtensorMap* map, int col, int64_t row0, const float* v) {
+        if (lane == 0) bulk_wait_group_read0();
+        __syncwarp();
+        const uint32_t row = buf + 128u * lane, sw = (uint32_t)lane & 7u;
 #pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] += r[i];
+        for (int c = 0; c < 8; ++c)
+            st_shared_v4(row + (((uint32_t)c ^ sw) << 4), __float_as_uint(v[4 * c]), __float_as_uint(v[4 * c + 1]),
+                         __float_as_uint(v[4 * c + 2]), __float_as_uint(v[4 * c + 3]));
+        send(map, buf, col, row0);
     }
-}
+};
 
 struct Tile {
     int64_t mt;
@@ -190,9 +210,13 @@ __device__ __forceinline__ Tile get_tile(const Params& p, int64_t t) {
     return r;
 }
 
+// tmY, tmZ, tmZ2: y (h), z (a's gate half) and a's up half as TMA stores see
+// them, boxes of 32 columns x 32 rows.
 template <bool A_MN, bool B_MN, int EPI>
 __global__ void __launch_bounds__(THREADS, 1)
-    k_dense_pair(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, const Params p) {
+    k_dense_pair(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                 const __grid_constant__ CUtensorMap tmY, const __grid_constant__ CUtensorMap tmZ,
+                 const __grid_constant__ CUtensorMap tmZ2, const Params p) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -243,10 +267,14 @@ __global__ void __launch_bounds__(THREADS, 1)
         int stage = 0;
         uint32_t phase = 0;
         bool aborted = false;
+        // B: bn / 2 rows, or bn / 2 columns in boxes of 64
+        const int b_boxes = (p.bn / 2 + 63) / 64;
+        const uint32_t tx = 2u * (HALF_BYTES + (uint32_t)(B_MN ? b_boxes * 64 : p.bn / 2) * TK * 2);
         for (int64_t t = pair; t < total && !aborted; t += npairs) {
             const Tile ti = get_tile(p, t);
             const int am = (int)(ti.mt * TM) + 128 * (int)rank;
-            const int bn = EPI == EPI_GLU ? ti.nt * 128 + p.up * (int)rank : ti.nt * TN + 128 * (int)rank;
+            const int bh = p.bn / 2;
+            const int bn = EPI == EPI_GLU ? ti.nt * bh + p.up * (int)rank : ti.nt * p.bn + bh * (int)rank;
             for (int ks = 0; ks < p.nk; ++ks) {
                 if (!mbar_wait_cluster(empty_bar(stage), phase ^ 1u, p, abort_flag)) {
                     aborted = true;
@@ -255,7 +283,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 const int k = ks * TK;
                 // both CTAs' bytes complete on the leader's full barrier
                 const uint32_t fb = leader_full[stage];
-                if (leader) mbar_expect_tx(full_bar(stage), 4 * HALF_BYTES);
+                if (leader) mbar_expect_tx(full_bar(stage), tx);
                 const uint32_t sa = smem_u32(smem + OFF_A + stage * HALF_BYTES);
                 const uint32_t sb = smem_u32(smem + OFF_B + stage * HALF_BYTES);
                 if constexpr (A_MN) {
@@ -266,7 +294,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 }
                 if constexpr (B_MN) {
                     tma2_load_2d(sb, &tmB, bn, k, fb);
-                    tma2_load_2d(sb + HALF_BYTES / 2, &tmB, bn + 64, k, fb);
+                    if (b_boxes > 1) tma2_load_2d(sb + HALF_BYTES / 2, &tmB, bn + 64, k, fb);
                 } else {
                     tma2_load_2d(sb, &tmB, k, bn, fb);
                 }
@@ -291,10 +319,11 @@ __global__ void __launch_bounds__(THREADS, 1)
         int stage = 0, acc = 0;
         uint32_t phase = 0, acc_phase = 0;
         bool aborted = false, issued = false;
+        const uint32_t idesc = make_idesc_pair<A_MN, B_MN>(p.bn);
         for (int64_t t = pair; t < total && !aborted; t += npairs) {
             if (!mbar_wait_cluster(tempty_bar(acc), acc_phase ^ 1u, p, abort_flag)) break;
             tc_fence_after();
-            const uint32_t d_tmem = tmem_base + (uint32_t)(acc * TN);
+            const uint32_t d_tmem = tmem_base + (uint32_t)(acc * ACC_COLS);
             for (int ks = 0; ks < p.nk; ++ks) {
                 if (!mbar_wait_cluster(full_bar(stage), phase, p, abort_flag)) {
                     aborted = true;
@@ -306,7 +335,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
                 for (int kk = 0; kk < TK / 16; ++kk)
                     tc_mma2_bf16(d_tmem, adesc + k16_step<A_MN>() * kk, bdesc + k16_step<B_MN>() * kk,
-                                 make_idesc_pair<A_MN, B_MN>(), (ks | kk) != 0 ? 1u : 0u);
+                                 idesc, (ks | kk) != 0 ? 1u : 0u);
                 issued = true;
                 tc_commit_both(empty_bar(stage));
                 if (++stage == STAGES) {
@@ -335,55 +364,86 @@ __global__ void __launch_bounds__(THREADS, 1)
         int acc = 0;
         uint32_t acc_phase = 0;
         const uint32_t lane_base = tmem_base + ((uint32_t)(quarter * 32) << 16);
+        Out out{smem_u32(smem + OFF_EPI + ew * EPI_STAGE), lane, 0u};
+        // this warp's chunks of 32 columns: the first or the second half of them
+        const int chunks = EPI == EPI_GLU ? p.bn / 64 : p.bn / 32;
+        const int c0 = half == 0 ? 0 : (chunks + 1) / 2, c1 = half == 0 ? (chunks + 1) / 2 : chunks;
         for (int64_t t = pair; t < total; t += npairs) {
             const Tile ti = get_tile(p, t);
-            const int64_t row = ti.mt * TM + 128 * rank + quarter * 32 + lane;
+            const int64_t row0 = ti.mt * TM + 128 * rank + quarter * 32;
+            const int64_t row = row0 + lane;
             if (!mbar_wait_cluster(tfull_bar(acc), acc_phase, p, abort_flag)) break;
             tc_fence_after();
-            const uint32_t tacc = lane_base + (uint32_t)(acc * TN);
-            if constexpr (EPI == EPI_GLU) {
-                for (int c = 0; c < 2; ++c) {
-                    float g[32], u[32];
-                    const int c32 = half * 64 + 32 * c;
-                    tmem_ld32(tacc + c32, g);
-                    tmem_ld32(tacc + 128 + c32, u);
-                    const int col = ti.nt * 128 + c32;
-                    const int n = p.N - col;
-                    if (row < p.M && n > 0) {
-                        if (p.z != nullptr) {
-                            store32(p.z + row * p.ldz + col, n, g);
-                            store32(p.z + row * p.ldz + p.N + col, n, u);
-                        }
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) u[i] *= act_of(g[i], p.act);
-                        store32(static_cast<__nv_bfloat16*>(p.y) + row * p.ldy + col, n, u);
-                    }
+            const uint32_t tacc = lane_base + (uint32_t)(acc * ACC_COLS);
+            const uint32_t tempty = mapa(tempty_bar(acc), 0);
+            for (int c = c0; c < c1; ++c) {
+                float v[32], u[EPI == EPI_GLU ? 32 : 1];
+                tmem_ld32(tacc + 32 * c, v);
+                if constexpr (EPI == EPI_GLU) tmem_ld32(tacc + p.bn / 2 + 32 * c, u);
+                if (c == c1 - 1) {      // the accumulator is read: the next tile may have it
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_remote(tempty);
                 }
-            } else {
-                for (int c = 0; c < 4; ++c) {
-                    float v[32];
-                    const int c32 = half * 128 + 32 * c;
-                    tmem_ld32(tacc + c32, v);
-                    const int col = ti.nt * TN + c32;
-                    const int n = p.N - col;
-                    if (row < p.M && n > 0) {
-                        if constexpr (EPI == EPI_F32) {
-                            store32(static_cast<float*>(p.y) + row * p.ldy + col, n, v);
-                        } else {
-                            linear32(p, row, col, n, v);
-                            store32(static_cast<__nv_bfloat16*>(p.y) + row * p.ldy + col, n, v);
-                        }
+                const int col = ti.nt * (EPI == EPI_GLU ? p.bn / 2 : p.bn) + 32 * c;
+                const int n = p.N - col;
+                if (n <= 0 || row0 >= p.M) continue;      // the whole warp
+                // a TMA store is clipped at D's edge to whole 16 bytes: the
+                // last columns of a width that is no multiple of 8 go
+                // element by element (GLU: f is one)
+                const bool edge = EPI != EPI_GLU && n < 32 && (p.N & 7) != 0;
+                if constexpr (EPI == EPI_GLU) {
+                    if (p.z != nullptr) {
+                        out.bf16(&tmZ, col, row0, v);
+                        out.bf16(&tmZ2, col, row0, u);
                     }
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) u[i] *= act_of(v[i], p.act);
+                    out.bf16(&tmY, col, row0, u);
+                } else if constexpr (EPI == EPI_F32) {
+                    if (!edge)
+                        out.f32(&tmY, col, row0, v);
+                    else if (row < p.M)
+                        store_edge(static_cast<float*>(p.y) + row * p.ldy + col, n, v);
+                } else {
+                    if (p.bias != nullptr) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) v[i] += i < n ? __bfloat162float(p.bias[col + i]) : 0.f;
+                    }
+                    if (p.z != nullptr) {
+                        if (!edge)
+                            out.bf16(&tmZ, col, row0, v);
+                        else if (row < p.M)
+                            store_edge(p.z + row * p.ldz + col, n, v);
+                    }
+                    if (p.act != MOE_ACT_NONE) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) v[i] = act_of(v[i], p.act);
+                    }
+                    if (p.res != nullptr && row < p.M) {
+                        float r[32];
+                        load32(p.res + row * p.ldres + col, n, r);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) v[i] += r[i];
+                    }
+                    if (!edge)
+                        out.bf16(&tmY, col, row0, v);
+                    else if (row < p.M)
+                        store_edge(static_cast<__nv_bfloat16*>(p.y) + row * p.ldy + col, n, v);
                 }
             }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_remote(mapa(tempty_bar(acc), 0));
+            if (c0 == c1) {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_remote(tempty);
+            }
             if (++acc == NACC) {
                 acc = 0;
                 acc_phase ^= 1u;
             }
         }
+        if (lane == 0) bulk_wait_group0();      // the stores are complete
+        __syncwarp();
     }
 
     tc_fence_before();
@@ -787,20 +847,29 @@ struct Mat {
 
 template <bool A_MN, bool B_MN, int EPI>
 static moe_status_t product(const Mat& a, const Mat& b, Params p, cudaStream_t s) {
-    CUtensorMap tmA, tmB;
-    MOE_REQUIRE(make_bf16_map(&tmA, a.p, a.rows, a.cols, a.ld, A_MN ? TK : 128) &&
-                    make_bf16_map(&tmB, b.p, b.rows, b.cols, b.ld, B_MN ? TK : 128),
-                MOE_ERR_CUDA);
     p.m_tiles = (p.M + TM - 1) / TM;
-    p.n_tiles = EPI == EPI_GLU ? (p.N + 127) / 128 : (p.N + TN - 1) / TN;
+    p.bn = 256;
+    const int cols = EPI == EPI_GLU ? p.bn / 2 : p.bn;      // of D per tile
+    p.n_tiles = (p.N + cols - 1) / cols;
     p.nk = (int)((p.K + TK - 1) / TK);
     p.band = 8;
     p.timeout_ns = 2000000000ull;
+    CUtensorMap tmA, tmB, tmY, tmZ, tmZ2;
+    MOE_REQUIRE(make_bf16_map(&tmA, a.p, a.rows, a.cols, a.ld, A_MN ? TK : 128) &&
+                    make_bf16_map(&tmB, b.p, b.rows, b.cols, b.ld, B_MN ? TK : p.bn / 2) &&
+                    make_store_map(&tmY, p.y, p.M, p.N, p.ldy, EPI == EPI_F32),
+                MOE_ERR_CUDA);
+    tmZ = tmZ2 = tmY;
+    if (p.z != nullptr)
+        MOE_REQUIRE(make_store_map(&tmZ, p.z, p.M, p.N, p.ldz, false) &&
+                        (EPI != EPI_GLU || make_store_map(&tmZ2, p.z + p.N, p.M, p.N, p.ldz, false)),
+                    MOE_ERR_CUDA);
     const int clusters = (int)std::min<int64_t>(p.m_tiles * p.n_tiles, g_max_clusters);
     MOE_REQUIRE(clusters > 0, MOE_ERR_NOT_INITIALIZED);
     cudaLaunchAttribute attr[1];
     cudaLaunchConfig_t cfg = launch_cfg(clusters, s, attr);
-    if (cudaLaunchKernelEx(&cfg, k_dense_pair<A_MN, B_MN, EPI>, tmA, tmB, p) != cudaSuccess) return MOE_ERR_CUDA;
+    if (cudaLaunchKernelEx(&cfg, k_dense_pair<A_MN, B_MN, EPI>, tmA, tmB, tmY, tmZ, tmZ2, p) != cudaSuccess)
+        return MOE_ERR_CUDA;
     MOE_CHECK_LAUNCH();
     return MOE_OK;
 }

@@ -597,6 +597,19 @@ bool make_bf16_map(CUtensorMap* m, const void* base, int64_t rows, int64_t cols,
     return r == CUDA_SUCCESS;
 }
 
+// bf16 or fp32 matrix [rows, cols] for TMA stores of 32 x 32 boxes (64-byte
+// swizzle for bf16, 128-byte for fp32).
+bool make_store_map(CUtensorMap* m, void* base, int64_t rows, int64_t cols, int64_t ld, bool f32) {
+    cuuint64_t gdim[2] = {(cuuint64_t)cols, (cuuint64_t)rows}, gstr[1] = {(cuuint64_t)ld * (f32 ? 4 : 2)};
+    cuuint32_t box[2] = {32, 32}, estr[2] = {1, 1};
+    if (g_encode == nullptr) return false;
+    CUresult r = g_encode(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, gdim,
+                          gstr, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                          f32 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS;
+}
+
 // rank-2/3 uint8 tensor map, 128x128 boxes, 128-byte swizzle
 static bool make_map(CUtensorMap* m, const void* base, int rank, const uint64_t* dims, const uint64_t* strides_bytes,
                      int box_rows = 128) {
