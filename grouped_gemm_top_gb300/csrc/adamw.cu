@@ -28,7 +28,7 @@
 
 #include <algorithm>
 
-#include "common.cuh"
+#include "gemm_common.cuh"
 
 namespace moe {
 namespace adamw {
@@ -51,7 +51,7 @@ struct Entry {
     int64_t n;
     int64_t rng;
     float wd;
-    int vec;        // every address allows 8-element vectors
+    int vec;        // every address allows 8-element vectors (1), and bulk copies (2)
 };
 static_assert(sizeof(Entry) == 80, "table layout");
 
@@ -147,15 +147,31 @@ __device__ __forceinline__ float rcp_approx(float x) {
     return r;
 }
 
+// Square roots of two values >= 0, correctly rounded for x above 2^-102:
+// y = x rsqrt(x) from the approximate instruction, then one step along the
+// exact residual, y + (x - y^2) rsqrt(x) / 2 in fused multiply-adds
+// (Markstein's correction).  No branch for the cases that sqrtf sets apart,
+// and half the issue slots.  Zero, infinity and NaN give themselves; below
+// 2^-102 the residual underflows and the root may be off in its last bits.
+__device__ __forceinline__ F2 sqrt2(F2 x) {
+    float x0, x1, r0, r1;
+    x.get(x0, x1);
+    asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(r0) : "f"(fmaxf(x0, 1.17549435e-38f)));
+    asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(r1) : "f"(fmaxf(x1, 1.17549435e-38f)));
+    const F2 r(r0, r1), y = mul2(x, r);
+    float z0, z1;
+    fma2(fma2(mul2(y, F2(-1.f)), y, x), mul2(r, F2(0.5f)), y).get(z0, z1);
+    return F2(x0 <= 3.402823466e38f ? z0 : x0, x1 <= 3.402823466e38f ? z1 : x1);
+}
+
 // E4M3 codes to fp32 times 2^-120, in integer arithmetic (the conversion
 // instructions run at a quarter of its rate): the code's exponent and
 // mantissa moved into those of an fp32, exact, subnormal codes included.
 // (Code 0x7F is written only where the block's scale is not finite.)
 template <bool SIGNED>
 __device__ __forceinline__ float e4m3_bits(uint32_t w, int i) {      // byte i of w
-    uint32_t f = (i == 3 ? w >> 4 : w << (20 - 8 * i)) & 0x07F00000u;
-    if (SIGNED) f |= (w << (24 - 8 * i)) & 0x80000000u;
-    return __uint_as_float(f);
+    if (SIGNED) return __uint_as_float((uint32_t)((int32_t)(w << (24 - 8 * i)) >> 4) & 0x87F00000u);
+    return __uint_as_float((i == 3 ? w >> 4 : w << (20 - 8 * i)) & 0x07F00000u);
 }
 template <bool SIGNED>
 __device__ __forceinline__ void load_codes(const uint8_t* p, int n, bool vec, float* f) {
@@ -183,17 +199,11 @@ __device__ __forceinline__ void store_codes(uint8_t* p, int n, bool vec, const u
 
 // |x| (up to 448) rounded to E4M3 as 16 dither bits say,
 //   floor(|x| / step + dither / 2^16) * step,  step = 2^(exponent - 3), 2^-9 below 2^-6.
-// The dither is added to the fp32 pattern right below the three mantissa
-// bits that stay; what is above bit 20 then is the code, but for the
-// exponent's offset (120 of 8).  Below 2^-6 the same with |x| + 2^-6, whose
-// last bit that stays is worth 2^-9 and whose code is 8 higher.
-// `dither20` are the bits in place (16 bits from bit 4 on); the code is
-// returned in bits 24..30, with noise below.
-__device__ __forceinline__ uint32_t e4m3_code(float x, uint32_t dither20) {
-    const bool sub = fabsf(x) < 0.015625f;
-    const uint32_t bits = __float_as_uint(fabsf(x) + (sub ? 0.015625f : 0.f));
-    return (bits + dither20 - (sub ? 968u << 20 : 960u << 20)) << 4;
-}
+// `x` comes times 2^-120: its fp32 pattern then has the code in bits 20..26,
+// subnormal where the code is, and the dither is added right below bit 20
+// (`d` holds it in bits 8..23, four places up).  The code is returned
+// in bits 24..30, with noise below and bit 31 clear.
+__device__ __forceinline__ uint32_t e4m3_code(float x, uint32_t d) { return (__float_as_uint(x) << 4) + d; }
 // the top bytes of four words
 __device__ __forceinline__ uint32_t top_bytes(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
     return __byte_perm(__byte_perm(a, b, 0x0073), __byte_perm(c, d, 0x0073), 0x5410);
@@ -214,10 +224,75 @@ __device__ __forceinline__ void block_scale(float top, float& scale, float& inv)
     inv = some ? __fmul_rn(__frcp_rn(top), 448.f) : 0.f;
 }
 
+// A tile's bytes in shared memory: p, g, m, v, and (8 bits) the 8 scales of each state.
 template <typename PT, typename GT, int BITS>
-__global__ void __launch_bounds__(kThreads, BITS == 8 ? 5 : 2) k_adamw(const Params p) {
+struct Stage {
+    static constexpr int P = kTile * (int)sizeof(PT), G = kTile * (int)sizeof(GT), S = kTile * (BITS == 32 ? 4 : 1);
+    static constexpr int SC = BITS == 32 ? 0 : kTile / kBlock * 4;
+    static constexpr int OFF_G = P, OFF_M = P + G, OFF_V = OFF_M + S, OFF_MS = OFF_V + S, OFF_VS = OFF_MS + SC;
+    static constexpr int BYTES = OFF_VS + SC;
+    // CTAs of an SM and stages of a CTA: about 192 KB on their way per SM
+    static constexpr int CTAS = BITS == 32 ? 2 : 4;
+    static constexpr int STAGES = 196608 / CTAS / BYTES < 4 ? 196608 / CTAS / BYTES : 4;
+};
+
+// A place in the table: a tile's tensor, and the tensor's tiles.
+struct Cursor {
+    int k;
+    int64_t first, next;
+    __device__ __forceinline__ bool seek(const Params& p, int64_t t) {      // whether the tensor changed
+        if (t < next) return false;                                         // (tiles are visited in order)
+        int hi = p.tensors - 1;      // the last tensor that starts at or before t
+        while (k < hi) {
+            const int mid = (k + hi + 1) >> 1;
+            if (p.tile0[mid] <= t) k = mid;
+            else hi = mid - 1;
+        }
+        first = p.tile0[k];
+        next = p.tile0[k + 1];
+        return true;
+    }
+};
+// Whole tiles of aligned tensors come through the ring of stages.
+__device__ __forceinline__ bool in_ring(const Entry& e, int64_t tile) { return e.vec == 2 && (tile + 1) * kTile <= e.n; }
+
+// A CTA takes every G-th tile (many small tensors in a row then are spread over
+// all CTAs).  Bulk copies bring the next whole tiles into a ring in shared memory while it works on one: loads into
+// registers, with the occupancy that the arithmetic's registers leave,
+// cover less than half of the memory's latency (8 bits: 3.1 TB/s).
+template <typename PT, typename GT, int BITS>
+__global__ void __launch_bounds__(kThreads, (Stage<PT, GT, BITS>::CTAS)) k_adamw(const Params p) {
+    using S = Stage<PT, GT, BITS>;
+    extern __shared__ __align__(128) uint8_t s_ring[];
+    __shared__ __align__(8) uint64_t s_bar[S::STAGES];
     __shared__ float s_h[4];
     __shared__ uint32_t s_key;
+    const int64_t t0 = blockIdx.x, t1 = p.tiles, G = gridDim.x;
+    Cursor pc{0, 0, 0};         // thread 0: the next tile to fetch
+    int64_t pt = t0;
+    int pstage = 0;
+    // Fetches up to `most` more whole tiles of the CTA's share.
+    auto fetch = [&](int most) {
+        while (most > 0 && pt < t1) {
+            pc.seek(p, pt);
+            const Entry& e = p.e[pc.k];
+            const int64_t tile = pt - pc.first;
+            pt += G;
+            if (!in_ring(e, tile)) continue;
+            const uint32_t bar = gg::smem_u32(&s_bar[pstage]), dst = gg::smem_u32(s_ring + pstage * S::BYTES);
+            gg::mbar_expect_tx(bar, S::BYTES);
+            gg::bulk_load(dst, static_cast<const uint8_t*>(e.p) + tile * S::P, S::P, bar);
+            gg::bulk_load(dst + S::OFF_G, static_cast<const uint8_t*>(e.g) + tile * S::G, S::G, bar);
+            gg::bulk_load(dst + S::OFF_M, static_cast<const uint8_t*>(e.m) + tile * S::S, S::S, bar);
+            gg::bulk_load(dst + S::OFF_V, static_cast<const uint8_t*>(e.v) + tile * S::S, S::S, bar);
+            if (BITS == 8) {
+                gg::bulk_load(dst + S::OFF_MS, e.ms + tile * (kTile / kBlock), S::SC, bar);
+                gg::bulk_load(dst + S::OFF_VS, e.vs + tile * (kTile / kBlock), S::SC, bar);
+            }
+            if (++pstage == S::STAGES) pstage = 0;
+            --most;
+        }
+    };
     if (threadIdx.x == 0) {
         float i1 = p.inv_bc1, i2 = p.inv_bc2;
         uint32_t key = p.key;
@@ -229,54 +304,76 @@ __global__ void __launch_bounds__(kThreads, BITS == 8 ? 5 : 2) k_adamw(const Par
         }
         s_h[0] = i1, s_h[1] = sqrtf(i2);
         s_h[2] = p.lr_dev ? *p.lr_dev : p.lr;
-        s_h[3] = p.grad_scale ? *p.grad_scale : 1.f;
+        const float gs = p.grad_scale ? *p.grad_scale : 1.f;
+        s_h[3] = gs;
         s_key = key;
+        for (int i = 0; i < S::STAGES; ++i) gg::mbar_init(gg::smem_u32(&s_bar[i]), 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        if (fabsf(gs) <= 3.402823466e38f) fetch(S::STAGES);
     }
     __syncthreads();
     const float lr = s_h[2], gs = s_h[3], root2 = s_h[1], lr1 = lr * s_h[0];
     const uint32_t key = s_key;
     const bool skip = !(fabsf(gs) <= 3.402823466e38f);      // NaN or infinite: the step is not taken
-    // the CTA's share of the tiles, in order
-    const int64_t t0 = p.tiles * blockIdx.x / gridDim.x, t1 = p.tiles * (blockIdx.x + 1) / gridDim.x;
-    int k = 0;
-    {
-        int hi = p.tensors - 1;      // the last tensor that starts at or before t0
-        while (k < hi) {
-            const int mid = (k + hi + 1) >> 1;
-            if (p.tile0[mid] <= t0) k = mid;
-            else hi = mid - 1;
-        }
-    }
-    int64_t first = p.tile0[k], next = p.tile0[k + 1];
-    Entry e = p.e[k];
-    for (int64_t t = t0; t < t1 && !skip; ++t) {
-        while (t >= next) {
-            first = next;
-            next = p.tile0[++k + 1];
-            e = p.e[k];
-        }
-        const int64_t at = (t - first) * kTile + 8 * (int)threadIdx.x;
+    Cursor cur{0, 0, 0};
+    Entry e{};
+    int stage = 0;
+    uint32_t phase = 0;
+    for (int64_t t = t0; t < t1 && !skip; t += G) {
+        if (cur.seek(p, t)) e = p.e[cur.k];
+        const int64_t tile = t - cur.first;
+        const int64_t at = tile * kTile + 8 * (int)threadIdx.x;
         const int64_t left = e.n - at;
         const int n = left >= 8 ? 8 : (left > 0 ? (int)left : 0);
-        if (BITS == 32 && n == 0) continue;      // 8 bits: the warp works together
         const bool vec = e.vec != 0;
         float g[8], w[8], m[8], v[8], u[8];
-        load(static_cast<const GT*>(e.g) + at, n, vec, g);
-        load(static_cast<PT*>(e.p) + at, n, vec, w);
-        if (BITS == 32) {
-            load(static_cast<float*>(e.m) + at, n, vec, m);
-            load(static_cast<float*>(e.v) + at, n, vec, v);
+        float sm = 0.f, sv = 0.f;
+        bool ok = true;
+        if (in_ring(e, tile)) {
+            const uint8_t* s = s_ring + stage * S::BYTES;
+            ok = false;
+            for (int i = 0; i < (1 << 16) && !ok; ++i) ok = gg::mbar_try_wait(gg::smem_u32(&s_bar[stage]), phase);
+            const int o = 8 * (int)threadIdx.x;
+            load(reinterpret_cast<const PT*>(s) + o, 8, true, w);
+            load(reinterpret_cast<const GT*>(s + S::OFF_G) + o, 8, true, g);
+            if (BITS == 32) {
+                load(reinterpret_cast<const float*>(s + S::OFF_M) + o, 8, true, m);
+                load(reinterpret_cast<const float*>(s + S::OFF_V) + o, 8, true, v);
+            } else {
+                load_codes<true>(s + S::OFF_M + o, 8, true, m);
+                load_codes<false>(s + S::OFF_V + o, 8, true, v);
+                sm = reinterpret_cast<const float*>(s + S::OFF_MS)[threadIdx.x >> 5];
+                sv = reinterpret_cast<const float*>(s + S::OFF_VS)[threadIdx.x >> 5];
+            }
+            __syncthreads();      // the stage is read
+            if (threadIdx.x == 0) fetch(1);
+            if (++stage == S::STAGES) {
+                stage = 0;
+                phase ^= 1u;
+            }
         } else {
-            load_codes<true>(static_cast<uint8_t*>(e.m) + at, n, vec, m);
-            load_codes<false>(static_cast<uint8_t*>(e.v) + at, n, vec, v);
-            // the warp's block: its first element exists or the whole warp is past the end
-            const int64_t b = (at - 8 * (int)(threadIdx.x & 31)) / kBlock;
-            const bool some = b * kBlock < e.n;
-            const F2 sm(some ? e.ms[b] : 0.f), sv(some ? e.vs[b] : 0.f), up(__uint_as_float((120u + 127u) << 23));
+            load(static_cast<const GT*>(e.g) + at, n, vec, g);
+            load(static_cast<PT*>(e.p) + at, n, vec, w);
+            if (BITS == 32) {
+                load(static_cast<float*>(e.m) + at, n, vec, m);
+                load(static_cast<float*>(e.v) + at, n, vec, v);
+            } else {
+                load_codes<true>(static_cast<uint8_t*>(e.m) + at, n, vec, m);
+                load_codes<false>(static_cast<uint8_t*>(e.v) + at, n, vec, v);
+                // the warp's block: its first element exists or the whole warp is past the end
+                const int64_t b = (at - 8 * (int)(threadIdx.x & 31)) / kBlock;
+                if (b * kBlock < e.n) {
+                    sm = e.ms[b];
+                    sv = e.vs[b];
+                }
+            }
+        }
+        if (BITS == 8) {
+            const F2 sm2(sm), sv2(sv), up(__uint_as_float((120u + 127u) << 23));
 #pragma unroll
             for (int i = 0; i < 8; i += 2) {
-                mul2(mul2(F2(m[i], m[i + 1]), up), sm).get(m[i], m[i + 1]);
-                const F2 r = mul2(mul2(F2(v[i], v[i + 1]), up), sv);
+                mul2(mul2(F2(m[i], m[i + 1]), up), sm2).get(m[i], m[i + 1]);
+                const F2 r = mul2(mul2(F2(v[i], v[i + 1]), up), sv2);
                 mul2(r, r).get(v[i], v[i + 1]);
             }
         }
@@ -288,12 +385,16 @@ __global__ void __launch_bounds__(kThreads, BITS == 8 ? 5 : 2) k_adamw(const Par
             const F2 v2 = add2(mul2(F2(p.b2), F2(v[i], v[i + 1])), mul2(mul2(F2(p.c2), g2), g2));
             m2.get(m[i], m[i + 1]);
             v2.get(v[i], v[i + 1]);
-            u[i] = sqrtf(v[i]);
-            u[i + 1] = sqrtf(v[i + 1]);
+            const F2 u2 = sqrt2(v2);
+            u2.get(u[i], u[i + 1]);
             float d0, d1;
-            fma2(F2(u[i], u[i + 1]), F2(root2), F2(p.eps)).get(d0, d1);
+            fma2(u2, F2(root2), F2(p.eps)).get(d0, d1);
             const F2 q = mul2(mul2(m2, F2(-lr1)), F2(rcp_approx(d0), rcp_approx(d1)));
             fma2(F2(w[i], w[i + 1]), decay, q).get(w[i], w[i + 1]);
+        }
+        if (!ok) {      // bytes that never came: the parameters say so
+#pragma unroll
+            for (int i = 0; i < 8; ++i) w[i] = __uint_as_float(0x7FC00000u);
         }
         store(static_cast<PT*>(e.p) + at, n, vec, w);
         if (e.copy != nullptr) store(e.copy + at, n, vec, w);
@@ -309,22 +410,23 @@ __global__ void __launch_bounds__(kThreads, BITS == 8 ? 5 : 2) k_adamw(const Par
                     u[i] = i < n ? u[i] : 0.f;
                 }
             }
-            float sm, im, su, iu;
+            float im, su, iu;
             block_scale(block_top(m), sm, im);
             block_scale(block_top(u), su, iu);
             const uint64_t c = (uint64_t)(e.rng + at);     // blocks start at multiples of 256 of the counter
             const uint32_t lo = (uint32_t)c + mix((uint32_t)(c >> 32) ^ key);
+            const F2 down(__uint_as_float((127u - 120u) << 23));
             uint32_t cm[8], cu[8];
 #pragma unroll
             for (int i = 0; i < 8; i += 2) {
-                mul2(F2(m[i], m[i + 1]), F2(im)).get(m[i], m[i + 1]);
-                mul2(F2(u[i], u[i + 1]), F2(iu)).get(u[i], u[i + 1]);
+                mul2(mul2(F2(m[i], m[i + 1]), F2(im)), down).get(m[i], m[i + 1]);
+                mul2(mul2(F2(u[i], u[i + 1]), F2(iu)), down).get(u[i], u[i + 1]);
 #pragma unroll
                 for (int j = i; j < i + 2; ++j) {
                     const uint32_t bits = mix(lo + (uint32_t)j);
-                    cm[j] = e4m3_code(m[j], (bits << 4) & 0xFFFF0u);
-                    const uint32_t k = e4m3_code(u[j], (bits >> 12) & 0xFFFF0u);
-                    cu[j] = u[j] > 0.f ? max(k, 1u << 24) : k;      // not zero: never rounded to zero
+                    cm[j] = e4m3_code(m[j], (bits << 8) & 0xFFFF00u);
+                    // not zero: never rounded to zero
+                    cu[j] = max(e4m3_code(u[j], (bits >> 8) & 0xFFFF00u), min(__float_as_uint(u[j]), 1u) << 24);
                 }
             }
             uint32_t wm[2], wu[2];
@@ -363,15 +465,36 @@ static bool al(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) 
 
 static size_t tile_table_at(int tensors) { return 16 + (size_t)tensors * sizeof(Entry); }
 
+template <typename PT, typename GT, int BITS>
+static void launch(const Params& p, int sms, cudaStream_t s) {
+    using S = Stage<PT, GT, BITS>;
+    const int grid = (int)std::max<int64_t>(1, std::min<int64_t>(p.tiles, (int64_t)sms * S::CTAS));
+    k_adamw<PT, GT, BITS><<<grid, kThreads, S::STAGES * S::BYTES, s>>>(p);
+}
 template <typename PT, typename GT>
-static void launch(int bits, int grid, const Params& p, cudaStream_t s) {
-    if (bits == 32)
-        k_adamw<PT, GT, 32><<<grid, kThreads, 0, s>>>(p);
-    else
-        k_adamw<PT, GT, 8><<<grid, kThreads, 0, s>>>(p);
+static void launch(int bits, const Params& p, int sms, cudaStream_t s) {
+    if (bits == 32) launch<PT, GT, 32>(p, sms, s);
+    else launch<PT, GT, 8>(p, sms, s);
+}
+template <typename PT, typename GT, int BITS>
+static cudaError_t set_one() {
+    using S = Stage<PT, GT, BITS>;
+    static_assert(S::STAGES >= 2, "ring");
+    return cudaFuncSetAttribute(k_adamw<PT, GT, BITS>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::STAGES * S::BYTES);
 }
 
 }  // namespace adamw
+
+cudaError_t adamw_set_attributes() {
+    using namespace adamw;
+    using B = __nv_bfloat16;
+    const cudaError_t es[] = {set_one<float, float, 32>(), set_one<float, B, 32>(), set_one<B, float, 32>(), set_one<B, B, 32>(),
+                              set_one<float, float, 8>(),  set_one<float, B, 8>(),  set_one<B, float, 8>(),  set_one<B, B, 8>()};
+    for (cudaError_t e : es)
+        if (e != cudaSuccess) return e;
+    return cudaSuccess;
+}
+
 }  // namespace moe
 
 extern "C" size_t adamw_plan_bytes(int tensors) {
@@ -409,6 +532,7 @@ extern "C" moe_status_t adamw_plan_encode(const moe_adamw_tensor_t* t, int tenso
         o.n = a.n, o.rng = a.rng_base, o.wd = a.weight_decay;
         o.vec = al(a.p, 16) && al(a.g, 16) && al(a.m, state_bits == 32 ? 16 : 8) &&
                 al(a.v, state_bits == 32 ? 16 : 8) && al(a.copy, 16);
+        if (o.vec && al(a.m, 16) && al(a.v, 16) && al(a.m_scale, 16) && al(a.v_scale, 16)) o.vec = 2;
         tile0[i] = at;
         at += (a.n + kTile - 1) / kTile;
     }
@@ -449,16 +573,15 @@ extern "C" moe_status_t adamw_step(void* plan, int tensors, int64_t tiles, int p
         p.key = mix(o->seed ^ mix((uint32_t)o->step));
     }
     if (tiles == 0 && !o->step_dev) return MOE_OK;
-    const int grid = (int)std::max<int64_t>(1, std::min<int64_t>(tiles, (int64_t)sms * 8));
     cudaStream_t s = (cudaStream_t)stream;
     if (p_type == MOE_TYPE_F32 && g_type == MOE_TYPE_F32)
-        launch<float, float>(state_bits, grid, p, s);
+        launch<float, float>(state_bits, p, sms, s);
     else if (p_type == MOE_TYPE_F32)
-        launch<float, __nv_bfloat16>(state_bits, grid, p, s);
+        launch<float, __nv_bfloat16>(state_bits, p, sms, s);
     else if (g_type == MOE_TYPE_F32)
-        launch<__nv_bfloat16, float>(state_bits, grid, p, s);
+        launch<__nv_bfloat16, float>(state_bits, p, sms, s);
     else
-        launch<__nv_bfloat16, __nv_bfloat16>(state_bits, grid, p, s);
+        launch<__nv_bfloat16, __nv_bfloat16>(state_bits, p, sms, s);
     MOE_CHECK_LAUNCH();
     return MOE_OK;
 }

@@ -15,6 +15,7 @@ cudaError_t quant_set_attributes();  // quant.cu
 cudaError_t gemm_init_driver();      // gemm.cu
 cudaError_t dense_set_attributes();  // dense.cu
 cudaError_t norm_set_attributes();   // norm.cu
+cudaError_t adamw_set_attributes();  // adamw.cu
 void route_scratch_forget(int device);  // route.cu
 
 int device_sm_count() {
@@ -73,6 +74,7 @@ extern "C" moe_status_t moe_init(int device) {
     if (quant_set_attributes() != cudaSuccess) return MOE_ERR_CUDA;
     if (dense_set_attributes() != cudaSuccess) return MOE_ERR_CUDA;
     if (norm_set_attributes() != cudaSuccess) return MOE_ERR_CUDA;
+    if (adamw_set_attributes() != cudaSuccess) return MOE_ERR_CUDA;
     g_sm_count[device] = sms;
     g_init[device] = true;
     return MOE_OK;

@@ -222,3 +222,51 @@ def test_refusals(ops):
     refused(bad, ops.adamw_step, plan, LR, betas=(1.0, 0.9))
     refused(bad, ops.adamw_step, plan, LR, eps=-1e-8)
     refused(bad, ops.adamw_step, plan, torch.zeros((1,)), step=1)
+
+
+def test_whole_tiles_partial_tiles_and_odd_addresses_in_one_plan(ops):
+    """Tensors of many whole tiles of 2,048 elements (which come through the
+    ring) between small, ragged and unaligned ones."""
+    sizes = [2048 * 700, 3, 2048 * 3 + 1, 100, 2048, 4095, 2048 * 50 + 2047, 7]
+    offs = [0, 0, 0, 1, 0, 3, 0, 0]
+    mk = lambda s, std, dt: [rnd(n, s + i, std, dt, o) for i, (n, o) in enumerate(zip(sizes, offs))]  # noqa: E731
+    p, g, m = mk(10, 0.02, F), mk(50, 1e-3, BF), mk(90, 3e-4, F)
+    v = [t.square() if o == 0 else torch.cat([t.new_zeros(o), t.square()])[o:] for t, o in zip(mk(130, 1e-3, F), offs)]
+    plan = ops.adamw_plan(p, g, m, v, weight_decay=WD)
+    for t in (1, 2):
+        old = [[f64(a) for a in lst] for lst in (p, g, m, v)]
+        ops.adamw_step(plan, LR, (B1, B2), EPS, step=t)
+        for i in range(len(sizes)):
+            o = [x[i] for x in old]
+            wp, wm, wv = D.adamw(*o, t, LR, B1, B2, EPS, WD)
+            assert np.all(np.abs(f64(m[i]) - wm) <= (np.abs(o[2]) + np.abs(o[1])) * 2.0 ** -21)
+            assert np.all(np.abs(f64(v[i]) - wv) <= (o[3] + o[1] ** 2) * 2.0 ** -21 + 1e-44)
+            check_p(p[i], wp, o, t, F)
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_non_finite_gradients_stay_with_their_elements(ops, bits):
+    """NaN and infinite gradients, and one whose square overflows, in one
+    block of one tensor (8 bits: its block's states are lost with it)."""
+    n = 4096 + 300
+    p, g = rnd(n, 1, 0.02), rnd(n, 2, 1e-3)
+    g[5], g[300], g[4100] = float("nan"), float("inf"), 1e25
+    keep = p.clone()
+    if bits == 32:
+        st = [torch.zeros((n,), device="cuda") for _ in range(2)]
+        plan = ops.adamw_plan([p], [g], [st[0]], [st[1]])
+    else:
+        nb = (n + 255) // 256
+        st = [torch.zeros((n,), dtype=torch.uint8, device="cuda") for _ in range(2)]
+        plan = ops.adamw_plan([p], [g], [st[0]], [st[1]], [torch.zeros((nb,), device="cuda")], [torch.zeros((nb,), device="cuda")])
+    ops.adamw_step(plan, LR, (B1, B2), EPS, step=1)
+    bad = torch.zeros((n,), dtype=torch.bool, device="cuda")
+    bad[[5, 300]] = True
+    assert torch.isnan(p[bad]).all() and torch.isfinite(p[~bad]).all()
+    assert p[4100] == keep[4100]                   # m / sqrt(inf) = 0
+    zero = torch.zeros_like(keep)
+    fine = ~bad
+    fine[4100] = False
+    want = D.adamw(f64(keep), f64(g), f64(zero), f64(zero), 1, LR, B1, B2, EPS, 0.0)[0]
+    f = fine.cpu().numpy()
+    assert np.all(np.abs(f64(p)[f] - want[f]) <= 2.0 ** -21 * np.abs(want[f]) + LR * 2.0 ** -18)
