@@ -23,7 +23,7 @@
 // (products and sums rounded one by one), so that states, which feed the next
 // step, are the same bits wherever they are computed.
 //
-// The pass is bound by its traffic: p, g, m, v read and p, m, v written once.
+// The pass has to read p, g, m, v and write p, m, v once.
 #include <math.h>
 
 #include <algorithm>
@@ -232,8 +232,9 @@ struct Stage {
     static constexpr int OFF_G = P, OFF_M = P + G, OFF_V = OFF_M + S, OFF_MS = OFF_V + S, OFF_VS = OFF_MS + SC;
     static constexpr int BYTES = OFF_VS + SC;
     // CTAs of an SM and stages of a CTA: about 192 KB on their way per SM
-    static constexpr int CTAS = BITS == 32 ? 2 : 4;
-    static constexpr int STAGES = 196608 / CTAS / BYTES < 4 ? 196608 / CTAS / BYTES : 4;
+    static constexpr int CTAS = BITS == 32 ? 3 : 4;
+    static constexpr int STAGES = BITS == 32 ? 1 : (196608 / CTAS / BYTES >= 4 ? 4 : (196608 / CTAS / BYTES >= 3 ? 3 : 2));
+    static constexpr int RING = BITS == 32 ? 0 : STAGES * BYTES;
 };
 
 // A place in the table: a tile's tensor, and the tensor's tiles.
@@ -254,12 +255,23 @@ struct Cursor {
     }
 };
 // Whole tiles of aligned tensors come through the ring of stages.
-__device__ __forceinline__ bool in_ring(const Entry& e, int64_t tile) { return e.vec == 2 && (tile + 1) * kTile <= e.n; }
+template <int BITS>
+__device__ __forceinline__ bool in_ring(const Entry& e, int64_t tile) {
+    return BITS == 8 && e.vec == 2 && (tile + 1) * kTile <= e.n;
+}
 
-// A CTA takes every G-th tile (many small tensors in a row then are spread over
-// all CTAs).  Bulk copies bring the next whole tiles into a ring in shared memory while it works on one: loads into
-// registers, with the occupancy that the arithmetic's registers leave,
-// cover less than half of the memory's latency (8 bits: 3.1 TB/s).
+// A CTA takes every G-th tile, so that many small tensors in a row are spread
+// over all CTAs.
+//
+// 32 bits: 28 bytes and about 30 instructions an element; loads straight into
+// registers, three CTAs an SM (176 M elements, fp32 p, bf16 g and copy: 751 us,
+// 6.57 TB/s, 97 % of the copy bandwidth; through a ring in shared memory 805 us).
+// 8 bits: 10 bytes and about 80 instructions an element (a third of them the
+// rounding of the codes), which is what bounds it.  Loads into registers covered
+// less than half of the memory's latency at the occupancy those leave, so
+// bulk copies bring the next whole tiles into a ring in shared memory
+// while the CTA works on one (130 M elements, bf16 p and g: 366 us, 3.6 TB/s;
+// 410 us without the ring).
 template <typename PT, typename GT, int BITS>
 __global__ void __launch_bounds__(kThreads, (Stage<PT, GT, BITS>::CTAS)) k_adamw(const Params p) {
     using S = Stage<PT, GT, BITS>;
@@ -278,7 +290,7 @@ __global__ void __launch_bounds__(kThreads, (Stage<PT, GT, BITS>::CTAS)) k_adamw
             const Entry& e = p.e[pc.k];
             const int64_t tile = pt - pc.first;
             pt += G;
-            if (!in_ring(e, tile)) continue;
+            if (!in_ring<BITS>(e, tile)) continue;
             const uint32_t bar = gg::smem_u32(&s_bar[pstage]), dst = gg::smem_u32(s_ring + pstage * S::BYTES);
             gg::mbar_expect_tx(bar, S::BYTES);
             gg::bulk_load(dst, static_cast<const uint8_t*>(e.p) + tile * S::P, S::P, bar);
@@ -329,7 +341,7 @@ __global__ void __launch_bounds__(kThreads, (Stage<PT, GT, BITS>::CTAS)) k_adamw
         float g[8], w[8], m[8], v[8], u[8];
         float sm = 0.f, sv = 0.f;
         bool ok = true;
-        if (in_ring(e, tile)) {
+        if (in_ring<BITS>(e, tile)) {
             const uint8_t* s = s_ring + stage * S::BYTES;
             ok = false;
             for (int i = 0; i < (1 << 16) && !ok; ++i) ok = gg::mbar_try_wait(gg::smem_u32(&s_bar[stage]), phase);
@@ -468,8 +480,8 @@ static size_t tile_table_at(int tensors) { return 16 + (size_t)tensors * sizeof(
 template <typename PT, typename GT, int BITS>
 static void launch(const Params& p, int sms, cudaStream_t s) {
     using S = Stage<PT, GT, BITS>;
-    const int grid = (int)std::max<int64_t>(1, std::min<int64_t>(p.tiles, (int64_t)sms * S::CTAS));
-    k_adamw<PT, GT, BITS><<<grid, kThreads, S::STAGES * S::BYTES, s>>>(p);
+    const int grid = (int)std::max<int64_t>(1, std::min<int64_t>(p.tiles, (int64_t)sms * (BITS == 32 ? 8 : S::CTAS)));
+    k_adamw<PT, GT, BITS><<<grid, kThreads, S::RING, s>>>(p);
 }
 template <typename PT, typename GT>
 static void launch(int bits, const Params& p, int sms, cudaStream_t s) {
@@ -479,8 +491,8 @@ static void launch(int bits, const Params& p, int sms, cudaStream_t s) {
 template <typename PT, typename GT, int BITS>
 static cudaError_t set_one() {
     using S = Stage<PT, GT, BITS>;
-    static_assert(S::STAGES >= 2, "ring");
-    return cudaFuncSetAttribute(k_adamw<PT, GT, BITS>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::STAGES * S::BYTES);
+    static_assert(BITS == 32 || S::STAGES >= 2, "ring");
+    return cudaFuncSetAttribute(k_adamw<PT, GT, BITS>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::RING);
 }
 
 }  // namespace adamw
