@@ -11,13 +11,20 @@
 //
 // Tile: 256 x bn of D per CTA pair (tcgen05.mma.cta_group::2, M = 256,
 // N = bn <= 256), 64 deep per pipeline stage; CTA r of the pair holds 128 of
-// the A rows and bn / 2 of the B rows, 32 KB per stage.  Two accumulators of
-// 256 TMEM columns, so that the epilogue of one tile runs under the next
-// tile's products.  Per k-step the pair reads 64 KB for 256 x 256 x 64
-// products: half the operand traffic per SM of a 128 x 256 tile on one SM.
+// the A rows and bn / 2 of the B rows, 32 KB per stage with bn = 256.  Two
+// accumulators of 256 TMEM columns, so that the epilogue of one tile runs
+// under the next tile's products.  Per k-step the pair reads 64 KB for
+// 256 x 256 x 64 products: half the operand traffic per SM of a 128 x 256
+// tile on one SM.
 // D leaves through shared memory: each epilogue warp stages 32 rows x 32
 // columns and one TMA store writes them, clipped at D's edges, which
 // leaves whole lines to the memory system and the warp free.
+//
+// When the tiles are too few for the SMs, `splits` pairs of a cluster share a
+// tile, each with its part of K.  They swap their fp32 partial tiles through
+// distributed shared memory, each pair adding up (in the order of the parts)
+// and writing its share of the columns: no workspace, no atomics, the same
+// bits on every run.
 //
 // Warps: 0 TMA, 1 MMA (of the leader CTA), 4-11 epilogue.  All waits are
 // bounded, as in the grouped GEMM kernels.
@@ -39,17 +46,20 @@ using namespace gg;
 constexpr int TM = 256, TK = 64;                // rows of the pair's tile, the k-step
 constexpr int ACC_COLS = 256;                   // TMEM columns of an accumulator
 constexpr int HALF_BYTES = 128 * TK * 2;        // one CTA's rows of an operand per stage
-constexpr int STAGES = 6;
+constexpr int MAX_STAGES = 8;
 constexpr int NACC = 2;
-constexpr int OFF_A = 0;
-constexpr int OFF_B = OFF_A + STAGES * HALF_BYTES;
-constexpr int OFF_EPI = OFF_B + STAGES * HALF_BYTES;      // staging, 4 KB per epilogue warp
+constexpr int SMEM_TILES = 12 * HALF_BYTES;     // 6 stages with bn = 256, 8 with bn = 128
+constexpr int OFF_EPI = SMEM_TILES;             // staging, 4 KB per epilogue warp
 constexpr int EPI_STAGE = 4096;
 constexpr int OFF_BAR = OFF_EPI + EPI_WARPS * EPI_STAGE;      // full[S], empty[S], tfull[A], tempty[A], drain
-constexpr int NBAR = 2 * STAGES + 2 * NACC + 1;
+constexpr int NBAR = 2 * MAX_STAGES + 2 * NACC + 1;
 constexpr int OFF_MISC = OFF_BAR + 8 * NBAR;
 constexpr int SMEM_BYTES = OFF_MISC + 16 + 1024;
 static_assert(SMEM_BYTES <= 232448, "shared memory budget");
+// a partial chunk of 128 rows x 32 columns on its way to another pair: rows
+// of 36 words, so that the row-per-lane accesses meet no bank twice
+constexpr int PART_ROW = 144;
+constexpr int PART_BYTES = 128 * PART_ROW;
 
 // What the epilogue makes of the product v:
 //   EPI_LINEAR  z = v + bias; y = act(z) + residual (bf16; z stored when asked for)
@@ -65,6 +75,8 @@ struct Params {
     int64_t m_tiles;
     int n_tiles, nk, band;
     int bn;                 // columns of the pair's tile
+    int stages, stage_bytes;
+    int splits;             // pairs that share a tile (cluster of 2 * splits)
     int up;                 // GLU: column of W where the up half begins
     int act;
     void* y;                // bf16, EPI_F32: fp32
@@ -209,6 +221,70 @@ __device__ __forceinline__ Tile get_tile(const Params& p, int64_t t) {
     band_decode(t, p.m_tiles, p.n_tiles, p.band, r.mt, r.nt);
     return r;
 }
+// arrive on the barrier at the same shared offset in both CTAs of the pair
+// that starts at cluster rank `lead`
+__device__ __forceinline__ void tc_commit_pair(uint32_t bar, uint32_t lead) {
+    const uint16_t mask = (uint16_t)(0x3u << lead);
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::
+                     "r"(bar),
+                 "h"(mask)
+                 : "memory");
+}
+__device__ __forceinline__ void st_cluster_v4(uint32_t addr, const float* v) {
+    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(v[0]), "f"(v[1]), "f"(v[2]),
+                 "f"(v[3])
+                 : "memory");
+}
+
+// 32 columns of a warp's 32 rows from the product (v; GLU: gate v and up u)
+// to memory.  `col`: the first one in D, `n` of them exist (n > 0).
+template <int EPI>
+__device__ __forceinline__ void finish(const Params& p, const CUtensorMap* tmY, const CUtensorMap* tmZ,
+                                       const CUtensorMap* tmZ2, Out& out, int64_t row0, int64_t row, int col, int n,
+                                       float* v, float* u) {
+    // a TMA store is clipped at D's edge to whole 16 bytes: the last columns
+    // of a width that is no multiple of 8 go element by element (GLU: f is one)
+    const bool edge = EPI != EPI_GLU && n < 32 && (p.N & 7) != 0;
+    if constexpr (EPI == EPI_GLU) {
+        if (p.z != nullptr) {
+            out.bf16(tmZ, col, row0, v);
+            out.bf16(tmZ2, col, row0, u);
+        }
+#pragma unroll
+        for (int i = 0; i < 32; ++i) u[i] *= act_of(v[i], p.act);
+        out.bf16(tmY, col, row0, u);
+    } else if constexpr (EPI == EPI_F32) {
+        if (!edge)
+            out.f32(tmY, col, row0, v);
+        else if (row < p.M)
+            store_edge(static_cast<float*>(p.y) + row * p.ldy + col, n, v);
+    } else {
+        if (p.bias != nullptr) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] += i < n ? __bfloat162float(p.bias[col + i]) : 0.f;
+        }
+        if (p.z != nullptr) {
+            if (!edge)
+                out.bf16(tmZ, col, row0, v);
+            else if (row < p.M)
+                store_edge(p.z + row * p.ldz + col, n, v);
+        }
+        if (p.act != MOE_ACT_NONE) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = act_of(v[i], p.act);
+        }
+        if (p.res != nullptr && row < p.M) {
+            float r[32];
+            load32(p.res + row * p.ldres + col, n, r);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] += r[i];
+        }
+        if (!edge)
+            out.bf16(tmY, col, row0, v);
+        else if (row < p.M)
+            store_edge(static_cast<__nv_bfloat16*>(p.y) + row * p.ldy + col, n, v);
+    }
+}
 
 // tmY, tmZ, tmZ2: y (h), z (a's gate half) and a's up half as TMA stores see
 // them, boxes of 32 columns x 32 rows.
@@ -220,22 +296,25 @@ __global__ void __launch_bounds__(THREADS, 1)
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint32_t rank = cluster_ctarank();
+    const uint32_t crank = cluster_ctarank();
+    const uint32_t rank = crank & 1u, lead = crank & ~1u;      // in the pair; the pair's leader in the cluster
+    const int part = (int)(crank >> 1);                        // of K
     const bool leader = rank == 0;
-    const int64_t pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
+    const int64_t first = blockIdx.x / (2 * p.splits), step = gridDim.x / (2 * p.splits);
     const int64_t total = p.m_tiles * p.n_tiles;
+    const int k0 = (int)((int64_t)p.nk * part / p.splits), k1 = (int)((int64_t)p.nk * (part + 1) / p.splits);
 
     const uint32_t bar0 = smem_u32(smem + OFF_BAR);
     auto full_bar = [&](int s) { return bar0 + 8u * s; };
-    auto empty_bar = [&](int s) { return bar0 + 8u * (STAGES + s); };
-    auto tfull_bar = [&](int a) { return bar0 + 8u * (2 * STAGES + a); };
-    auto tempty_bar = [&](int a) { return bar0 + 8u * (2 * STAGES + NACC + a); };
-    const uint32_t drain_bar = bar0 + 8u * (2 * STAGES + 2 * NACC);
+    auto empty_bar = [&](int s) { return bar0 + 8u * (MAX_STAGES + s); };
+    auto tfull_bar = [&](int a) { return bar0 + 8u * (2 * MAX_STAGES + a); };
+    auto tempty_bar = [&](int a) { return bar0 + 8u * (2 * MAX_STAGES + NACC + a); };
+    const uint32_t drain_bar = bar0 + 8u * (2 * MAX_STAGES + 2 * NACC);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + OFF_MISC);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + OFF_MISC + 4);
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < STAGES; ++s) {
+        for (int s = 0; s < p.stages; ++s) {
             mbar_init(full_bar(s), 1);
             mbar_init(empty_bar(s), 1);
         }
@@ -258,34 +337,33 @@ __global__ void __launch_bounds__(THREADS, 1)
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
 
+    const int ew = warp - 4;                       // epilogue warps: their rows and their half of the columns
+    const int quarter = ew & 3, half = ew >> 2;
+    const uint32_t lane_base = tmem_base + ((uint32_t)(quarter * 32) << 16);
+    Out out{smem_u32(smem + OFF_EPI + ew * EPI_STAGE), lane, 0u};
+
     if (warp == 0 && lane == 0) {
         // ------------------------------------------------ TMA producer ----
-        uint32_t leader_full[STAGES];
-        for (int s = 0; s < STAGES; ++s) leader_full[s] = mapa(full_bar(s), 0);
-        int pend[STAGES];
-        for (int s = 0; s < STAGES; ++s) pend[s] = -1;
-        int stage = 0;
+        const uint32_t lead_full = mapa(full_bar(0), lead);
+        int stage = 0, issued = 0;
         uint32_t phase = 0;
         bool aborted = false;
         // B: bn / 2 rows, or bn / 2 columns in boxes of 64
-        const int b_boxes = (p.bn / 2 + 63) / 64;
-        const uint32_t tx = 2u * (HALF_BYTES + (uint32_t)(B_MN ? b_boxes * 64 : p.bn / 2) * TK * 2);
-        for (int64_t t = pair; t < total && !aborted; t += npairs) {
+        const int bh = p.bn / 2, b_boxes = (bh + 63) / 64;
+        for (int64_t t = first; t < total && !aborted; t += step) {
             const Tile ti = get_tile(p, t);
             const int am = (int)(ti.mt * TM) + 128 * (int)rank;
-            const int bh = p.bn / 2;
             const int bn = EPI == EPI_GLU ? ti.nt * bh + p.up * (int)rank : ti.nt * p.bn + bh * (int)rank;
-            for (int ks = 0; ks < p.nk; ++ks) {
+            for (int ks = k0; ks < k1; ++ks) {
                 if (!mbar_wait_cluster(empty_bar(stage), phase ^ 1u, p, abort_flag)) {
                     aborted = true;
                     break;
                 }
                 const int k = ks * TK;
                 // both CTAs' bytes complete on the leader's full barrier
-                const uint32_t fb = leader_full[stage];
-                if (leader) mbar_expect_tx(full_bar(stage), tx);
-                const uint32_t sa = smem_u32(smem + OFF_A + stage * HALF_BYTES);
-                const uint32_t sb = smem_u32(smem + OFF_B + stage * HALF_BYTES);
+                const uint32_t fb = lead_full + 8u * stage;
+                if (leader) mbar_expect_tx(full_bar(stage), 2u * (uint32_t)p.stage_bytes);
+                const uint32_t sa = smem_u32(smem + stage * p.stage_bytes), sb = sa + HALF_BYTES;
                 if constexpr (A_MN) {
                     tma2_load_2d(sa, &tmA, am, k, fb);
                     tma2_load_2d(sa + HALF_BYTES / 2, &tmA, am + 64, k, fb);
@@ -298,21 +376,22 @@ __global__ void __launch_bounds__(THREADS, 1)
                 } else {
                     tma2_load_2d(sb, &tmB, k, bn, fb);
                 }
-                pend[stage] = (int)phase;
-                if (++stage == STAGES) {
+                ++issued;
+                if (++stage == p.stages) {
                     stage = 0;
                     phase ^= 1u;
                 }
             }
         }
         if (aborted && leader) {
-            // the leader's full barriers count both CTAs' bytes; the follower
-            // leaves only after the closing cluster barrier, i.e. after this
+            // wait (bounded) for the copies in flight: the leader's full
+            // barriers count both CTAs' bytes, and the follower leaves only
+            // after the closing cluster barrier, i.e. after this
             Params q = p;
             q.timeout_ns = 200000000ull;
             volatile int no_abort = 0;
-            for (int s = 0; s < STAGES; ++s)
-                if (pend[s] >= 0) mbar_wait_cluster(full_bar(s), (uint32_t)pend[s], q, &no_abort);
+            for (int i = issued - min(issued, p.stages); i < issued; ++i)
+                mbar_wait_cluster(full_bar(i % p.stages), (uint32_t)(i / p.stages) & 1u, q, &no_abort);
         }
     } else if (warp == 1 && lane == 0 && leader) {
         // ---------------------------------------- MMA issuer (leader) ----
@@ -320,31 +399,31 @@ __global__ void __launch_bounds__(THREADS, 1)
         uint32_t phase = 0, acc_phase = 0;
         bool aborted = false, issued = false;
         const uint32_t idesc = make_idesc_pair<A_MN, B_MN>(p.bn);
-        for (int64_t t = pair; t < total && !aborted; t += npairs) {
+        for (int64_t t = first; t < total && !aborted; t += step) {
             if (!mbar_wait_cluster(tempty_bar(acc), acc_phase ^ 1u, p, abort_flag)) break;
             tc_fence_after();
             const uint32_t d_tmem = tmem_base + (uint32_t)(acc * ACC_COLS);
-            for (int ks = 0; ks < p.nk; ++ks) {
+            for (int ks = k0; ks < k1; ++ks) {
                 if (!mbar_wait_cluster(full_bar(stage), phase, p, abort_flag)) {
                     aborted = true;
                     break;
                 }
                 tc_fence_after();
-                const uint64_t adesc = operand_desc<A_MN>(smem_u32(smem + OFF_A + stage * HALF_BYTES));
-                const uint64_t bdesc = operand_desc<B_MN>(smem_u32(smem + OFF_B + stage * HALF_BYTES));
+                const uint32_t sa = smem_u32(smem + stage * p.stage_bytes);
+                const uint64_t adesc = operand_desc<A_MN>(sa), bdesc = operand_desc<B_MN>(sa + HALF_BYTES);
 #pragma unroll
                 for (int kk = 0; kk < TK / 16; ++kk)
-                    tc_mma2_bf16(d_tmem, adesc + k16_step<A_MN>() * kk, bdesc + k16_step<B_MN>() * kk,
-                                 idesc, (ks | kk) != 0 ? 1u : 0u);
+                    tc_mma2_bf16(d_tmem, adesc + k16_step<A_MN>() * kk, bdesc + k16_step<B_MN>() * kk, idesc,
+                                 (ks != k0 || kk != 0) ? 1u : 0u);
                 issued = true;
-                tc_commit_both(empty_bar(stage));
-                if (++stage == STAGES) {
+                tc_commit_pair(empty_bar(stage), lead);
+                if (++stage == p.stages) {
                     stage = 0;
                     phase ^= 1u;
                 }
             }
             if (aborted) break;
-            tc_commit_both(tfull_bar(acc));
+            tc_commit_pair(tfull_bar(acc), lead);
             if (++acc == NACC) {
                 acc = 0;
                 acc_phase ^= 1u;
@@ -357,25 +436,19 @@ __global__ void __launch_bounds__(THREADS, 1)
             volatile int no_abort = 0;
             mbar_wait(drain_bar, 0, q, &no_abort);
         }
-    } else if (warp >= 4) {
+    } else if (warp >= 4 && p.splits == 1) {
         // ----------------------------------------------------- epilogue ----
-        const int ew = warp - 4;
-        const int quarter = ew & 3, half = ew >> 2;
         int acc = 0;
         uint32_t acc_phase = 0;
-        const uint32_t lane_base = tmem_base + ((uint32_t)(quarter * 32) << 16);
-        Out out{smem_u32(smem + OFF_EPI + ew * EPI_STAGE), lane, 0u};
         // this warp's chunks of 32 columns: the first or the second half of them
         const int chunks = EPI == EPI_GLU ? p.bn / 64 : p.bn / 32;
         const int c0 = half == 0 ? 0 : (chunks + 1) / 2, c1 = half == 0 ? (chunks + 1) / 2 : chunks;
-        for (int64_t t = pair; t < total; t += npairs) {
+        for (int64_t t = first; t < total; t += step) {
             const Tile ti = get_tile(p, t);
             const int64_t row0 = ti.mt * TM + 128 * rank + quarter * 32;
-            const int64_t row = row0 + lane;
             if (!mbar_wait_cluster(tfull_bar(acc), acc_phase, p, abort_flag)) break;
             tc_fence_after();
             const uint32_t tacc = lane_base + (uint32_t)(acc * ACC_COLS);
-            const uint32_t tempty = mapa(tempty_bar(acc), 0);
             for (int c = c0; c < c1; ++c) {
                 float v[32], u[EPI == EPI_GLU ? 32 : 1];
                 tmem_ld32(tacc + 32 * c, v);
@@ -383,59 +456,12 @@ __global__ void __launch_bounds__(THREADS, 1)
                 if (c == c1 - 1) {      // the accumulator is read: the next tile may have it
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive_remote(tempty);
+                    if (lane == 0) mbar_arrive_remote(mapa(tempty_bar(acc), lead));
                 }
                 const int col = ti.nt * (EPI == EPI_GLU ? p.bn / 2 : p.bn) + 32 * c;
                 const int n = p.N - col;
-                if (n <= 0 || row0 >= p.M) continue;      // the whole warp
-                // a TMA store is clipped at D's edge to whole 16 bytes: the
-                // last columns of a width that is no multiple of 8 go
-                // element by element (GLU: f is one)
-                const bool edge = EPI != EPI_GLU && n < 32 && (p.N & 7) != 0;
-                if constexpr (EPI == EPI_GLU) {
-                    if (p.z != nullptr) {
-                        out.bf16(&tmZ, col, row0, v);
-                        out.bf16(&tmZ2, col, row0, u);
-                    }
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) u[i] *= act_of(v[i], p.act);
-                    out.bf16(&tmY, col, row0, u);
-                } else if constexpr (EPI == EPI_F32) {
-                    if (!edge)
-                        out.f32(&tmY, col, row0, v);
-                    else if (row < p.M)
-                        store_edge(static_cast<float*>(p.y) + row * p.ldy + col, n, v);
-                } else {
-                    if (p.bias != nullptr) {
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) v[i] += i < n ? __bfloat162float(p.bias[col + i]) : 0.f;
-                    }
-                    if (p.z != nullptr) {
-                        if (!edge)
-                            out.bf16(&tmZ, col, row0, v);
-                        else if (row < p.M)
-                            store_edge(p.z + row * p.ldz + col, n, v);
-                    }
-                    if (p.act != MOE_ACT_NONE) {
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) v[i] = act_of(v[i], p.act);
-                    }
-                    if (p.res != nullptr && row < p.M) {
-                        float r[32];
-                        load32(p.res + row * p.ldres + col, n, r);
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) v[i] += r[i];
-                    }
-                    if (!edge)
-                        out.bf16(&tmY, col, row0, v);
-                    else if (row < p.M)
-                        store_edge(static_cast<__nv_bfloat16*>(p.y) + row * p.ldy + col, n, v);
-                }
-            }
-            if (c0 == c1) {
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_remote(tempty);
+                if (n > 0 && row0 < p.M)      // the whole warp
+                    finish<EPI>(p, &tmY, &tmZ, &tmZ2, out, row0, row0 + lane, col, n, v, u);
             }
             if (++acc == NACC) {
                 acc = 0;
@@ -444,6 +470,74 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
         if (lane == 0) bulk_wait_group0();      // the stores are complete
         __syncwarp();
+    }
+    if (p.splits > 1) {
+        // ------------------------- one tile per cluster: swap and add up ----
+        // A unit is what finish() takes (a chunk; GLU: a gate and an up
+        // chunk).  Part j owns units [j * own, (j + 1) * own).
+        constexpr int CPU = EPI == EPI_GLU ? 2 : 1;      // chunks per unit
+        const int units = EPI == EPI_GLU ? p.bn / 64 : p.bn / 32, own = units / p.splits;
+        const uint32_t buf = smem_u32(smem);
+        const int r = quarter * 32 + lane;
+        bool ok = true;
+        __syncwarp();
+        if (warp >= 4) {
+            ok = mbar_wait_cluster(tfull_bar(0), 0, p, abort_flag);
+            tc_fence_after();
+        }
+        cluster_sync();      // every part's products are done: its stages are free to write to
+        if (warp >= 4 && ok) {
+            for (int un = half; un < units; un += 2) {
+                const int to = un / own;
+                if (to == part) continue;
+                const int slot = part < to ? part : part - 1;      // of the receiver's other parts
+#pragma unroll
+                for (int c = 0; c < CPU; ++c) {
+                    float v[32];
+                    tmem_ld32(lane_base + (uint32_t)(32 * un + (c == 0 ? 0 : p.bn / 2)), v);
+                    const uint32_t at = buf + (uint32_t)(((slot * own + un - to * own) * CPU + c) * PART_BYTES + r * PART_ROW);
+                    const uint32_t dst = mapa(at, (uint32_t)(2 * to) + rank);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) st_cluster_v4(dst + 16u * i, v + 4 * i);
+                }
+            }
+        }
+        cluster_sync();      // every part has what it adds up
+        if (warp >= 4 && ok) {
+            const Tile ti = get_tile(p, first);
+            const int64_t row0 = ti.mt * TM + 128 * rank + quarter * 32;
+            for (int un = part * own + half; un < (part + 1) * own; un += 2) {
+                float s[2][32];
+#pragma unroll
+                for (int c = 0; c < CPU; ++c) {
+                    float v[32];
+                    tmem_ld32(lane_base + (uint32_t)(32 * un + (c == 0 ? 0 : p.bn / 2)), v);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) s[c][i] = 0.f;
+                    for (int j = 0; j < p.splits; ++j) {
+                        if (j == part) {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) s[c][i] += v[i];
+                            continue;
+                        }
+                        const int slot = j < part ? j : j - 1;
+                        const float4* q = reinterpret_cast<const float4*>(
+                            smem + ((slot * own + un - part * own) * CPU + c) * PART_BYTES + r * PART_ROW);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const float4 x = q[i];
+                            s[c][4 * i] += x.x, s[c][4 * i + 1] += x.y, s[c][4 * i + 2] += x.z, s[c][4 * i + 3] += x.w;
+                        }
+                    }
+                }
+                const int col = ti.nt * (EPI == EPI_GLU ? p.bn / 2 : p.bn) + 32 * un;
+                const int n = p.N - col;
+                if (n > 0 && row0 < p.M)
+                    finish<EPI>(p, &tmY, &tmZ, &tmZ2, out, row0, row0 + lane, col, n, s[0], s[1]);
+            }
+            if (lane == 0) bulk_wait_group0();
+            __syncwarp();
+        }
     }
 
     tc_fence_before();
@@ -797,16 +891,16 @@ __global__ void __launch_bounds__(256) k_act_bwd(const __nv_bfloat16* __restrict
 
 // ----------------------------------------------------------------- host ----
 
-static int g_max_clusters = 0;
+static int g_max_clusters[3] = {0, 0, 0};      // clusters of 2, 4, 8 CTAs that run at a time
 
-static cudaLaunchConfig_t launch_cfg(int clusters, cudaStream_t stream, cudaLaunchAttribute* attr) {
+static cudaLaunchConfig_t launch_cfg(int clusters, int splits, cudaStream_t stream, cudaLaunchAttribute* attr) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(2 * clusters, 1, 1);
+    cfg.gridDim = dim3(2 * splits * clusters, 1, 1);
     cfg.blockDim = dim3(THREADS, 1, 1);
     cfg.dynamicSmemBytes = SMEM_BYTES;
     cfg.stream = stream;
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.x = 2 * splits;
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
@@ -834,9 +928,13 @@ static cudaError_t set_attributes() {
         cudaFuncSetAttribute(few::k_dense_few<false, EPI_LINEAR>, cudaFuncAttributeMaxDynamicSharedMemorySize, few::SMEM_BYTES)};
     for (cudaError_t e : es)
         if (e != cudaSuccess) return e;
-    cudaLaunchAttribute attr[1];
-    cudaLaunchConfig_t cfg = launch_cfg(1024, nullptr, attr);
-    return cudaOccupancyMaxActiveClusters(&g_max_clusters, k_dense_pair<false, true, EPI_LINEAR>, &cfg);
+    for (int i = 0; i < 3; ++i) {
+        cudaLaunchAttribute attr[1];
+        cudaLaunchConfig_t cfg = launch_cfg(1024, 1 << i, nullptr, attr);
+        const cudaError_t e = cudaOccupancyMaxActiveClusters(&g_max_clusters[i], k_dense_pair<false, true, EPI_LINEAR>, &cfg);
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
 }
 
 // One matrix operand as it lies in memory: [rows, cols], rows of ld elements.
@@ -845,13 +943,49 @@ struct Mat {
     int64_t rows, cols, ld;
 };
 
+// The pair's tile width and the parts of K.  A wave of tiles costs about
+// nk / splits k-steps of step(bn) and a fixed part worth kFixed steps of the
+// widest tile; splitting adds the swap.  (Steps of a full machine, measured
+// on 4,096 x 7,168 x 7,168: 0.344, 0.31, 0.30 and 0.24 us for 256, 224, 192 and
+// 128 columns.)  Narrower tiles win where they fill the last wave better,
+// parts of K where the tiles are fewer than the SM pairs.
+struct Choice {
+    int bn, splits;
+};
+static double step_cost(int bn) { return bn == 256 ? 1.0 : (bn == 224 ? 0.90 : (bn == 192 ? 0.87 : 0.70)); }
+static Choice choose(int64_t m_tiles, int N, int nk, bool glu) {
+    constexpr double kFixed = 8., kSwap = 8.;
+    static const int widths[] = {256, 224, 192, 128};
+    Choice best{256, 1};
+    double best_cost = 1e300;
+    for (int bn : widths) {
+        if (glu && bn == 224) continue;      // gate and up in whole chunks of 32
+        const int cols = glu ? bn / 2 : bn;
+        const int64_t tiles = m_tiles * ((N + cols - 1) / cols);
+        for (int i = 0; i < 3; ++i) {
+            const int splits = 1 << i, units = glu ? bn / 64 : bn / 32;
+            if (splits > 1 && (units % splits != 0 || tiles > g_max_clusters[i] || nk < 4 * splits)) continue;
+            const int64_t waves = (tiles + g_max_clusters[i] - 1) / std::max(1, g_max_clusters[i]);
+            const double cost = (double)waves * ((nk + splits - 1) / splits * step_cost(bn) + kFixed * bn / 256.) +
+                                (splits > 1 ? kSwap : 0.);
+            if (cost < best_cost) best_cost = cost, best = {bn, splits};
+        }
+    }
+    return best;
+}
+
 template <bool A_MN, bool B_MN, int EPI>
 static moe_status_t product(const Mat& a, const Mat& b, Params p, cudaStream_t s) {
+    MOE_REQUIRE(g_max_clusters[0] > 0, MOE_ERR_NOT_INITIALIZED);
     p.m_tiles = (p.M + TM - 1) / TM;
-    p.bn = 256;
+    p.nk = (int)((p.K + TK - 1) / TK);
+    const Choice c = choose(p.m_tiles, p.N, p.nk, EPI == EPI_GLU);
+    p.bn = c.bn;
+    p.splits = c.splits;
+    p.stage_bytes = HALF_BYTES + (B_MN ? (p.bn / 2 + 63) / 64 * 64 : p.bn / 2) * TK * 2;
+    p.stages = std::min(MAX_STAGES, SMEM_TILES / p.stage_bytes);
     const int cols = EPI == EPI_GLU ? p.bn / 2 : p.bn;      // of D per tile
     p.n_tiles = (p.N + cols - 1) / cols;
-    p.nk = (int)((p.K + TK - 1) / TK);
     p.band = 8;
     p.timeout_ns = 2000000000ull;
     CUtensorMap tmA, tmB, tmY, tmZ, tmZ2;
@@ -864,10 +998,10 @@ static moe_status_t product(const Mat& a, const Mat& b, Params p, cudaStream_t s
         MOE_REQUIRE(make_store_map(&tmZ, p.z, p.M, p.N, p.ldz, false) &&
                         (EPI != EPI_GLU || make_store_map(&tmZ2, p.z + p.N, p.M, p.N, p.ldz, false)),
                     MOE_ERR_CUDA);
-    const int clusters = (int)std::min<int64_t>(p.m_tiles * p.n_tiles, g_max_clusters);
-    MOE_REQUIRE(clusters > 0, MOE_ERR_NOT_INITIALIZED);
+    const int64_t tiles = p.m_tiles * p.n_tiles;
+    const int clusters = (int)(p.splits > 1 ? tiles : std::min<int64_t>(tiles, g_max_clusters[0]));
     cudaLaunchAttribute attr[1];
-    cudaLaunchConfig_t cfg = launch_cfg(clusters, s, attr);
+    cudaLaunchConfig_t cfg = launch_cfg(clusters, p.splits, s, attr);
     if (cudaLaunchKernelEx(&cfg, k_dense_pair<A_MN, B_MN, EPI>, tmA, tmB, tmY, tmZ, tmZ2, p) != cudaSuccess)
         return MOE_ERR_CUDA;
     MOE_CHECK_LAUNCH();
