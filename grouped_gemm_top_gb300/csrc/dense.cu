@@ -62,18 +62,21 @@ constexpr int PART_ROW = 144;
 constexpr int PART_BYTES = 128 * PART_ROW;
 
 // What the epilogue makes of the product v:
-//   EPI_LINEAR  z = v + bias; y = act(z) + residual (bf16; z stored when asked for)
+//   EPI_PLAIN   y = v (bf16)
 //   EPI_F32     y = v (fp32)
+//   EPI_LINEAR  z = v + bias; y = act(z) + residual (bf16; z stored when asked for)
 //   EPI_GLU     columns [0, bn / 2) of the tile are gate, [bn / 2, bn) up:
 //               h = act(gate) * up; a = [gate | up] stored when asked for
-enum { EPI_LINEAR = 0, EPI_F32 = 1, EPI_GLU = 2 };
+// (the activation is a template argument of the pair kernel: an epilogue of
+// 32 columns in registers, unrolled for each of four activations, would be
+// fetched from memory at every launch's first tile)
+enum { EPI_PLAIN = 0, EPI_F32 = 1, EPI_LINEAR = 2, EPI_GLU = 3 };
 
 struct Params {
     int64_t M;              // rows and columns of D (GLU: N = f)
     int N;
     int64_t K;
-    int64_t m_tiles;
-    int n_tiles, nk, band;
+    int m_tiles, n_tiles, nk, band;
     int bn;                 // columns of the pair's tile
     int stages, stage_bytes;
     int splits;             // pairs that share a tile (cluster of 2 * splits)
@@ -120,6 +123,20 @@ __device__ __forceinline__ uint64_t operand_desc(uint32_t saddr) {
 template <bool MN>
 __device__ __forceinline__ constexpr uint64_t k16_step() {
     return MN ? (16 * 128) >> 4 : 32 >> 4;
+}
+
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* m) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(m) : "memory");
+}
+
+// Programmatic dependent launch: a kernel launched with the attribute may
+// start while the one before it in the stream ends, and sets up its barriers
+// and TMEM meanwhile.  Every thread waits here, before it touches memory that
+// is not its own, until the kernels before have completed and what they
+// wrote is visible; only then may the next kernel start its own set-up.
+__device__ __forceinline__ void wait_for_previous_kernels() {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
 __device__ __forceinline__ void tc_mma2_bf16(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
@@ -172,15 +189,22 @@ __device__ __forceinline__ void store_edge(T* p, int n, const float* v) {
     }
 }
 
-// A warp's way out: 32 rows (one per lane) x 32 columns staged in the warp's
-// 4 KB and written by a TMA store (bf16: two boxes of 2 KB that alternate,
-// 64-byte swizzle; fp32: one of 4 KB, 128-byte swizzle; either way the
-// row-per-lane stores to shared memory meet no bank twice).
+// A warp's way out: 32 rows (one per lane) x 32 columns staged in shared
+// memory and written by a TMA store (bf16: boxes of 2 KB, 64-byte swizzle;
+// fp32: 4 KB, 128-byte swizzle; either way the row-per-lane stores to shared
+// memory meet no bank twice).  While tiles follow, a warp has 4 KB, two
+// bf16 boxes or one fp32 box, and waits until a box has been read before it
+// fills it again; its last tile goes through the pipeline stages, free
+// by then, 16 KB a warp, where every chunk finds a box of its own and one
+// fence and one round of stores at the end do for all.
 struct Out {
-    uint32_t buf;
+    uint32_t buf, last;
     int lane;
-    uint32_t boxes;
+    uint32_t at;          // bytes of the buffer used so far
+    bool wide;            // the last tile
+    __device__ __forceinline__ void last_tile() { wide = true, at = 0; }
     __device__ __forceinline__ void send(const CUtensorMap* map, uint32_t b, int col, int64_t row0) {
+        if (wide) return;      // flush()
         fence_proxy_async_shared();
         __syncwarp();
         if (lane == 0) {
@@ -189,9 +213,12 @@ struct Out {
         }
     }
     __device__ __forceinline__ void bf16(const CUtensorMap* map, int col, int64_t row0, const float* v) {
-        const uint32_t b = buf + (boxes++ & 1u) * 2048u;
-        if (lane == 0) bulk_wait_group_read1();      // the box before the last one has been read
-        __syncwarp();
+        const uint32_t b = wide ? last + at : buf + (at & 2048u);
+        at += 2048u;
+        if (!wide) {
+            if (lane == 0) bulk_wait_group_read1();      // the box before the last one has been read
+            __syncwarp();
+        }
         const uint32_t row = b + 64u * lane, sw = (uint32_t)(lane >> 1) & 3u;
 #pragma unroll
         for (int c = 0; c < 4; ++c)
@@ -201,24 +228,33 @@ struct Out {
         send(map, b, col, row0);
     }
     __device__ __forceinline__ void f32(const CUtensorMap* map, int col, int64_t row0, const float* v) {
-        if (lane == 0) bulk_wait_group_read0();
-        __syncwarp();
-        const uint32_t row = buf + 128u * lane, sw = (uint32_t)lane & 7u;
+        const uint32_t b = wide ? last + at : buf;
+        at += 4096u;
+        if (!wide) {
+            if (lane == 0) bulk_wait_group_read0();
+            __syncwarp();
+        }
+        const uint32_t row = b + 128u * lane, sw = (uint32_t)lane & 7u;
 #pragma unroll
         for (int c = 0; c < 8; ++c)
             st_shared_v4(row + (((uint32_t)c ^ sw) << 4), __float_as_uint(v[4 * c]), __float_as_uint(v[4 * c + 1]),
                          __float_as_uint(v[4 * c + 2]), __float_as_uint(v[4 * c + 3]));
-        send(map, buf, col, row0);
+        send(map, b, col, row0);
     }
 };
+static_assert(8 * EPI_WARPS * 2048 <= SMEM_TILES, "the last tile's boxes (z and y of four chunks)");
 
+// Tiles in bands of p.band row tiles, consecutive ones down a band, so that
+// the tiles under way at a time share operand tiles in L2.
 struct Tile {
-    int64_t mt;
-    int nt;
+    int mt, nt;
 };
-__device__ __forceinline__ Tile get_tile(const Params& p, int64_t t) {
+__device__ __forceinline__ Tile get_tile(const Params& p, int t) {
+    const int band_tiles = p.band * p.n_tiles, b = t / band_tiles, rem = t - b * band_tiles;
+    const int m0 = b * p.band, bw = min(p.band, p.m_tiles - m0);
     Tile r;
-    band_decode(t, p.m_tiles, p.n_tiles, p.band, r.mt, r.nt);
+    r.nt = rem / bw;
+    r.mt = m0 + rem - r.nt * bw;
     return r;
 }
 // arrive on the barrier at the same shared offset in both CTAs of the pair
@@ -238,7 +274,7 @@ __device__ __forceinline__ void st_cluster_v4(uint32_t addr, const float* v) {
 
 // 32 columns of a warp's 32 rows from the product (v; GLU: gate v and up u)
 // to memory.  `col`: the first one in D, `n` of them exist (n > 0).
-template <int EPI>
+template <int EPI, int ACT>
 __device__ __forceinline__ void finish(const Params& p, const CUtensorMap* tmY, const CUtensorMap* tmZ,
                                        const CUtensorMap* tmZ2, Out& out, int64_t row0, int64_t row, int col, int n,
                                        float* v, float* u) {
@@ -251,7 +287,7 @@ __device__ __forceinline__ void finish(const Params& p, const CUtensorMap* tmY, 
             out.bf16(tmZ2, col, row0, u);
         }
 #pragma unroll
-        for (int i = 0; i < 32; ++i) u[i] *= act_of(v[i], p.act);
+        for (int i = 0; i < 32; ++i) u[i] *= act_of(v[i], ACT);
         out.bf16(tmY, col, row0, u);
     } else if constexpr (EPI == EPI_F32) {
         if (!edge)
@@ -259,25 +295,28 @@ __device__ __forceinline__ void finish(const Params& p, const CUtensorMap* tmY, 
         else if (row < p.M)
             store_edge(static_cast<float*>(p.y) + row * p.ldy + col, n, v);
     } else {
-        if (p.bias != nullptr) {
+        if constexpr (EPI == EPI_LINEAR) {
+            if (p.bias != nullptr) {
+                const float b = out.lane < n ? __bfloat162float(p.bias[col + out.lane]) : 0.f;
 #pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] += i < n ? __bfloat162float(p.bias[col + i]) : 0.f;
-        }
-        if (p.z != nullptr) {
-            if (!edge)
-                out.bf16(tmZ, col, row0, v);
-            else if (row < p.M)
-                store_edge(p.z + row * p.ldz + col, n, v);
-        }
-        if (p.act != MOE_ACT_NONE) {
+                for (int i = 0; i < 32; ++i) v[i] += __shfl_sync(0xFFFFFFFFu, b, i);
+            }
+            if (p.z != nullptr) {
+                if (!edge)
+                    out.bf16(tmZ, col, row0, v);
+                else if (row < p.M)
+                    store_edge(p.z + row * p.ldz + col, n, v);
+            }
+            if constexpr (ACT != MOE_ACT_NONE) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = act_of(v[i], p.act);
-        }
-        if (p.res != nullptr && row < p.M) {
-            float r[32];
-            load32(p.res + row * p.ldres + col, n, r);
+                for (int i = 0; i < 32; ++i) v[i] = act_of(v[i], ACT);
+            }
+            if (p.res != nullptr && row < p.M) {
+                float r[32];
+                load32(p.res + row * p.ldres + col, n, r);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] += r[i];
+                for (int i = 0; i < 32; ++i) v[i] += r[i];
+            }
         }
         if (!edge)
             out.bf16(tmY, col, row0, v);
@@ -286,9 +325,38 @@ __device__ __forceinline__ void finish(const Params& p, const CUtensorMap* tmY, 
     }
 }
 
+// The last tile's boxes go out, in the order in which finish() filled them:
+// chunks [c0, c1) at `stride` of the tile whose first column in D is col0.
+template <int EPI>
+__device__ __forceinline__ void flush(const Params& p, const CUtensorMap* tmY, const CUtensorMap* tmZ,
+                                      const CUtensorMap* tmZ2, Out& out, int64_t row0, int col0, int c0, int c1,
+                                      int stride) {
+    fence_proxy_async_shared();
+    __syncwarp();
+    if (out.lane != 0 || row0 >= p.M) return;
+    uint32_t b = out.last;
+    for (int c = c0; c < c1; c += stride) {
+        const int col = col0 + 32 * c, n = p.N - col;
+        if (n <= 0 || (EPI != EPI_GLU && n < 32 && (p.N & 7) != 0)) continue;
+        if (EPI == EPI_LINEAR || EPI == EPI_GLU) {
+            if (p.z != nullptr) {
+                tma_store_2d(tmZ, b, col, (int)row0);
+                b += 2048u;
+                if (EPI == EPI_GLU) {
+                    tma_store_2d(tmZ2, b, col, (int)row0);
+                    b += 2048u;
+                }
+            }
+        }
+        tma_store_2d(tmY, b, col, (int)row0);
+        b += EPI == EPI_F32 ? 4096u : 2048u;
+    }
+    bulk_commit_group();
+}
+
 // tmY, tmZ, tmZ2: y (h), z (a's gate half) and a's up half as TMA stores see
 // them, boxes of 32 columns x 32 rows.
-template <bool A_MN, bool B_MN, int EPI>
+template <bool A_MN, bool B_MN, int EPI, int ACT>
 __global__ void __launch_bounds__(THREADS, 1)
     k_dense_pair(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                  const __grid_constant__ CUtensorMap tmY, const __grid_constant__ CUtensorMap tmZ,
@@ -300,9 +368,9 @@ __global__ void __launch_bounds__(THREADS, 1)
     const uint32_t rank = crank & 1u, lead = crank & ~1u;      // in the pair; the pair's leader in the cluster
     const int part = (int)(crank >> 1);                        // of K
     const bool leader = rank == 0;
-    const int64_t first = blockIdx.x / (2 * p.splits), step = gridDim.x / (2 * p.splits);
-    const int64_t total = p.m_tiles * p.n_tiles;
-    const int k0 = (int)((int64_t)p.nk * part / p.splits), k1 = (int)((int64_t)p.nk * (part + 1) / p.splits);
+    const int first = blockIdx.x / (2 * p.splits), step = gridDim.x / (2 * p.splits);
+    const int total = p.m_tiles * p.n_tiles;
+    const int k0 = p.nk / p.splits * part + min(part, p.nk % p.splits), k1 = k0 + p.nk / p.splits + (part < p.nk % p.splits);
 
     const uint32_t bar0 = smem_u32(smem + OFF_BAR);
     auto full_bar = [&](int s) { return bar0 + 8u * s; };
@@ -325,22 +393,31 @@ __global__ void __launch_bounds__(THREADS, 1)
         mbar_init(drain_bar, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         *abort_flag = 0;
+    } else if (threadIdx.x == 64) {
+        prefetch_map(&tmA);
+        prefetch_map(&tmB);
+        prefetch_map(&tmY);
     }
+    __syncthreads();
+    cluster_sync();      // the peer's barriers are initialised
+    // TMEM is for the MMA and epilogue warps to wait for; the producer loads
     if (warp == 1) {
         asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
                      "r"(TMEM_COLS));
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+        tc_fence_before();
     }
-    tc_fence_before();
-    __syncthreads();
-    cluster_sync();      // the peer's barriers are initialised and TMEM is allocated
-    tc_fence_after();
-    const uint32_t tmem_base = *tmem_slot;
+    if (warp == 1 || warp >= 4) {
+        asm volatile("bar.sync 1, %0;" ::"n"(32 + 32 * EPI_WARPS) : "memory");
+        tc_fence_after();
+    }
+    const uint32_t tmem_base = warp == 1 || warp >= 4 ? *tmem_slot : 0u;
+    wait_for_previous_kernels();
 
     const int ew = warp - 4;                       // epilogue warps: their rows and their half of the columns
     const int quarter = ew & 3, half = ew >> 2;
     const uint32_t lane_base = tmem_base + ((uint32_t)(quarter * 32) << 16);
-    Out out{smem_u32(smem + OFF_EPI + ew * EPI_STAGE), lane, 0u};
+    Out out{smem_u32(smem + OFF_EPI + ew * EPI_STAGE), smem_u32(smem + ew * 16384), lane, 0u, false};
 
     if (warp == 0 && lane == 0) {
         // ------------------------------------------------ TMA producer ----
@@ -350,9 +427,9 @@ __global__ void __launch_bounds__(THREADS, 1)
         bool aborted = false;
         // B: bn / 2 rows, or bn / 2 columns in boxes of 64
         const int bh = p.bn / 2, b_boxes = (bh + 63) / 64;
-        for (int64_t t = first; t < total && !aborted; t += step) {
+        for (int t = first; t < total && !aborted; t += step) {
             const Tile ti = get_tile(p, t);
-            const int am = (int)(ti.mt * TM) + 128 * (int)rank;
+            const int am = ti.mt * TM + 128 * (int)rank;
             const int bn = EPI == EPI_GLU ? ti.nt * bh + p.up * (int)rank : ti.nt * p.bn + bh * (int)rank;
             for (int ks = k0; ks < k1; ++ks) {
                 if (!mbar_wait_cluster(empty_bar(stage), phase ^ 1u, p, abort_flag)) {
@@ -399,7 +476,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         uint32_t phase = 0, acc_phase = 0;
         bool aborted = false, issued = false;
         const uint32_t idesc = make_idesc_pair<A_MN, B_MN>(p.bn);
-        for (int64_t t = first; t < total && !aborted; t += step) {
+        for (int t = first; t < total && !aborted; t += step) {
             if (!mbar_wait_cluster(tempty_bar(acc), acc_phase ^ 1u, p, abort_flag)) break;
             tc_fence_after();
             const uint32_t d_tmem = tmem_base + (uint32_t)(acc * ACC_COLS);
@@ -443,26 +520,39 @@ __global__ void __launch_bounds__(THREADS, 1)
         // this warp's chunks of 32 columns: the first or the second half of them
         const int chunks = EPI == EPI_GLU ? p.bn / 64 : p.bn / 32;
         const int c0 = half == 0 ? 0 : (chunks + 1) / 2, c1 = half == 0 ? (chunks + 1) / 2 : chunks;
-        for (int64_t t = first; t < total; t += step) {
+        for (int t = first; t < total; t += step) {
             const Tile ti = get_tile(p, t);
-            const int64_t row0 = ti.mt * TM + 128 * rank + quarter * 32;
+            const int64_t row0 = (int64_t)ti.mt * TM + 128 * rank + quarter * 32;
             if (!mbar_wait_cluster(tfull_bar(acc), acc_phase, p, abort_flag)) break;
             tc_fence_after();
+            if (t + step >= total) out.last_tile();
             const uint32_t tacc = lane_base + (uint32_t)(acc * ACC_COLS);
+            const int col0 = ti.nt * (EPI == EPI_GLU ? p.bn / 2 : p.bn);
+            uint32_t v[32], u[EPI == EPI_GLU ? 32 : 1];
+            tmem_ld32_issue(tacc + 32 * c0, v);
+            if constexpr (EPI == EPI_GLU) tmem_ld32_issue(tacc + p.bn / 2 + 32 * c0, u);
             for (int c = c0; c < c1; ++c) {
-                float v[32], u[EPI == EPI_GLU ? 32 : 1];
-                tmem_ld32(tacc + 32 * c, v);
-                if constexpr (EPI == EPI_GLU) tmem_ld32(tacc + p.bn / 2 + 32 * c, u);
-                if (c == c1 - 1) {      // the accumulator is read: the next tile may have it
+                float fv[32], fu[EPI == EPI_GLU ? 32 : 1];
+                tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 32; ++i) fv[i] = __uint_as_float(v[i]);
+                if constexpr (EPI == EPI_GLU) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) fu[i] = __uint_as_float(u[i]);
+                }
+                if (c + 1 < c1) {      // the next chunk is on its way while this one is worked on
+                    tmem_ld32_issue(tacc + 32 * (c + 1), v);
+                    if constexpr (EPI == EPI_GLU) tmem_ld32_issue(tacc + p.bn / 2 + 32 * (c + 1), u);
+                } else if (!out.wide) {      // the accumulator is read: the next tile may have it
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive_remote(mapa(tempty_bar(acc), lead));
                 }
-                const int col = ti.nt * (EPI == EPI_GLU ? p.bn / 2 : p.bn) + 32 * c;
-                const int n = p.N - col;
+                const int col = col0 + 32 * c, n = p.N - col;
                 if (n > 0 && row0 < p.M)      // the whole warp
-                    finish<EPI>(p, &tmY, &tmZ, &tmZ2, out, row0, row0 + lane, col, n, v, u);
+                    finish<EPI, ACT>(p, &tmY, &tmZ, &tmZ2, out, row0, row0 + lane, col, n, fv, fu);
             }
+            if (out.wide) flush<EPI>(p, &tmY, &tmZ, &tmZ2, out, row0, col0, c0, c1, 1);
             if (++acc == NACC) {
                 acc = 0;
                 acc_phase ^= 1u;
@@ -505,7 +595,11 @@ __global__ void __launch_bounds__(THREADS, 1)
         cluster_sync();      // every part has what it adds up
         if (warp >= 4 && ok) {
             const Tile ti = get_tile(p, first);
-            const int64_t row0 = ti.mt * TM + 128 * rank + quarter * 32;
+            const int64_t row0 = (int64_t)ti.mt * TM + 128 * rank + quarter * 32;
+            const int col0 = ti.nt * (EPI == EPI_GLU ? p.bn / 2 : p.bn);
+            // boxes above the partial chunks: at most 3 of 2 KB (4 KB) a unit, four units a warp
+            out.last = smem_u32(smem + SMEM_TILES - (ew + 1) * 8192);
+            out.last_tile();
             for (int un = part * own + half; un < (part + 1) * own; un += 2) {
                 float s[2][32];
 #pragma unroll
@@ -530,11 +624,11 @@ __global__ void __launch_bounds__(THREADS, 1)
                         }
                     }
                 }
-                const int col = ti.nt * (EPI == EPI_GLU ? p.bn / 2 : p.bn) + 32 * un;
-                const int n = p.N - col;
+                const int col = col0 + 32 * un, n = p.N - col;
                 if (n > 0 && row0 < p.M)
-                    finish<EPI>(p, &tmY, &tmZ, &tmZ2, out, row0, row0 + lane, col, n, s[0], s[1]);
+                    finish<EPI, ACT>(p, &tmY, &tmZ, &tmZ2, out, row0, row0 + lane, col, n, s[0], s[1]);
             }
+            flush<EPI>(p, &tmY, &tmZ, &tmZ2, out, row0, col0, part * own + half, (part + 1) * own, 2);
             if (lane == 0) bulk_wait_group0();
             __syncwarp();
         }
@@ -630,11 +724,11 @@ __global__ void __launch_bounds__(THREADS, 2)
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = s.splits > 1 ? cluster_ctarank() : 0;
-    const int64_t tile = blockIdx.x / s.splits;
-    const int nt = (int)(tile % p.n_tiles);
-    const int64_t m0 = (tile / p.n_tiles) * s.rows;
+    const int tile = blockIdx.x / s.splits, mt = tile / p.n_tiles, nt = tile - mt * p.n_tiles;
+    const int64_t m0 = (int64_t)mt * s.rows;
     const int m = (int)min((int64_t)s.rows, p.M - m0);
-    const int k0 = (int)((int64_t)p.nk * rank / s.splits), k1 = (int)((int64_t)p.nk * (rank + 1) / s.splits);
+    const int k0 = p.nk / s.splits * (int)rank + min((int)rank, p.nk % s.splits);
+    const int k1 = k0 + p.nk / s.splits + ((int)rank < p.nk % s.splits);
     const int stage_bytes = W_BYTES + s.rows * TK * 2;
 
     const uint32_t bar0 = smem_u32(smem + OFF_BAR);
@@ -661,6 +755,7 @@ __global__ void __launch_bounds__(THREADS, 2)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
+    wait_for_previous_kernels();
 
     if (warp == 0 && lane == 0) {
         // ------------------------------------------------ TMA producer ----
@@ -812,6 +907,7 @@ __global__ void __launch_bounds__(THREADS, 2)
 __global__ void __launch_bounds__(256) k_glu_bwd(const __nv_bfloat16* __restrict__ dh, int64_t lddh,
                                                  const __nv_bfloat16* __restrict__ a, int64_t lda, int64_t M, int f,
                                                  int act, __nv_bfloat16* __restrict__ da, int64_t ldda) {
+    wait_for_previous_kernels();
     const int nvec = f / 8;
     const int64_t n = M * nvec, stride = (int64_t)gridDim.x * blockDim.x;
     for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += stride) {
@@ -841,6 +937,7 @@ __global__ void __launch_bounds__(256) k_act_bwd(const __nv_bfloat16* __restrict
                                                  int act, __nv_bfloat16* __restrict__ dz, int64_t lddz,
                                                  float* __restrict__ part) {
     __shared__ float s_sum[8][257];
+    wait_for_previous_kernels();
     const int lane = threadIdx.x & 31, grp = threadIdx.x >> 5;
     const int c = blockIdx.x * 256 + lane * 8;
     const int n = N - c < 0 ? 0 : (N - c > 8 ? 8 : N - c);
@@ -893,6 +990,8 @@ __global__ void __launch_bounds__(256) k_act_bwd(const __nv_bfloat16* __restrict
 
 static int g_max_clusters[3] = {0, 0, 0};      // clusters of 2, 4, 8 CTAs that run at a time
 
+// attr: room for two (the cluster, and the early start described at
+// wait_for_previous_kernels)
 static cudaLaunchConfig_t launch_cfg(int clusters, int splits, cudaStream_t stream, cudaLaunchAttribute* attr) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2 * splits * clusters, 1, 1);
@@ -903,20 +1002,39 @@ static cudaLaunchConfig_t launch_cfg(int clusters, int splits, cudaStream_t stre
     attr[0].val.clusterDim.x = 2 * splits;
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = 2;
     return cfg;
 }
 
-// the products that are built: forward (plain and GLU), input gradient, weight gradient (bf16, fp32)
-#define MOE_DENSE_INSTANCES(X) \
-    X(false, true, EPI_LINEAR) X(false, true, EPI_GLU) X(false, false, EPI_LINEAR) X(true, true, EPI_LINEAR) \
-    X(true, true, EPI_F32)
+template <typename... Ts, typename... As>
+static cudaError_t launch_early(dim3 grid, int threads, cudaStream_t s, void (*kernel)(Ts...), As... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, Ts(args)...);
+}
+
+// the products that are built: plain forward, input gradient and weight
+// gradient (bf16, fp32); forward with an epilogue, gated forward
+#define MOE_DENSE_INSTANCES(X)                                                                                       \
+    X(false, true, EPI_PLAIN, 0) X(false, false, EPI_PLAIN, 0) X(true, true, EPI_PLAIN, 0) X(true, true, EPI_F32, 0) \
+    X(false, true, EPI_LINEAR, 0) X(false, true, EPI_LINEAR, 1) X(false, true, EPI_LINEAR, 2)                        \
+    X(false, true, EPI_LINEAR, 3) X(false, true, EPI_GLU, 0) X(false, true, EPI_GLU, 1) X(false, true, EPI_GLU, 2)   \
+    X(false, true, EPI_GLU, 3)
 
 static cudaError_t set_attributes() {
-#define X(A, B, E)                                                                                                  \
+#define X(A, B, E, ACT)                                                                                                \
     {                                                                                                               \
-        cudaError_t e = cudaFuncSetAttribute(k_dense_pair<A, B, E>, cudaFuncAttributeMaxDynamicSharedMemorySize,    \
+        cudaError_t e = cudaFuncSetAttribute(k_dense_pair<A, B, E, ACT>, cudaFuncAttributeMaxDynamicSharedMemorySize,    \
                                              SMEM_BYTES);                                                           \
         if (e != cudaSuccess) return e;                                                                             \
     }
@@ -929,9 +1047,9 @@ static cudaError_t set_attributes() {
     for (cudaError_t e : es)
         if (e != cudaSuccess) return e;
     for (int i = 0; i < 3; ++i) {
-        cudaLaunchAttribute attr[1];
+        cudaLaunchAttribute attr[2];
         cudaLaunchConfig_t cfg = launch_cfg(1024, 1 << i, nullptr, attr);
-        const cudaError_t e = cudaOccupancyMaxActiveClusters(&g_max_clusters[i], k_dense_pair<false, true, EPI_LINEAR>, &cfg);
+        const cudaError_t e = cudaOccupancyMaxActiveClusters(&g_max_clusters[i], k_dense_pair<false, true, EPI_PLAIN, 0>, &cfg);
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;
@@ -974,10 +1092,10 @@ static Choice choose(int64_t m_tiles, int N, int nk, bool glu) {
     return best;
 }
 
-template <bool A_MN, bool B_MN, int EPI>
+template <bool A_MN, bool B_MN, int EPI, int ACT>
 static moe_status_t product(const Mat& a, const Mat& b, Params p, cudaStream_t s) {
     MOE_REQUIRE(g_max_clusters[0] > 0, MOE_ERR_NOT_INITIALIZED);
-    p.m_tiles = (p.M + TM - 1) / TM;
+    p.m_tiles = (int)((p.M + TM - 1) / TM);
     p.nk = (int)((p.K + TK - 1) / TK);
     const Choice c = choose(p.m_tiles, p.N, p.nk, EPI == EPI_GLU);
     p.bn = c.bn;
@@ -998,11 +1116,12 @@ static moe_status_t product(const Mat& a, const Mat& b, Params p, cudaStream_t s
         MOE_REQUIRE(make_store_map(&tmZ, p.z, p.M, p.N, p.ldz, false) &&
                         (EPI != EPI_GLU || make_store_map(&tmZ2, p.z + p.N, p.M, p.N, p.ldz, false)),
                     MOE_ERR_CUDA);
-    const int64_t tiles = p.m_tiles * p.n_tiles;
+    const int64_t tiles = (int64_t)p.m_tiles * p.n_tiles;
+    MOE_REQUIRE(tiles <= 0x3FFFFFFF, MOE_ERR_UNSUPPORTED);
     const int clusters = (int)(p.splits > 1 ? tiles : std::min<int64_t>(tiles, g_max_clusters[0]));
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     cudaLaunchConfig_t cfg = launch_cfg(clusters, p.splits, s, attr);
-    if (cudaLaunchKernelEx(&cfg, k_dense_pair<A_MN, B_MN, EPI>, tmA, tmB, tmY, tmZ, tmZ2, p) != cudaSuccess)
+    if (cudaLaunchKernelEx(&cfg, k_dense_pair<A_MN, B_MN, EPI, ACT>, tmA, tmB, tmY, tmZ, tmZ2, p) != cudaSuccess)
         return MOE_ERR_CUDA;
     MOE_CHECK_LAUNCH();
     return MOE_OK;
@@ -1018,10 +1137,10 @@ static moe_status_t product_few(const Mat& x, const Mat& w, Params p, cudaStream
     s.stages = std::min(few::MAX_STAGES, few::SMEM_TILES / (few::W_BYTES + s.rows * TK * 2));
     s.tmem_cols = s.rows <= 32 ? 32 : (s.rows <= 64 ? 64 : 128);
     p.n_tiles = EPI == EPI_GLU ? (p.N + 63) / 64 : (p.N + 127) / 128;
-    p.m_tiles = (p.M + s.rows - 1) / s.rows;
+    p.m_tiles = (int)((p.M + s.rows - 1) / s.rows);
     p.nk = (int)((p.K + TK - 1) / TK);
     p.timeout_ns = 2000000000ull;
-    const int64_t tiles = p.m_tiles * p.n_tiles;
+    const int64_t tiles = (int64_t)p.m_tiles * p.n_tiles;
     const int sms = device_sm_count();
     s.splits = 1;
     while (s.splits < 8 && tiles * s.splits * 2 <= 2 * sms && p.nk >= 8 * s.splits) s.splits *= 2;
@@ -1035,13 +1154,15 @@ static moe_status_t product_few(const Mat& x, const Mat& w, Params p, cudaStream
     cfg.blockDim = dim3(few::THREADS, 1, 1);
     cfg.dynamicSmemBytes = few::SMEM_BYTES;
     cfg.stream = st;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = s.splits;
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = 2;
     if (cudaLaunchKernelEx(&cfg, few::k_dense_few<W_MN, EPI>, tmW, tmX, p, s) != cudaSuccess) return MOE_ERR_CUDA;
     MOE_CHECK_LAUNCH();
     return MOE_OK;
@@ -1086,7 +1207,15 @@ extern "C" moe_status_t linear_fwd(const void* x, int64_t ldx, const void* w, in
     p.res = static_cast<const __nv_bfloat16*>(res), p.ldres = ldres;
     p.err = err;
     if (few_rows(M)) return product_few<true, EPI_LINEAR>({x, M, K, ldx}, {w, K, N, ldw}, p, (cudaStream_t)stream);
-    return product<false, true, EPI_LINEAR>({x, M, K, ldx}, {w, K, N, ldw}, p, (cudaStream_t)stream);
+    const Mat mx{x, M, K, ldx}, mw{w, K, N, ldw};
+    cudaStream_t s = (cudaStream_t)stream;
+    if (!bias && !res && !z && act == MOE_ACT_NONE) return product<false, true, EPI_PLAIN, 0>(mx, mw, p, s);
+    switch (act) {
+        case MOE_ACT_RELU: return product<false, true, EPI_LINEAR, MOE_ACT_RELU>(mx, mw, p, s);
+        case MOE_ACT_GELU: return product<false, true, EPI_LINEAR, MOE_ACT_GELU>(mx, mw, p, s);
+        case MOE_ACT_SILU: return product<false, true, EPI_LINEAR, MOE_ACT_SILU>(mx, mw, p, s);
+        default: return product<false, true, EPI_LINEAR, MOE_ACT_NONE>(mx, mw, p, s);
+    }
 }
 
 // D[M, N] = dy W^T and D = x^T dy with plain stores
@@ -1095,7 +1224,7 @@ static moe_status_t input_grad(const void* dy, int64_t lddy, const void* w, int6
     dense::Params p{};
     p.M = M, p.N = (int)K, p.K = N, p.act = MOE_ACT_NONE, p.y = dx, p.ldy = lddx, p.err = err;
     if (few_rows(M)) return product_few<false, EPI_LINEAR>({dy, M, N, lddy}, {w, K, N, ldw}, p, s);
-    return product<false, false, EPI_LINEAR>({dy, M, N, lddy}, {w, K, N, ldw}, p, s);
+    return product<false, false, EPI_PLAIN, 0>({dy, M, N, lddy}, {w, K, N, ldw}, p, s);
 }
 static moe_status_t weight_grad(const void* x, int64_t ldx, const void* dy, int64_t lddy, int64_t M, int N, int64_t K,
                                 void* dw, int dw_type, int64_t lddw, int32_t* err, cudaStream_t s) {
@@ -1105,8 +1234,8 @@ static moe_status_t weight_grad(const void* x, int64_t ldx, const void* dy, int6
     }
     dense::Params p{};
     p.M = K, p.N = N, p.K = M, p.act = MOE_ACT_NONE, p.y = dw, p.ldy = lddw, p.err = err;
-    if (dw_type == MOE_TYPE_F32) return product<true, true, EPI_F32>({x, M, K, ldx}, {dy, M, N, lddy}, p, s);
-    return product<true, true, EPI_LINEAR>({x, M, K, ldx}, {dy, M, N, lddy}, p, s);
+    if (dw_type == MOE_TYPE_F32) return product<true, true, EPI_F32, 0>({x, M, K, ldx}, {dy, M, N, lddy}, p, s);
+    return product<true, true, EPI_PLAIN, 0>({x, M, K, ldx}, {dy, M, N, lddy}, p, s);
 }
 
 static size_t dz_bytes(int64_t M, int N) { return ((size_t)M * ((N + 7) / 8 * 8) * 2 + 255) / 256 * 256; }
@@ -1143,10 +1272,9 @@ extern "C" moe_status_t linear_bwd(const void* dy, int64_t lddy, const void* x, 
     if (need_ws) {
         __nv_bfloat16* dz = static_cast<__nv_bfloat16*>(ws);
         const int64_t lddz = (N + 7) / 8 * 8;
-        k_act_bwd<<<dim3((N + 255) / 256, act_parts(M)), 256, 0, s>>>(
-            static_cast<const __nv_bfloat16*>(dy), lddy, static_cast<const __nv_bfloat16*>(z), ldz, M, N, act, dz,
-            lddz, part);
-        MOE_CHECK_LAUNCH();
+        if (launch_early(dim3((N + 255) / 256, act_parts(M)), 256, s, k_act_bwd, static_cast<const __nv_bfloat16*>(dy),
+                         lddy, static_cast<const __nv_bfloat16*>(z), ldz, M, N, act, dz, lddz, part) != cudaSuccess)
+            return MOE_ERR_CUDA;
         if (with_z) g = dz, ldg = lddz;
     }
     if (dbias) {
@@ -1177,7 +1305,14 @@ extern "C" moe_status_t gated_ffn_fwd(const void* x, int64_t ldx, const void* w1
     p.err = err;
     if (few_rows(M))
         return product_few<true, EPI_GLU>({x, M, d, ldx}, {w1, d, 2 * (int64_t)f, ldw}, p, (cudaStream_t)stream);
-    return product<false, true, EPI_GLU>({x, M, d, ldx}, {w1, d, 2 * (int64_t)f, ldw}, p, (cudaStream_t)stream);
+    const Mat mx{x, M, d, ldx}, mw{w1, d, 2 * (int64_t)f, ldw};
+    cudaStream_t s = (cudaStream_t)stream;
+    switch (act) {
+        case MOE_ACT_RELU: return product<false, true, EPI_GLU, MOE_ACT_RELU>(mx, mw, p, s);
+        case MOE_ACT_GELU: return product<false, true, EPI_GLU, MOE_ACT_GELU>(mx, mw, p, s);
+        case MOE_ACT_SILU: return product<false, true, EPI_GLU, MOE_ACT_SILU>(mx, mw, p, s);
+        default: return product<false, true, EPI_GLU, MOE_ACT_NONE>(mx, mw, p, s);
+    }
 }
 
 extern "C" moe_status_t gated_ffn_bwd(const void* dh, int64_t lddh, const void* a, int64_t lda, const void* x,
@@ -1202,10 +1337,10 @@ extern "C" moe_status_t gated_ffn_bwd(const void* dh, int64_t lddh, const void* 
     cudaStream_t s = (cudaStream_t)stream;
     if (M > 0) {
         const int64_t n = M * (f / 8);
-        k_glu_bwd<<<(unsigned)std::min<int64_t>((n + 255) / 256, (int64_t)sms * 8), 256, 0, s>>>(
-            static_cast<const __nv_bfloat16*>(dh), lddh, static_cast<const __nv_bfloat16*>(a), lda, M, f, act,
-            static_cast<__nv_bfloat16*>(da), ldda);
-        MOE_CHECK_LAUNCH();
+        if (launch_early(dim3((unsigned)std::min<int64_t>((n + 255) / 256, (int64_t)sms * 8)), 256, s, k_glu_bwd,
+                         static_cast<const __nv_bfloat16*>(dh), lddh, static_cast<const __nv_bfloat16*>(a), lda, M, f,
+                         act, static_cast<__nv_bfloat16*>(da), ldda) != cudaSuccess)
+            return MOE_ERR_CUDA;
     }
     if (dx && M > 0) {
         const moe_status_t st = input_grad(da, ldda, w1, ldw, M, 2 * f, d, dx, lddx, err, s);
