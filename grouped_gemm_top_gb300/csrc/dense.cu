@@ -928,13 +928,27 @@ __global__ void __launch_bounds__(256) k_glu_bwd(const __nv_bfloat16* __restrict
     }
 }
 
-// dz = dy * act'(z) (bf16, when act is not MOE_ACT_NONE) and the column sums of the
-// unrounded dz over this CTA's rows, one row of partial sums per blockIdx.y.
-// A thread owns 8 columns; the CTA's 8 groups of 32 threads take every
-// eighth row and are added in order at the end.
+// dz = dy * act'(z) (bf16, when ACT is not MOE_ACT_NONE) and the column sums of
+// the unrounded dz over this CTA's rows, one row of partial sums per
+// blockIdx.y.  A thread owns 8 columns; the CTA's 8 warps take every eighth
+// row, kActRowsInFlight of them loaded before the first is worked on (with
+// one at a time the loads covered 60 % of the memory's latency), and are added in
+// order at the end.  Bound by its 6 bytes an element.
+constexpr int kActRowsInFlight = 4;
+
+__device__ __forceinline__ uint4 load_vec8(const __nv_bfloat16* p, int n) {      // n < 8: zeros after them
+    if (n == 8) return *reinterpret_cast<const uint4*>(p);
+    uint32_t w[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        if (j < n) w[j >> 1] |= (uint32_t)__bfloat16_as_ushort(p[j]) << (16 * (j & 1));
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+template <int ACT>
 __global__ void __launch_bounds__(256) k_act_bwd(const __nv_bfloat16* __restrict__ dy, int64_t lddy,
                                                  const __nv_bfloat16* __restrict__ z, int64_t ldz, int64_t M, int N,
-                                                 int act, __nv_bfloat16* __restrict__ dz, int64_t lddz,
+                                                 __nv_bfloat16* __restrict__ dz, int64_t lddz,
                                                  float* __restrict__ part) {
     __shared__ float s_sum[8][257];
     wait_for_previous_kernels();
@@ -944,33 +958,37 @@ __global__ void __launch_bounds__(256) k_act_bwd(const __nv_bfloat16* __restrict
     float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     const int64_t step = (int64_t)gridDim.y * 8;
     if (n > 0) {
-        for (int64_t row = (int64_t)blockIdx.y * 8 + grp; row < M; row += step) {
-            float d[8], v[8];
-            if (n == 8) {
-                unpack8(*reinterpret_cast<const uint4*>(dy + row * lddy + c), d);
-            } else {
+        for (int64_t row0 = (int64_t)blockIdx.y * 8 + grp; row0 < M; row0 += step * kActRowsInFlight) {
+            uint4 a[kActRowsInFlight], b[kActRowsInFlight];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) d[j] = j < n ? __bfloat162float(dy[row * lddy + c + j]) : 0.f;
-            }
-            if (act != MOE_ACT_NONE) {
-                if (n == 8) {
-                    unpack8(*reinterpret_cast<const uint4*>(z + row * ldz + c), v);
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) v[j] = j < n ? __bfloat162float(z[row * ldz + c + j]) : 0.f;
-                }
-#pragma unroll
-                for (int j = 0; j < 8; ++j) d[j] *= act_slope(v[j], act);
-                if (n == 8) {
-                    *reinterpret_cast<uint4*>(dz + row * lddz + c) = pack8(d);
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        if (j < n) dz[row * lddz + c + j] = __float2bfloat16_rn(d[j]);
-                }
+            for (int i = 0; i < kActRowsInFlight; ++i) {
+                const int64_t row = row0 + i * step;
+                if (row >= M) continue;
+                a[i] = load_vec8(dy + row * lddy + c, n);
+                if (ACT != MOE_ACT_NONE) b[i] = load_vec8(z + row * ldz + c, n);
             }
 #pragma unroll
-            for (int j = 0; j < 8; ++j) sum[j] += d[j];
+            for (int i = 0; i < kActRowsInFlight; ++i) {
+                const int64_t row = row0 + i * step;
+                if (row >= M) continue;
+                float d[8];
+                unpack8(a[i], d);
+                if (ACT != MOE_ACT_NONE) {
+                    float v[8];
+                    unpack8(b[i], v);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) d[j] *= act_slope(v[j], ACT);
+                    if (n == 8) {
+                        *reinterpret_cast<uint4*>(dz + row * lddz + c) = pack8(d);
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            if (j < n) dz[row * lddz + c + j] = __float2bfloat16_rn(d[j]);
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < 8; ++j) sum[j] += d[j];
+            }
         }
     }
     if (part == nullptr) return;
@@ -1272,8 +1290,12 @@ extern "C" moe_status_t linear_bwd(const void* dy, int64_t lddy, const void* x, 
     if (need_ws) {
         __nv_bfloat16* dz = static_cast<__nv_bfloat16*>(ws);
         const int64_t lddz = (N + 7) / 8 * 8;
-        if (launch_early(dim3((N + 255) / 256, act_parts(M)), 256, s, k_act_bwd, static_cast<const __nv_bfloat16*>(dy),
-                         lddy, static_cast<const __nv_bfloat16*>(z), ldz, M, N, act, dz, lddz, part) != cudaSuccess)
+        void (*const kernels[])(const __nv_bfloat16*, int64_t, const __nv_bfloat16*, int64_t, int64_t, int,
+                                __nv_bfloat16*, int64_t, float*) = {
+            k_act_bwd<MOE_ACT_NONE>, k_act_bwd<MOE_ACT_RELU>, k_act_bwd<MOE_ACT_GELU>, k_act_bwd<MOE_ACT_SILU>};
+        if (launch_early(dim3((N + 255) / 256, act_parts(M)), 256, s, kernels[act],
+                         static_cast<const __nv_bfloat16*>(dy), lddy, static_cast<const __nv_bfloat16*>(z), ldz, M, N,
+                         dz, lddz, part) != cudaSuccess)
             return MOE_ERR_CUDA;
         if (with_z) g = dz, ldg = lddz;
     }

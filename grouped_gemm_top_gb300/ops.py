@@ -620,17 +620,13 @@ def moe_selftest_bounded_wait(timeout_ns, err, completed, stream=None):
 # stream come from torch's own C entry points, without the Python objects
 # around them.
 
-_TYPES = {torch.bfloat16: MOE_TYPE_BF16, torch.float32: MOE_TYPE_F32}
-_F32, _I32, _U8 = (torch.float32,), (torch.int32,), (torch.uint8,)
-_E4M3 = (torch.uint8, torch.float8_e4m3fn)
-
-
-def _device():
-    return torch._C._cuda_getDevice()
-
-
-def _raw_stream(device):
-    return torch._C._cuda_getCurrentRawStream(device)
+_BF16 = {torch.bfloat16: MOE_TYPE_BF16}
+_F32 = {torch.float32: MOE_TYPE_F32}
+_TYPES = {**_BF16, **_F32}
+_I32, _U8 = {torch.int32: 0}, {torch.uint8: 0}
+_E4M3 = {torch.uint8: 0, torch.float8_e4m3fn: 0}
+_device = torch._C._cuda_getDevice
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
 def _need(fn, ok):
@@ -638,36 +634,36 @@ def _need(fn, ok):
         raise MoEError(fn, MOE_ERR_INVALID_ARG)
 
 
-def _rows(fn, t, m=None, n=None, types=_TYPES):
-    """(pointer, type code, row stride) of a [m, n] matrix on the current
-    device; (None, 0, 0) for None."""
+def _rows(fn, t, dev, m=None, n=None, types=_TYPES):
+    """(pointer, type code, row stride) of a [m, n] matrix on device `dev`;
+    (None, 0, 0) for None."""
     if t is None:
         return None, 0, 0
-    shape, dtype = t.shape, t.dtype
+    shape, code = t.shape, types.get(t.dtype)
     # (a tensor in host memory has device -1)
-    if len(shape) != 2 or dtype not in types or t.get_device() != _device():
+    if code is None or len(shape) != 2 or t.get_device() != dev:
         raise MoEError(fn, MOE_ERR_INVALID_ARG)
     rows, cols = shape
     ld, step = t.stride()
-    if rows <= 1 and ld < cols:
+    if ld < cols and rows <= 1:
         ld = cols
-    if (m is not None and rows != m) or (n is not None and cols != n) or (step != 1 and cols != 1) or ld < cols:
+    if ld < cols or (step != 1 and cols != 1) or (m is not None and rows != m) or (n is not None and cols != n):
         raise MoEError(fn, MOE_ERR_INVALID_ARG)
-    return t.data_ptr(), _TYPES[dtype], ld
+    return t.data_ptr(), code, ld
 
 
-def _flat(fn, t, n, types):
-    """Pointer of a contiguous tensor of n elements on the current device."""
+def _flat(fn, t, dev, n, types):
+    """Pointer of a contiguous tensor of n elements on device `dev`."""
     if t is None:
         return None
-    if t.dtype not in types or t.numel() != n or t.get_device() != _device() or not t.is_contiguous():
+    if t.dtype not in types or t.numel() != n or t.get_device() != dev or not t.is_contiguous():
         raise MoEError(fn, MOE_ERR_INVALID_ARG)
     return t.data_ptr()
 
 
-def _handle(stream):
+def _handle(stream, dev):
     """The stream's handle; of the current stream for None."""
-    return _raw_stream(_device()) if stream is None else stream.cuda_stream
+    return _raw_stream(dev) if stream is None else stream.cuda_stream
 
 
 def _new(shape, dtype, like, stream):
@@ -686,14 +682,15 @@ def rmsnorm_residual_fwd(x, w, residual=None, eps=1e-6, y=None, r=None, rstd=Non
     given are allocated; r is only written when there is a residual.
     Returns (y, r, rstd, codes, scales), None for what is not produced."""
     fn = "rmsnorm_residual_fwd"
-    px, tx, ldx = _rows(fn, x)
+    dev = _device()
+    px, tx, ldx = _rows(fn, x, dev)
     M, N = x.shape
-    pres, tres, ldres = _rows(fn, residual, M, N)
+    pres, tres, ldres = _rows(fn, residual, dev, M, N)
     if residual is None:
         tres = tx if r is None else _TYPES.get(r.dtype, -1)
     elif r is None and want_r:
         r = _new((M, N), residual.dtype, x, stream)
-    pw = _flat(fn, w, N, _TYPES)
+    pw = _flat(fn, w, dev, N, _TYPES)
     if y is None and want_y:
         y = _new((M, N), y_dtype, x, stream)
     if rstd is None:
@@ -702,18 +699,18 @@ def rmsnorm_residual_fwd(x, w, residual=None, eps=1e-6, y=None, r=None, rstd=Non
         rows = (M + 127) // 128 * 128 if sf_layout == MOE_SF_ATOMS else M
         codes = _new((rows, N), torch.uint8, x, stream)
         scales = _new((rows * (N // 32),), torch.uint8, x, stream) if scales is None else scales
-    pr, tr, ldr = _rows(fn, r, M, N)
+    pr, tr, ldr = _rows(fn, r, dev, M, N)
     _need(fn, r is None or tr == tres)
-    py, ty, ldy = _rows(fn, y, M, N)
+    py, ty, ldy = _rows(fn, y, dev, M, N)
     pc = ps = None
     if codes is not None or scales is not None:
         rows = (M + 127) // 128 * 128 if sf_layout == MOE_SF_ATOMS else M
         _need(fn, codes is not None and scales is not None)
-        pc = _flat(fn, codes, rows * N, _E4M3)
-        ps = _flat(fn, scales, rows * (N // 32), _U8)
+        pc = _flat(fn, codes, dev, rows * N, _E4M3)
+        ps = _flat(fn, scales, dev, rows * (N // 32), _U8)
     _check(fn, lib.rmsnorm_residual_fwd(px, tx, ldx, pres, tres, ldres, pw, _TYPES[w.dtype], eps, M, N, pr, ldr, py,
-                                        ty, ldy, _flat(fn, rstd, M, _F32), pc, ps, int(sf_layout),
-                                        _handle(stream)))
+                                        ty, ldy, _flat(fn, rstd, dev, M, _F32), pc, ps, int(sf_layout),
+                                        _handle(stream, dev)))
     return y, r, rstd, codes, scales
 
 
@@ -726,10 +723,11 @@ def rmsnorm_residual_bwd(dy, r, w, rstd, dres=None, want_dw=True, dx=None, dw=No
     """Gradients of rmsnorm_residual_fwd: dx (of x and of the residual; + dres)
     and dw (fp32).  See include/moe.h.  Returns (dx, dw)."""
     fn = "rmsnorm_residual_bwd"
-    pr, tr, ldr = _rows(fn, r)
+    dev = _device()
+    pr, tr, ldr = _rows(fn, r, dev)
     M, N = r.shape
-    pdy, tdy, lddy = _rows(fn, dy, M, N)
-    pdr, tdr, lddr = _rows(fn, dres, M, N)
+    pdy, tdy, lddy = _rows(fn, dy, dev, M, N)
+    pdr, tdr, lddr = _rows(fn, dres, dev, M, N)
     _need(fn, dres is None or tdr == tr)
     _need(fn, w.dtype in _TYPES)
     if dx is None:
@@ -738,16 +736,16 @@ def rmsnorm_residual_bwd(dy, r, w, rstd, dres=None, want_dw=True, dx=None, dw=No
         dw = _new((N,), torch.float32, r, stream)
     if dw is not None and ws is None:
         ws = _new((max(rmsnorm_bwd_workspace_size(M, N), 0),), torch.uint8, r, stream)
-    pdx, tdx, lddx = _rows(fn, dx, M, N)
+    pdx, tdx, lddx = _rows(fn, dx, dev, M, N)
     _need(fn, tdx == tr)
-    nws = ws.numel() * ws.element_size() if ws is not None else 0
-    _check(fn, lib.rmsnorm_residual_bwd(pdy, tdy, lddy, pr, tr, ldr, _flat(fn, w, N, _TYPES), _TYPES[w.dtype],
-                                        _flat(fn, rstd, M, _F32), pdr, lddr, M, N, pdx, lddx,
-                                        _flat(fn, dw, N, _F32), _p(ws), nws, _handle(stream)))
+    nws = 0 if ws is None else ws.numel()
+    _check(fn, lib.rmsnorm_residual_bwd(pdy, tdy, lddy, pr, tr, ldr, _flat(fn, w, dev, N, _TYPES), _TYPES[w.dtype],
+                                        _flat(fn, rstd, dev, M, _F32), pdr, lddr, M, N, pdx, lddx,
+                                        _flat(fn, dw, dev, N, _F32), _flat(fn, ws, dev, nws, _U8), nws,
+                                        _handle(stream, dev)))
     return dx, dw
 
 
-_BF16 = (torch.bfloat16,)
 _ACTS = {"none": MOE_ACT_NONE, "relu": MOE_ACT_RELU, "gelu": MOE_ACT_GELU, "silu": MOE_ACT_SILU}
 
 
@@ -768,18 +766,19 @@ def linear_fwd(x, w, bias=None, act="none", residual=None, y=None, z=None, want_
     or "silu").  See include/moe.h.  Rows of every matrix start at multiples of 16 bytes.
     Returns y, or (y, z) when z is asked for."""
     fn = "linear_fwd"
-    px, _, ldx = _rows(fn, x, types=_BF16)
+    dev = _device()
+    px, _, ldx = _rows(fn, x, dev, types=_BF16)
     M, K = x.shape
-    pw, _, ldw = _rows(fn, w, K, types=_BF16)
+    pw, _, ldw = _rows(fn, w, dev, K, types=_BF16)
     N = w.shape[1]
     y = y if y is not None else _new_rows(M, N, torch.bfloat16, x, stream)
     if want_z and z is None:
         z = _new_rows(M, N, torch.bfloat16, x, stream)
-    pr, _, ldr = _rows(fn, residual, M, N, _BF16)
-    py, _, ldy = _rows(fn, y, M, N, _BF16)
-    pz, _, ldz = _rows(fn, z, M, N, _BF16)
-    _check(fn, lib.linear_fwd(px, ldx, pw, ldw, _flat(fn, bias, N, _BF16), _act(fn, act), pr, ldr, M, N, K, py, ldy,
-                              pz, ldz, _p(err), _handle(stream)))
+    pr, _, ldr = _rows(fn, residual, dev, M, N, _BF16)
+    py, _, ldy = _rows(fn, y, dev, M, N, _BF16)
+    pz, _, ldz = _rows(fn, z, dev, M, N, _BF16)
+    _check(fn, lib.linear_fwd(px, ldx, pw, ldw, _flat(fn, bias, dev, N, _BF16), _act(fn, act), pr, ldr, M, N, K, py,
+                              ldy, pz, ldz, _flat(fn, err, dev, 1, _I32), _handle(stream, dev)))
     return y if z is None else (y, z)
 
 
@@ -794,13 +793,14 @@ def linear_bwd(dy, x, w, z=None, act="none", want_dx=True, want_dw=True, want_db
     (float32), those that are wanted or given.  See include/moe.h.  Returns
     (dx, dw, dbias)."""
     fn = "linear_bwd"
+    dev = _device()
     act = _act(fn, act)
-    pdy, _, lddy = _rows(fn, dy, types=_BF16)
+    pdy, _, lddy = _rows(fn, dy, dev, types=_BF16)
     M, N = dy.shape
-    px, _, ldx = _rows(fn, x, M, types=_BF16)
+    px, _, ldx = _rows(fn, x, dev, M, types=_BF16)
     K = x.shape[1]
-    pw, _, ldw = _rows(fn, w, K, N, _BF16)
-    pz, _, ldz = _rows(fn, z, M, N, _BF16)
+    pw, _, ldw = _rows(fn, w, dev, K, N, _BF16)
+    pz, _, ldz = _rows(fn, z, dev, M, N, _BF16)
     if want_dx and dx is None:
         dx = _new_rows(M, K, torch.bfloat16, x, stream)
     if want_dw and dw is None:
@@ -809,11 +809,12 @@ def linear_bwd(dy, x, w, z=None, act="none", want_dx=True, want_dw=True, want_db
         dbias = _new((N,), torch.float32, x, stream)
     if ws is None and (dbias is not None or act != MOE_ACT_NONE):
         ws = _new((max(linear_bwd_workspace_size(M, N), 0),), torch.uint8, x, stream)
-    pdx, _, lddx = _rows(fn, dx, M, K, _BF16)
-    pdw, tdw, lddw = _rows(fn, dw, K, N)
-    nws = ws.numel() * ws.element_size() if ws is not None else 0
+    pdx, _, lddx = _rows(fn, dx, dev, M, K, _BF16)
+    pdw, tdw, lddw = _rows(fn, dw, dev, K, N)
+    nws = 0 if ws is None else ws.numel()
     _check(fn, lib.linear_bwd(pdy, lddy, px, ldx, pw, ldw, pz, ldz, act, M, N, K, pdx, lddx, pdw, tdw, lddw,
-                              _flat(fn, dbias, N, _F32), _p(ws), nws, _p(err), _handle(stream)))
+                              _flat(fn, dbias, dev, N, _F32), _flat(fn, ws, dev, nws, _U8), nws,
+                              _flat(fn, err, dev, 1, _I32), _handle(stream, dev)))
     return dx, dw, dbias
 
 
@@ -821,18 +822,19 @@ def gated_ffn_fwd(x, w1, act="silu", h=None, a=None, want_a=False, err=None, str
     """[gate | up] = x w1, h = act(gate) * up in one kernel (bf16).  See
     include/moe.h.  Returns h, or (h, a) when a = [gate | up] is asked for."""
     fn = "gated_ffn_fwd"
-    px, _, ldx = _rows(fn, x, types=_BF16)
+    dev = _device()
+    px, _, ldx = _rows(fn, x, dev, types=_BF16)
     M, d = x.shape
-    pw, _, ldw = _rows(fn, w1, d, types=_BF16)
+    pw, _, ldw = _rows(fn, w1, dev, d, types=_BF16)
     _need(fn, w1.shape[1] % 2 == 0)
     f = w1.shape[1] // 2
     h = h if h is not None else _new_rows(M, f, torch.bfloat16, x, stream)
     if want_a and a is None:
         a = _new_rows(M, 2 * f, torch.bfloat16, x, stream)
-    ph, _, ldh = _rows(fn, h, M, f, _BF16)
-    pa, _, lda = _rows(fn, a, M, 2 * f, _BF16)
-    _check(fn, lib.gated_ffn_fwd(px, ldx, pw, ldw, _act(fn, act), M, f, d, ph, ldh, pa, lda, _p(err),
-                                 _handle(stream)))
+    ph, _, ldh = _rows(fn, h, dev, M, f, _BF16)
+    pa, _, lda = _rows(fn, a, dev, M, 2 * f, _BF16)
+    _check(fn, lib.gated_ffn_fwd(px, ldx, pw, ldw, _act(fn, act), M, f, d, ph, ldh, pa, lda,
+                                 _flat(fn, err, dev, 1, _I32), _handle(stream, dev)))
     return h if a is None else (h, a)
 
 
@@ -842,22 +844,23 @@ def gated_ffn_bwd(dh, a, x, w1, act="silu", want_dx=True, want_dw=True, dx=None,
     float32); da [M, 2f] is written on the way (may be a itself).  See
     include/moe.h.  Returns (dx, dw1)."""
     fn = "gated_ffn_bwd"
-    pdh, _, lddh = _rows(fn, dh, types=_BF16)
+    dev = _device()
+    pdh, _, lddh = _rows(fn, dh, dev, types=_BF16)
     M, f = dh.shape
-    pa, _, lda = _rows(fn, a, M, 2 * f, _BF16)
-    px, _, ldx = _rows(fn, x, M, types=_BF16)
+    pa, _, lda = _rows(fn, a, dev, M, 2 * f, _BF16)
+    px, _, ldx = _rows(fn, x, dev, M, types=_BF16)
     d = x.shape[1]
-    pw, _, ldw = _rows(fn, w1, d, 2 * f, _BF16)
+    pw, _, ldw = _rows(fn, w1, dev, d, 2 * f, _BF16)
     da = da if da is not None else _new_rows(M, 2 * f, torch.bfloat16, x, stream)
     if want_dx and dx is None:
         dx = _new_rows(M, d, torch.bfloat16, x, stream)
     if want_dw and dw1 is None:
         dw1 = _new_rows(d, 2 * f, dw_dtype, x, stream)
-    pda, _, ldda = _rows(fn, da, M, 2 * f, _BF16)
-    pdx, _, lddx = _rows(fn, dx, M, d, _BF16)
-    pdw, tdw, lddw = _rows(fn, dw1, d, 2 * f)
+    pda, _, ldda = _rows(fn, da, dev, M, 2 * f, _BF16)
+    pdx, _, lddx = _rows(fn, dx, dev, M, d, _BF16)
+    pdw, tdw, lddw = _rows(fn, dw1, dev, d, 2 * f)
     _check(fn, lib.gated_ffn_bwd(pdh, lddh, pa, lda, px, ldx, pw, ldw, _act(fn, act), M, f, d, pda, ldda, pdx, lddx,
-                                 pdw, tdw, lddw, _p(err), _handle(stream)))
+                                 pdw, tdw, lddw, _flat(fn, err, dev, 1, _I32), _handle(stream, dev)))
     return dx, dw1
 
 
@@ -883,6 +886,7 @@ def adamw_plan(params, grads, ms, vs, m_scales=None, v_scales=None, copies=None,
     rng_base: first counter of each tensor's rounding (8 bits; multiples of
     256), by default one tensor after the other."""
     fn = "adamw_plan_encode"
+    dev = _device()
     n = len(params)
     _need(fn, n >= 1 and len(grads) == len(ms) == len(vs) == n)
     bits = 32 if ms[0].dtype == torch.float32 else 8
@@ -898,13 +902,13 @@ def adamw_plan(params, grads, ms, vs, m_scales=None, v_scales=None, copies=None,
     counter = 0
     for i in range(n):
         e, k = arr[i], params[i].numel()
-        e.p, e.g = _flat(fn, params[i], k, (pt,)), _flat(fn, grads[i], k, (gt,))
-        e.m, e.v = _flat(fn, ms[i], k, state), _flat(fn, vs[i], k, state)
+        e.p, e.g = _flat(fn, params[i], dev, k, {pt: 0}), _flat(fn, grads[i], dev, k, {gt: 0})
+        e.m, e.v = _flat(fn, ms[i], dev, k, state), _flat(fn, vs[i], dev, k, state)
         if bits == 8:
-            e.m_scale = _flat(fn, m_scales[i], (k + 255) // 256, _F32)
-            e.v_scale = _flat(fn, v_scales[i], (k + 255) // 256, _F32)
+            e.m_scale = _flat(fn, m_scales[i], dev, (k + 255) // 256, _F32)
+            e.v_scale = _flat(fn, v_scales[i], dev, (k + 255) // 256, _F32)
         if copies is not None:
-            e.copy = _flat(fn, copies[i], k, (torch.bfloat16,))
+            e.copy = _flat(fn, copies[i], dev, k, _BF16)
         e.n, e.weight_decay = k, wd[i]
         e.rng_base = counter if rng_base is None else int(rng_base[i])
         counter += (k + 255) // 256 * 256
@@ -927,11 +931,12 @@ def adamw_step(plan, lr, betas=(0.9, 0.999), eps=1e-8, step=1, grad_scale=None, 
     grad_scale: float32 device tensor, a factor of every gradient; when it is
     not finite the call changes nothing.  seed: of the 8-bit rounding."""
     fn = "adamw_step"
+    dev = _device()
     o = plan.opts
     o.beta1, o.beta2 = betas
     o.eps, o.seed = eps, seed & 0xFFFFFFFF
-    o.lr, o.lr_dev = (0.0, _flat(fn, lr, 1, _F32)) if isinstance(lr, torch.Tensor) else (lr, None)
-    o.step, o.step_dev = (0, _flat(fn, step, 1, _I32)) if isinstance(step, torch.Tensor) else (step, None)
-    o.grad_scale = _flat(fn, grad_scale, 1, _F32)
+    o.lr, o.lr_dev = (0.0, _flat(fn, lr, dev, 1, _F32)) if isinstance(lr, torch.Tensor) else (lr, None)
+    o.step, o.step_dev = (0, _flat(fn, step, dev, 1, _I32)) if isinstance(step, torch.Tensor) else (step, None)
+    o.grad_scale = _flat(fn, grad_scale, dev, 1, _F32)
     _check(fn, lib.adamw_step(plan.address, plan.tensors, plan.tiles, plan.p_type, plan.g_type, plan.state_bits,
-                              plan.opts_ref, _handle(stream)))
+                              plan.opts_ref, _handle(stream, dev)))
