@@ -305,6 +305,7 @@ __global__ void __launch_bounds__(kThreads, (Stage<PT, GT, BITS>::CTAS)) k_adamw
             --most;
         }
     };
+    wait_for_previous_kernels();
     if (threadIdx.x == 0) {
         float i1 = p.inv_bc1, i2 = p.inv_bc2;
         uint32_t key = p.key;
@@ -481,7 +482,7 @@ template <typename PT, typename GT, int BITS>
 static void launch(const Params& p, int sms, cudaStream_t s) {
     using S = Stage<PT, GT, BITS>;
     const int grid = (int)std::max<int64_t>(1, std::min<int64_t>(p.tiles, (int64_t)sms * (BITS == 32 ? 8 : S::CTAS)));
-    k_adamw<PT, GT, BITS><<<grid, kThreads, S::RING, s>>>(p);
+    (void)launch_early(dim3(grid), kThreads, S::RING, s, k_adamw<PT, GT, BITS>, p);
 }
 template <typename PT, typename GT>
 static void launch(int bits, const Params& p, int sms, cudaStream_t s) {

@@ -122,12 +122,40 @@ __device__ __forceinline__ int block_exclusive_scan(int v, int* s_warp, int* tot
     return warp_base + inc - v;
 }
 
+// Programmatic dependent launch: a kernel launched with the attribute may
+// start while the one before it in the stream ends, and sets up its barriers
+// and TMEM meanwhile.  Every thread waits here, before it touches memory that
+// is not its own, until the kernels before have completed and what they
+// wrote is visible; only then may the next kernel start its own set-up.
+__device__ __forceinline__ void wait_for_previous_kernels() {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
 }  // namespace moe
 
 // Host-side helpers (defined in api.cu).
 namespace moe {
 int device_sm_count();        // SM count of the current device (after moe_init)
 bool device_initialized();
+
+// Launches a kernel that calls wait_for_previous_kernels() with the early
+// start allowed.
+template <typename... Ts, typename... As>
+static inline cudaError_t launch_early(dim3 grid, int threads, size_t smem, cudaStream_t s, void (*kernel)(Ts...),
+                                       As... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, Ts(args)...);
+}
 }  // namespace moe
 
 #define MOE_CHECK_LAUNCH()                                   \

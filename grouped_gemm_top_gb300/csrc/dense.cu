@@ -129,16 +129,6 @@ __device__ __forceinline__ void prefetch_map(const CUtensorMap* m) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(m) : "memory");
 }
 
-// Programmatic dependent launch: a kernel launched with the attribute may
-// start while the one before it in the stream ends, and sets up its barriers
-// and TMEM meanwhile.  Every thread waits here, before it touches memory that
-// is not its own, until the kernels before have completed and what they
-// wrote is visible; only then may the next kernel start its own set-up.
-__device__ __forceinline__ void wait_for_previous_kernels() {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-}
-
 __device__ __forceinline__ void tc_mma2_bf16(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
                                              uint32_t accumulate) {
     asm volatile(
@@ -1027,20 +1017,6 @@ static cudaLaunchConfig_t launch_cfg(int clusters, int splits, cudaStream_t stre
     return cfg;
 }
 
-template <typename... Ts, typename... As>
-static cudaError_t launch_early(dim3 grid, int threads, cudaStream_t s, void (*kernel)(Ts...), As... args) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3(threads);
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, Ts(args)...);
-}
-
 // the products that are built: plain forward, input gradient and weight
 // gradient (bf16, fp32); forward with an epilogue, gated forward
 #define MOE_DENSE_INSTANCES(X)                                                                                       \
@@ -1293,7 +1269,7 @@ extern "C" moe_status_t linear_bwd(const void* dy, int64_t lddy, const void* x, 
         void (*const kernels[])(const __nv_bfloat16*, int64_t, const __nv_bfloat16*, int64_t, int64_t, int,
                                 __nv_bfloat16*, int64_t, float*) = {
             k_act_bwd<MOE_ACT_NONE>, k_act_bwd<MOE_ACT_RELU>, k_act_bwd<MOE_ACT_GELU>, k_act_bwd<MOE_ACT_SILU>};
-        if (launch_early(dim3((N + 255) / 256, act_parts(M)), 256, s, kernels[act],
+        if (launch_early(dim3((N + 255) / 256, act_parts(M)), 256, 0, s, kernels[act],
                          static_cast<const __nv_bfloat16*>(dy), lddy, static_cast<const __nv_bfloat16*>(z), ldz, M, N,
                          dz, lddz, part) != cudaSuccess)
             return MOE_ERR_CUDA;
@@ -1359,7 +1335,7 @@ extern "C" moe_status_t gated_ffn_bwd(const void* dh, int64_t lddh, const void* 
     cudaStream_t s = (cudaStream_t)stream;
     if (M > 0) {
         const int64_t n = M * (f / 8);
-        if (launch_early(dim3((unsigned)std::min<int64_t>((n + 255) / 256, (int64_t)sms * 8)), 256, s, k_glu_bwd,
+        if (launch_early(dim3((unsigned)std::min<int64_t>((n + 255) / 256, (int64_t)sms * 8)), 256, 0, s, k_glu_bwd,
                          static_cast<const __nv_bfloat16*>(dh), lddh, static_cast<const __nv_bfloat16*>(a), lda, M, f,
                          act, static_cast<__nv_bfloat16*>(da), ldda) != cudaSuccess)
             return MOE_ERR_CUDA;
