@@ -82,7 +82,9 @@ __device__ __forceinline__ void load8(const float* p, float* f) {
     const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
     f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
 }
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float* f) { unpack8(*reinterpret_cast<const uint4*>(p), f); }
+__device__ __forceinline__ void load8(const __nv_bfloat16* p, float* f) {
+    unpack8(*reinterpret_cast<const uint4*>(p), f);
+}
 __device__ __forceinline__ void store8(float* p, const float* f) {
     reinterpret_cast<float4*>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
     reinterpret_cast<float4*>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
@@ -120,7 +122,9 @@ struct F2 {
     __device__ __forceinline__ F2() {}
     __device__ __forceinline__ F2(float a, float b) { asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b)); }
     __device__ __forceinline__ explicit F2(float a) : F2(a, a) {}
-    __device__ __forceinline__ void get(float& a, float& b) const { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+    __device__ __forceinline__ void get(float& a, float& b) const {
+        asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+    }
 };
 __device__ __forceinline__ F2 mul2(F2 a, F2 b) {
     F2 r;
@@ -233,7 +237,8 @@ struct Stage {
     static constexpr int BYTES = OFF_VS + SC;
     // CTAs of an SM and stages of a CTA: about 192 KB on their way per SM
     static constexpr int CTAS = BITS == 32 ? 3 : 4;
-    static constexpr int STAGES = BITS == 32 ? 1 : (196608 / CTAS / BYTES >= 4 ? 4 : (196608 / CTAS / BYTES >= 3 ? 3 : 2));
+    static constexpr int FIT = 196608 / CTAS / BYTES;
+    static constexpr int STAGES = BITS == 32 ? 1 : (FIT >= 4 ? 4 : (FIT >= 3 ? 3 : 2));
     static constexpr int RING = BITS == 32 ? 0 : STAGES * BYTES;
 };
 
@@ -501,8 +506,9 @@ static cudaError_t set_one() {
 cudaError_t adamw_set_attributes() {
     using namespace adamw;
     using B = __nv_bfloat16;
-    const cudaError_t es[] = {set_one<float, float, 32>(), set_one<float, B, 32>(), set_one<B, float, 32>(), set_one<B, B, 32>(),
-                              set_one<float, float, 8>(),  set_one<float, B, 8>(),  set_one<B, float, 8>(),  set_one<B, B, 8>()};
+    const cudaError_t es[] = {set_one<float, float, 32>(), set_one<float, B, 32>(), set_one<B, float, 32>(),
+                              set_one<B, B, 32>(),         set_one<float, float, 8>(), set_one<float, B, 8>(),
+                              set_one<B, float, 8>(),      set_one<B, B, 8>()};
     for (cudaError_t e : es)
         if (e != cudaSuccess) return e;
     return cudaSuccess;

@@ -360,7 +360,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     const bool leader = rank == 0;
     const int first = blockIdx.x / (2 * p.splits), step = gridDim.x / (2 * p.splits);
     const int total = p.m_tiles * p.n_tiles;
-    const int k0 = p.nk / p.splits * part + min(part, p.nk % p.splits), k1 = k0 + p.nk / p.splits + (part < p.nk % p.splits);
+    const int k0 = p.nk / p.splits * part + min(part, p.nk % p.splits);
+    const int k1 = k0 + p.nk / p.splits + (part < p.nk % p.splits);
 
     const uint32_t bar0 = smem_u32(smem + OFF_BAR);
     auto full_bar = [&](int s) { return bar0 + 8u * s; };
@@ -554,9 +555,10 @@ __global__ void __launch_bounds__(THREADS, 1)
     if (p.splits > 1) {
         // ------------------------- one tile per cluster: swap and add up ----
         // A unit is what finish() takes (a chunk; GLU: a gate and an up
-        // chunk).  Part j owns units [j * own, (j + 1) * own).
+        // chunk).  Part j owns units [j * own, (j + 1) * own), those that exist.
         constexpr int CPU = EPI == EPI_GLU ? 2 : 1;      // chunks per unit
-        const int units = EPI == EPI_GLU ? p.bn / 64 : p.bn / 32, own = units / p.splits;
+        const int units = EPI == EPI_GLU ? p.bn / 64 : p.bn / 32, own = (units + p.splits - 1) / p.splits;
+        const int u0 = part * own, u1 = min(u0 + own, units);
         const uint32_t buf = smem_u32(smem);
         const int r = quarter * 32 + lane;
         bool ok = true;
@@ -575,7 +577,8 @@ __global__ void __launch_bounds__(THREADS, 1)
                 for (int c = 0; c < CPU; ++c) {
                     float v[32];
                     tmem_ld32(lane_base + (uint32_t)(32 * un + (c == 0 ? 0 : p.bn / 2)), v);
-                    const uint32_t at = buf + (uint32_t)(((slot * own + un - to * own) * CPU + c) * PART_BYTES + r * PART_ROW);
+                    const int chunk = (slot * own + un - to * own) * CPU + c;
+                    const uint32_t at = buf + (uint32_t)(chunk * PART_BYTES + r * PART_ROW);
                     const uint32_t dst = mapa(at, (uint32_t)(2 * to) + rank);
 #pragma unroll
                     for (int i = 0; i < 8; ++i) st_cluster_v4(dst + 16u * i, v + 4 * i);
@@ -590,7 +593,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             // boxes above the partial chunks: at most 3 of 2 KB (4 KB) a unit, four units a warp
             out.last = smem_u32(smem + SMEM_TILES - (ew + 1) * 8192);
             out.last_tile();
-            for (int un = part * own + half; un < (part + 1) * own; un += 2) {
+            for (int un = u0 + half; un < u1; un += 2) {
                 float s[2][32];
 #pragma unroll
                 for (int c = 0; c < CPU; ++c) {
@@ -606,7 +609,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                         }
                         const int slot = j < part ? j : j - 1;
                         const float4* q = reinterpret_cast<const float4*>(
-                            smem + ((slot * own + un - part * own) * CPU + c) * PART_BYTES + r * PART_ROW);
+                            smem + ((slot * own + un - u0) * CPU + c) * PART_BYTES + r * PART_ROW);
 #pragma unroll
                         for (int i = 0; i < 8; ++i) {
                             const float4 x = q[i];
@@ -618,7 +621,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 if (n > 0 && row0 < p.M)
                     finish<EPI, ACT>(p, &tmY, &tmZ, &tmZ2, out, row0, row0 + lane, col, n, s[0], s[1]);
             }
-            flush<EPI>(p, &tmY, &tmZ, &tmZ2, out, row0, col0, part * own + half, (part + 1) * own, 2);
+            flush<EPI>(p, &tmY, &tmZ, &tmZ2, out, row0, col0, u0 + half, u1, 2);
             if (lane == 0) bulk_wait_group0();
             __syncwarp();
         }
@@ -996,7 +999,7 @@ __global__ void __launch_bounds__(256) k_act_bwd(const __nv_bfloat16* __restrict
 
 // ----------------------------------------------------------------- host ----
 
-static int g_max_clusters[3] = {0, 0, 0};      // clusters of 2, 4, 8 CTAs that run at a time
+static int g_max_clusters[4] = {0, 0, 0, 0};      // clusters of 2, 4, 6, 8 CTAs that run at a time
 
 // attr: room for two (the cluster, and the early start described at
 // wait_for_previous_kernels)
@@ -1028,21 +1031,21 @@ static cudaLaunchConfig_t launch_cfg(int clusters, int splits, cudaStream_t stre
 static cudaError_t set_attributes() {
 #define X(A, B, E, ACT)                                                                                                \
     {                                                                                                               \
-        cudaError_t e = cudaFuncSetAttribute(k_dense_pair<A, B, E, ACT>, cudaFuncAttributeMaxDynamicSharedMemorySize,    \
-                                             SMEM_BYTES);                                                           \
+        const cudaError_t e = cudaFuncSetAttribute(k_dense_pair<A, B, E, ACT>,                                      \
+                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);        \
         if (e != cudaSuccess) return e;                                                                             \
     }
     MOE_DENSE_INSTANCES(X)
 #undef X
-    const cudaError_t es[] = {
-        cudaFuncSetAttribute(few::k_dense_few<true, EPI_LINEAR>, cudaFuncAttributeMaxDynamicSharedMemorySize, few::SMEM_BYTES),
-        cudaFuncSetAttribute(few::k_dense_few<true, EPI_GLU>, cudaFuncAttributeMaxDynamicSharedMemorySize, few::SMEM_BYTES),
-        cudaFuncSetAttribute(few::k_dense_few<false, EPI_LINEAR>, cudaFuncAttributeMaxDynamicSharedMemorySize, few::SMEM_BYTES)};
-    for (cudaError_t e : es)
+    const void* ks[] = {(const void*)few::k_dense_few<true, EPI_LINEAR>, (const void*)few::k_dense_few<true, EPI_GLU>,
+                        (const void*)few::k_dense_few<false, EPI_LINEAR>};
+    for (const void* k : ks) {
+        const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, few::SMEM_BYTES);
         if (e != cudaSuccess) return e;
-    for (int i = 0; i < 3; ++i) {
+    }
+    for (int i = 0; i < 4; ++i) {
         cudaLaunchAttribute attr[2];
-        cudaLaunchConfig_t cfg = launch_cfg(1024, 1 << i, nullptr, attr);
+        cudaLaunchConfig_t cfg = launch_cfg(1024, i + 1, nullptr, attr);
         const cudaError_t e = cudaOccupancyMaxActiveClusters(&g_max_clusters[i], k_dense_pair<false, true, EPI_PLAIN, 0>, &cfg);
         if (e != cudaSuccess) return e;
     }
@@ -1074,10 +1077,10 @@ static Choice choose(int64_t m_tiles, int N, int nk, bool glu) {
         if (glu && bn == 224) continue;      // gate and up in whole chunks of 32
         const int cols = glu ? bn / 2 : bn;
         const int64_t tiles = m_tiles * ((N + cols - 1) / cols);
-        for (int i = 0; i < 3; ++i) {
-            const int splits = 1 << i, units = glu ? bn / 64 : bn / 32;
-            if (splits > 1 && (units % splits != 0 || tiles > g_max_clusters[i] || nk < 4 * splits)) continue;
-            const int64_t waves = (tiles + g_max_clusters[i] - 1) / std::max(1, g_max_clusters[i]);
+        for (int splits = 1; splits <= 4; ++splits) {
+            const int slots = g_max_clusters[splits - 1];
+            if (splits > 1 && (tiles > slots || nk < 4 * splits)) continue;
+            const int64_t waves = (tiles + slots - 1) / slots;
             const double cost = (double)waves * ((nk + splits - 1) / splits * step_cost(bn) + kFixed * bn / 256.) +
                                 (splits > 1 ? kSwap : 0.);
             if (cost < best_cost) best_cost = cost, best = {bn, splits};
@@ -1169,8 +1172,10 @@ static bool act_ok(int a) { return a >= MOE_ACT_NONE && a <= MOE_ACT_SILU; }
 static bool size_ok(int64_t v) { return v >= 1 && v <= 0x7FFFFF00LL; }
 static bool row_ok(const void* p, int64_t ld) { return moe_aligned16(p) && ld % 8 == 0; }
 
-constexpr int kActRows = 256;      // rows of partial sums of k_act_bwd at most
-static int act_parts(int64_t M) { return (int)std::min<int64_t>((M + 31) / 32, kActRows); }
+// Rows of partial sums of k_act_bwd: one for up to 128 rows of dy (then it is
+// dbias itself, and the launch that adds up is saved: 2.3 us of the host's), one
+// for every 32 rows, 256 at most.
+static int act_parts(int64_t M) { return M <= 128 ? 1 : (int)std::min<int64_t>((M + 31) / 32, 256); }
 
 }  // namespace dense
 
@@ -1262,7 +1267,9 @@ extern "C" moe_status_t linear_bwd(const void* dy, int64_t lddy, const void* x, 
     cudaStream_t s = (cudaStream_t)stream;
     const void* g = dy;
     int64_t ldg = lddy;
-    float* part = need_ws && dbias ? reinterpret_cast<float*>(static_cast<char*>(ws) + dz_bytes(M, N)) : nullptr;
+    const bool one_part = M > 0 && act_parts(M) == 1;
+    float* part = nullptr;
+    if (need_ws && dbias) part = one_part ? dbias : reinterpret_cast<float*>(static_cast<char*>(ws) + dz_bytes(M, N));
     if (need_ws) {
         __nv_bfloat16* dz = static_cast<__nv_bfloat16*>(ws);
         const int64_t lddz = (N + 7) / 8 * 8;
@@ -1275,7 +1282,7 @@ extern "C" moe_status_t linear_bwd(const void* dy, int64_t lddy, const void* x, 
             return MOE_ERR_CUDA;
         if (with_z) g = dz, ldg = lddz;
     }
-    if (dbias) {
+    if (dbias && !one_part) {
         launch_column_sum(part, M > 0 ? act_parts(M) : 0, N, dbias, s);
         MOE_CHECK_LAUNCH();
     }
