@@ -35,7 +35,12 @@ namespace adamw {
 
 constexpr int kBlock = 256;                 // elements per 8-bit scale: one warp, 8 per lane
 constexpr int kThreads = 256;
-constexpr int kTile = kThreads * 8;         // elements per CTA and iteration
+constexpr int kSub = kThreads * 8;          // elements that a CTA works on at a time
+// Elements of a tile, the unit that CTAs take.  8-bit states of bf16 tensors
+// take two parts in one stage, with one barrier for both (344 against 358 us
+// for 130 M elements); with fp32 tensors, whose stages are larger, that costs
+// a CTA per SM (60 M elements, fp32 p and g: 169 against 155 us).
+constexpr int tile_of(int bits, int p_and_g_bytes) { return bits == 8 && p_and_g_bytes == 4 ? 2 * kSub : kSub; }
 constexpr int kMaxTensors = 1 << 20;
 
 // One tensor in the device table (moe_adamw_tensor_t plus what the kernel
@@ -71,10 +76,14 @@ struct Params {
     const float* grad_scale;
 };
 
-// 32 mixed bits of 32: two rounds of xor-shift and an odd multiplier.
-__host__ __device__ __forceinline__ uint32_t mix(uint32_t x) {
+// 32 mixed bits of 32: two rounds of xor-shift and an odd multiplier, and
+// the upper half folded onto the lower one.
+__host__ __device__ __forceinline__ uint32_t mix_unfolded(uint32_t x) {
     x = (x ^ (x >> 16)) * 0x9E3779B1u;
-    x = (x ^ (x >> 15)) * 0x85EBCA77u;
+    return (x ^ (x >> 15)) * 0x85EBCA77u;
+}
+__host__ __device__ __forceinline__ uint32_t mix(uint32_t x) {
+    x = mix_unfolded(x);
     return x ^ (x >> 16);
 }
 
@@ -231,13 +240,14 @@ __device__ __forceinline__ void block_scale(float top, float& scale, float& inv)
 // A tile's bytes in shared memory: p, g, m, v, and (8 bits) the 8 scales of each state.
 template <typename PT, typename GT, int BITS>
 struct Stage {
+    static constexpr int kTile = tile_of(BITS, (int)(sizeof(PT) + sizeof(GT)));
     static constexpr int P = kTile * (int)sizeof(PT), G = kTile * (int)sizeof(GT), S = kTile * (BITS == 32 ? 4 : 1);
     static constexpr int SC = BITS == 32 ? 0 : kTile / kBlock * 4;
     static constexpr int OFF_G = P, OFF_M = P + G, OFF_V = OFF_M + S, OFF_MS = OFF_V + S, OFF_VS = OFF_MS + SC;
     static constexpr int BYTES = OFF_VS + SC;
     // CTAs of an SM and stages of a CTA: about 192 KB on their way per SM
     static constexpr int CTAS = BITS == 32 ? 3 : 4;
-    static constexpr int FIT = 196608 / CTAS / BYTES;
+    static constexpr int FIT = 204800 / CTAS / BYTES;
     static constexpr int STAGES = BITS == 32 ? 1 : (FIT >= 4 ? 4 : (FIT >= 3 ? 3 : 2));
     static constexpr int RING = BITS == 32 ? 0 : STAGES * BYTES;
 };
@@ -260,9 +270,9 @@ struct Cursor {
     }
 };
 // Whole tiles of aligned tensors come through the ring of stages.
-template <int BITS>
+template <typename S>
 __device__ __forceinline__ bool in_ring(const Entry& e, int64_t tile) {
-    return BITS == 8 && e.vec == 2 && (tile + 1) * kTile <= e.n;
+    return S::RING > 0 && e.vec == 2 && (tile + 1) * S::kTile <= e.n;
 }
 
 // A CTA takes every G-th tile, so that many small tensors in a row are spread
@@ -275,7 +285,7 @@ __device__ __forceinline__ bool in_ring(const Entry& e, int64_t tile) {
 // rounding of the codes), which is what bounds it.  Loads into registers covered
 // less than half of the memory's latency at the occupancy those leave, so
 // bulk copies bring the next whole tiles into a ring in shared memory
-// while the CTA works on one (130 M elements, bf16 p and g: 366 us, 3.6 TB/s;
+// while the CTA works on one (130 M elements, bf16 p and g: 344 us, 3.8 TB/s;
 // 410 us without the ring).
 template <typename PT, typename GT, int BITS>
 __global__ void __launch_bounds__(kThreads, (Stage<PT, GT, BITS>::CTAS)) k_adamw(const Params p) {
@@ -295,7 +305,7 @@ __global__ void __launch_bounds__(kThreads, (Stage<PT, GT, BITS>::CTAS)) k_adamw
             const Entry& e = p.e[pc.k];
             const int64_t tile = pt - pc.first;
             pt += G;
-            if (!in_ring<BITS>(e, tile)) continue;
+            if (!in_ring<S>(e, tile)) continue;
             const uint32_t bar = gg::smem_u32(&s_bar[pstage]), dst = gg::smem_u32(s_ring + pstage * S::BYTES);
             gg::mbar_expect_tx(bar, S::BYTES);
             gg::bulk_load(dst, static_cast<const uint8_t*>(e.p) + tile * S::P, S::P, bar);
@@ -303,8 +313,8 @@ __global__ void __launch_bounds__(kThreads, (Stage<PT, GT, BITS>::CTAS)) k_adamw
             gg::bulk_load(dst + S::OFF_M, static_cast<const uint8_t*>(e.m) + tile * S::S, S::S, bar);
             gg::bulk_load(dst + S::OFF_V, static_cast<const uint8_t*>(e.v) + tile * S::S, S::S, bar);
             if (BITS == 8) {
-                gg::bulk_load(dst + S::OFF_MS, e.ms + tile * (kTile / kBlock), S::SC, bar);
-                gg::bulk_load(dst + S::OFF_VS, e.vs + tile * (kTile / kBlock), S::SC, bar);
+                gg::bulk_load(dst + S::OFF_MS, e.ms + tile * (S::kTile / kBlock), S::SC, bar);
+                gg::bulk_load(dst + S::OFF_VS, e.vs + tile * (S::kTile / kBlock), S::SC, bar);
             }
             if (++pstage == S::STAGES) pstage = 0;
             --most;
@@ -340,128 +350,148 @@ __global__ void __launch_bounds__(kThreads, (Stage<PT, GT, BITS>::CTAS)) k_adamw
     for (int64_t t = t0; t < t1 && !skip; t += G) {
         if (cur.seek(p, t)) e = p.e[cur.k];
         const int64_t tile = t - cur.first;
-        const int64_t at = tile * kTile + 8 * (int)threadIdx.x;
-        const int64_t left = e.n - at;
-        const int n = left >= 8 ? 8 : (left > 0 ? (int)left : 0);
-        const bool vec = e.vec != 0;
-        float g[8], w[8], m[8], v[8], u[8];
-        float sm = 0.f, sv = 0.f;
+        const bool ring = in_ring<S>(e, tile);
         bool ok = true;
-        if (in_ring<BITS>(e, tile)) {
-            const uint8_t* s = s_ring + stage * S::BYTES;
+        if (ring) {
             ok = false;
             for (int i = 0; i < (1 << 16) && !ok; ++i) ok = gg::mbar_try_wait(gg::smem_u32(&s_bar[stage]), phase);
-            const int o = 8 * (int)threadIdx.x;
-            load(reinterpret_cast<const PT*>(s) + o, 8, true, w);
-            load(reinterpret_cast<const GT*>(s + S::OFF_G) + o, 8, true, g);
-            if (BITS == 32) {
-                load(reinterpret_cast<const float*>(s + S::OFF_M) + o, 8, true, m);
-                load(reinterpret_cast<const float*>(s + S::OFF_V) + o, 8, true, v);
+        }
+#pragma unroll 1
+        for (int sub = 0; sub < S::kTile; sub += kSub) {
+            const int64_t at = tile * S::kTile + sub + 8 * (int)threadIdx.x;
+            const int64_t left = e.n - at;
+            const int n = left >= 8 ? 8 : (left > 0 ? (int)left : 0);
+            const bool vec = e.vec != 0;
+            float g[8], w[8], m[8], v[8], u[8];
+            float sm = 0.f, sv = 0.f;
+            if (ring) {
+                const uint8_t* s = s_ring + stage * S::BYTES;
+                const int o = sub + 8 * (int)threadIdx.x;
+                load(reinterpret_cast<const PT*>(s) + o, 8, true, w);
+                load(reinterpret_cast<const GT*>(s + S::OFF_G) + o, 8, true, g);
+                if (BITS == 32) {
+                    load(reinterpret_cast<const float*>(s + S::OFF_M) + o, 8, true, m);
+                    load(reinterpret_cast<const float*>(s + S::OFF_V) + o, 8, true, v);
+                } else {
+                    load_codes<true>(s + S::OFF_M + o, 8, true, m);
+                    load_codes<false>(s + S::OFF_V + o, 8, true, v);
+                    sm = reinterpret_cast<const float*>(s + S::OFF_MS)[o / kBlock];
+                    sv = reinterpret_cast<const float*>(s + S::OFF_VS)[o / kBlock];
+                }
+                if (sub == S::kTile - kSub) {
+                    __syncthreads();      // the stage is read
+                    if (threadIdx.x == 0) fetch(1);
+                    if (++stage == S::STAGES) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
             } else {
-                load_codes<true>(s + S::OFF_M + o, 8, true, m);
-                load_codes<false>(s + S::OFF_V + o, 8, true, v);
-                sm = reinterpret_cast<const float*>(s + S::OFF_MS)[threadIdx.x >> 5];
-                sv = reinterpret_cast<const float*>(s + S::OFF_VS)[threadIdx.x >> 5];
+                load(static_cast<const GT*>(e.g) + at, n, vec, g);
+                load(static_cast<PT*>(e.p) + at, n, vec, w);
+                if (BITS == 32) {
+                    load(static_cast<float*>(e.m) + at, n, vec, m);
+                    load(static_cast<float*>(e.v) + at, n, vec, v);
+                } else {
+                    load_codes<true>(static_cast<uint8_t*>(e.m) + at, n, vec, m);
+                    load_codes<false>(static_cast<uint8_t*>(e.v) + at, n, vec, v);
+                    // the warp's block: its first element exists or the whole warp is past the end
+                    const int64_t b = (at - 8 * (int)(threadIdx.x & 31)) / kBlock;
+                    if (b * kBlock < e.n) {
+                        sm = e.ms[b];
+                        sv = e.vs[b];
+                    }
+                }
             }
-            __syncthreads();      // the stage is read
-            if (threadIdx.x == 0) fetch(1);
-            if (++stage == S::STAGES) {
-                stage = 0;
-                phase ^= 1u;
+            if (BITS == 8) {
+                // code * 2^-120 * (2^120 * scale), rounded once; scales of 128 and
+                // more, whose product fp32 does not hold, in two steps
+                const float up = __uint_as_float((120u + 127u) << 23);
+                const bool one = sm < 128.f && sv < 128.f;
+                const F2 sm2(one ? sm * up : up), sv2(one ? sv * up : up);
+#pragma unroll
+                for (int i = 0; i < 8; i += 2) {
+                    mul2(F2(m[i], m[i + 1]), sm2).get(m[i], m[i + 1]);
+                    mul2(F2(v[i], v[i + 1]), sv2).get(v[i], v[i + 1]);
+                }
+                if (!one) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) m[i] *= sm, v[i] *= sv;
+                }
+#pragma unroll
+                for (int i = 0; i < 8; i += 2) mul2(F2(v[i], v[i + 1]), F2(v[i], v[i + 1])).get(v[i], v[i + 1]);
             }
-        } else {
-            load(static_cast<const GT*>(e.g) + at, n, vec, g);
-            load(static_cast<PT*>(e.p) + at, n, vec, w);
+            const F2 decay(1.f - lr * e.wd);
+#pragma unroll
+            for (int i = 0; i < 8; i += 2) {
+                const F2 g2 = mul2(F2(g[i], g[i + 1]), F2(gs));
+                const F2 m2 = add2(mul2(F2(p.b1), F2(m[i], m[i + 1])), mul2(F2(p.c1), g2));
+                const F2 v2 = add2(mul2(F2(p.b2), F2(v[i], v[i + 1])), mul2(mul2(F2(p.c2), g2), g2));
+                m2.get(m[i], m[i + 1]);
+                v2.get(v[i], v[i + 1]);
+                const F2 u2 = sqrt2(v2);
+                u2.get(u[i], u[i + 1]);
+                float d0, d1;
+                fma2(u2, F2(root2), F2(p.eps)).get(d0, d1);
+                const F2 q = mul2(mul2(m2, F2(-lr1)), F2(rcp_approx(d0), rcp_approx(d1)));
+                fma2(F2(w[i], w[i + 1]), decay, q).get(w[i], w[i + 1]);
+            }
+            if (!ok) {      // bytes that never came: the parameters say so
+#pragma unroll
+                for (int i = 0; i < 8; ++i) w[i] = __uint_as_float(0x7FC00000u);
+            }
+            store(static_cast<PT*>(e.p) + at, n, vec, w);
+            if (e.copy != nullptr) store(e.copy + at, n, vec, w);
             if (BITS == 32) {
-                load(static_cast<float*>(e.m) + at, n, vec, m);
-                load(static_cast<float*>(e.v) + at, n, vec, v);
+                store(static_cast<float*>(e.m) + at, n, vec, m);
+                store(static_cast<float*>(e.v) + at, n, vec, v);
             } else {
-                load_codes<true>(static_cast<uint8_t*>(e.m) + at, n, vec, m);
-                load_codes<false>(static_cast<uint8_t*>(e.v) + at, n, vec, v);
-                // the warp's block: its first element exists or the whole warp is past the end
                 const int64_t b = (at - 8 * (int)(threadIdx.x & 31)) / kBlock;
-                if (b * kBlock < e.n) {
-                    sm = e.ms[b];
-                    sv = e.vs[b];
+                if (n < 8) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        m[i] = i < n ? m[i] : 0.f;
+                        u[i] = i < n ? u[i] : 0.f;
+                    }
                 }
-            }
-        }
-        if (BITS == 8) {
-            const F2 sm2(sm), sv2(sv), up(__uint_as_float((120u + 127u) << 23));
+                float im, su, iu;
+                block_scale(block_top(m), sm, im);
+                block_scale(block_top(u), su, iu);
+                const uint64_t c = (uint64_t)(e.rng + at);     // blocks start at multiples of 256 of the counter
+                const uint32_t lo = (uint32_t)c + mix((uint32_t)(c >> 32) ^ key);
+                const F2 down(__uint_as_float((127u - 120u) << 23));
+                uint32_t cm[8], cu[8];
 #pragma unroll
-            for (int i = 0; i < 8; i += 2) {
-                mul2(mul2(F2(m[i], m[i + 1]), up), sm2).get(m[i], m[i + 1]);
-                const F2 r = mul2(mul2(F2(v[i], v[i + 1]), up), sv2);
-                mul2(r, r).get(v[i], v[i + 1]);
-            }
-        }
-        const F2 decay(1.f - lr * e.wd);
+                for (int i = 0; i < 8; i += 2) {
+                    mul2(mul2(F2(m[i], m[i + 1]), F2(im)), down).get(m[i], m[i + 1]);
+                    float x[2];
+                    mul2(mul2(F2(u[i], u[i + 1]), F2(iu)), down).get(x[0], x[1]);
 #pragma unroll
-        for (int i = 0; i < 8; i += 2) {
-            const F2 g2 = mul2(F2(g[i], g[i + 1]), F2(gs));
-            const F2 m2 = add2(mul2(F2(p.b1), F2(m[i], m[i + 1])), mul2(F2(p.c1), g2));
-            const F2 v2 = add2(mul2(F2(p.b2), F2(v[i], v[i + 1])), mul2(mul2(F2(p.c2), g2), g2));
-            m2.get(m[i], m[i + 1]);
-            v2.get(v[i], v[i + 1]);
-            const F2 u2 = sqrt2(v2);
-            u2.get(u[i], u[i + 1]);
-            float d0, d1;
-            fma2(u2, F2(root2), F2(p.eps)).get(d0, d1);
-            const F2 q = mul2(mul2(m2, F2(-lr1)), F2(rcp_approx(d0), rcp_approx(d1)));
-            fma2(F2(w[i], w[i + 1]), decay, q).get(w[i], w[i + 1]);
-        }
-        if (!ok) {      // bytes that never came: the parameters say so
-#pragma unroll
-            for (int i = 0; i < 8; ++i) w[i] = __uint_as_float(0x7FC00000u);
-        }
-        store(static_cast<PT*>(e.p) + at, n, vec, w);
-        if (e.copy != nullptr) store(e.copy + at, n, vec, w);
-        if (BITS == 32) {
-            store(static_cast<float*>(e.m) + at, n, vec, m);
-            store(static_cast<float*>(e.v) + at, n, vec, v);
-        } else {
-            const int64_t b = (at - 8 * (int)(threadIdx.x & 31)) / kBlock;
-            if (n < 8) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    m[i] = i < n ? m[i] : 0.f;
-                    u[i] = i < n ? u[i] : 0.f;
+                    for (int j = i; j < i + 2; ++j) {
+                        const uint32_t bits = mix_unfolded(lo + (uint32_t)j);
+                        // the low 16 bits of bits ^ bits >> 16, and the high ones, in bits 8..23
+                        cm[j] = e4m3_code(m[j], __byte_perm(bits ^ (bits >> 16), 0u, 0x4104));
+                        // not zero: never rounded to zero
+                        cu[j] = max(e4m3_code(x[j - i], __byte_perm(bits, 0u, 0x4324)),
+                                    min(__float_as_uint(u[j]), 1u) << 24);
+                    }
                 }
-            }
-            float im, su, iu;
-            block_scale(block_top(m), sm, im);
-            block_scale(block_top(u), su, iu);
-            const uint64_t c = (uint64_t)(e.rng + at);     // blocks start at multiples of 256 of the counter
-            const uint32_t lo = (uint32_t)c + mix((uint32_t)(c >> 32) ^ key);
-            const F2 down(__uint_as_float((127u - 120u) << 23));
-            uint32_t cm[8], cu[8];
+                uint32_t wm[2], wu[2];
 #pragma unroll
-            for (int i = 0; i < 8; i += 2) {
-                mul2(mul2(F2(m[i], m[i + 1]), F2(im)), down).get(m[i], m[i + 1]);
-                mul2(mul2(F2(u[i], u[i + 1]), F2(iu)), down).get(u[i], u[i + 1]);
+                for (int j = 0; j < 2; ++j) {
+                    uint32_t sign[4];
 #pragma unroll
-                for (int j = i; j < i + 2; ++j) {
-                    const uint32_t bits = mix(lo + (uint32_t)j);
-                    cm[j] = e4m3_code(m[j], (bits << 8) & 0xFFFF00u);
-                    // not zero: never rounded to zero
-                    cu[j] = max(e4m3_code(u[j], (bits >> 8) & 0xFFFF00u), min(__float_as_uint(u[j]), 1u) << 24);
+                    for (int i = 0; i < 4; ++i) sign[i] = __float_as_uint(m[4 * j + i]);
+                    wm[j] = top_bytes(cm[4 * j], cm[4 * j + 1], cm[4 * j + 2], cm[4 * j + 3]) |
+                            (top_bytes(sign[0], sign[1], sign[2], sign[3]) & 0x80808080u);
+                    wu[j] = top_bytes(cu[4 * j], cu[4 * j + 1], cu[4 * j + 2], cu[4 * j + 3]);
                 }
-            }
-            uint32_t wm[2], wu[2];
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                uint32_t sign[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) sign[i] = __float_as_uint(m[4 * j + i]);
-                wm[j] = top_bytes(cm[4 * j], cm[4 * j + 1], cm[4 * j + 2], cm[4 * j + 3]) |
-                        (top_bytes(sign[0], sign[1], sign[2], sign[3]) & 0x80808080u);
-                wu[j] = top_bytes(cu[4 * j], cu[4 * j + 1], cu[4 * j + 2], cu[4 * j + 3]);
-            }
-            store_codes(static_cast<uint8_t*>(e.m) + at, n, vec, wm);
-            store_codes(static_cast<uint8_t*>(e.v) + at, n, vec, wu);
-            if ((threadIdx.x & 31) == 0 && n > 0) {
-                e.ms[b] = sm;
-                e.vs[b] = su;
+                store_codes(static_cast<uint8_t*>(e.m) + at, n, vec, wm);
+                store_codes(static_cast<uint8_t*>(e.v) + at, n, vec, wu);
+                if ((threadIdx.x & 31) == 0 && n > 0) {
+                    e.ms[b] = sm;
+                    e.vs[b] = su;
+                }
             }
         }
     }
@@ -534,6 +564,7 @@ extern "C" moe_status_t adamw_plan_encode(const moe_adamw_tensor_t* t, int tenso
     int64_t* tile0 = reinterpret_cast<int64_t*>(base + tile_table_at(tensors));
     int64_t at = 0;
     const size_t sb = state_bits == 32 ? 4 : 1;
+    const int tile = tile_of(state_bits, esize(p_type) + esize(g_type));
     for (int i = 0; i < tensors; ++i) {
         const moe_adamw_tensor_t& a = t[i];
         MOE_REQUIRE(a.n >= 0 && a.n <= (1LL << 40), MOE_ERR_INVALID_ARG);
@@ -553,7 +584,7 @@ extern "C" moe_status_t adamw_plan_encode(const moe_adamw_tensor_t* t, int tenso
                 al(a.v, state_bits == 32 ? 16 : 8) && al(a.copy, 16);
         if (o.vec && al(a.m, 16) && al(a.v, 16) && al(a.m_scale, 16) && al(a.v_scale, 16)) o.vec = 2;
         tile0[i] = at;
-        at += (a.n + kTile - 1) / kTile;
+        at += (a.n + tile - 1) / tile;
     }
     tile0[tensors] = at;
     *tiles = at;

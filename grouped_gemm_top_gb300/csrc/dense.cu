@@ -658,7 +658,7 @@ constexpr int MAX_STAGES = 5;
 constexpr int OFF_BAR = SMEM_TILES;             // full[S], empty[S], done
 constexpr int OFF_MISC = OFF_BAR + 8 * (2 * MAX_STAGES + 1);
 constexpr int SMEM_BYTES = OFF_MISC + 16 + 1024;
-constexpr int THREADS = 128;
+constexpr int THREADS = 256;                    // warps 0 and 1 load and multiply, all of them join the parts
 
 struct Split {
     int rows;          // rows of x per tile, padded to 16
@@ -704,6 +704,82 @@ __device__ __forceinline__ void store4(__nv_bfloat16* p, int n, const float* f) 
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             if (i < n) p[i] = __float2bfloat16_rn(f[i]);
+    }
+}
+
+// 4 columns a lane of a row of the tile, from the product to memory (GLU:
+// lanes 0..15 hold gate columns, lanes 16..31 the up columns of the same h).
+template <int EPI>
+__device__ __forceinline__ void finish_row(const Params& p, int64_t row, int nt, int lane, float* v) {
+    if constexpr (EPI == EPI_GLU) {
+        float u[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) u[i] = __shfl_down_sync(0xFFFFFFFFu, v[i], 16);
+        const int col = nt * 64 + lane * 4, n = p.N - col;
+        if (lane < 16 && n > 0) {
+            if (p.z != nullptr) {
+                store4(p.z + row * p.ldz + col, n, v);
+                store4(p.z + row * p.ldz + p.N + col, n, u);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) u[i] *= act_of(v[i], p.act);
+            store4(static_cast<__nv_bfloat16*>(p.y) + row * p.ldy + col, n, u);
+        }
+    } else {
+        const int col = nt * 128 + lane * 4, n = p.N - col;
+        if (n <= 0) return;
+        if (p.bias != nullptr) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] += i < n ? __bfloat162float(p.bias[col + i]) : 0.f;
+        }
+        if (p.z != nullptr) store4(p.z + row * p.ldz + col, n, v);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = act_of(v[i], p.act);
+        if (p.res != nullptr) {
+            float q[4];
+            load4(p.res + row * p.ldres + col, n, q);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] += q[i];
+        }
+        store4(static_cast<__nv_bfloat16*>(p.y) + row * p.ldy + col, n, v);
+    }
+}
+
+// Rows rank, rank + splits, ... of the tile from the parts' partial tiles
+// ([rows][128] fp32 at `part` of each CTA): a warp takes a row, 4 columns a
+// lane.  ROWS rows and PARTS parts of each are on their way at a time; one
+// after the other, 128 rows were joined at the latency of distributed shared memory.
+template <int EPI, int ROWS, int PARTS>
+__device__ __forceinline__ void join(const Params& p, const Split& s, uint32_t part, uint32_t rank, int64_t m0, int m,
+                                     int nt) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int stride = s.splits * (THREADS / 32);
+    for (int r0 = (int)rank + s.splits * warp; r0 < m; r0 += stride * ROWS) {
+        float v[ROWS][4];
+#pragma unroll
+        for (int j = 0; j < ROWS; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[j][i] = 0.f;
+        for (int c0 = 0; c0 < s.splits; c0 += PARTS) {      // splits is a multiple of PARTS
+            float q[ROWS][PARTS][4];
+#pragma unroll
+            for (int j = 0; j < ROWS; ++j) {
+                const int r = r0 + j * stride;
+                if (r >= m) continue;
+#pragma unroll
+                for (int c = 0; c < PARTS; ++c)
+                    ld_cluster_v4(mapa(part + (uint32_t)(r * 128 + lane * 4) * 4u, (uint32_t)(c0 + c)), q[j][c]);
+            }
+#pragma unroll
+            for (int j = 0; j < ROWS; ++j)
+#pragma unroll
+                for (int c = 0; c < PARTS; ++c)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) v[j][i] += q[j][c][i];      // (rows past the end: not used)
+        }
+#pragma unroll
+        for (int j = 0; j < ROWS; ++j)
+            if (r0 + j * stride < m) finish_row<EPI>(p, m0 + r0 + j * stride, nt, lane, v[j]);      // the whole warp
     }
 }
 
@@ -820,68 +896,22 @@ __global__ void __launch_bounds__(THREADS, 2)
     tc_fence_after();
     float* part = reinterpret_cast<float*>(smem);          // [rows of x][128]
     if (ready) {
-        for (int c = 0; c < m; c += 16) {
+        // a warp reads its lane quarter, the upper four warps every second 16 rows
+        const int quarter = warp & 3;
+        for (int c = 16 * (warp >> 2); c < m; c += 32) {
             float v[16];
-            tmem_ld16(tmem + ((uint32_t)(warp * 32) << 16) + (uint32_t)c, v);
+            tmem_ld16(tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)c, v);
 #pragma unroll
             for (int i = 0; i < 16; ++i)
-                if (c + i < m) part[(c + i) * 128 + warp * 32 + lane] = v[i];
+                if (c + i < m) part[(c + i) * 128 + quarter * 32 + lane] = v[i];
         }
     }
     tc_fence_before();
     if (s.splits > 1) cluster_sync();
     else __syncthreads();
-    // rows rank, rank + splits, ... of the tile: 32 threads take a row, 4 columns each
-    const uint32_t part_addr = smem_u32(part);
-    for (int r = (int)rank + s.splits * warp; r < m; r += s.splits * (THREADS / 32)) {
-        float v[4] = {0.f, 0.f, 0.f, 0.f};
-        const uint32_t at = part_addr + (uint32_t)(r * 128 + lane * 4) * 4u;
-        if (s.splits == 1) {
-            const float4 q = *reinterpret_cast<const float4*>(part + r * 128 + lane * 4);
-            v[0] = q.x, v[1] = q.y, v[2] = q.z, v[3] = q.w;
-        } else {
-            for (int c = 0; c < s.splits; ++c) {
-                float q[4];
-                ld_cluster_v4(mapa(at, (uint32_t)c), q);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) v[i] += q[i];
-            }
-        }
-        const int64_t row = m0 + r;
-        if constexpr (EPI == EPI_GLU) {
-            float u[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) u[i] = __shfl_down_sync(0xFFFFFFFFu, v[i], 16);      // lanes 16..31 hold up
-            const int col = nt * 64 + lane * 4, n = p.N - col;
-            if (lane < 16 && n > 0) {
-                if (p.z != nullptr) {
-                    store4(p.z + row * p.ldz + col, n, v);
-                    store4(p.z + row * p.ldz + p.N + col, n, u);
-                }
-#pragma unroll
-                for (int i = 0; i < 4; ++i) u[i] *= act_of(v[i], p.act);
-                store4(static_cast<__nv_bfloat16*>(p.y) + row * p.ldy + col, n, u);
-            }
-        } else {
-            const int col = nt * 128 + lane * 4, n = p.N - col;
-            if (n > 0) {
-                if (p.bias != nullptr) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) v[i] += i < n ? __bfloat162float(p.bias[col + i]) : 0.f;
-                }
-                if (p.z != nullptr) store4(p.z + row * p.ldz + col, n, v);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) v[i] = act_of(v[i], p.act);
-                if (p.res != nullptr) {
-                    float q[4];
-                    load4(p.res + row * p.ldres + col, n, q);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) v[i] += q[i];
-                }
-                store4(static_cast<__nv_bfloat16*>(p.y) + row * p.ldy + col, n, v);
-            }
-        }
-    }
+    if (s.splits == 1) join<EPI, 8, 1>(p, s, smem_u32(part), rank, m0, m, nt);
+    else if (s.splits == 2) join<EPI, 4, 2>(p, s, smem_u32(part), rank, m0, m, nt);
+    else join<EPI, 2, 4>(p, s, smem_u32(part), rank, m0, m, nt);
     if (s.splits > 1) cluster_sync();      // nobody leaves while its partial tile is read
     else __syncthreads();
     if (warp == 1) {

@@ -837,7 +837,9 @@ typedef enum { MOE_TYPE_BF16 = 0, MOE_TYPE_F32 = 1 } moe_type_t;
  *        [M, N], scales [M, N / 32].  codes 16-byte aligned.
  * The sum, the norm and y are fp32 until stored: the norm is that of the
  * unrounded sum, and the codes are those of the unrounded y (the scale rule
- * above, applied to fp32 values).  M = 0 does nothing.
+ * above, applied to fp32 values).  M = 0 does nothing.  (These calls and
+ * adamw_step have no error word: should a bounded wait inside a kernel give
+ * up, the rows or parameters concerned become NaN.)
  */
 MOE_API moe_status_t rmsnorm_residual_fwd(const void* x, int x_type, int64_t ldx, const void* res, int res_type,
                                           int64_t ldres, const void* w, int w_type, float eps, int64_t M, int N,

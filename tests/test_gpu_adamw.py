@@ -148,7 +148,7 @@ def test_8_bit_rounding_keeps_the_mean_and_v_moves(ops):
 def test_8_bit_second_moment_is_never_rounded_to_zero(ops):
     n = 512
     g = torch.zeros((n,), device="cuda")
-    g[0], g[1:256], g[256:] = 1.0, 1e-9, 0.0
+    g[0], g[1:128], g[128:256], g[256:] = 1.0, 1e-9, 1e-15, 0.0
     m, v = (torch.zeros((n,), dtype=torch.uint8, device="cuda") for _ in range(2))
     ms, vs = torch.zeros((2,), device="cuda"), torch.zeros((2,), device="cuda")
     p = torch.zeros((n,), device="cuda")
