@@ -1,4 +1,6 @@
-"""Build libmoe.so (the C-ABI library) in-tree with nvcc for sm_103a.
+"""Build libmoe.so (the C-ABI library) in-tree with nvcc for sm_103a, and
+_marshal.so, the compiled argument marshalling of the dense operators' Python
+entry points, with the host compiler.
 
 Each .cu file under csrc/ is compiled in parallel to an object file under
 _build/, then linked into grouped_gemm_top_gb300/libmoe.so.  Objects are
@@ -12,6 +14,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -19,6 +22,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmoe.so")
+MARSHAL = os.path.join(PKG, "_marshal.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVFLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
@@ -76,7 +80,23 @@ def build(verbose: bool = False, ptxas_verbose: bool = False, force: bool = Fals
         if r.returncode != 0:
             raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
         os.replace(tmp, LIB)
+    _build_marshal(force)
     return LIB
+
+
+def _build_marshal(force):
+    """csrc/marshal.c against Python's headers and libmoe.so beside it."""
+    src = os.path.join(CSRC, "marshal.c")
+    newest = max(os.path.getmtime(src), _deps_mtime())
+    if not force and os.path.exists(MARSHAL) and os.path.getmtime(MARSHAL) >= newest:
+        return
+    tmp = MARSHAL + ".tmp"
+    cmd = [shutil.which("gcc") or shutil.which("cc") or "gcc", "-O2", "-Wall", "-shared", "-fPIC", "-I", INCLUDE, "-I",
+           sysconfig.get_paths()["include"], src, "-o", tmp, "-L", PKG, "-l:libmoe.so", "-Wl,-rpath,$ORIGIN"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"building _marshal.so failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, MARSHAL)
 
 
 if __name__ == "__main__":

@@ -2,8 +2,8 @@
 
 Argument marshalling only -- every step runs in the library's CUDA kernels.
 Torch is used for device memory and the current stream.  If the shared
-library is missing the import of this module fails loudly; there is no
-fallback path.
+library (or _marshal.so, the dense operators' compiled marshalling) is missing
+the import of this module fails loudly; there is no fallback path.
 """
 from __future__ import annotations
 
@@ -178,6 +178,7 @@ def _load():
 
 
 lib = _load()
+from . import _marshal  # noqa: E402  (links libmoe.so, loaded above)
 
 
 def status_string(status: int) -> str:
@@ -611,22 +612,17 @@ def moe_selftest_bounded_wait(timeout_ns, err, completed, stream=None):
 
 
 
-# --------------------------------------------- dense operators (norm, AdamW) --
+# ------------------------------------------------------ dense operators ----
 # These take any strided rows (unit stride inside a row) on the current
 # device; a tensor that does not fit the call is refused with
-# MOE_ERR_INVALID_ARG before anything is launched.
+# MOE_ERR_INVALID_ARG before anything is launched.  They also serve steps of a
+# few microseconds, so tensors are read and checked in compiled code
+# (csrc/marshal.c); what is left here is defaults and allocation.
 
-# These calls also serve steps of a few microseconds: the current device and
-# stream come from torch's own C entry points, without the Python objects
-# around them.
-
-_BF16 = {torch.bfloat16: MOE_TYPE_BF16}
-_F32 = {torch.float32: MOE_TYPE_F32}
-_TYPES = {**_BF16, **_F32}
-_I32, _U8 = {torch.int32: 0}, {torch.uint8: 0}
-_E4M3 = {torch.uint8: 0, torch.float8_e4m3fn: 0}
-_device = torch._C._cuda_getDevice
-_raw_stream = torch._C._cuda_getCurrentRawStream
+_TYPES = {torch.bfloat16: MOE_TYPE_BF16, torch.float32: MOE_TYPE_F32}
+_ACTS = {"none": MOE_ACT_NONE, "relu": MOE_ACT_RELU, "gelu": MOE_ACT_GELU, "silu": MOE_ACT_SILU}
+_marshal.setup(torch.bfloat16, torch.float32, torch.uint8, torch.float8_e4m3fn, torch.int32,
+               torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream)
 
 
 def _need(fn, ok):
@@ -634,36 +630,10 @@ def _need(fn, ok):
         raise MoEError(fn, MOE_ERR_INVALID_ARG)
 
 
-def _rows(fn, t, dev, m=None, n=None, types=_TYPES):
-    """(pointer, type code, row stride) of a [m, n] matrix on device `dev`;
-    (None, 0, 0) for None."""
-    if t is None:
-        return None, 0, 0
-    shape, code = t.shape, types.get(t.dtype)
-    # (a tensor in host memory has device -1)
-    if code is None or len(shape) != 2 or t.get_device() != dev:
-        raise MoEError(fn, MOE_ERR_INVALID_ARG)
-    rows, cols = shape
-    ld, step = t.stride()
-    if ld < cols and rows <= 1:
-        ld = cols
-    if ld < cols or (step != 1 and cols != 1) or (m is not None and rows != m) or (n is not None and cols != n):
-        raise MoEError(fn, MOE_ERR_INVALID_ARG)
-    return t.data_ptr(), code, ld
-
-
-def _flat(fn, t, dev, n, types):
-    """Pointer of a contiguous tensor of n elements on device `dev`."""
-    if t is None:
-        return None
-    if t.dtype not in types or t.numel() != n or t.get_device() != dev or not t.is_contiguous():
-        raise MoEError(fn, MOE_ERR_INVALID_ARG)
-    return t.data_ptr()
-
-
-def _handle(stream, dev):
-    """The stream's handle; of the current stream for None."""
-    return _raw_stream(dev) if stream is None else stream.cuda_stream
+def _act(fn, act):
+    a = _ACTS.get(act, act)
+    _need(fn, isinstance(a, int))
+    return a
 
 
 def _new(shape, dtype, like, stream):
@@ -674,43 +644,43 @@ def _new(shape, dtype, like, stream):
         return torch.empty(shape, dtype=dtype, device=like.device)
 
 
+def _new_rows(fn, m, n, dtype, like, stream):
+    """An uninitialised [m, n] whose rows start at multiples of 16 bytes."""
+    t = _new((m, (n + 7) // 8 * 8), dtype, like, stream)
+    return t if n % 8 == 0 else t[:, :n]
+
+
+def _size(fn, *matrices):
+    """(rows, columns) of the first one; all have to be matrices."""
+    for t in matrices:
+        _need(fn, isinstance(t, torch.Tensor) and t.dim() == 2)
+    return matrices[0].shape
+
+
 def rmsnorm_residual_fwd(x, w, residual=None, eps=1e-6, y=None, r=None, rstd=None, codes=None, scales=None,
                          want_y=True, want_r=True, want_codes=False, sf_layout=MOE_SF_ATOMS, y_dtype=torch.bfloat16,
                          stream=None):
     """r = x + residual, y = r / sqrt(mean r^2 + eps) * w, and y's MXFP8
     codes and scales.  See include/moe.h.  Outputs that are wanted and not
-    given are allocated; r is only written when there is a residual.
+    given are allocated; r is only written when there is a residual, or given.
     Returns (y, r, rstd, codes, scales), None for what is not produced."""
     fn = "rmsnorm_residual_fwd"
-    dev = _device()
-    px, tx, ldx = _rows(fn, x, dev)
-    M, N = x.shape
-    pres, tres, ldres = _rows(fn, residual, dev, M, N)
-    if residual is None:
-        tres = tx if r is None else _TYPES.get(r.dtype, -1)
-    elif r is None and want_r:
-        r = _new((M, N), residual.dtype, x, stream)
-    pw = _flat(fn, w, dev, N, _TYPES)
-    if y is None and want_y:
-        y = _new((M, N), y_dtype, x, stream)
-    if rstd is None:
-        rstd = _new((M,), torch.float32, x, stream)
-    if want_codes and codes is None:
-        rows = (M + 127) // 128 * 128 if sf_layout == MOE_SF_ATOMS else M
-        codes = _new((rows, N), torch.uint8, x, stream)
-        scales = _new((rows * (N // 32),), torch.uint8, x, stream) if scales is None else scales
-    pr, tr, ldr = _rows(fn, r, dev, M, N)
-    _need(fn, r is None or tr == tres)
-    py, ty, ldy = _rows(fn, y, dev, M, N)
-    pc = ps = None
-    if codes is not None or scales is not None:
-        rows = (M + 127) // 128 * 128 if sf_layout == MOE_SF_ATOMS else M
-        _need(fn, codes is not None and scales is not None)
-        pc = _flat(fn, codes, dev, rows * N, _E4M3)
-        ps = _flat(fn, scales, dev, rows * (N // 32), _U8)
-    _check(fn, lib.rmsnorm_residual_fwd(px, tx, ldx, pres, tres, ldres, pw, _TYPES[w.dtype], eps, M, N, pr, ldr, py,
-                                        ty, ldy, _flat(fn, rstd, dev, M, _F32), pc, ps, int(sf_layout),
-                                        _handle(stream, dev)))
+    if rstd is None or (y is None and want_y) or (want_codes and codes is None) or (
+            r is None and want_r and residual is not None):
+        M, N = _size(fn, x)
+        if rstd is None:
+            rstd = _new((M,), torch.float32, x, stream)
+        if y is None and want_y:
+            y = _new((M, N), y_dtype, x, stream)
+        if r is None and want_r and residual is not None:
+            r = _new((M, N), residual.dtype, x, stream)
+        if want_codes and codes is None:
+            rows = (M + 127) // 128 * 128 if sf_layout == MOE_SF_ATOMS else M
+            codes = _new((rows, N), torch.uint8, x, stream)
+            scales = _new((rows * (N // 32),), torch.uint8, x, stream) if scales is None else scales
+    st = _marshal.rmsnorm_residual_fwd(x, w, residual, eps, y, r, rstd, codes, scales, sf_layout, stream)
+    if st:
+        raise MoEError(fn, st)
     return y, r, rstd, codes, scales
 
 
@@ -723,62 +693,32 @@ def rmsnorm_residual_bwd(dy, r, w, rstd, dres=None, want_dw=True, dx=None, dw=No
     """Gradients of rmsnorm_residual_fwd: dx (of x and of the residual; + dres)
     and dw (fp32).  See include/moe.h.  Returns (dx, dw)."""
     fn = "rmsnorm_residual_bwd"
-    dev = _device()
-    pr, tr, ldr = _rows(fn, r, dev)
-    M, N = r.shape
-    pdy, tdy, lddy = _rows(fn, dy, dev, M, N)
-    pdr, tdr, lddr = _rows(fn, dres, dev, M, N)
-    _need(fn, dres is None or tdr == tr)
-    _need(fn, w.dtype in _TYPES)
-    if dx is None:
-        dx = _new((M, N), r.dtype, r, stream)
-    if want_dw and dw is None:
-        dw = _new((N,), torch.float32, r, stream)
-    if dw is not None and ws is None:
-        ws = _new((max(rmsnorm_bwd_workspace_size(M, N), 0),), torch.uint8, r, stream)
-    pdx, tdx, lddx = _rows(fn, dx, dev, M, N)
-    _need(fn, tdx == tr)
-    nws = 0 if ws is None else ws.numel()
-    _check(fn, lib.rmsnorm_residual_bwd(pdy, tdy, lddy, pr, tr, ldr, _flat(fn, w, dev, N, _TYPES), _TYPES[w.dtype],
-                                        _flat(fn, rstd, dev, M, _F32), pdr, lddr, M, N, pdx, lddx,
-                                        _flat(fn, dw, dev, N, _F32), _flat(fn, ws, dev, nws, _U8), nws,
-                                        _handle(stream, dev)))
+    if dx is None or (want_dw and dw is None) or (ws is None and (want_dw or dw is not None)):
+        M, N = _size(fn, r)
+        if dx is None:
+            dx = _new((M, N), r.dtype, r, stream)
+        if want_dw and dw is None:
+            dw = _new((N,), torch.float32, r, stream)
+        if dw is not None and ws is None:
+            ws = _new((max(rmsnorm_bwd_workspace_size(M, N), 0),), torch.uint8, r, stream)
+    st = _marshal.rmsnorm_residual_bwd(dy, r, w, rstd, dres, dx, dw, ws, stream)
+    if st:
+        raise MoEError(fn, st)
     return dx, dw
-
-
-_ACTS = {"none": MOE_ACT_NONE, "relu": MOE_ACT_RELU, "gelu": MOE_ACT_GELU, "silu": MOE_ACT_SILU}
-
-
-def _act(fn, act):
-    a = _ACTS.get(act, act)
-    _need(fn, isinstance(a, int))
-    return a
-
-
-def _new_rows(m, n, dtype, like, stream):
-    """An uninitialised [m, n] whose rows start at multiples of 16 bytes."""
-    t = _new((m, (n + 7) // 8 * 8), dtype, like, stream)
-    return t if n % 8 == 0 else t[:, :n]
 
 
 def linear_fwd(x, w, bias=None, act="none", residual=None, y=None, z=None, want_z=False, err=None, stream=None):
     """z = x w + bias, y = act(z) + residual (bf16; act "none", "relu", "gelu"
-    or "silu").  See include/moe.h.  Rows of every matrix start at multiples of 16 bytes.
-    Returns y, or (y, z) when z is asked for."""
+    or "silu").  See include/moe.h.  Rows of every matrix start at multiples
+    of 16 bytes.  Returns y, or (y, z) when z is asked for."""
     fn = "linear_fwd"
-    dev = _device()
-    px, _, ldx = _rows(fn, x, dev, types=_BF16)
-    M, K = x.shape
-    pw, _, ldw = _rows(fn, w, dev, K, types=_BF16)
-    N = w.shape[1]
-    y = y if y is not None else _new_rows(M, N, torch.bfloat16, x, stream)
-    if want_z and z is None:
-        z = _new_rows(M, N, torch.bfloat16, x, stream)
-    pr, _, ldr = _rows(fn, residual, dev, M, N, _BF16)
-    py, _, ldy = _rows(fn, y, dev, M, N, _BF16)
-    pz, _, ldz = _rows(fn, z, dev, M, N, _BF16)
-    _check(fn, lib.linear_fwd(px, ldx, pw, ldw, _flat(fn, bias, dev, N, _BF16), _act(fn, act), pr, ldr, M, N, K, py,
-                              ldy, pz, ldz, _flat(fn, err, dev, 1, _I32), _handle(stream, dev)))
+    if y is None or (want_z and z is None):
+        M, N = _size(fn, x, w)[0], w.shape[1]
+        y = y if y is not None else _new_rows(fn, M, N, torch.bfloat16, x, stream)
+        z = z if z is not None or not want_z else _new_rows(fn, M, N, torch.bfloat16, x, stream)
+    st = _marshal.linear_fwd(x, w, bias, _act(fn, act), residual, y, z, err, stream)
+    if st:
+        raise MoEError(fn, st)
     return y if z is None else (y, z)
 
 
@@ -793,28 +733,21 @@ def linear_bwd(dy, x, w, z=None, act="none", want_dx=True, want_dw=True, want_db
     (float32), those that are wanted or given.  See include/moe.h.  Returns
     (dx, dw, dbias)."""
     fn = "linear_bwd"
-    dev = _device()
     act = _act(fn, act)
-    pdy, _, lddy = _rows(fn, dy, dev, types=_BF16)
-    M, N = dy.shape
-    px, _, ldx = _rows(fn, x, dev, M, types=_BF16)
-    K = x.shape[1]
-    pw, _, ldw = _rows(fn, w, dev, K, N, _BF16)
-    pz, _, ldz = _rows(fn, z, dev, M, N, _BF16)
-    if want_dx and dx is None:
-        dx = _new_rows(M, K, torch.bfloat16, x, stream)
-    if want_dw and dw is None:
-        dw = _new_rows(K, N, dw_dtype, x, stream)
-    if want_dbias and dbias is None:
-        dbias = _new((N,), torch.float32, x, stream)
-    if ws is None and (dbias is not None or act != MOE_ACT_NONE):
-        ws = _new((max(linear_bwd_workspace_size(M, N), 0),), torch.uint8, x, stream)
-    pdx, _, lddx = _rows(fn, dx, dev, M, K, _BF16)
-    pdw, tdw, lddw = _rows(fn, dw, dev, K, N)
-    nws = 0 if ws is None else ws.numel()
-    _check(fn, lib.linear_bwd(pdy, lddy, px, ldx, pw, ldw, pz, ldz, act, M, N, K, pdx, lddx, pdw, tdw, lddw,
-                              _flat(fn, dbias, dev, N, _F32), _flat(fn, ws, dev, nws, _U8), nws,
-                              _flat(fn, err, dev, 1, _I32), _handle(stream, dev)))
+    need_ws = ws is None and (want_dbias or dbias is not None or act != MOE_ACT_NONE)
+    if need_ws or (want_dx and dx is None) or (want_dw and dw is None) or (want_dbias and dbias is None):
+        (M, N), K = _size(fn, dy, x), x.shape[1]
+        if want_dx and dx is None:
+            dx = _new_rows(fn, M, K, torch.bfloat16, x, stream)
+        if want_dw and dw is None:
+            dw = _new_rows(fn, K, N, dw_dtype, x, stream)
+        if want_dbias and dbias is None:
+            dbias = _new((N,), torch.float32, x, stream)
+        if need_ws:
+            ws = _new((max(linear_bwd_workspace_size(M, N), 0),), torch.uint8, x, stream)
+    st = _marshal.linear_bwd(dy, x, w, z, act, dx, dw, dbias, ws, err, stream)
+    if st:
+        raise MoEError(fn, st)
     return dx, dw, dbias
 
 
@@ -822,19 +755,13 @@ def gated_ffn_fwd(x, w1, act="silu", h=None, a=None, want_a=False, err=None, str
     """[gate | up] = x w1, h = act(gate) * up in one kernel (bf16).  See
     include/moe.h.  Returns h, or (h, a) when a = [gate | up] is asked for."""
     fn = "gated_ffn_fwd"
-    dev = _device()
-    px, _, ldx = _rows(fn, x, dev, types=_BF16)
-    M, d = x.shape
-    pw, _, ldw = _rows(fn, w1, dev, d, types=_BF16)
-    _need(fn, w1.shape[1] % 2 == 0)
-    f = w1.shape[1] // 2
-    h = h if h is not None else _new_rows(M, f, torch.bfloat16, x, stream)
-    if want_a and a is None:
-        a = _new_rows(M, 2 * f, torch.bfloat16, x, stream)
-    ph, _, ldh = _rows(fn, h, dev, M, f, _BF16)
-    pa, _, lda = _rows(fn, a, dev, M, 2 * f, _BF16)
-    _check(fn, lib.gated_ffn_fwd(px, ldx, pw, ldw, _act(fn, act), M, f, d, ph, ldh, pa, lda,
-                                 _flat(fn, err, dev, 1, _I32), _handle(stream, dev)))
+    if h is None or (want_a and a is None):
+        M, f2 = _size(fn, x, w1)[0], w1.shape[1]
+        h = h if h is not None else _new_rows(fn, M, f2 // 2, torch.bfloat16, x, stream)
+        a = a if a is not None or not want_a else _new_rows(fn, M, f2, torch.bfloat16, x, stream)
+    st = _marshal.gated_ffn_fwd(x, w1, _act(fn, act), h, a, err, stream)
+    if st:
+        raise MoEError(fn, st)
     return h if a is None else (h, a)
 
 
@@ -844,23 +771,14 @@ def gated_ffn_bwd(dh, a, x, w1, act="silu", want_dx=True, want_dw=True, dx=None,
     float32); da [M, 2f] is written on the way (may be a itself).  See
     include/moe.h.  Returns (dx, dw1)."""
     fn = "gated_ffn_bwd"
-    dev = _device()
-    pdh, _, lddh = _rows(fn, dh, dev, types=_BF16)
-    M, f = dh.shape
-    pa, _, lda = _rows(fn, a, dev, M, 2 * f, _BF16)
-    px, _, ldx = _rows(fn, x, dev, M, types=_BF16)
-    d = x.shape[1]
-    pw, _, ldw = _rows(fn, w1, dev, d, 2 * f, _BF16)
-    da = da if da is not None else _new_rows(M, 2 * f, torch.bfloat16, x, stream)
-    if want_dx and dx is None:
-        dx = _new_rows(M, d, torch.bfloat16, x, stream)
-    if want_dw and dw1 is None:
-        dw1 = _new_rows(d, 2 * f, dw_dtype, x, stream)
-    pda, _, ldda = _rows(fn, da, dev, M, 2 * f, _BF16)
-    pdx, _, lddx = _rows(fn, dx, dev, M, d, _BF16)
-    pdw, tdw, lddw = _rows(fn, dw1, dev, d, 2 * f)
-    _check(fn, lib.gated_ffn_bwd(pdh, lddh, pa, lda, px, ldx, pw, ldw, _act(fn, act), M, f, d, pda, ldda, pdx, lddx,
-                                 pdw, tdw, lddw, _flat(fn, err, dev, 1, _I32), _handle(stream, dev)))
+    if da is None or (want_dx and dx is None) or (want_dw and dw1 is None):
+        (M, f), d = _size(fn, dh, x), x.shape[1]
+        da = da if da is not None else _new_rows(fn, M, 2 * f, torch.bfloat16, x, stream)
+        dx = dx if dx is not None or not want_dx else _new_rows(fn, M, d, torch.bfloat16, x, stream)
+        dw1 = dw1 if dw1 is not None or not want_dw else _new_rows(fn, d, 2 * f, dw_dtype, x, stream)
+    st = _marshal.gated_ffn_bwd(dh, a, x, w1, _act(fn, act), da, dx, dw1, err, stream)
+    if st:
+        raise MoEError(fn, st)
     return dx, dw1
 
 
@@ -869,11 +787,8 @@ class AdamWPlan:
     and the references that keep the tensors alive."""
 
     def __init__(self, table, tensors, tiles, p_type, g_type, state_bits, kept):
-        self.table, self.tensors, self.tiles = table, tensors, tiles
-        self.p_type, self.g_type, self.state_bits = p_type, g_type, state_bits
-        self.kept = kept
-        self.address, self.opts = table.data_ptr(), AdamWOpts()
-        self.opts_ref = ctypes.byref(self.opts)      # filled in by each adamw_step
+        self.table, self.kept = table, kept
+        self.args = (table.data_ptr(), tensors, tiles, p_type, g_type, state_bits)
 
 
 def adamw_plan(params, grads, ms, vs, m_scales=None, v_scales=None, copies=None, weight_decay=0.0, rng_base=None,
@@ -882,16 +797,21 @@ def adamw_plan(params, grads, ms, vs, m_scales=None, v_scales=None, copies=None,
     contiguous tensors of equal sizes: params, grads (each list of one dtype,
     float32 or bfloat16), first and second moments (float32; or 8 bits:
     uint8 / float8_e4m3fn with m_scales and v_scales, float32 of ceil(n/256)),
-    optional bfloat16 copies of the params.  weight_decay: one number, or one per tensor.
-    rng_base: first counter of each tensor's rounding (8 bits; multiples of
-    256), by default one tensor after the other."""
+    optional bfloat16 copies of the params.  weight_decay: one number, or one
+    per tensor.  rng_base: first counter of each tensor's rounding (8 bits;
+    multiples of 256), by default one tensor after the other."""
     fn = "adamw_plan_encode"
-    dev = _device()
+    dev = torch._C._cuda_getDevice()
+
+    def address(t, n, *dtypes):
+        _need(fn, t.dtype in dtypes and t.numel() == n and t.get_device() == dev and t.is_contiguous())
+        return t.data_ptr()
+
     n = len(params)
     _need(fn, n >= 1 and len(grads) == len(ms) == len(vs) == n)
     bits = 32 if ms[0].dtype == torch.float32 else 8
     _need(fn, (bits == 8) == (m_scales is not None) == (v_scales is not None))
-    state = _F32 if bits == 32 else _E4M3
+    state = (torch.float32,) if bits == 32 else (torch.uint8, torch.float8_e4m3fn)
     pt, gt = params[0].dtype, grads[0].dtype
     _need(fn, pt in _TYPES and gt in _TYPES)
     for opt in (m_scales, v_scales, copies, rng_base):
@@ -902,13 +822,13 @@ def adamw_plan(params, grads, ms, vs, m_scales=None, v_scales=None, copies=None,
     counter = 0
     for i in range(n):
         e, k = arr[i], params[i].numel()
-        e.p, e.g = _flat(fn, params[i], dev, k, {pt: 0}), _flat(fn, grads[i], dev, k, {gt: 0})
-        e.m, e.v = _flat(fn, ms[i], dev, k, state), _flat(fn, vs[i], dev, k, state)
+        e.p, e.g = address(params[i], k, pt), address(grads[i], k, gt)
+        e.m, e.v = address(ms[i], k, *state), address(vs[i], k, *state)
         if bits == 8:
-            e.m_scale = _flat(fn, m_scales[i], dev, (k + 255) // 256, _F32)
-            e.v_scale = _flat(fn, v_scales[i], dev, (k + 255) // 256, _F32)
+            e.m_scale = address(m_scales[i], (k + 255) // 256, torch.float32)
+            e.v_scale = address(v_scales[i], (k + 255) // 256, torch.float32)
         if copies is not None:
-            e.copy = _flat(fn, copies[i], dev, k, _BF16)
+            e.copy = address(copies[i], k, torch.bfloat16)
         e.n, e.weight_decay = k, wd[i]
         e.rng_base = counter if rng_base is None else int(rng_base[i])
         counter += (k + 255) // 256 * 256
@@ -930,13 +850,6 @@ def adamw_step(plan, lr, betas=(0.9, 0.999), eps=1e-8, step=1, grad_scale=None, 
     which the call counts up.  lr: a number or a float32 device tensor.
     grad_scale: float32 device tensor, a factor of every gradient; when it is
     not finite the call changes nothing.  seed: of the 8-bit rounding."""
-    fn = "adamw_step"
-    dev = _device()
-    o = plan.opts
-    o.beta1, o.beta2 = betas
-    o.eps, o.seed = eps, seed & 0xFFFFFFFF
-    o.lr, o.lr_dev = (0.0, _flat(fn, lr, dev, 1, _F32)) if isinstance(lr, torch.Tensor) else (lr, None)
-    o.step, o.step_dev = (0, _flat(fn, step, dev, 1, _I32)) if isinstance(step, torch.Tensor) else (step, None)
-    o.grad_scale = _flat(fn, grad_scale, dev, 1, _F32)
-    _check(fn, lib.adamw_step(plan.address, plan.tensors, plan.tiles, plan.p_type, plan.g_type, plan.state_bits,
-                              plan.opts_ref, _handle(stream, dev)))
+    st = _marshal.adamw_step(*plan.args, lr, betas[0], betas[1], eps, step, grad_scale, seed, stream)
+    if st:
+        raise MoEError("adamw_step", st)
