@@ -1195,7 +1195,17 @@ static moe_status_t product_few(const Mat& x, const Mat& w, Params p, cudaStream
     return MOE_OK;
 }
 
-static bool few_rows(int64_t M) { return M <= few::ROWS; }
+// Up to 128 rows go to k_dense_few, whose tile costs what the rows cost.  So do
+// up to 384 rows when the pair kernel would have at most 16 tiles and
+// would have to split them (us, few rows' kernel against pairs, both in graphs
+// of 16: 256 x 1,024 x 1,024 6.9 / 9.2, 256 x 4,096 x 4,096 15.7 / 17.3, 384 x 2,000 x 608 8.0 / 10.5,
+// 256 x 7,168 x 512 11.1 / 15.1), but for short contractions, which pairs do not split
+// (256 x 608 x 2,000 7.5 / 6.2), and long ones (256 x 14,336 x 4,096 34.0 / 32.7).
+static bool few_rows(int64_t M, int64_t N, int64_t K) {
+    if (M <= few::ROWS) return true;
+    const int64_t tiles = (M + 255) / 256 * ((N + 255) / 256), nk = (K + TK - 1) / TK;
+    return M <= 384 && tiles <= 16 && nk >= 12 && nk <= 128;
+}
 
 static bool act_ok(int a) { return a >= MOE_ACT_NONE && a <= MOE_ACT_SILU; }
 // sizes the tensor maps and the tile counts hold
@@ -1235,7 +1245,7 @@ extern "C" moe_status_t linear_fwd(const void* x, int64_t ldx, const void* w, in
     p.bias = static_cast<const __nv_bfloat16*>(bias);
     p.res = static_cast<const __nv_bfloat16*>(res), p.ldres = ldres;
     p.err = err;
-    if (few_rows(M)) return product_few<true, EPI_LINEAR>({x, M, K, ldx}, {w, K, N, ldw}, p, (cudaStream_t)stream);
+    if (few_rows(M, N, K)) return product_few<true, EPI_LINEAR>({x, M, K, ldx}, {w, K, N, ldw}, p, (cudaStream_t)stream);
     const Mat mx{x, M, K, ldx}, mw{w, K, N, ldw};
     cudaStream_t s = (cudaStream_t)stream;
     if (!bias && !res && !z && act == MOE_ACT_NONE) return product<false, true, EPI_PLAIN, 0>(mx, mw, p, s);
@@ -1252,7 +1262,7 @@ static moe_status_t input_grad(const void* dy, int64_t lddy, const void* w, int6
                                void* dx, int64_t lddx, int32_t* err, cudaStream_t s) {
     dense::Params p{};
     p.M = M, p.N = (int)K, p.K = N, p.act = MOE_ACT_NONE, p.y = dx, p.ldy = lddx, p.err = err;
-    if (few_rows(M)) return product_few<false, EPI_LINEAR>({dy, M, N, lddy}, {w, K, N, ldw}, p, s);
+    if (few_rows(M, K, N)) return product_few<false, EPI_LINEAR>({dy, M, N, lddy}, {w, K, N, ldw}, p, s);
     return product<false, false, EPI_PLAIN, 0>({dy, M, N, lddy}, {w, K, N, ldw}, p, s);
 }
 static moe_status_t weight_grad(const void* x, int64_t ldx, const void* dy, int64_t lddy, int64_t M, int N, int64_t K,
@@ -1338,7 +1348,7 @@ extern "C" moe_status_t gated_ffn_fwd(const void* x, int64_t ldx, const void* w1
     p.M = M, p.N = f, p.K = d, p.act = act, p.up = f;
     p.y = h, p.ldy = ldh, p.z = static_cast<__nv_bfloat16*>(a), p.ldz = lda;
     p.err = err;
-    if (few_rows(M))
+    if (few_rows(M, 2 * (int64_t)f, d))
         return product_few<true, EPI_GLU>({x, M, d, ldx}, {w1, d, 2 * (int64_t)f, ldw}, p, (cudaStream_t)stream);
     const Mat mx{x, M, d, ldx}, mw{w1, d, 2 * (int64_t)f, ldw};
     cudaStream_t s = (cudaStream_t)stream;

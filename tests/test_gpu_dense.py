@@ -65,7 +65,7 @@ def linear_tol(x, w, b, act, res, want, z):
 
 # (M, N, K): one tile, ragged everywhere, several tiles per pair, one row, one column, one deep
 SIZES = [(256, 256, 64), (1, 1, 1), (1, 4096, 256), (3, 257, 65), (16, 520, 1000), (127, 128, 129), (255, 300, 8),
-         (257, 513, 777), (1000, 1001, 130), (2049, 264, 4099), (5000, 4100, 70), (64, 24, 14336)]
+         (257, 513, 777), (200, 1030, 900), (384, 520, 1000), (1000, 1001, 130), (2049, 264, 4099), (5000, 4100, 70), (64, 24, 14336)]
 
 
 @pytest.mark.parametrize("m,n,k", SIZES)
