@@ -129,6 +129,13 @@ __device__ __forceinline__ void prefetch_map(const CUtensorMap* m) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(m) : "memory");
 }
 
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t one;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
+    return one != 0;
+}
+
 __device__ __forceinline__ void tc_mma2_bf16(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
                                              uint32_t accumulate) {
     asm volatile(
@@ -353,7 +360,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                  const __grid_constant__ CUtensorMap tmZ2, const Params p) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xFFFFFFFFu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
     const uint32_t crank = cluster_ctarank();
     const uint32_t rank = crank & 1u, lead = crank & ~1u;      // in the pair; the pair's leader in the cluster
     const int part = (int)(crank >> 1);                        // of K
@@ -410,8 +417,9 @@ __global__ void __launch_bounds__(THREADS, 1)
     const uint32_t lane_base = tmem_base + ((uint32_t)(quarter * 32) << 16);
     Out out{smem_u32(smem + OFF_EPI + ew * EPI_STAGE), smem_u32(smem + ew * 16384), lane, 0u, false};
 
-    if (warp == 0 && lane == 0) {
+    if (warp == 0) {
         // ------------------------------------------------ TMA producer ----
+        const bool elected = elect_one();
         const uint32_t lead_full = mapa(full_bar(0), lead);
         int stage = 0, issued = 0;
         uint32_t phase = 0;
@@ -430,19 +438,21 @@ __global__ void __launch_bounds__(THREADS, 1)
                 const int k = ks * TK;
                 // both CTAs' bytes complete on the leader's full barrier
                 const uint32_t fb = lead_full + 8u * stage;
-                if (leader) mbar_expect_tx(full_bar(stage), 2u * (uint32_t)p.stage_bytes);
-                const uint32_t sa = smem_u32(smem + stage * p.stage_bytes), sb = sa + HALF_BYTES;
-                if constexpr (A_MN) {
-                    tma2_load_2d(sa, &tmA, am, k, fb);
-                    tma2_load_2d(sa + HALF_BYTES / 2, &tmA, am + 64, k, fb);
-                } else {
-                    tma2_load_2d(sa, &tmA, k, am, fb);
-                }
-                if constexpr (B_MN) {
-                    tma2_load_2d(sb, &tmB, bn, k, fb);
-                    if (b_boxes > 1) tma2_load_2d(sb + HALF_BYTES / 2, &tmB, bn + 64, k, fb);
-                } else {
-                    tma2_load_2d(sb, &tmB, k, bn, fb);
+                if (elected) {
+                    if (leader) mbar_expect_tx(full_bar(stage), 2u * (uint32_t)p.stage_bytes);
+                    const uint32_t sa = smem_u32(smem + stage * p.stage_bytes), sb = sa + HALF_BYTES;
+                    if constexpr (A_MN) {
+                        tma2_load_2d(sa, &tmA, am, k, fb);
+                        tma2_load_2d(sa + HALF_BYTES / 2, &tmA, am + 64, k, fb);
+                    } else {
+                        tma2_load_2d(sa, &tmA, k, am, fb);
+                    }
+                    if constexpr (B_MN) {
+                        tma2_load_2d(sb, &tmB, bn, k, fb);
+                        if (b_boxes > 1) tma2_load_2d(sb + HALF_BYTES / 2, &tmB, bn + 64, k, fb);
+                    } else {
+                        tma2_load_2d(sb, &tmB, k, bn, fb);
+                    }
                 }
                 ++issued;
                 if (++stage == p.stages) {
@@ -451,6 +461,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 }
             }
         }
+        __syncwarp();
         if (aborted && leader) {
             // wait (bounded) for the copies in flight: the leader's full
             // barriers count both CTAs' bytes, and the follower leaves only
@@ -461,49 +472,58 @@ __global__ void __launch_bounds__(THREADS, 1)
             for (int i = issued - min(issued, p.stages); i < issued; ++i)
                 mbar_wait_cluster(full_bar(i % p.stages), (uint32_t)(i / p.stages) & 1u, q, &no_abort);
         }
-    } else if (warp == 1 && lane == 0 && leader) {
+    } else if (warp == 1 && leader) {
         // ---------------------------------------- MMA issuer (leader) ----
+        // The whole warp goes through the loop, one elected lane issues: with
+        // warp-uniform control the descriptors stay in uniform registers, and the
+        // loop has to be short -- a k-step's four products take 512 cycles.
+        const bool elected = elect_one();
         int stage = 0, acc = 0;
         uint32_t phase = 0, acc_phase = 0;
         bool aborted = false, issued = false;
         const uint32_t idesc = make_idesc_pair<A_MN, B_MN>(p.bn);
+        const uint64_t adesc0 = operand_desc<A_MN>(smem_u32(smem));
+        const uint64_t bdesc0 = operand_desc<B_MN>(smem_u32(smem) + HALF_BYTES);
+        const uint32_t stage_step = (uint32_t)p.stage_bytes >> 4;
         for (int t = first; t < total && !aborted; t += step) {
             if (!mbar_wait_cluster(tempty_bar(acc), acc_phase ^ 1u, p, abort_flag)) break;
             tc_fence_after();
             const uint32_t d_tmem = tmem_base + (uint32_t)(acc * ACC_COLS);
             for (int ks = k0; ks < k1; ++ks) {
-                if (!mbar_wait_cluster(full_bar(stage), phase, p, abort_flag)) {
+                if (!mbar_wait(full_bar(stage), phase, p, abort_flag)) {
                     aborted = true;
                     break;
                 }
                 tc_fence_after();
-                const uint32_t sa = smem_u32(smem + stage * p.stage_bytes);
-                const uint64_t adesc = operand_desc<A_MN>(sa), bdesc = operand_desc<B_MN>(sa + HALF_BYTES);
+                if (elected) {
+                    const uint64_t adesc = adesc0 + stage * stage_step, bdesc = bdesc0 + stage * stage_step;
 #pragma unroll
-                for (int kk = 0; kk < TK / 16; ++kk)
-                    tc_mma2_bf16(d_tmem, adesc + k16_step<A_MN>() * kk, bdesc + k16_step<B_MN>() * kk, idesc,
-                                 (ks != k0 || kk != 0) ? 1u : 0u);
+                    for (int kk = 0; kk < TK / 16; ++kk)
+                        tc_mma2_bf16(d_tmem, adesc + k16_step<A_MN>() * kk, bdesc + k16_step<B_MN>() * kk, idesc,
+                                     (ks != k0 || kk != 0) ? 1u : 0u);
+                    tc_commit_pair(empty_bar(stage), lead);
+                }
                 issued = true;
-                tc_commit_pair(empty_bar(stage), lead);
                 if (++stage == p.stages) {
                     stage = 0;
                     phase ^= 1u;
                 }
             }
             if (aborted) break;
-            tc_commit_pair(tfull_bar(acc), lead);
+            if (elected) tc_commit_pair(tfull_bar(acc), lead);
             if (++acc == NACC) {
                 acc = 0;
                 acc_phase ^= 1u;
             }
         }
         if (issued) {
-            tc_commit_local2(drain_bar);
+            if (elected) tc_commit_local2(drain_bar);
             Params q = p;
             q.timeout_ns = 200000000ull;
             volatile int no_abort = 0;
             mbar_wait(drain_bar, 0, q, &no_abort);
         }
+        __syncwarp();
     } else if (warp >= 4 && p.splits == 1) {
         // ----------------------------------------------------- epilogue ----
         int acc = 0;
@@ -791,7 +811,7 @@ __global__ void __launch_bounds__(THREADS, 2)
                 const Split s) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xFFFFFFFFu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
     const uint32_t rank = s.splits > 1 ? cluster_ctarank() : 0;
     const int tile = blockIdx.x / s.splits, mt = tile / p.n_tiles, nt = tile - mt * p.n_tiles;
     const int64_t m0 = (int64_t)mt * s.rows;
@@ -860,34 +880,33 @@ __global__ void __launch_bounds__(THREADS, 2)
             for (int i = issued - min(issued, s.stages); i < issued; ++i)
                 mbar_wait(full_bar(i % s.stages), (uint32_t)(i / s.stages) & 1u, q, &no_abort);
         }
-    } else if (warp == 1 && lane == 0) {
-        // -------------------------------------------------- MMA issuer ----
+    } else if (warp == 1) {
+        // ------------------------- MMA issuer (one lane of the warp) ----
+        const bool elected = elect_one();
         // bf16 A and B, fp32 D, M = 128, N = s.rows, A along M (W_MN) or K
         const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | (W_MN ? 1u << 15 : 0u) |
                                ((uint32_t)(s.rows >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
         int stage = 0;
         uint32_t phase = 0;
-        bool ok = true;
+        const uint32_t sw0 = smem_u32(smem), stage_step = (uint32_t)stage_bytes >> 4;
+        const uint64_t wdesc0 = operand_desc<W_MN>(sw0), xdesc0 = desc_sw128(sw0 + W_BYTES);
         for (int k = k0; k < k1; ++k) {
-            if (!mbar_wait(full_bar(stage), phase, p, abort_flag)) {
-                ok = false;
-                break;
-            }
+            if (!mbar_wait(full_bar(stage), phase, p, abort_flag)) break;
             tc_fence_after();
-            const uint32_t sw = smem_u32(smem + stage * stage_bytes);
-            const uint64_t wdesc = operand_desc<W_MN>(sw), xdesc = desc_sw128(sw + W_BYTES);
+            if (elected) {
+                const uint64_t wdesc = wdesc0 + stage * stage_step, xdesc = xdesc0 + stage * stage_step;
 #pragma unroll
-            for (int kk = 0; kk < TK / 16; ++kk)
-                tc_mma_bf16(tmem, wdesc + k16_step<W_MN>() * kk, xdesc + k16_step<false>() * kk, idesc,
-                            (k != k0 || kk != 0) ? 1u : 0u);
-            tc_commit(empty_bar(stage));
+                for (int kk = 0; kk < TK / 16; ++kk)
+                    tc_mma_bf16(tmem, wdesc + k16_step<W_MN>() * kk, xdesc + k16_step<false>() * kk, idesc,
+                                (k != k0 || kk != 0) ? 1u : 0u);
+                tc_commit(empty_bar(stage));
+            }
             if (++stage == s.stages) {
                 stage = 0;
                 phase ^= 1u;
             }
         }
-        (void)ok;
-        tc_commit(done_bar);
+        if (elected) tc_commit(done_bar);
     }
     __syncwarp();
     // every product of this CTA is done (and every stage read), or the CTA gives up
