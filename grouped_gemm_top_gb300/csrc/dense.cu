@@ -1095,7 +1095,8 @@ static cudaError_t set_attributes() {
     for (int i = 0; i < 4; ++i) {
         cudaLaunchAttribute attr[2];
         cudaLaunchConfig_t cfg = launch_cfg(1024, i + 1, nullptr, attr);
-        const cudaError_t e = cudaOccupancyMaxActiveClusters(&g_max_clusters[i], k_dense_pair<false, true, EPI_PLAIN, 0>, &cfg);
+        const cudaError_t e =
+            cudaOccupancyMaxActiveClusters(&g_max_clusters[i], k_dense_pair<false, true, EPI_PLAIN, 0>, &cfg);
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;
@@ -1107,18 +1108,22 @@ struct Mat {
     int64_t rows, cols, ld;
 };
 
-// The pair's tile width and the parts of K.  A wave of tiles costs about
-// nk / splits k-steps of step(bn) and a fixed part worth kFixed steps of the
-// widest tile; splitting adds the swap.  (Steps of a full machine, measured
-// on 4,096 x 7,168 x 7,168: 0.344, 0.31, 0.30 and 0.24 us for 256, 224, 192 and
-// 128 columns.)  Narrower tiles win where they fill the last wave better,
-// parts of K where the tiles are fewer than the SM pairs.
+// The pair's tile width and the parts of K, by what a launch costs in k-steps
+// of the widest tile (0.27 us): waves of tiles, each nk / splits k-steps of
+// step_cost(bn), no shorter than the epilogue that runs under it, the last tile's
+// epilogue, and the swap when K is split (5.5 us: three cluster barriers and the partial
+// tiles).  Steps, measured alone / on a full machine under its power cap,
+// relative to 256 columns: 224 0.87 / 0.94, 192 0.75 / 0.84, 128 0.54 / 0.57.
+// Narrower tiles win where the wide ones are fewer than the SM pairs or leave the
+// last wave half empty (256 x 4,096 x 4,096: 13.8 us with 128 columns, 22.0 with 256, 17.9
+// with 256 in two parts), parts of K where even those are few (256 x 14,336 x
+// 2,048: 23.4 us with 128 columns in two parts, 38.3 with 256).
 struct Choice {
     int bn, splits;
 };
-static double step_cost(int bn) { return bn == 256 ? 1.0 : (bn == 224 ? 0.90 : (bn == 192 ? 0.87 : 0.70)); }
+static double step_cost(int bn) { return bn == 256 ? 1.0 : (bn == 224 ? 0.91 : (bn == 192 ? 0.80 : 0.56)); }
 static Choice choose(int64_t m_tiles, int N, int nk, bool glu) {
-    constexpr double kFixed = 8., kSwap = 8.;
+    constexpr double kEpilogue = 5., kSwap = 20.;
     static const int widths[] = {256, 224, 192, 128};
     Choice best{256, 1};
     double best_cost = 1e300;
@@ -1126,12 +1131,13 @@ static Choice choose(int64_t m_tiles, int N, int nk, bool glu) {
         if (glu && bn == 224) continue;      // gate and up in whole chunks of 32
         const int cols = glu ? bn / 2 : bn;
         const int64_t tiles = m_tiles * ((N + cols - 1) / cols);
+        const double epilogue = kEpilogue * bn / 256.;
         for (int splits = 1; splits <= 4; ++splits) {
             const int slots = g_max_clusters[splits - 1];
             if (splits > 1 && (tiles > slots || nk < 4 * splits)) continue;
             const int64_t waves = (tiles + slots - 1) / slots;
-            const double cost = (double)waves * ((nk + splits - 1) / splits * step_cost(bn) + kFixed * bn / 256.) +
-                                (splits > 1 ? kSwap : 0.);
+            const double steps = (nk + splits - 1) / splits * step_cost(bn);
+            const double cost = (double)waves * (std::max(steps, epilogue) + 1.) + epilogue + (splits > 1 ? kSwap : 0.);
             if (cost < best_cost) best_cost = cost, best = {bn, splits};
         }
     }
@@ -1189,7 +1195,12 @@ static moe_status_t product_few(const Mat& x, const Mat& w, Params p, cudaStream
     const int64_t tiles = (int64_t)p.m_tiles * p.n_tiles;
     const int sms = device_sm_count();
     s.splits = 1;
-    while (s.splits < 8 && tiles * s.splits * 2 <= 2 * sms && p.nk >= 8 * s.splits) s.splits *= 2;
+    // Twice the parts save nk / (2 splits) k-steps and lengthen the swap by rows x splits
+    // (128 x 2,048 x 2,048: 7.6 us in four parts, 9.9 in eight; 128 x 7,168 x 512: 11.8, 9.8),
+    // the more the fuller the machine is (128 x 4,096 x 4,096: 13.3 in four, 15.2 in eight)
+    while (s.splits < 8 && tiles * s.splits * 2 <= 2 * sms && p.nk >= 8 * s.splits &&
+           (tiles * s.splits * 2 <= sms ? 40 : 16) * p.nk > s.rows * s.splits * s.splits)
+        s.splits *= 2;
     MOE_REQUIRE(tiles * s.splits <= 0x7FFFFFFFLL, MOE_ERR_UNSUPPORTED);
     CUtensorMap tmW, tmX;
     MOE_REQUIRE(make_bf16_map(&tmW, w.p, w.rows, w.cols, w.ld, W_MN ? TK : 128) &&
@@ -1214,16 +1225,17 @@ static moe_status_t product_few(const Mat& x, const Mat& w, Params p, cudaStream
     return MOE_OK;
 }
 
-// Up to 128 rows go to k_dense_few, whose tile costs what the rows cost.  So do
-// up to 384 rows when the pair kernel would have at most 16 tiles and
-// would have to split them (us, few rows' kernel against pairs, both in graphs
-// of 16: 256 x 1,024 x 1,024 6.9 / 9.2, 256 x 4,096 x 4,096 15.7 / 17.3, 384 x 2,000 x 608 8.0 / 10.5,
-// 256 x 7,168 x 512 11.1 / 15.1), but for short contractions, which pairs do not split
-// (256 x 608 x 2,000 7.5 / 6.2), and long ones (256 x 14,336 x 4,096 34.0 / 32.7).
+// Few rows go to k_dense_few, whose tile costs what the rows cost and which
+// splits K over more CTAs than the pair kernel.  Measured in graphs of 16
+// (us, k_dense_few / pairs): up to 64 rows nearly always (64 x 4,096 x 4,096 10.3 / 13.4);
+// up to 128 where K has steps to split (128 x 2,048 x 2,048 7.6 / 8.2, 128 x 7,168 x 7,168
+// 24.9 / 24.6, but 128 x 1,024 x 1,024 6.7 / 5.7); up to 384 where that also leaves
+// few tiles (384 x 2,000 x 608 7.8 / 9.1, 384 x 7,168 x 512 10.7 / 12.3, but 384 x 4,096 x 1,024 13.3 / 12.3).
 static bool few_rows(int64_t M, int64_t N, int64_t K) {
-    if (M <= few::ROWS) return true;
-    const int64_t tiles = (M + 255) / 256 * ((N + 255) / 256), nk = (K + TK - 1) / TK;
-    return M <= 384 && tiles <= 16 && nk >= 12 && nk <= 128;
+    const int64_t nk = (K + TK - 1) / TK;
+    if (M <= 64) return true;
+    if (M <= few::ROWS) return nk > 16;
+    return M <= 384 && nk >= 24 && M * N < (1 << 18);
 }
 
 static bool act_ok(int a) { return a >= MOE_ACT_NONE && a <= MOE_ACT_SILU; }
@@ -1264,9 +1276,9 @@ extern "C" moe_status_t linear_fwd(const void* x, int64_t ldx, const void* w, in
     p.bias = static_cast<const __nv_bfloat16*>(bias);
     p.res = static_cast<const __nv_bfloat16*>(res), p.ldres = ldres;
     p.err = err;
-    if (few_rows(M, N, K)) return product_few<true, EPI_LINEAR>({x, M, K, ldx}, {w, K, N, ldw}, p, (cudaStream_t)stream);
     const Mat mx{x, M, K, ldx}, mw{w, K, N, ldw};
     cudaStream_t s = (cudaStream_t)stream;
+    if (few_rows(M, N, K)) return product_few<true, EPI_LINEAR>(mx, mw, p, s);
     if (!bias && !res && !z && act == MOE_ACT_NONE) return product<false, true, EPI_PLAIN, 0>(mx, mw, p, s);
     switch (act) {
         case MOE_ACT_RELU: return product<false, true, EPI_LINEAR, MOE_ACT_RELU>(mx, mw, p, s);
