@@ -164,22 +164,31 @@ __device__ __forceinline__ float act_slope(float z, int act) {
     return 1.f;
 }
 
-// 32 columns of one row from / to memory; `n` of them exist.  Rows start at
+__device__ __forceinline__ uint4 load_vec8(const __nv_bfloat16* p, int n) {      // n < 8: zeros after them
+    if (n == 8) return *reinterpret_cast<const uint4*>(p);
+    uint32_t w[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        if (j < n) w[j >> 1] |= (uint32_t)__bfloat16_as_ushort(p[j]) << (16 * (j & 1));
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+// 32 columns of one row from memory; `n` of them exist.  Rows start at
 // multiples of 16 bytes and columns at multiples of 32.
 __device__ __forceinline__ void load32(const __nv_bfloat16* p, int n, float* f) {
     if (n >= 32) {
         load_row32(p, f);
     } else {
 #pragma unroll
-        for (int i = 0; i < 32; ++i) f[i] = i < n ? __bfloat162float(p[i]) : 0.f;
+        for (int g = 0; g < 4; ++g)
+            unpack8(n > 8 * g ? load_vec8(p + 8 * g, min(n - 8 * g, 8)) : make_uint4(0u, 0u, 0u, 0u), f + 8 * g);
     }
 }
-// The columns of a row from `p` on, n < 32 of them, element by element.
+// The last n % 8 of the n < 32 columns of a row from `p` on.
 template <typename T>
-__device__ __forceinline__ void store_edge(T* p, int n, const float* v) {
+__device__ __forceinline__ void store_tail(T* p, int n, const float* v) {
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
-        if (i < n) {
+    for (int i = 0; i < 31; ++i) {
+        if (i < n && i >= (n & ~7)) {
             if constexpr (sizeof(T) == 4) p[i] = v[i];
             else p[i] = __float2bfloat16_rn(v[i]);
         }
@@ -275,9 +284,10 @@ template <int EPI, int ACT>
 __device__ __forceinline__ void finish(const Params& p, const CUtensorMap* tmY, const CUtensorMap* tmZ,
                                        const CUtensorMap* tmZ2, Out& out, int64_t row0, int64_t row, int col, int n,
                                        float* v, float* u) {
-    // a TMA store is clipped at D's edge to whole 16 bytes: the last columns
-    // of a width that is no multiple of 8 go element by element (GLU: f is one)
-    const bool edge = EPI != EPI_GLU && n < 32 && (p.N & 7) != 0;
+    // a TMA store is clipped at D's edge to whole 16 bytes: of a width that is
+    // no multiple of 8 the boxes end at the last one, and the columns after it
+    // are stored from here (GLU: f is a multiple)
+    const bool tail = EPI != EPI_GLU && n < 32 && (n & 7) != 0, box = !tail || n > 8;
     if constexpr (EPI == EPI_GLU) {
         if (p.z != nullptr) {
             out.bf16(tmZ, col, row0, v);
@@ -287,10 +297,8 @@ __device__ __forceinline__ void finish(const Params& p, const CUtensorMap* tmY, 
         for (int i = 0; i < 32; ++i) u[i] *= act_of(v[i], ACT);
         out.bf16(tmY, col, row0, u);
     } else if constexpr (EPI == EPI_F32) {
-        if (!edge)
-            out.f32(tmY, col, row0, v);
-        else if (row < p.M)
-            store_edge(static_cast<float*>(p.y) + row * p.ldy + col, n, v);
+        if (box) out.f32(tmY, col, row0, v);
+        if (tail && row < p.M) store_tail(static_cast<float*>(p.y) + row * p.ldy + col, n, v);
     } else {
         if constexpr (EPI == EPI_LINEAR) {
             if (p.bias != nullptr) {
@@ -299,10 +307,8 @@ __device__ __forceinline__ void finish(const Params& p, const CUtensorMap* tmY, 
                 for (int i = 0; i < 32; ++i) v[i] += __shfl_sync(0xFFFFFFFFu, b, i);
             }
             if (p.z != nullptr) {
-                if (!edge)
-                    out.bf16(tmZ, col, row0, v);
-                else if (row < p.M)
-                    store_edge(p.z + row * p.ldz + col, n, v);
+                if (box) out.bf16(tmZ, col, row0, v);
+                if (tail && row < p.M) store_tail(p.z + row * p.ldz + col, n, v);
             }
             if constexpr (ACT != MOE_ACT_NONE) {
 #pragma unroll
@@ -315,10 +321,8 @@ __device__ __forceinline__ void finish(const Params& p, const CUtensorMap* tmY, 
                 for (int i = 0; i < 32; ++i) v[i] += r[i];
             }
         }
-        if (!edge)
-            out.bf16(tmY, col, row0, v);
-        else if (row < p.M)
-            store_edge(static_cast<__nv_bfloat16*>(p.y) + row * p.ldy + col, n, v);
+        if (box) out.bf16(tmY, col, row0, v);
+        if (tail && row < p.M) store_tail(static_cast<__nv_bfloat16*>(p.y) + row * p.ldy + col, n, v);
     }
 }
 
@@ -334,7 +338,7 @@ __device__ __forceinline__ void flush(const Params& p, const CUtensorMap* tmY, c
     uint32_t b = out.last;
     for (int c = c0; c < c1; c += stride) {
         const int col = col0 + 32 * c, n = p.N - col;
-        if (n <= 0 || (EPI != EPI_GLU && n < 32 && (p.N & 7) != 0)) continue;
+        if (n <= 0 || (EPI != EPI_GLU && n < 8)) continue;
         if (EPI == EPI_LINEAR || EPI == EPI_GLU) {
             if (p.z != nullptr) {
                 tma_store_2d(tmZ, b, col, (int)row0);
@@ -978,14 +982,6 @@ __global__ void __launch_bounds__(256) k_glu_bwd(const __nv_bfloat16* __restrict
 // order at the end.  Bound by its 6 bytes an element.
 constexpr int kActRowsInFlight = 4;
 
-__device__ __forceinline__ uint4 load_vec8(const __nv_bfloat16* p, int n) {      // n < 8: zeros after them
-    if (n == 8) return *reinterpret_cast<const uint4*>(p);
-    uint32_t w[4] = {0u, 0u, 0u, 0u};
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-        if (j < n) w[j >> 1] |= (uint32_t)__bfloat16_as_ushort(p[j]) << (16 * (j & 1));
-    return make_uint4(w[0], w[1], w[2], w[3]);
-}
 
 template <int ACT>
 __global__ void __launch_bounds__(256) k_act_bwd(const __nv_bfloat16* __restrict__ dy, int64_t lddy,
@@ -1159,13 +1155,14 @@ static moe_status_t product(const Mat& a, const Mat& b, Params p, cudaStream_t s
     p.band = 8;
     p.timeout_ns = 2000000000ull;
     CUtensorMap tmA, tmB, tmY, tmZ, tmZ2;
+    const int boxed = std::max(p.N & ~7, 8);      // finish(): N < 8 sends no box
     MOE_REQUIRE(make_bf16_map(&tmA, a.p, a.rows, a.cols, a.ld, A_MN ? TK : 128) &&
                     make_bf16_map(&tmB, b.p, b.rows, b.cols, b.ld, B_MN ? TK : p.bn / 2) &&
-                    make_store_map(&tmY, p.y, p.M, p.N, p.ldy, EPI == EPI_F32),
+                    make_store_map(&tmY, p.y, p.M, boxed, p.ldy, EPI == EPI_F32),
                 MOE_ERR_CUDA);
     tmZ = tmZ2 = tmY;
     if (p.z != nullptr)
-        MOE_REQUIRE(make_store_map(&tmZ, p.z, p.M, p.N, p.ldz, false) &&
+        MOE_REQUIRE(make_store_map(&tmZ, p.z, p.M, boxed, p.ldz, false) &&
                         (EPI != EPI_GLU || make_store_map(&tmZ2, p.z + p.N, p.M, p.N, p.ldz, false)),
                     MOE_ERR_CUDA);
     const int64_t tiles = (int64_t)p.m_tiles * p.n_tiles;

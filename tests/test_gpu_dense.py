@@ -117,6 +117,24 @@ def test_linear_backward(ops, m, n, k, act, dw_dtype):
     assert torch.equal(dx, again[0]) and torch.equal(dw, again[1]) and torch.equal(db, again[2])
 
 
+@pytest.mark.parametrize("n", list(range(1, 35)) + [63, 121, 127, 250, 253, 287])
+def test_every_width_of_the_last_columns(ops, n):
+    m, k = 400, 72
+    x, w, b, r = mat(m, k, 1, pad=8), mat(k, n, 2, 0.1), mat(1, n, 3)[0], mat(m, n, 4)
+    out = mat(m, n, 5, pad=8)
+    y, z = ops.linear_fwd(x, w, b, "relu", r, y=out, want_z=True)
+    want, wz = D.linear(f64(x), f64(w), f64(b), "relu", f64(r))
+    close(y, want, linear_tol(f64(x), f64(w), f64(b), "relu", f64(r), want, wz), "y")
+    close(z, wz, linear_tol(f64(x), f64(w), f64(b), "none", None, wz, wz), "z")
+    assert torch.isnan(out._base[:, n:]).all()
+    for dtype in (BF, F):
+        dw = torch.full((m, up8(n) + 8), float("nan"), dtype=dtype, device="cuda")
+        ops.linear_bwd(mat(k, n, 6), mat(k, m, 7), mat(m, n, 8), want_dx=False, dw=dw[:, :n])
+        g, h = f64(mat(k, m, 7)).T, f64(mat(k, n, 6))
+        close(dw[:, :n], g @ h, np.abs(g @ h) * (HALF if dtype == BF else 0) + acc(k) * (np.abs(g) @ np.abs(h)), "dw")
+        assert torch.isnan(dw[:, n:]).all()
+
+
 # (M, f, d)
 GLU_SIZES = [(1, 8, 1), (1, 4096, 256), (4, 520, 1000), (128, 128, 64), (130, 136, 129), (257, 264, 777),
              (1000, 1000, 65), (2049, 128, 2050), (33, 3000, 72)]
