@@ -1107,33 +1107,40 @@ struct Mat {
 // The pair's tile width and the parts of K, by what a launch costs in k-steps
 // of the widest tile (0.27 us): waves of tiles, each nk / splits k-steps of
 // step_cost(bn), no shorter than the epilogue that runs under it, the last tile's
-// epilogue, and the swap when K is split (5.5 us: three cluster barriers and the partial
-// tiles).  Steps, measured alone / on a full machine under its power cap,
-// relative to 256 columns: 224 0.87 / 0.94, 192 0.75 / 0.84, 128 0.54 / 0.57.
+// epilogue, and the swap when K is split.  Steps, measured alone / on a full
+// machine under its power cap, relative to 256 columns: 224 0.87 / 0.94, 192
+// 0.75 / 0.84, 128 0.54 / 0.57, bound by the products; 64 0.56 alone, bound by the
+// loads in flight, and 1.2 on a full machine.
 // Narrower tiles win where the wide ones are fewer than the SM pairs or leave the
 // last wave half empty (256 x 4,096 x 4,096: 13.8 us with 128 columns, 22.0 with 256, 17.9
-// with 256 in two parts), parts of K where even those are few (256 x 14,336 x
-// 2,048: 23.4 us with 128 columns in two parts, 38.3 with 256).
+// with 256 in two parts; 256 x 1,024 x 1,024: 5.4 with 64 columns, 5.8 with 128), parts of
+// K where even those are few (256 x 14,336 x 2,048: 23.4 us with 128 columns in two
+// parts, 38.3 with 256; 512 x 2,000 x 608: 8.7 with 64 columns, 7.7 in two parts).
 struct Choice {
     int bn, splits;
 };
 static double step_cost(int bn) { return bn == 256 ? 1.0 : (bn == 224 ? 0.91 : (bn == 192 ? 0.80 : 0.56)); }
+// 1.5 to 2 us for 64 columns in two parts, 2.7 for 128, 4.3 for 256; 6 for 256 in three, 3.5 for 64 in four
+static double swap_cost(int bn, int splits) { return (4. + 12. * bn / 256.) * (1. + 0.4 * (splits - 2)); }
 static Choice choose(int64_t m_tiles, int N, int nk, bool glu) {
-    constexpr double kEpilogue = 5., kSwap = 20.;
-    static const int widths[] = {256, 224, 192, 128};
+    constexpr double kEpilogue = 5.;
+    static const int widths[] = {256, 224, 192, 128, 64};
     Choice best{256, 1};
     double best_cost = 1e300;
     for (int bn : widths) {
-        if (glu && bn == 224) continue;      // gate and up in whole chunks of 32
+        // gate and up in whole chunks of 32, one at least for each half of the epilogue's warps
+        if (glu && (bn == 224 || bn == 64)) continue;
         const int cols = glu ? bn / 2 : bn;
         const int64_t tiles = m_tiles * ((N + cols - 1) / cols);
+        if (bn == 64 && tiles > g_max_clusters[1]) continue;
         const double epilogue = kEpilogue * bn / 256.;
         for (int splits = 1; splits <= 4; ++splits) {
             const int slots = g_max_clusters[splits - 1];
             if (splits > 1 && (tiles > slots || nk < 4 * splits)) continue;
             const int64_t waves = (tiles + slots - 1) / slots;
             const double steps = (nk + splits - 1) / splits * step_cost(bn);
-            const double cost = (double)waves * (std::max(steps, epilogue) + 1.) + epilogue + (splits > 1 ? kSwap : 0.);
+            const double cost = (double)waves * (std::max(steps, epilogue) + 1.) + epilogue +
+                                (splits > 1 ? swap_cost(bn, splits) : 0.);
             if (cost < best_cost) best_cost = cost, best = {bn, splits};
         }
     }
@@ -1225,15 +1232,9 @@ static moe_status_t product_few(const Mat& x, const Mat& w, Params p, cudaStream
 // Few rows go to k_dense_few, whose tile costs what the rows cost and which
 // splits K over more CTAs than the pair kernel.  Measured in graphs of 16
 // (us, k_dense_few / pairs): up to 64 rows nearly always (64 x 4,096 x 4,096 10.3 / 13.4);
-// up to 128 where K has steps to split (128 x 2,048 x 2,048 7.6 / 8.2, 128 x 7,168 x 7,168
-// 24.9 / 24.6, but 128 x 1,024 x 1,024 6.7 / 5.7); up to 384 where that also leaves
-// few tiles (384 x 2,000 x 608 7.8 / 9.1, 384 x 7,168 x 512 10.7 / 12.3, but 384 x 4,096 x 1,024 13.3 / 12.3).
-static bool few_rows(int64_t M, int64_t N, int64_t K) {
-    const int64_t nk = (K + TK - 1) / TK;
-    if (M <= 64) return true;
-    if (M <= few::ROWS) return nk > 16;
-    return M <= 384 && nk >= 24 && M * N < (1 << 18);
-}
+// up to 128 where K has steps to split (128 x 2,048 x 2,048 7.6 / 8.0, 128 x 4,096 x 1,024
+// 8.6 / 9.8, but 128 x 1,024 x 1,024 6.7 / 5.4); none above (256 x 4,096 x 1,024 10.8 / 9.9).
+static bool few_rows(int64_t M, int64_t K) { return M <= 64 || (M <= few::ROWS && K > 16 * TK); }
 
 static bool act_ok(int a) { return a >= MOE_ACT_NONE && a <= MOE_ACT_SILU; }
 // sizes the tensor maps and the tile counts hold
@@ -1275,7 +1276,7 @@ extern "C" moe_status_t linear_fwd(const void* x, int64_t ldx, const void* w, in
     p.err = err;
     const Mat mx{x, M, K, ldx}, mw{w, K, N, ldw};
     cudaStream_t s = (cudaStream_t)stream;
-    if (few_rows(M, N, K)) return product_few<true, EPI_LINEAR>(mx, mw, p, s);
+    if (few_rows(M, K)) return product_few<true, EPI_LINEAR>(mx, mw, p, s);
     if (!bias && !res && !z && act == MOE_ACT_NONE) return product<false, true, EPI_PLAIN, 0>(mx, mw, p, s);
     switch (act) {
         case MOE_ACT_RELU: return product<false, true, EPI_LINEAR, MOE_ACT_RELU>(mx, mw, p, s);
@@ -1290,7 +1291,7 @@ static moe_status_t input_grad(const void* dy, int64_t lddy, const void* w, int6
                                void* dx, int64_t lddx, int32_t* err, cudaStream_t s) {
     dense::Params p{};
     p.M = M, p.N = (int)K, p.K = N, p.act = MOE_ACT_NONE, p.y = dx, p.ldy = lddx, p.err = err;
-    if (few_rows(M, K, N)) return product_few<false, EPI_LINEAR>({dy, M, N, lddy}, {w, K, N, ldw}, p, s);
+    if (few_rows(M, N)) return product_few<false, EPI_LINEAR>({dy, M, N, lddy}, {w, K, N, ldw}, p, s);
     return product<false, false, EPI_PLAIN, 0>({dy, M, N, lddy}, {w, K, N, ldw}, p, s);
 }
 static moe_status_t weight_grad(const void* x, int64_t ldx, const void* dy, int64_t lddy, int64_t M, int N, int64_t K,
@@ -1376,7 +1377,7 @@ extern "C" moe_status_t gated_ffn_fwd(const void* x, int64_t ldx, const void* w1
     p.M = M, p.N = f, p.K = d, p.act = act, p.up = f;
     p.y = h, p.ldy = ldh, p.z = static_cast<__nv_bfloat16*>(a), p.ldz = lda;
     p.err = err;
-    if (few_rows(M, 2 * (int64_t)f, d))
+    if (few_rows(M, d))
         return product_few<true, EPI_GLU>({x, M, d, ldx}, {w1, d, 2 * (int64_t)f, ldw}, p, (cudaStream_t)stream);
     const Mat mx{x, M, d, ldx}, mw{w1, d, 2 * (int64_t)f, ldw};
     cudaStream_t s = (cudaStream_t)stream;
