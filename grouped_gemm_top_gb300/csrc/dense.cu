@@ -355,6 +355,243 @@ __device__ __forceinline__ void flush(const Params& p, const CUtensorMap* tmY, c
     bulk_commit_group();
 }
 
+// A CTA's place: in its pair, in the grid, in shared memory.
+struct Place {
+    uint8_t* smem;
+    uint32_t bar0, rank, lead;      // rank in the pair; the pair's leader in the cluster
+    int warp, lane, first, step;    // the pair's tiles: first, first + step, ..
+    volatile int* abort_flag;
+    __device__ __forceinline__ uint32_t full_bar(int s) const { return bar0 + 8u * s; }
+    __device__ __forceinline__ uint32_t empty_bar(int s) const { return bar0 + 8u * (MAX_STAGES + s); }
+    __device__ __forceinline__ uint32_t tfull_bar(int a) const { return bar0 + 8u * (2 * MAX_STAGES + a); }
+    __device__ __forceinline__ uint32_t tempty_bar(int a) const { return bar0 + 8u * (2 * MAX_STAGES + NACC + a); }
+    __device__ __forceinline__ uint32_t drain_bar() const { return bar0 + 8u * (2 * MAX_STAGES + 2 * NACC); }
+};
+// Where a role is in the ring of stages, or in that of accumulators.
+struct Ring {
+    int at = 0, count = 0;
+    uint32_t phase = 0;
+    bool aborted = false;
+    __device__ __forceinline__ void next(int n) {
+        ++count;
+        if (++at == n) {
+            at = 0;
+            phase ^= 1u;
+        }
+    }
+};
+
+// Barriers, TMEM; returns what the warps that use TMEM have to know of it.
+__device__ __forceinline__ uint32_t set_up(Place& pl, int splits, int stages) {
+    extern __shared__ uint8_t smem_raw[];
+    pl.smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+    pl.warp = __shfl_sync(0xFFFFFFFFu, (int)(threadIdx.x >> 5), 0), pl.lane = threadIdx.x & 31;
+    const uint32_t crank = cluster_ctarank();
+    pl.rank = crank & 1u, pl.lead = crank & ~1u;
+    pl.first = blockIdx.x / (2 * splits), pl.step = gridDim.x / (2 * splits);
+    pl.bar0 = smem_u32(pl.smem + OFF_BAR);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(pl.smem + OFF_MISC);
+    pl.abort_flag = reinterpret_cast<volatile int*>(pl.smem + OFF_MISC + 4);
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < stages; ++s) {
+            mbar_init(pl.full_bar(s), 1);
+            mbar_init(pl.empty_bar(s), 1);
+        }
+        for (int a = 0; a < NACC; ++a) {
+            mbar_init(pl.tfull_bar(a), 1);
+            mbar_init(pl.tempty_bar(a), 2 * EPI_WARPS);
+        }
+        mbar_init(pl.drain_bar(), 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        *pl.abort_flag = 0;
+    }
+    __syncthreads();
+    cluster_sync();      // the peer's barriers are initialised
+    // TMEM is for the MMA and epilogue warps to wait for; the producer loads
+    if (pl.warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
+                     "r"(TMEM_COLS));
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+        tc_fence_before();
+    }
+    if (pl.warp == 1 || pl.warp >= 4) {
+        asm volatile("bar.sync 1, %0;" ::"n"(32 + 32 * EPI_WARPS) : "memory");
+        tc_fence_after();
+    }
+    return pl.warp == 1 || pl.warp >= 4 ? *tmem_slot : 0u;
+}
+__device__ __forceinline__ void tear_down(const Place& pl, uint32_t tmem_base) {
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();      // both CTAs are done with TMEM and with each other's barriers
+    tc_fence_after();
+    if (pl.warp == 1) {
+        __syncwarp();
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(TMEM_COLS));
+    }
+}
+
+// The TMA warp: k-steps [k0, k1) of the product's tiles, which are tiles
+// [t0, t1) of the launch; t: the pair's next one.
+template <bool A_MN, bool B_MN, int EPI>
+__device__ __forceinline__ void load_tiles(const Place& pl, const Params& p, const CUtensorMap* tmA,
+                                           const CUtensorMap* tmB, int k0, int k1, int& t, int t0, int t1, Ring& r) {
+    const bool elected = elect_one();
+    const uint32_t lead_full = mapa(pl.full_bar(0), pl.lead);
+    // B: bn / 2 rows, or bn / 2 columns in boxes of 64
+    const int bh = p.bn / 2, b_boxes = (bh + 63) / 64;
+    const uint32_t bytes = HALF_BYTES + (B_MN ? 64 * b_boxes : bh) * TK * 2;
+    for (; t < t1 && !r.aborted; t += pl.step) {
+        const Tile ti = get_tile(p, t - t0);
+        const int am = ti.mt * TM + 128 * (int)pl.rank;
+        const int bn = EPI == EPI_GLU ? ti.nt * bh + p.up * (int)pl.rank : ti.nt * p.bn + bh * (int)pl.rank;
+        for (int ks = k0; ks < k1; ++ks) {
+            if (!mbar_wait_cluster(pl.empty_bar(r.at), r.phase ^ 1u, p, pl.abort_flag)) {
+                r.aborted = true;
+                break;
+            }
+            const int k = ks * TK;
+            // both CTAs' bytes complete on the leader's full barrier
+            const uint32_t fb = lead_full + 8u * r.at;
+            if (elected) {
+                if (pl.rank == 0) mbar_expect_tx(pl.full_bar(r.at), 2u * bytes);
+                const uint32_t sa = smem_u32(pl.smem + r.at * p.stage_bytes), sb = sa + HALF_BYTES;
+                if constexpr (A_MN) {
+                    tma2_load_2d(sa, tmA, am, k, fb);
+                    tma2_load_2d(sa + HALF_BYTES / 2, tmA, am + 64, k, fb);
+                } else {
+                    tma2_load_2d(sa, tmA, k, am, fb);
+                }
+                if constexpr (B_MN) {
+                    tma2_load_2d(sb, tmB, bn, k, fb);
+                    if (b_boxes > 1) tma2_load_2d(sb + HALF_BYTES / 2, tmB, bn + 64, k, fb);
+                } else {
+                    tma2_load_2d(sb, tmB, k, bn, fb);
+                }
+            }
+            r.next(p.stages);
+        }
+    }
+}
+// After an abort: wait (bounded) for the copies in flight.  The leader's full
+// barriers count both CTAs' bytes, and the follower leaves only after the
+// closing cluster barrier, i.e. after this.
+__device__ __forceinline__ void loads_end(const Place& pl, const Params& p, const Ring& r) {
+    __syncwarp();
+    if (!r.aborted || pl.rank != 0) return;
+    Params q = p;
+    q.timeout_ns = 200000000ull;
+    volatile int no_abort = 0;
+    for (int i = r.count - min(r.count, p.stages); i < r.count; ++i)
+        mbar_wait_cluster(pl.full_bar(i % p.stages), (uint32_t)(i / p.stages) & 1u, q, &no_abort);
+}
+
+// The MMA warp of the pair's leader.  The whole warp goes through the loop,
+// one elected lane issues: with warp-uniform control the descriptors stay in
+// uniform registers, and the loop has to be short -- a k-step's four products
+// take 512 cycles.  (`ring`: stages; `acc`: accumulators)
+template <bool A_MN, bool B_MN>
+__device__ __forceinline__ void multiply_tiles(const Place& pl, const Params& p, uint32_t tmem_base, int k0, int k1,
+                                               int& t, int t1, Ring& ring, Ring& acc) {
+    const bool elected = elect_one();
+    const uint32_t idesc = make_idesc_pair<A_MN, B_MN>(p.bn);
+    const uint64_t adesc0 = operand_desc<A_MN>(smem_u32(pl.smem));
+    const uint64_t bdesc0 = operand_desc<B_MN>(smem_u32(pl.smem) + HALF_BYTES);
+    const uint32_t stage_step = (uint32_t)p.stage_bytes >> 4;
+    for (; t < t1 && !ring.aborted; t += pl.step) {
+        if (!mbar_wait_cluster(pl.tempty_bar(acc.at), acc.phase ^ 1u, p, pl.abort_flag)) {
+            ring.aborted = true;
+            break;
+        }
+        tc_fence_after();
+        const uint32_t d_tmem = tmem_base + (uint32_t)(acc.at * ACC_COLS);
+        for (int ks = k0; ks < k1; ++ks) {
+            if (!mbar_wait(pl.full_bar(ring.at), ring.phase, p, pl.abort_flag)) {
+                ring.aborted = true;
+                break;
+            }
+            tc_fence_after();
+            if (elected) {
+                const uint64_t adesc = adesc0 + ring.at * stage_step, bdesc = bdesc0 + ring.at * stage_step;
+#pragma unroll
+                for (int kk = 0; kk < TK / 16; ++kk)
+                    tc_mma2_bf16(d_tmem, adesc + k16_step<A_MN>() * kk, bdesc + k16_step<B_MN>() * kk, idesc,
+                                 (ks != k0 || kk != 0) ? 1u : 0u);
+                tc_commit_pair(pl.empty_bar(ring.at), pl.lead);
+            }
+            ring.next(p.stages);
+        }
+        if (ring.aborted) break;
+        if (elected) tc_commit_pair(pl.tfull_bar(acc.at), pl.lead);
+        acc.next(NACC);
+    }
+}
+// wait (bounded) for the products issued
+__device__ __forceinline__ void products_end(const Place& pl, const Params& p, const Ring& ring) {
+    if (ring.count > 0) {
+        if (elect_one()) tc_commit_local2(pl.drain_bar());
+        Params q = p;
+        q.timeout_ns = 200000000ull;
+        volatile int no_abort = 0;
+        mbar_wait(pl.drain_bar(), 0, q, &no_abort);
+    }
+    __syncwarp();
+}
+
+// An epilogue warp (its 32 rows of the accumulator, its half of the columns);
+// the launch has `total` tiles.
+template <int EPI, int ACT>
+__device__ __forceinline__ void store_tiles(const Place& pl, const Params& p, const CUtensorMap* tmY,
+                                            const CUtensorMap* tmZ, const CUtensorMap* tmZ2, Out& out,
+                                            uint32_t lane_base, int& t, int t0, int t1, int total, Ring& acc) {
+    const int quarter = (pl.warp - 4) & 3, half = (pl.warp - 4) >> 2, lane = pl.lane;
+    // this warp's chunks of 32 columns: the first or the second half of them
+    const int chunks = EPI == EPI_GLU ? p.bn / 64 : p.bn / 32;
+    const int c0 = half == 0 ? 0 : (chunks + 1) / 2, c1 = half == 0 ? (chunks + 1) / 2 : chunks;
+    for (; t < t1 && !acc.aborted; t += pl.step) {
+        const Tile ti = get_tile(p, t - t0);
+        const int64_t row0 = (int64_t)ti.mt * TM + 128 * pl.rank + quarter * 32;
+        if (!mbar_wait_cluster(pl.tfull_bar(acc.at), acc.phase, p, pl.abort_flag)) {
+            acc.aborted = true;
+            break;
+        }
+        tc_fence_after();
+        if (t + pl.step >= total) out.last_tile();
+        const uint32_t tacc = lane_base + (uint32_t)(acc.at * ACC_COLS);
+        const int col0 = ti.nt * (EPI == EPI_GLU ? p.bn / 2 : p.bn);
+        uint32_t v[32], u[EPI == EPI_GLU ? 32 : 1];
+        tmem_ld32_issue(tacc + 32 * c0, v);
+        if constexpr (EPI == EPI_GLU) tmem_ld32_issue(tacc + p.bn / 2 + 32 * c0, u);
+        for (int c = c0; c < c1; ++c) {
+            float fv[32], fu[EPI == EPI_GLU ? 32 : 1];
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) fv[i] = __uint_as_float(v[i]);
+            if constexpr (EPI == EPI_GLU) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) fu[i] = __uint_as_float(u[i]);
+            }
+            if (c + 1 < c1) {      // the next chunk is on its way while this one is worked on
+                tmem_ld32_issue(tacc + 32 * (c + 1), v);
+                if constexpr (EPI == EPI_GLU) tmem_ld32_issue(tacc + p.bn / 2 + 32 * (c + 1), u);
+            } else if (!out.wide) {      // the accumulator is read: the next tile may have it
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_remote(mapa(pl.tempty_bar(acc.at), pl.lead));
+            }
+            const int col = col0 + 32 * c, n = p.N - col;
+            if (n > 0 && row0 < p.M)      // the whole warp
+                finish<EPI, ACT>(p, tmY, tmZ, tmZ2, out, row0, row0 + lane, col, n, fv, fu);
+        }
+        if (out.wide) flush<EPI>(p, tmY, tmZ, tmZ2, out, row0, col0, c0, c1, 1);
+        acc.next(NACC);
+    }
+}
+__device__ __forceinline__ void stores_end(int lane) {
+    if (lane == 0) bulk_wait_group0();      // the stores are complete
+    __syncwarp();
+}
+
 // tmY, tmZ, tmZ2: y (h), z (a's gate half) and a's up half as TMA stores see
 // them, boxes of 32 columns x 32 rows.
 template <bool A_MN, bool B_MN, int EPI, int ACT>
@@ -362,219 +599,33 @@ __global__ void __launch_bounds__(THREADS, 1)
     k_dense_pair(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                  const __grid_constant__ CUtensorMap tmY, const __grid_constant__ CUtensorMap tmZ,
                  const __grid_constant__ CUtensorMap tmZ2, const Params p) {
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
-    const int warp = __shfl_sync(0xFFFFFFFFu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
-    const uint32_t crank = cluster_ctarank();
-    const uint32_t rank = crank & 1u, lead = crank & ~1u;      // in the pair; the pair's leader in the cluster
-    const int part = (int)(crank >> 1);                        // of K
-    const bool leader = rank == 0;
-    const int first = blockIdx.x / (2 * p.splits), step = gridDim.x / (2 * p.splits);
-    const int total = p.m_tiles * p.n_tiles;
-    const int k0 = p.nk / p.splits * part + min(part, p.nk % p.splits);
-    const int k1 = k0 + p.nk / p.splits + (part < p.nk % p.splits);
-
-    const uint32_t bar0 = smem_u32(smem + OFF_BAR);
-    auto full_bar = [&](int s) { return bar0 + 8u * s; };
-    auto empty_bar = [&](int s) { return bar0 + 8u * (MAX_STAGES + s); };
-    auto tfull_bar = [&](int a) { return bar0 + 8u * (2 * MAX_STAGES + a); };
-    auto tempty_bar = [&](int a) { return bar0 + 8u * (2 * MAX_STAGES + NACC + a); };
-    const uint32_t drain_bar = bar0 + 8u * (2 * MAX_STAGES + 2 * NACC);
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + OFF_MISC);
-    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + OFF_MISC + 4);
-
-    if (threadIdx.x == 0) {
-        for (int s = 0; s < p.stages; ++s) {
-            mbar_init(full_bar(s), 1);
-            mbar_init(empty_bar(s), 1);
-        }
-        for (int a = 0; a < NACC; ++a) {
-            mbar_init(tfull_bar(a), 1);
-            mbar_init(tempty_bar(a), 2 * EPI_WARPS);
-        }
-        mbar_init(drain_bar, 1);
-        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-        *abort_flag = 0;
-    } else if (threadIdx.x == 64) {
+    if (threadIdx.x == 64) {
         prefetch_map(&tmA);
         prefetch_map(&tmB);
         prefetch_map(&tmY);
     }
-    __syncthreads();
-    cluster_sync();      // the peer's barriers are initialised
-    // TMEM is for the MMA and epilogue warps to wait for; the producer loads
-    if (warp == 1) {
-        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
-                     "r"(TMEM_COLS));
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
-        tc_fence_before();
-    }
-    if (warp == 1 || warp >= 4) {
-        asm volatile("bar.sync 1, %0;" ::"n"(32 + 32 * EPI_WARPS) : "memory");
-        tc_fence_after();
-    }
-    const uint32_t tmem_base = warp == 1 || warp >= 4 ? *tmem_slot : 0u;
+    Place pl;
+    const uint32_t tmem_base = set_up(pl, p.splits, p.stages);
+    const int part = (int)(pl.lead >> 1);      // of K
+    const int k0 = p.nk / p.splits * part + min(part, p.nk % p.splits);
+    const int k1 = k0 + p.nk / p.splits + (part < p.nk % p.splits);
     wait_for_previous_kernels();
 
-    const int ew = warp - 4;                       // epilogue warps: their rows and their half of the columns
-    const int quarter = ew & 3, half = ew >> 2;
+    const int total = p.m_tiles * p.n_tiles;
+    const int warp = pl.warp, lane = pl.lane, ew = warp - 4, quarter = ew & 3, half = ew >> 2;
     const uint32_t lane_base = tmem_base + ((uint32_t)(quarter * 32) << 16);
-    Out out{smem_u32(smem + OFF_EPI + ew * EPI_STAGE), smem_u32(smem + ew * 16384), lane, 0u, false};
-
+    Out out{smem_u32(pl.smem + OFF_EPI + ew * EPI_STAGE), smem_u32(pl.smem + ew * 16384), lane, 0u, false};
+    int t = pl.first;
+    Ring ring, acc;
     if (warp == 0) {
-        // ------------------------------------------------ TMA producer ----
-        const bool elected = elect_one();
-        const uint32_t lead_full = mapa(full_bar(0), lead);
-        int stage = 0, issued = 0;
-        uint32_t phase = 0;
-        bool aborted = false;
-        // B: bn / 2 rows, or bn / 2 columns in boxes of 64
-        const int bh = p.bn / 2, b_boxes = (bh + 63) / 64;
-        for (int t = first; t < total && !aborted; t += step) {
-            const Tile ti = get_tile(p, t);
-            const int am = ti.mt * TM + 128 * (int)rank;
-            const int bn = EPI == EPI_GLU ? ti.nt * bh + p.up * (int)rank : ti.nt * p.bn + bh * (int)rank;
-            for (int ks = k0; ks < k1; ++ks) {
-                if (!mbar_wait_cluster(empty_bar(stage), phase ^ 1u, p, abort_flag)) {
-                    aborted = true;
-                    break;
-                }
-                const int k = ks * TK;
-                // both CTAs' bytes complete on the leader's full barrier
-                const uint32_t fb = lead_full + 8u * stage;
-                if (elected) {
-                    if (leader) mbar_expect_tx(full_bar(stage), 2u * (uint32_t)p.stage_bytes);
-                    const uint32_t sa = smem_u32(smem + stage * p.stage_bytes), sb = sa + HALF_BYTES;
-                    if constexpr (A_MN) {
-                        tma2_load_2d(sa, &tmA, am, k, fb);
-                        tma2_load_2d(sa + HALF_BYTES / 2, &tmA, am + 64, k, fb);
-                    } else {
-                        tma2_load_2d(sa, &tmA, k, am, fb);
-                    }
-                    if constexpr (B_MN) {
-                        tma2_load_2d(sb, &tmB, bn, k, fb);
-                        if (b_boxes > 1) tma2_load_2d(sb + HALF_BYTES / 2, &tmB, bn + 64, k, fb);
-                    } else {
-                        tma2_load_2d(sb, &tmB, k, bn, fb);
-                    }
-                }
-                ++issued;
-                if (++stage == p.stages) {
-                    stage = 0;
-                    phase ^= 1u;
-                }
-            }
-        }
-        __syncwarp();
-        if (aborted && leader) {
-            // wait (bounded) for the copies in flight: the leader's full
-            // barriers count both CTAs' bytes, and the follower leaves only
-            // after the closing cluster barrier, i.e. after this
-            Params q = p;
-            q.timeout_ns = 200000000ull;
-            volatile int no_abort = 0;
-            for (int i = issued - min(issued, p.stages); i < issued; ++i)
-                mbar_wait_cluster(full_bar(i % p.stages), (uint32_t)(i / p.stages) & 1u, q, &no_abort);
-        }
-    } else if (warp == 1 && leader) {
-        // ---------------------------------------- MMA issuer (leader) ----
-        // The whole warp goes through the loop, one elected lane issues: with
-        // warp-uniform control the descriptors stay in uniform registers, and the
-        // loop has to be short -- a k-step's four products take 512 cycles.
-        const bool elected = elect_one();
-        int stage = 0, acc = 0;
-        uint32_t phase = 0, acc_phase = 0;
-        bool aborted = false, issued = false;
-        const uint32_t idesc = make_idesc_pair<A_MN, B_MN>(p.bn);
-        const uint64_t adesc0 = operand_desc<A_MN>(smem_u32(smem));
-        const uint64_t bdesc0 = operand_desc<B_MN>(smem_u32(smem) + HALF_BYTES);
-        const uint32_t stage_step = (uint32_t)p.stage_bytes >> 4;
-        for (int t = first; t < total && !aborted; t += step) {
-            if (!mbar_wait_cluster(tempty_bar(acc), acc_phase ^ 1u, p, abort_flag)) break;
-            tc_fence_after();
-            const uint32_t d_tmem = tmem_base + (uint32_t)(acc * ACC_COLS);
-            for (int ks = k0; ks < k1; ++ks) {
-                if (!mbar_wait(full_bar(stage), phase, p, abort_flag)) {
-                    aborted = true;
-                    break;
-                }
-                tc_fence_after();
-                if (elected) {
-                    const uint64_t adesc = adesc0 + stage * stage_step, bdesc = bdesc0 + stage * stage_step;
-#pragma unroll
-                    for (int kk = 0; kk < TK / 16; ++kk)
-                        tc_mma2_bf16(d_tmem, adesc + k16_step<A_MN>() * kk, bdesc + k16_step<B_MN>() * kk, idesc,
-                                     (ks != k0 || kk != 0) ? 1u : 0u);
-                    tc_commit_pair(empty_bar(stage), lead);
-                }
-                issued = true;
-                if (++stage == p.stages) {
-                    stage = 0;
-                    phase ^= 1u;
-                }
-            }
-            if (aborted) break;
-            if (elected) tc_commit_pair(tfull_bar(acc), lead);
-            if (++acc == NACC) {
-                acc = 0;
-                acc_phase ^= 1u;
-            }
-        }
-        if (issued) {
-            if (elected) tc_commit_local2(drain_bar);
-            Params q = p;
-            q.timeout_ns = 200000000ull;
-            volatile int no_abort = 0;
-            mbar_wait(drain_bar, 0, q, &no_abort);
-        }
-        __syncwarp();
+        load_tiles<A_MN, B_MN, EPI>(pl, p, &tmA, &tmB, k0, k1, t, 0, total, ring);
+        loads_end(pl, p, ring);
+    } else if (warp == 1 && pl.rank == 0) {
+        multiply_tiles<A_MN, B_MN>(pl, p, tmem_base, k0, k1, t, total, ring, acc);
+        products_end(pl, p, ring);
     } else if (warp >= 4 && p.splits == 1) {
-        // ----------------------------------------------------- epilogue ----
-        int acc = 0;
-        uint32_t acc_phase = 0;
-        // this warp's chunks of 32 columns: the first or the second half of them
-        const int chunks = EPI == EPI_GLU ? p.bn / 64 : p.bn / 32;
-        const int c0 = half == 0 ? 0 : (chunks + 1) / 2, c1 = half == 0 ? (chunks + 1) / 2 : chunks;
-        for (int t = first; t < total; t += step) {
-            const Tile ti = get_tile(p, t);
-            const int64_t row0 = (int64_t)ti.mt * TM + 128 * rank + quarter * 32;
-            if (!mbar_wait_cluster(tfull_bar(acc), acc_phase, p, abort_flag)) break;
-            tc_fence_after();
-            if (t + step >= total) out.last_tile();
-            const uint32_t tacc = lane_base + (uint32_t)(acc * ACC_COLS);
-            const int col0 = ti.nt * (EPI == EPI_GLU ? p.bn / 2 : p.bn);
-            uint32_t v[32], u[EPI == EPI_GLU ? 32 : 1];
-            tmem_ld32_issue(tacc + 32 * c0, v);
-            if constexpr (EPI == EPI_GLU) tmem_ld32_issue(tacc + p.bn / 2 + 32 * c0, u);
-            for (int c = c0; c < c1; ++c) {
-                float fv[32], fu[EPI == EPI_GLU ? 32 : 1];
-                tmem_wait_ld();
-#pragma unroll
-                for (int i = 0; i < 32; ++i) fv[i] = __uint_as_float(v[i]);
-                if constexpr (EPI == EPI_GLU) {
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) fu[i] = __uint_as_float(u[i]);
-                }
-                if (c + 1 < c1) {      // the next chunk is on its way while this one is worked on
-                    tmem_ld32_issue(tacc + 32 * (c + 1), v);
-                    if constexpr (EPI == EPI_GLU) tmem_ld32_issue(tacc + p.bn / 2 + 32 * (c + 1), u);
-                } else if (!out.wide) {      // the accumulator is read: the next tile may have it
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive_remote(mapa(tempty_bar(acc), lead));
-                }
-                const int col = col0 + 32 * c, n = p.N - col;
-                if (n > 0 && row0 < p.M)      // the whole warp
-                    finish<EPI, ACT>(p, &tmY, &tmZ, &tmZ2, out, row0, row0 + lane, col, n, fv, fu);
-            }
-            if (out.wide) flush<EPI>(p, &tmY, &tmZ, &tmZ2, out, row0, col0, c0, c1, 1);
-            if (++acc == NACC) {
-                acc = 0;
-                acc_phase ^= 1u;
-            }
-        }
-        if (lane == 0) bulk_wait_group0();      // the stores are complete
-        __syncwarp();
+        store_tiles<EPI, ACT>(pl, p, &tmY, &tmZ, &tmZ2, out, lane_base, t, 0, total, total, acc);
+        stores_end(lane);
     }
     if (p.splits > 1) {
         // ------------------------- one tile per cluster: swap and add up ----
@@ -583,12 +634,12 @@ __global__ void __launch_bounds__(THREADS, 1)
         constexpr int CPU = EPI == EPI_GLU ? 2 : 1;      // chunks per unit
         const int units = EPI == EPI_GLU ? p.bn / 64 : p.bn / 32, own = (units + p.splits - 1) / p.splits;
         const int u0 = part * own, u1 = min(u0 + own, units);
-        const uint32_t buf = smem_u32(smem);
+        const uint32_t buf = smem_u32(pl.smem);
         const int r = quarter * 32 + lane;
         bool ok = true;
         __syncwarp();
         if (warp >= 4) {
-            ok = mbar_wait_cluster(tfull_bar(0), 0, p, abort_flag);
+            ok = mbar_wait_cluster(pl.tfull_bar(0), 0, p, pl.abort_flag);
             tc_fence_after();
         }
         cluster_sync();      // every part's products are done: its stages are free to write to
@@ -603,7 +654,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     tmem_ld32(lane_base + (uint32_t)(32 * un + (c == 0 ? 0 : p.bn / 2)), v);
                     const int chunk = (slot * own + un - to * own) * CPU + c;
                     const uint32_t at = buf + (uint32_t)(chunk * PART_BYTES + r * PART_ROW);
-                    const uint32_t dst = mapa(at, (uint32_t)(2 * to) + rank);
+                    const uint32_t dst = mapa(at, (uint32_t)(2 * to) + pl.rank);
 #pragma unroll
                     for (int i = 0; i < 8; ++i) st_cluster_v4(dst + 16u * i, v + 4 * i);
                 }
@@ -611,11 +662,11 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
         cluster_sync();      // every part has what it adds up
         if (warp >= 4 && ok) {
-            const Tile ti = get_tile(p, first);
-            const int64_t row0 = (int64_t)ti.mt * TM + 128 * rank + quarter * 32;
+            const Tile ti = get_tile(p, pl.first);
+            const int64_t row0 = (int64_t)ti.mt * TM + 128 * pl.rank + quarter * 32;
             const int col0 = ti.nt * (EPI == EPI_GLU ? p.bn / 2 : p.bn);
             // boxes above the partial chunks: at most 3 of 2 KB (4 KB) a unit, four units a warp
-            out.last = smem_u32(smem + SMEM_TILES - (ew + 1) * 8192);
+            out.last = smem_u32(pl.smem + SMEM_TILES - (ew + 1) * 8192);
             out.last_tile();
             for (int un = u0 + half; un < u1; un += 2) {
                 float s[2][32];
@@ -633,7 +684,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                         }
                         const int slot = j < part ? j : j - 1;
                         const float4* q = reinterpret_cast<const float4*>(
-                            smem + ((slot * own + un - u0) * CPU + c) * PART_BYTES + r * PART_ROW);
+                            pl.smem + ((slot * own + un - u0) * CPU + c) * PART_BYTES + r * PART_ROW);
 #pragma unroll
                         for (int i = 0; i < 8; ++i) {
                             const float4 x = q[i];
@@ -651,14 +702,49 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
     }
 
-    tc_fence_before();
-    __syncthreads();
-    cluster_sync();      // both CTAs are done with TMEM and with each other's barriers
-    tc_fence_after();
-    if (warp == 1) {
-        __syncwarp();
-        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(TMEM_COLS));
+    tear_down(pl, tmem_base);
+}
+
+// The two products of a backward pass, dx = dz W^T (p) and dW = x^T dz (q), as
+// the tiles of one launch.  One set-up and one last wave instead of two (us,
+// in two launches): 512 x 512 x 512 4.4 (8.3), 1,024 x 1,024 x 1,024 6.9 (11.8), 1,839 x
+// 314 x 3,013 10.9 (19.2), 2,048 x 2,048 x 2,048 23.3 (28.8), 4,096 x 4,096 x 4,096 140 (149).
+template <int EPI_W>
+__global__ void __launch_bounds__(THREADS, 1)
+    k_dense_both(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                 const __grid_constant__ CUtensorMap tmY, const __grid_constant__ CUtensorMap tmA2,
+                 const __grid_constant__ CUtensorMap tmB2, const __grid_constant__ CUtensorMap tmY2, const Params p,
+                 const Params q) {
+    if (threadIdx.x == 64) {
+        prefetch_map(&tmA);
+        prefetch_map(&tmB);
+        prefetch_map(&tmA2);
+        prefetch_map(&tmB2);
     }
+    Place pl;
+    const uint32_t tmem_base = set_up(pl, 1, p.stages);
+    wait_for_previous_kernels();
+
+    const int mid = p.m_tiles * p.n_tiles, total = mid + q.m_tiles * q.n_tiles;
+    const int ew = pl.warp - 4;
+    const uint32_t lane_base = tmem_base + ((uint32_t)((ew & 3) * 32) << 16);
+    int t = pl.first;
+    Ring ring, acc;
+    if (pl.warp == 0) {
+        load_tiles<false, false, EPI_PLAIN>(pl, p, &tmA, &tmB, 0, p.nk, t, 0, mid, ring);
+        load_tiles<true, true, EPI_W>(pl, q, &tmA2, &tmB2, 0, q.nk, t, mid, total, ring);
+        loads_end(pl, p, ring);
+    } else if (pl.warp == 1 && pl.rank == 0) {
+        multiply_tiles<false, false>(pl, p, tmem_base, 0, p.nk, t, mid, ring, acc);
+        multiply_tiles<true, true>(pl, q, tmem_base, 0, q.nk, t, total, ring, acc);
+        products_end(pl, p, ring);
+    } else if (pl.warp >= 4) {
+        Out out{smem_u32(pl.smem + OFF_EPI + ew * EPI_STAGE), smem_u32(pl.smem + ew * 16384), pl.lane, 0u, false};
+        store_tiles<EPI_PLAIN, 0>(pl, p, &tmY, &tmY, &tmY, out, lane_base, t, 0, mid, total, acc);
+        store_tiles<EPI_W, 0>(pl, q, &tmY2, &tmY2, &tmY2, out, lane_base, t, mid, total, total, acc);
+        stores_end(pl.lane);
+    }
+    tear_down(pl, tmem_base);
 }
 
 // ------------------------------------------------------- few rows ----
@@ -1082,6 +1168,10 @@ static cudaError_t set_attributes() {
     }
     MOE_DENSE_INSTANCES(X)
 #undef X
+    for (const void* k : {(const void*)k_dense_both<EPI_PLAIN>, (const void*)k_dense_both<EPI_F32>}) {
+        const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
+        if (e != cudaSuccess) return e;
+    }
     const void* ks[] = {(const void*)few::k_dense_few<true, EPI_LINEAR>, (const void*)few::k_dense_few<true, EPI_GLU>,
                         (const void*)few::k_dense_few<false, EPI_LINEAR>};
     for (const void* k : ks) {
@@ -1118,33 +1208,76 @@ struct Mat {
 // parts, 38.3 with 256; 512 x 2,000 x 608: 8.7 with 64 columns, 7.7 in two parts).
 struct Choice {
     int bn, splits;
+    double cost;
 };
 static double step_cost(int bn) { return bn == 256 ? 1.0 : (bn == 224 ? 0.91 : (bn == 192 ? 0.80 : 0.56)); }
 // 1.5 to 2 us for 64 columns in two parts, 2.7 for 128, 4.3 for 256; 6 for 256 in three, 3.5 for 64 in four
 static double swap_cost(int bn, int splits) { return (4. + 12. * bn / 256.) * (1. + 0.4 * (splits - 2)); }
+constexpr double kEpilogue = 5. / 256.;      // a column
+constexpr int kWidths[] = {256, 224, 192, 128, 64};
+static double tile_cost(int nk, int bn) { return std::max(nk * step_cost(bn), kEpilogue * bn) + 1.; }
 static Choice choose(int64_t m_tiles, int N, int nk, bool glu) {
-    constexpr double kEpilogue = 5.;
-    static const int widths[] = {256, 224, 192, 128, 64};
-    Choice best{256, 1};
-    double best_cost = 1e300;
-    for (int bn : widths) {
+    Choice best{256, 1, 1e300};
+    for (int bn : kWidths) {
         // gate and up in whole chunks of 32, one at least for each half of the epilogue's warps
         if (glu && (bn == 224 || bn == 64)) continue;
         const int cols = glu ? bn / 2 : bn;
         const int64_t tiles = m_tiles * ((N + cols - 1) / cols);
         if (bn == 64 && tiles > g_max_clusters[1]) continue;
-        const double epilogue = kEpilogue * bn / 256.;
         for (int splits = 1; splits <= 4; ++splits) {
             const int slots = g_max_clusters[splits - 1];
             if (splits > 1 && (tiles > slots || nk < 4 * splits)) continue;
             const int64_t waves = (tiles + slots - 1) / slots;
-            const double steps = (nk + splits - 1) / splits * step_cost(bn);
-            const double cost = (double)waves * (std::max(steps, epilogue) + 1.) + epilogue +
+            const double cost = (double)waves * tile_cost((nk + splits - 1) / splits, bn) + kEpilogue * bn +
                                 (splits > 1 ? swap_cost(bn, splits) : 0.);
-            if (cost < best_cost) best_cost = cost, best = {bn, splits};
+            if (cost < best.cost) best = {bn, splits, cost};
         }
     }
     return best;
+}
+// Both products of a backward pass in one launch (k_dense_both): the
+// longest share of its tiles, nk steps each (p) or nk2 (q).  Two launches
+// instead where they split K and come out shorter by more than the second
+// set-up (8 steps: with 3 instead, 2,048 x 1,024 x 4,096 27.6 us instead of 24.0), and
+// where the work is long and a set-up does not count (8,192 x 4,096 x 7,168 with
+// SiLU: 566 us, in one launch 577; 4,096 x 1,024 x 14,336 still 148, in one 131).
+constexpr double kBothSaves = 8., kBothMax = 1000.;
+static Choice choose_both(int64_t m_tiles, int N, int nk, int64_t m_tiles2, int N2, int nk2) {
+    const int64_t slots = g_max_clusters[0];
+    Choice best{256, 1, 1e300};
+    for (int bn : kWidths) {
+        const int64_t mid = m_tiles * ((N + bn - 1) / bn), total = mid + m_tiles2 * ((N2 + bn - 1) / bn);
+        if (bn == 64 && total > g_max_clusters[1]) continue;
+        double cost = 0.;
+        for (int64_t i : {(int64_t)0, mid % slots, total % slots}) {      // the shares change there
+            const int64_t n = (std::max<int64_t>(mid - i, 0) + slots - 1) / slots;
+            const int64_t all = (std::max<int64_t>(total - i, 0) + slots - 1) / slots;
+            cost = std::max(cost, n * tile_cost(nk, bn) + (all - n) * tile_cost(nk2, bn));
+        }
+        cost += kEpilogue * bn;
+        if (cost < best.cost) best = {bn, 1, cost};
+    }
+    return best;
+}
+
+// The fields of p that the tile width decides; the maps of a product's operands and of y.
+static void set_width(Params& p, int bn, int stage_bytes, bool glu) {
+    p.bn = bn;
+    p.stage_bytes = stage_bytes;
+    p.stages = std::min(MAX_STAGES, SMEM_TILES / stage_bytes);
+    const int cols = glu ? bn / 2 : bn;      // of D per tile
+    p.n_tiles = (p.N + cols - 1) / cols;
+    p.band = 8;
+    p.timeout_ns = 2000000000ull;
+}
+static int stage_size(bool b_mn, int bn) { return HALF_BYTES + (b_mn ? (bn / 2 + 63) / 64 * 64 : bn / 2) * TK * 2; }
+static int boxed(int N) { return std::max(N & ~7, 8); }      // finish(): N < 8 sends no box
+template <bool A_MN, bool B_MN, int EPI>
+static bool make_maps(CUtensorMap* tmA, CUtensorMap* tmB, CUtensorMap* tmY, const Mat& a, const Mat& b,
+                      const Params& p) {
+    return make_bf16_map(tmA, a.p, a.rows, a.cols, a.ld, A_MN ? TK : 128) &&
+           make_bf16_map(tmB, b.p, b.rows, b.cols, b.ld, B_MN ? TK : p.bn / 2) &&
+           make_store_map(tmY, p.y, p.M, boxed(p.N), p.ldy, EPI == EPI_F32);
 }
 
 template <bool A_MN, bool B_MN, int EPI, int ACT>
@@ -1153,23 +1286,13 @@ static moe_status_t product(const Mat& a, const Mat& b, Params p, cudaStream_t s
     p.m_tiles = (int)((p.M + TM - 1) / TM);
     p.nk = (int)((p.K + TK - 1) / TK);
     const Choice c = choose(p.m_tiles, p.N, p.nk, EPI == EPI_GLU);
-    p.bn = c.bn;
     p.splits = c.splits;
-    p.stage_bytes = HALF_BYTES + (B_MN ? (p.bn / 2 + 63) / 64 * 64 : p.bn / 2) * TK * 2;
-    p.stages = std::min(MAX_STAGES, SMEM_TILES / p.stage_bytes);
-    const int cols = EPI == EPI_GLU ? p.bn / 2 : p.bn;      // of D per tile
-    p.n_tiles = (p.N + cols - 1) / cols;
-    p.band = 8;
-    p.timeout_ns = 2000000000ull;
+    set_width(p, c.bn, stage_size(B_MN, c.bn), EPI == EPI_GLU);
     CUtensorMap tmA, tmB, tmY, tmZ, tmZ2;
-    const int boxed = std::max(p.N & ~7, 8);      // finish(): N < 8 sends no box
-    MOE_REQUIRE(make_bf16_map(&tmA, a.p, a.rows, a.cols, a.ld, A_MN ? TK : 128) &&
-                    make_bf16_map(&tmB, b.p, b.rows, b.cols, b.ld, B_MN ? TK : p.bn / 2) &&
-                    make_store_map(&tmY, p.y, p.M, boxed, p.ldy, EPI == EPI_F32),
-                MOE_ERR_CUDA);
+    MOE_REQUIRE((make_maps<A_MN, B_MN, EPI>(&tmA, &tmB, &tmY, a, b, p)), MOE_ERR_CUDA);
     tmZ = tmZ2 = tmY;
     if (p.z != nullptr)
-        MOE_REQUIRE(make_store_map(&tmZ, p.z, p.M, boxed, p.ldz, false) &&
+        MOE_REQUIRE(make_store_map(&tmZ, p.z, p.M, boxed(p.N), p.ldz, false) &&
                         (EPI != EPI_GLU || make_store_map(&tmZ2, p.z + p.N, p.M, p.N, p.ldz, false)),
                     MOE_ERR_CUDA);
     const int64_t tiles = (int64_t)p.m_tiles * p.n_tiles;
@@ -1178,6 +1301,28 @@ static moe_status_t product(const Mat& a, const Mat& b, Params p, cudaStream_t s
     cudaLaunchAttribute attr[2];
     cudaLaunchConfig_t cfg = launch_cfg(clusters, p.splits, s, attr);
     if (cudaLaunchKernelEx(&cfg, k_dense_pair<A_MN, B_MN, EPI, ACT>, tmA, tmB, tmY, tmZ, tmZ2, p) != cudaSuccess)
+        return MOE_ERR_CUDA;
+    MOE_CHECK_LAUNCH();
+    return MOE_OK;
+}
+
+// dx = dz W^T (p) and dW = x^T dz (q) in one launch
+template <int EPI_W>
+static moe_status_t product_both(const Mat& x, const Mat& w, const Mat& dz, Params p, Params q, int bn,
+                                 cudaStream_t s) {
+    const int bytes = std::max(stage_size(false, bn), stage_size(true, bn));
+    set_width(p, bn, bytes, false);
+    set_width(q, bn, bytes, false);
+    p.splits = q.splits = 1;
+    CUtensorMap tmA, tmB, tmY, tmA2, tmB2, tmY2;
+    MOE_REQUIRE((make_maps<false, false, EPI_PLAIN>(&tmA, &tmB, &tmY, dz, w, p)) &&
+                    (make_maps<true, true, EPI_W>(&tmA2, &tmB2, &tmY2, x, dz, q)),
+                MOE_ERR_CUDA);
+    const int64_t tiles = (int64_t)p.m_tiles * p.n_tiles + (int64_t)q.m_tiles * q.n_tiles;
+    MOE_REQUIRE(tiles <= 0x3FFFFFFF, MOE_ERR_UNSUPPORTED);
+    cudaLaunchAttribute attr[2];
+    cudaLaunchConfig_t cfg = launch_cfg((int)std::min<int64_t>(tiles, g_max_clusters[0]), 1, s, attr);
+    if (cudaLaunchKernelEx(&cfg, k_dense_both<EPI_W>, tmA, tmB, tmY, tmA2, tmB2, tmY2, p, q) != cudaSuccess)
         return MOE_ERR_CUDA;
     MOE_CHECK_LAUNCH();
     return MOE_OK;
@@ -1286,24 +1431,36 @@ extern "C" moe_status_t linear_fwd(const void* x, int64_t ldx, const void* w, in
     }
 }
 
-// D[M, N] = dy W^T and D = x^T dy with plain stores
-static moe_status_t input_grad(const void* dy, int64_t lddy, const void* w, int64_t ldw, int64_t M, int N, int64_t K,
-                               void* dx, int64_t lddx, int32_t* err, cudaStream_t s) {
-    dense::Params p{};
+// dx[M, K] = dz W^T and dw[K, N] = x^T dz, each if asked for
+static moe_status_t gradients(const void* dz, int64_t lddz, const void* x, int64_t ldx, const void* w, int64_t ldw,
+                              int64_t M, int N, int64_t K, void* dx, int64_t lddx, void* dw, int dw_type,
+                              int64_t lddw, int32_t* err, cudaStream_t s) {
+    const bool f32 = dw_type == MOE_TYPE_F32;
+    if (M == 0)
+        return dw && cudaMemset2DAsync(dw, lddw * (f32 ? 4 : 2), 0, (size_t)N * (f32 ? 4 : 2), K, s) != cudaSuccess
+                   ? MOE_ERR_CUDA : MOE_OK;
+    const Mat mz{dz, M, N, lddz}, mx{x, M, K, ldx}, mw{w, K, N, ldw};
+    dense::Params p{}, q{};
     p.M = M, p.N = (int)K, p.K = N, p.act = MOE_ACT_NONE, p.y = dx, p.ldy = lddx, p.err = err;
-    if (few_rows(M, N)) return product_few<false, EPI_LINEAR>({dy, M, N, lddy}, {w, K, N, ldw}, p, s);
-    return product<false, false, EPI_PLAIN, 0>({dy, M, N, lddy}, {w, K, N, ldw}, p, s);
-}
-static moe_status_t weight_grad(const void* x, int64_t ldx, const void* dy, int64_t lddy, int64_t M, int N, int64_t K,
-                                void* dw, int dw_type, int64_t lddw, int32_t* err, cudaStream_t s) {
-    if (M == 0) {
-        const size_t e = dw_type == MOE_TYPE_F32 ? 4 : 2;
-        return cudaMemset2DAsync(dw, lddw * e, 0, N * e, K, s) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+    q.M = K, q.N = N, q.K = M, q.act = MOE_ACT_NONE, q.y = dw, q.ldy = lddw, q.err = err;
+    const bool few = few_rows(M, N);
+    if (dx && dw && !few) {
+        MOE_REQUIRE(g_max_clusters[0] > 0, MOE_ERR_NOT_INITIALIZED);
+        p.m_tiles = (int)((M + TM - 1) / TM), p.nk = (N + TK - 1) / TK;
+        q.m_tiles = (int)((K + TM - 1) / TM), q.nk = (int)((M + TK - 1) / TK);
+        const Choice c = choose_both(p.m_tiles, p.N, p.nk, q.m_tiles, q.N, q.nk);
+        const double two = choose(p.m_tiles, p.N, p.nk, false).cost + choose(q.m_tiles, q.N, q.nk, false).cost;
+        if (c.cost <= kBothMax && c.cost <= two + kBothSaves)
+            return f32 ? product_both<EPI_F32>(mx, mw, mz, p, q, c.bn, s)
+                       : product_both<EPI_PLAIN>(mx, mw, mz, p, q, c.bn, s);
     }
-    dense::Params p{};
-    p.M = K, p.N = N, p.K = M, p.act = MOE_ACT_NONE, p.y = dw, p.ldy = lddw, p.err = err;
-    if (dw_type == MOE_TYPE_F32) return product<true, true, EPI_F32, 0>({x, M, K, ldx}, {dy, M, N, lddy}, p, s);
-    return product<true, true, EPI_PLAIN, 0>({x, M, K, ldx}, {dy, M, N, lddy}, p, s);
+    if (dx) {
+        const moe_status_t st = few ? product_few<false, EPI_LINEAR>(mz, mw, p, s)
+                                    : product<false, false, EPI_PLAIN, 0>(mz, mw, p, s);
+        if (st != MOE_OK) return st;
+    }
+    if (!dw) return MOE_OK;
+    return f32 ? product<true, true, EPI_F32, 0>(mx, mz, q, s) : product<true, true, EPI_PLAIN, 0>(mx, mz, q, s);
 }
 
 static size_t dz_bytes(int64_t M, int N) { return ((size_t)M * ((N + 7) / 8 * 8) * 2 + 255) / 256 * 256; }
@@ -1355,12 +1512,7 @@ extern "C" moe_status_t linear_bwd(const void* dy, int64_t lddy, const void* x, 
         launch_column_sum(part, M > 0 ? act_parts(M) : 0, N, dbias, s);
         MOE_CHECK_LAUNCH();
     }
-    if (dx && M > 0) {
-        const moe_status_t st = input_grad(g, ldg, w, ldw, M, N, K, dx, lddx, err, s);
-        if (st != MOE_OK) return st;
-    }
-    if (dw) return weight_grad(x, ldx, g, ldg, M, N, K, dw, dw_type, lddw, err, s);
-    return MOE_OK;
+    return gradients(g, ldg, x, ldx, w, ldw, M, N, K, dx, lddx, dw, dw_type, lddw, err, s);
 }
 
 extern "C" moe_status_t gated_ffn_fwd(const void* x, int64_t ldx, const void* w1, int64_t ldw, int act, int64_t M,
@@ -1416,10 +1568,5 @@ extern "C" moe_status_t gated_ffn_bwd(const void* dh, int64_t lddh, const void* 
                          act, static_cast<__nv_bfloat16*>(da), ldda) != cudaSuccess)
             return MOE_ERR_CUDA;
     }
-    if (dx && M > 0) {
-        const moe_status_t st = input_grad(da, ldda, w1, ldw, M, 2 * f, d, dx, lddx, err, s);
-        if (st != MOE_OK) return st;
-    }
-    if (dw1) return weight_grad(x, ldx, da, ldda, M, 2 * f, d, dw1, dw_type, lddw, err, s);
-    return MOE_OK;
+    return gradients(da, ldda, x, ldx, w1, ldw, M, 2 * f, d, dx, lddx, dw1, dw_type, lddw, err, s);
 }

@@ -117,6 +117,19 @@ def test_linear_backward(ops, m, n, k, act, dw_dtype):
     assert torch.equal(dx, again[0]) and torch.equal(dw, again[1]) and torch.equal(db, again[2])
 
 
+@pytest.mark.parametrize("m,n,k", [(300, 520, 1000), (1000, 1001, 130), (130, 136, 5000)])
+@pytest.mark.parametrize("dw_dtype", [BF, F])
+def test_linear_backward_one_gradient(ops, m, n, k, dw_dtype):
+    x, w, dy = mat(m, k, 1), mat(k, n, 2, 0.05, pad=8), mat(m, n, 3)
+    wdx, wdw, _, dz = D.linear_bwd(f64(dy), f64(x), f64(w), None, "none")
+    dx, none, _ = ops.linear_bwd(dy, x, w, want_dw=False)
+    assert none is None
+    close(dx, wdx, np.abs(wdx) * HALF + acc(n) * (np.abs(dz) @ np.abs(f64(w)).T), "dx")
+    none, dw, _ = ops.linear_bwd(dy, x, w, want_dx=False, dw_dtype=dw_dtype)
+    assert none is None
+    close(dw, wdw, np.abs(wdw) * (HALF if dw_dtype == BF else 0) + acc(m) * (np.abs(f64(x)).T @ np.abs(dz)), "dw")
+
+
 @pytest.mark.parametrize("n", list(range(1, 35)) + [63, 121, 127, 250, 253, 287])
 def test_every_width_of_the_last_columns(ops, n):
     m, k = 400, 72
