@@ -26,6 +26,12 @@
 // and writing its share of the columns: no workspace, no atomics, the same
 // bits on every run.
 //
+// Bound by the tensor cores under the power cap when the product is large
+// (4,096 x 4,096 x 4,096 73 us, 1.87 PFLOP/s; gated 2,003 x 4,096 x 2 * 14,336 240 us,
+// 1.96), by set-up, first loads and last stores when it is small (512 x 512 x
+// 512 4.3 us).  Rows that start at no multiple of 128 bytes cost the TMA two
+// lines for one: 4,096 x 4,096 x 4,096 then 105 to 120 us.
+//
 // Warps: 0 TMA, 1 MMA (of the leader CTA), 4-11 epilogue.  All waits are
 // bounded, as in the grouped GEMM kernels.
 
@@ -758,7 +764,8 @@ __global__ void __launch_bounds__(THREADS, 1)
 // each CTA adds every S-th row over all of them, in rank order, and runs the
 // epilogue on it (no workspace, no atomics, the same bits on every run).
 // About 96 KB of shared memory per CTA, so that two share an SM and one's
-// reduction runs under the other's loads.
+// reduction runs under the other's loads.  Bound by the reading of W: 1 x 14,336
+// x 4,096 21 us, 5.6 TB/s; 4 rows gated, 4,096 x 2 * 14,336, 37 us, 6.3 TB/s.
 namespace few {
 
 constexpr int ROWS = 128;                       // most rows of x per tile
@@ -1034,7 +1041,7 @@ __global__ void __launch_bounds__(THREADS, 2)
 // ------------------------------------------------- elementwise backward ----
 
 // da = [dh * up * act'(gate) | dh * act(gate)] from a = [gate | up].  Bound by
-// its 10 bytes per element of h; each product is rounded to bf16 once, as the
+// its 10 bytes per element of h (8,192 x 14,336: 178 us, 6.6 TB/s); each product is rounded to bf16 once, as the
 // operand of the two GEMMs that follow.
 __global__ void __launch_bounds__(256) k_glu_bwd(const __nv_bfloat16* __restrict__ dh, int64_t lddh,
                                                  const __nv_bfloat16* __restrict__ a, int64_t lda, int64_t M, int f,
@@ -1065,7 +1072,7 @@ __global__ void __launch_bounds__(256) k_glu_bwd(const __nv_bfloat16* __restrict
 // blockIdx.y.  A thread owns 8 columns; the CTA's 8 warps take every eighth
 // row, kActRowsInFlight of them loaded before the first is worked on (with
 // one at a time the loads covered 60 % of the memory's latency), and are added in
-// order at the end.  Bound by its 6 bytes an element.
+// order at the end.  Bound by its 6 bytes an element (8,192 x 7,168: 60 us, 5.9 TB/s).
 constexpr int kActRowsInFlight = 4;
 
 
