@@ -140,21 +140,30 @@ int device_sm_count();        // SM count of the current device (after moe_init)
 bool device_initialized();
 
 // Launches a kernel that calls wait_for_previous_kernels() with the early
-// start allowed.
+// start allowed; the first form in clusters of cluster_y CTAs along y.
 template <typename... Ts, typename... As>
-static inline cudaError_t launch_early(dim3 grid, int threads, size_t smem, cudaStream_t s, void (*kernel)(Ts...),
-                                       As... args) {
+static inline cudaError_t launch_early_clusters(int cluster_y, dim3 grid, int threads, size_t smem, cudaStream_t s,
+                                                void (*kernel)(Ts...), As... args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = 1;
+    attr[1].val.clusterDim.y = cluster_y;
+    attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = cluster_y > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kernel, Ts(args)...);
+}
+template <typename... Ts, typename... As>
+static inline cudaError_t launch_early(dim3 grid, int threads, size_t smem, cudaStream_t s, void (*kernel)(Ts...),
+                                       As... args) {
+    return launch_early_clusters(1, grid, threads, smem, s, kernel, args...);
 }
 }  // namespace moe
 

@@ -1068,20 +1068,28 @@ __global__ void __launch_bounds__(256) k_glu_bwd(const __nv_bfloat16* __restrict
 }
 
 // dz = dy * act'(z) (bf16, when ACT is not MOE_ACT_NONE) and the column sums of
-// the unrounded dz over this CTA's rows, one row of partial sums per
-// blockIdx.y.  A thread owns 8 columns; the CTA's 8 warps take every eighth
+// the unrounded dz over this CTA's rows: one row of partial sums per
+// blockIdx.y, or, in up to kJoin parts, a cluster's CTAs add theirs up through
+// distributed shared memory, in the order of the parts, and part is dbias
+// itself.  A thread owns 8 columns; the CTA's 8 warps take every eighth
 // row, kActRowsInFlight of them loaded before the first is worked on (with
 // one at a time the loads covered 60 % of the memory's latency), and are added in
 // order at the end.  Bound by its 6 bytes an element (8,192 x 7,168: 60 us, 5.9 TB/s).
 constexpr int kActRowsInFlight = 4;
+constexpr int kJoin = 8;
 
+__device__ __forceinline__ float ld_cluster(uint32_t addr) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
+}
 
 template <int ACT>
 __global__ void __launch_bounds__(256) k_act_bwd(const __nv_bfloat16* __restrict__ dy, int64_t lddy,
                                                  const __nv_bfloat16* __restrict__ z, int64_t ldz, int64_t M, int N,
                                                  __nv_bfloat16* __restrict__ dz, int64_t lddz,
                                                  float* __restrict__ part) {
-    __shared__ float s_sum[8][257];
+    __shared__ float s_sum[8][257], s_part[256];
     wait_for_previous_kernels();
     const int lane = threadIdx.x & 31, grp = threadIdx.x >> 5;
     const int c = blockIdx.x * 256 + lane * 8;
@@ -1126,13 +1134,28 @@ __global__ void __launch_bounds__(256) k_act_bwd(const __nv_bfloat16* __restrict
 #pragma unroll
     for (int j = 0; j < 8; ++j) s_sum[grp][lane * 8 + j] = sum[j];
     __syncthreads();
-    const int col = blockIdx.x * 256 + threadIdx.x;
-    if (col < N) {
-        float t = 0.f;
+    float t = 0.f;
 #pragma unroll
-        for (int g = 0; g < 8; ++g) t += s_sum[g][threadIdx.x];
-        part[(int64_t)blockIdx.y * N + col] = t;
+    for (int g = 0; g < 8; ++g) t += s_sum[g][threadIdx.x];
+    const int col = blockIdx.x * 256 + threadIdx.x;
+    if (gridDim.y == 1 || gridDim.y > kJoin) {
+        if (col < N) part[(int64_t)blockIdx.y * N + col] = t;
+        return;
     }
+    s_part[threadIdx.x] = t;
+    cluster_sync();
+    const int own = 256 / gridDim.y, at = blockIdx.y * own + threadIdx.x;      // this CTA's columns
+    if (threadIdx.x < own && blockIdx.x * 256 + at < N) {
+        const uint32_t src = smem_u32(&s_part[at]);
+        float v[kJoin], total = 0.f;
+#pragma unroll
+        for (int j = 0; j < kJoin; ++j)
+            v[j] = j < gridDim.y ? ld_cluster(mapa(src, (uint32_t)j)) : 0.f;
+#pragma unroll
+        for (int j = 0; j < kJoin; ++j) total += v[j];
+        part[blockIdx.x * 256 + at] = total;
+    }
+    cluster_sync();      // nobody leaves while its sums are read
 }
 
 // ----------------------------------------------------------------- host ----
@@ -1393,10 +1416,17 @@ static bool act_ok(int a) { return a >= MOE_ACT_NONE && a <= MOE_ACT_SILU; }
 static bool size_ok(int64_t v) { return v >= 1 && v <= 0x7FFFFF00LL; }
 static bool row_ok(const void* p, int64_t ld) { return moe_aligned16(p) && ld % 8 == 0; }
 
-// Rows of partial sums of k_act_bwd: one for up to 128 rows of dy (then it is
-// dbias itself, and the launch that adds up is saved: 2.3 us of the host's), one
-// for every 32 rows, 256 at most.
-static int act_parts(int64_t M) { return M <= 128 ? 1 : (int)std::min<int64_t>((M + 31) / 32, 256); }
+// Parts of k_act_bwd's rows: for up to 256 rows of dy 1, 2, 4 or 8 CTAs of a
+// cluster, which write dbias itself (128 x 1,024 dy, bias gradient only: 2.3 us, 3.2
+// in one CTA per 256 columns; with SiLU in a whole backward 8.8 against 12.3); else one
+// for every 32 rows, 256 at most, whose sums a second launch adds up (504 x 2,004:
+// 4.3 us, 4.7 in a cluster, with SiLU in a whole backward 19.8 against 21.9).
+static int act_parts(int64_t M) {
+    if (M > 256) return (int)std::min<int64_t>((M + 31) / 32, 256);
+    int parts = 1;
+    while (parts < kJoin && M > 16 * parts) parts *= 2;
+    return parts;
+}
 
 }  // namespace dense
 
@@ -1474,7 +1504,7 @@ static size_t dz_bytes(int64_t M, int N) { return ((size_t)M * ((N + 7) / 8 * 8)
 
 extern "C" size_t linear_bwd_workspace_size(int64_t M, int N) {
     if (M < 0 || M > 0x7FFFFF00LL || !size_ok(N)) return (size_t)-1;
-    return dz_bytes(M, N) + (size_t)act_parts(M) * N * sizeof(float);
+    return dz_bytes(M, N) + (act_parts(M) > kJoin ? (size_t)act_parts(M) * N * sizeof(float) : 0);
 }
 
 extern "C" moe_status_t linear_bwd(const void* dy, int64_t lddy, const void* x, int64_t ldx, const void* w, int64_t ldw,
@@ -1500,23 +1530,24 @@ extern "C" moe_status_t linear_bwd(const void* dy, int64_t lddy, const void* x, 
     cudaStream_t s = (cudaStream_t)stream;
     const void* g = dy;
     int64_t ldg = lddy;
-    const bool one_part = M > 0 && act_parts(M) == 1;
+    const int parts = act_parts(M);
+    const bool joined = M > 0 && parts <= kJoin;
     float* part = nullptr;
-    if (need_ws && dbias) part = one_part ? dbias : reinterpret_cast<float*>(static_cast<char*>(ws) + dz_bytes(M, N));
+    if (need_ws && dbias) part = joined ? dbias : reinterpret_cast<float*>(static_cast<char*>(ws) + dz_bytes(M, N));
     if (need_ws) {
         __nv_bfloat16* dz = static_cast<__nv_bfloat16*>(ws);
         const int64_t lddz = (N + 7) / 8 * 8;
         void (*const kernels[])(const __nv_bfloat16*, int64_t, const __nv_bfloat16*, int64_t, int64_t, int,
                                 __nv_bfloat16*, int64_t, float*) = {
             k_act_bwd<MOE_ACT_NONE>, k_act_bwd<MOE_ACT_RELU>, k_act_bwd<MOE_ACT_GELU>, k_act_bwd<MOE_ACT_SILU>};
-        if (launch_early(dim3((N + 255) / 256, act_parts(M)), 256, 0, s, kernels[act],
-                         static_cast<const __nv_bfloat16*>(dy), lddy, static_cast<const __nv_bfloat16*>(z), ldz, M, N,
-                         dz, lddz, part) != cudaSuccess)
+        if (launch_early_clusters(joined ? parts : 1, dim3((N + 255) / 256, parts), 256, 0, s, kernels[act],
+                                  static_cast<const __nv_bfloat16*>(dy), lddy, static_cast<const __nv_bfloat16*>(z),
+                                  ldz, M, N, dz, lddz, part) != cudaSuccess)
             return MOE_ERR_CUDA;
         if (with_z) g = dz, ldg = lddz;
     }
-    if (dbias && !one_part) {
-        launch_column_sum(part, M > 0 ? act_parts(M) : 0, N, dbias, s);
+    if (dbias && !joined) {
+        launch_column_sum(part, M > 0 ? parts : 0, N, dbias, s);
         MOE_CHECK_LAUNCH();
     }
     return gradients(g, ldg, x, ldx, w, ldw, M, N, K, dx, lddx, dw, dw_type, lddw, err, s);
