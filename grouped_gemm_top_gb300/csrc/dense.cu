@@ -1504,7 +1504,8 @@ static size_t dz_bytes(int64_t M, int N) { return ((size_t)M * ((N + 7) / 8 * 8)
 
 extern "C" size_t linear_bwd_workspace_size(int64_t M, int N) {
     if (M < 0 || M > 0x7FFFFF00LL || !size_ok(N)) return (size_t)-1;
-    return dz_bytes(M, N) + (act_parts(M) > kJoin ? (size_t)act_parts(M) * N * sizeof(float) : 0);
+    const int rows = act_parts(M) > kJoin ? act_parts(M) : 1;      // of partial sums
+    return dz_bytes(M, N) + (size_t)rows * N * sizeof(float);
 }
 
 extern "C" moe_status_t linear_bwd(const void* dy, int64_t lddy, const void* x, int64_t ldx, const void* w, int64_t ldw,
