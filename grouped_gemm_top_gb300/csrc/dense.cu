@@ -67,6 +67,32 @@ static_assert(SMEM_BYTES <= 232448, "shared memory budget");
 constexpr int PART_ROW = 144;
 constexpr int PART_BYTES = 128 * PART_ROW;
 
+// Shared memory of a tile in parts, over the pipeline stages: from the start on
+// the chunks that the other parts send, below the end the boxes on their way
+// out, where a warp finds room for all of its units (a unit is what finish()
+// takes: a chunk of 32 columns, GLU a gate and an up chunk).  A warp fills its
+// boxes while others still read chunks, so the two must not overlap.
+constexpr int swap_units(bool glu, int bn) { return glu ? bn / 64 : bn / 32; }
+constexpr int swap_own(bool glu, int bn, int splits) { return (swap_units(glu, bn) + splits - 1) / splits; }
+constexpr int swap_bytes(bool glu, int bn, int splits) {
+    return (splits - 1) * swap_own(glu, bn, splits) * (glu ? 2 : 1) * PART_BYTES;
+}
+// of one warp, which takes every second unit: GLU three boxes of 2 KB a unit
+// (gate, up, h), else two (z, y) or one of 4 KB (fp32)
+constexpr int swap_boxes(bool glu, int bn, int splits) {
+    return (swap_own(glu, bn, splits) + 1) / 2 * (glu ? 6144 : 4096);
+}
+constexpr int kWidths[] = {256, 224, 192, 128, 64};      // of a tile
+constexpr int kMaxSplits = 4;
+constexpr bool swap_fits() {
+    for (int bn : kWidths)
+        for (int splits = 2; splits <= kMaxSplits; ++splits)
+            for (int glu = 0; glu < 2; ++glu)
+                if (swap_bytes(glu, bn, splits) + EPI_WARPS * swap_boxes(glu, bn, splits) > SMEM_TILES) return false;
+    return true;
+}
+static_assert(swap_fits(), "boxes over chunks that other warps read");
+
 // What the epilogue makes of the product v:
 //   EPI_PLAIN   y = v (bf16)
 //   EPI_F32     y = v (fp32)
@@ -635,10 +661,10 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
     if (p.splits > 1) {
         // ------------------------- one tile per cluster: swap and add up ----
-        // A unit is what finish() takes (a chunk; GLU: a gate and an up
-        // chunk).  Part j owns units [j * own, (j + 1) * own), those that exist.
-        constexpr int CPU = EPI == EPI_GLU ? 2 : 1;      // chunks per unit
-        const int units = EPI == EPI_GLU ? p.bn / 64 : p.bn / 32, own = (units + p.splits - 1) / p.splits;
+        // Part j owns units [j * own, (j + 1) * own), those that exist.
+        constexpr bool GLU = EPI == EPI_GLU;
+        constexpr int CPU = GLU ? 2 : 1;      // chunks per unit
+        const int units = swap_units(GLU, p.bn), own = swap_own(GLU, p.bn, p.splits);
         const int u0 = part * own, u1 = min(u0 + own, units);
         const uint32_t buf = smem_u32(pl.smem);
         const int r = quarter * 32 + lane;
@@ -671,8 +697,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             const Tile ti = get_tile(p, pl.first);
             const int64_t row0 = (int64_t)ti.mt * TM + 128 * pl.rank + quarter * 32;
             const int col0 = ti.nt * (EPI == EPI_GLU ? p.bn / 2 : p.bn);
-            // boxes above the partial chunks: at most 3 of 2 KB (4 KB) a unit, four units a warp
-            out.last = smem_u32(pl.smem + SMEM_TILES - (ew + 1) * 8192);
+            out.last = smem_u32(pl.smem + SMEM_TILES - (ew + 1) * swap_boxes(GLU, p.bn, p.splits));
             out.last_tile();
             for (int un = u0 + half; un < u1; un += 2) {
                 float s[2][32];
@@ -1160,7 +1185,7 @@ __global__ void __launch_bounds__(256) k_act_bwd(const __nv_bfloat16* __restrict
 
 // ----------------------------------------------------------------- host ----
 
-static int g_max_clusters[4] = {0, 0, 0, 0};      // clusters of 2, 4, 6, 8 CTAs that run at a time
+static int g_max_clusters[kMaxSplits] = {0, 0, 0, 0};      // clusters of 2, 4, 6, 8 CTAs that run at a time
 
 // attr: room for two (the cluster, and the early start described at
 // wait_for_previous_kernels)
@@ -1208,7 +1233,7 @@ static cudaError_t set_attributes() {
         const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, few::SMEM_BYTES);
         if (e != cudaSuccess) return e;
     }
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < kMaxSplits; ++i) {
         cudaLaunchAttribute attr[2];
         cudaLaunchConfig_t cfg = launch_cfg(1024, i + 1, nullptr, attr);
         const cudaError_t e =
@@ -1244,18 +1269,18 @@ static double step_cost(int bn) { return bn == 256 ? 1.0 : (bn == 224 ? 0.91 : (
 // 1.5 to 2 us for 64 columns in two parts, 2.7 for 128, 4.3 for 256; 6 for 256 in three, 3.5 for 64 in four
 static double swap_cost(int bn, int splits) { return (4. + 12. * bn / 256.) * (1. + 0.4 * (splits - 2)); }
 constexpr double kEpilogue = 5. / 256.;      // a column
-constexpr int kWidths[] = {256, 224, 192, 128, 64};
 static double tile_cost(int nk, int bn) { return std::max(nk * step_cost(bn), kEpilogue * bn) + 1.; }
-static Choice choose(int64_t m_tiles, int N, int nk, bool glu) {
+// clusters: those of 2, 4, 6, 8 CTAs that run at a time
+static Choice choose(int64_t m_tiles, int N, int nk, bool glu, const int* clusters) {
     Choice best{256, 1, 1e300};
     for (int bn : kWidths) {
         // gate and up in whole chunks of 32, one at least for each half of the epilogue's warps
         if (glu && (bn == 224 || bn == 64)) continue;
         const int cols = glu ? bn / 2 : bn;
         const int64_t tiles = m_tiles * ((N + cols - 1) / cols);
-        if (bn == 64 && tiles > g_max_clusters[1]) continue;
-        for (int splits = 1; splits <= 4; ++splits) {
-            const int slots = g_max_clusters[splits - 1];
+        if (bn == 64 && tiles > clusters[1]) continue;
+        for (int splits = 1; splits <= kMaxSplits; ++splits) {
+            const int slots = clusters[splits - 1];
             if (splits > 1 && (tiles > slots || nk < 4 * splits)) continue;
             const int64_t waves = (tiles + slots - 1) / slots;
             const double cost = (double)waves * tile_cost((nk + splits - 1) / splits, bn) + kEpilogue * bn +
@@ -1315,7 +1340,7 @@ static moe_status_t product(const Mat& a, const Mat& b, Params p, cudaStream_t s
     MOE_REQUIRE(g_max_clusters[0] > 0, MOE_ERR_NOT_INITIALIZED);
     p.m_tiles = (int)((p.M + TM - 1) / TM);
     p.nk = (int)((p.K + TK - 1) / TK);
-    const Choice c = choose(p.m_tiles, p.N, p.nk, EPI == EPI_GLU);
+    const Choice c = choose(p.m_tiles, p.N, p.nk, EPI == EPI_GLU, g_max_clusters);
     p.splits = c.splits;
     set_width(p, c.bn, stage_size(B_MN, c.bn), EPI == EPI_GLU);
     CUtensorMap tmA, tmB, tmY, tmZ, tmZ2;
@@ -1486,7 +1511,8 @@ static moe_status_t gradients(const void* dz, int64_t lddz, const void* x, int64
         p.m_tiles = (int)((M + TM - 1) / TM), p.nk = (N + TK - 1) / TK;
         q.m_tiles = (int)((K + TM - 1) / TM), q.nk = (int)((M + TK - 1) / TK);
         const Choice c = choose_both(p.m_tiles, p.N, p.nk, q.m_tiles, q.N, q.nk);
-        const double two = choose(p.m_tiles, p.N, p.nk, false).cost + choose(q.m_tiles, q.N, q.nk, false).cost;
+        const double two = choose(p.m_tiles, p.N, p.nk, false, g_max_clusters).cost +
+                           choose(q.m_tiles, q.N, q.nk, false, g_max_clusters).cost;
         if (c.cost <= kBothMax && c.cost <= two + kBothSaves)
             return f32 ? product_both<EPI_F32>(mx, mw, mz, p, q, c.bn, s)
                        : product_both<EPI_PLAIN>(mx, mw, mz, p, q, c.bn, s);
@@ -1608,4 +1634,28 @@ extern "C" moe_status_t gated_ffn_bwd(const void* dh, int64_t lddh, const void* 
             return MOE_ERR_CUDA;
     }
     return gradients(da, ldda, x, ldx, w1, ldw, M, 2 * f, d, dx, lddx, dw1, dw_type, lddw, err, s);
+}
+
+extern "C" moe_status_t moe_selftest_dense_plan(int product, int64_t M, int64_t N, int64_t K, const int* clusters,
+                                                moe_dense_plan_t* plan) {
+    MOE_REQUIRE(plan && product >= MOE_DENSE_FWD && product <= MOE_DENSE_WGRAD, MOE_ERR_INVALID_ARG);
+    MOE_REQUIRE(M >= 1 && N >= 1 && K >= 1, MOE_ERR_INVALID_ARG);
+    MOE_REQUIRE(M <= 0x7FFFFF00LL && size_ok(N) && size_ok(K), MOE_ERR_UNSUPPORTED);
+    *plan = {};
+    if (product != MOE_DENSE_WGRAD && few_rows(M, K)) {
+        plan->few_rows = 1;
+        return MOE_OK;
+    }
+    const int* slots = clusters ? clusters : g_max_clusters;
+    MOE_REQUIRE(slots[0] > 0, clusters ? MOE_ERR_INVALID_ARG : MOE_ERR_NOT_INITIALIZED);
+    const bool glu = product == MOE_DENSE_GATED;
+    const Choice c = choose((M + TM - 1) / TM, (int)N, (int)((K + TK - 1) / TK), glu, slots);
+    plan->tile_cols = c.bn;
+    plan->parts = c.splits;
+    if (c.splits > 1) {
+        plan->swap_bytes = swap_bytes(glu, c.bn, c.splits);
+        plan->box_bytes = swap_boxes(glu, c.bn, c.splits);
+        plan->box_at = SMEM_TILES - EPI_WARPS * plan->box_bytes;
+    }
+    return MOE_OK;
 }

@@ -37,6 +37,7 @@ MOE_B_GNK, MOE_B_NGK, MOE_B_SF_TILE224 = 0, 1, 2
 MOE_SF_ATOMS, MOE_SF_TILE224, MOE_SF_CANONICAL, MOE_SF_TILE224_AND_ATOMS = 0, 1, 2, 3
 MOE_TYPE_BF16, MOE_TYPE_F32 = 0, 1
 MOE_ACT_NONE, MOE_ACT_RELU, MOE_ACT_GELU, MOE_ACT_SILU = range(4)
+MOE_DENSE_FWD, MOE_DENSE_GATED, MOE_DENSE_DGRAD, MOE_DENSE_WGRAD = range(4)
 MOE_GEMM_KERNEL_AUTO, MOE_GEMM_KERNEL_1SM, MOE_GEMM_KERNEL_1SM_N128 = 0, 1, 2
 MOE_GEMM_KERNEL_PAIR, MOE_GEMM_KERNEL_PAIR_N128 = 3, 4
 (MOE_OP_ROUTE_TOPK, MOE_OP_PERMUTE, MOE_OP_GROUP_QUANTIZE, MOE_OP_GATHER_QUANTIZE, MOE_OP_GROUPED_GEMM,
@@ -56,6 +57,7 @@ EXPORTS = [
     "rmsnorm_residual_fwd", "rmsnorm_bwd_workspace_size", "rmsnorm_residual_bwd",
     "adamw_plan_bytes", "adamw_plan_encode", "adamw_step",
     "linear_fwd", "linear_bwd_workspace_size", "linear_bwd", "gated_ffn_fwd", "gated_ffn_bwd",
+    "moe_selftest_dense_plan",
 ]
 
 _vp, _i32, _i64, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t
@@ -66,6 +68,11 @@ class GemmOpts(ctypes.Structure):
     """moe_gemm_opts_t (include/moe.h): per-call grouped-GEMM kernel choice."""
     _fields_ = [("kernel", ctypes.c_int), ("band", ctypes.c_int), ("register_stores", ctypes.c_int),
                 ("wgrad_rows_lo", ctypes.c_int), ("wgrad_rows_hi", ctypes.c_int)]
+
+
+class DensePlan(ctypes.Structure):
+    """moe_dense_plan_t (include/moe.h)."""
+    _fields_ = [(k, ctypes.c_int) for k in ("few_rows", "tile_cols", "parts", "swap_bytes", "box_at", "box_bytes")]
 
 
 class AdamWTensor(ctypes.Structure):
@@ -154,6 +161,7 @@ _SIGS = {
     "gated_ffn_fwd": (_i32, [_vp, _i64, _vp, _i64, _i32, _i64, _i32, _i64, _vp, _i64, _vp, _i64, _vp, _vp]),
     "gated_ffn_bwd": (_i32, [_vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _i32, _i64, _i32, _i64, _vp, _i64, _vp,
                              _i64, _vp, _i32, _i64, _vp, _vp]),
+    "moe_selftest_dense_plan": (_i32, [_i32, _i64, _i64, _i64, _vp, ctypes.POINTER(DensePlan)]),
     "adamw_plan_bytes": (_sz, [_i32]),
     "adamw_plan_encode": (_i32, [_vp, _i32, _i32, _i32, _i32, _vp, ctypes.POINTER(_i64)]),
     "adamw_step": (_i32, [_vp, _i32, _i64, _i32, _i32, _i32, _vp, _vp]),
@@ -780,6 +788,16 @@ def gated_ffn_bwd(dh, a, x, w1, act="silu", want_dx=True, want_dw=True, dx=None,
     if st:
         raise MoEError(fn, st)
     return dx, dw1
+
+
+def moe_selftest_dense_plan(product, M, N, K, clusters=None) -> DensePlan:
+    """How the product D[M, N] of depth K (MOE_DENSE_*) is launched.  See
+    include/moe.h."""
+    plan = DensePlan()
+    slots = None if clusters is None else (ctypes.c_int * 4)(*clusters)
+    _check("moe_selftest_dense_plan", lib.moe_selftest_dense_plan(int(product), int(M), int(N), int(K), slots,
+                                                                  ctypes.byref(plan)))
+    return plan
 
 
 class AdamWPlan:
