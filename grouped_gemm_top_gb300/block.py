@@ -8,8 +8,9 @@ sublayer, and AdamW over the weights of both:
     out = r + h W2                                   residual in the epilogue
 
 and the backward pass and update of every step.  Buffers are sized once;
-forward_ and backward_ allocate nothing and never synchronise, so they can be
-captured in a CUDA graph.
+forward_, backward_ and (once the weights have been set) update_ allocate
+nothing and never synchronise, so they can be captured in a CUDA graph, in
+one or apart: an update writes every weight and operand in place.
 
 ``python -m grouped_gemm_top_gb300.block`` trains one on synthetic data."""
 from __future__ import annotations

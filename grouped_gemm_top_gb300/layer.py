@@ -176,20 +176,26 @@ class MoELayer:
     def set_weights(self, W1, W2):
         """Quantize bf16 W1 [G, d, 2f] and W2 [G, f, d] along both axes (done
         once per weight update, outside the step; G = E + n_shared, the
-        shared experts last)."""
+        shared experts last).  The operands are allocated by the first call
+        and written in place by later ones, so a captured step sees new
+        weights, and the call can be captured itself."""
         E, d, f = self.G, self.d, self.f
-        dev = self.device
         W1v = W1.reshape(E * d, 2 * f)
         W2v = W2.reshape(E * f, d)
+
+        def quantize(name, w, axis, groups=0):
+            codes, scales = ops.mxfp8_group_quantize(w, axis, None, groups, getattr(self, name, None),
+                                                     getattr(self, name + "_s", None), err=self.err)
+            setattr(self, name, codes)
+            setattr(self, name + "_s", scales)
         # fwd operands: blocks along the contraction axis (d for W1, f for W2),
         # stored per expert as [E][N][K] (W1's gate/up halves interleaved in
         # 64-row chunks for the SwiGLU epilogue)
-        self.W1f, self.W1f_s = ops.mxfp8_group_quantize(W1v, ops.MOE_QUANT_COLWISE_BATCHED_GLU, None, E,
-                                                        err=self.err)
-        self.W2f, self.W2f_s = ops.mxfp8_group_quantize(W2v, ops.MOE_QUANT_COLWISE_BATCHED, None, E, err=self.err)
+        quantize("W1f", W1v, ops.MOE_QUANT_COLWISE_BATCHED_GLU, E)
+        quantize("W2f", W2v, ops.MOE_QUANT_COLWISE_BATCHED, E)
         # dgrad operands: blocks along the other axis (2f for W1, d for W2)
-        self.W1d, self.W1d_s = ops.mxfp8_group_quantize(W1v, ops.MOE_QUANT_ROWWISE, err=self.err)
-        self.W2d, self.W2d_s = ops.mxfp8_group_quantize(W2v, ops.MOE_QUANT_ROWWISE, err=self.err)
+        quantize("W1d", W1v, ops.MOE_QUANT_ROWWISE)
+        quantize("W2d", W2v, ops.MOE_QUANT_ROWWISE)
         self.weights_ready = True
 
     def set_router_weights(self, Wr):
