@@ -40,9 +40,13 @@ class AdamW:
                 raise ValueError(f"parameter {tuple(p.shape)} and gradient {tuple(g.shape)}")
             if rows[0] is None or rows[1] is None:
                 raise ValueError("parameters and gradients: contiguous, or rows with unit stride")
+            if p.dtype != torch.bfloat16 or g.dtype not in (torch.bfloat16, torch.float32):
+                raise ValueError(f"parameter {p.dtype}, gradient {g.dtype}: bfloat16, and bfloat16 or float32")
             if rows[0].shape != rows[1].shape and p.shape == g.shape:      # one is contiguous, the other is not
                 rows = p.view(-1, p.shape[-1]), g.view(-1, p.shape[-1])
             entries.append((*rows, float(wd[0]) if wd else float(weight_decay)))
+        if not entries:
+            raise ValueError("params: empty")
         dev = entries[0][0].device
         ops.moe_init(dev.index or 0)
         self.lr = torch.full((1,), float(lr), dtype=torch.float32, device=dev)

@@ -37,3 +37,13 @@ def test_what_does_not_lie_in_rows_is_refused(optim):
     for p, g in ((w.t(), w.t()), (w, torch.zeros((6, 4), dtype=torch.bfloat16).t()), (padded(4, 6), torch.zeros((6, 4)))):
         with pytest.raises(ValueError):
             optim.AdamW([(p, g)], 1e-3)
+
+
+def test_types_that_no_plan_takes_are_refused(optim):
+    """A gradient of another type has no plan and would never be applied."""
+    w = torch.zeros((4, 8), dtype=torch.bfloat16)
+    for p, g in ((w, w.half()), (w, w.double()), (w.float(), w), (w.half(), w)):
+        with pytest.raises(ValueError):
+            optim.AdamW([(w, w), (p, g)], 1e-3)
+    with pytest.raises(ValueError):
+        optim.AdamW([], 1e-3)
