@@ -58,6 +58,10 @@ class AdamW:
             ld = n if rows == 1 else (n + to - 1) // to * to
             return torch.zeros((rows, ld), dtype=dtype, device=dev)[:, :n]
 
+        def pieces(matrices):
+            return None if matrices is None else [row for t in matrices for row in t.unbind(0)]
+
+        counter = 0      # of the 8-bit rounding: every element of the optimizer has its own
         for dtype in (torch.bfloat16, torch.float32):
             mine = [e for e in entries if e[1].dtype == dtype]
             if not mine:
@@ -71,13 +75,14 @@ class AdamW:
                 return ([padded(*s, torch.uint8, 16) for s in shapes],
                         [padded(s[0], (s[1] + 255) // 256, torch.float32, 4) for s in shapes])
 
-            def pieces(matrices):
-                return None if matrices is None else [row for t in matrices for row in t.unbind(0)]
-
             (m, ms), (v, vs) = state(), state()
+            base = []
+            for row in pieces(masters):
+                base.append(counter)
+                counter += (row.numel() + 255) // 256 * 256
             plan = ops.adamw_plan(pieces(masters), pieces([g for _, g, _ in mine]), pieces(m), pieces(v), pieces(ms),
                                   pieces(vs), copies=pieces([p for p, _, _ in mine]),
-                                  weight_decay=[w for p, _, w in mine for _ in range(p.shape[0])])
+                                  weight_decay=[w for p, _, w in mine for _ in range(p.shape[0])], rng_base=base)
             self.masters += [t.view(-1) if len(t) == 1 else t for t in masters]
             self.groups.append((plan, torch.zeros((1,), dtype=torch.int32, device=dev)))
 

@@ -47,3 +47,23 @@ def test_types_that_no_plan_takes_are_refused(optim):
             optim.AdamW([(w, w), (p, g)], 1e-3)
     with pytest.raises(ValueError):
         optim.AdamW([], 1e-3)
+
+
+def test_every_element_has_its_own_rounding_counter(optim, monkeypatch):
+    """Over the plans of both gradient types, padded rows among them."""
+    plans = []
+
+    def plan(params, grads, m, v, m_scales, v_scales, copies, weight_decay, rng_base=None):
+        base = 0
+        for i, t in enumerate(params):      # the default: one tensor after the other
+            plans.append((base if rng_base is None else rng_base[i], t.numel()))
+            base += (t.numel() + 255) // 256 * 256
+
+    monkeypatch.setattr(optim.ops, "adamw_plan", plan)
+    monkeypatch.setattr(optim.ops, "moe_init", lambda device: None)
+    w = [torch.zeros(s, dtype=torch.bfloat16) for s in ((4, 300), (1000,), (512,), (3, 5))] + [padded(5, 41)]
+    optim.AdamW([(t, torch.zeros_like(t, dtype=d)) for t, d in zip(w, [torch.float32, torch.bfloat16] * 3)], 1e-3,
+                state_bits=8)
+    assert len(plans) == 9 and all(b % 256 == 0 for b, _ in plans)
+    taken = sorted((b, b + n) for b, n in plans)
+    assert all(x[1] <= y[0] for x, y in zip(taken, taken[1:])), taken
