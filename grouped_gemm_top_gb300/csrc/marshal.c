@@ -318,42 +318,43 @@ static PyObject* ffn_bwd(PyObject* self, PyObject* const* a, Py_ssize_t k) {
                        dx.ld, dw.p, dw.type, dw.ld, err, st));
 }
 
-/* (table address, tensors, tiles, p_type, g_type, state_bits, lr, beta1, beta2, eps, step, grad_scale, seed, stream);
-   lr and step: a number or a device tensor */
+/* (table address, its device, tensors, tiles, p_type, g_type, state_bits, lr, beta1, beta2, eps, step, grad_scale, seed,
+   stream); lr and step: a number or a device tensor */
 static PyObject* adamw(PyObject* self, PyObject* const* a, Py_ssize_t k) {
     long long dev;
     moe_adamw_opts_t o;
     void *p, *st;
     memset(&o, 0, sizeof(o));
-    TRY(arity(k, 14));
+    TRY(arity(k, 15));
     TRY(current_device(&dev));
     void* table = PyLong_AsVoidPtr(a[0]);
-    const long tensors = PyLong_AsLong(a[1]), pt = PyLong_AsLong(a[3]), gt = PyLong_AsLong(a[4]);
-    const long bits = PyLong_AsLong(a[5]);
-    const long long tiles = PyLong_AsLongLong(a[2]);
-    o.beta1 = PyFloat_AsDouble(a[7]);
-    o.beta2 = PyFloat_AsDouble(a[8]);
-    o.eps = PyFloat_AsDouble(a[9]);
-    o.seed = (uint32_t)PyLong_AsUnsignedLongLongMask(a[12]);
+    const long long table_dev = PyLong_AsLongLong(a[1]), tiles = PyLong_AsLongLong(a[3]);
+    const long tensors = PyLong_AsLong(a[2]), pt = PyLong_AsLong(a[4]), gt = PyLong_AsLong(a[5]);
+    const long bits = PyLong_AsLong(a[6]);
+    o.beta1 = PyFloat_AsDouble(a[8]);
+    o.beta2 = PyFloat_AsDouble(a[9]);
+    o.eps = PyFloat_AsDouble(a[10]);
+    o.seed = (uint32_t)PyLong_AsUnsignedLongLongMask(a[13]);
     if (PyErr_Occurred()) return NULL;
-    if (PyFloat_Check(a[6]) || PyLong_Check(a[6])) {
-        o.lr = PyFloat_AsDouble(a[6]);
+    TRY(table_dev == dev);      /* every tensor of the plan is where its table is (ops.adamw_plan) */
+    if (PyFloat_Check(a[7]) || PyLong_Check(a[7])) {
+        o.lr = PyFloat_AsDouble(a[7]);
     } else {
-        TRY(flat(a[6], dev, F32, 1, &p, NULL));
+        TRY(flat(a[7], dev, F32, 1, &p, NULL));
         TRY(p != NULL);
         o.lr_dev = (const float*)p;
     }
-    if (PyLong_Check(a[10])) {
-        o.step = PyLong_AsLongLong(a[10]);
+    if (PyLong_Check(a[11])) {
+        o.step = PyLong_AsLongLong(a[11]);
     } else {
-        TRY(flat(a[10], dev, I32, 1, &p, NULL));
+        TRY(flat(a[11], dev, I32, 1, &p, NULL));
         TRY(p != NULL);
         o.step_dev = (int32_t*)p;
     }
     if (PyErr_Occurred()) return NULL;
-    TRY(flat(a[11], dev, F32, 1, &p, NULL));
+    TRY(flat(a[12], dev, F32, 1, &p, NULL));
     o.grad_scale = (const float*)p;
-    TRY(handle(a[13], dev, &st));
+    TRY(handle(a[14], dev, &st));
     MAKE(adamw_step(table, (int)tensors, tiles, (int)pt, (int)gt, (int)bits, &o, st));
 }
 

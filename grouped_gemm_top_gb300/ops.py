@@ -806,7 +806,7 @@ class AdamWPlan:
 
     def __init__(self, table, tensors, tiles, p_type, g_type, state_bits, kept):
         self.table, self.kept = table, kept
-        self.args = (table.data_ptr(), tensors, tiles, p_type, g_type, state_bits)
+        self.args = (table.data_ptr(), table.get_device(), tensors, tiles, p_type, g_type, state_bits)
 
 
 def adamw_plan(params, grads, ms, vs, m_scales=None, v_scales=None, copies=None, weight_decay=0.0, rng_base=None,
