@@ -160,21 +160,34 @@ __device__ __forceinline__ float rcp_approx(float x) {
     return r;
 }
 
-// Square roots of two values >= 0, correctly rounded for x above 2^-102:
-// y = x rsqrt(x) from the approximate instruction, then one step along the
-// exact residual, y + (x - y^2) rsqrt(x) / 2 in fused multiply-adds
-// (Markstein's correction).  No branch for the cases that sqrtf sets apart,
-// and half the issue slots.  Zero, infinity and NaN give themselves; below
-// 2^-102 the residual underflows and the root may be off in its last bits.
+// Square roots of two values from 2^-100 on, correctly rounded: y = x rsqrt(x)
+// from the approximate instruction, then one step along the exact residual,
+// y + (x - y^2) rsqrt(x) / 2 in fused multiply-adds (Markstein's correction).
+// No branch for the cases that sqrtf sets apart, and half the issue slots.
+// Infinity and NaN give themselves.
+constexpr float kSqrtLeast = 7.888609052e-31f;      // 2^-100: below, x - y^2 has bits that fp32 does not hold
 __device__ __forceinline__ F2 sqrt2(F2 x) {
     float x0, x1, r0, r1;
     x.get(x0, x1);
-    asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(r0) : "f"(fmaxf(x0, 1.17549435e-38f)));
-    asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(r1) : "f"(fmaxf(x1, 1.17549435e-38f)));
+    asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(r0) : "f"(x0));
+    asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(r1) : "f"(x1));
     const F2 r(r0, r1), y = mul2(x, r);
     float z0, z1;
     fma2(fma2(mul2(y, F2(-1.f)), y, x), mul2(r, F2(0.5f)), y).get(z0, z1);
     return F2(x0 <= 3.402823466e38f ? z0 : x0, x1 <= 3.402823466e38f ? z1 : x1);
+}
+// The same of any value >= 0: small ones, zero and subnormals among them, as
+// 2^-50 sqrt(2^100 x), both factors exact.
+__device__ __forceinline__ F2 sqrt2_small(F2 x) {
+    float x0, x1;
+    x.get(x0, x1);
+    const bool s0 = x0 < kSqrtLeast, s1 = x1 < kSqrtLeast;
+    const F2 up(s0 ? 1.267650600e30f : 1.f, s1 ? 1.267650600e30f : 1.f);
+    const F2 down(s0 ? 8.881784197e-16f : 1.f, s1 ? 8.881784197e-16f : 1.f);
+    float z0, z1;
+    mul2(x, up).get(z0, z1);
+    sqrt2(F2(x0 == 0.f ? 1.f : z0, x1 == 0.f ? 1.f : z1)).get(z0, z1);
+    return mul2(F2(x0 == 0.f ? 0.f : z0, x1 == 0.f ? 0.f : z1), down);
 }
 
 // E4M3 codes to fp32 times 2^-120, in integer arithmetic (the conversion
@@ -429,11 +442,22 @@ __global__ void __launch_bounds__(kThreads, (Stage<PT, GT, BITS>::CTAS)) k_adamw
                 const F2 v2 = add2(mul2(F2(p.b2), F2(v[i], v[i + 1])), mul2(mul2(F2(p.c2), g2), g2));
                 m2.get(m[i], m[i + 1]);
                 v2.get(v[i], v[i + 1]);
-                const F2 u2 = sqrt2(v2);
-                u2.get(u[i], u[i + 1]);
+            }
+            float least = v[0];
+#pragma unroll
+            for (int i = 1; i < 8; ++i) least = fminf(least, v[i]);
+            if (least >= kSqrtLeast) {
+#pragma unroll
+                for (int i = 0; i < 8; i += 2) sqrt2(F2(v[i], v[i + 1])).get(u[i], u[i + 1]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; i += 2) sqrt2_small(F2(v[i], v[i + 1])).get(u[i], u[i + 1]);
+            }
+#pragma unroll
+            for (int i = 0; i < 8; i += 2) {
                 float d0, d1;
-                fma2(u2, F2(root2), F2(p.eps)).get(d0, d1);
-                const F2 q = mul2(mul2(m2, F2(-lr1)), F2(rcp_approx(d0), rcp_approx(d1)));
+                fma2(F2(u[i], u[i + 1]), F2(root2), F2(p.eps)).get(d0, d1);
+                const F2 q = mul2(mul2(F2(m[i], m[i + 1]), F2(-lr1)), F2(rcp_approx(d0), rcp_approx(d1)));
                 fma2(F2(w[i], w[i + 1]), decay, q).get(w[i], w[i + 1]);
             }
             if (!ok) {      // bytes that never came: the parameters say so
