@@ -250,12 +250,12 @@ __device__ __forceinline__ void block_scale(float top, float& scale, float& inv)
     inv = some ? __fmul_rn(__frcp_rn(top), 448.f) : 0.f;
 }
 
-// A tile's bytes in shared memory: p, g, m, v, and (8 bits) the 8 scales of each state.
+// A tile's bytes in shared memory (8 bits only): p, g, m, v, and the scales of each state.
 template <typename PT, typename GT, int BITS>
 struct Stage {
     static constexpr int kTile = tile_of(BITS, (int)(sizeof(PT) + sizeof(GT)));
-    static constexpr int P = kTile * (int)sizeof(PT), G = kTile * (int)sizeof(GT), S = kTile * (BITS == 32 ? 4 : 1);
-    static constexpr int SC = BITS == 32 ? 0 : kTile / kBlock * 4;
+    static constexpr int P = kTile * (int)sizeof(PT), G = kTile * (int)sizeof(GT), S = kTile;
+    static constexpr int SC = kTile / kBlock * 4;
     static constexpr int OFF_G = P, OFF_M = P + G, OFF_V = OFF_M + S, OFF_MS = OFF_V + S, OFF_VS = OFF_MS + SC;
     static constexpr int BYTES = OFF_VS + SC;
     // CTAs of an SM and stages of a CTA: about 192 KB on their way per SM
@@ -325,10 +325,8 @@ __global__ void __launch_bounds__(kThreads, (Stage<PT, GT, BITS>::CTAS)) k_adamw
             gg::bulk_load(dst + S::OFF_G, static_cast<const uint8_t*>(e.g) + tile * S::G, S::G, bar);
             gg::bulk_load(dst + S::OFF_M, static_cast<const uint8_t*>(e.m) + tile * S::S, S::S, bar);
             gg::bulk_load(dst + S::OFF_V, static_cast<const uint8_t*>(e.v) + tile * S::S, S::S, bar);
-            if (BITS == 8) {
-                gg::bulk_load(dst + S::OFF_MS, e.ms + tile * (S::kTile / kBlock), S::SC, bar);
-                gg::bulk_load(dst + S::OFF_VS, e.vs + tile * (S::kTile / kBlock), S::SC, bar);
-            }
+            gg::bulk_load(dst + S::OFF_MS, e.ms + tile * (S::kTile / kBlock), S::SC, bar);
+            gg::bulk_load(dst + S::OFF_VS, e.vs + tile * (S::kTile / kBlock), S::SC, bar);
             if (++pstage == S::STAGES) pstage = 0;
             --most;
         }
@@ -348,9 +346,11 @@ __global__ void __launch_bounds__(kThreads, (Stage<PT, GT, BITS>::CTAS)) k_adamw
         const float gs = p.grad_scale ? *p.grad_scale : 1.f;
         s_h[3] = gs;
         s_key = key;
-        for (int i = 0; i < S::STAGES; ++i) gg::mbar_init(gg::smem_u32(&s_bar[i]), 1);
-        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-        if (fabsf(gs) <= 3.402823466e38f) fetch(S::STAGES);
+        if constexpr (S::RING > 0) {
+            for (int i = 0; i < S::STAGES; ++i) gg::mbar_init(gg::smem_u32(&s_bar[i]), 1);
+            asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+            if (fabsf(gs) <= 3.402823466e38f) fetch(S::STAGES);
+        }
     }
     __syncthreads();
     const float lr = s_h[2], gs = s_h[3], root2 = s_h[1], lr1 = lr * s_h[0];
@@ -382,15 +382,10 @@ __global__ void __launch_bounds__(kThreads, (Stage<PT, GT, BITS>::CTAS)) k_adamw
                 const int o = sub + 8 * (int)threadIdx.x;
                 load(reinterpret_cast<const PT*>(s) + o, 8, true, w);
                 load(reinterpret_cast<const GT*>(s + S::OFF_G) + o, 8, true, g);
-                if (BITS == 32) {
-                    load(reinterpret_cast<const float*>(s + S::OFF_M) + o, 8, true, m);
-                    load(reinterpret_cast<const float*>(s + S::OFF_V) + o, 8, true, v);
-                } else {
-                    load_codes<true>(s + S::OFF_M + o, 8, true, m);
-                    load_codes<false>(s + S::OFF_V + o, 8, true, v);
-                    sm = reinterpret_cast<const float*>(s + S::OFF_MS)[o / kBlock];
-                    sv = reinterpret_cast<const float*>(s + S::OFF_VS)[o / kBlock];
-                }
+                load_codes<true>(s + S::OFF_M + o, 8, true, m);
+                load_codes<false>(s + S::OFF_V + o, 8, true, v);
+                sm = reinterpret_cast<const float*>(s + S::OFF_MS)[o / kBlock];
+                sv = reinterpret_cast<const float*>(s + S::OFF_VS)[o / kBlock];
                 if (sub == S::kTile - kSub) {
                     __syncthreads();      // the stage is read
                     if (threadIdx.x == 0) fetch(1);
