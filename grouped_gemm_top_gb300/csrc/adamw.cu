@@ -164,30 +164,28 @@ __device__ __forceinline__ float rcp_approx(float x) {
 // from the approximate instruction, then one step along the exact residual,
 // y + (x - y^2) rsqrt(x) / 2 in fused multiply-adds (Markstein's correction).
 // No branch for the cases that sqrtf sets apart, and half the issue slots.
-// Infinity and NaN give themselves.
+// Infinity and NaN give themselves; zero does where ZERO says that it may come.
 constexpr float kSqrtLeast = 7.888609052e-31f;      // 2^-100: below, x - y^2 has bits that fp32 does not hold
+template <bool ZERO>
 __device__ __forceinline__ F2 sqrt2(F2 x) {
     float x0, x1, r0, r1;
     x.get(x0, x1);
-    asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(r0) : "f"(x0));
-    asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(r1) : "f"(x1));
+    asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(r0) : "f"(ZERO ? fmaxf(x0, 1.17549435e-38f) : x0));
+    asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(r1) : "f"(ZERO ? fmaxf(x1, 1.17549435e-38f) : x1));
     const F2 r(r0, r1), y = mul2(x, r);
     float z0, z1;
     fma2(fma2(mul2(y, F2(-1.f)), y, x), mul2(r, F2(0.5f)), y).get(z0, z1);
     return F2(x0 <= 3.402823466e38f ? z0 : x0, x1 <= 3.402823466e38f ? z1 : x1);
 }
-// The same of any value >= 0: small ones, zero and subnormals among them, as
-// 2^-50 sqrt(2^100 x), both factors exact.
-__device__ __forceinline__ F2 sqrt2_small(F2 x) {
+// The same of any value >= 0: below 2^-100, zero and subnormals among them,
+// as 2^-50 sqrt(2^100 x), both factors exact.
+__device__ __forceinline__ F2 sqrt2_any(F2 x) {
     float x0, x1;
     x.get(x0, x1);
     const bool s0 = x0 < kSqrtLeast, s1 = x1 < kSqrtLeast;
     const F2 up(s0 ? 1.267650600e30f : 1.f, s1 ? 1.267650600e30f : 1.f);
     const F2 down(s0 ? 8.881784197e-16f : 1.f, s1 ? 8.881784197e-16f : 1.f);
-    float z0, z1;
-    mul2(x, up).get(z0, z1);
-    sqrt2(F2(x0 == 0.f ? 1.f : z0, x1 == 0.f ? 1.f : z1)).get(z0, z1);
-    return mul2(F2(x0 == 0.f ? 0.f : z0, x1 == 0.f ? 0.f : z1), down);
+    return mul2(sqrt2<true>(mul2(x, up)), down);
 }
 
 // E4M3 codes to fp32 times 2^-120, in integer arithmetic (the conversion
@@ -437,16 +435,22 @@ __global__ void __launch_bounds__(kThreads, (Stage<PT, GT, BITS>::CTAS)) k_adamw
                 const F2 v2 = add2(mul2(F2(p.b2), F2(v[i], v[i + 1])), mul2(mul2(F2(p.c2), g2), g2));
                 m2.get(m[i], m[i + 1]);
                 v2.get(v[i], v[i + 1]);
+                if (BITS == 32) sqrt2_any(v2).get(u[i], u[i + 1]);
             }
-            float least = v[0];
+            if (BITS == 8) {
+                // bound by issue: four instructions an element fewer while none of the
+                // eight is small (with 32 bits, where they are free, small steps gain
+                // 0.2 us without the branch)
+                float least = v[0];
 #pragma unroll
-            for (int i = 1; i < 8; ++i) least = fminf(least, v[i]);
-            if (least >= kSqrtLeast) {
+                for (int i = 1; i < 8; ++i) least = fminf(least, v[i]);
+                if (least >= kSqrtLeast) {
 #pragma unroll
-                for (int i = 0; i < 8; i += 2) sqrt2(F2(v[i], v[i + 1])).get(u[i], u[i + 1]);
-            } else {
+                    for (int i = 0; i < 8; i += 2) sqrt2<false>(F2(v[i], v[i + 1])).get(u[i], u[i + 1]);
+                } else {
 #pragma unroll
-                for (int i = 0; i < 8; i += 2) sqrt2_small(F2(v[i], v[i + 1])).get(u[i], u[i + 1]);
+                    for (int i = 0; i < 8; i += 2) sqrt2_any(F2(v[i], v[i + 1])).get(u[i], u[i + 1]);
+                }
             }
 #pragma unroll
             for (int i = 0; i < 8; i += 2) {
