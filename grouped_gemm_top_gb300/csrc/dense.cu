@@ -1440,6 +1440,9 @@ static bool act_ok(int a) { return a >= MOE_ACT_NONE && a <= MOE_ACT_SILU; }
 // sizes the tensor maps and the tile counts hold
 static bool size_ok(int64_t v) { return v >= 1 && v <= 0x7FFFFF00LL; }
 static bool row_ok(const void* p, int64_t ld) { return moe_aligned16(p) && ld % 8 == 0; }
+// The stride of a matrix of one row means nothing; the tensor maps want some
+// multiple of 16 bytes.
+static int64_t stride_of(int64_t rows, int64_t cols, int64_t ld) { return rows == 1 && ld >= cols ? (cols + 7) / 8 * 8 : ld; }
 
 // Parts of k_act_bwd's rows: for up to 256 rows of dy 1, 2, 4 or 8 CTAs of a
 // cluster, which write dbias itself (128 x 1,024 dy, bias gradient only: 2.3 us, 3.2
@@ -1470,6 +1473,8 @@ extern "C" moe_status_t linear_fwd(const void* x, int64_t ldx, const void* w, in
     MOE_REQUIRE(ldx >= K && ldw >= N && ldy >= N && (!res || ldres >= N) && (!z || ldz >= N), MOE_ERR_INVALID_ARG);
     MOE_REQUIRE(M <= 0x7FFFFF00LL && size_ok(N) && size_ok(K), MOE_ERR_UNSUPPORTED);
     if (M == 0) return MOE_OK;
+    ldx = stride_of(M, K, ldx), ldw = stride_of(K, N, ldw), ldy = stride_of(M, N, ldy);
+    ldres = stride_of(M, N, ldres), ldz = stride_of(M, N, ldz);
     MOE_REQUIRE(x && w && y, MOE_ERR_INVALID_ARG);
     MOE_REQUIRE(row_ok(x, ldx) && row_ok(w, ldw) && row_ok(y, ldy) && (!res || row_ok(res, ldres)) &&
                     (!z || row_ok(z, ldz)) && reinterpret_cast<uintptr_t>(bias) % 2 == 0,
@@ -1546,6 +1551,8 @@ extern "C" moe_status_t linear_bwd(const void* dy, int64_t lddy, const void* x, 
                 MOE_ERR_INVALID_ARG);
     MOE_REQUIRE(M <= 0x7FFFFF00LL && size_ok(N) && size_ok(K), MOE_ERR_UNSUPPORTED);
     MOE_REQUIRE(dx || dw || dbias, MOE_ERR_INVALID_ARG);
+    lddy = stride_of(M, N, lddy), ldz = stride_of(M, N, ldz), ldx = stride_of(M, K, ldx);
+    lddx = stride_of(M, K, lddx), ldw = stride_of(K, N, ldw), lddw = stride_of(K, N, lddw);
     MOE_REQUIRE(M == 0 || (dy && (!with_z || z) && (!dx || w) && (!dw || x)), MOE_ERR_INVALID_ARG);
     MOE_REQUIRE(row_ok(dy, lddy) && (!with_z || row_ok(z, ldz)) && (!dx || (row_ok(w, ldw) && row_ok(dx, lddx))) &&
                     (!dw || (row_ok(x, ldx) && row_ok(dw, lddw))) && reinterpret_cast<uintptr_t>(dbias) % 4 == 0 &&
@@ -1587,6 +1594,8 @@ extern "C" moe_status_t gated_ffn_fwd(const void* x, int64_t ldx, const void* w1
     MOE_REQUIRE(ldx >= d && ldw >= 2 * (int64_t)f && ldh >= f && (!a || lda >= 2 * (int64_t)f), MOE_ERR_INVALID_ARG);
     MOE_REQUIRE(f % 8 == 0 && M <= 0x7FFFFF00LL && f <= 0x3FFFFF00 && size_ok(d), MOE_ERR_UNSUPPORTED);
     if (M == 0) return MOE_OK;
+    ldx = stride_of(M, d, ldx), ldw = stride_of(d, 2 * (int64_t)f, ldw), ldh = stride_of(M, f, ldh);
+    lda = stride_of(M, 2 * (int64_t)f, lda);
     MOE_REQUIRE(x && w1 && h, MOE_ERR_INVALID_ARG);
     MOE_REQUIRE(row_ok(x, ldx) && row_ok(w1, ldw) && row_ok(h, ldh) && (!a || row_ok(a, lda)), MOE_ERR_ALIGNMENT);
     MOE_REQUIRE(device_initialized(), MOE_ERR_NOT_INITIALIZED);
@@ -1617,6 +1626,9 @@ extern "C" moe_status_t gated_ffn_bwd(const void* dh, int64_t lddh, const void* 
                     (!dw1 || (ldx >= d && lddw >= f2)),
                 MOE_ERR_INVALID_ARG);
     MOE_REQUIRE(f % 8 == 0 && M <= 0x7FFFFF00LL && f <= 0x3FFFFF00 && size_ok(d), MOE_ERR_UNSUPPORTED);
+    lddh = stride_of(M, f, lddh), lda = stride_of(M, f2, lda), ldda = stride_of(M, f2, ldda);
+    ldx = stride_of(M, d, ldx), lddx = stride_of(M, d, lddx), ldw = stride_of(d, f2, ldw);
+    lddw = stride_of(d, f2, lddw);
     MOE_REQUIRE(M == 0 || (dh && a && da && (!dx || w1) && (!dw1 || x)), MOE_ERR_INVALID_ARG);
     MOE_REQUIRE(row_ok(dh, lddh) && row_ok(a, lda) && row_ok(da, ldda) &&
                     (!dx || (row_ok(w1, ldw) && row_ok(dx, lddx))) &&

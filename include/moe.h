@@ -866,9 +866,10 @@ MOE_API moe_status_t rmsnorm_residual_bwd(const void* dy, int dy_type, int64_t l
  * Dense bf16 layers on the tensor cores, fp32 accumulation.  All matrices are
  * row-major bf16 with rows that start at multiples of 16 bytes (base address
  * 16-byte aligned, strides multiples of 8 elements; the TMA's rule); the
- * sizes M, N and K themselves are free.  What lies between a row's end
- * and the next row's start is neither used nor written.  err (may be NULL)
- * receives MOE_ERR_DEVICE_TIMEOUT if a bounded wait inside a kernel gives up.
+ * sizes M, N and K themselves are free, and so is the stride of a matrix of
+ * one row.  What lies between a row's end and the next row's start is neither
+ * used nor written.  err (may be NULL) receives MOE_ERR_DEVICE_TIMEOUT if a
+ * bounded wait inside a kernel gives up.
  */
 typedef enum { MOE_ACT_NONE = 0, MOE_ACT_RELU = 1, MOE_ACT_GELU = 2, MOE_ACT_SILU = 3 } moe_act_t;  /* GELU: z Phi(z) */
 
