@@ -652,7 +652,7 @@ def _new(shape, dtype, like, stream):
         return torch.empty(shape, dtype=dtype, device=like.device)
 
 
-def _new_rows(fn, m, n, dtype, like, stream):
+def _new_rows(m, n, dtype, like, stream):
     """An uninitialised [m, n] whose rows start at multiples of 16 bytes."""
     t = _new((m, (n + 7) // 8 * 8), dtype, like, stream)
     return t if n % 8 == 0 else t[:, :n]
@@ -670,7 +670,8 @@ def rmsnorm_residual_fwd(x, w, residual=None, eps=1e-6, y=None, r=None, rstd=Non
                          stream=None):
     """r = x + residual, y = r / sqrt(mean r^2 + eps) * w, and y's MXFP8
     codes and scales.  See include/moe.h.  Outputs that are wanted and not
-    given are allocated; r is only written when there is a residual, or given.
+    given are allocated, their rows at multiples of 16 bytes, as the linear
+    layers take them; r is only written when there is a residual, or given.
     Returns (y, r, rstd, codes, scales), None for what is not produced."""
     fn = "rmsnorm_residual_fwd"
     if rstd is None or (y is None and want_y) or (want_codes and codes is None) or (
@@ -679,9 +680,9 @@ def rmsnorm_residual_fwd(x, w, residual=None, eps=1e-6, y=None, r=None, rstd=Non
         if rstd is None:
             rstd = _new((M,), torch.float32, x, stream)
         if y is None and want_y:
-            y = _new((M, N), y_dtype, x, stream)
+            y = _new_rows(M, N, y_dtype, x, stream)
         if r is None and want_r and residual is not None:
-            r = _new((M, N), residual.dtype, x, stream)
+            r = _new_rows(M, N, residual.dtype, x, stream)
         if want_codes and codes is None:
             rows = (M + 127) // 128 * 128 if sf_layout == MOE_SF_ATOMS else M
             codes = _new((rows, N), torch.uint8, x, stream)
@@ -704,7 +705,7 @@ def rmsnorm_residual_bwd(dy, r, w, rstd, dres=None, want_dw=True, dx=None, dw=No
     if dx is None or (want_dw and dw is None) or (ws is None and (want_dw or dw is not None)):
         M, N = _size(fn, r)
         if dx is None:
-            dx = _new((M, N), r.dtype, r, stream)
+            dx = _new_rows(M, N, r.dtype, r, stream)
         if want_dw and dw is None:
             dw = _new((N,), torch.float32, r, stream)
         if dw is not None and ws is None:
@@ -722,8 +723,8 @@ def linear_fwd(x, w, bias=None, act="none", residual=None, y=None, z=None, want_
     fn = "linear_fwd"
     if y is None or (want_z and z is None):
         M, N = _size(fn, x, w)[0], w.shape[1]
-        y = y if y is not None else _new_rows(fn, M, N, torch.bfloat16, x, stream)
-        z = z if z is not None or not want_z else _new_rows(fn, M, N, torch.bfloat16, x, stream)
+        y = y if y is not None else _new_rows(M, N, torch.bfloat16, x, stream)
+        z = z if z is not None or not want_z else _new_rows(M, N, torch.bfloat16, x, stream)
     st = _marshal.linear_fwd(x, w, bias, _act(fn, act), residual, y, z, err, stream)
     if st:
         raise MoEError(fn, st)
@@ -746,9 +747,9 @@ def linear_bwd(dy, x, w, z=None, act="none", want_dx=True, want_dw=True, want_db
     if need_ws or (want_dx and dx is None) or (want_dw and dw is None) or (want_dbias and dbias is None):
         (M, N), K = _size(fn, dy, x), x.shape[1]
         if want_dx and dx is None:
-            dx = _new_rows(fn, M, K, torch.bfloat16, x, stream)
+            dx = _new_rows(M, K, torch.bfloat16, x, stream)
         if want_dw and dw is None:
-            dw = _new_rows(fn, K, N, dw_dtype, x, stream)
+            dw = _new_rows(K, N, dw_dtype, x, stream)
         if want_dbias and dbias is None:
             dbias = _new((N,), torch.float32, x, stream)
         if need_ws:
@@ -765,8 +766,8 @@ def gated_ffn_fwd(x, w1, act="silu", h=None, a=None, want_a=False, err=None, str
     fn = "gated_ffn_fwd"
     if h is None or (want_a and a is None):
         M, f2 = _size(fn, x, w1)[0], w1.shape[1]
-        h = h if h is not None else _new_rows(fn, M, f2 // 2, torch.bfloat16, x, stream)
-        a = a if a is not None or not want_a else _new_rows(fn, M, f2, torch.bfloat16, x, stream)
+        h = h if h is not None else _new_rows(M, f2 // 2, torch.bfloat16, x, stream)
+        a = a if a is not None or not want_a else _new_rows(M, f2, torch.bfloat16, x, stream)
     st = _marshal.gated_ffn_fwd(x, w1, _act(fn, act), h, a, err, stream)
     if st:
         raise MoEError(fn, st)
@@ -781,9 +782,9 @@ def gated_ffn_bwd(dh, a, x, w1, act="silu", want_dx=True, want_dw=True, dx=None,
     fn = "gated_ffn_bwd"
     if da is None or (want_dx and dx is None) or (want_dw and dw1 is None):
         (M, f), d = _size(fn, dh, x), x.shape[1]
-        da = da if da is not None else _new_rows(fn, M, 2 * f, torch.bfloat16, x, stream)
-        dx = dx if dx is not None or not want_dx else _new_rows(fn, M, d, torch.bfloat16, x, stream)
-        dw1 = dw1 if dw1 is not None or not want_dw else _new_rows(fn, d, 2 * f, dw_dtype, x, stream)
+        da = da if da is not None else _new_rows(M, 2 * f, torch.bfloat16, x, stream)
+        dx = dx if dx is not None or not want_dx else _new_rows(M, d, torch.bfloat16, x, stream)
+        dw1 = dw1 if dw1 is not None or not want_dw else _new_rows(d, 2 * f, dw_dtype, x, stream)
     st = _marshal.gated_ffn_bwd(dh, a, x, w1, _act(fn, act), da, dx, dw1, err, stream)
     if st:
         raise MoEError(fn, st)
