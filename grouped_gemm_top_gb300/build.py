@@ -85,14 +85,24 @@ def build(verbose: bool = False, ptxas_verbose: bool = False, force: bool = Fals
 
 
 def _build_marshal(force):
-    """csrc/marshal.c against Python's headers and libmoe.so beside it."""
+    """csrc/marshal.c against Python's headers and libmoe.so beside it.  Where
+    there is no C compiler or Python has no headers, the library is built
+    without it (and says so): the MoE layer does not need it."""
     src = os.path.join(CSRC, "marshal.c")
-    newest = max(os.path.getmtime(src), _deps_mtime())
-    if not force and os.path.exists(MARSHAL) and os.path.getmtime(MARSHAL) >= newest:
+    there = os.path.exists(MARSHAL)
+    fresh = there and os.path.getmtime(MARSHAL) >= max(os.path.getmtime(src), _deps_mtime())
+    if fresh and not force:
+        return
+    cc, headers = shutil.which("gcc") or shutil.which("cc"), sysconfig.get_paths()["include"]
+    if cc is None or not os.path.exists(os.path.join(headers, "Python.h")):
+        if there and not fresh:
+            os.remove(MARSHAL)      # older than the calls it makes
+        print(f"_marshal.so not built: no {'C compiler' if cc is None else 'Python.h in ' + headers}; the dense "
+              "operators (norm, linear, gated feed-forward, AdamW) need it", file=sys.stderr)
         return
     tmp = MARSHAL + ".tmp"
-    cmd = [shutil.which("gcc") or shutil.which("cc") or "gcc", "-O2", "-Wall", "-shared", "-fPIC", "-I", INCLUDE, "-I",
-           sysconfig.get_paths()["include"], src, "-o", tmp, "-L", PKG, "-l:libmoe.so", "-Wl,-rpath,$ORIGIN"]
+    cmd = [cc, "-O2", "-Wall", "-shared", "-fPIC", "-I", INCLUDE, "-I", headers, src, "-o", tmp, "-L", PKG,
+           "-l:libmoe.so", "-Wl,-rpath,$ORIGIN"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"building _marshal.so failed:\n{r.stdout}\n{r.stderr}")

@@ -2,8 +2,9 @@
 
 Argument marshalling only -- every step runs in the library's CUDA kernels.
 Torch is used for device memory and the current stream.  If the shared
-library (or _marshal.so, the dense operators' compiled marshalling) is missing
-the import of this module fails loudly; there is no fallback path.
+library is missing the import of this module fails loudly, and so does every
+call of a dense operator without _marshal.so, their compiled marshalling;
+there is no fallback path.
 """
 from __future__ import annotations
 
@@ -186,7 +187,24 @@ def _load():
 
 
 lib = _load()
-from . import _marshal  # noqa: E402  (links libmoe.so, loaded above)
+
+
+class _NoMarshal:
+    """In _marshal's place where it was not built: the dense operators say so,
+    everything else works."""
+
+    def __init__(self, why):
+        self._why = why
+
+    def __getattr__(self, name):
+        raise ImportError(f"{name} needs _marshal.so: run grouped_gemm_top_gb300.build with a C compiler and "
+                          f"Python's headers ({self._why})")
+
+
+try:
+    from . import _marshal  # noqa: E402  (links libmoe.so, loaded above)
+except ImportError as e:
+    _marshal = _NoMarshal(e)
 
 
 def status_string(status: int) -> str:
@@ -629,8 +647,9 @@ def moe_selftest_bounded_wait(timeout_ns, err, completed, stream=None):
 
 _TYPES = {torch.bfloat16: MOE_TYPE_BF16, torch.float32: MOE_TYPE_F32}
 _ACTS = {"none": MOE_ACT_NONE, "relu": MOE_ACT_RELU, "gelu": MOE_ACT_GELU, "silu": MOE_ACT_SILU}
-_marshal.setup(torch.bfloat16, torch.float32, torch.uint8, torch.float8_e4m3fn, torch.int32,
-               torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream)
+if not isinstance(_marshal, _NoMarshal):
+    _marshal.setup(torch.bfloat16, torch.float32, torch.uint8, torch.float8_e4m3fn, torch.int32,
+                   torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream)
 
 
 def _need(fn, ok):
