@@ -205,10 +205,12 @@ __device__ __forceinline__ uint4 load_vec8(const __nv_bfloat16* p, int n) {     
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 // 32 columns of one row from memory; `n` of them exist.  Rows start at
-// multiples of 16 bytes and columns at multiples of 32.
+// multiples of 16 bytes and columns at multiples of 32.  (Plain loads: the
+// residual may be y itself, which this kernel writes.)
 __device__ __forceinline__ void load32(const __nv_bfloat16* p, int n, float* f) {
     if (n >= 32) {
-        load_row32(p, f);
+#pragma unroll
+        for (int g = 0; g < 4; ++g) unpack8(reinterpret_cast<const uint4*>(p)[g], f + 8 * g);
     } else {
 #pragma unroll
         for (int g = 0; g < 4; ++g)
@@ -1068,9 +1070,11 @@ __global__ void __launch_bounds__(THREADS, 2)
 // da = [dh * up * act'(gate) | dh * act(gate)] from a = [gate | up].  Bound by
 // its 10 bytes per element of h (8,192 x 14,336: 178 us, 6.6 TB/s); each product is rounded to bf16 once, as the
 // operand of the two GEMMs that follow.
+// (da may be a itself: neither is __restrict__, which would let a be read
+// through the cache for memory that no one writes.)
 __global__ void __launch_bounds__(256) k_glu_bwd(const __nv_bfloat16* __restrict__ dh, int64_t lddh,
-                                                 const __nv_bfloat16* __restrict__ a, int64_t lda, int64_t M, int f,
-                                                 int act, __nv_bfloat16* __restrict__ da, int64_t ldda) {
+                                                 const __nv_bfloat16* a, int64_t lda, int64_t M, int f, int act,
+                                                 __nv_bfloat16* da, int64_t ldda) {
     wait_for_previous_kernels();
     const int nvec = f / 8;
     const int64_t n = M * nvec, stride = (int64_t)gridDim.x * blockDim.x;
