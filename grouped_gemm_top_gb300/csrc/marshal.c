@@ -185,6 +185,7 @@ static PyObject* norm_fwd(PyObject* self, PyObject* const* a, Py_ssize_t k) {
     TRY(flat(a[1], dev, BF16 | F32, x.n, &w, &wt));
     TRY(mat(a[2], dev, BF16 | F32, x.m, x.n, &res));
     const double eps = PyFloat_AsDouble(a[3]);
+    if (eps == -1. && PyErr_Occurred()) return NULL;
     TRY(mat(a[4], dev, BF16 | F32, x.m, x.n, &y));
     TRY(mat(a[5], dev, BF16 | F32, x.m, x.n, &r));
     TRY(flat(a[6], dev, F32, x.m, &rstd, NULL));
@@ -339,6 +340,7 @@ static PyObject* adamw(PyObject* self, PyObject* const* a, Py_ssize_t k) {
     TRY(table_dev == dev);      /* every tensor of the plan is where its table is (ops.adamw_plan) */
     if (PyFloat_Check(a[7]) || PyLong_Check(a[7])) {
         o.lr = PyFloat_AsDouble(a[7]);
+        if (o.lr == -1. && PyErr_Occurred()) return NULL;
     } else {
         TRY(flat(a[7], dev, F32, 1, &p, NULL));
         TRY(p != NULL);

@@ -37,3 +37,16 @@ def test_a_plan_of_another_device_is_refused(marshal):
         step(0)
     except ops.MoEError as e:
         assert e.status == ops.MOE_ERR_NOT_INITIALIZED      # past the marshalling; the library has no device here
+
+
+def test_a_python_error_is_raised_before_anything_else_is_looked_at(marshal):
+    m, ops = marshal
+    m.setup(torch.bfloat16, torch.float32, torch.uint8, torch.float8_e4m3fn, torch.int32, lambda: -1, lambda device: 0)
+    x, w = torch.zeros((4, 8)), torch.zeros(8)                 # host memory is "on" device -1
+    with pytest.raises(TypeError):
+        m.rmsnorm_residual_fwd(x, w, None, "eps", x[:3], None, None, None, None, 0, None)
+    plan = (4096, -1, 1, 0, 1, 1, 32)
+    with pytest.raises(OverflowError):
+        m.adamw_step(*plan, 10 ** 400, 0.9, 0.999, 1e-8, x, None, 0, None)
+    with pytest.raises(OverflowError):
+        m.adamw_step(*plan, 1e-3, 0.9, 0.999, 1e-8, 10 ** 40, x, 0, None)
