@@ -1301,12 +1301,12 @@ static Choice choose(int64_t m_tiles, int N, int nk, bool glu, const int* cluste
 // where the work is long and a set-up does not count (8,192 x 4,096 x 7,168 with
 // SiLU: 566 us, in one launch 577; 4,096 x 1,024 x 14,336 still 148, in one 131).
 constexpr double kBothSaves = 8., kBothMax = 1000.;
-static Choice choose_both(int64_t m_tiles, int N, int nk, int64_t m_tiles2, int N2, int nk2) {
-    const int64_t slots = g_max_clusters[0];
+static Choice choose_both(int64_t m_tiles, int N, int nk, int64_t m_tiles2, int N2, int nk2, const int* clusters) {
+    const int64_t slots = clusters[0];
     Choice best{256, 1, 1e300};
     for (int bn : kWidths) {
         const int64_t mid = m_tiles * ((N + bn - 1) / bn), total = mid + m_tiles2 * ((N2 + bn - 1) / bn);
-        if (bn == 64 && total > g_max_clusters[1]) continue;
+        if (bn == 64 && total > clusters[1]) continue;
         double cost = 0.;
         for (int64_t i : {(int64_t)0, mid % slots, total % slots}) {      // the shares change there
             const int64_t n = (std::max<int64_t>(mid - i, 0) + slots - 1) / slots;
@@ -1316,6 +1316,8 @@ static Choice choose_both(int64_t m_tiles, int N, int nk, int64_t m_tiles2, int 
         cost += kEpilogue * bn;
         if (cost < best.cost) best = {bn, 1, cost};
     }
+    const double two = choose(m_tiles, N, nk, false, clusters).cost + choose(m_tiles2, N2, nk2, false, clusters).cost;
+    if (best.cost > kBothMax || best.cost > two + kBothSaves) best.bn = 0;      // two launches
     return best;
 }
 
@@ -1387,6 +1389,17 @@ static moe_status_t product_both(const Mat& x, const Mat& w, const Mat& dz, Para
     return MOE_OK;
 }
 
+// Twice the parts save nk / (2 splits) k-steps and lengthen the swap by rows x splits
+// (128 x 2,048 x 2,048: 7.6 us in four parts, 9.9 in eight; 128 x 7,168 x 512: 11.8, 9.8),
+// the more the fuller the machine is (128 x 4,096 x 4,096: 13.3 in four, 15.2 in eight).
+static int few_splits(int64_t tiles, int rows, int nk, int sms) {
+    int splits = 1;
+    while (splits < 8 && tiles * splits * 2 <= 2 * sms && nk >= 8 * splits &&
+           (tiles * splits * 2 <= sms ? 40 : 16) * nk > rows * splits * splits)
+        splits *= 2;
+    return splits;
+}
+
 // Few rows: see k_dense_few.  The product D[M, N] = x op(W), W's columns
 // (W_MN) or rows in tiles of 128 (GLU: 64 gate and 64 up columns).
 template <bool W_MN, int EPI>
@@ -1402,13 +1415,7 @@ static moe_status_t product_few(const Mat& x, const Mat& w, Params p, cudaStream
     p.timeout_ns = 2000000000ull;
     const int64_t tiles = (int64_t)p.m_tiles * p.n_tiles;
     const int sms = device_sm_count();
-    s.splits = 1;
-    // Twice the parts save nk / (2 splits) k-steps and lengthen the swap by rows x splits
-    // (128 x 2,048 x 2,048: 7.6 us in four parts, 9.9 in eight; 128 x 7,168 x 512: 11.8, 9.8),
-    // the more the fuller the machine is (128 x 4,096 x 4,096: 13.3 in four, 15.2 in eight)
-    while (s.splits < 8 && tiles * s.splits * 2 <= 2 * sms && p.nk >= 8 * s.splits &&
-           (tiles * s.splits * 2 <= sms ? 40 : 16) * p.nk > s.rows * s.splits * s.splits)
-        s.splits *= 2;
+    s.splits = few_splits(tiles, s.rows, p.nk, sms);
     MOE_REQUIRE(tiles * s.splits <= 0x7FFFFFFFLL, MOE_ERR_UNSUPPORTED);
     CUtensorMap tmW, tmX;
     MOE_REQUIRE(make_bf16_map(&tmW, w.p, w.rows, w.cols, w.ld, W_MN ? TK : 128) &&
@@ -1519,10 +1526,8 @@ static moe_status_t gradients(const void* dz, int64_t lddz, const void* x, int64
         MOE_REQUIRE(g_max_clusters[0] > 0, MOE_ERR_NOT_INITIALIZED);
         p.m_tiles = (int)((M + TM - 1) / TM), p.nk = (N + TK - 1) / TK;
         q.m_tiles = (int)((K + TM - 1) / TM), q.nk = (int)((M + TK - 1) / TK);
-        const Choice c = choose_both(p.m_tiles, p.N, p.nk, q.m_tiles, q.N, q.nk);
-        const double two = choose(p.m_tiles, p.N, p.nk, false, g_max_clusters).cost +
-                           choose(q.m_tiles, q.N, q.nk, false, g_max_clusters).cost;
-        if (c.cost <= kBothMax && c.cost <= two + kBothSaves)
+        const Choice c = choose_both(p.m_tiles, p.N, p.nk, q.m_tiles, q.N, q.nk, g_max_clusters);
+        if (c.bn > 0)
             return f32 ? product_both<EPI_F32>(mx, mw, mz, p, q, c.bn, s)
                        : product_both<EPI_PLAIN>(mx, mw, mz, p, q, c.bn, s);
     }
@@ -1654,18 +1659,28 @@ extern "C" moe_status_t gated_ffn_bwd(const void* dh, int64_t lddh, const void* 
 
 extern "C" moe_status_t moe_selftest_dense_plan(int product, int64_t M, int64_t N, int64_t K, const int* clusters,
                                                 moe_dense_plan_t* plan) {
-    MOE_REQUIRE(plan && product >= MOE_DENSE_FWD && product <= MOE_DENSE_WGRAD, MOE_ERR_INVALID_ARG);
+    MOE_REQUIRE(plan && product >= MOE_DENSE_FWD && product <= MOE_DENSE_BACKWARD, MOE_ERR_INVALID_ARG);
     MOE_REQUIRE(M >= 1 && N >= 1 && K >= 1, MOE_ERR_INVALID_ARG);
     MOE_REQUIRE(M <= 0x7FFFFF00LL && size_ok(N) && size_ok(K), MOE_ERR_UNSUPPORTED);
     *plan = {};
-    if (product != MOE_DENSE_WGRAD && few_rows(M, K)) {
+    const int* slots = clusters ? clusters : g_max_clusters;
+    const int sms = clusters ? 2 * clusters[0] : device_sm_count();
+    const bool glu = product == MOE_DENSE_GATED;
+    const int nk = (int)((K + TK - 1) / TK);
+    if (product == MOE_DENSE_BACKWARD ? few_rows(M, N) : product != MOE_DENSE_WGRAD && few_rows(M, K)) {
         plan->few_rows = 1;
+        if (product == MOE_DENSE_BACKWARD) return MOE_OK;
+        MOE_REQUIRE(sms > 0, clusters ? MOE_ERR_INVALID_ARG : MOE_ERR_NOT_INITIALIZED);
+        plan->few_parts = few_splits(glu ? (N + 63) / 64 : (N + 127) / 128, (int)(M + 15) / 16 * 16, nk, sms);
         return MOE_OK;
     }
-    const int* slots = clusters ? clusters : g_max_clusters;
     MOE_REQUIRE(slots[0] > 0, clusters ? MOE_ERR_INVALID_ARG : MOE_ERR_NOT_INITIALIZED);
-    const bool glu = product == MOE_DENSE_GATED;
-    const Choice c = choose((M + TM - 1) / TM, (int)N, (int)((K + TK - 1) / TK), glu, slots);
+    if (product == MOE_DENSE_BACKWARD) {
+        plan->tile_cols = choose_both((M + TM - 1) / TM, (int)K, (int)((N + TK - 1) / TK), (K + TM - 1) / TM, (int)N,
+                                      (int)((M + TK - 1) / TK), slots).bn;
+        return MOE_OK;
+    }
+    const Choice c = choose((M + TM - 1) / TM, (int)N, nk, glu, slots);
     plan->tile_cols = c.bn;
     plan->parts = c.splits;
     if (c.splits > 1) {

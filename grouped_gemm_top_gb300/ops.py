@@ -38,7 +38,7 @@ MOE_B_GNK, MOE_B_NGK, MOE_B_SF_TILE224 = 0, 1, 2
 MOE_SF_ATOMS, MOE_SF_TILE224, MOE_SF_CANONICAL, MOE_SF_TILE224_AND_ATOMS = 0, 1, 2, 3
 MOE_TYPE_BF16, MOE_TYPE_F32 = 0, 1
 MOE_ACT_NONE, MOE_ACT_RELU, MOE_ACT_GELU, MOE_ACT_SILU = range(4)
-MOE_DENSE_FWD, MOE_DENSE_GATED, MOE_DENSE_DGRAD, MOE_DENSE_WGRAD = range(4)
+MOE_DENSE_FWD, MOE_DENSE_GATED, MOE_DENSE_DGRAD, MOE_DENSE_WGRAD, MOE_DENSE_BACKWARD = range(5)
 MOE_GEMM_KERNEL_AUTO, MOE_GEMM_KERNEL_1SM, MOE_GEMM_KERNEL_1SM_N128 = 0, 1, 2
 MOE_GEMM_KERNEL_PAIR, MOE_GEMM_KERNEL_PAIR_N128 = 3, 4
 (MOE_OP_ROUTE_TOPK, MOE_OP_PERMUTE, MOE_OP_GROUP_QUANTIZE, MOE_OP_GATHER_QUANTIZE, MOE_OP_GROUPED_GEMM,
@@ -73,7 +73,8 @@ class GemmOpts(ctypes.Structure):
 
 class DensePlan(ctypes.Structure):
     """moe_dense_plan_t (include/moe.h)."""
-    _fields_ = [(k, ctypes.c_int) for k in ("few_rows", "tile_cols", "parts", "swap_bytes", "box_at", "box_bytes")]
+    _fields_ = [(k, ctypes.c_int) for k in ("few_rows", "tile_cols", "parts", "swap_bytes", "box_at", "box_bytes",
+                                           "few_parts")]
 
 
 class AdamWTensor(ctypes.Structure):

@@ -924,18 +924,27 @@ MOE_API moe_status_t gated_ffn_bwd(const void* dh, int64_t lddh, const void* a, 
 /*
  * moe_selftest_dense_plan (host only) -- how the product D[M, N] of depth K
  * is launched: forward (MOE_DENSE_FWD; MOE_DENSE_GATED: N = f), input gradient
- * or weight gradient, each asked for alone.  clusters: how many clusters of 2,
- * 4, 6 and 8 CTAs run at a time, or NULL for the device's (after moe_init).
- * For tests: the sizes that reach a form, and its shared memory.
+ * or weight gradient, each asked for alone; MOE_DENSE_BACKWARD: both gradients
+ * of a layer of M rows, N outputs and K inputs.  clusters: how many clusters
+ * of 2, 4, 6 and 8 CTAs run at a time, or NULL for the device's (after
+ * moe_init).  For tests: the sizes that reach a form, and its shared memory.
  */
-typedef enum { MOE_DENSE_FWD = 0, MOE_DENSE_GATED = 1, MOE_DENSE_DGRAD = 2, MOE_DENSE_WGRAD = 3 } moe_dense_product_t;
+typedef enum {
+    MOE_DENSE_FWD = 0,
+    MOE_DENSE_GATED = 1,
+    MOE_DENSE_DGRAD = 2,
+    MOE_DENSE_WGRAD = 3,
+    MOE_DENSE_BACKWARD = 4
+} moe_dense_product_t;
 typedef struct {
-    int few_rows;        /* 1: the kernel for few rows of x (the other fields are 0) */
-    int tile_cols;       /* columns of a CTA pair's tile of 256 rows (gated: gate and up columns) */
+    int few_rows;        /* 1: the kernel for few rows of x (both gradients: the input gradient's) */
+    int tile_cols;       /* columns of a CTA pair's tile of 256 rows (gated: gate and up columns); both
+                            gradients: of the one launch of both, 0 when they take two */
     int parts;           /* of K, each by one pair of a cluster; of parts > 1, in bytes of shared memory: */
     int swap_bytes;      /* what the other parts send, from 0 on */
     int box_at;          /* where the output boxes of the 8 epilogue warps begin */
     int box_bytes;       /* of one warp */
+    int few_parts;       /* few rows: parts of K, each by one CTA of a cluster */
 } moe_dense_plan_t;
 MOE_API moe_status_t moe_selftest_dense_plan(int product, int64_t M, int64_t N, int64_t K, const int* clusters,
                                              moe_dense_plan_t* plan);

@@ -57,7 +57,7 @@ def test_gated_256_columns_in_three_parts_is_reached(ops):
 
 
 def test_refusals(ops):
-    for bad in ((4, 256, 256, 256), (-1, 256, 256, 256), (0, 0, 256, 256), (0, 256, 0, 256), (0, 256, 256, 0)):
+    for bad in ((5, 256, 256, 256), (-1, 256, 256, 256), (0, 0, 256, 256), (0, 256, 0, 256), (0, 256, 256, 0)):
         with pytest.raises(ops.MoEError) as e:
             ops.moe_selftest_dense_plan(*bad, SLOTS[0])
         assert e.value.status == ops.MOE_ERR_INVALID_ARG, bad
@@ -66,3 +66,17 @@ def test_refusals(ops):
     assert e.value.status == ops.MOE_ERR_UNSUPPORTED
     assert ops.lib.moe_selftest_dense_plan(0, 256, 256, 256, None, None) == ops.MOE_ERR_INVALID_ARG
     assert ops.moe_selftest_dense_plan(0, 4, 256, 256, SLOTS[0]).few_rows == 1
+
+
+@pytest.mark.parametrize("slots", SLOTS[:4])
+def test_both_gradients_and_few_rows(ops, slots):
+    """One launch of both gradients in every tile width, two launches for long
+    work; few rows in 1, 2, 4 and 8 parts."""
+    sizes = [(m, n, k) for m in (129, 256, 1000, 4096, 8192) for n in (64, 512, 1024, 2048, 4096, 8192) for k in (64, 512, 2048, 4096)]
+    widths = {ops.moe_selftest_dense_plan(ops.MOE_DENSE_BACKWARD, *s, slots).tile_cols for s in sizes}
+    assert {0, 64, 128, 256} <= widths <= {0, 64, 128, 192, 224, 256}
+    assert ops.moe_selftest_dense_plan(ops.MOE_DENSE_BACKWARD, 32, 512, 512, slots).few_rows == 1
+    for product in (ops.MOE_DENSE_FWD, ops.MOE_DENSE_GATED, ops.MOE_DENSE_DGRAD):
+        parts = {ops.moe_selftest_dense_plan(product, m, n, k, slots).few_parts for m in (1, 64) for n in (128, 4096, 65536)
+                 for k in (64, 512, 1024, 4096)}
+        assert parts == {1, 2, 4, 8}

@@ -149,3 +149,67 @@ def test_weight_gradient(ops, dtype):
             ops.linear_bwd(dy, x, w, want_dx=False, dw=dw, err=err)
             assert torch.equal(dw, first), what
         assert untouched(dw) and int(err) == 0, what
+
+
+def test_both_gradients_in_one_launch(ops):
+    """Every tile width of the launch that computes dx and dw."""
+    best = {}
+    for m in (256, 300, 512, 1024, 2048, 4096, 8192):
+        for n in (64, 320, 512, 1024, 1536, 2048, 4096, 7168):
+            for k in (64, 320, 512, 1024, 1536, 2048, 4096):
+                size = (m - 7, n - 3, k - 1)
+                w = ops.moe_selftest_dense_plan(ops.MOE_DENSE_BACKWARD, *size).tile_cols
+                if w and (w not in best or m * n * k < best[w][0]):
+                    best[w] = (m * n * k, size)
+    assert {64, 128, 256} <= set(best)
+    for w, (_, (m, n, k)) in sorted(best.items()):
+        for dtype in (BF, F):
+            what = (w, m, n, k, dtype)
+            dy, x, wt = mat(m, n, 1), mat(m, k, 2), mat(k, n, 3, n ** -0.5)
+            dx, dw, err = mat(m, k, 4), mat(k, n, 5, dtype=dtype), torch.zeros(1, dtype=torch.int32, device="cuda")
+            ops.linear_bwd(dy, x, wt, dx=dx, dw=dw, err=err)
+            want, size = product(dy, wt.t())
+            close(dx, want, acc(n) * size + want.abs() * HALF, ("dx", what))
+            want, size = product(x.t(), dy)
+            close(dw, want, acc(m) * size + want.abs() * (HALF if dtype == BF else 0), ("dw", what))
+            first = dx.clone(), dw.clone()
+            for _ in range(4):
+                ops.linear_bwd(dy, x, wt, dx=dx, dw=dw, err=err)
+                assert torch.equal(dx, first[0]) and torch.equal(dw, first[1]), what
+            assert untouched(dx) and untouched(dw) and int(err) == 0, what
+
+
+@pytest.mark.parametrize("m", [1, 13, 64, 128])
+def test_few_rows_in_every_number_of_parts(ops, m):
+    seen = {"f": set(), "g": set(), "d": set()}
+    for k in (63, 511, 1023, 4095):
+        for n in (120, 4099):
+            what = (m, n, k)
+            x, w, b, r, y, z = mat(m, k, 1), mat(k, n, 2, k ** -0.5), mat(1, n, 3)[0], mat(m, n, 4), mat(m, n, 5), mat(m, n, 6)
+            err = torch.zeros(1, dtype=torch.int32, device="cuda")
+            plain, size = product(x, w)
+            wz, ez = plain + b.double(), acc(k) * (size + b.double().abs())
+            wy = ACTS["gelu"](wz) + r.double()
+            ops.linear_fwd(x, w, b, "gelu", r, y=y, z=z, err=err)
+            close(z, wz, ez + wz.abs() * HALF, ("z", what))
+            close(y, wy, 1.2 * ez + wz.abs() * WORK + r.double().abs() * 2.0 ** -22 + wy.abs() * (HALF + 2.0 ** -22), ("y", what))
+            seen["f"].add(ops.moe_selftest_dense_plan(ops.MOE_DENSE_FWD, m, n, k).few_parts)
+            f = n // 8 * 8
+            w1, h, a = mat(k, 2 * f, 7, k ** -0.5), mat(m, f, 8), mat(m, 2 * f, 9)
+            ops.gated_ffn_fwd(x, w1, h=h, a=a, err=err)
+            wa, size = product(x, w1)
+            ea = acc(k) * size
+            close(a, wa, ea + wa.abs() * HALF, ("a", what))
+            g, u, eg, eu = wa[:, :f], wa[:, f:], ea[:, :f], ea[:, f:]
+            wh = ACTS["silu"](g) * u
+            close(h, wh, 1.2 * eg * (u.abs() + eu) + ACTS["silu"](g).abs() * eu + (g * u).abs() * WORK + wh.abs() * HALF, ("h", what))
+            seen["g"].add(ops.moe_selftest_dense_plan(ops.MOE_DENSE_GATED, m, f, k).few_parts)
+            # the input gradient's depth is dy's width: n outputs from depth k
+            dy, wt, dx = mat(m, k, 10), mat(n, k, 11, k ** -0.5), mat(m, n, 12)
+            ops.linear_bwd(dy, mat(m, n, 13), wt, want_dw=False, dx=dx, err=err)
+            want, size = product(dy, wt.t())
+            close(dx, want, acc(k) * size + want.abs() * HALF, ("dx", what))
+            seen["d"].add(ops.moe_selftest_dense_plan(ops.MOE_DENSE_DGRAD, m, n, k).few_parts)
+            assert all(untouched(t) for t in (y, z, h, a, dx)) and int(err) == 0, what
+    if m <= 13:
+        assert all(s == {1, 2, 4, 8} for s in seen.values()), seen
