@@ -292,12 +292,14 @@ __device__ __forceinline__ bool in_ring(const Entry& e, int64_t tile) {
 // 32 bits: 28 bytes and about 30 instructions an element; loads straight into
 // registers, three CTAs an SM (176 M elements, fp32 p, bf16 g and copy: 751 us,
 // 6.57 TB/s, 97 % of the copy bandwidth; through a ring in shared memory 805 us).
-// 8 bits: 10 bytes and about 80 instructions an element (a third of them the
-// rounding of the codes), which is what bounds it.  Loads into registers covered
-// less than half of the memory's latency at the occupancy those leave, so
-// bulk copies bring the next whole tiles into a ring in shared memory
-// while the CTA works on one (130 M elements, bf16 p and g: 344 us, 3.8 TB/s;
-// 410 us without the ring).
+// 8 bits: 10 bytes and 73 instructions an element (a third of them the rounding
+// of the codes).  Loads into registers covered less than half of the memory's
+// latency at the occupancy those leave, so bulk copies bring the next whole
+// tiles into a ring in shared memory while the CTA works on one (130 M
+// elements, bf16 p and g: 340 us, 3.8 TB/s; 410 us without the ring, when that
+// was measured).  Nothing is at its limit: 70 % of the issue slots and 45 % of the
+// memory's rate are used, a sixth of the warps' time goes at the CTA's barrier
+// and as much waiting for the math pipes; with every slot used it would be 240 us.
 template <typename PT, typename GT, int BITS>
 __global__ void __launch_bounds__(kThreads, (Stage<PT, GT, BITS>::CTAS)) k_adamw(const Params p) {
     using S = Stage<PT, GT, BITS>;
@@ -438,9 +440,9 @@ __global__ void __launch_bounds__(kThreads, (Stage<PT, GT, BITS>::CTAS)) k_adamw
                 if (BITS == 32) sqrt2_any(v2).get(u[i], u[i + 1]);
             }
             if (BITS == 8) {
-                // bound by issue: four instructions an element fewer while none of the
-                // eight is small (with 32 bits, where they are free, small steps gain
-                // 0.2 us without the branch)
+                // instructions count here: four an element fewer while none of the eight
+                // is small (with 32 bits, bound by memory, they are free, and the smallest
+                // steps take 4.8 us without the branch, 5.1 with it)
                 float least = v[0];
 #pragma unroll
                 for (int i = 1; i < 8; ++i) least = fminf(least, v[i]);

@@ -27,10 +27,11 @@
 // bits on every run.
 //
 // Bound by the tensor cores under the power cap when the product is large
-// (4,096 x 4,096 x 4,096 73 us, 1.87 PFLOP/s; gated 2,003 x 4,096 x 2 * 14,336 240 us,
-// 1.96), by set-up, first loads and last stores when it is small (512 x 512 x
-// 512 4.3 us).  Rows that start at no multiple of 128 bytes cost the TMA two
-// lines for one: 4,096 x 4,096 x 4,096 then 105 to 120 us.
+// (4,096 x 4,096 x 4,096 73 us, 1.87 PFLOP/s; gated 2,003 x 4,096 x 2 * 14,336 284 to
+// 293 us, 1.61 to 1.66, from card to card, 240 in bursts too short for the cap),
+// by set-up, first loads and last stores when it is small (512 x 512 x 512 4.3 us).
+// Rows that start at no multiple of 128 bytes cost the TMA two lines for one:
+// 4,096 x 4,096 x 4,096 then 105 to 120 us.
 //
 // Warps: 0 TMA, 1 MMA (of the leader CTA), 4-11 epilogue.  All waits are
 // bounded, as in the grouped GEMM kernels.

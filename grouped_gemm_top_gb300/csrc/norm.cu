@@ -97,7 +97,8 @@ __device__ __forceinline__ float row_sum(float v, bool block, float* s_part, int
 
 // Smallest e (as the byte e + 127) with amax <= 448 * 2^e, for an fp32 amax:
 // amax = M * 2^q with M in [1, 2) fits e = q - 8 when M <= 1.75, e = q - 7
-// otherwise.  Zero and fp32-subnormal amax give byte 0, NaN and infinity 247 or 248.
+// otherwise.  Zero and fp32-subnormal amax give byte 0, infinity 247 (a NaN is
+// no part of a block's amax, and has a NaN code).
 __device__ __forceinline__ uint32_t e8m0_byte_f32(float amax) {
     const uint32_t bits = __float_as_uint(amax);
     const int be = (int)((bits >> 23) & 0xFF);

@@ -224,7 +224,8 @@ typedef enum {
 
 /* Version of this ABI (major*100 + minor): 200.  2.0 grew moe_gemm_opts_t
  * by wgrad_rows_lo / wgrad_rows_hi (a caller built against the 1.x struct
- * passes too few bytes) and added MOE_SF_TILE224_AND_ATOMS. */
+ * passes too few bytes) and added MOE_SF_TILE224_AND_ATOMS.  Calls that are
+ * only added (the dense operators) leave it as it is. */
 MOE_API int moe_abi_version(void);
 
 /* Human-readable name of a status code (static string). */
@@ -833,7 +834,9 @@ typedef enum { MOE_TYPE_BF16 = 0, MOE_TYPE_F32 = 1 } moe_type_t;
  *        MOE_SF_ATOMS (N % 128 == 0): codes [ceil128(M), N], scales
  *        ceil128(M) * N / 32 bytes in the atom layout; the rows from M on get
  *        zero codes and scale bytes, so the pair is an operand of
- *        grouped_gemm_mxfp8 as it is.  MOE_SF_CANONICAL (N % 32 == 0): codes
+ *        grouped_gemm_mxfp8 as it is (one group: an MXFP8 projection of all
+ *        rows; the MoE layer itself gathers bf16 rows and quantizes after
+ *        that).  MOE_SF_CANONICAL (N % 32 == 0): codes
  *        [M, N], scales [M, N / 32].  codes 16-byte aligned.
  * The sum, the norm and y are fp32 until stored: the norm is that of the
  * unrounded sum, and the codes are those of the unrounded y (the scale rule
