@@ -16,6 +16,7 @@ cudaError_t gemm_init_driver();      // gemm.cu
 cudaError_t dense_set_attributes();  // dense.cu
 cudaError_t norm_set_attributes();   // norm.cu
 cudaError_t adamw_set_attributes();  // adamw.cu
+cudaError_t distill_set_attributes();  // distill.cu
 void route_scratch_forget(int device);  // route.cu
 
 int device_sm_count() {
@@ -47,6 +48,7 @@ extern "C" const char* moe_status_string(int s) {
         case MOE_ERR_BAD_OFFSETS: return "group offsets not monotone, not 128-aligned or beyond the buffer";
         case MOE_ERR_DEVICE_TIMEOUT: return "a bounded wait inside a kernel timed out";
         case MOE_ERR_CAPACITY: return "padded rows exceed the buffer capacity";
+        case MOE_ERR_BAD_INDEX: return "token index outside the vocabulary";
         default: return "unknown status";
     }
 }
@@ -75,6 +77,7 @@ extern "C" moe_status_t moe_init(int device) {
     if (dense_set_attributes() != cudaSuccess) return MOE_ERR_CUDA;
     if (norm_set_attributes() != cudaSuccess) return MOE_ERR_CUDA;
     if (adamw_set_attributes() != cudaSuccess) return MOE_ERR_CUDA;
+    if (distill_set_attributes() != cudaSuccess) return MOE_ERR_CUDA;
     g_sm_count[device] = sms;
     g_init[device] = true;
     return MOE_OK;

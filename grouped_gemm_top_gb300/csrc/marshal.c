@@ -360,6 +360,79 @@ static PyObject* adamw(PyObject* self, PyObject* const* a, Py_ssize_t k) {
     MAKE(adamw_step(table, (int)tensors, tiles, (int)pt, (int)gt, (int)bits, &o, st));
 }
 
+/* a[0..3]: logits, idx, teacher, teacher_lse, a[4]: temperature */
+typedef struct {
+    Mat x, idx, t;
+    void* lse;
+    float tau;
+} Distill;
+
+static int distill_args(PyObject* const* a, long long dev, Distill* o) {
+    int r;
+    if ((r = mat(a[0], dev, BF16 | F32, -1, -1, &o->x)) <= 0) return r;
+    if ((r = mat(a[1], dev, I32, o->x.m, -1, &o->idx)) <= 0) return r;
+    if ((r = mat(a[2], dev, BF16 | F32, o->x.m, o->idx.n, &o->t)) <= 0) return r;
+    if ((r = flat(a[3], dev, F32, o->x.m, &o->lse, NULL)) <= 0) return r;
+    const double tau = PyFloat_AsDouble(a[4]);
+    if (tau == -1. && PyErr_Occurred()) return -1;
+    o->tau = (float)tau;
+    return a[0] != Py_None && a[1] != Py_None && a[2] != Py_None && o->x.n <= INT32_MAX && o->idx.n <= INT32_MAX;
+}
+
+/* (logits, idx, teacher, teacher_lse, temperature, loss, stats, err, stream) */
+static PyObject* dist_fwd(PyObject* self, PyObject* const* a, Py_ssize_t k) {
+    long long dev;
+    Distill d;
+    void *loss, *stats, *err, *st;
+    TRY(arity(k, 9));
+    TRY(current_device(&dev));
+    TRY(distill_args(a, dev, &d));
+    TRY(flat(a[5], dev, F32, d.x.m, &loss, NULL));
+    TRY(flat(a[6], dev, F32, 3 * d.x.m, &stats, NULL));
+    TRY(flat(a[7], dev, I32, 1, &err, NULL));
+    TRY(handle(a[8], dev, &st));
+    MAKE(distill_loss_fwd(d.x.p, d.x.type, d.x.ld, d.idx.p, d.idx.ld, d.t.p, d.t.type, d.t.ld, d.lse, d.tau, d.x.m,
+                          (int)d.x.n, (int)d.idx.n, loss, stats, err, st));
+}
+
+/* (logits, idx, teacher, teacher_lse, temperature, dloss, stats, dlogits, err, stream) */
+static PyObject* dist_bwd(PyObject* self, PyObject* const* a, Py_ssize_t k) {
+    long long dev;
+    Distill d;
+    Mat dx;
+    void *dloss, *stats, *err, *st;
+    TRY(arity(k, 10));
+    TRY(current_device(&dev));
+    TRY(distill_args(a, dev, &d));
+    TRY(flat(a[5], dev, F32, d.x.m, &dloss, NULL));
+    TRY(flat(a[6], dev, F32, 3 * d.x.m, &stats, NULL));
+    TRY(mat(a[7], dev, BF16 | F32, d.x.m, d.x.n, &dx));
+    TRY(flat(a[8], dev, I32, 1, &err, NULL));
+    TRY(a[5] != Py_None && a[6] != Py_None && a[7] != Py_None && dx.type == d.x.type);
+    TRY(handle(a[9], dev, &st));
+    MAKE(distill_loss_bwd(dloss, d.x.p, d.x.type, d.x.ld, d.idx.p, d.idx.ld, d.t.p, d.t.type, d.t.ld, stats, d.lse,
+                          d.tau, d.x.m, (int)d.x.n, (int)d.idx.n, dx.p, dx.ld, err, st));
+}
+
+/* (logits, idx, teacher, teacher_lse, temperature, dloss, loss, dlogits, err, stream) */
+static PyObject* dist_both(PyObject* self, PyObject* const* a, Py_ssize_t k) {
+    long long dev;
+    Distill d;
+    Mat dx;
+    void *dloss, *loss, *err, *st;
+    TRY(arity(k, 10));
+    TRY(current_device(&dev));
+    TRY(distill_args(a, dev, &d));
+    TRY(flat(a[5], dev, F32, d.x.m, &dloss, NULL));
+    TRY(flat(a[6], dev, F32, d.x.m, &loss, NULL));
+    TRY(mat(a[7], dev, BF16 | F32, d.x.m, d.x.n, &dx));
+    TRY(flat(a[8], dev, I32, 1, &err, NULL));
+    TRY(a[5] != Py_None && a[7] != Py_None && dx.type == d.x.type);
+    TRY(handle(a[9], dev, &st));
+    MAKE(distill_loss(dloss, d.x.p, d.x.type, d.x.ld, d.idx.p, d.idx.ld, d.t.p, d.t.type, d.t.ld, d.lse, d.tau, d.x.m,
+                      (int)d.x.n, (int)d.idx.n, loss, dx.p, dx.ld, err, st));
+}
+
 /* (bfloat16, float32, uint8, float8_e4m3fn, int32, current device, current stream's handle) */
 static PyObject* setup(PyObject* self, PyObject* const* a, Py_ssize_t k) {
     TRY(arity(k, 7));
@@ -378,6 +451,9 @@ static PyMethodDef methods[] = {FAST("setup", setup),
                                 FAST("gated_ffn_fwd", ffn_fwd),
                                 FAST("gated_ffn_bwd", ffn_bwd),
                                 FAST("adamw_step", adamw),
+                                FAST("distill_loss_fwd", dist_fwd),
+                                FAST("distill_loss_bwd", dist_bwd),
+                                FAST("distill_loss", dist_both),
                                 {NULL, NULL, 0, NULL}};
 static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "_marshal", NULL, -1, methods, NULL, NULL, NULL, NULL};
 

@@ -28,6 +28,7 @@ MOE_ERR_BAD_EXPERT = 16
 MOE_ERR_BAD_OFFSETS = 17
 MOE_ERR_DEVICE_TIMEOUT = 18
 MOE_ERR_CAPACITY = 19
+MOE_ERR_BAD_INDEX = 20
 
 MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
 MOE_QUANT_ROWWISE, MOE_QUANT_COLWISE_GROUPED, MOE_QUANT_COLWISE_GLU = 0, 1, 2
@@ -58,7 +59,7 @@ EXPORTS = [
     "rmsnorm_residual_fwd", "rmsnorm_bwd_workspace_size", "rmsnorm_residual_bwd",
     "adamw_plan_bytes", "adamw_plan_encode", "adamw_step",
     "linear_fwd", "linear_bwd_workspace_size", "linear_bwd", "gated_ffn_fwd", "gated_ffn_bwd",
-    "moe_selftest_dense_plan",
+    "moe_selftest_dense_plan", "distill_loss_fwd", "distill_loss_bwd", "distill_loss",
 ]
 
 _vp, _i32, _i64, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t
@@ -167,6 +168,12 @@ _SIGS = {
     "adamw_plan_bytes": (_sz, [_i32]),
     "adamw_plan_encode": (_i32, [_vp, _i32, _i32, _i32, _i32, _vp, ctypes.POINTER(_i64)]),
     "adamw_step": (_i32, [_vp, _i32, _i64, _i32, _i32, _i32, _vp, _vp]),
+    "distill_loss_fwd": (_i32, [_vp, _i32, _i64, _vp, _i64, _vp, _i32, _i64, _vp, _f32, _i64, _i32, _i32, _vp, _vp, _vp,
+                                _vp]),
+    "distill_loss_bwd": (_i32, [_vp, _vp, _i32, _i64, _vp, _i64, _vp, _i32, _i64, _vp, _vp, _f32, _i64, _i32, _i32, _vp,
+                                _i64, _vp, _vp]),
+    "distill_loss": (_i32, [_vp, _vp, _i32, _i64, _vp, _i64, _vp, _i32, _i64, _vp, _f32, _i64, _i32, _i32, _vp, _vp, _i64,
+                            _vp, _vp]),
 }
 
 
@@ -892,3 +899,53 @@ def adamw_step(plan, lr, betas=(0.9, 0.999), eps=1e-8, step=1, grad_scale=None, 
     st = _marshal.adamw_step(*plan.args, lr, betas[0], betas[1], eps, step, grad_scale, seed, stream)
     if st:
         raise MoEError("adamw_step", st)
+
+
+# ------------------------------------------------------ distillation loss ----
+
+def distill_loss_fwd(logits, idx, teacher, teacher_lse=None, temperature=1.0, loss=None, stats=None, err=None,
+                     stream=None):
+    """Loss of every row of logits [M, V] (bfloat16 or float32) against the
+    teacher's top logits: idx [M, k] int32 (negative: not kept), teacher [M, k]
+    (bfloat16 or float32).  See include/moe.h.  Returns (loss [M], stats
+    [M, 3]), float32; the backward pass needs stats."""
+    fn = "distill_loss_fwd"
+    if loss is None or stats is None:
+        M, _ = _size(fn, logits)
+        loss = loss if loss is not None else _new((M,), torch.float32, logits, stream)
+        stats = stats if stats is not None else _new((M, 3), torch.float32, logits, stream)
+    st = _marshal.distill_loss_fwd(logits, idx, teacher, teacher_lse, temperature, loss, stats, err, stream)
+    if st:
+        raise MoEError(fn, st)
+    return loss, stats
+
+
+def distill_loss_bwd(dloss, logits, idx, teacher, stats, teacher_lse=None, temperature=1.0, dlogits=None, err=None,
+                     stream=None):
+    """Gradient of logits from dloss [M] (float32, of each row's loss) and the
+    forward call's stats; dlogits (of the logits' type) may be logits itself.
+    See include/moe.h.  Returns dlogits."""
+    fn = "distill_loss_bwd"
+    if dlogits is None:
+        M, V = _size(fn, logits)
+        dlogits = _new_rows(M, V, logits.dtype, logits, stream)
+    st = _marshal.distill_loss_bwd(logits, idx, teacher, teacher_lse, temperature, dloss, stats, dlogits, err, stream)
+    if st:
+        raise MoEError(fn, st)
+    return dlogits
+
+
+def distill_loss(dloss, logits, idx, teacher, teacher_lse=None, temperature=1.0, loss=None, dlogits=None,
+                 want_loss=True, err=None, stream=None):
+    """Loss of every row and gradient of logits in one pass, for a dloss [M]
+    that is known beforehand (the rows' weights in the training loss); dlogits
+    may be logits itself.  See include/moe.h.  Returns (loss, dlogits)."""
+    fn = "distill_loss"
+    if dlogits is None or (loss is None and want_loss):
+        M, V = _size(fn, logits)
+        dlogits = dlogits if dlogits is not None else _new_rows(M, V, logits.dtype, logits, stream)
+        loss = loss if loss is not None or not want_loss else _new((M,), torch.float32, logits, stream)
+    st = _marshal.distill_loss(logits, idx, teacher, teacher_lse, temperature, dloss, loss, dlogits, err, stream)
+    if st:
+        raise MoEError(fn, st)
+    return loss, dlogits

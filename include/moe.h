@@ -93,7 +93,8 @@ typedef enum {
     MOE_ERR_BAD_OFFSETS = 17,  /* group offsets not monotone / not 128-aligned /
                                   beyond the buffer                         */
     MOE_ERR_DEVICE_TIMEOUT = 18, /* a bounded wait inside a kernel gave up   */
-    MOE_ERR_CAPACITY = 19      /* padded rows exceed the buffer capacity     */
+    MOE_ERR_CAPACITY = 19,     /* padded rows exceed the buffer capacity     */
+    MOE_ERR_BAD_INDEX = 20     /* token index outside the vocabulary         */
 } moe_status_t;
 
 typedef enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score_t;
@@ -1007,6 +1008,50 @@ MOE_API moe_status_t adamw_plan_encode(const moe_adamw_tensor_t* t, int tensors,
                                        int state_bits, void* plan, int64_t* tiles);
 MOE_API moe_status_t adamw_step(void* plan, int tensors, int64_t tiles, int p_type, int g_type, int state_bits,
                                 const moe_adamw_opts_t* opts, void* stream);
+
+/*
+ * Distillation from a teacher's top logits.  For every row (token) of the
+ * student's logits x [M, V], with z = x / tau and q = softmax(z), and the k
+ * tokens idx [M, k] that the teacher kept with their logits t [M, k]:
+ *   p = softmax over the kept tokens of t / tau, or, when teacher_lse [M] (log
+ *       of the sum of exp(t / tau) over the teacher's whole vocabulary) is
+ *       given, exp(t / tau - teacher_lse); then rest = max(0, 1 - sum p) is held
+ *       against q_rest, the sum of q over the tokens that were not kept
+ *   loss = tau^2 (sum p (log p - log q) + rest (log rest - log q_rest))
+ *   dx = dloss * d loss / d x
+ * A negative idx is a token that was not kept; a row without any (or, without
+ * teacher_lse, with none above -inf) has loss 0 and gradient 0: padding, or a
+ * masked token.  An idx of V or more is taken as not kept and puts
+ * MOE_ERR_BAD_INDEX in err.  A token that occurs several times in a row has the sum
+ * of its probabilities.  Terms with p = 0 are 0; a rest without student tokens
+ * of any probability is dropped.  dloss = 0 gives a gradient of zeros whatever
+ * the row's logits are.  Infinities and NaN otherwise show in the results as the
+ * formulas have them.
+ *   x      x_type, any row stride and element-aligned address (16-byte units
+ *          that hold a row's ends are read whole); dx [M, V] of the same type, its
+ *          own stride, or x itself (same stride).
+ *   t      t_type; idx and t with row strides ldi, ldt; 1 <= k <= 1024.
+ *   loss [M], dloss [M] fp32 (dloss: gradient of the row's loss, a row's weight).
+ *   stats [M, 3] fp32: max x, and sums of exp((x - max x) / tau) over all tokens and
+ *          over those not kept (all, without teacher_lse): what the backward
+ *          pass needs of the forward pass.
+ *   tau    1e-6 .. 1e6.  V up to 720,882 (bf16), 360,442 (fp32).
+ * All sums are fp32.  distill_loss_fwd writes loss and stats, those that are
+ * not NULL; distill_loss_bwd dx from stats; distill_loss loss (may be NULL) and dx
+ * with one read of x.  One launch each, no workspace; every sum has a fixed
+ * order.  M = 0 does nothing.
+ */
+MOE_API moe_status_t distill_loss_fwd(const void* x, int x_type, int64_t ldx, const int32_t* idx, int64_t ldi,
+                                      const void* t, int t_type, int64_t ldt, const float* teacher_lse, float tau,
+                                      int64_t M, int V, int k, float* loss, float* stats, int32_t* err, void* stream);
+MOE_API moe_status_t distill_loss_bwd(const float* dloss, const void* x, int x_type, int64_t ldx, const int32_t* idx,
+                                      int64_t ldi, const void* t, int t_type, int64_t ldt, const float* stats,
+                                      const float* teacher_lse, float tau, int64_t M, int V, int k, void* dx,
+                                      int64_t lddx, int32_t* err, void* stream);
+MOE_API moe_status_t distill_loss(const float* dloss, const void* x, int x_type, int64_t ldx, const int32_t* idx,
+                                  int64_t ldi, const void* t, int t_type, int64_t ldt, const float* teacher_lse,
+                                  float tau, int64_t M, int V, int k, float* loss, void* dx, int64_t lddx,
+                                  int32_t* err, void* stream);
 
 #ifdef __cplusplus
 }
