@@ -34,7 +34,7 @@ using namespace gg;
 constexpr int MAX_K = 1024;              // tokens of the teacher
 constexpr int MAX_C = 8;                 // CTAs of a cluster
 constexpr int CHUNKS = 4;                // of a part, each with its own barriers
-constexpr int MAX_PART = 11264;          // 16-byte units of a part
+constexpr int MAX_PART = 8960;           // 16-byte units of a part
 constexpr float kLog2e = 1.4426950408889634f;
 enum { FWD = 1, BWD = 2, BOTH = 3 };
 
@@ -65,36 +65,41 @@ struct Teacher {
     float mass, rest, p_sum;        // mass = sum p + rest
     float fit, x_ref, t_lse;        // sum p ((t - max t) - (x - x_ref) / tau); log-sum-exp of t - max t
     float top_max, top_sum;         // of the kept tokens in this CTA's part
+    float dloss, m, s, s_rest;      // of the row (BWD: what the forward pass kept)
     int some;                       // 0: no teacher, loss and gradient are zero
 };
 
-// Shared memory: the part, then (two buffers each) a byte per 16-byte unit,
-// and of each of the teacher's tokens its column (bit 31: counted with an
-// earlier one; -1: none), its probability and the student's logit.
+// Rows that the teacher's warp may be ahead of: the loss alone is finished a
+// row late, under the next row's sums.
+constexpr int buffers(int mode) { return mode == FWD ? 4 : 2; }
+
+// Shared memory: the part, then (a buffer each) a byte per 16-byte unit, and
+// of each of the teacher's tokens its column (bit 31: counted with an earlier
+// one; -1: none), its probability and the student's logit.
 struct Smem {
     uint8_t* rows;
-    int part, k;
+    int part, k, nb;
     __device__ __forceinline__ uint8_t* bits(int b) const;
     __device__ __forceinline__ int* col(int b) const;
     __device__ __forceinline__ float* p(int b) const { return reinterpret_cast<float*>(col(b)) + k; }
     __device__ __forceinline__ float* x(int b) const { return p(b) + k; }
-    __device__ __forceinline__ uint8_t* fixed() const { return reinterpret_cast<uint8_t*>(col(2)); }
+    __device__ __forceinline__ uint8_t* fixed() const { return reinterpret_cast<uint8_t*>(col(nb)); }
 };
 struct Fixed {
-    unsigned long long bar[2 * CHUNKS + 6];
-    float4 mail[2][MAX_C];          // max, s, s_rest of the cluster's parts
-    float2 warp_part[8];
-    Teacher teacher[2];
+    unsigned long long bar[2 * CHUNKS + 14];
+    float4 mail[4][MAX_C];          // max, s, s_rest of the cluster's parts
+    float2 warp_part[2][8];
+    Teacher teacher[4];
     int abort_flag;
 };
 
 __host__ __device__ inline int bits_bytes(int part) { return (part + 15) / 16 * 16; }
-__host__ __device__ inline size_t smem_bytes(int part, int k) {
-    return (size_t)part * 16 + 2 * bits_bytes(part) + 24 * (size_t)((k + 3) / 4 * 4) + sizeof(Fixed);
+__host__ __device__ inline size_t smem_bytes(int part, int k, int nb) {
+    return (size_t)part * 16 + nb * (bits_bytes(part) + 12 * (size_t)((k + 3) / 4 * 4)) + sizeof(Fixed);
 }
 __device__ __forceinline__ uint8_t* Smem::bits(int b) const { return rows + 16 * part + b * bits_bytes(part); }
-__device__ __forceinline__ int* Smem::col(int b) const { return reinterpret_cast<int*>(bits(2)) + 3 * b * k; }
-static_assert(MAX_PART * 18 + 24 * MAX_K + sizeof(Fixed) <= 232448 && MAX_PART % 16 == 0, "shared memory budget");
+__device__ __forceinline__ int* Smem::col(int b) const { return reinterpret_cast<int*>(bits(nb)) + 3 * b * k; }
+static_assert(MAX_PART * 20 + 48 * MAX_K + sizeof(Fixed) <= 232448 && MAX_PART % 16 == 0, "shared memory budget");
 
 __device__ __forceinline__ uint32_t cluster_size() {
     uint32_t n;
@@ -111,13 +116,52 @@ __device__ __forceinline__ float ex2(float x) {
 __device__ __forceinline__ float e_of(float x, float m, float c) { return ex2((x - m) * c); }
 __device__ __forceinline__ float finite_max(float m) { return m == -INFINITY ? 0.f : m; }
 
+// Two fp32 at a time (the FMA pipe's packed form).
+typedef unsigned long long f2;
+__device__ __forceinline__ f2 pack(float a, float b) {
+    f2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void unpack(f2 v, float& a, float& b) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ f2 add2(f2 a, f2 b) {
+    f2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+    f2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+// e_of of two, for -m and c twice
+__device__ __forceinline__ f2 e_of2(f2 x, f2 neg_m, f2 c) {
+    float a, b;
+    unpack(mul2(add2(x, neg_m), c), a, b);
+    return pack(ex2(a), ex2(b));
+}
+
+// 16 bytes of logits, E of them: as they lie in memory, as pairs of fp32, their maximum.
 template <typename T>
-struct Unit;      // 16 bytes of logits
+struct Unit;
 template <>
 struct Unit<__nv_bfloat16> {
     static constexpr int E = 8;
-    static __device__ __forceinline__ void load(const uint8_t* p, float* f) {
-        unpack8(*reinterpret_cast<const uint4*>(p), f);
+    static __device__ __forceinline__ void pairs(const uint4& v, f2* f) {
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f[i] = pack(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
+    }
+    static __device__ __forceinline__ __nv_bfloat162 two(uint32_t w) { return *reinterpret_cast<__nv_bfloat162*>(&w); }
+    template <int N>
+    static __device__ __forceinline__ float max_of(const uint4* v) {
+        __nv_bfloat162 m = __hmax2(__hmax2(two(v[0].x), two(v[0].y)), __hmax2(two(v[0].z), two(v[0].w)));
+#pragma unroll
+        for (int n = 1; n < N; ++n)
+            m = __hmax2(m, __hmax2(__hmax2(two(v[n].x), two(v[n].y)), __hmax2(two(v[n].z), two(v[n].w))));
+        return fmaxf(__low2float(m), __high2float(m));
     }
     static __device__ __forceinline__ void store(__nv_bfloat16* p, const float* f) {
         *reinterpret_cast<uint4*>(p) = pack8(f);
@@ -130,9 +174,17 @@ struct Unit<__nv_bfloat16> {
 template <>
 struct Unit<float> {
     static constexpr int E = 4;
-    static __device__ __forceinline__ void load(const uint8_t* p, float* f) {
-        const float4 v = *reinterpret_cast<const float4*>(p);
-        f[0] = v.x, f[1] = v.y, f[2] = v.z, f[3] = v.w;
+    static __device__ __forceinline__ void pairs(const uint4& v, f2* f) {
+        f[0] = pack(__uint_as_float(v.x), __uint_as_float(v.y)), f[1] = pack(__uint_as_float(v.z), __uint_as_float(v.w));
+    }
+    template <int N>
+    static __device__ __forceinline__ float max_of(const uint4* v) {
+        float m = -INFINITY;
+#pragma unroll
+        for (int n = 0; n < N; ++n)
+            m = fmaxf(fmaxf(fmaxf(m, __uint_as_float(v[n].x)), fmaxf(__uint_as_float(v[n].y), __uint_as_float(v[n].z))),
+                      __uint_as_float(v[n].w));
+        return m;
     }
     static __device__ __forceinline__ void store(float* p, const float* f) {
         *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
@@ -140,12 +192,68 @@ struct Unit<float> {
     static __device__ __forceinline__ float one(const void* p, int64_t i) { return static_cast<const float*>(p)[i]; }
     static __device__ __forceinline__ float to(float f) { return f; }
 };
+// the elements that `out` (a bit each) names become -inf
+template <int E>
+__device__ __forceinline__ void leave_out(uint4& v, uint32_t out) {
+    uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (E == 4) {
+            if (out >> i & 1) w[i] = 0xFF800000u;
+        } else {
+            if (out >> (2 * i) & 1) w[i] = (w[i] & 0xFFFF0000u) | 0xFF80u;
+            if (out >> (2 * i + 1) & 1) w[i] = (w[i] & 0xFFFFu) | 0xFF800000u;
+        }
+    }
+    v = make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// A thread's running maximum and sum of exponentials (two accumulators of
+// two), N units at a time.
+struct Sum {
+    float m = -INFINITY;
+    f2 s[2] = {0ull, 0ull};
+    template <typename T, int N>
+    __device__ __forceinline__ void add(const uint4* v, float c) {
+        constexpr int E = Unit<T>::E;
+        const float um = Unit<T>::template max_of<N>(v);
+        if (um > m) {
+            const float r = e_of(m, um, c);
+            s[0] = mul2(s[0], pack(r, r)), s[1] = mul2(s[1], pack(r, r));
+            m = um;
+        }
+        const float ref = -finite_max(m);
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            f2 f[E / 2];
+            Unit<T>::pairs(v[n], f);
+#pragma unroll
+            for (int i = 0; i < E / 2; ++i) s[i & 1] = add2(s[i & 1], e_of2(f[i], pack(ref, ref), pack(c, c)));
+        }
+    }
+    __device__ __forceinline__ float total() const {
+        float a, b;
+        unpack(add2(s[0], s[1]), a, b);
+        return a + b;
+    }
+};
 
 // Where a row's part lies: its units [g0, g0 + n) counted from the row's first
 // 16-byte boundary; element e of unit g is column g E + e - head.
 struct Part {
     int head, g0, n;
+    int lo, hi;        // the row's elements among the part's
+    int u0, u1;        // units that are the row's entirely
 };
+// the elements of unit u that are not the row's, a bit each
+template <int E>
+__device__ __forceinline__ uint32_t outside(const Part& pt, int u) {
+    const int a = pt.lo - u * E, b = pt.hi - u * E;
+    uint32_t out = 0;
+    if (a > 0) out |= (1u << a) - 1u;             // a < E: the row begins in its first unit
+    if (b < E) out |= ~((1u << b) - 1u);          // b > 0: it ends in its last one
+    return out & ((1u << E) - 1u);
+}
 template <typename T>
 __device__ __forceinline__ Part part_of(const Params& p, int64_t row, uint32_t rank) {
     constexpr int E = Unit<T>::E;
@@ -155,6 +263,10 @@ __device__ __forceinline__ Part part_of(const Params& p, int64_t row, uint32_t r
     const int units = (r.head + p.V + E - 1) / E;
     r.g0 = (int)rank * p.part;
     r.n = max(0, min(p.part, units - r.g0));
+    r.lo = r.head - r.g0 * E;
+    r.hi = r.head + p.V - r.g0 * E;
+    r.u0 = r.lo > 0 ? 1 : 0;
+    r.u1 = r.n * E > r.hi ? r.n - 1 : r.n;
     return r;
 }
 
@@ -163,58 +275,111 @@ __device__ __forceinline__ float warp_max(float v) {
     for (int o = 16; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
     return v;
 }
+// two at a time take no longer than one
+__device__ __forceinline__ void warp_max2(float& a, float& b) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+        const float x = __shfl_xor_sync(0xFFFFFFFFu, a, o), y = __shfl_xor_sync(0xFFFFFFFFu, b, o);
+        a = fmaxf(a, x), b = fmaxf(b, y);
+    }
+}
+__device__ __forceinline__ void warp_sum2(float& a, float& b) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+        const float x = __shfl_xor_sync(0xFFFFFFFFu, a, o), y = __shfl_xor_sync(0xFFFFFFFFu, b, o);
+        a += x, b += y;
+    }
+}
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
     for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
     return v;
 }
 
+// What the teacher's warp loads before a row's turn comes: 128 of its tokens,
+// four a lane, and the row's own numbers.
+struct Ahead {
+    int i[4];
+    uint32_t t[4];
+    float lse, dloss, m, s, s_rest;
+};
+template <int MODE, bool TAIL>
+__device__ __forceinline__ void load_tokens(const Params& p, int64_t row, int j0, int lane, Ahead& a) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        const int j = j0 + 32 * q + lane;
+        a.i[q] = -1, a.t[q] = 0u;
+        if (row < p.M && j < p.k) {
+            const int64_t at = row * p.ldt + j;
+            a.i[q] = p.idx[row * p.ldi + j];
+            a.t[q] = p.t_f32 ? static_cast<const uint32_t*>(p.t)[at] : static_cast<const uint16_t*>(p.t)[at];
+        }
+    }
+    if (row < p.M && j0 == 0) {
+        if (TAIL) a.lse = p.lse[row];
+        if (MODE != FWD) a.dloss = p.dloss[row];
+        if (MODE == BWD) a.m = p.stats[3 * row], a.s = p.stats[3 * row + 1], a.s_rest = p.stats[3 * row + 2];
+    }
+}
+// of the tokens in this CTA's part; the first CTA, which works out the loss, of all
+template <typename T, int MODE>
+__device__ __forceinline__ void load_logits(const Params& p, int64_t row, uint32_t rank, const Ahead& a, float* x) {
+    const Part pt = part_of<T>(p, row, rank);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        const int i = a.i[q], g = (i + pt.head) / Unit<T>::E - pt.g0;
+        x[q] = 0.f;
+        if (i >= 0 && i < p.V && row < p.M && ((g >= 0 && g < pt.n) || (rank == 0 && MODE != BWD)))
+            x[q] = Unit<T>::one(p.x, row * p.ldx + i);
+    }
+}
+
 // The teacher's row (one warp): probabilities, what the loss needs of them,
 // and, of the tokens in this CTA's part, their bits, sums and logits.
 template <typename T, int MODE, bool TAIL>
 __device__ __forceinline__ void teacher_row(const Params& p, const Smem& sm, Teacher& out, int b, int64_t row,
-                                            uint32_t rank, int lane, bool fresh) {
+                                            int64_t next, uint32_t rank, int lane, Ahead& ah) {
     constexpr int E = Unit<T>::E;
     const Part pt = part_of<T>(p, row, rank);
     int* col = sm.col(b);
     float *pr = sm.p(b), *xs = sm.x(b);
     uint32_t* words = reinterpret_cast<uint32_t*>(sm.bits(b));
-    if (fresh) {
-        for (int i = lane; i < bits_bytes(p.part) / 4; i += 32) words[i] = 0u;
-        __syncwarp();
-    }
     const float inv_tau = p.inv_tau;
     bool any = false, dup = false;
     float t_max = -INFINITY, x_max = -INFINITY;
-    for (int j = lane; j < p.k; j += 32) {
-        const int i = p.idx[row * p.ldi + j];
-        const bool ok = i >= 0 && i < p.V;
-        if (i >= p.V) set_err(p.err, MOE_ERR_BAD_INDEX);
-        float t = -INFINITY, x = 0.f;
-        if (ok) {
-            const int64_t at = row * p.ldt + j;
-            t = p.t_f32 ? static_cast<const float*>(p.t)[at]
-                        : __bfloat162float(static_cast<const __nv_bfloat16*>(p.t)[at]);
-            t *= inv_tau;
-            const int u = i + pt.head, g = u / E - pt.g0;
-            const bool mine = g >= 0 && g < pt.n;
-            if (mine || (rank == 0 && MODE != BWD)) x = Unit<T>::one(p.x, row * p.ldx + i);
-            if (mine && (TAIL || MODE != FWD)) {
-                const uint32_t bit = 1u << (8 * (g & 3) + u % E);
-                dup |= (atomicOr(words + (g >> 2), bit) & bit) != 0;
+    for (int j0 = 0; j0 < p.k; j0 += 128) {
+        float x[4];
+        if (j0 > 0) load_tokens<MODE, TAIL>(p, row, j0, lane, ah);
+        load_logits<T, MODE>(p, row, rank, ah, x);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const int j = j0 + 32 * q + lane, i = ah.i[q];
+            if (j >= p.k) continue;
+            const bool ok = i >= 0 && i < p.V;
+            if (i >= p.V) set_err(p.err, MOE_ERR_BAD_INDEX);
+            const float t = ok ? __uint_as_float(p.t_f32 ? ah.t[q] : ah.t[q] << 16) * inv_tau : -INFINITY;
+            if (ok) {
+                any = true;
+                const int u = i + pt.head, g = u / E - pt.g0;
+                if (g >= 0 && g < pt.n && (TAIL || MODE != FWD)) {
+                    const uint32_t bit = 1u << (8 * (g & 3) + u % E);
+                    dup |= (atomicOr(words + (g >> 2), bit) & bit) != 0;
+                }
+                if (t > -INFINITY) x_max = fmaxf(x_max, x[q]);
             }
-            any = true;
+            col[j] = ok ? i : -1;
+            pr[j] = t;
+            xs[j] = x[q];
+            t_max = fmaxf(t_max, t);
         }
-        col[j] = ok ? i : -1;
-        pr[j] = t;
-        xs[j] = x;
-        t_max = fmaxf(t_max, t);
-        if (ok && t > -INFINITY) x_max = fmaxf(x_max, x);
     }
+    if (lane == 0 && MODE != FWD) out.dloss = ah.dloss, out.m = ah.m, out.s = ah.s, out.s_rest = ah.s_rest;
+    const float row_lse = ah.lse;
+    load_tokens<MODE, TAIL>(p, next, 0, lane, ah);
     any = __any_sync(0xFFFFFFFFu, any);
     dup = __any_sync(0xFFFFFFFFu, dup);
-    const float top = warp_max(t_max), t_ref = finite_max(top);
-    const float x_ref = finite_max(warp_max(x_max));
+    warp_max2(t_max, x_max);
+    const float t_ref = finite_max(t_max), x_ref = finite_max(x_max);
     __syncwarp();
     float sum = 0.f;
     if (!TAIL) {
@@ -222,7 +387,7 @@ __device__ __forceinline__ void teacher_row(const Params& p, const Smem& sm, Tea
             if (col[j] >= 0) sum += expf(pr[j] - t_ref);
         sum = warp_sum(sum);
     }
-    const float t_lse = TAIL ? p.lse[row] - t_ref : logf(sum), inv = 1.f / sum;
+    const float t_lse = TAIL ? row_lse - t_ref : logf(sum), inv = 1.f / sum;
     // a NaN among the teacher's logits is a teacher: it shows in the loss
     const bool some = any && (TAIL || sum != 0.f);
     float mass = 0.f, fit = 0.f;
@@ -236,8 +401,7 @@ __device__ __forceinline__ void teacher_row(const Params& p, const Smem& sm, Tea
         pr[j] = q;
         mass += q;
     }
-    mass = warp_sum(mass);
-    fit = warp_sum(fit);
+    warp_sum2(mass, fit);
     __syncwarp();
     if (dup) {      // the first of several holds the sum of their probabilities
         for (int j = lane; j < p.k; j += 32) {
@@ -278,7 +442,7 @@ __device__ __forceinline__ void teacher_row(const Params& p, const Smem& sm, Tea
     }
     __syncwarp();
 }
-// the bits of the row before last in this buffer
+// the bits of the row that this buffer held
 template <typename T>
 __device__ __forceinline__ void clear_bits(const Params& p, const Smem& sm, int b, const Part& pt, int lane) {
     constexpr int E = Unit<T>::E;
@@ -293,23 +457,26 @@ __device__ __forceinline__ void clear_bits(const Params& p, const Smem& sm, int 
 
 // T: logits; W warps go over them.
 template <typename T, int MODE, bool TAIL, int W>
-__global__ void __launch_bounds__(32 * W + 64, W == 8 ? 4 : 12) k_distill(const Params p) {
+__global__ void __launch_bounds__(32 * W + 64, W == 8 ? 3 : 10) k_distill(const Params p) {
     constexpr int E = Unit<T>::E;
     extern __shared__ __align__(16) uint8_t smem[];
-    const Smem sm{smem, p.part, (p.k + 3) / 4 * 4};
+    constexpr int NB = buffers(MODE);
+    const Smem sm{smem, p.part, (p.k + 3) / 4 * 4, NB};
     Fixed& fx = *reinterpret_cast<Fixed*>(sm.fixed());
     const uint32_t bar0 = smem_u32(&fx.bar[0]);
     auto full = [&](int i) { return bar0 + 8u * i; };
     auto empty = [&](int i) { return bar0 + 8u * (CHUNKS + i); };
     auto tfull = [&](int i) { return bar0 + 8u * (2 * CHUNKS + i); };
-    auto tempty = [&](int i) { return bar0 + 8u * (2 * CHUNKS + 2 + i); };
-    auto xbar = [&](int i) { return bar0 + 8u * (2 * CHUNKS + 4 + i); };
+    auto tempty = [&](int i) { return bar0 + 8u * (2 * CHUNKS + 4 + i); };
+    auto xbar = [&](int i) { return bar0 + 8u * (2 * CHUNKS + 8 + i); };
+    auto wbar = [&](int i) { return bar0 + 8u * (2 * CHUNKS + 12 + i); };
     volatile int* abort_flag = &fx.abort_flag;
     const uint32_t C = cluster_size(), rank = C > 1 ? cluster_ctarank() : 0u;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int i = 0; i < CHUNKS; ++i) mbar_init(full(i), 1), mbar_init(empty(i), W);
-        for (int i = 0; i < 2; ++i) mbar_init(tfull(i), 1), mbar_init(tempty(i), W), mbar_init(xbar(i), C);
+        for (int i = 0; i < NB; ++i) mbar_init(tfull(i), 1), mbar_init(tempty(i), MODE == FWD ? 1 : W), mbar_init(xbar(i), C);
+        for (int i = 0; i < 2; ++i) mbar_init(wbar(i), W);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         fx.abort_flag = 0;
     }
@@ -317,6 +484,41 @@ __global__ void __launch_bounds__(32 * W + 64, W == 8 ? 4 : 12) k_distill(const 
     if (C > 1) cluster_sync();      // the peers' barriers are initialised
     wait_for_previous_kernels();
     const int64_t row0 = blockIdx.x / C, step = gridDim.x / C;
+
+    // the row's maximum and sums from the parts'
+    auto gather_mail = [&](int b, float& m, float& s, float& s_rest) {
+        m = -INFINITY, s = 0.f, s_rest = 0.f;
+        for (int i = 0; i < (int)C; ++i) m = fmaxf(m, fx.mail[b][i].x);
+        const float ref = finite_max(m);
+        for (int i = 0; i < (int)C; ++i) {
+            const float4 v = fx.mail[b][i];
+            const float f = e_of(v.x, ref, p.c);
+            s += v.y * f;
+            s_rest += v.z * f;
+        }
+    };
+    auto write_loss = [&](int64_t row, const Teacher& te, float m, float s, float s_rest) {
+        if (p.stats) p.stats[3 * row] = m, p.stats[3 * row + 1] = s, p.stats[3 * row + 2] = s_rest;
+        if (p.loss) {
+            float loss = te.fit + te.p_sum * ((finite_max(m) - te.x_ref) * p.inv_tau + logf(s) - te.t_lse);
+            if (TAIL && te.rest > 0.f && s_rest > 0.f) loss += te.rest * (logf(te.rest) - logf(s_rest / s));
+            p.loss[row] = te.some ? loss * p.tau * p.tau : 0.f;
+        }
+    };
+    // FWD, warp 0, a row late.  A CTA sends row r after it has finished row
+    // r - 2, which every CTA sent after it had finished row r - 4: four buffers do.
+    auto finish_row = [&](int64_t row, int it) -> bool {
+        const int b = it % NB;
+        if (!__all_sync(0xFFFFFFFFu, mbar_wait_cluster(xbar(b), (uint32_t)(it / NB & 1), p, abort_flag))) return false;
+        if (rank == 0 && lane == 0) {
+            float m, s, s_rest;
+            gather_mail(b, m, s, s_rest);
+            write_loss(row, fx.teacher[b], m, s, s_rest);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(tempty(b));
+        return true;
+    };
 
     if (warp == W) {
         // ------------------------------------------------------ loads ----
@@ -352,12 +554,18 @@ __global__ void __launch_bounds__(32 * W + 64, W == 8 ? 4 : 12) k_distill(const 
         __syncwarp();
     } else if (warp == W + 1) {
         // ---------------------------------------------- teacher, a row ahead ----
+        if (TAIL || MODE != FWD) {
+            for (int i = lane; i < NB * bits_bytes(p.part) / 4; i += 32) reinterpret_cast<uint32_t*>(sm.bits(0))[i] = 0u;
+            __syncwarp();
+        }
         int it = 0;
+        Ahead ah = {};
+        load_tokens<MODE, TAIL>(p, row0, 0, lane, ah);
         for (int64_t row = row0; row < p.M; row += step, ++it) {
-            const int b = it & 1;
-            if (!__all_sync(0xFFFFFFFFu, mbar_wait(tempty(b), (uint32_t)((it >> 1) & 1) ^ 1u, p, abort_flag))) break;
-            if (it >= 2 && (TAIL || MODE != FWD)) clear_bits<T>(p, sm, b, part_of<T>(p, row - 2 * step, rank), lane);
-            teacher_row<T, MODE, TAIL>(p, sm, fx.teacher[b], b, row, rank, lane, it < 2);
+            const int b = it % NB;
+            if (!__all_sync(0xFFFFFFFFu, mbar_wait(tempty(b), (uint32_t)(it / NB & 1) ^ 1u, p, abort_flag))) break;
+            if (it >= NB && (TAIL || MODE != FWD)) clear_bits<T>(p, sm, b, part_of<T>(p, row - NB * step, rank), lane);
+            teacher_row<T, MODE, TAIL>(p, sm, fx.teacher[b], b, row, row + step, rank, lane, ah);
             if (lane == 0) mbar_arrive(tfull(b));
         }
     } else {
@@ -366,65 +574,70 @@ __global__ void __launch_bounds__(32 * W + 64, W == 8 ? 4 : 12) k_distill(const 
         int it = 0;
         bool ok = true;
         for (int64_t row = row0; row < p.M; row += step, ++it) {
-            const int b = it & 1;
-            const uint32_t row_phase = (uint32_t)(it & 1), buf_phase = (uint32_t)((it >> 1) & 1);
+            const int b = it % NB;
+            const uint32_t row_phase = (uint32_t)(it & 1), buf_phase = (uint32_t)(it / NB & 1);
             const Part pt = part_of<T>(p, row, rank);
-            ok = ok && mbar_wait(tfull(b), buf_phase, p, abort_flag);
             const Teacher& te = fx.teacher[b];
-            const uint8_t* bits = sm.bits(b);
-            const int lo0 = pt.head - pt.g0 * E, hi0 = pt.head + p.V - pt.g0 * E;      // of the part's elements, those of the row
+            // which of a unit's tokens were kept has to be known before the sums
+            if (TAIL || MODE == BWD) ok = ok && mbar_wait(tfull(b), buf_phase, p, abort_flag);
             float m = 0.f, s = 1.f, s_rest = 1.f;
             if constexpr (MODE != BWD) {
                 // -------------------------------- maximum and sum ----
-                float tm = -INFINITY, ts = 0.f;
+                const uint8_t* bits = sm.bits(b);
+                Sum sum;
                 for (int ch = 0; ch < CHUNKS; ++ch) {
                     ok = ok && mbar_wait(full(ch), row_phase, p, abort_flag);
-                    const int u1 = min((ch + 1) * p.chunk, pt.n);
-                    for (int u = ch * p.chunk + (int)threadIdx.x; u < u1 && ok; u += 32 * W) {
-                        float f[E];
-                        Unit<T>::load(sm.rows + 16 * u, f);
-                        if (u * E < lo0 || u * E + E > hi0) {
+                    const int u1 = ok ? min((ch + 1) * p.chunk, pt.n) : 0;
+                    int u = ch * p.chunk + (int)threadIdx.x;
+                    constexpr int N = 4;
+                    for (; u + (N - 1) * 32 * W < min(u1, pt.u1); u += N * 32 * W) {
+                        uint4 v[N];
+                        uint32_t kept[N], any = u < pt.u0;
 #pragma unroll
-                            for (int e = 0; e < E; ++e)
-                                if (u * E + e < lo0 || u * E + e >= hi0) f[e] = -INFINITY;
+                        for (int n = 0; n < N; ++n) {
+                            v[n] = *reinterpret_cast<const uint4*>(sm.rows + 16 * (u + n * 32 * W));
+                            if (TAIL) any |= kept[n] = bits[u + n * 32 * W];
                         }
-                        if constexpr (TAIL) {
-                            const uint32_t kept = bits[u];
-                            if (kept) {
+                        if (any) {
 #pragma unroll
-                                for (int e = 0; e < E; ++e)
-                                    if (kept >> e & 1) f[e] = -INFINITY;
+                            for (int n = 0; n < N; ++n) {
+                                uint32_t out = n == 0 && u < pt.u0 ? outside<E>(pt, u) : 0u;
+                                if (TAIL) out |= kept[n];
+                                leave_out<E>(v[n], out);
                             }
                         }
-                        float um = f[0];
-#pragma unroll
-                        for (int e = 1; e < E; ++e) um = fmaxf(um, f[e]);
-                        if (um > tm) {
-                            ts *= e_of(tm, um, p.c);
-                            tm = um;
-                        }
-                        const float ref = finite_max(tm);
-#pragma unroll
-                        for (int e = 0; e < E; ++e) ts += e_of(f[e], ref, p.c);
+                        sum.add<T, N>(v, p.c);
+                    }
+                    for (; u < u1; u += 32 * W) {
+                        uint4 v = *reinterpret_cast<const uint4*>(sm.rows + 16 * u);
+                        uint32_t out = TAIL ? bits[u] : 0u;
+                        if (u < pt.u0 || u >= pt.u1) out |= outside<E>(pt, u);
+                        if (out) leave_out<E>(v, out);
+                        sum.add<T, 1>(&v, p.c);
                     }
                     if (MODE == FWD) {
                         __syncwarp();
                         if (lane == 0) mbar_arrive(empty(ch));
                     }
                 }
-                const float wm = warp_max(tm);
-                ts = warp_sum(ts * e_of(tm, finite_max(wm), p.c));
-                if (lane == 0) fx.warp_part[warp] = make_float2(wm, ts);
-                asm volatile("bar.sync 1, %0;" ::"n"(32 * W) : "memory");
-                if (warp == 0 && ok) {
+                const float wm = warp_max(sum.m);
+                const float ws = warp_sum(sum.total() * e_of(sum.m, finite_max(wm), p.c));
+                if (lane == 0) {
+                    fx.warp_part[it & 1][warp] = make_float2(wm, ws);
+                    if (ok) mbar_arrive(wbar(it & 1));
+                }
+                if (warp == 0) {      // this CTA's sums, to every CTA that goes on with them
+                    ok = ok && mbar_wait(wbar(it & 1), (uint32_t)(it >> 1) & 1u, p, abort_flag);
+                    if (!TAIL) ok = ok && mbar_wait(tfull(b), buf_phase, p, abort_flag);
+                    const float2* part = fx.warp_part[it & 1];
                     float cm = te.top_max, rest = 0.f;
 #pragma unroll
-                    for (int w = 0; w < W; ++w) cm = fmaxf(cm, fx.warp_part[w].x);
+                    for (int w = 0; w < W; ++w) cm = fmaxf(cm, part[w].x);
                     const float ref = finite_max(cm);
 #pragma unroll
-                    for (int w = 0; w < W; ++w) rest += fx.warp_part[w].y * e_of(fx.warp_part[w].x, ref, p.c);
+                    for (int w = 0; w < W; ++w) rest += part[w].y * e_of(part[w].x, ref, p.c);
                     const float all = TAIL ? rest + te.top_sum * e_of(te.top_max, ref, p.c) : rest;
-                    if (lane < (int)C) {
+                    if (lane < (int)C && ok) {
                         const uint32_t to = mapa(smem_u32(&fx.mail[b][rank]), (uint32_t)lane);
                         asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(to), "f"(cm), "f"(all),
                                      "f"(rest), "f"(0.f)
@@ -432,52 +645,60 @@ __global__ void __launch_bounds__(32 * W + 64, W == 8 ? 4 : 12) k_distill(const 
                         mbar_arrive_remote(mapa(xbar(b), (uint32_t)lane));
                     }
                 }
-                ok = ok && mbar_wait_cluster(xbar(b), buf_phase, p, abort_flag);
-                m = -INFINITY, s = 0.f, s_rest = 0.f;
-                for (int i = 0; i < (int)C; ++i) m = fmaxf(m, fx.mail[b][i].x);
-                const float ref = finite_max(m);
-                for (int i = 0; i < (int)C; ++i) {
-                    const float4 v = fx.mail[b][i];
-                    const float f = e_of(v.x, ref, p.c);
-                    s += v.y * f;
-                    s_rest += v.z * f;
-                }
-                if (rank == 0 && threadIdx.x == 0 && ok) {
-                    if (p.stats) p.stats[3 * row] = m, p.stats[3 * row + 1] = s, p.stats[3 * row + 2] = s_rest;
-                    if (p.loss) {
-                        float loss = te.fit + te.p_sum * ((ref - te.x_ref) * p.inv_tau + logf(s) - te.t_lse);
-                        if (TAIL && te.rest > 0.f && s_rest > 0.f) loss += te.rest * (logf(te.rest) - logf(s_rest / s));
-                        p.loss[row] = te.some ? loss * p.tau * p.tau : 0.f;
-                    }
+                if (MODE == FWD) {
+                    ok = __all_sync(0xFFFFFFFFu, ok);
+                    if (warp == 0 && it > 0) ok = ok && finish_row(row - step, it - 1);
+                    if (warp == 0 && row + step >= p.M) ok = ok && finish_row(row, it);
+                } else {
+                    if (!TAIL) ok = ok && mbar_wait(tfull(b), buf_phase, p, abort_flag);
+                    ok = ok && mbar_wait_cluster(xbar(b), buf_phase, p, abort_flag);
+                    gather_mail(b, m, s, s_rest);
+                    if (rank == 0 && threadIdx.x == 0 && ok) write_loss(row, te, m, s, s_rest);
                 }
             } else {
-                m = p.stats[3 * row], s = p.stats[3 * row + 1], s_rest = p.stats[3 * row + 2];
+                m = te.m, s = te.s, s_rest = te.s_rest;
             }
             if constexpr (MODE != FWD) {
                 // ------------------------------------------ gradient ----
-                const float g = p.dloss[row] * p.tau;
+                const float g = te.dloss * p.tau;
                 const bool zero = !te.some || g == 0.f;
                 const bool with_rest = TAIL && te.rest > 0.f && s_rest > 0.f;
                 const float mass = with_rest ? te.mass : te.p_sum;
                 const float f_top = g * (mass / s);
                 const float f_all = with_rest ? g * (mass / s - te.rest / s_rest) : f_top;
                 const float ref = finite_max(m);
+                const f2 neg2 = pack(-ref, -ref), f2_all = pack(f_all, f_all), c2 = pack(p.c, p.c);
                 T* dx = static_cast<T*>(p.dx) + row * p.lddx - pt.head + (int64_t)pt.g0 * E;
                 const bool vec = (reinterpret_cast<uintptr_t>(dx) & 15) == 0;
+                auto slopes = [&](int u, float* d) {
+                    f2 f[E / 2];
+                    Unit<T>::pairs(*reinterpret_cast<const uint4*>(sm.rows + 16 * u), f);
+#pragma unroll
+                    for (int i = 0; i < E / 2; ++i) unpack(mul2(e_of2(f[i], neg2, c2), f2_all), d[2 * i], d[2 * i + 1]);
+                };
                 for (int ch = 0; ch < CHUNKS; ++ch) {
                     if (MODE == BWD) ok = ok && mbar_wait(full(ch), row_phase, p, abort_flag);
-                    const int u1 = min((ch + 1) * p.chunk, pt.n);
-                    for (int u = ch * p.chunk + (int)threadIdx.x; u < u1 && ok; u += 32 * W) {
-                        float f[E];
-                        Unit<T>::load(sm.rows + 16 * u, f);
-#pragma unroll
-                        for (int e = 0; e < E; ++e) f[e] = zero ? 0.f : e_of(f[e], ref, p.c) * f_all;
-                        if (vec && u * E >= lo0 && u * E + E <= hi0) {
-                            Unit<T>::store(dx + (int64_t)u * E, f);
+                    const int u1 = ok ? min((ch + 1) * p.chunk, pt.n) : 0;
+                    int u = ch * p.chunk + (int)threadIdx.x;
+                    if (vec && !zero) {
+#pragma unroll 2
+                        for (; u < min(u1, pt.u1); u += 32 * W) {
+                            if (u < pt.u0) break;
+                            float d[E];
+                            slopes(u, d);
+                            Unit<T>::store(dx + u * E, d);
+                        }
+                    }
+                    // the row's ends, and rows that do not lie as the logits do
+                    for (; u < u1; u += 32 * W) {
+                        float d[E] = {};
+                        if (!zero) slopes(u, d);
+                        if (vec && u >= pt.u0 && u < pt.u1) {
+                            Unit<T>::store(dx + u * E, d);
                         } else {
 #pragma unroll
                             for (int e = 0; e < E; ++e)
-                                if (u * E + e >= lo0 && u * E + e < hi0) dx[(int64_t)u * E + e] = Unit<T>::to(f[e]);
+                                if (u * E + e >= pt.lo && u * E + e < pt.hi) dx[u * E + e] = Unit<T>::to(d[e]);
                         }
                     }
                     __syncwarp();
@@ -488,14 +709,16 @@ __global__ void __launch_bounds__(32 * W + 64, W == 8 ? 4 : 12) k_distill(const 
                 if (!zero && ok) {
                     for (int j = threadIdx.x; j < p.k; j += 32 * W) {
                         const int cj = sm.col(b)[j];
-                        const int u = cj + lo0;      // element of the part
+                        const int u = cj + pt.lo;      // element of the part
                         if (cj >= 0 && u >= 0 && u < pt.n * E)
                             dx[u] = Unit<T>::to(e_of(sm.x(b)[j], ref, p.c) * f_top - g * sm.p(b)[j]);
                     }
                 }
             }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(tempty(b));
+            if (MODE != FWD) {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(tempty(b));
+            }
         }
     }
     __syncthreads();
@@ -510,8 +733,31 @@ __global__ void __launch_bounds__(32 * W + 64, W == 8 ? 4 : 12) k_distill(const 
     X(float, FWD, false) X(float, FWD, true) X(float, BWD, false) X(float, BWD, true) X(float, BOTH, false) \
     X(float, BOTH, true)
 
+constexpr int kPerSm = 3, kNarrowPerSm = 10;      // CTAs of an SM, by registers
+constexpr int kSmemSm = 233472;                   // shared memory of an SM, 1 KB of it the system's per CTA
+static int g_clusters[2][4][kPerSm];              // that run at a time: wide CTAs or not; of 1, 2, 4, 8; CTAs an SM
+static size_t smem_of(int per_sm) { return kSmemSm / per_sm / 128 * 128 - 1024; }
+
+static cudaLaunchConfig_t launch_cfg(int64_t clusters, int C, bool wide, size_t smem, cudaStream_t stream,
+                                     cudaLaunchAttribute* attr) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(clusters * C));
+    cfg.blockDim = dim3(wide ? 320 : 128);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = C;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cfg;
+}
+
 static cudaError_t set_attributes() {
-    const int most = (int)smem_bytes(MAX_PART, MAX_K);
+    const int most = (int)smem_bytes(MAX_PART, MAX_K, 4);
 #define X(T, M, R)                                                                                             \
     for (const void* k : {(const void*)k_distill<T, M, R, 2>, (const void*)k_distill<T, M, R, 8>}) {            \
         const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, most);       \
@@ -519,6 +765,16 @@ static cudaError_t set_attributes() {
     }
     MOE_DISTILL_INSTANCES(X)
 #undef X
+    for (int wide = 0; wide < 2; ++wide)
+        for (int c = 0; c < 4; ++c)
+            for (int n = 1; n <= (wide ? kPerSm : 1); ++n) {
+                cudaLaunchAttribute attr[2];
+                const cudaLaunchConfig_t cfg = launch_cfg(1024, 1 << c, wide, wide ? smem_of(n) : smem_of(kNarrowPerSm), nullptr, attr);
+                const cudaError_t e = cudaOccupancyMaxActiveClusters(
+                    &g_clusters[wide][c][n - 1],
+                    wide ? k_distill<__nv_bfloat16, BOTH, true, 8> : k_distill<__nv_bfloat16, BOTH, true, 2>, &cfg);
+                if (e != cudaSuccess) return e;
+            }
     return cudaSuccess;
 }
 typedef void (*Kernel)(const Params);
@@ -531,14 +787,15 @@ static Kernel kernel_of(bool f32, int mode, bool tail, bool wide) {
     return nullptr;
 }
 
-// CTAs that share a row, and its part in 16-byte units: parts of at most 36
-// KB, so that four CTAs and more share an SM; smaller ones while rows are too
-// few to give every SM a part.
+// CTAs that share a row, and its part in 16-byte units: parts of at most 65
+// KB, so that three CTAs share an SM; smaller ones while rows are too few to
+// give every SM a part.
+constexpr int kPart = 4160;
 static int cluster_of(int64_t M, int V, int elem, int sms, int* part) {
     const int E = 16 / elem, units = (E - 1 + V + E - 1) / E;
     int c = 1;
     auto size = [&] { return (units + c - 1) / c; };
-    while (c < MAX_C && (size() > 2304 || (M * c * 2 <= sms && size() > 128))) c *= 2;
+    while (c < MAX_C && (size() > kPart || (M * c * 2 <= sms && size() > 128))) c *= 2;
     *part = size();
     return c;
 }
@@ -548,25 +805,18 @@ static moe_status_t launch(Params p, bool f32, int mode, cudaStream_t stream) {
     MOE_REQUIRE(sms > 0, MOE_ERR_NOT_INITIALIZED);
     const int C = cluster_of(p.M, p.V, f32 ? 4 : 2, sms, &p.part);
     p.chunk = (p.part + CHUNKS - 1) / CHUNKS;
+    if (p.chunk > 256) p.chunk = (p.chunk + 255) / 256 * 256;      // whole turns of a CTA's threads
     p.timeout_ns = 2000000000ull;
     const bool wide = p.part > 256;
-    const size_t smem = smem_bytes(p.part, p.k);
-    const int per_sm = std::max(1, std::min(wide ? 4 : 12, (int)(233472 / (smem + 1024))));
-    const int64_t clusters = std::min<int64_t>(p.M, std::max(1, sms * per_sm / C));
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(clusters * C));
-    cfg.blockDim = dim3(wide ? 320 : 128);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
+    const size_t smem = smem_bytes(p.part, p.k, buffers(mode));
+    int per_sm = wide ? kPerSm : kNarrowPerSm;
+    while (per_sm > 1 && smem > smem_of(per_sm)) --per_sm;
+    // no more clusters than run at a time: rows are dealt out evenly
+    const int c = C == 1 ? 0 : (C == 2 ? 1 : (C == 4 ? 2 : 3));
+    const int64_t slots = wide ? g_clusters[1][c][per_sm - 1] : (int64_t)g_clusters[0][c][0] * per_sm / kNarrowPerSm;
+    const int64_t clusters = std::min<int64_t>(p.M, std::max<int64_t>(1, slots));
     cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = C;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[1].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 2;
+    const cudaLaunchConfig_t cfg = launch_cfg(clusters, C, wide, smem, stream, attr);
     if (cudaLaunchKernelEx(&cfg, kernel_of(f32, mode, p.lse != nullptr, wide), p) != cudaSuccess) return MOE_ERR_CUDA;
     MOE_CHECK_LAUNCH();
     return MOE_OK;
