@@ -13,15 +13,18 @@
 // tokens themselves (a bit per token says which were kept): as s - sum of the
 // kept it would be lost where the student is sure of them.
 //
-// A row is split over the CTAs of a cluster, and each keeps its part in
-// shared memory, so that loss and gradient together read the logits once: 4
-// bytes an element of bf16 logits instead of 6 in two calls.  The parts'
-// maxima and sums are exchanged through distributed shared memory.  Several
-// CTAs share an SM: one's loads run under another's arithmetic and stores.
-// Warps: 0 .. W - 1 go over the logits, W loads them (bulk copies of whole
-// 16-byte units, so rows may start at any element; what is read of the
-// neighbouring rows is not used), W + 1 works on the teacher's tokens a row
-// ahead.  All waits are bounded.
+// Loss and gradient together read the logits once: a row's parts lie in the
+// shared memory of a cluster's CTAs, whose maxima and sums are exchanged
+// through distributed shared memory; 4 bytes an element of bf16 logits instead
+// of 6 in two calls.  The loss alone and the gradient alone keep nothing, and
+// stream whole rows, one CTA each, through a ring; there a cluster shares a row
+// only when rows are few.
+// Warps 0 .. W - 1 go over the logits.  A thread loads the 16-byte units that it
+// works on itself (asynchronous copies to shared memory, in groups; rows may
+// start at any element, what is read of the neighbouring rows is not used) and
+// sends for the next ones as it is done with some, so that nobody waits for
+// another's loads.  (Bulk copies by one thread were no faster.)  Warp W works on
+// the teacher's tokens a row ahead.  All waits are bounded.
 #include <algorithm>
 
 #include "gemm_common.cuh"
@@ -33,8 +36,8 @@ using namespace gg;
 
 constexpr int MAX_K = 1024;              // tokens of the teacher
 constexpr int MAX_C = 8;                 // CTAs of a cluster
-constexpr int CHUNKS = 4;                // of a part, each with its own barriers
-constexpr int MAX_PART = 8960;           // 16-byte units of a part
+constexpr int CHUNKS = 4;                // groups of copies on their way: of the part, or the ring's
+constexpr int MAX_PART = 11264;          // 16-byte units of a part
 constexpr float kLog2e = 1.4426950408889634f;
 enum { FWD = 1, BWD = 2, BOTH = 3 };
 
@@ -55,7 +58,7 @@ struct Params {
     int64_t M;
     int V, k;
     float tau, inv_tau, c;    // c = log2(e) / tau
-    int part, chunk;          // 16-byte units of a CTA's part, of a chunk
+    int part, chunk, held;    // 16-byte units of a CTA's part, of a chunk, in shared memory
     int32_t* err;
     uint64_t timeout_ns;
 };
@@ -69,42 +72,46 @@ struct Teacher {
     int some;                       // 0: no teacher, loss and gradient are zero
 };
 
-// Rows that the teacher's warp may be ahead of: the loss alone is finished a
-// row late, under the next row's sums.
-constexpr int buffers(int mode) { return mode == FWD ? 4 : 2; }
-
-// Shared memory: the part, then (a buffer each) a byte per 16-byte unit, and
-// of each of the teacher's tokens its column (bit 31: counted with an earlier
-// one; -1: none), its probability and the student's logit.
+// Shared memory: the part or the ring of its chunks, then (two buffers each) a
+// byte per 16-byte unit of the part, and of each of the teacher's tokens its column
+// (bit 31: counted with an earlier one; -1: none), its probability and the
+// student's logit.
 struct Smem {
     uint8_t* rows;
-    int part, k, nb;
+    int held, part, k;      // units in shared memory, of the part
     __device__ __forceinline__ uint8_t* bits(int b) const;
     __device__ __forceinline__ int* col(int b) const;
     __device__ __forceinline__ float* p(int b) const { return reinterpret_cast<float*>(col(b)) + k; }
     __device__ __forceinline__ float* x(int b) const { return p(b) + k; }
-    __device__ __forceinline__ uint8_t* fixed() const { return reinterpret_cast<uint8_t*>(col(nb)); }
+    __device__ __forceinline__ uint8_t* fixed() const { return reinterpret_cast<uint8_t*>(col(2)); }
 };
 struct Fixed {
-    unsigned long long bar[2 * CHUNKS + 14];
-    float4 mail[4][MAX_C];          // max, s, s_rest of the cluster's parts
+    unsigned long long bar[6];
+    float4 mail[2][MAX_C];          // max, s, s_rest of the cluster's parts
     float2 warp_part[2][8];
-    Teacher teacher[4];
+    Teacher teacher[2];
     int abort_flag;
 };
 
 __host__ __device__ inline int bits_bytes(int part) { return (part + 15) / 16 * 16; }
-__host__ __device__ inline size_t smem_bytes(int part, int k, int nb) {
-    return (size_t)part * 16 + nb * (bits_bytes(part) + 12 * (size_t)((k + 3) / 4 * 4)) + sizeof(Fixed);
+__host__ __device__ inline size_t smem_bytes(int held, int part, int k) {
+    return (size_t)held * 16 + 2 * (bits_bytes(part) + 12 * (size_t)((k + 3) / 4 * 4)) + sizeof(Fixed);
 }
-__device__ __forceinline__ uint8_t* Smem::bits(int b) const { return rows + 16 * part + b * bits_bytes(part); }
-__device__ __forceinline__ int* Smem::col(int b) const { return reinterpret_cast<int*>(bits(nb)) + 3 * b * k; }
-static_assert(MAX_PART * 20 + 48 * MAX_K + sizeof(Fixed) <= 232448 && MAX_PART % 16 == 0, "shared memory budget");
+__device__ __forceinline__ uint8_t* Smem::bits(int b) const { return rows + 16 * held + b * bits_bytes(part); }
+__device__ __forceinline__ int* Smem::col(int b) const { return reinterpret_cast<int*>(bits(2)) + 3 * b * k; }
+static_assert(MAX_PART * 18 + 24 * MAX_K + sizeof(Fixed) <= 232448 && MAX_PART % 16 == 0, "shared memory budget");
 
 __device__ __forceinline__ uint32_t cluster_size() {
     uint32_t n;
     asm volatile("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(n));
     return n;
+}
+// this thread's copies have landed, all but the last n groups
+__device__ __forceinline__ void wait_group(int n) {
+    if (n == 0) asm volatile("cp.async.wait_group 0;" ::: "memory");
+    else if (n == 1) asm volatile("cp.async.wait_group 1;" ::: "memory");
+    else if (n == 2) asm volatile("cp.async.wait_group 2;" ::: "memory");
+    else asm volatile("cp.async.wait_group 3;" ::: "memory");
 }
 __device__ __forceinline__ float ex2(float x) {
     float y;
@@ -457,26 +464,20 @@ __device__ __forceinline__ void clear_bits(const Params& p, const Smem& sm, int 
 
 // T: logits; W warps go over them.
 template <typename T, int MODE, bool TAIL, int W>
-__global__ void __launch_bounds__(32 * W + 64, W == 8 ? 3 : 10) k_distill(const Params p) {
+__global__ void __launch_bounds__(32 * W + 32, W == 8 ? 3 : 10) k_distill(const Params p) {
     constexpr int E = Unit<T>::E;
     extern __shared__ __align__(16) uint8_t smem[];
-    constexpr int NB = buffers(MODE);
-    const Smem sm{smem, p.part, (p.k + 3) / 4 * 4, NB};
+    const Smem sm{smem, p.held, p.part, (p.k + 3) / 4 * 4};
     Fixed& fx = *reinterpret_cast<Fixed*>(sm.fixed());
     const uint32_t bar0 = smem_u32(&fx.bar[0]);
-    auto full = [&](int i) { return bar0 + 8u * i; };
-    auto empty = [&](int i) { return bar0 + 8u * (CHUNKS + i); };
-    auto tfull = [&](int i) { return bar0 + 8u * (2 * CHUNKS + i); };
-    auto tempty = [&](int i) { return bar0 + 8u * (2 * CHUNKS + 4 + i); };
-    auto xbar = [&](int i) { return bar0 + 8u * (2 * CHUNKS + 8 + i); };
-    auto wbar = [&](int i) { return bar0 + 8u * (2 * CHUNKS + 12 + i); };
+    auto tfull = [&](int i) { return bar0 + 8u * i; };
+    auto tempty = [&](int i) { return bar0 + 8u * (2 + i); };
+    auto xbar = [&](int i) { return bar0 + 8u * (4 + i); };
     volatile int* abort_flag = &fx.abort_flag;
     const uint32_t C = cluster_size(), rank = C > 1 ? cluster_ctarank() : 0u;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
-        for (int i = 0; i < CHUNKS; ++i) mbar_init(full(i), 1), mbar_init(empty(i), W);
-        for (int i = 0; i < NB; ++i) mbar_init(tfull(i), 1), mbar_init(tempty(i), MODE == FWD ? 1 : W), mbar_init(xbar(i), C);
-        for (int i = 0; i < 2; ++i) mbar_init(wbar(i), W);
+        for (int i = 0; i < 2; ++i) mbar_init(tfull(i), 1), mbar_init(tempty(i), MODE == FWD ? 1 : W), mbar_init(xbar(i), 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         fx.abort_flag = 0;
     }
@@ -505,66 +506,19 @@ __global__ void __launch_bounds__(32 * W + 64, W == 8 ? 3 : 10) k_distill(const 
             p.loss[row] = te.some ? loss * p.tau * p.tau : 0.f;
         }
     };
-    // FWD, warp 0, a row late.  A CTA sends row r after it has finished row
-    // r - 2, which every CTA sent after it had finished row r - 4: four buffers do.
-    auto finish_row = [&](int64_t row, int it) -> bool {
-        const int b = it % NB;
-        if (!__all_sync(0xFFFFFFFFu, mbar_wait_cluster(xbar(b), (uint32_t)(it / NB & 1), p, abort_flag))) return false;
-        if (rank == 0 && lane == 0) {
-            float m, s, s_rest;
-            gather_mail(b, m, s, s_rest);
-            write_loss(row, fx.teacher[b], m, s, s_rest);
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(tempty(b));
-        return true;
-    };
-
     if (warp == W) {
-        // ------------------------------------------------------ loads ----
-        if (lane == 0) {
-            int it = 0, issued = 0;
-            bool ok = true;
-            for (int64_t row = row0; row < p.M && ok; row += step, ++it) {
-                const Part pt = part_of<T>(p, row, rank);
-                const uint8_t* src = reinterpret_cast<const uint8_t*>(static_cast<const T*>(p.x) + row * p.ldx) -
-                                     pt.head * sizeof(T) + (size_t)pt.g0 * 16;
-                for (int ch = 0; ch < CHUNKS; ++ch) {
-                    if (!mbar_wait(empty(ch), (uint32_t)(it & 1) ^ 1u, p, abort_flag)) {
-                        ok = false;
-                        break;
-                    }
-                    const int u0 = ch * p.chunk, n = min(p.chunk, pt.n - u0);
-                    if (n > 0) {
-                        mbar_expect_tx(full(ch), 16u * n);
-                        bulk_load(smem_u32(sm.rows + 16 * u0), src + 16 * (size_t)u0, 16u * n, full(ch));
-                    } else {
-                        mbar_arrive(full(ch));
-                    }
-                    ++issued;
-                }
-            }
-            // nobody leaves with copies in flight
-            Params q = p;
-            q.timeout_ns = 200000000ull;
-            volatile int no_abort = 0;
-            for (int i = issued - min(issued, CHUNKS); i < issued; ++i)
-                mbar_wait(full(i % CHUNKS), (uint32_t)(i / CHUNKS) & 1u, q, &no_abort);
-        }
-        __syncwarp();
-    } else if (warp == W + 1) {
         // ---------------------------------------------- teacher, a row ahead ----
         if (TAIL || MODE != FWD) {
-            for (int i = lane; i < NB * bits_bytes(p.part) / 4; i += 32) reinterpret_cast<uint32_t*>(sm.bits(0))[i] = 0u;
+            for (int i = lane; i < bits_bytes(p.part) / 2; i += 32) reinterpret_cast<uint32_t*>(sm.bits(0))[i] = 0u;
             __syncwarp();
         }
         int it = 0;
         Ahead ah = {};
         load_tokens<MODE, TAIL>(p, row0, 0, lane, ah);
         for (int64_t row = row0; row < p.M; row += step, ++it) {
-            const int b = it % NB;
-            if (!__all_sync(0xFFFFFFFFu, mbar_wait(tempty(b), (uint32_t)(it / NB & 1) ^ 1u, p, abort_flag))) break;
-            if (it >= NB && (TAIL || MODE != FWD)) clear_bits<T>(p, sm, b, part_of<T>(p, row - NB * step, rank), lane);
+            const int b = it & 1;
+            if (!__all_sync(0xFFFFFFFFu, mbar_wait(tempty(b), (uint32_t)(it >> 1 & 1) ^ 1u, p, abort_flag))) break;
+            if (it >= 2 && (TAIL || MODE != FWD)) clear_bits<T>(p, sm, b, part_of<T>(p, row - 2 * step, rank), lane);
             teacher_row<T, MODE, TAIL>(p, sm, fx.teacher[b], b, row, row + step, rank, lane, ah);
             if (lane == 0) mbar_arrive(tfull(b));
         }
@@ -573,9 +527,39 @@ __global__ void __launch_bounds__(32 * W + 64, W == 8 ? 3 : 10) k_distill(const 
         // others do not wait for it, and touches nothing)
         int it = 0;
         bool ok = true;
+        // this thread's units [c0, c0 + chunk) of a row's part go to `slot`, one group of copies
+        auto send_for = [&](int64_t row, int c0, int slot) {
+            if (row < p.M) {
+                const Part pt = part_of<T>(p, row, rank);
+                const uint8_t* src = reinterpret_cast<const uint8_t*>(static_cast<const T*>(p.x) + row * p.ldx) -
+                                     pt.head * (int)sizeof(T) + (int64_t)(pt.g0 + c0) * 16;
+                const int n = min(p.chunk, pt.n - c0);
+                const uint32_t dst = smem_u32(sm.rows + 16 * slot);
+#pragma unroll 4
+                for (int u = (int)threadIdx.x; u < n; u += 32 * W)
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + 16 * u), "l"(src + 16 * (int64_t)u)
+                                 : "memory");
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        };
+        // STREAM: the ring's next chunk to send for, and its slot
+        constexpr bool STREAM = MODE != BOTH;
+        int64_t next_row = row0;
+        int next_c0 = 0, next_slot = 0, slot = 0;
+        auto send_next = [&] {
+            send_for(next_row, next_c0, next_slot);
+            next_slot = next_slot == (CHUNKS - 1) * p.chunk ? 0 : next_slot + p.chunk;
+            next_c0 += p.chunk;
+            if (next_c0 >= p.part) next_c0 = 0, next_row += step;
+        };
+        auto advance = [&] { slot = slot == (CHUNKS - 1) * p.chunk ? 0 : slot + p.chunk; };
+        for (int ch = 0; ch < CHUNKS; ++ch) {
+            if (STREAM) send_next();
+            else send_for(row0, ch * p.chunk, ch * p.chunk);
+        }
         for (int64_t row = row0; row < p.M; row += step, ++it) {
-            const int b = it % NB;
-            const uint32_t row_phase = (uint32_t)(it & 1), buf_phase = (uint32_t)(it / NB & 1);
+            const int b = it & 1;
+            const uint32_t buf_phase = (uint32_t)(it >> 1 & 1);
             const Part pt = part_of<T>(p, row, rank);
             const Teacher& te = fx.teacher[b];
             // which of a unit's tokens were kept has to be known before the sums
@@ -585,17 +569,18 @@ __global__ void __launch_bounds__(32 * W + 64, W == 8 ? 3 : 10) k_distill(const 
                 // -------------------------------- maximum and sum ----
                 const uint8_t* bits = sm.bits(b);
                 Sum sum;
-                for (int ch = 0; ch < CHUNKS; ++ch) {
-                    ok = ok && mbar_wait(full(ch), row_phase, p, abort_flag);
-                    const int u1 = ok ? min((ch + 1) * p.chunk, pt.n) : 0;
-                    int u = ch * p.chunk + (int)threadIdx.x;
+                for (int c0 = 0, ch = 0; STREAM ? c0 < p.part : ch < CHUNKS; c0 += p.chunk, ++ch) {
+                    wait_group(STREAM ? CHUNKS - 1 : CHUNKS - 1 - ch);
+                    const uint8_t* rows = STREAM ? sm.rows + 16 * (slot - c0) : sm.rows;
+                    const int u1 = ok ? min(c0 + p.chunk, pt.n) : 0;
+                    int u = c0 + (int)threadIdx.x;
                     constexpr int N = 4;
                     for (; u + (N - 1) * 32 * W < min(u1, pt.u1); u += N * 32 * W) {
                         uint4 v[N];
                         uint32_t kept[N], any = u < pt.u0;
 #pragma unroll
                         for (int n = 0; n < N; ++n) {
-                            v[n] = *reinterpret_cast<const uint4*>(sm.rows + 16 * (u + n * 32 * W));
+                            v[n] = *reinterpret_cast<const uint4*>(rows + 16 * (u + n * 32 * W));
                             if (TAIL) any |= kept[n] = bits[u + n * 32 * W];
                         }
                         if (any) {
@@ -609,25 +594,23 @@ __global__ void __launch_bounds__(32 * W + 64, W == 8 ? 3 : 10) k_distill(const 
                         sum.add<T, N>(v, p.c);
                     }
                     for (; u < u1; u += 32 * W) {
-                        uint4 v = *reinterpret_cast<const uint4*>(sm.rows + 16 * u);
+                        uint4 v = *reinterpret_cast<const uint4*>(rows + 16 * u);
                         uint32_t out = TAIL ? bits[u] : 0u;
                         if (u < pt.u0 || u >= pt.u1) out |= outside<E>(pt, u);
                         if (out) leave_out<E>(v, out);
                         sum.add<T, 1>(&v, p.c);
                     }
-                    if (MODE == FWD) {
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(empty(ch));
+                    if (STREAM) {
+                        send_next();
+                        advance();
                     }
                 }
                 const float wm = warp_max(sum.m);
                 const float ws = warp_sum(sum.total() * e_of(sum.m, finite_max(wm), p.c));
-                if (lane == 0) {
-                    fx.warp_part[it & 1][warp] = make_float2(wm, ws);
-                    if (ok) mbar_arrive(wbar(it & 1));
-                }
+                if (lane == 0) fx.warp_part[it & 1][warp] = make_float2(wm, ws);
+                // (also keeps the warps within a row of one another: warp_part has two rows)
+                asm volatile("bar.sync 1, %0;" ::"n"(32 * W) : "memory");
                 if (warp == 0) {      // this CTA's sums, to every CTA that goes on with them
-                    ok = ok && mbar_wait(wbar(it & 1), (uint32_t)(it >> 1) & 1u, p, abort_flag);
                     if (!TAIL) ok = ok && mbar_wait(tfull(b), buf_phase, p, abort_flag);
                     const float2* part = fx.warp_part[it & 1];
                     float cm = te.top_max, rest = 0.f;
@@ -637,21 +620,29 @@ __global__ void __launch_bounds__(32 * W + 64, W == 8 ? 3 : 10) k_distill(const 
 #pragma unroll
                     for (int w = 0; w < W; ++w) rest += part[w].y * e_of(part[w].x, ref, p.c);
                     const float all = TAIL ? rest + te.top_sum * e_of(te.top_max, ref, p.c) : rest;
-                    if (lane < (int)C && ok) {
-                        const uint32_t to = mapa(smem_u32(&fx.mail[b][rank]), (uint32_t)lane);
-                        asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(to), "f"(cm), "f"(all),
-                                     "f"(rest), "f"(0.f)
-                                     : "memory");
-                        mbar_arrive_remote(mapa(xbar(b), (uint32_t)lane));
-                    }
+                    // the bytes themselves count on the barriers: a release at cluster scope
+                    // would wait for every store of this warp, 1 to 2 us a row
+                    if (lane == 0 && ok) mbar_expect_tx(xbar(b), 16u * C);
+                    if (lane < (int)C && ok)
+                        asm volatile(
+                            "st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(
+                                mapa(smem_u32(&fx.mail[b][rank]), (uint32_t)lane)),
+                            "f"(cm), "f"(all), "f"(rest), "f"(0.f), "r"(mapa(xbar(b), (uint32_t)lane))
+                            : "memory");
                 }
-                if (MODE == FWD) {
-                    ok = __all_sync(0xFFFFFFFFu, ok);
-                    if (warp == 0 && it > 0) ok = ok && finish_row(row - step, it - 1);
-                    if (warp == 0 && row + step >= p.M) ok = ok && finish_row(row, it);
+                if (MODE == FWD) {      // the other warps go on to the next row
+                    if (warp == 0) {
+                        ok = __all_sync(0xFFFFFFFFu, ok && mbar_wait(xbar(b), buf_phase, p, abort_flag));
+                        if (rank == 0 && lane == 0 && ok) {
+                            gather_mail(b, m, s, s_rest);
+                            write_loss(row, te, m, s, s_rest);
+                        }
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(tempty(b));
+                    }
                 } else {
                     if (!TAIL) ok = ok && mbar_wait(tfull(b), buf_phase, p, abort_flag);
-                    ok = ok && mbar_wait_cluster(xbar(b), buf_phase, p, abort_flag);
+                    ok = ok && mbar_wait(xbar(b), buf_phase, p, abort_flag);
                     gather_mail(b, m, s, s_rest);
                     if (rank == 0 && threadIdx.x == 0 && ok) write_loss(row, te, m, s, s_rest);
                 }
@@ -670,29 +661,31 @@ __global__ void __launch_bounds__(32 * W + 64, W == 8 ? 3 : 10) k_distill(const 
                 const f2 neg2 = pack(-ref, -ref), f2_all = pack(f_all, f_all), c2 = pack(p.c, p.c);
                 T* dx = static_cast<T*>(p.dx) + row * p.lddx - pt.head + (int64_t)pt.g0 * E;
                 const bool vec = (reinterpret_cast<uintptr_t>(dx) & 15) == 0;
-                auto slopes = [&](int u, float* d) {
+                auto slopes = [&](const uint8_t* unit, float* d) {
                     f2 f[E / 2];
-                    Unit<T>::pairs(*reinterpret_cast<const uint4*>(sm.rows + 16 * u), f);
+                    Unit<T>::pairs(*reinterpret_cast<const uint4*>(unit), f);
 #pragma unroll
                     for (int i = 0; i < E / 2; ++i) unpack(mul2(e_of2(f[i], neg2, c2), f2_all), d[2 * i], d[2 * i + 1]);
                 };
-                for (int ch = 0; ch < CHUNKS; ++ch) {
-                    if (MODE == BWD) ok = ok && mbar_wait(full(ch), row_phase, p, abort_flag);
-                    const int u1 = ok ? min((ch + 1) * p.chunk, pt.n) : 0;
-                    int u = ch * p.chunk + (int)threadIdx.x;
+#pragma unroll 1
+                for (int c0 = 0, ch = 0; STREAM ? c0 < p.part : ch < CHUNKS; c0 += p.chunk, ++ch) {
+                    if (STREAM) wait_group(CHUNKS - 1);
+                    const uint8_t* rows = STREAM ? sm.rows + 16 * (slot - c0) : sm.rows;
+                    const int u1 = ok ? min(c0 + p.chunk, pt.n) : 0;
+                    int u = c0 + (int)threadIdx.x;
                     if (vec && !zero) {
 #pragma unroll 2
                         for (; u < min(u1, pt.u1); u += 32 * W) {
                             if (u < pt.u0) break;
                             float d[E];
-                            slopes(u, d);
+                            slopes(rows + 16 * u, d);
                             Unit<T>::store(dx + u * E, d);
                         }
                     }
                     // the row's ends, and rows that do not lie as the logits do
                     for (; u < u1; u += 32 * W) {
                         float d[E] = {};
-                        if (!zero) slopes(u, d);
+                        if (!zero) slopes(rows + 16 * u, d);
                         if (vec && u >= pt.u0 && u < pt.u1) {
                             Unit<T>::store(dx + u * E, d);
                         } else {
@@ -701,8 +694,12 @@ __global__ void __launch_bounds__(32 * W + 64, W == 8 ? 3 : 10) k_distill(const 
                                 if (u * E + e >= pt.lo && u * E + e < pt.hi) dx[u * E + e] = Unit<T>::to(d[e]);
                         }
                     }
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(empty(ch));
+                    if (STREAM) {
+                        send_next();
+                        advance();
+                    } else {
+                        send_for(row + step, c0, c0);
+                    }
                 }
                 // the kept tokens, over what was just stored there
                 asm volatile("bar.sync 1, %0;" ::"n"(32 * W) : "memory");
@@ -721,6 +718,7 @@ __global__ void __launch_bounds__(32 * W + 64, W == 8 ? 3 : 10) k_distill(const 
             }
         }
     }
+    wait_group(0);
     __syncthreads();
     if (C > 1) cluster_sync();      // nobody leaves while its mail is written
 }
@@ -742,7 +740,7 @@ static cudaLaunchConfig_t launch_cfg(int64_t clusters, int C, bool wide, size_t 
                                      cudaLaunchAttribute* attr) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(clusters * C));
-    cfg.blockDim = dim3(wide ? 320 : 128);
+    cfg.blockDim = dim3(wide ? 288 : 96);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -757,7 +755,7 @@ static cudaLaunchConfig_t launch_cfg(int64_t clusters, int C, bool wide, size_t 
 }
 
 static cudaError_t set_attributes() {
-    const int most = (int)smem_bytes(MAX_PART, MAX_K, 4);
+    const int most = 232448;
 #define X(T, M, R)                                                                                             \
     for (const void* k : {(const void*)k_distill<T, M, R, 2>, (const void*)k_distill<T, M, R, 8>}) {            \
         const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, most);       \
@@ -787,37 +785,57 @@ static Kernel kernel_of(bool f32, int mode, bool tail, bool wide) {
     return nullptr;
 }
 
-// CTAs that share a row, and its part in 16-byte units: parts of at most 65
-// KB, so that three CTAs share an SM; smaller ones while rows are too few to
-// give every SM a part.
-constexpr int kPart = 4160;
-static int cluster_of(int64_t M, int V, int elem, int sms, int* part) {
+// How a call is spread: CTAs of a cluster (they share a row), 288 threads each
+// or, for small parts, 96, and clusters, no more than run at a time, so that
+// rows are dealt out evenly.  Of the sizes of clusters the one with the shortest
+// time by this count, in ns: a 16-byte unit takes an SM 0.36 to read at the
+// memory's rate and as much to write, shared by its CTAs (one alone gets no more
+// than half of it), and a row 700 besides for the chain of its sums (800 more where they
+// go through the cluster), 600 for the gradient alone.
+struct Spread {
+    int C, part, chunk, held, per_sm;
+    bool wide;
+    size_t smem;
+    int64_t clusters;
+};
+static Spread spread(int64_t M, int V, int elem, int k, int mode, int sms) {
     const int E = 16 / elem, units = (E - 1 + V + E - 1) / E;
-    int c = 1;
-    auto size = [&] { return (units + c - 1) / c; };
-    while (c < MAX_C && (size() > kPart || (M * c * 2 <= sms && size() > 128))) c *= 2;
-    *part = size();
-    return c;
+    Spread best{};
+    double least = 1e300;
+    for (int c = 0; c < 4; ++c) {
+        Spread s{};
+        s.C = 1 << c;
+        s.part = (units + s.C - 1) / s.C;
+        s.wide = s.part > 256;
+        const int turn = s.wide ? 256 : 64;      // units that a CTA's threads take at a time
+        s.chunk = mode == BOTH ? (s.part + CHUNKS * turn - 1) / (CHUNKS * turn) * turn
+                               : std::min(4, (s.part + turn - 1) / turn) * turn;
+        s.held = mode == BOTH ? s.part : CHUNKS * s.chunk;
+        s.smem = smem_bytes(s.held, s.part, k);
+        if (s.smem > 232448 || (c > 0 && s.part < 32)) continue;
+        s.per_sm = s.wide ? kPerSm : kNarrowPerSm;
+        while (s.per_sm > 1 && s.smem > smem_of(s.per_sm)) --s.per_sm;
+        const int64_t slots =
+            s.wide ? g_clusters[1][c][s.per_sm - 1] : (int64_t)g_clusters[0][c][0] * s.per_sm / kNarrowPerSm;
+        s.clusters = std::min<int64_t>(M, std::max<int64_t>(1, slots));
+        const double ctas = std::max(2., std::min<double>(s.per_sm, (double)s.clusters * s.C / sms));
+        const double cost = (double)((M + s.clusters - 1) / s.clusters) *
+                            (s.part * 0.36 * (mode == FWD ? 1 : 2) * ctas + (mode == BWD ? 600 : (c ? 1500 : 700)));
+        if (cost < least) least = cost, best = s;
+    }
+    return best;
 }
 
 static moe_status_t launch(Params p, bool f32, int mode, cudaStream_t stream) {
     const int sms = device_sm_count();
     MOE_REQUIRE(sms > 0, MOE_ERR_NOT_INITIALIZED);
-    const int C = cluster_of(p.M, p.V, f32 ? 4 : 2, sms, &p.part);
-    p.chunk = (p.part + CHUNKS - 1) / CHUNKS;
-    if (p.chunk > 256) p.chunk = (p.chunk + 255) / 256 * 256;      // whole turns of a CTA's threads
+    const Spread d = spread(p.M, p.V, f32 ? 4 : 2, p.k, mode, sms);
+    MOE_REQUIRE(d.C > 0, MOE_ERR_UNSUPPORTED);
+    p.part = d.part, p.chunk = d.chunk, p.held = d.held;
     p.timeout_ns = 2000000000ull;
-    const bool wide = p.part > 256;
-    const size_t smem = smem_bytes(p.part, p.k, buffers(mode));
-    int per_sm = wide ? kPerSm : kNarrowPerSm;
-    while (per_sm > 1 && smem > smem_of(per_sm)) --per_sm;
-    // no more clusters than run at a time: rows are dealt out evenly
-    const int c = C == 1 ? 0 : (C == 2 ? 1 : (C == 4 ? 2 : 3));
-    const int64_t slots = wide ? g_clusters[1][c][per_sm - 1] : (int64_t)g_clusters[0][c][0] * per_sm / kNarrowPerSm;
-    const int64_t clusters = std::min<int64_t>(p.M, std::max<int64_t>(1, slots));
     cudaLaunchAttribute attr[2];
-    const cudaLaunchConfig_t cfg = launch_cfg(clusters, C, wide, smem, stream, attr);
-    if (cudaLaunchKernelEx(&cfg, kernel_of(f32, mode, p.lse != nullptr, wide), p) != cudaSuccess) return MOE_ERR_CUDA;
+    const cudaLaunchConfig_t cfg = launch_cfg(d.clusters, d.C, d.wide, d.smem, stream, attr);
+    if (cudaLaunchKernelEx(&cfg, kernel_of(f32, mode, p.lse != nullptr, d.wide), p) != cudaSuccess) return MOE_ERR_CUDA;
     MOE_CHECK_LAUNCH();
     return MOE_OK;
 }

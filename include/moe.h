@@ -1035,7 +1035,7 @@ MOE_API moe_status_t adamw_step(void* plan, int tensors, int64_t tiles, int p_ty
  *   stats [M, 3] fp32: max x, and sums of exp((x - max x) / tau) over all tokens and
  *          over those not kept (all, without teacher_lse): what the backward
  *          pass needs of the forward pass.
- *   tau    1e-6 .. 1e6.  V up to 573,426 (bf16), 286,714 (fp32).
+ *   tau    1e-6 .. 1e6.  V up to 720,882 (bf16), 360,442 (fp32).
  * All sums are fp32.  distill_loss_fwd writes loss and stats, those that are
  * not NULL; distill_loss_bwd dx from stats; distill_loss loss (may be NULL) and dx
  * with one read of x.  One launch each, no workspace; every sum has a fixed

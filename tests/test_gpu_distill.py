@@ -148,6 +148,7 @@ def test_in_place(ops, xt, m, v):
             loss2, _ = ops.distill_loss(dloss, y, idx, t, lse, dlogits=y)
             assert torch.equal(loss, loss2)
         else:
+            d = ops.distill_loss_bwd(dloss, x, idx, t, stats, lse)
             ops.distill_loss_bwd(dloss, y, idx, t, stats, lse, dlogits=y)
         assert torch.equal(y, d)
 
