@@ -143,8 +143,6 @@ def prepare_grouped(case, g, s, seed):
         for _, a, b in s["spans"]:
             inside[a:b] = True
         s["x"].mul_(inside)
-    if own:
-        s["ws"] = torch.empty((s["ops"].grouped_workspace_size(groups),), dtype=torch.uint8, device="cuda")
     if case["way"] == "fwd":
         s["y"] = room(m, n)
         s["a"] = room(m, cols) if ffn and case["keep"] else None
@@ -202,22 +200,22 @@ def run(s):
 
 
 def own_linear_fwd(s):
-    s["ops"].grouped_linear_fwd(s["x"], s["w"], s["offsets"], s["rows"], y=s["y"], ws=s["ws"])
+    s["ops"].grouped_linear_fwd(s["x"], s["w"], s["offsets"], s["rows"], y=s["y"])
     return s["y"]
 
 
 def own_linear_bwd(s):
-    s["ops"].grouped_linear_bwd(s["dy"], s["x"], s["w"], s["offsets"], s["rows"], dx=s["dx"], dw=s["dw"], ws=s["ws"])
+    s["ops"].grouped_linear_bwd(s["dy"], s["x"], s["w"], s["offsets"], s["rows"], dx=s["dx"], dw=s["dw"])
     return {"dx": s["dx"], "dw": s["dw"]}
 
 
 def own_ffn_fwd(s):
-    s["ops"].grouped_ffn_fwd(s["x"], s["w"], s["offsets"], s["rows"], h=s["y"], a=s["a"], ws=s["ws"])
+    s["ops"].grouped_ffn_fwd(s["x"], s["w"], s["offsets"], s["rows"], h=s["y"], a=s["a"])
     return {"h": s["y"], "a": s["a"]}
 
 
 def own_ffn_bwd(s):
-    s["ops"].grouped_ffn_bwd(s["dy"], s["a"], s["x"], s["w"], s["offsets"], s["rows"], dx=s["dx"], dw1=s["dw"], da=s["da"], ws=s["ws"])
+    s["ops"].grouped_ffn_bwd(s["dy"], s["a"], s["x"], s["w"], s["offsets"], s["rows"], dx=s["dx"], dw1=s["dw"], da=s["da"])
     return {"dx": s["dx"], "dw1": s["dw"]}
 
 
