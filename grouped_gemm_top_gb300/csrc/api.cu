@@ -17,6 +17,7 @@ cudaError_t dense_set_attributes();  // dense.cu
 cudaError_t norm_set_attributes();   // norm.cu
 cudaError_t adamw_set_attributes();  // adamw.cu
 cudaError_t distill_set_attributes();  // distill.cu
+cudaError_t grouped_set_attributes();  // grouped.cu
 void route_scratch_forget(int device);  // route.cu
 
 int device_sm_count() {
@@ -78,6 +79,7 @@ extern "C" moe_status_t moe_init(int device) {
     if (norm_set_attributes() != cudaSuccess) return MOE_ERR_CUDA;
     if (adamw_set_attributes() != cudaSuccess) return MOE_ERR_CUDA;
     if (distill_set_attributes() != cudaSuccess) return MOE_ERR_CUDA;
+    if (grouped_set_attributes() != cudaSuccess) return MOE_ERR_CUDA;
     g_sm_count[device] = sms;
     g_init[device] = true;
     return MOE_OK;

@@ -610,6 +610,31 @@ bool make_store_map(CUtensorMap* m, void* base, int64_t rows, int64_t cols, int6
     return r == CUDA_SUCCESS;
 }
 
+// The same of G matrices [rows, cols], gs elements apart: the TMA fills with
+// zeros, or clips, at each one's own edges.
+bool make_bf16_map3(CUtensorMap* m, const void* base, int64_t G, int64_t rows, int64_t cols, int64_t ld, int64_t gs,
+                    int box_rows) {
+    cuuint64_t gdim[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)G};
+    cuuint64_t gstr[2] = {(cuuint64_t)ld * 2, (cuuint64_t)gs * 2};
+    cuuint32_t box[3] = {64, (cuuint32_t)box_rows, 1}, estr[3] = {1, 1, 1};
+    if (g_encode == nullptr) return false;
+    return g_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), gdim, gstr, box, estr,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+bool make_store_map3(CUtensorMap* m, void* base, int64_t G, int64_t rows, int64_t cols, int64_t ld, int64_t gs,
+                     bool f32) {
+    const cuuint64_t size = f32 ? 4 : 2;
+    cuuint64_t gdim[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)G};
+    cuuint64_t gstr[2] = {(cuuint64_t)ld * size, (cuuint64_t)gs * size};
+    cuuint32_t box[3] = {32, 32, 1}, estr[3] = {1, 1, 1};
+    if (g_encode == nullptr) return false;
+    return g_encode(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, base, gdim, gstr,
+                    box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                    f32 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // rank-2/3 uint8 tensor map, 128x128 boxes, 128-byte swizzle
 static bool make_map(CUtensorMap* m, const void* base, int rank, const uint64_t* dims, const uint64_t* strides_bytes,
                      int box_rows = 128) {

@@ -1,0 +1,1031 @@
+// bf16 products grouped by expert, groups of any number of rows.
+//
+// x [M, K] holds the rows of group g at offsets[g] ..; W_g [K, N]:
+//   forward            y[rows of g] = x[rows of g] W_g, or act(x Wg) * (x Wu)
+//   input gradient     dx[rows of g] = dy[rows of g] W_g^T
+//   weight gradient    dW_g = x[rows of g]^T dy[rows of g]
+// The offsets stay on the device; the grid depends on sizes the host knows.
+//
+// The first two (k_rows) run on the tensor cores transposed, D^T = W_g^T x^T:
+// 256 columns of W_g are the M of a CTA pair's product and the group's rows its N,
+// which may be any multiple of 32.  With rows as M, every group would be padded
+// to 256 rows, a sixth more products for experts of 768 rows each, and a few
+// rows per expert (decoding) would cost as much as 256.  A group's rows are
+// split evenly into tiles of at most 256.  Rows are read in place: a tile
+// that is too long for the group reads the next one's rows, whose results are not
+// stored (a product's rows do not mix).  D^T is turned round on its way to
+// memory by the matrix stores to shared memory.
+// The weight gradient (k_wgrad) contracts over the group's rows; those of the next
+// group that its last 16-row step holds are set to zero in shared memory, in both
+// operands (zero times an infinity would not be zero).
+//
+// Warps: 0 TMA, 1 MMA (of the leader CTA), 2 (k_wgrad) zeros after a group's last row,
+// 4-11 epilogue.  All waits are bounded.
+#include <algorithm>
+
+#include "pair_bf16.cuh"
+
+namespace moe {
+
+// gemm.cu
+bool make_bf16_map3(CUtensorMap* m, const void* base, int64_t G, int64_t rows, int64_t cols, int64_t ld, int64_t gs,
+                    int box_rows);
+bool make_store_map3(CUtensorMap* m, void* base, int64_t G, int64_t rows, int64_t cols, int64_t ld, int64_t gs,
+                     bool f32);
+
+namespace grouped {
+
+using namespace dense;
+
+constexpr int ACC_COLS = 256;                   // TMEM columns of an accumulator
+constexpr int NACC = 2;
+constexpr int HALF_BYTES = 128 * TK * 2;        // one CTA's 128 rows of an operand per stage
+constexpr int MAX_STAGES = 10;
+constexpr int SMEM_WORK = 14 * HALF_BYTES;      // stages, then the epilogue's boxes
+constexpr int OFF_BAR = SMEM_WORK;              // full[S], empty[S], tail[S], tfull[A], tempty[A], xfull[4], xempty[4], drain
+constexpr int NBAR = 3 * MAX_STAGES + 2 * NACC + 9;
+constexpr int OFF_MISC = OFF_BAR + 8 * NBAR;
+constexpr int SMEM_BYTES = OFF_MISC + 16 + 1024;
+static_assert(SMEM_BYTES <= 232448, "shared memory budget");
+constexpr int MAX_GROUPS = 65536;
+
+struct Params {
+    const int32_t* offsets;      // [G + 1]
+    const int32_t* rows;         // [G] or NULL: up to the next offset
+    int G;
+    int64_t M;
+    int N, K;                    // k_rows: columns of D (GLU: f), depth; k_wgrad: D_g is [K, N]
+    int nk;                      // k_rows: steps of the depth
+    int n_max;                   // k_rows: most rows of a tile, a multiple of 32
+    int col_tiles;               // k_rows: tiles along N; k_wgrad: tiles along N
+    int m_tiles, bn;             // k_wgrad: tiles along K, columns of a tile
+    int64_t max_tiles;
+    int stages, stage_bytes;
+    int up;                      // GLU: column of W where the up half begins
+    void* y;
+    int64_t ldy, gsy;
+    __nv_bfloat16* a;            // GLU: [gate | up] or NULL
+    int64_t lda;
+    int32_t* err;
+    uint64_t timeout_ns;
+};
+
+// First row and number of rows of group g; none where the offsets are wrong.
+struct Span {
+    int start, rows;
+};
+__device__ __forceinline__ Span span_of(const Params& p, int g) {
+    Span s{0, 0};
+    if (g >= p.G) return s;
+    const int a = p.offsets[g], b = p.offsets[g + 1];
+    const int n = p.rows ? p.rows[g] : b - a;
+    if (a < 0 || b < a || b > p.M || n < 0 || n > b - a) {
+        set_err(p.err, MOE_ERR_BAD_OFFSETS);
+        return s;
+    }
+    s.start = a, s.rows = n;
+    return s;
+}
+
+// Where tile t of k_rows lies.  A warp keeps 32 groups, a lane each, and moves on
+// to the next 32 as its tiles do (t only grows).
+struct Tile {
+    int g, ct;          // group, tile of W's columns
+    int row0, rows;     // of x
+};
+struct Cursor {
+    int base = -32;                 // of the 32 groups
+    int64_t first = 0, end = 0;     // this lane's group's first tile; the tiles up to the last lane's
+    int start, rows, per, tiles;    // of this lane's group; rows of its tiles; how many there are
+    __device__ __forceinline__ bool find(const Params& p, int64_t t, int lane, Tile& out) {
+        while (t >= end) {
+            base += 32;
+            if (base >= p.G) return false;
+            const Span s = span_of(p, base + lane);
+            start = s.start, rows = s.rows, per = 32, tiles = 0;
+            if (rows > 0) {
+                const int n = (rows + p.n_max - 1) / p.n_max;
+                per = ((rows + n - 1) / n + 31) / 32 * 32;      // evenly
+                tiles = (rows + per - 1) / per * p.col_tiles;
+            }
+            int64_t sum = tiles;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int64_t v = __shfl_up_sync(0xFFFFFFFFu, sum, o);
+                if (lane >= o) sum += v;
+            }
+            first = end + sum - tiles;
+            if (first + tiles > p.max_tiles) tiles = 0;      // groups that overlap
+            end = min(end + __shfl_sync(0xFFFFFFFFu, sum, 31), p.max_tiles);
+        }
+        const uint32_t here = __ballot_sync(0xFFFFFFFFu, t >= first && t < first + tiles);
+        if (here == 0) return false;
+        const int src = __ffs(here) - 1;
+        const int i = (int)(t - __shfl_sync(0xFFFFFFFFu, first, src));
+        const int n_rows = __shfl_sync(0xFFFFFFFFu, rows, src), n_per = __shfl_sync(0xFFFFFFFFu, per, src);
+        // bands of 8 row tiles, consecutive tiles down a band: those under way share
+        // W's columns and x's rows in L2
+        const int row_tiles = (n_rows + n_per - 1) / n_per, band = 8 * p.col_tiles;
+        const int b = i / band, rem = i - b * band, width = min(8, row_tiles - 8 * b);
+        out.g = base + src;
+        out.ct = rem / width;
+        const int r = (8 * b + rem - out.ct * width) * n_per;
+        out.row0 = __shfl_sync(0xFFFFFFFFu, start, src) + r;
+        out.rows = min(n_per, n_rows - r);
+        return true;
+    }
+};
+
+// A CTA's place: in its pair, in the grid, in shared memory.
+struct Place {
+    uint8_t* smem;
+    uint32_t bar0, rank;
+    int warp, lane, first, step;      // the pair's tiles: first, first + step, ..
+    volatile int* abort_flag;
+    __device__ __forceinline__ uint32_t bar(int i) const { return bar0 + 8u * i; }
+    __device__ __forceinline__ uint32_t full(int s) const { return bar(s); }
+    __device__ __forceinline__ uint32_t empty(int s) const { return bar(MAX_STAGES + s); }
+    __device__ __forceinline__ uint32_t tail(int s) const { return bar(2 * MAX_STAGES + s); }
+    __device__ __forceinline__ uint32_t tfull(int a) const { return bar(3 * MAX_STAGES + a); }
+    __device__ __forceinline__ uint32_t tempty(int a) const { return bar(3 * MAX_STAGES + NACC + a); }
+    __device__ __forceinline__ uint32_t xfull(int i) const { return bar(3 * MAX_STAGES + 2 * NACC + i); }
+    __device__ __forceinline__ uint32_t xempty(int i) const { return bar(3 * MAX_STAGES + 2 * NACC + 4 + i); }
+    __device__ __forceinline__ uint32_t drain() const { return bar(3 * MAX_STAGES + 2 * NACC + 8); }
+};
+
+// Barriers, TMEM; returns its base to every warp.
+__device__ __forceinline__ uint32_t set_up(Place& pl, int stages, int full_arrivals) {
+    extern __shared__ uint8_t smem_raw[];
+    pl.smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+    pl.warp = __shfl_sync(0xFFFFFFFFu, (int)(threadIdx.x >> 5), 0), pl.lane = threadIdx.x & 31;
+    pl.rank = cluster_ctarank();
+    pl.first = blockIdx.x / 2, pl.step = gridDim.x / 2;
+    pl.bar0 = smem_u32(pl.smem + OFF_BAR);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(pl.smem + OFF_MISC);
+    pl.abort_flag = reinterpret_cast<volatile int*>(pl.smem + OFF_MISC + 4);
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < stages; ++s) {
+            mbar_init(pl.full(s), full_arrivals);
+            mbar_init(pl.empty(s), 1);
+            mbar_init(pl.tail(s), 1);
+        }
+        for (int a = 0; a < NACC; ++a) {
+            mbar_init(pl.tfull(a), 1);
+            mbar_init(pl.tempty(a), 2 * EPI_WARPS);
+        }
+        for (int i = 0; i < 4; ++i) mbar_init(pl.xfull(i), 1), mbar_init(pl.xempty(i), 1);
+        mbar_init(pl.drain(), 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        *pl.abort_flag = 0;
+    }
+    __syncthreads();
+    cluster_sync();      // the peer's barriers are initialised
+    if (pl.warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
+                     "r"(TMEM_COLS));
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+        tc_fence_before();
+    }
+    if (pl.warp == 1 || pl.warp >= 4) {      // the producer need not wait for TMEM
+        asm volatile("bar.sync 1, %0;" ::"n"(32 + 32 * EPI_WARPS) : "memory");
+        tc_fence_after();
+    }
+    return pl.warp == 1 || pl.warp >= 4 ? *tmem_slot : 0u;
+}
+__device__ __forceinline__ void tear_down(const Place& pl, uint32_t tmem_base) {
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();      // both CTAs are done with TMEM and with each other's barriers
+    tc_fence_after();
+    if (pl.warp == 1) {
+        __syncwarp();
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(TMEM_COLS));
+    }
+}
+__device__ __forceinline__ Params patient(const Params& p) {      // for what is in flight after an abort
+    Params q = p;
+    q.timeout_ns = 200000000ull;
+    return q;
+}
+// wait (bounded) for the products issued
+__device__ __forceinline__ void products_end(const Place& pl, const Params& p, const Ring& ring) {
+    if (ring.count > 0) {
+        if (elect_one()) tc_commit_local2(pl.drain());
+        volatile int no_abort = 0;
+        mbar_wait(pl.drain(), 0, patient(p), &no_abort);
+    }
+    __syncwarp();
+}
+
+// ---------------------------------------- forward and input gradient ----
+
+// 16 TMEM lanes x 32 columns: thread T holds of every 8 columns 2 (T % 4) and
+// the next one, of lanes T / 4 (first two registers) and T / 4 + 8.
+__device__ __forceinline__ void tmem_ld_16x32(uint32_t taddr, uint32_t* r) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
+
+// The way out of an epilogue warp: a chunk of D^T, 32 columns of D (lanes) x 32
+// rows (TMEM columns), in bf16 and turned round, as a box of 32 rows of 64 bytes
+// (64-byte swizzle).  A TMA store writes it; where the group ends inside the
+// box, or a width that is no multiple of 8 does, the rows are copied out.
+struct Out {
+    uint32_t buf;
+    int lane;
+    uint32_t at;      // which of the two boxes
+    // v: what tmem_ld_16x32 gave for lanes 0..15 and 16..31
+    __device__ __forceinline__ void put(const CUtensorMap* map, __nv_bfloat16* d, int64_t ld, int col, int cols,
+                                        int64_t row, int rows, const float* v) {
+        const uint32_t b = buf + at;
+        at ^= 2048u;
+        if (lane == 0) bulk_wait_group_read1();      // the box before the last one has been read
+        __syncwarp();
+        // one store for 8 rows: its four 8 x 8 matrices are 8 columns each
+        const uint32_t r = (uint32_t)lane & 7u, c = (uint32_t)lane >> 3;
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+            const uint32_t line = 8u * n + r;
+            asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(
+                             b + 64u * line + ((c ^ (line >> 1 & 3u)) << 4)),
+                         "r"(pack_bf16x2(v[4 * n], v[4 * n + 1])), "r"(pack_bf16x2(v[4 * n + 2], v[4 * n + 3])),
+                         "r"(pack_bf16x2(v[16 + 4 * n], v[16 + 4 * n + 1])),
+                         "r"(pack_bf16x2(v[16 + 4 * n + 2], v[16 + 4 * n + 3]))
+                         : "memory");
+        }
+        const bool whole = rows >= 32 && (cols >= 32 || (cols & 7) == 0);
+        if (whole) fence_proxy_async_shared();
+        __syncwarp();
+        if (whole) {
+            if (lane == 0) tma_store_2d(map, b, col, (int)row);
+        } else if (lane < rows) {
+            __nv_bfloat16* dst = d + (row + lane) * ld + col;
+#pragma unroll
+            for (uint32_t q = 0; q < 4; ++q) {
+                const int n = cols - 8 * (int)q;
+                if (n <= 0) break;
+                uint32_t w[4];
+                asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                             : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                             : "r"(b + 64u * lane + ((q ^ ((uint32_t)lane >> 1 & 3u)) << 4))
+                             : "memory");
+                if (n >= 8) {
+                    *reinterpret_cast<uint4*>(dst + 8 * q) = make_uint4(w[0], w[1], w[2], w[3]);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 7; ++i)
+                        if (i < n) dst[8 * q + i] = __ushort_as_bfloat16((unsigned short)(w[i >> 1] >> (16 * (i & 1))));
+                }
+            }
+        }
+        if (lane == 0) bulk_commit_group();      // (an empty one, so that every box counts)
+        __syncwarp();
+    }
+};
+
+// W_MN: the forward product (D's columns are contiguous in W).  GLU: the
+// tile's 128 columns per CTA are 64 of gate and the same 64 of up.
+template <bool W_MN, bool GLU, int ACT>
+__global__ void __launch_bounds__(THREADS, 1)
+    k_rows(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX16,
+           const __grid_constant__ CUtensorMap tmX32, const __grid_constant__ CUtensorMap tmX64,
+           const __grid_constant__ CUtensorMap tmX128, const __grid_constant__ CUtensorMap tmY,
+           const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmA2, const Params p) {
+    constexpr int EPI_STAGE = GLU ? 8192 : 4096;      // GLU: 4 KB more, gate's way to up
+    constexpr int TILE_COLS = GLU ? 128 : 256;        // of D, per pair
+    if (threadIdx.x == 64) {
+        prefetch_map(&tmW);
+        prefetch_map(&tmX128);
+        prefetch_map(&tmY);
+    }
+    Place pl;
+    const uint32_t tmem_base = set_up(pl, p.stages, 1);
+    wait_for_previous_kernels();
+    const int warp = pl.warp, lane = pl.lane;
+    Cursor cur;
+    Ring ring, acc;
+    Tile ti;
+    int64_t t = pl.first;
+
+    if (warp == 0) {
+        // ------------------------------------------------------ loads ----
+        const bool elected = elect_one();
+        const uint32_t lead_full = mapa(pl.full(0), 0);
+        for (; !ring.aborted && cur.find(p, t, lane, ti); t += pl.step) {
+            const int half = (ti.rows + 31) / 32 * 16;     // rows of this CTA
+            const CUtensorMap* tmX = half <= 16 ? &tmX16 : (half <= 32 ? &tmX32 : (half <= 64 ? &tmX64 : &tmX128));
+            const uint32_t x_rows = half <= 16 ? 16 : (half <= 32 ? 32 : (half <= 64 ? 64 : 128));
+            const uint32_t bytes = 2u * (HALF_BYTES + x_rows * TK * 2);
+            const int col = ti.ct * TILE_COLS + (GLU ? 64 : 128) * (int)pl.rank, row = ti.row0 + half * (int)pl.rank;
+            for (int ks = 0; ks < p.nk; ++ks) {
+                if (!__all_sync(0xFFFFFFFFu, mbar_wait_cluster(pl.empty(ring.at), ring.phase ^ 1u, p, pl.abort_flag))) {
+                    ring.aborted = true;
+                    break;
+                }
+                // both CTAs' bytes complete on the leader's full barrier
+                const uint32_t fb = lead_full + 8u * ring.at;
+                if (elected) {
+                    if (pl.rank == 0) mbar_expect_tx(pl.full(ring.at), bytes);
+                    const uint32_t sw = smem_u32(pl.smem + ring.at * p.stage_bytes);
+                    if constexpr (W_MN) {
+                        tma2_load_3d(sw, &tmW, col, ks * TK, ti.g, fb);
+                        tma2_load_3d(sw + HALF_BYTES / 2, &tmW, GLU ? col + p.up : col + 64, ks * TK, ti.g, fb);
+                    } else {
+                        tma2_load_3d(sw, &tmW, ks * TK, col, ti.g, fb);
+                    }
+                    tma2_load_2d(sw + HALF_BYTES, tmX, ks * TK, row, fb);
+                }
+                ring.next(p.stages);
+            }
+        }
+        __syncwarp();
+        if (ring.aborted && pl.rank == 0) {      // the copies in flight
+            const Params q = patient(p);
+            volatile int no_abort = 0;
+            for (int i = ring.count - min(ring.count, p.stages); i < ring.count; ++i)
+                mbar_wait_cluster(pl.full(i % p.stages), (uint32_t)(i / p.stages) & 1u, q, &no_abort);
+        }
+    } else if (warp == 1 && pl.rank == 0) {
+        // --------------------------------------------------- products ----
+        const bool elected = elect_one();
+        const uint64_t adesc0 = operand_desc<W_MN>(smem_u32(pl.smem));
+        const uint64_t bdesc0 = operand_desc<false>(smem_u32(pl.smem) + HALF_BYTES);
+        const uint32_t stage_step = (uint32_t)p.stage_bytes >> 4;
+        for (; !ring.aborted && cur.find(p, t, lane, ti); t += pl.step) {
+            const uint32_t idesc = make_idesc_pair<W_MN, false>((ti.rows + 31) / 32 * 32);
+            if (!__all_sync(0xFFFFFFFFu, mbar_wait_cluster(pl.tempty(acc.at), acc.phase ^ 1u, p, pl.abort_flag))) {
+                ring.aborted = true;
+                break;
+            }
+            tc_fence_after();
+            const uint32_t d_tmem = tmem_base + (uint32_t)(acc.at * ACC_COLS);
+            for (int ks = 0; ks < p.nk; ++ks) {
+                if (!__all_sync(0xFFFFFFFFu, mbar_wait(pl.full(ring.at), ring.phase, p, pl.abort_flag))) {
+                    ring.aborted = true;
+                    break;
+                }
+                tc_fence_after();
+                if (elected) {
+                    const uint64_t adesc = adesc0 + ring.at * stage_step, bdesc = bdesc0 + ring.at * stage_step;
+#pragma unroll
+                    for (int kk = 0; kk < TK / 16; ++kk)
+                        tc_mma2_bf16(d_tmem, adesc + k16_step<W_MN>() * kk, bdesc + k16_step<false>() * kk, idesc,
+                                     (ks != 0 || kk != 0) ? 1u : 0u);
+                    tc_commit_pair(pl.empty(ring.at), 0);
+                }
+                ring.next(p.stages);
+            }
+            if (ring.aborted) break;
+            if (elected) tc_commit_pair(pl.tfull(acc.at), 0);
+            acc.next(NACC);
+        }
+        products_end(pl, p, ring);
+    } else if (warp >= 4) {
+        // --------------------------------------------------- epilogue ----
+        const int ew = warp - 4, quarter = ew & 3, half = ew >> 2;
+        const uint32_t lane_base = tmem_base + ((uint32_t)(quarter * 32) << 16);
+        const uint32_t stage = smem_u32(pl.smem + SMEM_WORK - (EPI_WARPS - ew) * EPI_STAGE);
+        Out out{stage, lane, 0u};
+        // GLU: lanes 0..63 hold gate columns, 64..127 the up columns of the same h;
+        // the gate warp hands act(gate) in fp32 to the up warp two quarters on
+        const bool gate = GLU && quarter < 2;
+        const int pair = (quarter & 1) + 2 * half;
+        const uint32_t to_up = smem_u32(pl.smem + SMEM_WORK - (EPI_WARPS - (quarter & 1) - 4 * half) * EPI_STAGE + 4096) +
+                               16u * lane;
+        uint32_t handed = 0;
+        bool ok = true;
+        for (; ok && cur.find(p, t, lane, ti); t += pl.step) {
+            ok = __all_sync(0xFFFFFFFFu, mbar_wait_cluster(pl.tfull(acc.at), acc.phase, p, pl.abort_flag));
+            if (!ok) break;
+            tc_fence_after();
+            const int chunks = (ti.rows + 31) / 32;
+            const int c0 = half == 0 ? 0 : (chunks + 1) / 2, c1 = half == 0 ? (chunks + 1) / 2 : chunks;
+            const uint32_t tacc = lane_base + (uint32_t)(acc.at * ACC_COLS);
+            const int col = GLU ? ti.ct * 128 + 64 * (int)pl.rank + 32 * (quarter & 1)
+                                : ti.ct * 256 + 128 * (int)pl.rank + 32 * quarter;
+            const int cols = p.N - col;
+            for (int c = c0; c < c1 && ok; ++c) {
+                uint32_t r[32];
+                tmem_ld_16x32(tacc + 32 * c, r);
+                tmem_ld_16x32(tacc + (16u << 16) + 32 * c, r + 16);
+                tmem_wait_ld();
+                if (c + 1 == c1) {      // the accumulator is read: the next tile may have it
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_remote(mapa(pl.tempty(acc.at), 0));
+                }
+                float v[32];
+#pragma unroll
+                for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+                const int64_t row = ti.row0 + 32 * c;
+                const int rows = ti.rows - 32 * c;
+                if constexpr (!GLU) {
+                    if (cols > 0) out.put(&tmY, static_cast<__nv_bfloat16*>(p.y), p.ldy, col, cols, row, rows, v);
+                } else {
+                    if (cols <= 0) continue;      // both warps
+                    if (p.a != nullptr)
+                        out.put(gate ? &tmA : &tmA2, p.a + (gate ? 0 : p.N), p.lda, col, cols, row, rows, v);
+                    if (gate) {
+                        ok = __all_sync(0xFFFFFFFFu, mbar_wait(pl.xempty(pair), handed & 1u ^ 1u, p, pl.abort_flag));
+                        if (!ok) break;
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) v[i] = act_of(v[i], ACT);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            st_shared_v4(to_up + 512u * i, __float_as_uint(v[4 * i]), __float_as_uint(v[4 * i + 1]),
+                                         __float_as_uint(v[4 * i + 2]), __float_as_uint(v[4 * i + 3]));
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(pl.xfull(pair));
+                    } else {
+                        ok = __all_sync(0xFFFFFFFFu, mbar_wait(pl.xfull(pair), handed & 1u, p, pl.abort_flag));
+                        if (!ok) break;
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            float g[4];
+                            asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                                         : "=f"(g[0]), "=f"(g[1]), "=f"(g[2]), "=f"(g[3])
+                                         : "r"(to_up + 512u * i)
+                                         : "memory");
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) v[4 * i + j] *= g[j];
+                        }
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(pl.xempty(pair));
+                        out.put(&tmY, static_cast<__nv_bfloat16*>(p.y), p.ldy, col, cols, row, rows, v);
+                    }
+                    ++handed;
+                }
+            }
+            if (c0 >= c1) {      // nothing of this tile is this warp's
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_remote(mapa(pl.tempty(acc.at), 0));
+            }
+            acc.next(NACC);
+        }
+        if (lane == 0) bulk_wait_group0();      // the stores are complete
+        __syncwarp();
+    }
+    tear_down(pl, tmem_base);
+}
+
+// ----------------------------------------------------- weight gradient ----
+
+// Tiles of 256 x p.bn of every group's D_g = x^T dy, the groups one after the
+// other; an empty group's are zeros.
+struct WTile {
+    int g, mt, nt, start, rows;
+};
+__device__ __forceinline__ WTile w_tile(const Params& p, int64_t t) {
+    const int per = p.m_tiles * p.col_tiles;
+    WTile w;
+    w.g = (int)(t / per);
+    const int i = (int)(t - (int64_t)w.g * per);
+    const int band = 8 * p.col_tiles, b = i / band, rem = i - b * band, width = min(8, p.m_tiles - 8 * b);
+    w.nt = rem / width;
+    w.mt = 8 * b + rem - w.nt * width;
+    const Span s = span_of(p, w.g);
+    w.start = s.start, w.rows = s.rows;
+    return w;
+}
+
+// 32 rows (a lane each) x 32 columns of D_g out of registers: a TMA store of a
+// staged box, or, of a width whose last columns are no whole 16 bytes, from here.
+template <bool F32>
+struct WOut {
+    uint32_t buf;
+    int lane;
+    uint32_t at;
+    __device__ __forceinline__ void put(const Params& p, const CUtensorMap* map, int g, int row0, int col,
+                                        const float* v) {
+        const int cols = p.N - col;
+        if (cols < 32 && (cols & 7) != 0) {
+            const int row = row0 + lane;
+            if (row >= p.K) return;
+            const int64_t o = g * p.gsy + (int64_t)row * p.ldy + col;
+#pragma unroll
+            for (int i = 0; i < 31; ++i) {
+                if (i < cols) {
+                    if (F32) static_cast<float*>(p.y)[o + i] = v[i];
+                    else static_cast<__nv_bfloat16*>(p.y)[o + i] = __float2bfloat16_rn(v[i]);
+                }
+            }
+            return;
+        }
+        const uint32_t b = F32 ? buf : buf + at;
+        at ^= 2048u;
+        if (lane == 0) {
+            if (F32) bulk_wait_group_read0();
+            else bulk_wait_group_read1();
+        }
+        __syncwarp();
+        if constexpr (F32) {
+            const uint32_t row = b + 128u * lane, sw = (uint32_t)lane & 7u;
+#pragma unroll
+            for (int c = 0; c < 8; ++c)
+                st_shared_v4(row + (((uint32_t)c ^ sw) << 4), __float_as_uint(v[4 * c]), __float_as_uint(v[4 * c + 1]),
+                             __float_as_uint(v[4 * c + 2]), __float_as_uint(v[4 * c + 3]));
+        } else {
+            const uint32_t row = b + 64u * lane, sw = (uint32_t)(lane >> 1) & 3u;
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+                st_shared_v4(row + (((uint32_t)c ^ sw) << 4), pack_bf16x2(v[8 * c], v[8 * c + 1]),
+                             pack_bf16x2(v[8 * c + 2], v[8 * c + 3]), pack_bf16x2(v[8 * c + 4], v[8 * c + 5]),
+                             pack_bf16x2(v[8 * c + 6], v[8 * c + 7]));
+        }
+        fence_proxy_async_shared();
+        __syncwarp();
+        if (lane == 0) {
+            asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(map),
+                         "r"(b), "r"(col), "r"(row0), "r"(g)
+                         : "memory");
+            bulk_commit_group();
+        }
+    }
+};
+
+template <bool F32>
+__global__ void __launch_bounds__(THREADS, 1)
+    k_wgrad(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmDY,
+            const __grid_constant__ CUtensorMap tmD, const Params p) {
+    if (threadIdx.x == 64) {
+        prefetch_map(&tmX);
+        prefetch_map(&tmDY);
+        prefetch_map(&tmD);
+    }
+    Place pl;
+    // two arrivals on a full barrier: the leader's producer makes both, or, of a
+    // step with rows to set to zero, warp 2 of either CTA one
+    const uint32_t tmem_base = set_up(pl, p.stages, 2);
+    wait_for_previous_kernels();
+    const int warp = pl.warp, lane = pl.lane;
+    const int bh = p.bn / 2, boxes = (bh + 63) / 64;      // of dy's columns, per CTA
+    const uint32_t bytes = HALF_BYTES + boxes * (HALF_BYTES / 2);
+    Ring ring, acc;
+    int64_t t = pl.first;
+
+    if (warp == 0) {
+        // ------------------------------------------------------ loads ----
+        const bool elected = elect_one();
+        const uint32_t lead_full = mapa(pl.full(0), 0);
+        for (; t < p.max_tiles && !ring.aborted; t += pl.step) {
+            const WTile w = w_tile(p, t);
+            const int nk = (w.rows + TK - 1) / TK;
+            const int am = w.mt * TM + 128 * (int)pl.rank, bn = w.nt * p.bn + bh * (int)pl.rank;
+            for (int ks = 0; ks < nk; ++ks) {
+                if (!__all_sync(0xFFFFFFFFu, mbar_wait_cluster(pl.empty(ring.at), ring.phase ^ 1u, p, pl.abort_flag))) {
+                    ring.aborted = true;
+                    break;
+                }
+                const bool ragged = ks + 1 == nk && (w.rows & 15) != 0;
+                const uint32_t fb = ragged ? mapa(pl.tail(ring.at), pl.rank) : lead_full + 8u * ring.at;
+                if (elected) {
+                    if (ragged) {
+                        mbar_expect_tx(pl.tail(ring.at), bytes);
+                    } else if (pl.rank == 0) {
+                        mbar_expect_tx(pl.full(ring.at), 2u * bytes);
+                        mbar_arrive(pl.full(ring.at));
+                    }
+                    const uint32_t sa = smem_u32(pl.smem + ring.at * p.stage_bytes), sb = sa + HALF_BYTES;
+                    const int row = w.start + ks * TK;
+                    tma2_load_2d(sa, &tmX, am, row, fb);
+                    tma2_load_2d(sa + HALF_BYTES / 2, &tmX, am + 64, row, fb);
+                    tma2_load_2d(sb, &tmDY, bn, row, fb);
+                    if (boxes > 1) tma2_load_2d(sb + HALF_BYTES / 2, &tmDY, bn + 64, row, fb);
+                }
+                ring.next(p.stages);
+            }
+        }
+        __syncwarp();
+        if (ring.aborted) {      // the copies in flight
+            const Params q = patient(p);
+            volatile int no_abort = 0;
+            for (int i = ring.count - min(ring.count, p.stages); i < ring.count; ++i)
+                mbar_wait_cluster(pl.full(i % p.stages), (uint32_t)(i / p.stages) & 1u, q, &no_abort);
+        }
+    } else if (warp == 2) {
+        // ------------------------------- zeros behind a group's last row ----
+        const uint32_t lead_full = mapa(pl.full(0), 0);
+        uint32_t phases = 0;      // of the tail barriers
+        for (; t < p.max_tiles; t += pl.step) {
+            const WTile w = w_tile(p, t);
+            const int nk = (w.rows + TK - 1) / TK, rest = w.rows & 15;
+            if (nk == 0) continue;
+            ring.at = (ring.at + nk) % p.stages;
+            if (rest == 0) continue;
+            const int s = ring.at == 0 ? p.stages - 1 : ring.at - 1;
+            if (!__all_sync(0xFFFFFFFFu, mbar_wait_cluster(pl.tail(s), phases >> s & 1u, p, pl.abort_flag))) break;
+            phases ^= 1u << s;
+            const int r0 = w.rows & (TK - 1), n = (16 - rest) * 8;      // 16-byte units of a box's rows r0 ..
+            const uint32_t at = smem_u32(pl.smem + s * p.stage_bytes) + 128u * r0;
+            for (int b = 0; b < 2 + boxes; ++b)
+                for (int i = lane; i < n; i += 32) st_shared_v4(at + b * (HALF_BYTES / 2) + 16u * i, 0u, 0u, 0u, 0u);
+            fence_proxy_async_shared();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_remote(lead_full + 8u * s);
+        }
+    } else if (warp == 1 && pl.rank == 0) {
+        // --------------------------------------------------- products ----
+        const bool elected = elect_one();
+        const uint32_t idesc = make_idesc_pair<true, true>(p.bn);
+        const uint64_t adesc0 = operand_desc<true>(smem_u32(pl.smem));
+        const uint64_t bdesc0 = operand_desc<true>(smem_u32(pl.smem) + HALF_BYTES);
+        const uint32_t stage_step = (uint32_t)p.stage_bytes >> 4;
+        for (; t < p.max_tiles && !ring.aborted; t += pl.step) {
+            const WTile w = w_tile(p, t);
+            if (w.rows == 0) continue;
+            const int nk = (w.rows + TK - 1) / TK;
+            if (!__all_sync(0xFFFFFFFFu, mbar_wait_cluster(pl.tempty(acc.at), acc.phase ^ 1u, p, pl.abort_flag))) {
+                ring.aborted = true;
+                break;
+            }
+            tc_fence_after();
+            const uint32_t d_tmem = tmem_base + (uint32_t)(acc.at * ACC_COLS);
+            for (int ks = 0; ks < nk; ++ks) {
+                if (!__all_sync(0xFFFFFFFFu, mbar_wait_cluster(pl.full(ring.at), ring.phase, p, pl.abort_flag))) {
+                    ring.aborted = true;
+                    break;
+                }
+                tc_fence_after();
+                if (elected) {
+                    const uint64_t adesc = adesc0 + ring.at * stage_step, bdesc = bdesc0 + ring.at * stage_step;
+                    const int left = (w.rows - ks * TK + 15) / 16;      // 16-row steps
+#pragma unroll
+                    for (int kk = 0; kk < TK / 16; ++kk)
+                        if (kk < left)
+                            tc_mma2_bf16(d_tmem, adesc + k16_step<true>() * kk, bdesc + k16_step<true>() * kk, idesc,
+                                         (ks != 0 || kk != 0) ? 1u : 0u);
+                    tc_commit_pair(pl.empty(ring.at), 0);
+                }
+                ring.next(p.stages);
+            }
+            if (ring.aborted) break;
+            if (elected) tc_commit_pair(pl.tfull(acc.at), 0);
+            acc.next(NACC);
+        }
+        products_end(pl, p, ring);
+    } else if (warp >= 4) {
+        // --------------------------------------------------- epilogue ----
+        const int ew = warp - 4, quarter = ew & 3, half = ew >> 2;
+        const uint32_t lane_base = tmem_base + ((uint32_t)(quarter * 32) << 16);
+        WOut<F32> out{smem_u32(pl.smem + SMEM_WORK - (EPI_WARPS - ew) * 4096), lane, 0u};
+        const int chunks = p.bn / 32, c0 = half == 0 ? 0 : (chunks + 1) / 2, c1 = half == 0 ? (chunks + 1) / 2 : chunks;
+        for (; t < p.max_tiles; t += pl.step) {
+            const WTile w = w_tile(p, t);
+            const int row0 = w.mt * TM + 128 * (int)pl.rank + quarter * 32;
+            const uint32_t tacc = lane_base + (uint32_t)(acc.at * ACC_COLS);
+            if (w.rows > 0) {
+                if (!__all_sync(0xFFFFFFFFu, mbar_wait_cluster(pl.tfull(acc.at), acc.phase, p, pl.abort_flag))) break;
+                tc_fence_after();
+            }
+            for (int c = c0; c < c1; ++c) {
+                float v[32];
+                if (w.rows > 0) {
+                    tmem_ld32(tacc + 32 * c, v);
+                    if (c + 1 == c1) {      // the accumulator is read: the next tile may have it
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive_remote(mapa(pl.tempty(acc.at), 0));
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) v[i] = 0.f;
+                }
+                const int col = w.nt * p.bn + 32 * c;
+                if (col < p.N && row0 < p.K) out.put(p, &tmD, w.g, row0, col, v);      // the whole warp
+            }
+            if (w.rows > 0) acc.next(NACC);
+        }
+        if (lane == 0) bulk_wait_group0();      // the stores are complete
+        __syncwarp();
+    }
+    tear_down(pl, tmem_base);
+}
+
+// -------------------------------------------- elementwise gated backward ----
+
+// da = [dh * up * act'(gate) | dh * act(gate)] of the rows that belong to a
+// group (da may be a itself).  `tpr` threads take a row; bound by its 10 bytes
+// per element of h.
+__global__ void __launch_bounds__(256) k_glu_rows(const __nv_bfloat16* __restrict__ dh, int64_t lddh,
+                                                  const __nv_bfloat16* a, int64_t lda, int act, __nv_bfloat16* da,
+                                                  int64_t ldda, int tpr, const Params p) {
+    wait_for_previous_kernels();
+    const int f = p.N, per = 256 / tpr;
+    const int64_t step = (int64_t)gridDim.x * per;
+    for (int64_t row = (int64_t)blockIdx.x * per + threadIdx.x / tpr; row < p.M; row += step) {
+        int lo = 0, hi = p.G;      // offsets[lo] <= row < offsets[hi], were they in order
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (p.offsets[mid] <= row) lo = mid;
+            else hi = mid;
+        }
+        const Span s = span_of(p, lo);
+        if (row < s.start || row >= (int64_t)s.start + s.rows) continue;
+        for (int c = threadIdx.x % tpr * 8; c < f; c += tpr * 8) {
+            float d[8], g[8], u[8];
+            unpack8(*reinterpret_cast<const uint4*>(dh + row * lddh + c), d);
+            unpack8(*reinterpret_cast<const uint4*>(a + row * lda + c), g);
+            unpack8(*reinterpret_cast<const uint4*>(a + row * lda + f + c), u);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float gj = g[j];
+                g[j] = d[j] * u[j] * act_slope(gj, act);
+                u[j] = d[j] * act_of(gj, act);
+            }
+            *reinterpret_cast<uint4*>(da + row * ldda + c) = pack8(g);
+            *reinterpret_cast<uint4*>(da + row * ldda + f + c) = pack8(u);
+        }
+    }
+}
+
+// ----------------------------------------------------------------- host ----
+
+static int g_max_clusters = 0;      // CTA pairs that run at a time
+
+static cudaLaunchConfig_t launch_cfg(int64_t pairs, cudaStream_t stream, cudaLaunchAttribute* attr) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(2 * pairs), 1, 1);
+    cfg.blockDim = dim3(THREADS, 1, 1);
+    cfg.dynamicSmemBytes = SMEM_BYTES;
+    cfg.stream = stream;
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cfg;
+}
+
+static cudaError_t set_attributes() {
+    const void* ks[] = {(const void*)k_rows<true, false, 0>,
+                        (const void*)k_rows<false, false, 0>,
+                        (const void*)k_rows<true, true, MOE_ACT_NONE>,
+                        (const void*)k_rows<true, true, MOE_ACT_RELU>,
+                        (const void*)k_rows<true, true, MOE_ACT_GELU>,
+                        (const void*)k_rows<true, true, MOE_ACT_SILU>,
+                        (const void*)k_wgrad<false>,
+                        (const void*)k_wgrad<true>};
+    for (const void* k : ks) {
+        const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
+        if (e != cudaSuccess) return e;
+    }
+    cudaLaunchAttribute attr[2];
+    cudaLaunchConfig_t cfg = launch_cfg(1024, nullptr, attr);
+    return cudaOccupancyMaxActiveClusters(&g_max_clusters, k_wgrad<false>, &cfg);
+}
+
+struct Mat {
+    const void* p;
+    int64_t rows, cols, ld, gs;      // gs: from one group's matrix to the next
+};
+constexpr int64_t kMaxTiles = 0x3FFFFFFF;
+
+// D = x op(W) of every group; x [M, depth], D's columns W's (W_MN) or its rows.
+template <bool W_MN, bool GLU, int ACT>
+static moe_status_t product_rows(const Mat& x, const Mat& w, Params p, cudaStream_t s) {
+    MOE_REQUIRE(g_max_clusters > 0, MOE_ERR_NOT_INITIALIZED);
+    p.n_max = (int)std::min<int64_t>(256, (p.M + 31) / 32 * 32);
+    int box = 16;      // rows of x per CTA that a stage has room for
+    while (2 * box < p.n_max) box *= 2;
+    p.stage_bytes = HALF_BYTES + box * TK * 2;
+    p.stages = std::min(MAX_STAGES, (SMEM_WORK - EPI_WARPS * (GLU ? 8192 : 4096)) / p.stage_bytes);
+    p.nk = (p.K + TK - 1) / TK;
+    const int cols = GLU ? 128 : 256;
+    p.col_tiles = (p.N + cols - 1) / cols;
+    p.max_tiles = (p.M / p.n_max + std::min<int64_t>(p.G, p.M)) * p.col_tiles;
+    MOE_REQUIRE(p.max_tiles <= kMaxTiles, MOE_ERR_UNSUPPORTED);
+    p.timeout_ns = 2000000000ull;
+    CUtensorMap tmW, tmX[4], tmY, tmA, tmA2;
+    bool ok = make_bf16_map3(&tmW, w.p, p.G, w.rows, w.cols, w.ld, w.gs, W_MN ? TK : 128);
+    for (int i = 0; i < 4; ++i) ok = ok && make_bf16_map(&tmX[i], x.p, x.rows, x.cols, x.ld, 16 << i);
+    // boxes that end inside 16 bytes are not stored through the map
+    ok = ok && make_store_map(&tmY, p.y, p.M, std::max(p.N & ~7, 8), p.ldy, false);
+    tmA = tmA2 = tmY;
+    if (p.a != nullptr)
+        ok = ok && make_store_map(&tmA, p.a, p.M, p.N, p.lda, false) &&
+             make_store_map(&tmA2, p.a + p.N, p.M, p.N, p.lda, false);
+    MOE_REQUIRE(ok, MOE_ERR_CUDA);
+    cudaLaunchAttribute attr[2];
+    cudaLaunchConfig_t cfg = launch_cfg(std::min<int64_t>(p.max_tiles, g_max_clusters), s, attr);
+    if (cudaLaunchKernelEx(&cfg, k_rows<W_MN, GLU, ACT>, tmW, tmX[0], tmX[1], tmX[2], tmX[3], tmY, tmA, tmA2, p) !=
+        cudaSuccess)
+        return MOE_ERR_CUDA;
+    MOE_CHECK_LAUNCH();
+    return MOE_OK;
+}
+
+// Columns of a weight gradient's tiles: the narrower ones' steps take 0.91, 0.80
+// and 0.56 of 256 columns', and fill 256-wide waves or odd widths better; no tile is
+// shorter than its epilogue.
+static int wgrad_width(int64_t tiles256, int N, double nk, int slots) {
+    const struct {
+        int bn;
+        double step;
+    } widths[] = {{256, 1.0}, {224, 0.91}, {192, 0.80}, {128, 0.56}};
+    int best = 256;
+    double least = 1e300;
+    for (const auto& w : widths) {
+        const int64_t tiles = tiles256 * ((N + w.bn - 1) / w.bn);
+        const double cost = (double)((tiles + slots - 1) / slots) * (std::max(nk * w.step, 5. * w.bn / 256.) + 1.);
+        if (cost < least) least = cost, best = w.bn;
+    }
+    return best;
+}
+
+// D_g [K, N] = x^T dy of every group
+static moe_status_t product_wgrad(const Mat& x, const Mat& dy, Params p, bool f32, cudaStream_t s) {
+    MOE_REQUIRE(g_max_clusters > 0, MOE_ERR_NOT_INITIALIZED);
+    const size_t size = f32 ? 4 : 2;
+    if (p.M == 0) {
+        for (int g = 0; g < p.G; ++g)
+            if (cudaMemset2DAsync(static_cast<char*>(p.y) + g * p.gsy * size, p.ldy * size, 0, p.N * size, p.K, s) !=
+                cudaSuccess)
+                return MOE_ERR_CUDA;
+        return MOE_OK;
+    }
+    p.m_tiles = (p.K + TM - 1) / TM;
+    p.bn = wgrad_width((int64_t)p.G * p.m_tiles, p.N, (double)p.M / p.G / TK, g_max_clusters);
+    p.col_tiles = (p.N + p.bn - 1) / p.bn;
+    p.max_tiles = (int64_t)p.G * p.m_tiles * p.col_tiles;
+    MOE_REQUIRE(p.max_tiles <= kMaxTiles, MOE_ERR_UNSUPPORTED);
+    p.stage_bytes = HALF_BYTES + (p.bn / 2 + 63) / 64 * (HALF_BYTES / 2);
+    p.stages = std::min(MAX_STAGES, (SMEM_WORK - EPI_WARPS * 4096) / p.stage_bytes);
+    p.timeout_ns = 2000000000ull;
+    CUtensorMap tmX, tmDY, tmD;
+    MOE_REQUIRE(make_bf16_map(&tmX, x.p, x.rows, x.cols, x.ld, TK) &&
+                    make_bf16_map(&tmDY, dy.p, dy.rows, dy.cols, dy.ld, TK) &&
+                    make_store_map3(&tmD, p.y, p.G, p.K, std::max(p.N & ~7, 8), p.ldy, p.gsy, f32),
+                MOE_ERR_CUDA);
+    cudaLaunchAttribute attr[2];
+    cudaLaunchConfig_t cfg = launch_cfg(std::min<int64_t>(p.max_tiles, g_max_clusters), s, attr);
+    const cudaError_t e = f32 ? cudaLaunchKernelEx(&cfg, k_wgrad<true>, tmX, tmDY, tmD, p)
+                              : cudaLaunchKernelEx(&cfg, k_wgrad<false>, tmX, tmDY, tmD, p);
+    if (e != cudaSuccess) return MOE_ERR_CUDA;
+    MOE_CHECK_LAUNCH();
+    return MOE_OK;
+}
+
+static bool size_ok(int64_t v) { return v >= 1 && v <= 0x7FFFFF00LL; }
+static bool row_ok(const void* p, int64_t ld) { return moe_aligned16(p) && ld % 8 == 0; }
+// strides that mean nothing (of one row, of one group), as the maps want them
+static int64_t stride_of(int64_t rows, int64_t cols, int64_t ld) {
+    return rows == 1 && ld >= cols ? (cols + 7) / 8 * 8 : ld;
+}
+static int64_t group_stride_of(int G, int64_t rows, int64_t ld, int64_t gs) { return G == 1 ? rows * ld : gs; }
+static bool groups_apart(int G, int64_t rows, int64_t cols, int64_t ld, int64_t gs) {
+    return G == 1 || gs >= (rows - 1) * ld + cols;
+}
+static bool act_ok(int a) { return a >= MOE_ACT_NONE && a <= MOE_ACT_SILU; }
+static bool groups_ok(const int32_t* offsets, const int32_t* rows) {
+    return reinterpret_cast<uintptr_t>(offsets) % 4 == 0 && reinterpret_cast<uintptr_t>(rows) % 4 == 0;
+}
+
+// dx = dz W^T and dW = x^T dz, each if asked for; W_g [K, N]
+static moe_status_t gradients(const Mat& dz, const Mat& x, const Mat& w, const Params& groups, int N, int K, void* dx,
+                              int64_t lddx, void* dw, bool f32, int64_t lddw, int64_t gsdw, cudaStream_t s) {
+    if (dx && groups.M > 0) {
+        Params p = groups;
+        p.N = K, p.K = N, p.y = dx, p.ldy = lddx;
+        const moe_status_t st = product_rows<false, false, 0>(dz, w, p, s);
+        if (st != MOE_OK) return st;
+    }
+    if (!dw) return MOE_OK;
+    Params p = groups;
+    p.N = N, p.K = K, p.y = dw, p.ldy = lddw, p.gsy = gsdw;
+    return product_wgrad(x, dz, p, f32, s);
+}
+
+}  // namespace grouped
+
+cudaError_t grouped_set_attributes() { return grouped::set_attributes(); }
+
+}  // namespace moe
+
+using namespace moe;
+using grouped::group_stride_of;
+using grouped::groups_apart;
+using grouped::row_ok;
+using grouped::size_ok;
+using grouped::stride_of;
+
+extern "C" moe_status_t grouped_linear_fwd(const void* x, int64_t ldx, const void* w, int64_t ldw, int64_t gsw,
+                                           const int32_t* offsets, const int32_t* rows, int G, int64_t M, int N,
+                                           int64_t K, void* y, int64_t ldy, int32_t* err, void* stream) {
+    MOE_REQUIRE(M >= 0 && N >= 1 && K >= 1 && G >= 1, MOE_ERR_INVALID_ARG);
+    MOE_REQUIRE(ldx >= K && ldw >= N && ldy >= N && groups_apart(G, K, N, ldw, gsw), MOE_ERR_INVALID_ARG);
+    MOE_REQUIRE(M <= 0x7FFFFF00LL && size_ok(N) && size_ok(K) && G <= grouped::MAX_GROUPS, MOE_ERR_UNSUPPORTED);
+    if (M == 0) return MOE_OK;
+    MOE_REQUIRE(x && w && y && offsets, MOE_ERR_INVALID_ARG);
+    ldx = stride_of(M, K, ldx), ldy = stride_of(M, N, ldy), ldw = stride_of(K, N, ldw);
+    gsw = group_stride_of(G, K, ldw, gsw);
+    MOE_REQUIRE(row_ok(x, ldx) && row_ok(w, ldw) && row_ok(y, ldy) && gsw % 8 == 0 && grouped::groups_ok(offsets, rows),
+                MOE_ERR_ALIGNMENT);
+    MOE_REQUIRE(device_initialized(), MOE_ERR_NOT_INITIALIZED);
+    grouped::Params p{};
+    p.offsets = offsets, p.rows = rows, p.G = G, p.M = M, p.N = N, p.K = (int)K;
+    p.y = y, p.ldy = ldy, p.err = err;
+    return grouped::product_rows<true, false, 0>({x, M, K, ldx, 0}, {w, K, N, ldw, gsw}, p, (cudaStream_t)stream);
+}
+
+extern "C" moe_status_t grouped_linear_bwd(const void* dy, int64_t lddy, const void* x, int64_t ldx, const void* w,
+                                           int64_t ldw, int64_t gsw, const int32_t* offsets, const int32_t* rows, int G,
+                                           int64_t M, int N, int64_t K, void* dx, int64_t lddx, void* dw, int dw_type,
+                                           int64_t lddw, int64_t gsdw, int32_t* err, void* stream) {
+    MOE_REQUIRE(M >= 0 && N >= 1 && K >= 1 && G >= 1 && (dx || dw), MOE_ERR_INVALID_ARG);
+    MOE_REQUIRE(dw_type == MOE_TYPE_BF16 || dw_type == MOE_TYPE_F32, MOE_ERR_INVALID_ARG);
+    MOE_REQUIRE(lddy >= N && (!dx || (ldw >= N && lddx >= K && groups_apart(G, K, N, ldw, gsw))) &&
+                    (!dw || (ldx >= K && lddw >= N && groups_apart(G, K, N, lddw, gsdw))),
+                MOE_ERR_INVALID_ARG);
+    MOE_REQUIRE(M <= 0x7FFFFF00LL && size_ok(N) && size_ok(K) && G <= grouped::MAX_GROUPS, MOE_ERR_UNSUPPORTED);
+    MOE_REQUIRE(M == 0 || (dy && offsets && (!dx || w) && (!dw || x)), MOE_ERR_INVALID_ARG);
+    lddy = stride_of(M, N, lddy), ldx = stride_of(M, K, ldx), lddx = stride_of(M, K, lddx);
+    ldw = stride_of(K, N, ldw), lddw = stride_of(K, N, lddw);
+    gsw = group_stride_of(G, K, ldw, gsw), gsdw = group_stride_of(G, K, lddw, gsdw);
+    MOE_REQUIRE(row_ok(dy, lddy) && (!dx || (row_ok(w, ldw) && gsw % 8 == 0 && row_ok(dx, lddx))) &&
+                    (!dw || (row_ok(x, ldx) && row_ok(dw, lddw) && gsdw % 8 == 0)) && grouped::groups_ok(offsets, rows),
+                MOE_ERR_ALIGNMENT);
+    MOE_REQUIRE(device_initialized(), MOE_ERR_NOT_INITIALIZED);
+    grouped::Params p{};
+    p.offsets = offsets, p.rows = rows, p.G = G, p.M = M, p.err = err;
+    return grouped::gradients({dy, M, N, lddy, 0}, {x, M, K, ldx, 0}, {w, K, N, ldw, gsw}, p, N, (int)K, dx, lddx, dw,
+                              dw_type == MOE_TYPE_F32, lddw, gsdw, (cudaStream_t)stream);
+}
+
+extern "C" moe_status_t grouped_ffn_fwd(const void* x, int64_t ldx, const void* w1, int64_t ldw, int64_t gsw, int act,
+                                        const int32_t* offsets, const int32_t* rows, int G, int64_t M, int f, int64_t d,
+                                        void* h, int64_t ldh, void* a, int64_t lda, int32_t* err, void* stream) {
+    const int64_t f2 = 2 * (int64_t)f;
+    MOE_REQUIRE(M >= 0 && f >= 1 && d >= 1 && G >= 1 && grouped::act_ok(act), MOE_ERR_INVALID_ARG);
+    MOE_REQUIRE(ldx >= d && ldw >= f2 && ldh >= f && (!a || lda >= f2) && groups_apart(G, d, f2, ldw, gsw),
+                MOE_ERR_INVALID_ARG);
+    MOE_REQUIRE(f % 8 == 0 && M <= 0x7FFFFF00LL && f <= 0x3FFFFF00 && size_ok(d) && G <= grouped::MAX_GROUPS,
+                MOE_ERR_UNSUPPORTED);
+    if (M == 0) return MOE_OK;
+    MOE_REQUIRE(x && w1 && h && offsets, MOE_ERR_INVALID_ARG);
+    ldx = stride_of(M, d, ldx), ldw = stride_of(d, f2, ldw), ldh = stride_of(M, f, ldh), lda = stride_of(M, f2, lda);
+    gsw = group_stride_of(G, d, ldw, gsw);
+    MOE_REQUIRE(row_ok(x, ldx) && row_ok(w1, ldw) && row_ok(h, ldh) && (!a || row_ok(a, lda)) && gsw % 8 == 0 &&
+                    grouped::groups_ok(offsets, rows),
+                MOE_ERR_ALIGNMENT);
+    MOE_REQUIRE(device_initialized(), MOE_ERR_NOT_INITIALIZED);
+    grouped::Params p{};
+    p.offsets = offsets, p.rows = rows, p.G = G, p.M = M, p.N = f, p.K = (int)d, p.up = f;
+    p.y = h, p.ldy = ldh, p.a = static_cast<__nv_bfloat16*>(a), p.lda = lda, p.err = err;
+    const grouped::Mat mx{x, M, d, ldx, 0}, mw{w1, d, f2, ldw, gsw};
+    cudaStream_t s = (cudaStream_t)stream;
+    switch (act) {
+        case MOE_ACT_RELU: return grouped::product_rows<true, true, MOE_ACT_RELU>(mx, mw, p, s);
+        case MOE_ACT_GELU: return grouped::product_rows<true, true, MOE_ACT_GELU>(mx, mw, p, s);
+        case MOE_ACT_SILU: return grouped::product_rows<true, true, MOE_ACT_SILU>(mx, mw, p, s);
+        default: return grouped::product_rows<true, true, MOE_ACT_NONE>(mx, mw, p, s);
+    }
+}
+
+extern "C" moe_status_t grouped_ffn_bwd(const void* dh, int64_t lddh, const void* a, int64_t lda, const void* x,
+                                        int64_t ldx, const void* w1, int64_t ldw, int64_t gsw, int act,
+                                        const int32_t* offsets, const int32_t* rows, int G, int64_t M, int f, int64_t d,
+                                        void* da, int64_t ldda, void* dx, int64_t lddx, void* dw1, int dw_type,
+                                        int64_t lddw, int64_t gsdw, int32_t* err, void* stream) {
+    const int64_t f2 = 2 * (int64_t)f;
+    MOE_REQUIRE(M >= 0 && f >= 1 && d >= 1 && G >= 1 && grouped::act_ok(act), MOE_ERR_INVALID_ARG);
+    MOE_REQUIRE(dw_type == MOE_TYPE_BF16 || dw_type == MOE_TYPE_F32, MOE_ERR_INVALID_ARG);
+    MOE_REQUIRE(lddh >= f && lda >= f2 && ldda >= f2 &&
+                    (!dx || (ldw >= f2 && lddx >= d && groups_apart(G, d, f2, ldw, gsw))) &&
+                    (!dw1 || (ldx >= d && lddw >= f2 && groups_apart(G, d, f2, lddw, gsdw))),
+                MOE_ERR_INVALID_ARG);
+    MOE_REQUIRE(f % 8 == 0 && M <= 0x7FFFFF00LL && f <= 0x3FFFFF00 && size_ok(d) && G <= grouped::MAX_GROUPS,
+                MOE_ERR_UNSUPPORTED);
+    MOE_REQUIRE(M == 0 || (dh && a && da && offsets && (!dx || w1) && (!dw1 || x)), MOE_ERR_INVALID_ARG);
+    lddh = stride_of(M, f, lddh), lda = stride_of(M, f2, lda), ldda = stride_of(M, f2, ldda);
+    ldx = stride_of(M, d, ldx), lddx = stride_of(M, d, lddx), ldw = stride_of(d, f2, ldw), lddw = stride_of(d, f2, lddw);
+    gsw = group_stride_of(G, d, ldw, gsw), gsdw = group_stride_of(G, d, lddw, gsdw);
+    MOE_REQUIRE(row_ok(dh, lddh) && row_ok(a, lda) && row_ok(da, ldda) &&
+                    (!dx || (row_ok(w1, ldw) && gsw % 8 == 0 && row_ok(dx, lddx))) &&
+                    (!dw1 || (row_ok(x, ldx) && row_ok(dw1, lddw) && gsdw % 8 == 0)) && grouped::groups_ok(offsets, rows),
+                MOE_ERR_ALIGNMENT);
+    MOE_REQUIRE(device_initialized(), MOE_ERR_NOT_INITIALIZED);
+    grouped::Params p{};
+    p.offsets = offsets, p.rows = rows, p.G = G, p.M = M, p.err = err;
+    cudaStream_t s = (cudaStream_t)stream;
+    if (M > 0) {
+        int tpr = 8;
+        while (tpr < 256 && tpr * 8 < f) tpr *= 2;
+        const int64_t blocks = std::min<int64_t>((M * tpr + 255) / 256, (int64_t)device_sm_count() * 8);
+        grouped::Params q = p;
+        q.N = f;
+        if (launch_early(dim3((unsigned)blocks), 256, 0, s, grouped::k_glu_rows, static_cast<const __nv_bfloat16*>(dh),
+                         lddh, static_cast<const __nv_bfloat16*>(a), lda, act, static_cast<__nv_bfloat16*>(da), ldda, tpr,
+                         q) != cudaSuccess)
+            return MOE_ERR_CUDA;
+    }
+    return grouped::gradients({da, M, f2, ldda, 0}, {x, M, d, ldx, 0}, {w1, d, f2, ldw, gsw}, p, (int)f2, (int)d, dx, lddx,
+                              dw1, dw_type == MOE_TYPE_F32, lddw, gsdw, s);
+}

@@ -101,6 +101,50 @@ static int mat(PyObject* t, long long dev, int types, int64_t m, int64_t n, Mat*
     return address(t, &o->p);
 }
 
+typedef struct {
+    Mat m;
+    int64_t g, gs;         /* matrices, elements from one to the next */
+} Mats;
+
+/* [g, m, n] (-1: any): g matrices; all zero for None. */
+static int mats(PyObject* t, long long dev, int types, int64_t g, int64_t m, int64_t n, Mats* o) {
+    memset(o, 0, sizeof(*o));
+    if (t == Py_None) return 1;
+    int bit, r = dtype_bit(t, &bit);
+    if (r <= 0) return r;
+    if (!(bit & types)) return 0;
+    if ((r = on_device(t, dev)) <= 0) return r;
+    PyObject* shape = PyObject_GetAttr(t, s_shape);
+    if (shape == NULL) return -1;
+    PyObject* stride = NULL;
+    r = 0;
+    if (PyTuple_Check(shape) && PyTuple_GET_SIZE(shape) == 3) {
+        r = -1;
+        stride = PyObject_CallMethodNoArgs(t, s_stride);
+        if (stride != NULL) r = PyTuple_Check(stride) && PyTuple_GET_SIZE(stride) == 3;
+    }
+    if (r > 0) {
+        o->g = PyLong_AsLongLong(PyTuple_GET_ITEM(shape, 0));
+        o->m.m = PyLong_AsLongLong(PyTuple_GET_ITEM(shape, 1));
+        o->m.n = PyLong_AsLongLong(PyTuple_GET_ITEM(shape, 2));
+        o->gs = PyLong_AsLongLong(PyTuple_GET_ITEM(stride, 0));
+        o->m.ld = PyLong_AsLongLong(PyTuple_GET_ITEM(stride, 1));
+        const int64_t step = PyLong_AsLongLong(PyTuple_GET_ITEM(stride, 2));
+        if (PyErr_Occurred()) {
+            r = -1;
+        } else {
+            if (o->m.m <= 1 && o->m.ld < o->m.n) o->m.ld = o->m.n;
+            r = o->m.ld >= o->m.n && (step == 1 || o->m.n == 1) && (g < 0 || o->g == g) && (m < 0 || o->m.m == m) &&
+                (n < 0 || o->m.n == n);
+        }
+    }
+    Py_DECREF(shape);
+    Py_XDECREF(stride);
+    if (r <= 0) return r;
+    o->m.type = bit == F32 ? MOE_TYPE_F32 : MOE_TYPE_BF16;
+    return address(t, &o->m.p);
+}
+
 /* A contiguous tensor of n elements; NULL for None. */
 static int flat(PyObject* t, long long dev, int types, int64_t n, void** p, int* type) {
     *p = NULL;
@@ -360,6 +404,103 @@ static PyObject* adamw(PyObject* self, PyObject* const* a, Py_ssize_t k) {
     MAKE(adamw_step(table, (int)tensors, tiles, (int)pt, (int)gt, (int)bits, &o, st));
 }
 
+/* offsets [g + 1] and rows [g] or None */
+static int groups(PyObject* offsets, PyObject* rows, long long dev, int64_t g, void** o, void** r) {
+    const int st = flat(offsets, dev, I32, g + 1, o, NULL);
+    if (st <= 0) return st;
+    if (offsets == Py_None || g > INT32_MAX) return 0;
+    return flat(rows, dev, I32, g, r, NULL);
+}
+
+/* (x, w, offsets, rows, y, err, stream) */
+static PyObject* grp_fwd(PyObject* self, PyObject* const* a, Py_ssize_t k) {
+    long long dev;
+    Mat x, y;
+    Mats w;
+    void *o, *r, *err, *st;
+    TRY(arity(k, 7));
+    TRY(current_device(&dev));
+    TRY(mat(a[0], dev, BF16, -1, -1, &x));
+    TRY(mats(a[1], dev, BF16, -1, x.n, -1, &w));
+    TRY(groups(a[2], a[3], dev, w.g, &o, &r));
+    TRY(mat(a[4], dev, BF16, x.m, w.m.n, &y));
+    TRY(flat(a[5], dev, I32, 1, &err, NULL));
+    TRY(a[0] != Py_None && a[1] != Py_None && a[4] != Py_None && w.m.n <= INT32_MAX);
+    TRY(handle(a[6], dev, &st));
+    MAKE(grouped_linear_fwd(x.p, x.ld, w.m.p, w.m.ld, w.gs, o, r, (int)w.g, x.m, (int)w.m.n, x.n, y.p, y.ld, err, st));
+}
+
+/* (dy, x, w, offsets, rows, dx, dw, err, stream) */
+static PyObject* grp_bwd(PyObject* self, PyObject* const* a, Py_ssize_t k) {
+    long long dev;
+    Mat dy, x, dx;
+    Mats w, dw;
+    void *o, *r, *err, *st;
+    TRY(arity(k, 9));
+    TRY(current_device(&dev));
+    TRY(mat(a[0], dev, BF16, -1, -1, &dy));
+    TRY(mat(a[1], dev, BF16, dy.m, -1, &x));
+    TRY(mats(a[2], dev, BF16, -1, x.n, dy.n, &w));
+    TRY(groups(a[3], a[4], dev, w.g, &o, &r));
+    TRY(mat(a[5], dev, BF16, dy.m, x.n, &dx));
+    TRY(mats(a[6], dev, BF16 | F32, w.g, x.n, dy.n, &dw));
+    TRY(flat(a[7], dev, I32, 1, &err, NULL));
+    TRY(a[0] != Py_None && a[1] != Py_None && a[2] != Py_None && dy.n <= INT32_MAX);
+    TRY(handle(a[8], dev, &st));
+    MAKE(grouped_linear_bwd(dy.p, dy.ld, x.p, x.ld, w.m.p, w.m.ld, w.gs, o, r, (int)w.g, dy.m, (int)dy.n, x.n, dx.p, dx.ld,
+                            dw.m.p, dw.m.type, dw.m.ld, dw.gs, err, st));
+}
+
+/* (x, w1, act, offsets, rows, h, a, err, stream) */
+static PyObject* grp_ffn_fwd(PyObject* self, PyObject* const* a, Py_ssize_t k) {
+    long long dev;
+    Mat x, h, g;
+    Mats w;
+    void *o, *r, *err, *st;
+    TRY(arity(k, 9));
+    TRY(current_device(&dev));
+    TRY(mat(a[0], dev, BF16, -1, -1, &x));
+    TRY(mats(a[1], dev, BF16, -1, x.n, -1, &w));
+    const long act = PyLong_AsLong(a[2]);
+    if (act == -1 && PyErr_Occurred()) return NULL;
+    TRY(w.m.n % 2 == 0 && w.m.n <= INT32_MAX);
+    TRY(groups(a[3], a[4], dev, w.g, &o, &r));
+    TRY(mat(a[5], dev, BF16, x.m, w.m.n / 2, &h));
+    TRY(mat(a[6], dev, BF16, x.m, w.m.n, &g));
+    TRY(flat(a[7], dev, I32, 1, &err, NULL));
+    TRY(a[0] != Py_None && a[1] != Py_None && a[5] != Py_None);
+    TRY(handle(a[8], dev, &st));
+    MAKE(grouped_ffn_fwd(x.p, x.ld, w.m.p, w.m.ld, w.gs, (int)act, o, r, (int)w.g, x.m, (int)(w.m.n / 2), x.n, h.p, h.ld,
+                         g.p, g.ld, err, st));
+}
+
+/* (dh, a, x, w1, act, offsets, rows, da, dx, dw1, err, stream) */
+static PyObject* grp_ffn_bwd(PyObject* self, PyObject* const* a, Py_ssize_t k) {
+    long long dev;
+    Mat dh, g, x, da, dx;
+    Mats w, dw;
+    void *o, *r, *err, *st;
+    TRY(arity(k, 12));
+    TRY(current_device(&dev));
+    TRY(mat(a[0], dev, BF16, -1, -1, &dh));
+    TRY(dh.n <= INT32_MAX / 2);
+    TRY(mat(a[1], dev, BF16, dh.m, 2 * dh.n, &g));
+    TRY(mat(a[2], dev, BF16, dh.m, -1, &x));
+    TRY(mats(a[3], dev, BF16, -1, x.n, 2 * dh.n, &w));
+    const long act = PyLong_AsLong(a[4]);
+    if (act == -1 && PyErr_Occurred()) return NULL;
+    TRY(groups(a[5], a[6], dev, w.g, &o, &r));
+    TRY(mat(a[7], dev, BF16, dh.m, 2 * dh.n, &da));
+    TRY(mat(a[8], dev, BF16, dh.m, x.n, &dx));
+    TRY(mats(a[9], dev, BF16 | F32, w.g, x.n, 2 * dh.n, &dw));
+    TRY(flat(a[10], dev, I32, 1, &err, NULL));
+    for (int i = 0; i < 4; ++i) TRY(a[i] != Py_None);
+    TRY(a[7] != Py_None);
+    TRY(handle(a[11], dev, &st));
+    MAKE(grouped_ffn_bwd(dh.p, dh.ld, g.p, g.ld, x.p, x.ld, w.m.p, w.m.ld, w.gs, (int)act, o, r, (int)w.g, dh.m,
+                         (int)dh.n, x.n, da.p, da.ld, dx.p, dx.ld, dw.m.p, dw.m.type, dw.m.ld, dw.gs, err, st));
+}
+
 /* a[0..3]: logits, idx, teacher, teacher_lse, a[4]: temperature */
 typedef struct {
     Mat x, idx, t;
@@ -451,6 +592,10 @@ static PyMethodDef methods[] = {FAST("setup", setup),
                                 FAST("gated_ffn_fwd", ffn_fwd),
                                 FAST("gated_ffn_bwd", ffn_bwd),
                                 FAST("adamw_step", adamw),
+                                FAST("grouped_linear_fwd", grp_fwd),
+                                FAST("grouped_linear_bwd", grp_bwd),
+                                FAST("grouped_ffn_fwd", grp_ffn_fwd),
+                                FAST("grouped_ffn_bwd", grp_ffn_bwd),
                                 FAST("distill_loss_fwd", dist_fwd),
                                 FAST("distill_loss_bwd", dist_bwd),
                                 FAST("distill_loss", dist_both),

@@ -59,7 +59,8 @@ EXPORTS = [
     "rmsnorm_residual_fwd", "rmsnorm_bwd_workspace_size", "rmsnorm_residual_bwd",
     "adamw_plan_bytes", "adamw_plan_encode", "adamw_step",
     "linear_fwd", "linear_bwd_workspace_size", "linear_bwd", "gated_ffn_fwd", "gated_ffn_bwd",
-    "moe_selftest_dense_plan", "distill_loss_fwd", "distill_loss_bwd", "distill_loss",
+    "moe_selftest_dense_plan", "grouped_linear_fwd", "grouped_linear_bwd", "grouped_ffn_fwd", "grouped_ffn_bwd",
+    "distill_loss_fwd", "distill_loss_bwd", "distill_loss",
 ]
 
 _vp, _i32, _i64, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t
@@ -168,6 +169,13 @@ _SIGS = {
     "adamw_plan_bytes": (_sz, [_i32]),
     "adamw_plan_encode": (_i32, [_vp, _i32, _i32, _i32, _i32, _vp, ctypes.POINTER(_i64)]),
     "adamw_step": (_i32, [_vp, _i32, _i64, _i32, _i32, _i32, _vp, _vp]),
+    "grouped_linear_fwd": (_i32, [_vp, _i64, _vp, _i64, _i64, _vp, _vp, _i32, _i64, _i32, _i64, _vp, _i64, _vp, _vp]),
+    "grouped_linear_bwd": (_i32, [_vp, _i64, _vp, _i64, _vp, _i64, _i64, _vp, _vp, _i32, _i64, _i32, _i64, _vp, _i64, _vp,
+                                  _i32, _i64, _i64, _vp, _vp]),
+    "grouped_ffn_fwd": (_i32, [_vp, _i64, _vp, _i64, _i64, _i32, _vp, _vp, _i32, _i64, _i32, _i64, _vp, _i64, _vp, _i64,
+                               _vp, _vp]),
+    "grouped_ffn_bwd": (_i32, [_vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _i64, _i32, _vp, _vp, _i32, _i64, _i32, _i64,
+                               _vp, _i64, _vp, _i64, _vp, _i32, _i64, _i64, _vp, _vp]),
     "distill_loss_fwd": (_i32, [_vp, _i32, _i64, _vp, _i64, _vp, _i32, _i64, _vp, _f32, _i64, _i32, _i32, _vp, _vp, _vp,
                                 _vp]),
     "distill_loss_bwd": (_i32, [_vp, _vp, _i32, _i64, _vp, _i64, _vp, _i32, _i64, _vp, _vp, _f32, _i64, _i32, _i32, _vp,
@@ -899,6 +907,83 @@ def adamw_step(plan, lr, betas=(0.9, 0.999), eps=1e-8, step=1, grad_scale=None, 
     st = _marshal.adamw_step(*plan.args, lr, betas[0], betas[1], eps, step, grad_scale, seed, stream)
     if st:
         raise MoEError("adamw_step", st)
+
+
+# ------------------------------------------- bf16 products grouped by expert ----
+
+def _new_groups(w, dtype, like, stream):
+    """Uninitialised matrices of w's shape, their rows at multiples of 16 bytes."""
+    G, K, N = w.shape
+    t = _new((G, K, (N + 7) // 8 * 8), dtype, like, stream)
+    return t if N % 8 == 0 else t[:, :, :N]
+
+
+def _size_groups(fn, x, w):
+    _need(fn, isinstance(x, torch.Tensor) and x.dim() == 2 and isinstance(w, torch.Tensor) and w.dim() == 3)
+
+
+def grouped_linear_fwd(x, w, offsets, rows=None, y=None, err=None, stream=None):
+    """y[r] = x[r] w[g] for the rows r of every group g (bf16; w [G, K, N]):
+    offsets[g] .. offsets[g + 1], or rows[g] of them (int32 device tensors).
+    Rows of no group are not written.  See include/moe.h.  Returns y."""
+    fn = "grouped_linear_fwd"
+    if y is None:
+        _size_groups(fn, x, w)
+        y = _new_rows(x.shape[0], w.shape[2], torch.bfloat16, x, stream)
+    st = _marshal.grouped_linear_fwd(x, w, offsets, rows, y, err, stream)
+    if st:
+        raise MoEError(fn, st)
+    return y
+
+
+def grouped_linear_bwd(dy, x, w, offsets, rows=None, want_dx=True, want_dw=True, dx=None, dw=None,
+                       dw_dtype=torch.bfloat16, err=None, stream=None):
+    """Gradients of grouped_linear_fwd: dx and dw [G, K, N] (bfloat16 or float32),
+    those that are wanted or given.  See include/moe.h.  Returns (dx, dw)."""
+    fn = "grouped_linear_bwd"
+    if (want_dx and dx is None) or (want_dw and dw is None):
+        _size_groups(fn, x, w)
+        if want_dx and dx is None:
+            dx = _new_rows(x.shape[0], x.shape[1], torch.bfloat16, x, stream)
+        if want_dw and dw is None:
+            dw = _new_groups(w, dw_dtype, x, stream)
+    st = _marshal.grouped_linear_bwd(dy, x, w, offsets, rows, dx, dw, err, stream)
+    if st:
+        raise MoEError(fn, st)
+    return dx, dw
+
+
+def grouped_ffn_fwd(x, w1, offsets, rows=None, act="silu", h=None, a=None, want_a=False, err=None, stream=None):
+    """[gate | up] = x[r] w1[g], h = act(gate) * up for the rows r of every group
+    g in one kernel (bf16; w1 [G, d, 2f]).  See include/moe.h.  Returns h, or
+    (h, a) when a = [gate | up] is asked for."""
+    fn = "grouped_ffn_fwd"
+    if h is None or (want_a and a is None):
+        _size_groups(fn, x, w1)
+        M, f2 = x.shape[0], w1.shape[2]
+        h = h if h is not None else _new_rows(M, f2 // 2, torch.bfloat16, x, stream)
+        a = a if a is not None or not want_a else _new_rows(M, f2, torch.bfloat16, x, stream)
+    st = _marshal.grouped_ffn_fwd(x, w1, _act(fn, act), offsets, rows, h, a, err, stream)
+    if st:
+        raise MoEError(fn, st)
+    return h if a is None else (h, a)
+
+
+def grouped_ffn_bwd(dh, a, x, w1, offsets, rows=None, act="silu", want_dx=True, want_dw=True, dx=None, dw1=None, da=None,
+                    dw_dtype=torch.bfloat16, err=None, stream=None):
+    """Gradients of grouped_ffn_fwd from the kept a: dx and dw1 (bfloat16 or
+    float32); da [M, 2f] is written on the way (may be a itself).  See
+    include/moe.h.  Returns (dx, dw1)."""
+    fn = "grouped_ffn_bwd"
+    if da is None or (want_dx and dx is None) or (want_dw and dw1 is None):
+        _size_groups(fn, x, w1)
+        da = da if da is not None else _new_rows(x.shape[0], w1.shape[2], torch.bfloat16, x, stream)
+        dx = dx if dx is not None or not want_dx else _new_rows(x.shape[0], x.shape[1], torch.bfloat16, x, stream)
+        dw1 = dw1 if dw1 is not None or not want_dw else _new_groups(w1, dw_dtype, x, stream)
+    st = _marshal.grouped_ffn_bwd(dh, a, x, w1, _act(fn, act), offsets, rows, da, dx, dw1, err, stream)
+    if st:
+        raise MoEError(fn, st)
+    return dx, dw1
 
 
 # ------------------------------------------------------ distillation loss ----

@@ -1010,6 +1010,50 @@ MOE_API moe_status_t adamw_step(void* plan, int tensors, int64_t tiles, int p_ty
                                 const moe_adamw_opts_t* opts, void* stream);
 
 /*
+ * bf16 products grouped by expert, groups of any number of rows (the MXFP8 and
+ * NVFP4 grouped GEMMs above take quantized operands and groups of whole 128
+ * rows).  x [M, K] holds the rows of group g = 0 .. G - 1 from offsets[g] on;
+ * W_g [K, N] starts gsw elements after W_{g-1}.
+ *   offsets  device, G + 1 values, 0 <= offsets[g] <= offsets[g + 1] <= M.  Rows
+ *            before offsets[0] and from offsets[G] on belong to no group.
+ *   rows     device, G values, or NULL: group g has the rows offsets[g] ..
+ *            offsets[g] + rows[g] - 1, at most up to offsets[g + 1] (a layout with
+ *            padding between the groups); NULL: up to offsets[g + 1].
+ * Rows of no group are not written, and what they hold (NaN included) enters
+ * no result.  Offsets out of order or range give MOE_ERR_BAD_OFFSETS in err and
+ * results that are not specified, inside the outputs.  All matrices are bf16 with rows
+ * at multiples of 16 bytes (the TMA's rule; gsw, gsdw multiples of 8), sizes
+ * free; the strides of one row and of one group mean nothing.  G <= 65536.
+ * Products are accumulated in fp32 and rounded once; the same bits on every
+ * run.  M = 0 does nothing, but for zeros to dw.  err (may be NULL) also receives
+ * MOE_ERR_DEVICE_TIMEOUT.
+ *
+ * grouped_linear_fwd  y[r] = x[r] W_g for the rows r of every group g; y [M, N].
+ * grouped_linear_bwd  dx[r] = dy[r] W_g^T and dW_g = x_g^T dy_g (dw_type; gsdw
+ *   elements from one to the next; zeros for a group without rows), each if not NULL.
+ * grouped_ffn_fwd     [gate | up] = x[r] W1_g, h = act(gate) * up of the unrounded two
+ *   in one kernel; W1_g [d, 2f], f % 8 == 0; a [M, 2f] = [gate | up] or NULL (kept for
+ *   the backward pass).
+ * grouped_ffn_bwd     da = [dh up act'(gate) | dh act(gate)] (bf16, the operand of the
+ *   two products; may be a itself), dx = da W1_g^T, dW1_g = x_g^T da_g.
+ */
+MOE_API moe_status_t grouped_linear_fwd(const void* x, int64_t ldx, const void* w, int64_t ldw, int64_t gsw,
+                                        const int32_t* offsets, const int32_t* rows, int G, int64_t M, int N, int64_t K,
+                                        void* y, int64_t ldy, int32_t* err, void* stream);
+MOE_API moe_status_t grouped_linear_bwd(const void* dy, int64_t lddy, const void* x, int64_t ldx, const void* w,
+                                        int64_t ldw, int64_t gsw, const int32_t* offsets, const int32_t* rows, int G,
+                                        int64_t M, int N, int64_t K, void* dx, int64_t lddx, void* dw, int dw_type,
+                                        int64_t lddw, int64_t gsdw, int32_t* err, void* stream);
+MOE_API moe_status_t grouped_ffn_fwd(const void* x, int64_t ldx, const void* w1, int64_t ldw, int64_t gsw, int act,
+                                     const int32_t* offsets, const int32_t* rows, int G, int64_t M, int f, int64_t d,
+                                     void* h, int64_t ldh, void* a, int64_t lda, int32_t* err, void* stream);
+MOE_API moe_status_t grouped_ffn_bwd(const void* dh, int64_t lddh, const void* a, int64_t lda, const void* x,
+                                     int64_t ldx, const void* w1, int64_t ldw, int64_t gsw, int act,
+                                     const int32_t* offsets, const int32_t* rows, int G, int64_t M, int f, int64_t d,
+                                     void* da, int64_t ldda, void* dx, int64_t lddx, void* dw1, int dw_type,
+                                     int64_t lddw, int64_t gsdw, int32_t* err, void* stream);
+
+/*
  * Distillation from a teacher's top logits.  For every row (token) of the
  * student's logits x [M, V], with z = x / tau and q = softmax(z), and the k
  * tokens idx [M, k] that the teacher kept with their logits t [M, k]:
