@@ -627,12 +627,11 @@ bool make_store_map3(CUtensorMap* m, void* base, int64_t G, int64_t rows, int64_
     const cuuint64_t size = f32 ? 4 : 2;
     cuuint64_t gdim[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)G};
     cuuint64_t gstr[2] = {(cuuint64_t)ld * size, (cuuint64_t)gs * size};
-    cuuint32_t box[3] = {32, 32, 1}, estr[3] = {1, 1, 1};
+    cuuint32_t box[3] = {f32 ? 16u : 32u, 32, 1}, estr[3] = {1, 1, 1};      // 64 bytes x 32 rows
     if (g_encode == nullptr) return false;
     return g_encode(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, base, gdim, gstr,
-                    box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                    f32 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
-                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+                    box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B,
+                    CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // rank-2/3 uint8 tensor map, 128x128 boxes, 128-byte swizzle

@@ -15,11 +15,13 @@
 // that is too long for the group reads the next one's rows, whose results are not
 // stored (a product's rows do not mix).  D^T is turned round on its way to
 // memory by the matrix stores to shared memory.
-// The weight gradient (k_wgrad) contracts over the group's rows; those of the next
-// group that its last 16-row step holds are set to zero in shared memory, in both
-// operands (zero times an infinity would not be zero).
+// The weight gradient (k_wgrad) contracts over the group's rows.  The TMA brings
+// whole 16-row steps; the up to 15 rows that remain come in a 16-row step of their own,
+// which two warps fill with plain loads a tile ahead, zeros behind the last row (in both
+// operands: zero times a next group's infinity would not be zero).  Zeros
+// written over the TMA's own last step instead held up every tile by 0.8 us.
 //
-// Warps: 0 TMA, 1 MMA (of the leader CTA), 2 (k_wgrad) zeros after a group's last row,
+// Warps: 0 TMA, 1 MMA (of the leader CTA), 2 and 3 (k_wgrad) a group's last rows,
 // 4-11 epilogue.  All waits are bounded.
 #include <algorithm>
 
@@ -42,12 +44,16 @@ constexpr int NACC = 2;
 constexpr int HALF_BYTES = 128 * TK * 2;        // one CTA's 128 rows of an operand per stage
 constexpr int MAX_STAGES = 10;
 constexpr int SMEM_WORK = 14 * HALF_BYTES;      // stages, then the epilogue's boxes
-constexpr int OFF_BAR = SMEM_WORK;              // full[S], empty[S], tail[S], tfull[A], tempty[A], xfull[4], xempty[4], drain
-constexpr int NBAR = 3 * MAX_STAGES + 2 * NACC + 9;
+constexpr int OFF_BAR = SMEM_WORK;              // full[S], empty[S], tfull[A], tempty[A], xfull[4], xempty[4], drain
+constexpr int NBAR = 2 * MAX_STAGES + 2 * NACC + 9;
 constexpr int OFF_MISC = OFF_BAR + 8 * NBAR;
 constexpr int SMEM_BYTES = OFF_MISC + 16 + 1024;
 static_assert(SMEM_BYTES <= 232448, "shared memory budget");
 constexpr int MAX_GROUPS = 65536;
+// k_wgrad: a box of 32 rows of 64 bytes per epilogue warp, and before them two
+// buffers of a group's last rows, 16 rows of 256 columns each
+constexpr int W_BOX = 2048, LAST_BYTES = 8192;
+constexpr int OFF_LAST = SMEM_WORK - EPI_WARPS * W_BOX - 2 * LAST_BYTES;
 
 struct Params {
     const int32_t* offsets;      // [G + 1]
@@ -62,6 +68,8 @@ struct Params {
     int64_t max_tiles;
     int stages, stage_bytes;
     int up;                      // GLU: column of W where the up half begins
+    const __nv_bfloat16 *x, *dy; // k_wgrad: the operands, for the last rows
+    int64_t ldx, lddy;
     void* y;
     int64_t ldy, gsy;
     __nv_bfloat16* a;            // GLU: [gate | up] or NULL
@@ -145,16 +153,16 @@ struct Place {
     __device__ __forceinline__ uint32_t bar(int i) const { return bar0 + 8u * i; }
     __device__ __forceinline__ uint32_t full(int s) const { return bar(s); }
     __device__ __forceinline__ uint32_t empty(int s) const { return bar(MAX_STAGES + s); }
-    __device__ __forceinline__ uint32_t tail(int s) const { return bar(2 * MAX_STAGES + s); }
-    __device__ __forceinline__ uint32_t tfull(int a) const { return bar(3 * MAX_STAGES + a); }
-    __device__ __forceinline__ uint32_t tempty(int a) const { return bar(3 * MAX_STAGES + NACC + a); }
-    __device__ __forceinline__ uint32_t xfull(int i) const { return bar(3 * MAX_STAGES + 2 * NACC + i); }
-    __device__ __forceinline__ uint32_t xempty(int i) const { return bar(3 * MAX_STAGES + 2 * NACC + 4 + i); }
-    __device__ __forceinline__ uint32_t drain() const { return bar(3 * MAX_STAGES + 2 * NACC + 8); }
+    __device__ __forceinline__ uint32_t tfull(int a) const { return bar(2 * MAX_STAGES + a); }
+    __device__ __forceinline__ uint32_t tempty(int a) const { return bar(2 * MAX_STAGES + NACC + a); }
+    // k_rows: from a gate warp to its up warp and back; k_wgrad: a group's last rows
+    __device__ __forceinline__ uint32_t xfull(int i) const { return bar(2 * MAX_STAGES + 2 * NACC + i); }
+    __device__ __forceinline__ uint32_t xempty(int i) const { return bar(2 * MAX_STAGES + 2 * NACC + 4 + i); }
+    __device__ __forceinline__ uint32_t drain() const { return bar(2 * MAX_STAGES + 2 * NACC + 8); }
 };
 
 // Barriers, TMEM; returns its base to every warp.
-__device__ __forceinline__ uint32_t set_up(Place& pl, int stages, int full_arrivals) {
+__device__ __forceinline__ uint32_t set_up(Place& pl, int stages, int x_arrivals) {
     extern __shared__ uint8_t smem_raw[];
     pl.smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
     pl.warp = __shfl_sync(0xFFFFFFFFu, (int)(threadIdx.x >> 5), 0), pl.lane = threadIdx.x & 31;
@@ -165,15 +173,14 @@ __device__ __forceinline__ uint32_t set_up(Place& pl, int stages, int full_arriv
     pl.abort_flag = reinterpret_cast<volatile int*>(pl.smem + OFF_MISC + 4);
     if (threadIdx.x == 0) {
         for (int s = 0; s < stages; ++s) {
-            mbar_init(pl.full(s), full_arrivals);
+            mbar_init(pl.full(s), 1);
             mbar_init(pl.empty(s), 1);
-            mbar_init(pl.tail(s), 1);
         }
         for (int a = 0; a < NACC; ++a) {
             mbar_init(pl.tfull(a), 1);
             mbar_init(pl.tempty(a), 2 * EPI_WARPS);
         }
-        for (int i = 0; i < 4; ++i) mbar_init(pl.xfull(i), 1), mbar_init(pl.xempty(i), 1);
+        for (int i = 0; i < 4; ++i) mbar_init(pl.xfull(i), x_arrivals), mbar_init(pl.xempty(i), 1);
         mbar_init(pl.drain(), 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         *pl.abort_flag = 0;
@@ -322,7 +329,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             const uint32_t bytes = 2u * (HALF_BYTES + x_rows * TK * 2);
             const int col = ti.ct * TILE_COLS + (GLU ? 64 : 128) * (int)pl.rank, row = ti.row0 + half * (int)pl.rank;
             for (int ks = 0; ks < p.nk; ++ks) {
-                if (!__all_sync(0xFFFFFFFFu, mbar_wait_cluster(pl.empty(ring.at), ring.phase ^ 1u, p, pl.abort_flag))) {
+                if (!mbar_wait_cluster(pl.empty(ring.at), ring.phase ^ 1u, p, pl.abort_flag)) {
                     ring.aborted = true;
                     break;
                 }
@@ -341,6 +348,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 }
                 ring.next(p.stages);
             }
+            ring.aborted = __any_sync(0xFFFFFFFFu, ring.aborted);      // the warp goes on as one
         }
         __syncwarp();
         if (ring.aborted && pl.rank == 0) {      // the copies in flight
@@ -364,7 +372,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             tc_fence_after();
             const uint32_t d_tmem = tmem_base + (uint32_t)(acc.at * ACC_COLS);
             for (int ks = 0; ks < p.nk; ++ks) {
-                if (!__all_sync(0xFFFFFFFFu, mbar_wait(pl.full(ring.at), ring.phase, p, pl.abort_flag))) {
+                if (!mbar_wait(pl.full(ring.at), ring.phase, p, pl.abort_flag)) {
                     ring.aborted = true;
                     break;
                 }
@@ -379,6 +387,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 }
                 ring.next(p.stages);
             }
+            ring.aborted = __any_sync(0xFFFFFFFFu, ring.aborted);
             if (ring.aborted) break;
             if (elected) tc_commit_pair(pl.tfull(acc.at), 0);
             acc.next(NACC);
@@ -499,7 +508,6 @@ template <bool F32>
 struct WOut {
     uint32_t buf;
     int lane;
-    uint32_t at;
     __device__ __forceinline__ void put(const Params& p, const CUtensorMap* map, int g, int row0, int col,
                                         const float* v) {
         const int cols = p.N - col;
@@ -516,34 +524,31 @@ struct WOut {
             }
             return;
         }
-        const uint32_t b = F32 ? buf : buf + at;
-        at ^= 2048u;
-        if (lane == 0) {
-            if (F32) bulk_wait_group_read0();
-            else bulk_wait_group_read1();
-        }
-        __syncwarp();
-        if constexpr (F32) {
-            const uint32_t row = b + 128u * lane, sw = (uint32_t)lane & 7u;
 #pragma unroll
-            for (int c = 0; c < 8; ++c)
-                st_shared_v4(row + (((uint32_t)c ^ sw) << 4), __float_as_uint(v[4 * c]), __float_as_uint(v[4 * c + 1]),
-                             __float_as_uint(v[4 * c + 2]), __float_as_uint(v[4 * c + 3]));
-        } else {
-            const uint32_t row = b + 64u * lane, sw = (uint32_t)(lane >> 1) & 3u;
+        for (int h = 0; h < (F32 ? 2 : 1); ++h) {
+            if (F32 && 16 * h >= cols) break;
+            if (lane == 0) bulk_wait_group_read0();
+            __syncwarp();
+            const uint32_t row = buf + 64u * lane, sw = (uint32_t)(lane >> 1) & 3u;
 #pragma unroll
-            for (int c = 0; c < 4; ++c)
-                st_shared_v4(row + (((uint32_t)c ^ sw) << 4), pack_bf16x2(v[8 * c], v[8 * c + 1]),
-                             pack_bf16x2(v[8 * c + 2], v[8 * c + 3]), pack_bf16x2(v[8 * c + 4], v[8 * c + 5]),
-                             pack_bf16x2(v[8 * c + 6], v[8 * c + 7]));
-        }
-        fence_proxy_async_shared();
-        __syncwarp();
-        if (lane == 0) {
-            asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(map),
-                         "r"(b), "r"(col), "r"(row0), "r"(g)
-                         : "memory");
-            bulk_commit_group();
+            for (int c = 0; c < 4; ++c) {
+                const float* u = F32 ? v + 16 * h + 4 * c : v + 8 * c;
+                const uint32_t at = row + (((uint32_t)c ^ sw) << 4);
+                if constexpr (F32)
+                    st_shared_v4(at, __float_as_uint(u[0]), __float_as_uint(u[1]), __float_as_uint(u[2]),
+                                 __float_as_uint(u[3]));
+                else
+                    st_shared_v4(at, pack_bf16x2(u[0], u[1]), pack_bf16x2(u[2], u[3]), pack_bf16x2(u[4], u[5]),
+                                 pack_bf16x2(u[6], u[7]));
+            }
+            fence_proxy_async_shared();
+            __syncwarp();
+            if (lane == 0) {
+                asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(map),
+                             "r"(buf), "r"(col + 16 * h), "r"(row0), "r"(g)
+                             : "memory");
+                bulk_commit_group();
+            }
         }
     }
 };
@@ -558,9 +563,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         prefetch_map(&tmD);
     }
     Place pl;
-    // two arrivals on a full barrier: the leader's producer makes both, or, of a
-    // step with rows to set to zero, warp 2 of either CTA one
-    const uint32_t tmem_base = set_up(pl, p.stages, 2);
+    const uint32_t tmem_base = set_up(pl, p.stages, 4);      // warps 2 and 3 of both CTAs
     wait_for_previous_kernels();
     const int warp = pl.warp, lane = pl.lane;
     const int bh = p.bn / 2, boxes = (bh + 63) / 64;      // of dy's columns, per CTA
@@ -574,22 +577,16 @@ __global__ void __launch_bounds__(THREADS, 1)
         const uint32_t lead_full = mapa(pl.full(0), 0);
         for (; t < p.max_tiles && !ring.aborted; t += pl.step) {
             const WTile w = w_tile(p, t);
-            const int nk = (w.rows + TK - 1) / TK;
+            const int nk = (w.rows / 16 + 3) / 4;      // steps of 64 rows, the last of fewer 16-row ones
             const int am = w.mt * TM + 128 * (int)pl.rank, bn = w.nt * p.bn + bh * (int)pl.rank;
             for (int ks = 0; ks < nk; ++ks) {
-                if (!__all_sync(0xFFFFFFFFu, mbar_wait_cluster(pl.empty(ring.at), ring.phase ^ 1u, p, pl.abort_flag))) {
+                if (!mbar_wait_cluster(pl.empty(ring.at), ring.phase ^ 1u, p, pl.abort_flag)) {
                     ring.aborted = true;
                     break;
                 }
-                const bool ragged = ks + 1 == nk && (w.rows & 15) != 0;
-                const uint32_t fb = ragged ? mapa(pl.tail(ring.at), pl.rank) : lead_full + 8u * ring.at;
+                const uint32_t fb = lead_full + 8u * ring.at;
                 if (elected) {
-                    if (ragged) {
-                        mbar_expect_tx(pl.tail(ring.at), bytes);
-                    } else if (pl.rank == 0) {
-                        mbar_expect_tx(pl.full(ring.at), 2u * bytes);
-                        mbar_arrive(pl.full(ring.at));
-                    }
+                    if (pl.rank == 0) mbar_expect_tx(pl.full(ring.at), 2u * bytes);
                     const uint32_t sa = smem_u32(pl.smem + ring.at * p.stage_bytes), sb = sa + HALF_BYTES;
                     const int row = w.start + ks * TK;
                     tma2_load_2d(sa, &tmX, am, row, fb);
@@ -601,36 +598,58 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
         }
         __syncwarp();
-        if (ring.aborted) {      // the copies in flight
+        if (ring.aborted && pl.rank == 0) {      // the copies in flight
             const Params q = patient(p);
             volatile int no_abort = 0;
             for (int i = ring.count - min(ring.count, p.stages); i < ring.count; ++i)
                 mbar_wait_cluster(pl.full(i % p.stages), (uint32_t)(i / p.stages) & 1u, q, &no_abort);
         }
-    } else if (warp == 2) {
-        // ------------------------------- zeros behind a group's last row ----
-        const uint32_t lead_full = mapa(pl.full(0), 0);
-        uint32_t phases = 0;      // of the tail barriers
+    } else if (warp == 2 || warp == 3) {
+        // ------------------- a group's last rows, fewer than 16, two buffers ----
+        // laid out as the TMA does: boxes of 64 columns, rows of 128 bytes, their
+        // 16-byte units swizzled by the row
+        const uint32_t lead = mapa(pl.xfull(0), 0);
+        Ring last;
         for (; t < p.max_tiles; t += pl.step) {
             const WTile w = w_tile(p, t);
-            const int nk = (w.rows + TK - 1) / TK, rest = w.rows & 15;
-            if (nk == 0) continue;
-            ring.at = (ring.at + nk) % p.stages;
-            if (rest == 0) continue;
-            const int s = ring.at == 0 ? p.stages - 1 : ring.at - 1;
-            if (!__all_sync(0xFFFFFFFFu, mbar_wait_cluster(pl.tail(s), phases >> s & 1u, p, pl.abort_flag))) break;
-            phases ^= 1u << s;
-            const int r0 = w.rows & (TK - 1), n = (16 - rest) * 8;      // 16-byte units of a box's rows r0 ..
-            const uint32_t at = smem_u32(pl.smem + s * p.stage_bytes) + 128u * r0;
-            for (int b = 0; b < 2 + boxes; ++b)
-                for (int i = lane; i < n; i += 32) st_shared_v4(at + b * (HALF_BYTES / 2) + 16u * i, 0u, 0u, 0u, 0u);
+            const int n = w.rows & 15;
+            if (n == 0) continue;
+            if (!__all_sync(0xFFFFFFFFu, mbar_wait_cluster(pl.xempty(last.at), last.phase ^ 1u, p, pl.abort_flag))) break;
+            const uint32_t buf = smem_u32(pl.smem + OFF_LAST + last.at * LAST_BYTES);
+            const int64_t row0 = (int64_t)w.start + w.rows - n;
+            const int am = w.mt * TM + 128 * (int)pl.rank, bn = w.nt * p.bn + bh * (int)pl.rank;
+            const int lane2 = (int)threadIdx.x - 64, unit = lane2 & 7;
+            // two boxes of x, then dy's: 8 units of 16 rows each
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+                if (b >= 2 + boxes) break;
+                const bool is_x = b < 2;
+                const int col = (is_x ? am + 64 * b : bn + 64 * (b - 2)) + 8 * unit;
+                const int cols = min((is_x ? p.K : p.N) - col, 8);
+                uint4 v[2];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int r = (lane2 >> 3) + 8 * i;
+                    v[i] = make_uint4(0u, 0u, 0u, 0u);
+                    if (r < n && cols > 0)
+                        v[i] = load_vec8(is_x ? p.x + (row0 + r) * p.ldx + col : p.dy + (row0 + r) * p.lddy + col, cols);
+                }
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int r = (lane2 >> 3) + 8 * i;
+                    st_shared_v4(buf + 2048u * b + 128u * r + (((uint32_t)unit ^ (r & 7u)) << 4), v[i].x, v[i].y, v[i].z,
+                                 v[i].w);
+                }
+            }
             fence_proxy_async_shared();
             __syncwarp();
-            if (lane == 0) mbar_arrive_remote(lead_full + 8u * s);
+            if (lane == 0) mbar_arrive_remote(lead + 8u * last.at);
+            last.next(2);
         }
     } else if (warp == 1 && pl.rank == 0) {
         // --------------------------------------------------- products ----
         const bool elected = elect_one();
+        Ring last;
         const uint32_t idesc = make_idesc_pair<true, true>(p.bn);
         const uint64_t adesc0 = operand_desc<true>(smem_u32(pl.smem));
         const uint64_t bdesc0 = operand_desc<true>(smem_u32(pl.smem) + HALF_BYTES);
@@ -638,31 +657,46 @@ __global__ void __launch_bounds__(THREADS, 1)
         for (; t < p.max_tiles && !ring.aborted; t += pl.step) {
             const WTile w = w_tile(p, t);
             if (w.rows == 0) continue;
-            const int nk = (w.rows + TK - 1) / TK;
+            const int steps = w.rows / 16, nk = (steps + 3) / 4;
             if (!__all_sync(0xFFFFFFFFu, mbar_wait_cluster(pl.tempty(acc.at), acc.phase ^ 1u, p, pl.abort_flag))) {
                 ring.aborted = true;
                 break;
             }
             tc_fence_after();
             const uint32_t d_tmem = tmem_base + (uint32_t)(acc.at * ACC_COLS);
+            // (the loop has to be short: a step's four products take 512 cycles)
             for (int ks = 0; ks < nk; ++ks) {
-                if (!__all_sync(0xFFFFFFFFu, mbar_wait_cluster(pl.full(ring.at), ring.phase, p, pl.abort_flag))) {
+                if (!mbar_wait(pl.full(ring.at), ring.phase, p, pl.abort_flag)) {
                     ring.aborted = true;
                     break;
                 }
                 tc_fence_after();
                 if (elected) {
                     const uint64_t adesc = adesc0 + ring.at * stage_step, bdesc = bdesc0 + ring.at * stage_step;
-                    const int left = (w.rows - ks * TK + 15) / 16;      // 16-row steps
 #pragma unroll
                     for (int kk = 0; kk < TK / 16; ++kk)
-                        if (kk < left)
+                        if (4 * ks + kk < steps)
                             tc_mma2_bf16(d_tmem, adesc + k16_step<true>() * kk, bdesc + k16_step<true>() * kk, idesc,
                                          (ks != 0 || kk != 0) ? 1u : 0u);
                     tc_commit_pair(pl.empty(ring.at), 0);
                 }
                 ring.next(p.stages);
             }
+            if ((w.rows & 15) != 0 && !ring.aborted) {      // both CTAs have filled the last step
+                if (mbar_wait_cluster(pl.xfull(last.at), last.phase, p, pl.abort_flag)) {
+                    tc_fence_after();
+                    if (elected) {
+                        const uint32_t buf = smem_u32(pl.smem + OFF_LAST + last.at * LAST_BYTES);
+                        tc_mma2_bf16(d_tmem, desc_mn_sw128(buf, 2048), desc_mn_sw128(buf + 4096, 2048), idesc,
+                                     steps > 0 ? 1u : 0u);
+                        tc_commit_pair(pl.xempty(last.at), 0);
+                    }
+                    last.next(2);
+                } else {
+                    ring.aborted = true;
+                }
+            }
+            ring.aborted = __any_sync(0xFFFFFFFFu, ring.aborted);      // the warp goes on as one
             if (ring.aborted) break;
             if (elected) tc_commit_pair(pl.tfull(acc.at), 0);
             acc.next(NACC);
@@ -672,7 +706,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         // --------------------------------------------------- epilogue ----
         const int ew = warp - 4, quarter = ew & 3, half = ew >> 2;
         const uint32_t lane_base = tmem_base + ((uint32_t)(quarter * 32) << 16);
-        WOut<F32> out{smem_u32(pl.smem + SMEM_WORK - (EPI_WARPS - ew) * 4096), lane, 0u};
+        WOut<F32> out{smem_u32(pl.smem + SMEM_WORK - (EPI_WARPS - ew) * W_BOX), lane};
         const int chunks = p.bn / 32, c0 = half == 0 ? 0 : (chunks + 1) / 2, c1 = half == 0 ? (chunks + 1) / 2 : chunks;
         for (; t < p.max_tiles; t += pl.step) {
             const WTile w = w_tile(p, t);
@@ -857,8 +891,10 @@ static moe_status_t product_wgrad(const Mat& x, const Mat& dy, Params p, bool f3
     p.max_tiles = (int64_t)p.G * p.m_tiles * p.col_tiles;
     MOE_REQUIRE(p.max_tiles <= kMaxTiles, MOE_ERR_UNSUPPORTED);
     p.stage_bytes = HALF_BYTES + (p.bn / 2 + 63) / 64 * (HALF_BYTES / 2);
-    p.stages = std::min(MAX_STAGES, (SMEM_WORK - EPI_WARPS * 4096) / p.stage_bytes);
+    p.stages = std::min(MAX_STAGES, OFF_LAST / p.stage_bytes);
     p.timeout_ns = 2000000000ull;
+    p.x = static_cast<const __nv_bfloat16*>(x.p), p.ldx = x.ld;
+    p.dy = static_cast<const __nv_bfloat16*>(dy.p), p.lddy = dy.ld;
     CUtensorMap tmX, tmDY, tmD;
     MOE_REQUIRE(make_bf16_map(&tmX, x.p, x.rows, x.cols, x.ld, TK) &&
                     make_bf16_map(&tmDY, dy.p, dy.rows, dy.cols, dy.ld, TK) &&
