@@ -12,23 +12,34 @@ forward_, backward_ and (once the weights have been set) update_ allocate
 nothing and never synchronise, so they can be captured in a CUDA graph, in
 one or apart: an update writes every weight and operand in place.
 
-``python -m grouped_gemm_top_gb300.block`` trains one on synthetic data."""
+``python -m grouped_gemm_top_gb300.block`` trains one on synthetic data;
+``--experts bf16`` with its experts in 16 bits, ``--distill`` under a head that
+learns from a teacher's top logits."""
 from __future__ import annotations
+
+import argparse
 
 import torch
 
 from . import ops, synth
+from .head import DistillHead
 from .layer import MoELayer
+from .layer_bf16 import MoELayerBF16
 from .optim import AdamW
 
 
 class TrainBlock:
-    def __init__(self, T, d, E, k, f_moe, f, act="silu", eps=1e-6, score="softmax", normalize=True, device="cuda:0"):
+    def __init__(self, T, d, E, k, f_moe, f, act="silu", eps=1e-6, score="softmax", normalize=True, device="cuda:0",
+                 experts="mxfp8"):
         """T tokens of width d; an MoE sublayer of E experts of width f_moe,
-        top-k, with its router; a dense gated sublayer of width f (f % 8 == 0)."""
+        top-k, with its router, whose products are in MXFP8 or (experts="bf16")
+        in bf16; a dense gated sublayer of width f (f % 8 == 0)."""
         self.T, self.d, self.f, self.act, self.eps = T, d, f, act, eps
         self.device = torch.device(device)
-        self.moe = MoELayer(T, d, E, k, f_moe, score, normalize, device=device, router=True)
+        if experts not in ("mxfp8", "bf16"):
+            raise ValueError('experts: "mxfp8" or "bf16"')
+        layer = MoELayer if experts == "mxfp8" else MoELayerBF16
+        self.moe = layer(T, d, E, k, f_moe, score, normalize, device=device, router=True)
 
         def z(shape, dtype=torch.bfloat16):
             return torch.zeros(shape, dtype=dtype, device=self.device)
@@ -38,7 +49,7 @@ class TrainBlock:
         self.W1, self.W2 = z((d, 2 * f)), z((f, d))
         self.dW1, self.dW2 = z((d, 2 * f)), z((f, d))
         self.dw_norm1, self.dw_norm2 = z((d,), torch.float32), z((d,), torch.float32)
-        # the MoE sublayer's bf16 weights (it quantizes its operands from them)
+        # the MoE sublayer's bf16 weights (MXFP8: it quantizes its operands from them)
         self.We1, self.We2 = z((E, d, 2 * f_moe)), z((E, f_moe, d))
         self.Wr = z((d, E))
         # the stream in and out, and what the backward pass needs
@@ -57,16 +68,17 @@ class TrainBlock:
         self.set_weights()
 
     def set_weights(self):
-        """The MoE sublayer's MXFP8 operands, from its bf16 weights."""
+        """The MoE sublayer's operands (MXFP8: quantized) from its bf16 weights."""
         self.moe.set_weights(self.We1, self.We2)
         self.moe.set_router_weights(self.Wr)
 
-    def make_optimizer(self, lr, weight_decay=0.1, state_bits=32, **kw):
-        """AdamW over every weight (no decay on the norms' and the router's)."""
+    def make_optimizer(self, lr, weight_decay=0.1, state_bits=32, others=(), **kw):
+        """AdamW over every weight (no decay on the norms' and the router's)
+        and `others`, (parameter, gradient, decay) of what is trained with it."""
         m = self.moe
         self.optimizer = AdamW([(self.W1, self.dW1), (self.W2, self.dW2), (self.We1, m.dW1), (self.We2, m.dW2),
                                 (self.Wr, m.dWr, 0.0), (self.w_norm1, self.dw_norm1, 0.0),
-                                (self.w_norm2, self.dw_norm2, 0.0)],
+                                (self.w_norm2, self.dw_norm2, 0.0), *others],
                                lr, weight_decay=weight_decay, state_bits=state_bits, **kw)
         return self.optimizer
 
@@ -99,22 +111,44 @@ class TrainBlock:
         self.set_weights()
 
 
-def main():
-    T, d, E, k, f_moe, f = 1024, 512, 8, 2, 256, 1024
-    b = TrainBlock(T, d, E, k, f_moe, f)
+def main(argv=None):
+    ap = argparse.ArgumentParser(prog="python -m grouped_gemm_top_gb300.block", description="Trains a small block on synthetic data.")
+    ap.add_argument("--experts", choices=("mxfp8", "bf16"), default="mxfp8", help="the experts' products")
+    ap.add_argument("--distill", action="store_true", help="learn from a teacher's top logits instead of a target")
+    ap.add_argument("--steps", type=int, default=40)
+    args = ap.parse_args(argv)
+    T, d, E, k, f_moe, f, V, top = 1024, 512, 8, 2, 256, 1024, 4000, 16
+    b = TrainBlock(T, d, E, k, f_moe, f, experts=args.experts)
     b.init_weights()
-    b.make_optimizer(lr=2e-3, state_bits=8)
     b.s.copy_(synth.make_normal_bf16((T, d), 100, b.device))
-    target = synth.make_normal_bf16((T, d), 101, b.device).float()
-    for step in range(1, 41):
+    if args.distill:
+        head = DistillHead(T, d, V, top, temperature=2.0)
+        head.init_weights(200)
+        g = torch.Generator(device=b.device).manual_seed(201)
+        head.idx.copy_(torch.randint(V, (T, 1), generator=g, device=b.device) + 7 * torch.arange(top, device=b.device))
+        head.idx.remainder_(V)
+        head.teacher.copy_(4 * torch.randn((T, top), generator=g, device=b.device))
+        b.make_optimizer(lr=2e-3, state_bits=8, others=head.parameters())
+    else:
+        b.make_optimizer(lr=2e-3, state_bits=8)
+        target = synth.make_normal_bf16((T, d), 101, b.device).float()
+    for step in range(1, args.steps + 1):
         b.forward_()
-        err = b.out.float() - target
-        b.dout.copy_(err / T)      # of the loss sum |out - target|^2 / 2T
+        if args.distill:
+            head.s.copy_(b.out)
+            head.forward_backward_()
+            b.dout.copy_(head.ds)
+        else:
+            err = b.out.float() - target
+            b.dout.copy_(err / T)      # of the loss sum |out - target|^2 / 2T
         b.backward_()
         b.update_()
         if step == 1 or step % 10 == 0:
-            print(f"step {step}: loss {0.5 * float(err.square().sum()) / T:.4f}")
+            loss = float(head.loss.mean()) if args.distill else 0.5 * float(err.square().sum()) / T
+            print(f"step {step}: loss {loss:.4f}")
     b.moe.check_err()
+    if args.distill:
+        head.check_err()
 
 
 if __name__ == "__main__":
