@@ -104,18 +104,15 @@ struct Tile {
 struct Cursor {
     int base = -32;                 // of the 32 groups
     int64_t first = 0, end = 0;     // this lane's group's first tile; the tiles up to the last lane's
-    int start, rows, per, tiles;    // of this lane's group; rows of its tiles; how many there are
+    int start, rows, parts, tiles;  // of this lane's group; tiles down its rows, and in all
     __device__ __forceinline__ bool find(const Params& p, int64_t t, int lane, Tile& out) {
         while (t >= end) {
             base += 32;
             if (base >= p.G) return false;
             const Span s = span_of(p, base + lane);
-            start = s.start, rows = s.rows, per = 32, tiles = 0;
-            if (rows > 0) {
-                const int n = (rows + p.n_max - 1) / p.n_max;
-                per = ((rows + n - 1) / n + 31) / 32 * 32;      // evenly
-                tiles = (rows + per - 1) / per * p.col_tiles;
-            }
+            start = s.start, rows = s.rows;
+            parts = (rows + p.n_max - 1) / p.n_max;
+            tiles = parts * p.col_tiles;
             int64_t sum = tiles;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -130,16 +127,18 @@ struct Cursor {
         if (here == 0) return false;
         const int src = __ffs(here) - 1;
         const int i = (int)(t - __shfl_sync(0xFFFFFFFFu, first, src));
-        const int n_rows = __shfl_sync(0xFFFFFFFFu, rows, src), n_per = __shfl_sync(0xFFFFFFFFu, per, src);
+        const int n_rows = __shfl_sync(0xFFFFFFFFu, rows, src), n = __shfl_sync(0xFFFFFFFFu, parts, src);
         // bands of 8 row tiles, consecutive tiles down a band: those under way share
         // W's columns and x's rows in L2
-        const int row_tiles = (n_rows + n_per - 1) / n_per, band = 8 * p.col_tiles;
-        const int b = i / band, rem = i - b * band, width = min(8, row_tiles - 8 * b);
+        const int band = 8 * p.col_tiles, b = i / band, rem = i - b * band, width = min(8, n - 8 * b);
         out.g = base + src;
         out.ct = rem / width;
-        const int r = (8 * b + rem - out.ct * width) * n_per;
-        out.row0 = __shfl_sync(0xFFFFFFFFu, start, src) + r;
-        out.rows = min(n_per, n_rows - r);
+        // the group's rows, 32 by 32, evenly over its tiles (all but the last full, the
+        // pairs whose turn is always the last one would have less to do)
+        const int r = 8 * b + rem - out.ct * width, units = (n_rows + 31) / 32, each = units / n, more = units - each * n;
+        const int first_row = 32 * (r * each + min(r, more));
+        out.row0 = __shfl_sync(0xFFFFFFFFu, start, src) + first_row;
+        out.rows = min(32 * (each + (r < more)), n_rows - first_row);
         return true;
     }
 };
@@ -241,6 +240,7 @@ __device__ __forceinline__ void tmem_ld_16x32(uint32_t taddr, uint32_t* r) {
 // rows (TMEM columns), in bf16 and turned round, as a box of 32 rows of 64 bytes
 // (64-byte swizzle).  A TMA store writes it; where the group ends inside the
 // box, or a width that is no multiple of 8 does, the rows are copied out.
+template <int BOXES>
 struct Out {
     uint32_t buf;
     int lane;
@@ -249,8 +249,11 @@ struct Out {
     __device__ __forceinline__ void put(const CUtensorMap* map, __nv_bfloat16* d, int64_t ld, int col, int cols,
                                         int64_t row, int rows, const float* v) {
         const uint32_t b = buf + at;
-        at ^= 2048u;
-        if (lane == 0) bulk_wait_group_read1();      // the box before the last one has been read
+        if (BOXES == 2) at ^= 2048u;
+        if (lane == 0) {      // this box has been read
+            if (BOXES == 2) bulk_wait_group_read1();
+            else bulk_wait_group_read0();
+        }
         __syncwarp();
         // one store for 8 rows: its four 8 x 8 matrices are 8 columns each
         const uint32_t r = (uint32_t)lane & 7u, c = (uint32_t)lane >> 3;
@@ -294,16 +297,196 @@ struct Out {
     }
 };
 
-// W_MN: the forward product (D's columns are contiguous in W).  GLU: the
-// tile's 128 columns per CTA are 64 of gate and the same 64 of up.
+// The tiles of D = x op(W), from the pair's next one, t, on; t is behind the last
+// one afterwards.  W_MN: the forward product (D's columns are contiguous in W).
+// GLU: the tile's 128 columns per CTA are 64 of gate and the same 64 of up.
+template <bool W_MN, bool GLU>
+__device__ __forceinline__ void load_rows(const Place& pl, const Params& p, const CUtensorMap* tmW,
+                                          const CUtensorMap* tmX16, const CUtensorMap* tmX32, const CUtensorMap* tmX64,
+                                          const CUtensorMap* tmX128, Cursor& cur, int64_t& t, Ring& ring) {
+    constexpr int TILE_COLS = GLU ? 128 : 256;        // of D, per pair
+    Tile ti;
+    const bool elected = elect_one();
+    const uint32_t lead_full = mapa(pl.full(0), 0);
+    for (; !ring.aborted && cur.find(p, t, pl.lane, ti); t += pl.step) {
+        const int half = (ti.rows + 31) / 32 * 16;     // rows of this CTA
+        const CUtensorMap* tmX = half <= 16 ? tmX16 : (half <= 32 ? tmX32 : (half <= 64 ? tmX64 : tmX128));
+        const uint32_t x_rows = half <= 16 ? 16 : (half <= 32 ? 32 : (half <= 64 ? 64 : 128));
+        const uint32_t bytes = 2u * (HALF_BYTES + x_rows * TK * 2);
+        const int col = ti.ct * TILE_COLS + (GLU ? 64 : 128) * (int)pl.rank, row = ti.row0 + half * (int)pl.rank;
+        for (int ks = 0; ks < p.nk; ++ks) {
+            if (!mbar_wait_cluster(pl.empty(ring.at), ring.phase ^ 1u, p, pl.abort_flag)) {
+                ring.aborted = true;
+                break;
+            }
+            // both CTAs' bytes complete on the leader's full barrier
+            const uint32_t fb = lead_full + 8u * ring.at;
+            if (elected) {
+                if (pl.rank == 0) mbar_expect_tx(pl.full(ring.at), bytes);
+                const uint32_t sw = smem_u32(pl.smem + ring.at * p.stage_bytes);
+                if constexpr (W_MN) {
+                    tma2_load_3d(sw, tmW, col, ks * TK, ti.g, fb);
+                    tma2_load_3d(sw + HALF_BYTES / 2, tmW, GLU ? col + p.up : col + 64, ks * TK, ti.g, fb);
+                } else {
+                    tma2_load_3d(sw, tmW, ks * TK, col, ti.g, fb);
+                }
+                tma2_load_2d(sw + HALF_BYTES, tmX, ks * TK, row, fb);
+            }
+            ring.next(p.stages);
+        }
+        ring.aborted = __any_sync(0xFFFFFFFFu, ring.aborted);      // the warp goes on as one
+    }
+}
+template <bool W_MN>
+__device__ __forceinline__ void multiply_rows(const Place& pl, const Params& p, uint32_t tmem_base, Cursor& cur,
+                                              int64_t& t, Ring& ring, Ring& acc) {
+    Tile ti;
+    const bool elected = elect_one();
+    const uint64_t adesc0 = operand_desc<W_MN>(smem_u32(pl.smem));
+    const uint64_t bdesc0 = operand_desc<false>(smem_u32(pl.smem) + HALF_BYTES);
+    const uint32_t stage_step = (uint32_t)p.stage_bytes >> 4;
+    for (; !ring.aborted && cur.find(p, t, pl.lane, ti); t += pl.step) {
+        const uint32_t idesc = make_idesc_pair<W_MN, false>((ti.rows + 31) / 32 * 32);
+        if (!__all_sync(0xFFFFFFFFu, mbar_wait_cluster(pl.tempty(acc.at), acc.phase ^ 1u, p, pl.abort_flag))) {
+            ring.aborted = true;
+            break;
+        }
+        tc_fence_after();
+        const uint32_t d_tmem = tmem_base + (uint32_t)(acc.at * ACC_COLS);
+        for (int ks = 0; ks < p.nk; ++ks) {
+            if (!mbar_wait(pl.full(ring.at), ring.phase, p, pl.abort_flag)) {
+                ring.aborted = true;
+                break;
+            }
+            tc_fence_after();
+            if (elected) {
+                const uint64_t adesc = adesc0 + ring.at * stage_step, bdesc = bdesc0 + ring.at * stage_step;
+#pragma unroll
+                for (int kk = 0; kk < TK / 16; ++kk)
+                    tc_mma2_bf16(d_tmem, adesc + k16_step<W_MN>() * kk, bdesc + k16_step<false>() * kk, idesc,
+                                 (ks != 0 || kk != 0) ? 1u : 0u);
+                tc_commit_pair(pl.empty(ring.at), 0);
+            }
+            ring.next(p.stages);
+        }
+        ring.aborted = __any_sync(0xFFFFFFFFu, ring.aborted);
+        if (ring.aborted) break;
+        if (elected) tc_commit_pair(pl.tfull(acc.at), 0);
+        acc.next(NACC);
+    }
+}
+// BOXES: 2 KB boxes of a warp on their way out
+template <bool GLU, int ACT, int BOXES>
+__device__ __forceinline__ bool store_rows(const Place& pl, const Params& p, const CUtensorMap* tmY,
+                                           const CUtensorMap* tmA, const CUtensorMap* tmA2, uint32_t tmem_base,
+                                           Cursor& cur, int64_t& t, Ring& acc) {
+    constexpr int EPI_STAGE = 2048 * BOXES + (GLU ? 4096 : 0);      // GLU: gate's way to up
+    Tile ti;
+    const int lane = pl.lane, ew = pl.warp - 4, quarter = ew & 3, half = ew >> 2;
+    const uint32_t lane_base = tmem_base + ((uint32_t)(quarter * 32) << 16);
+    const uint32_t stage = smem_u32(pl.smem + SMEM_WORK - (EPI_WARPS - ew) * EPI_STAGE);
+    Out<BOXES> out{stage, lane, 0u};
+    // GLU: lanes 0..63 hold gate columns, 64..127 the up columns of the same h;
+    // the gate warp hands act(gate) in fp32 to the up warp two quarters on
+    const bool gate = GLU && quarter < 2;
+    const int pair = (quarter & 1) + 2 * half;
+    const uint32_t to_up = smem_u32(pl.smem + SMEM_WORK - (EPI_WARPS - (quarter & 1) - 4 * half) * EPI_STAGE + 4096) +
+                           16u * lane;
+    uint32_t handed = 0;
+    bool ok = true;
+    for (; ok && cur.find(p, t, lane, ti); t += pl.step) {
+        ok = __all_sync(0xFFFFFFFFu, mbar_wait_cluster(pl.tfull(acc.at), acc.phase, p, pl.abort_flag));
+        if (!ok) break;
+        tc_fence_after();
+        const int chunks = (ti.rows + 31) / 32;
+        const int c0 = half == 0 ? 0 : (chunks + 1) / 2, c1 = half == 0 ? (chunks + 1) / 2 : chunks;
+        const uint32_t tacc = lane_base + (uint32_t)(acc.at * ACC_COLS);
+        const int col = GLU ? ti.ct * 128 + 64 * (int)pl.rank + 32 * (quarter & 1)
+                            : ti.ct * 256 + 128 * (int)pl.rank + 32 * quarter;
+        const int cols = p.N - col;
+        for (int c = c0; c < c1 && ok; ++c) {
+            uint32_t r[32];
+            tmem_ld_16x32(tacc + 32 * c, r);
+            tmem_ld_16x32(tacc + (16u << 16) + 32 * c, r + 16);
+            tmem_wait_ld();
+            if (c + 1 == c1) {      // the accumulator is read: the next tile may have it
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_remote(mapa(pl.tempty(acc.at), 0));
+            }
+            float v[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+            const int64_t row = ti.row0 + 32 * c;
+            const int rows = ti.rows - 32 * c;
+            if constexpr (!GLU) {
+                if (cols > 0) out.put(tmY, static_cast<__nv_bfloat16*>(p.y), p.ldy, col, cols, row, rows, v);
+            } else {
+                if (cols <= 0) continue;      // both warps
+                if (p.a != nullptr)
+                    out.put(gate ? tmA : tmA2, p.a + (gate ? 0 : p.N), p.lda, col, cols, row, rows, v);
+                if (gate) {
+                    ok = __all_sync(0xFFFFFFFFu, mbar_wait(pl.xempty(pair), handed & 1u ^ 1u, p, pl.abort_flag));
+                    if (!ok) break;
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) v[i] = act_of(v[i], ACT);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        st_shared_v4(to_up + 512u * i, __float_as_uint(v[4 * i]), __float_as_uint(v[4 * i + 1]),
+                                     __float_as_uint(v[4 * i + 2]), __float_as_uint(v[4 * i + 3]));
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(pl.xfull(pair));
+                } else {
+                    ok = __all_sync(0xFFFFFFFFu, mbar_wait(pl.xfull(pair), handed & 1u, p, pl.abort_flag));
+                    if (!ok) break;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        float g[4];
+                        asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                                     : "=f"(g[0]), "=f"(g[1]), "=f"(g[2]), "=f"(g[3])
+                                     : "r"(to_up + 512u * i)
+                                     : "memory");
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) v[4 * i + j] *= g[j];
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(pl.xempty(pair));
+                    out.put(tmY, static_cast<__nv_bfloat16*>(p.y), p.ldy, col, cols, row, rows, v);
+                }
+                ++handed;
+            }
+        }
+        if (c0 >= c1) {      // nothing of this tile is this warp's
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_remote(mapa(pl.tempty(acc.at), 0));
+        }
+        acc.next(NACC);
+    }
+    return ok;
+}
+// After an abort: wait (bounded) for the copies in flight.  The leader's full
+// barriers count both CTAs' bytes, and the follower leaves only after the
+// closing cluster barrier, i.e. after this.
+__device__ __forceinline__ void loads_end(const Place& pl, const Params& p, const Ring& ring) {
+    __syncwarp();
+    if (!ring.aborted || pl.rank != 0) return;
+    const Params q = patient(p);
+    volatile int no_abort = 0;
+    for (int i = ring.count - min(ring.count, p.stages); i < ring.count; ++i)
+        mbar_wait_cluster(pl.full(i % p.stages), (uint32_t)(i / p.stages) & 1u, q, &no_abort);
+}
+__device__ __forceinline__ void stores_end(int lane) {
+    if (lane == 0) bulk_wait_group0();      // the stores are complete
+    __syncwarp();
+}
+
 template <bool W_MN, bool GLU, int ACT>
 __global__ void __launch_bounds__(THREADS, 1)
     k_rows(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX16,
            const __grid_constant__ CUtensorMap tmX32, const __grid_constant__ CUtensorMap tmX64,
            const __grid_constant__ CUtensorMap tmX128, const __grid_constant__ CUtensorMap tmY,
            const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmA2, const Params p) {
-    constexpr int EPI_STAGE = GLU ? 8192 : 4096;      // GLU: 4 KB more, gate's way to up
-    constexpr int TILE_COLS = GLU ? 128 : 256;        // of D, per pair
     if (threadIdx.x == 64) {
         prefetch_map(&tmW);
         prefetch_map(&tmX128);
@@ -312,172 +495,18 @@ __global__ void __launch_bounds__(THREADS, 1)
     Place pl;
     const uint32_t tmem_base = set_up(pl, p.stages, 1);
     wait_for_previous_kernels();
-    const int warp = pl.warp, lane = pl.lane;
     Cursor cur;
     Ring ring, acc;
-    Tile ti;
     int64_t t = pl.first;
-
-    if (warp == 0) {
-        // ------------------------------------------------------ loads ----
-        const bool elected = elect_one();
-        const uint32_t lead_full = mapa(pl.full(0), 0);
-        for (; !ring.aborted && cur.find(p, t, lane, ti); t += pl.step) {
-            const int half = (ti.rows + 31) / 32 * 16;     // rows of this CTA
-            const CUtensorMap* tmX = half <= 16 ? &tmX16 : (half <= 32 ? &tmX32 : (half <= 64 ? &tmX64 : &tmX128));
-            const uint32_t x_rows = half <= 16 ? 16 : (half <= 32 ? 32 : (half <= 64 ? 64 : 128));
-            const uint32_t bytes = 2u * (HALF_BYTES + x_rows * TK * 2);
-            const int col = ti.ct * TILE_COLS + (GLU ? 64 : 128) * (int)pl.rank, row = ti.row0 + half * (int)pl.rank;
-            for (int ks = 0; ks < p.nk; ++ks) {
-                if (!mbar_wait_cluster(pl.empty(ring.at), ring.phase ^ 1u, p, pl.abort_flag)) {
-                    ring.aborted = true;
-                    break;
-                }
-                // both CTAs' bytes complete on the leader's full barrier
-                const uint32_t fb = lead_full + 8u * ring.at;
-                if (elected) {
-                    if (pl.rank == 0) mbar_expect_tx(pl.full(ring.at), bytes);
-                    const uint32_t sw = smem_u32(pl.smem + ring.at * p.stage_bytes);
-                    if constexpr (W_MN) {
-                        tma2_load_3d(sw, &tmW, col, ks * TK, ti.g, fb);
-                        tma2_load_3d(sw + HALF_BYTES / 2, &tmW, GLU ? col + p.up : col + 64, ks * TK, ti.g, fb);
-                    } else {
-                        tma2_load_3d(sw, &tmW, ks * TK, col, ti.g, fb);
-                    }
-                    tma2_load_2d(sw + HALF_BYTES, tmX, ks * TK, row, fb);
-                }
-                ring.next(p.stages);
-            }
-            ring.aborted = __any_sync(0xFFFFFFFFu, ring.aborted);      // the warp goes on as one
-        }
-        __syncwarp();
-        if (ring.aborted && pl.rank == 0) {      // the copies in flight
-            const Params q = patient(p);
-            volatile int no_abort = 0;
-            for (int i = ring.count - min(ring.count, p.stages); i < ring.count; ++i)
-                mbar_wait_cluster(pl.full(i % p.stages), (uint32_t)(i / p.stages) & 1u, q, &no_abort);
-        }
-    } else if (warp == 1 && pl.rank == 0) {
-        // --------------------------------------------------- products ----
-        const bool elected = elect_one();
-        const uint64_t adesc0 = operand_desc<W_MN>(smem_u32(pl.smem));
-        const uint64_t bdesc0 = operand_desc<false>(smem_u32(pl.smem) + HALF_BYTES);
-        const uint32_t stage_step = (uint32_t)p.stage_bytes >> 4;
-        for (; !ring.aborted && cur.find(p, t, lane, ti); t += pl.step) {
-            const uint32_t idesc = make_idesc_pair<W_MN, false>((ti.rows + 31) / 32 * 32);
-            if (!__all_sync(0xFFFFFFFFu, mbar_wait_cluster(pl.tempty(acc.at), acc.phase ^ 1u, p, pl.abort_flag))) {
-                ring.aborted = true;
-                break;
-            }
-            tc_fence_after();
-            const uint32_t d_tmem = tmem_base + (uint32_t)(acc.at * ACC_COLS);
-            for (int ks = 0; ks < p.nk; ++ks) {
-                if (!mbar_wait(pl.full(ring.at), ring.phase, p, pl.abort_flag)) {
-                    ring.aborted = true;
-                    break;
-                }
-                tc_fence_after();
-                if (elected) {
-                    const uint64_t adesc = adesc0 + ring.at * stage_step, bdesc = bdesc0 + ring.at * stage_step;
-#pragma unroll
-                    for (int kk = 0; kk < TK / 16; ++kk)
-                        tc_mma2_bf16(d_tmem, adesc + k16_step<W_MN>() * kk, bdesc + k16_step<false>() * kk, idesc,
-                                     (ks != 0 || kk != 0) ? 1u : 0u);
-                    tc_commit_pair(pl.empty(ring.at), 0);
-                }
-                ring.next(p.stages);
-            }
-            ring.aborted = __any_sync(0xFFFFFFFFu, ring.aborted);
-            if (ring.aborted) break;
-            if (elected) tc_commit_pair(pl.tfull(acc.at), 0);
-            acc.next(NACC);
-        }
+    if (pl.warp == 0) {
+        load_rows<W_MN, GLU>(pl, p, &tmW, &tmX16, &tmX32, &tmX64, &tmX128, cur, t, ring);
+        loads_end(pl, p, ring);
+    } else if (pl.warp == 1 && pl.rank == 0) {
+        multiply_rows<W_MN>(pl, p, tmem_base, cur, t, ring, acc);
         products_end(pl, p, ring);
-    } else if (warp >= 4) {
-        // --------------------------------------------------- epilogue ----
-        const int ew = warp - 4, quarter = ew & 3, half = ew >> 2;
-        const uint32_t lane_base = tmem_base + ((uint32_t)(quarter * 32) << 16);
-        const uint32_t stage = smem_u32(pl.smem + SMEM_WORK - (EPI_WARPS - ew) * EPI_STAGE);
-        Out out{stage, lane, 0u};
-        // GLU: lanes 0..63 hold gate columns, 64..127 the up columns of the same h;
-        // the gate warp hands act(gate) in fp32 to the up warp two quarters on
-        const bool gate = GLU && quarter < 2;
-        const int pair = (quarter & 1) + 2 * half;
-        const uint32_t to_up = smem_u32(pl.smem + SMEM_WORK - (EPI_WARPS - (quarter & 1) - 4 * half) * EPI_STAGE + 4096) +
-                               16u * lane;
-        uint32_t handed = 0;
-        bool ok = true;
-        for (; ok && cur.find(p, t, lane, ti); t += pl.step) {
-            ok = __all_sync(0xFFFFFFFFu, mbar_wait_cluster(pl.tfull(acc.at), acc.phase, p, pl.abort_flag));
-            if (!ok) break;
-            tc_fence_after();
-            const int chunks = (ti.rows + 31) / 32;
-            const int c0 = half == 0 ? 0 : (chunks + 1) / 2, c1 = half == 0 ? (chunks + 1) / 2 : chunks;
-            const uint32_t tacc = lane_base + (uint32_t)(acc.at * ACC_COLS);
-            const int col = GLU ? ti.ct * 128 + 64 * (int)pl.rank + 32 * (quarter & 1)
-                                : ti.ct * 256 + 128 * (int)pl.rank + 32 * quarter;
-            const int cols = p.N - col;
-            for (int c = c0; c < c1 && ok; ++c) {
-                uint32_t r[32];
-                tmem_ld_16x32(tacc + 32 * c, r);
-                tmem_ld_16x32(tacc + (16u << 16) + 32 * c, r + 16);
-                tmem_wait_ld();
-                if (c + 1 == c1) {      // the accumulator is read: the next tile may have it
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive_remote(mapa(pl.tempty(acc.at), 0));
-                }
-                float v[32];
-#pragma unroll
-                for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
-                const int64_t row = ti.row0 + 32 * c;
-                const int rows = ti.rows - 32 * c;
-                if constexpr (!GLU) {
-                    if (cols > 0) out.put(&tmY, static_cast<__nv_bfloat16*>(p.y), p.ldy, col, cols, row, rows, v);
-                } else {
-                    if (cols <= 0) continue;      // both warps
-                    if (p.a != nullptr)
-                        out.put(gate ? &tmA : &tmA2, p.a + (gate ? 0 : p.N), p.lda, col, cols, row, rows, v);
-                    if (gate) {
-                        ok = __all_sync(0xFFFFFFFFu, mbar_wait(pl.xempty(pair), handed & 1u ^ 1u, p, pl.abort_flag));
-                        if (!ok) break;
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) v[i] = act_of(v[i], ACT);
-#pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            st_shared_v4(to_up + 512u * i, __float_as_uint(v[4 * i]), __float_as_uint(v[4 * i + 1]),
-                                         __float_as_uint(v[4 * i + 2]), __float_as_uint(v[4 * i + 3]));
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(pl.xfull(pair));
-                    } else {
-                        ok = __all_sync(0xFFFFFFFFu, mbar_wait(pl.xfull(pair), handed & 1u, p, pl.abort_flag));
-                        if (!ok) break;
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            float g[4];
-                            asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
-                                         : "=f"(g[0]), "=f"(g[1]), "=f"(g[2]), "=f"(g[3])
-                                         : "r"(to_up + 512u * i)
-                                         : "memory");
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) v[4 * i + j] *= g[j];
-                        }
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(pl.xempty(pair));
-                        out.put(&tmY, static_cast<__nv_bfloat16*>(p.y), p.ldy, col, cols, row, rows, v);
-                    }
-                    ++handed;
-                }
-            }
-            if (c0 >= c1) {      // nothing of this tile is this warp's
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_remote(mapa(pl.tempty(acc.at), 0));
-            }
-            acc.next(NACC);
-        }
-        if (lane == 0) bulk_wait_group0();      // the stores are complete
-        __syncwarp();
+    } else if (pl.warp >= 4) {
+        store_rows<GLU, ACT, 2>(pl, p, &tmY, &tmA, &tmA2, tmem_base, cur, t, acc);
+        stores_end(pl.lane);
     }
     tear_down(pl, tmem_base);
 }
@@ -553,6 +582,171 @@ struct WOut {
     }
 };
 
+// The weight gradients' tiles from the pair's next one, t, on.
+__device__ __forceinline__ void load_wgrad(const Place& pl, const Params& p, const CUtensorMap* tmX,
+                                           const CUtensorMap* tmDY, int64_t t, Ring& ring) {
+    const bool elected = elect_one();
+    const int bh = p.bn / 2, boxes = (bh + 63) / 64;      // of dy's columns, per CTA
+    const uint32_t bytes = HALF_BYTES + boxes * (HALF_BYTES / 2);
+    const uint32_t lead_full = mapa(pl.full(0), 0);
+    for (; t < p.max_tiles && !ring.aborted; t += pl.step) {
+        const WTile w = w_tile(p, t);
+        const int nk = (w.rows / 16 + 3) / 4;      // steps of 64 rows, the last of fewer 16-row ones
+        const int am = w.mt * TM + 128 * (int)pl.rank, bn = w.nt * p.bn + bh * (int)pl.rank;
+        for (int ks = 0; ks < nk; ++ks) {
+            if (!mbar_wait_cluster(pl.empty(ring.at), ring.phase ^ 1u, p, pl.abort_flag)) {
+                ring.aborted = true;
+                break;
+            }
+            const uint32_t fb = lead_full + 8u * ring.at;
+            if (elected) {
+                if (pl.rank == 0) mbar_expect_tx(pl.full(ring.at), 2u * bytes);
+                const uint32_t sa = smem_u32(pl.smem + ring.at * p.stage_bytes), sb = sa + HALF_BYTES;
+                const int row = w.start + ks * TK;
+                tma2_load_2d(sa, tmX, am, row, fb);
+                tma2_load_2d(sa + HALF_BYTES / 2, tmX, am + 64, row, fb);
+                tma2_load_2d(sb, tmDY, bn, row, fb);
+                if (boxes > 1) tma2_load_2d(sb + HALF_BYTES / 2, tmDY, bn + 64, row, fb);
+            }
+            ring.next(p.stages);
+        }
+    }
+}
+__device__ __forceinline__ void fill_last_rows(const Place& pl, const Params& p, int64_t t) {
+    // ------------------- a group's last rows, fewer than 16, two buffers ----
+    // laid out as the TMA does: boxes of 64 columns, rows of 128 bytes, their
+    // 16-byte units swizzled by the row
+    const int lane = pl.lane, bh = p.bn / 2, boxes = (bh + 63) / 64;
+    const uint32_t lead = mapa(pl.xfull(0), 0);
+    Ring last;
+    for (; t < p.max_tiles; t += pl.step) {
+        const WTile w = w_tile(p, t);
+        const int n = w.rows & 15;
+        if (n == 0) continue;
+        if (!__all_sync(0xFFFFFFFFu, mbar_wait_cluster(pl.xempty(last.at), last.phase ^ 1u, p, pl.abort_flag))) break;
+        const uint32_t buf = smem_u32(pl.smem + OFF_LAST + last.at * LAST_BYTES);
+        const int64_t row0 = (int64_t)w.start + w.rows - n;
+        const int am = w.mt * TM + 128 * (int)pl.rank, bn = w.nt * p.bn + bh * (int)pl.rank;
+        const int lane2 = (int)threadIdx.x - 64, unit = lane2 & 7;
+        // two boxes of x, then dy's: 8 units of 16 rows each
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+            if (b >= 2 + boxes) break;
+            const bool is_x = b < 2;
+            const int col = (is_x ? am + 64 * b : bn + 64 * (b - 2)) + 8 * unit;
+            const int cols = min((is_x ? p.K : p.N) - col, 8);
+            uint4 v[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int r = (lane2 >> 3) + 8 * i;
+                v[i] = make_uint4(0u, 0u, 0u, 0u);
+                if (r < n && cols > 0)
+                    v[i] = load_vec8(is_x ? p.x + (row0 + r) * p.ldx + col : p.dy + (row0 + r) * p.lddy + col, cols);
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int r = (lane2 >> 3) + 8 * i;
+                st_shared_v4(buf + 2048u * b + 128u * r + (((uint32_t)unit ^ (r & 7u)) << 4), v[i].x, v[i].y, v[i].z,
+                             v[i].w);
+            }
+        }
+        fence_proxy_async_shared();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_remote(lead + 8u * last.at);
+        last.next(2);
+    }
+}
+__device__ __forceinline__ void multiply_wgrad(const Place& pl, const Params& p, uint32_t tmem_base, int64_t t, Ring& ring,
+                                               Ring& acc) {
+    const bool elected = elect_one();
+    Ring last;
+    const uint32_t idesc = make_idesc_pair<true, true>(p.bn);
+    const uint64_t adesc0 = operand_desc<true>(smem_u32(pl.smem));
+    const uint64_t bdesc0 = operand_desc<true>(smem_u32(pl.smem) + HALF_BYTES);
+    const uint32_t stage_step = (uint32_t)p.stage_bytes >> 4;
+    for (; t < p.max_tiles && !ring.aborted; t += pl.step) {
+        const WTile w = w_tile(p, t);
+        if (w.rows == 0) continue;
+        const int steps = w.rows / 16, nk = (steps + 3) / 4;
+        if (!__all_sync(0xFFFFFFFFu, mbar_wait_cluster(pl.tempty(acc.at), acc.phase ^ 1u, p, pl.abort_flag))) {
+            ring.aborted = true;
+            break;
+        }
+        tc_fence_after();
+        const uint32_t d_tmem = tmem_base + (uint32_t)(acc.at * ACC_COLS);
+        // (the loop has to be short: a step's four products take 512 cycles)
+        for (int ks = 0; ks < nk; ++ks) {
+            if (!mbar_wait(pl.full(ring.at), ring.phase, p, pl.abort_flag)) {
+                ring.aborted = true;
+                break;
+            }
+            tc_fence_after();
+            if (elected) {
+                const uint64_t adesc = adesc0 + ring.at * stage_step, bdesc = bdesc0 + ring.at * stage_step;
+#pragma unroll
+                for (int kk = 0; kk < TK / 16; ++kk)
+                    if (4 * ks + kk < steps)
+                        tc_mma2_bf16(d_tmem, adesc + k16_step<true>() * kk, bdesc + k16_step<true>() * kk, idesc,
+                                     (ks != 0 || kk != 0) ? 1u : 0u);
+                tc_commit_pair(pl.empty(ring.at), 0);
+            }
+            ring.next(p.stages);
+        }
+        if ((w.rows & 15) != 0 && !ring.aborted) {      // both CTAs have filled the last step
+            if (mbar_wait_cluster(pl.xfull(last.at), last.phase, p, pl.abort_flag)) {
+                tc_fence_after();
+                if (elected) {
+                    const uint32_t buf = smem_u32(pl.smem + OFF_LAST + last.at * LAST_BYTES);
+                    tc_mma2_bf16(d_tmem, desc_mn_sw128(buf, 2048), desc_mn_sw128(buf + 4096, 2048), idesc,
+                                 steps > 0 ? 1u : 0u);
+                    tc_commit_pair(pl.xempty(last.at), 0);
+                }
+                last.next(2);
+            } else {
+                ring.aborted = true;
+            }
+        }
+        ring.aborted = __any_sync(0xFFFFFFFFu, ring.aborted);      // the warp goes on as one
+        if (ring.aborted) break;
+        if (elected) tc_commit_pair(pl.tfull(acc.at), 0);
+        acc.next(NACC);
+    }
+}
+template <bool F32>
+__device__ __forceinline__ void store_wgrad(const Place& pl, const Params& p, const CUtensorMap* tmD, uint32_t tmem_base,
+                                            int64_t t, Ring& acc) {
+    const int lane = pl.lane, ew = pl.warp - 4, quarter = ew & 3, half = ew >> 2;
+    const uint32_t lane_base = tmem_base + ((uint32_t)(quarter * 32) << 16);
+    WOut<F32> out{smem_u32(pl.smem + SMEM_WORK - (EPI_WARPS - ew) * W_BOX), lane};
+    const int chunks = p.bn / 32, c0 = half == 0 ? 0 : (chunks + 1) / 2, c1 = half == 0 ? (chunks + 1) / 2 : chunks;
+    for (; t < p.max_tiles; t += pl.step) {
+        const WTile w = w_tile(p, t);
+        const int row0 = w.mt * TM + 128 * (int)pl.rank + quarter * 32;
+        const uint32_t tacc = lane_base + (uint32_t)(acc.at * ACC_COLS);
+        if (w.rows > 0) {
+            if (!__all_sync(0xFFFFFFFFu, mbar_wait_cluster(pl.tfull(acc.at), acc.phase, p, pl.abort_flag))) break;
+            tc_fence_after();
+        }
+        for (int c = c0; c < c1; ++c) {
+            float v[32];
+            if (w.rows > 0) {
+                tmem_ld32(tacc + 32 * c, v);
+                if (c + 1 == c1) {      // the accumulator is read: the next tile may have it
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_remote(mapa(pl.tempty(acc.at), 0));
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) v[i] = 0.f;
+            }
+            const int col = w.nt * p.bn + 32 * c;
+            if (col < p.N && row0 < p.K) out.put(p, tmD, w.g, row0, col, v);      // the whole warp
+        }
+        if (w.rows > 0) acc.next(NACC);
+    }
+}
+
 template <bool F32>
 __global__ void __launch_bounds__(THREADS, 1)
     k_wgrad(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmDY,
@@ -565,177 +759,66 @@ __global__ void __launch_bounds__(THREADS, 1)
     Place pl;
     const uint32_t tmem_base = set_up(pl, p.stages, 4);      // warps 2 and 3 of both CTAs
     wait_for_previous_kernels();
-    const int warp = pl.warp, lane = pl.lane;
-    const int bh = p.bn / 2, boxes = (bh + 63) / 64;      // of dy's columns, per CTA
-    const uint32_t bytes = HALF_BYTES + boxes * (HALF_BYTES / 2);
+    Ring ring, acc;
+    if (pl.warp == 0) {
+        load_wgrad(pl, p, &tmX, &tmDY, pl.first, ring);
+        loads_end(pl, p, ring);
+    } else if (pl.warp == 1 && pl.rank == 0) {
+        multiply_wgrad(pl, p, tmem_base, pl.first, ring, acc);
+        products_end(pl, p, ring);
+    } else if (pl.warp == 2 || pl.warp == 3) {
+        fill_last_rows(pl, p, pl.first);
+    } else if (pl.warp >= 4) {
+        store_wgrad<F32>(pl, p, &tmD, tmem_base, pl.first, acc);
+        stores_end(pl.lane);
+    }
+    tear_down(pl, tmem_base);
+}
+
+// Both gradients of a layer, dx = dz W^T (p) and then dW = x^T dz (q), as the tiles
+// of one launch: one set-up, and the short tiles of dW fill the last wave of
+// the long ones of dx.  A pair's tile t of the launch is dW's tile t - end, where
+// end is the number of dx's, known when the groups have been gone through.
+__device__ __forceinline__ int64_t wgrad_first(const Place& pl, const Cursor& cur, int64_t t) {
+    int64_t u = t - cur.end;
+    while (u < 0) u += pl.step;      // (offsets out of order)
+    return u;
+}
+template <bool F32>
+__global__ void __launch_bounds__(THREADS, 1)
+    k_both(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmZ16,
+           const __grid_constant__ CUtensorMap tmZ32, const __grid_constant__ CUtensorMap tmZ64,
+           const __grid_constant__ CUtensorMap tmZ128, const __grid_constant__ CUtensorMap tmDX,
+           const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmDY,
+           const __grid_constant__ CUtensorMap tmD, const Params p, const Params q) {
+    if (threadIdx.x == 64) {
+        prefetch_map(&tmW);
+        prefetch_map(&tmZ128);
+        prefetch_map(&tmX);
+        prefetch_map(&tmDY);
+    }
+    Place pl;
+    const uint32_t tmem_base = set_up(pl, p.stages, 4);
+    wait_for_previous_kernels();
+    Cursor cur;
     Ring ring, acc;
     int64_t t = pl.first;
-
-    if (warp == 0) {
-        // ------------------------------------------------------ loads ----
-        const bool elected = elect_one();
-        const uint32_t lead_full = mapa(pl.full(0), 0);
-        for (; t < p.max_tiles && !ring.aborted; t += pl.step) {
-            const WTile w = w_tile(p, t);
-            const int nk = (w.rows / 16 + 3) / 4;      // steps of 64 rows, the last of fewer 16-row ones
-            const int am = w.mt * TM + 128 * (int)pl.rank, bn = w.nt * p.bn + bh * (int)pl.rank;
-            for (int ks = 0; ks < nk; ++ks) {
-                if (!mbar_wait_cluster(pl.empty(ring.at), ring.phase ^ 1u, p, pl.abort_flag)) {
-                    ring.aborted = true;
-                    break;
-                }
-                const uint32_t fb = lead_full + 8u * ring.at;
-                if (elected) {
-                    if (pl.rank == 0) mbar_expect_tx(pl.full(ring.at), 2u * bytes);
-                    const uint32_t sa = smem_u32(pl.smem + ring.at * p.stage_bytes), sb = sa + HALF_BYTES;
-                    const int row = w.start + ks * TK;
-                    tma2_load_2d(sa, &tmX, am, row, fb);
-                    tma2_load_2d(sa + HALF_BYTES / 2, &tmX, am + 64, row, fb);
-                    tma2_load_2d(sb, &tmDY, bn, row, fb);
-                    if (boxes > 1) tma2_load_2d(sb + HALF_BYTES / 2, &tmDY, bn + 64, row, fb);
-                }
-                ring.next(p.stages);
-            }
-        }
-        __syncwarp();
-        if (ring.aborted && pl.rank == 0) {      // the copies in flight
-            const Params q = patient(p);
-            volatile int no_abort = 0;
-            for (int i = ring.count - min(ring.count, p.stages); i < ring.count; ++i)
-                mbar_wait_cluster(pl.full(i % p.stages), (uint32_t)(i / p.stages) & 1u, q, &no_abort);
-        }
-    } else if (warp == 2 || warp == 3) {
-        // ------------------- a group's last rows, fewer than 16, two buffers ----
-        // laid out as the TMA does: boxes of 64 columns, rows of 128 bytes, their
-        // 16-byte units swizzled by the row
-        const uint32_t lead = mapa(pl.xfull(0), 0);
-        Ring last;
-        for (; t < p.max_tiles; t += pl.step) {
-            const WTile w = w_tile(p, t);
-            const int n = w.rows & 15;
-            if (n == 0) continue;
-            if (!__all_sync(0xFFFFFFFFu, mbar_wait_cluster(pl.xempty(last.at), last.phase ^ 1u, p, pl.abort_flag))) break;
-            const uint32_t buf = smem_u32(pl.smem + OFF_LAST + last.at * LAST_BYTES);
-            const int64_t row0 = (int64_t)w.start + w.rows - n;
-            const int am = w.mt * TM + 128 * (int)pl.rank, bn = w.nt * p.bn + bh * (int)pl.rank;
-            const int lane2 = (int)threadIdx.x - 64, unit = lane2 & 7;
-            // two boxes of x, then dy's: 8 units of 16 rows each
-#pragma unroll
-            for (int b = 0; b < 4; ++b) {
-                if (b >= 2 + boxes) break;
-                const bool is_x = b < 2;
-                const int col = (is_x ? am + 64 * b : bn + 64 * (b - 2)) + 8 * unit;
-                const int cols = min((is_x ? p.K : p.N) - col, 8);
-                uint4 v[2];
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int r = (lane2 >> 3) + 8 * i;
-                    v[i] = make_uint4(0u, 0u, 0u, 0u);
-                    if (r < n && cols > 0)
-                        v[i] = load_vec8(is_x ? p.x + (row0 + r) * p.ldx + col : p.dy + (row0 + r) * p.lddy + col, cols);
-                }
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int r = (lane2 >> 3) + 8 * i;
-                    st_shared_v4(buf + 2048u * b + 128u * r + (((uint32_t)unit ^ (r & 7u)) << 4), v[i].x, v[i].y, v[i].z,
-                                 v[i].w);
-                }
-            }
-            fence_proxy_async_shared();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_remote(lead + 8u * last.at);
-            last.next(2);
-        }
-    } else if (warp == 1 && pl.rank == 0) {
-        // --------------------------------------------------- products ----
-        const bool elected = elect_one();
-        Ring last;
-        const uint32_t idesc = make_idesc_pair<true, true>(p.bn);
-        const uint64_t adesc0 = operand_desc<true>(smem_u32(pl.smem));
-        const uint64_t bdesc0 = operand_desc<true>(smem_u32(pl.smem) + HALF_BYTES);
-        const uint32_t stage_step = (uint32_t)p.stage_bytes >> 4;
-        for (; t < p.max_tiles && !ring.aborted; t += pl.step) {
-            const WTile w = w_tile(p, t);
-            if (w.rows == 0) continue;
-            const int steps = w.rows / 16, nk = (steps + 3) / 4;
-            if (!__all_sync(0xFFFFFFFFu, mbar_wait_cluster(pl.tempty(acc.at), acc.phase ^ 1u, p, pl.abort_flag))) {
-                ring.aborted = true;
-                break;
-            }
-            tc_fence_after();
-            const uint32_t d_tmem = tmem_base + (uint32_t)(acc.at * ACC_COLS);
-            // (the loop has to be short: a step's four products take 512 cycles)
-            for (int ks = 0; ks < nk; ++ks) {
-                if (!mbar_wait(pl.full(ring.at), ring.phase, p, pl.abort_flag)) {
-                    ring.aborted = true;
-                    break;
-                }
-                tc_fence_after();
-                if (elected) {
-                    const uint64_t adesc = adesc0 + ring.at * stage_step, bdesc = bdesc0 + ring.at * stage_step;
-#pragma unroll
-                    for (int kk = 0; kk < TK / 16; ++kk)
-                        if (4 * ks + kk < steps)
-                            tc_mma2_bf16(d_tmem, adesc + k16_step<true>() * kk, bdesc + k16_step<true>() * kk, idesc,
-                                         (ks != 0 || kk != 0) ? 1u : 0u);
-                    tc_commit_pair(pl.empty(ring.at), 0);
-                }
-                ring.next(p.stages);
-            }
-            if ((w.rows & 15) != 0 && !ring.aborted) {      // both CTAs have filled the last step
-                if (mbar_wait_cluster(pl.xfull(last.at), last.phase, p, pl.abort_flag)) {
-                    tc_fence_after();
-                    if (elected) {
-                        const uint32_t buf = smem_u32(pl.smem + OFF_LAST + last.at * LAST_BYTES);
-                        tc_mma2_bf16(d_tmem, desc_mn_sw128(buf, 2048), desc_mn_sw128(buf + 4096, 2048), idesc,
-                                     steps > 0 ? 1u : 0u);
-                        tc_commit_pair(pl.xempty(last.at), 0);
-                    }
-                    last.next(2);
-                } else {
-                    ring.aborted = true;
-                }
-            }
-            ring.aborted = __any_sync(0xFFFFFFFFu, ring.aborted);      // the warp goes on as one
-            if (ring.aborted) break;
-            if (elected) tc_commit_pair(pl.tfull(acc.at), 0);
-            acc.next(NACC);
-        }
+    if (pl.warp == 0) {
+        load_rows<false, false>(pl, p, &tmW, &tmZ16, &tmZ32, &tmZ64, &tmZ128, cur, t, ring);
+        if (!ring.aborted) load_wgrad(pl, q, &tmX, &tmDY, wgrad_first(pl, cur, t), ring);
+        loads_end(pl, p, ring);
+    } else if (pl.warp == 1 && pl.rank == 0) {
+        multiply_rows<false>(pl, p, tmem_base, cur, t, ring, acc);
+        if (!ring.aborted) multiply_wgrad(pl, q, tmem_base, wgrad_first(pl, cur, t), ring, acc);
         products_end(pl, p, ring);
-    } else if (warp >= 4) {
-        // --------------------------------------------------- epilogue ----
-        const int ew = warp - 4, quarter = ew & 3, half = ew >> 2;
-        const uint32_t lane_base = tmem_base + ((uint32_t)(quarter * 32) << 16);
-        WOut<F32> out{smem_u32(pl.smem + SMEM_WORK - (EPI_WARPS - ew) * W_BOX), lane};
-        const int chunks = p.bn / 32, c0 = half == 0 ? 0 : (chunks + 1) / 2, c1 = half == 0 ? (chunks + 1) / 2 : chunks;
-        for (; t < p.max_tiles; t += pl.step) {
-            const WTile w = w_tile(p, t);
-            const int row0 = w.mt * TM + 128 * (int)pl.rank + quarter * 32;
-            const uint32_t tacc = lane_base + (uint32_t)(acc.at * ACC_COLS);
-            if (w.rows > 0) {
-                if (!__all_sync(0xFFFFFFFFu, mbar_wait_cluster(pl.tfull(acc.at), acc.phase, p, pl.abort_flag))) break;
-                tc_fence_after();
-            }
-            for (int c = c0; c < c1; ++c) {
-                float v[32];
-                if (w.rows > 0) {
-                    tmem_ld32(tacc + 32 * c, v);
-                    if (c + 1 == c1) {      // the accumulator is read: the next tile may have it
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive_remote(mapa(pl.tempty(acc.at), 0));
-                    }
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) v[i] = 0.f;
-                }
-                const int col = w.nt * p.bn + 32 * c;
-                if (col < p.N && row0 < p.K) out.put(p, &tmD, w.g, row0, col, v);      // the whole warp
-            }
-            if (w.rows > 0) acc.next(NACC);
-        }
-        if (lane == 0) bulk_wait_group0();      // the stores are complete
-        __syncwarp();
+    } else if (pl.warp == 2 || pl.warp == 3) {
+        Tile ti;
+        while (cur.find(p, t, pl.lane, ti)) t += pl.step;
+        fill_last_rows(pl, q, wgrad_first(pl, cur, t));
+    } else if (pl.warp >= 4) {
+        if (store_rows<false, 0, 1>(pl, p, &tmDX, nullptr, nullptr, tmem_base, cur, t, acc))
+            store_wgrad<F32>(pl, q, &tmD, tmem_base, wgrad_first(pl, cur, t), acc);
+        stores_end(pl.lane);
     }
     tear_down(pl, tmem_base);
 }
@@ -806,7 +889,9 @@ static cudaError_t set_attributes() {
                         (const void*)k_rows<true, true, MOE_ACT_GELU>,
                         (const void*)k_rows<true, true, MOE_ACT_SILU>,
                         (const void*)k_wgrad<false>,
-                        (const void*)k_wgrad<true>};
+                        (const void*)k_wgrad<true>,
+                        (const void*)k_both<false>,
+                        (const void*)k_both<true>};
     for (const void* k : ks) {
         const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
         if (e != cudaSuccess) return e;
@@ -822,26 +907,36 @@ struct Mat {
 };
 constexpr int64_t kMaxTiles = 0x3FFFFFFF;
 
-// D = x op(W) of every group; x [M, depth], D's columns W's (W_MN) or its rows.
-template <bool W_MN, bool GLU, int ACT>
-static moe_status_t product_rows(const Mat& x, const Mat& w, Params p, cudaStream_t s) {
-    MOE_REQUIRE(g_max_clusters > 0, MOE_ERR_NOT_INITIALIZED);
+// The fields of p that sizes decide, for D = x op(W) of x [M, depth]; the maps of x.
+template <bool GLU>
+static moe_status_t plan_rows(Params& p) {
     p.n_max = (int)std::min<int64_t>(256, (p.M + 31) / 32 * 32);
     int box = 16;      // rows of x per CTA that a stage has room for
     while (2 * box < p.n_max) box *= 2;
     p.stage_bytes = HALF_BYTES + box * TK * 2;
-    p.stages = std::min(MAX_STAGES, (SMEM_WORK - EPI_WARPS * (GLU ? 8192 : 4096)) / p.stage_bytes);
     p.nk = (p.K + TK - 1) / TK;
     const int cols = GLU ? 128 : 256;
     p.col_tiles = (p.N + cols - 1) / cols;
     p.max_tiles = (p.M / p.n_max + std::min<int64_t>(p.G, p.M)) * p.col_tiles;
-    MOE_REQUIRE(p.max_tiles <= kMaxTiles, MOE_ERR_UNSUPPORTED);
     p.timeout_ns = 2000000000ull;
-    CUtensorMap tmW, tmX[4], tmY, tmA, tmA2;
-    bool ok = make_bf16_map3(&tmW, w.p, p.G, w.rows, w.cols, w.ld, w.gs, W_MN ? TK : 128);
+    return p.max_tiles <= kMaxTiles ? MOE_OK : MOE_ERR_UNSUPPORTED;
+}
+static bool rows_maps(CUtensorMap* tmX, CUtensorMap* tmY, const Mat& x, const Params& p) {
+    bool ok = true;
     for (int i = 0; i < 4; ++i) ok = ok && make_bf16_map(&tmX[i], x.p, x.rows, x.cols, x.ld, 16 << i);
     // boxes that end inside 16 bytes are not stored through the map
-    ok = ok && make_store_map(&tmY, p.y, p.M, std::max(p.N & ~7, 8), p.ldy, false);
+    return ok && make_store_map(tmY, p.y, p.M, std::max(p.N & ~7, 8), p.ldy, false);
+}
+
+// D = x op(W) of every group; D's columns are W's (W_MN) or its rows.
+template <bool W_MN, bool GLU, int ACT>
+static moe_status_t product_rows(const Mat& x, const Mat& w, Params p, cudaStream_t s) {
+    MOE_REQUIRE(g_max_clusters > 0, MOE_ERR_NOT_INITIALIZED);
+    const moe_status_t st = plan_rows<GLU>(p);
+    if (st != MOE_OK) return st;
+    p.stages = std::min(MAX_STAGES, (SMEM_WORK - EPI_WARPS * (GLU ? 8192 : 4096)) / p.stage_bytes);
+    CUtensorMap tmW, tmX[4], tmY, tmA, tmA2;
+    bool ok = make_bf16_map3(&tmW, w.p, p.G, w.rows, w.cols, w.ld, w.gs, W_MN ? TK : 128) && rows_maps(tmX, &tmY, x, p);
     tmA = tmA2 = tmY;
     if (p.a != nullptr)
         ok = ok && make_store_map(&tmA, p.a, p.M, p.N, p.lda, false) &&
@@ -873,6 +968,22 @@ static int wgrad_width(int64_t tiles256, int N, double nk, int slots) {
     }
     return best;
 }
+static moe_status_t plan_wgrad(Params& p) {
+    p.m_tiles = (p.K + TM - 1) / TM;
+    p.bn = wgrad_width((int64_t)p.G * p.m_tiles, p.N, (double)p.M / p.G / TK, g_max_clusters);
+    p.col_tiles = (p.N + p.bn - 1) / p.bn;
+    p.max_tiles = (int64_t)p.G * p.m_tiles * p.col_tiles;
+    p.stage_bytes = HALF_BYTES + (p.bn / 2 + 63) / 64 * (HALF_BYTES / 2);
+    p.timeout_ns = 2000000000ull;
+    return p.max_tiles <= kMaxTiles ? MOE_OK : MOE_ERR_UNSUPPORTED;
+}
+static bool wgrad_maps(CUtensorMap* tmX, CUtensorMap* tmDY, CUtensorMap* tmD, const Mat& x, const Mat& dy, Params& p,
+                       bool f32) {
+    p.x = static_cast<const __nv_bfloat16*>(x.p), p.ldx = x.ld;
+    p.dy = static_cast<const __nv_bfloat16*>(dy.p), p.lddy = dy.ld;
+    return make_bf16_map(tmX, x.p, x.rows, x.cols, x.ld, TK) && make_bf16_map(tmDY, dy.p, dy.rows, dy.cols, dy.ld, TK) &&
+           make_store_map3(tmD, p.y, p.G, p.K, std::max(p.N & ~7, 8), p.ldy, p.gsy, f32);
+}
 
 // D_g [K, N] = x^T dy of every group
 static moe_status_t product_wgrad(const Mat& x, const Mat& dy, Params p, bool f32, cudaStream_t s) {
@@ -885,25 +996,38 @@ static moe_status_t product_wgrad(const Mat& x, const Mat& dy, Params p, bool f3
                 return MOE_ERR_CUDA;
         return MOE_OK;
     }
-    p.m_tiles = (p.K + TM - 1) / TM;
-    p.bn = wgrad_width((int64_t)p.G * p.m_tiles, p.N, (double)p.M / p.G / TK, g_max_clusters);
-    p.col_tiles = (p.N + p.bn - 1) / p.bn;
-    p.max_tiles = (int64_t)p.G * p.m_tiles * p.col_tiles;
-    MOE_REQUIRE(p.max_tiles <= kMaxTiles, MOE_ERR_UNSUPPORTED);
-    p.stage_bytes = HALF_BYTES + (p.bn / 2 + 63) / 64 * (HALF_BYTES / 2);
+    const moe_status_t st = plan_wgrad(p);
+    if (st != MOE_OK) return st;
     p.stages = std::min(MAX_STAGES, OFF_LAST / p.stage_bytes);
-    p.timeout_ns = 2000000000ull;
-    p.x = static_cast<const __nv_bfloat16*>(x.p), p.ldx = x.ld;
-    p.dy = static_cast<const __nv_bfloat16*>(dy.p), p.lddy = dy.ld;
     CUtensorMap tmX, tmDY, tmD;
-    MOE_REQUIRE(make_bf16_map(&tmX, x.p, x.rows, x.cols, x.ld, TK) &&
-                    make_bf16_map(&tmDY, dy.p, dy.rows, dy.cols, dy.ld, TK) &&
-                    make_store_map3(&tmD, p.y, p.G, p.K, std::max(p.N & ~7, 8), p.ldy, p.gsy, f32),
-                MOE_ERR_CUDA);
+    MOE_REQUIRE(wgrad_maps(&tmX, &tmDY, &tmD, x, dy, p, f32), MOE_ERR_CUDA);
     cudaLaunchAttribute attr[2];
     cudaLaunchConfig_t cfg = launch_cfg(std::min<int64_t>(p.max_tiles, g_max_clusters), s, attr);
     const cudaError_t e = f32 ? cudaLaunchKernelEx(&cfg, k_wgrad<true>, tmX, tmDY, tmD, p)
                               : cudaLaunchKernelEx(&cfg, k_wgrad<false>, tmX, tmDY, tmD, p);
+    if (e != cudaSuccess) return MOE_ERR_CUDA;
+    MOE_CHECK_LAUNCH();
+    return MOE_OK;
+}
+
+// dx = dz W^T (p) and dW = x^T dz (q) in one launch
+static moe_status_t product_both(const Mat& dz, const Mat& x, const Mat& w, Params p, Params q, bool f32,
+                                 cudaStream_t s) {
+    MOE_REQUIRE(g_max_clusters > 0, MOE_ERR_NOT_INITIALIZED);
+    moe_status_t st = plan_rows<false>(p);
+    if (st == MOE_OK) st = plan_wgrad(q);
+    if (st != MOE_OK) return st;
+    p.stage_bytes = q.stage_bytes = std::max(p.stage_bytes, q.stage_bytes);
+    p.stages = q.stages = std::min(MAX_STAGES, OFF_LAST / p.stage_bytes);
+    CUtensorMap tmW, tmZ[4], tmDX, tmX, tmDY, tmD;
+    MOE_REQUIRE(make_bf16_map3(&tmW, w.p, p.G, w.rows, w.cols, w.ld, w.gs, 128) && rows_maps(tmZ, &tmDX, dz, p) &&
+                    wgrad_maps(&tmX, &tmDY, &tmD, x, dz, q, f32),
+                MOE_ERR_CUDA);
+    cudaLaunchAttribute attr[2];
+    cudaLaunchConfig_t cfg = launch_cfg(std::min<int64_t>(p.max_tiles + q.max_tiles, g_max_clusters), s, attr);
+    const cudaError_t e =
+        f32 ? cudaLaunchKernelEx(&cfg, k_both<true>, tmW, tmZ[0], tmZ[1], tmZ[2], tmZ[3], tmDX, tmX, tmDY, tmD, p, q)
+            : cudaLaunchKernelEx(&cfg, k_both<false>, tmW, tmZ[0], tmZ[1], tmZ[2], tmZ[3], tmDX, tmX, tmDY, tmD, p, q);
     if (e != cudaSuccess) return MOE_ERR_CUDA;
     MOE_CHECK_LAUNCH();
     return MOE_OK;
@@ -927,16 +1051,20 @@ static bool groups_ok(const int32_t* offsets, const int32_t* rows) {
 // dx = dz W^T and dW = x^T dz, each if asked for; W_g [K, N]
 static moe_status_t gradients(const Mat& dz, const Mat& x, const Mat& w, const Params& groups, int N, int K, void* dx,
                               int64_t lddx, void* dw, bool f32, int64_t lddw, int64_t gsdw, cudaStream_t s) {
+    Params p = groups, q = groups;
+    p.N = K, p.K = N, p.y = dx, p.ldy = lddx;
+    q.N = N, q.K = K, q.y = dw, q.ldy = lddw, q.gsy = gsdw;
+    // One launch saves a set-up and a last wave (16 groups' 300 rows, 515 x 259: 11.2 us,
+    // 15.8 in two); long work runs faster in two (64 groups of 768 rows, 2,048 x
+    // 7,168: 1.85 ms, 1.90 in one; 8,192 x 4,096 x 7,168 551 us, 567): up to about 1,000 steps of
+    // 256 x 256 x 64 a pair.
+    const double steps = 2. * groups.M * K * N / (256. * 256. * 64.);
+    if (dx && dw && groups.M > 0 && steps < 1000. * g_max_clusters) return product_both(dz, x, w, p, q, f32, s);
     if (dx && groups.M > 0) {
-        Params p = groups;
-        p.N = K, p.K = N, p.y = dx, p.ldy = lddx;
         const moe_status_t st = product_rows<false, false, 0>(dz, w, p, s);
         if (st != MOE_OK) return st;
     }
-    if (!dw) return MOE_OK;
-    Params p = groups;
-    p.N = N, p.K = K, p.y = dw, p.ldy = lddw, p.gsy = gsdw;
-    return product_wgrad(x, dz, p, f32, s);
+    return dw ? product_wgrad(x, dz, q, f32, s) : MOE_OK;
 }
 
 }  // namespace grouped
