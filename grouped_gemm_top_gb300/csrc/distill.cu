@@ -786,8 +786,10 @@ static Kernel kernel_of(bool f32, int mode, bool tail, bool wide) {
 }
 
 // How a call is spread: CTAs of a cluster (they share a row), 288 threads each
-// or, for small parts, 96, and clusters, no more than run at a time, so that
-// rows are dealt out evenly.  Of the sizes of clusters the one with the shortest
+// or, for small parts, 96, of which three times as many rows are under way on
+// an SM (16,384 x 4,096 bf16, loss and gradient: 80 us, 149 with 288; 8,000 columns 107
+// and 179, 16,000 240 and 231), and clusters, no more than run at a time, so that rows are
+// dealt out evenly.  Of the sizes of clusters the one with the shortest
 // time by this count, in ns: a 16-byte unit takes an SM 0.36 to read at the
 // memory's rate and as much to write, shared by its CTAs (one alone gets no more
 // than half of it), and a row 700 besides for the chain of its sums (800 more where they
@@ -806,7 +808,7 @@ static Spread spread(int64_t M, int V, int elem, int k, int mode, int sms) {
         Spread s{};
         s.C = 1 << c;
         s.part = (units + s.C - 1) / s.C;
-        s.wide = s.part > 256;
+        s.wide = s.part > 1200 || (s.part > 256 && M * s.C <= (int64_t)sms * kPerSm);
         const int turn = s.wide ? 256 : 64;      // units that a CTA's threads take at a time
         s.chunk = mode == BOTH ? (s.part + CHUNKS * turn - 1) / (CHUNKS * turn) * turn
                                : std::min(4, (s.part + turn - 1) / turn) * turn;

@@ -990,9 +990,10 @@ static moe_status_t product_wgrad(const Mat& x, const Mat& dy, Params p, bool f3
     MOE_REQUIRE(g_max_clusters > 0, MOE_ERR_NOT_INITIALIZED);
     const size_t size = f32 ? 4 : 2;
     if (p.M == 0) {
-        for (int g = 0; g < p.G; ++g)
-            if (cudaMemset2DAsync(static_cast<char*>(p.y) + g * p.gsy * size, p.ldy * size, 0, p.N * size, p.K, s) !=
-                cudaSuccess)
+        const bool joined = p.gsy == p.K * p.ldy;      // one matrix of G K rows
+        for (int g = 0; g < (joined ? 1 : p.G); ++g)
+            if (cudaMemset2DAsync(static_cast<char*>(p.y) + g * p.gsy * size, p.ldy * size, 0, p.N * size,
+                                  (size_t)p.K * (joined ? p.G : 1), s) != cudaSuccess)
                 return MOE_ERR_CUDA;
         return MOE_OK;
     }
