@@ -21,6 +21,16 @@
 // operands: zero times a next group's infinity would not be zero).  Zeros
 // written over the TMA's own last step instead held up every tile by 0.8 us.
 //
+// Tiles of 256 columns x up to 256 rows (k_wgrad: 256 x 256), 64 deep per stage, six
+// stages of 32 KB per CTA, two accumulators in TMEM.  Bound by the tensor cores under
+// the power cap when groups have hundreds of rows (64 groups of 718 to 818 rows, 2,048 x
+// 7,168: forward 0.97 ms, 1.49 PFLOP/s back to back; weight gradient 1.00 ms, in
+// bursts too short for the cap 0.84 ms, 1.71; a weight gradient of many groups is also bound by
+// writing dW), by the reading of W when they have few (32 rows over 256 experts,
+// 7,168 x 2 * 2,048: 240 us, 7.1 TB/s of the touched weights), by set-up, first
+// loads and last stores when everything is small (both gradients of 300 rows, 16 groups of
+// 515 x 259: 11 us).  Short of a step the rows of one group cost what 32 do.
+//
 // Warps: 0 TMA, 1 MMA (of the leader CTA), 2 and 3 (k_wgrad) a group's last rows,
 // 4-11 epilogue.  All waits are bounded.
 #include <algorithm>
