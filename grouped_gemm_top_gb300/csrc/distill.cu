@@ -28,8 +28,8 @@
 // Bound by the memory for large vocabularies (a plain copy 6.8 TB/s): 8,192 x 129,280 bf16
 // loss 322 us (6.6 TB/s), loss and gradient 734 us (5.8; 58 % of the issue slots, the rest of
 // the gap is the chain of a row's sums through the cluster, three CTAs an SM in turn),
-// gradient of 2,048 rows 172 us (6.2), loss of 4,099 x 50,257 fp32 137 us (6.0); by that chain,
-// about 3 us a row and CTA, for small ones; 5.5 us for 4 x 32,000.
+// gradient of 2,048 rows 172 us (6.2), loss of 4,099 x 50,257 fp32 137 us (6.0); by that chain
+// for small ones; 5.5 us for 4 x 32,000.
 #include <algorithm>
 
 #include "gemm_common.cuh"
@@ -467,6 +467,82 @@ __device__ __forceinline__ void clear_bits(const Params& p, const Smem& sm, int 
     __syncwarp();
 }
 
+// The row's loss, and what the backward pass needs, from the sums over it.
+template <bool TAIL>
+__device__ __forceinline__ void write_loss(const Params& p, int64_t row, const Teacher& te, float m, float s,
+                                           float s_rest) {
+    if (p.stats) p.stats[3 * row] = m, p.stats[3 * row + 1] = s, p.stats[3 * row + 2] = s_rest;
+    if (p.loss) {
+        float loss = te.fit + te.p_sum * ((finite_max(m) - te.x_ref) * p.inv_tau + logf(s) - te.t_lse);
+        if (TAIL && te.rest > 0.f && s_rest > 0.f) loss += te.rest * (logf(te.rest) - logf(s_rest / s));
+        p.loss[row] = te.some ? loss * p.tau * p.tau : 0.f;
+    }
+}
+
+// The row's gradient: e times a factor, one for the kept tokens and one for the
+// others, and the kept ones' probabilities.
+template <typename T, bool TAIL>
+struct Slope {
+    static constexpr int E = Unit<T>::E;
+    float g, f_top, ref, c;
+    f2 neg2, f2_all, c2;
+    bool zero, vec;
+    T* dx;      // element 0 of the part
+    __device__ __forceinline__ Slope(const Params& p, const Part& pt, const Teacher& te, int64_t row, float m, float s,
+                                     float s_rest) {
+        g = te.dloss * p.tau;
+        zero = !te.some || g == 0.f;
+        const bool with_rest = TAIL && te.rest > 0.f && s_rest > 0.f;
+        const float mass = with_rest ? te.mass : te.p_sum;
+        f_top = g * (mass / s);
+        const float f_all = with_rest ? g * (mass / s - te.rest / s_rest) : f_top;
+        ref = finite_max(m), c = p.c;
+        neg2 = pack(-ref, -ref), f2_all = pack(f_all, f_all), c2 = pack(c, c);
+        dx = static_cast<T*>(p.dx) + row * p.lddx - pt.head + (int64_t)pt.g0 * E;
+        vec = (reinterpret_cast<uintptr_t>(dx) & 15) == 0;
+    }
+    __device__ __forceinline__ void unit(const uint8_t* x, float* d) const {
+        f2 f[E / 2];
+        Unit<T>::pairs(*reinterpret_cast<const uint4*>(x), f);
+#pragma unroll
+        for (int i = 0; i < E / 2; ++i) unpack(mul2(e_of2(f[i], neg2, c2), f2_all), d[2 * i], d[2 * i + 1]);
+    }
+    // units u, u + step, .. of `rows` (unit 0 of the part at rows) before u1
+    __device__ __forceinline__ void units(const Part& pt, const uint8_t* rows, int u, int u1, int step) const {
+        if (vec && !zero) {
+#pragma unroll 2
+            for (; u < min(u1, pt.u1); u += step) {
+                if (u < pt.u0) break;
+                float d[E];
+                unit(rows + 16 * u, d);
+                Unit<T>::store(dx + u * E, d);
+            }
+        }
+        // the row's ends, and rows that do not lie as the logits do
+        for (; u < u1; u += step) {
+            float d[E] = {};
+            if (!zero) unit(rows + 16 * u, d);
+            if (vec && u >= pt.u0 && u < pt.u1) {
+                Unit<T>::store(dx + u * E, d);
+            } else {
+#pragma unroll
+                for (int e = 0; e < E; ++e)
+                    if (u * E + e >= pt.lo && u * E + e < pt.hi) dx[u * E + e] = Unit<T>::to(d[e]);
+            }
+        }
+    }
+    // the kept tokens first, first + step, .., over what units() stored there
+    __device__ __forceinline__ void kept(const Params& p, const Part& pt, const Smem& sm, int b, int first, int step) const {
+        if (zero) return;
+        for (int j = first; j < p.k; j += step) {
+            const int cj = sm.col(b)[j];
+            const int u = cj + pt.lo;      // element of the part
+            if (cj >= 0 && u >= 0 && u < pt.n * E)
+                dx[u] = Unit<T>::to(e_of(sm.x(b)[j], ref, c) * f_top - g * sm.p(b)[j]);
+        }
+    }
+};
+
 // T: logits; W warps go over them.
 template <typename T, int MODE, bool TAIL, int W>
 __global__ void __launch_bounds__(32 * W + 32, W == 8 ? 3 : 10) k_distill(const Params p) {
@@ -501,14 +577,6 @@ __global__ void __launch_bounds__(32 * W + 32, W == 8 ? 3 : 10) k_distill(const 
             const float f = e_of(v.x, ref, p.c);
             s += v.y * f;
             s_rest += v.z * f;
-        }
-    };
-    auto write_loss = [&](int64_t row, const Teacher& te, float m, float s, float s_rest) {
-        if (p.stats) p.stats[3 * row] = m, p.stats[3 * row + 1] = s, p.stats[3 * row + 2] = s_rest;
-        if (p.loss) {
-            float loss = te.fit + te.p_sum * ((finite_max(m) - te.x_ref) * p.inv_tau + logf(s) - te.t_lse);
-            if (TAIL && te.rest > 0.f && s_rest > 0.f) loss += te.rest * (logf(te.rest) - logf(s_rest / s));
-            p.loss[row] = te.some ? loss * p.tau * p.tau : 0.f;
         }
     };
     if (warp == W) {
@@ -640,7 +708,7 @@ __global__ void __launch_bounds__(32 * W + 32, W == 8 ? 3 : 10) k_distill(const 
                         ok = __all_sync(0xFFFFFFFFu, ok && mbar_wait(xbar(b), buf_phase, p, abort_flag));
                         if (rank == 0 && lane == 0 && ok) {
                             gather_mail(b, m, s, s_rest);
-                            write_loss(row, te, m, s, s_rest);
+                            write_loss<TAIL>(p, row, te, m, s, s_rest);
                         }
                         __syncwarp();
                         if (lane == 0) mbar_arrive(tempty(b));
@@ -649,56 +717,20 @@ __global__ void __launch_bounds__(32 * W + 32, W == 8 ? 3 : 10) k_distill(const 
                     if (!TAIL) ok = ok && mbar_wait(tfull(b), buf_phase, p, abort_flag);
                     ok = ok && mbar_wait(xbar(b), buf_phase, p, abort_flag);
                     gather_mail(b, m, s, s_rest);
-                    if (rank == 0 && threadIdx.x == 0 && ok) write_loss(row, te, m, s, s_rest);
+                    if (rank == 0 && threadIdx.x == 0 && ok) write_loss<TAIL>(p, row, te, m, s, s_rest);
                 }
             } else {
                 m = te.m, s = te.s, s_rest = te.s_rest;
             }
             if constexpr (MODE != FWD) {
                 // ------------------------------------------ gradient ----
-                const float g = te.dloss * p.tau;
-                const bool zero = !te.some || g == 0.f;
-                const bool with_rest = TAIL && te.rest > 0.f && s_rest > 0.f;
-                const float mass = with_rest ? te.mass : te.p_sum;
-                const float f_top = g * (mass / s);
-                const float f_all = with_rest ? g * (mass / s - te.rest / s_rest) : f_top;
-                const float ref = finite_max(m);
-                const f2 neg2 = pack(-ref, -ref), f2_all = pack(f_all, f_all), c2 = pack(p.c, p.c);
-                T* dx = static_cast<T*>(p.dx) + row * p.lddx - pt.head + (int64_t)pt.g0 * E;
-                const bool vec = (reinterpret_cast<uintptr_t>(dx) & 15) == 0;
-                auto slopes = [&](const uint8_t* unit, float* d) {
-                    f2 f[E / 2];
-                    Unit<T>::pairs(*reinterpret_cast<const uint4*>(unit), f);
-#pragma unroll
-                    for (int i = 0; i < E / 2; ++i) unpack(mul2(e_of2(f[i], neg2, c2), f2_all), d[2 * i], d[2 * i + 1]);
-                };
+                const Slope<T, TAIL> slope(p, pt, te, row, m, s, s_rest);
 #pragma unroll 1
                 for (int c0 = 0, ch = 0; STREAM ? c0 < p.part : ch < CHUNKS; c0 += p.chunk, ++ch) {
                     if (STREAM) wait_group(CHUNKS - 1);
                     const uint8_t* rows = STREAM ? sm.rows + 16 * (slot - c0) : sm.rows;
                     const int u1 = ok ? min(c0 + p.chunk, pt.n) : 0;
-                    int u = c0 + (int)threadIdx.x;
-                    if (vec && !zero) {
-#pragma unroll 2
-                        for (; u < min(u1, pt.u1); u += 32 * W) {
-                            if (u < pt.u0) break;
-                            float d[E];
-                            slopes(rows + 16 * u, d);
-                            Unit<T>::store(dx + u * E, d);
-                        }
-                    }
-                    // the row's ends, and rows that do not lie as the logits do
-                    for (; u < u1; u += 32 * W) {
-                        float d[E] = {};
-                        if (!zero) slopes(rows + 16 * u, d);
-                        if (vec && u >= pt.u0 && u < pt.u1) {
-                            Unit<T>::store(dx + u * E, d);
-                        } else {
-#pragma unroll
-                            for (int e = 0; e < E; ++e)
-                                if (u * E + e >= pt.lo && u * E + e < pt.hi) dx[u * E + e] = Unit<T>::to(d[e]);
-                        }
-                    }
+                    slope.units(pt, rows, c0 + (int)threadIdx.x, u1, 32 * W);
                     if (STREAM) {
                         send_next();
                         advance();
@@ -706,16 +738,8 @@ __global__ void __launch_bounds__(32 * W + 32, W == 8 ? 3 : 10) k_distill(const 
                         send_for(row + step, c0, c0);
                     }
                 }
-                // the kept tokens, over what was just stored there
-                asm volatile("bar.sync 1, %0;" ::"n"(32 * W) : "memory");
-                if (!zero && ok) {
-                    for (int j = threadIdx.x; j < p.k; j += 32 * W) {
-                        const int cj = sm.col(b)[j];
-                        const int u = cj + pt.lo;      // element of the part
-                        if (cj >= 0 && u >= 0 && u < pt.n * E)
-                            dx[u] = Unit<T>::to(e_of(sm.x(b)[j], ref, p.c) * f_top - g * sm.p(b)[j]);
-                    }
-                }
+                asm volatile("bar.sync 1, %0;" ::"n"(32 * W) : "memory");      // what the other warps stored is there
+                if (ok) slope.kept(p, pt, sm, b, threadIdx.x, 32 * W);
             }
             if (MODE != FWD) {
                 __syncwarp();
@@ -726,6 +750,77 @@ __global__ void __launch_bounds__(32 * W + 32, W == 8 ? 3 : 10) k_distill(const 
     wait_group(0);
     __syncthreads();
     if (C > 1) cluster_sync();      // nobody leaves while its mail is written
+}
+
+// Small vocabularies: one warp does all of a row, the next row's logits on
+// their way meanwhile, and up to 28 rows are under way on an SM.  The chain of a
+// row's sums, which bounds them, has no barrier in it (16,384 x 1,000 bf16, loss and
+// gradient: 29 us, 54 by three warps with 10 rows an SM; 2,500 columns 58 and 75).
+constexpr int kWarpPerSm = 28;
+template <typename T, int MODE, bool TAIL>
+__global__ void __launch_bounds__(32, kWarpPerSm) k_distill_warp(const Params p) {
+    constexpr int E = Unit<T>::E;
+    extern __shared__ __align__(16) uint8_t smem[];
+    const Smem sm{smem, p.held, p.part, (p.k + 3) / 4 * 4};
+    Teacher& te = *reinterpret_cast<Teacher*>(sm.fixed());
+    const int lane = threadIdx.x;
+    const int64_t step = gridDim.x;
+    auto send_for = [&](int64_t row, int buf) {      // this lane's units of a row
+        if (row < p.M) {
+            const Part pt = part_of<T>(p, row, 0u);
+            const uint8_t* src = reinterpret_cast<const uint8_t*>(static_cast<const T*>(p.x) + row * p.ldx) -
+                                 pt.head * (int)sizeof(T);
+            const uint32_t dst = smem_u32(smem + 16 * buf * p.part);
+#pragma unroll 4
+            for (int u = lane; u < pt.n; u += 32)
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + 16 * u), "l"(src + 16 * (int64_t)u)
+                             : "memory");
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    for (int i = lane; i < bits_bytes(p.part) / 4; i += 32) reinterpret_cast<uint32_t*>(sm.bits(0))[i] = 0u;
+    __syncwarp();
+    wait_for_previous_kernels();
+    Ahead ah = {};
+    int buf = 0;
+    send_for(blockIdx.x, 0);
+    load_tokens<MODE, TAIL>(p, blockIdx.x, 0, lane, ah);
+    for (int64_t row = blockIdx.x; row < p.M; row += step, buf ^= 1) {
+        send_for(row + step, buf ^ 1);
+        const Part pt = part_of<T>(p, row, 0u);
+        teacher_row<T, MODE, TAIL>(p, sm, te, 0, row, row + step, 0u, lane, ah);
+        wait_group(1);
+        const uint8_t* rows = smem + 16 * buf * p.part;
+        float m, s, s_rest;
+        if constexpr (MODE != BWD) {
+            Sum sum;
+#pragma unroll 2
+            for (int u = lane; u < pt.n; u += 32) {
+                uint4 v = *reinterpret_cast<const uint4*>(rows + 16 * u);
+                uint32_t out = TAIL ? sm.bits(0)[u] : 0u;
+                if (u < pt.u0 || u >= pt.u1) out |= outside<E>(pt, u);
+                if (out) leave_out<E>(v, out);
+                sum.add<T, 1>(&v, p.c);
+            }
+            m = warp_max(sum.m);
+            if (TAIL) m = fmaxf(m, te.top_max);
+            const float ref = finite_max(m);
+            s_rest = warp_sum(sum.total() * e_of(sum.m, ref, p.c));
+            s = TAIL ? s_rest + te.top_sum * e_of(te.top_max, ref, p.c) : s_rest;
+            if (lane == 0) write_loss<TAIL>(p, row, te, m, s, s_rest);
+        } else {
+            m = te.m, s = te.s, s_rest = te.s_rest;
+        }
+        if constexpr (MODE != FWD) {
+            const Slope<T, TAIL> slope(p, pt, te, row, m, s, s_rest);
+            slope.units(pt, rows, lane, pt.n, 32);
+            __syncwarp();      // what the other lanes stored is there
+            slope.kept(p, pt, sm, 0, lane, 32);
+        }
+        __syncwarp();
+        if (TAIL || MODE != FWD) clear_bits<T>(p, sm, 0, pt, lane);
+    }
+    wait_group(0);
 }
 
 // ----------------------------------------------------------------- host ----
@@ -762,7 +857,8 @@ static cudaLaunchConfig_t launch_cfg(int64_t clusters, int C, bool wide, size_t 
 static cudaError_t set_attributes() {
     const int most = 232448;
 #define X(T, M, R)                                                                                             \
-    for (const void* k : {(const void*)k_distill<T, M, R, 2>, (const void*)k_distill<T, M, R, 8>}) {            \
+    for (const void* k :                                                                                       \
+         {(const void*)k_distill<T, M, R, 2>, (const void*)k_distill<T, M, R, 8>, (const void*)k_distill_warp<T, M, R>}) { \
         const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, most);       \
         if (e != cudaSuccess) return e;                                                                        \
     }
@@ -788,6 +884,32 @@ static Kernel kernel_of(bool f32, int mode, bool tail, bool wide) {
     MOE_DISTILL_INSTANCES(X)
 #undef X
     return nullptr;
+}
+static Kernel warp_kernel_of(bool f32, int mode, bool tail) {
+#define X(T, M, R) \
+    if (f32 == (sizeof(T) == 4) && mode == M && tail == R) return (Kernel)k_distill_warp<T, M, R>;
+    MOE_DISTILL_INSTANCES(X)
+#undef X
+    return nullptr;
+}
+
+// Rows of up to 320 16-byte units, more of them than a few for every SM: a warp each.
+constexpr int kWarpUnits = 320;
+static moe_status_t launch_warps(Params p, bool f32, int mode, int sms, cudaStream_t stream) {
+    const int E = f32 ? 4 : 8;
+    p.part = (E - 1 + p.V + E - 1) / E;
+    p.held = 2 * p.part;
+    const size_t smem = smem_bytes(p.held, p.part, p.k);
+    const int64_t per_sm = std::min<int64_t>(kWarpPerSm, kSmemSm / (smem + 1024));
+    const dim3 grid((unsigned)std::min<int64_t>(p.M, sms * per_sm));
+    if (launch_early(grid, 32, smem, stream, warp_kernel_of(f32, mode, p.lse != nullptr), p) != cudaSuccess)
+        return MOE_ERR_CUDA;
+    MOE_CHECK_LAUNCH();
+    return MOE_OK;
+}
+static bool warps_do(int64_t M, int V, bool f32, int sms) {
+    const int E = f32 ? 4 : 8;
+    return (E - 1 + V + E - 1) / E <= kWarpUnits && M > 4 * (int64_t)sms;
 }
 
 // How a call is spread: CTAs of a cluster (they share a row), 288 threads each
@@ -836,6 +958,7 @@ static Spread spread(int64_t M, int V, int elem, int k, int mode, int sms) {
 static moe_status_t launch(Params p, bool f32, int mode, cudaStream_t stream) {
     const int sms = device_sm_count();
     MOE_REQUIRE(sms > 0, MOE_ERR_NOT_INITIALIZED);
+    if (warps_do(p.M, p.V, f32, sms)) return launch_warps(p, f32, mode, sms, stream);
     const Spread d = spread(p.M, p.V, f32 ? 4 : 2, p.k, mode, sms);
     MOE_REQUIRE(d.C > 0, MOE_ERR_UNSUPPORTED);
     p.part = d.part, p.chunk = d.chunk, p.held = d.held;

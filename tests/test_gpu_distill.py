@@ -102,8 +102,10 @@ def check(ops, x, idx, t, lse, dloss, tau, dx=None):
 
 # (M, V, k): one element, one token kept, every token kept, one 16-byte unit and its neighbours, parts of a cluster,
 # odd rows, more rows than CTAs, wide
+# the last ones: a warp to a row, its longest rows, many tokens
 SIZES = [(1, 1, 1), (3, 8, 1), (5, 7, 7), (4, 9, 4), (2, 17, 20), (7, 256, 32), (300, 1000, 5), (1300, 130, 3), (5, 2047, 100),
-         (33, 4099, 17), (2, 32000, 64), (9, 50257, 20), (40, 36865, 33), (3, 129280, 128), (1, 262147, 1000)]
+         (33, 4099, 17), (2, 32000, 64), (9, 50257, 20), (40, 36865, 33), (3, 129280, 128), (1, 262147, 1000), (1500, 1, 1),
+         (700, 33, 40), (650, 1271, 129), (620, 2551, 16), (5000, 300, 7)]
 
 
 @pytest.mark.parametrize("m,v,k", SIZES)
@@ -137,7 +139,7 @@ def test_strides_and_addresses(ops, xt, pad, offset, dpad):
 
 
 @pytest.mark.parametrize("xt", [BF, F])
-@pytest.mark.parametrize("m,v", [(4, 40001), (200, 777)])
+@pytest.mark.parametrize("m,v", [(4, 40001), (200, 777), (2000, 777), (2000, 1000)])
 def test_in_place(ops, xt, m, v):
     x, idx, t, lse, dloss = example(m, v, 24, 4, xt, F, True)
     loss, d = ops.distill_loss(dloss, x, idx, t, lse)
