@@ -547,6 +547,35 @@ template <bool F32>
 struct WOut {
     uint32_t buf;
     int lane;
+    bool zeros;      // the box holds zeros, from an empty group's tile before
+    __device__ __forceinline__ void store(const CUtensorMap* map, int g, int row0, int col) {
+        asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(map),
+                     "r"(buf), "r"(col), "r"(row0), "r"(g)
+                     : "memory");
+        bulk_commit_group();
+    }
+    // an empty group's chunk: the box is filled once and stored as often as it is wanted
+    __device__ __forceinline__ void put_zeros(const Params& p, const CUtensorMap* map, int g, int row0, int col) {
+        const int cols = p.N - col;
+        if (cols < 32 && (cols & 7) != 0) {
+            const float v[32] = {};
+            put(p, map, g, row0, col, v);
+            return;
+        }
+        if (!zeros) {
+            if (lane == 0) bulk_wait_group_read0();
+            __syncwarp();
+#pragma unroll
+            for (int c = 0; c < 4; ++c) st_shared_v4(buf + 64u * lane + 16u * c, 0u, 0u, 0u, 0u);
+            fence_proxy_async_shared();
+            __syncwarp();
+            zeros = true;
+        }
+        if (lane == 0) {
+            store(map, g, row0, col);
+            if (F32 && cols > 16) store(map, g, row0, col + 16);
+        }
+    }
     __device__ __forceinline__ void put(const Params& p, const CUtensorMap* map, int g, int row0, int col,
                                         const float* v) {
         const int cols = p.N - col;
@@ -563,6 +592,7 @@ struct WOut {
             }
             return;
         }
+        zeros = false;
 #pragma unroll
         for (int h = 0; h < (F32 ? 2 : 1); ++h) {
             if (F32 && 16 * h >= cols) break;
@@ -582,12 +612,7 @@ struct WOut {
             }
             fence_proxy_async_shared();
             __syncwarp();
-            if (lane == 0) {
-                asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(map),
-                             "r"(buf), "r"(col + 16 * h), "r"(row0), "r"(g)
-                             : "memory");
-                bulk_commit_group();
-            }
+            if (lane == 0) store(map, g, row0, col + 16 * h);
         }
     }
 };
@@ -727,33 +752,32 @@ __device__ __forceinline__ void store_wgrad(const Place& pl, const Params& p, co
                                             int64_t t, Ring& acc) {
     const int lane = pl.lane, ew = pl.warp - 4, quarter = ew & 3, half = ew >> 2;
     const uint32_t lane_base = tmem_base + ((uint32_t)(quarter * 32) << 16);
-    WOut<F32> out{smem_u32(pl.smem + SMEM_WORK - (EPI_WARPS - ew) * W_BOX), lane};
+    WOut<F32> out{smem_u32(pl.smem + SMEM_WORK - (EPI_WARPS - ew) * W_BOX), lane, false};
     const int chunks = p.bn / 32, c0 = half == 0 ? 0 : (chunks + 1) / 2, c1 = half == 0 ? (chunks + 1) / 2 : chunks;
     for (; t < p.max_tiles; t += pl.step) {
         const WTile w = w_tile(p, t);
         const int row0 = w.mt * TM + 128 * (int)pl.rank + quarter * 32;
         const uint32_t tacc = lane_base + (uint32_t)(acc.at * ACC_COLS);
-        if (w.rows > 0) {
-            if (!__all_sync(0xFFFFFFFFu, mbar_wait_cluster(pl.tfull(acc.at), acc.phase, p, pl.abort_flag))) break;
-            tc_fence_after();
+        const int col0 = w.nt * p.bn;
+        if (w.rows == 0) {
+            for (int c = c0; c < c1; ++c)
+                if (col0 + 32 * c < p.N && row0 < p.K) out.put_zeros(p, tmD, w.g, row0, col0 + 32 * c);
+            continue;
         }
+        if (!__all_sync(0xFFFFFFFFu, mbar_wait_cluster(pl.tfull(acc.at), acc.phase, p, pl.abort_flag))) break;
+        tc_fence_after();
         for (int c = c0; c < c1; ++c) {
             float v[32];
-            if (w.rows > 0) {
-                tmem_ld32(tacc + 32 * c, v);
-                if (c + 1 == c1) {      // the accumulator is read: the next tile may have it
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive_remote(mapa(pl.tempty(acc.at), 0));
-                }
-            } else {
-#pragma unroll
-                for (int i = 0; i < 32; ++i) v[i] = 0.f;
+            tmem_ld32(tacc + 32 * c, v);
+            if (c + 1 == c1) {      // the accumulator is read: the next tile may have it
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_remote(mapa(pl.tempty(acc.at), 0));
             }
-            const int col = w.nt * p.bn + 32 * c;
+            const int col = col0 + 32 * c;
             if (col < p.N && row0 < p.K) out.put(p, tmD, w.g, row0, col, v);      // the whole warp
         }
-        if (w.rows > 0) acc.next(NACC);
+        acc.next(NACC);
     }
 }
 
@@ -920,13 +944,18 @@ constexpr int64_t kMaxTiles = 0x3FFFFFFF;
 // The fields of p that sizes decide, for D = x op(W) of x [M, depth]; the maps of x.
 template <bool GLU>
 static moe_status_t plan_rows(Params& p) {
+    const int cols = GLU ? 128 : 256;
+    p.col_tiles = (p.N + cols - 1) / cols;
     p.n_max = (int)std::min<int64_t>(256, (p.M + 31) / 32 * 32);
+    // Where even M rows in one group give fewer tiles than half of the pairs, tiles of
+    // fewer rows: a step of 64 rows takes half the time of one of 256 (428 rows, 1,589 x 432: 8.8 us, with
+    // 256 rows 13.0; gated 411 rows, 3,713 x 2 * 72: 18.1 and 27.6).
+    while (p.n_max > 64 && (p.M + p.n_max - 1) / p.n_max * p.col_tiles * 2 <= g_max_clusters)
+        p.n_max = (p.n_max / 2 + 31) / 32 * 32;
     int box = 16;      // rows of x per CTA that a stage has room for
     while (2 * box < p.n_max) box *= 2;
     p.stage_bytes = HALF_BYTES + box * TK * 2;
     p.nk = (p.K + TK - 1) / TK;
-    const int cols = GLU ? 128 : 256;
-    p.col_tiles = (p.N + cols - 1) / cols;
     p.max_tiles = (p.M / p.n_max + std::min<int64_t>(p.G, p.M)) * p.col_tiles;
     p.timeout_ns = 2000000000ull;
     return p.max_tiles <= kMaxTiles ? MOE_OK : MOE_ERR_UNSUPPORTED;
