@@ -1083,7 +1083,8 @@ MOE_API moe_status_t grouped_ffn_bwd(const void* dh, int64_t lddh, const void* a
  * All sums are fp32.  distill_loss_fwd writes loss and stats, those that are
  * not NULL; distill_loss_bwd dx from stats; distill_loss loss (may be NULL) and dx
  * with one read of x.  One launch each, no workspace; every sum has a fixed
- * order.  M = 0 does nothing.
+ * order (of its own in each call, and for rows that start elsewhere in their 16
+ * bytes).  M = 0 does nothing.
  */
 MOE_API moe_status_t distill_loss_fwd(const void* x, int x_type, int64_t ldx, const int32_t* idx, int64_t ldi,
                                       const void* t, int t_type, int64_t ldt, const float* teacher_lse, float tau,

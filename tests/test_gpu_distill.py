@@ -244,6 +244,39 @@ def test_student_that_is_sure(ops):
     assert np.allclose(np64(d), dx, rtol=2e-5, atol=1e-6)
 
 
+@pytest.mark.parametrize("v", [600, 5000])
+@pytest.mark.parametrize("xt", [BF, F])
+@pytest.mark.parametrize("tail", [False, True])
+def test_many_rows(ops, v, xt, tail):
+    """the forms for more rows than the GPU has SMs: repeated tokens, masked ones, bad ones,
+    rows without weight, padded rows at any element"""
+    M = 700
+    x, idx, t, lse, dloss = example(M, v, 24, 17, xt, F, tail, 1.0, 3, 1)
+    idx[0::7, 1::2] = idx[0::7, :1]
+    idx[3::7] = -1
+    t[4::7, 5:] = -torch.inf
+    x[5::7, 11:400:3] = torch.where(torch.isin(torch.arange(11, 400, 3, device="cuda"), idx[5::7]), x[5::7, 11:400:3], -torch.inf)
+    if tail:
+        lse = torch.logsumexp(torch.where(idx >= 0, t, -torch.inf), 1) + 0.2
+        lse = torch.where((idx >= 0).any(1), lse, 0.0)
+    buf = torch.full((M, v + 5), 7.0, dtype=xt, device="cuda")
+    check(ops, x, idx, t, lse, dloss, 1.0, dx=buf[:, :v])
+    assert bool((buf[:, v:] == 7.0).all())
+    y = x.contiguous()                                   # (rows that lie otherwise are summed in another order)
+    loss, d = ops.distill_loss(dloss, y, idx, t, lse)
+    bad, w = idx.clone(), dloss.clone()
+    bad[1, 1] = v                                        # taken as not kept
+    y[6], w[6] = float("nan"), 0.0
+    y[8, 3] = float("nan")
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    loss2, d2 = ops.distill_loss(w, y, bad, t, lse, dlogits=y, err=err)
+    assert int(err) == ops.MOE_ERR_BAD_INDEX and float(d2[6].abs().max()) == 0
+    assert bool(torch.isnan(loss2[8])) and bool(torch.isnan(d2[8]).any())
+    rest = torch.ones(M, dtype=torch.bool, device="cuda")
+    rest[[1, 6, 8]] = False
+    assert torch.equal(loss[rest], loss2[rest]) and torch.equal(d[rest], d2[rest])
+
+
 def test_nothing_to_do(ops):
     x = torch.empty((0, 100), dtype=BF, device="cuda")
     idx, t = torch.empty((0, 4), dtype=torch.int32, device="cuda"), torch.empty((0, 4), device="cuda")

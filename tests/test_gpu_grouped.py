@@ -277,6 +277,34 @@ def test_strides(ops, pad, gap):
                 product(dw[g], x[a:b].T, dy[a:b], "dw")
 
 
+@pytest.mark.parametrize("counts,k,n", [([30, 0, 200, 70], 300, 264), ([1500, 3, 0, 497], 4096, 5120)])
+def test_gradients_alone_and_together(ops, counts, k, n):
+    """in one launch (few steps), in two (many), or one of them: the same bits"""
+    gr = Groups(counts)
+    x, w, dy = mat(gr.M, k, 50), weights(gr.G, k, n, 51), mat(gr.M, n, 52)
+    dx, dw = ops.grouped_linear_bwd(dy, x, w, gr.offsets)
+    dx1, none = ops.grouped_linear_bwd(dy, x, w, gr.offsets, want_dw=False)
+    none1, dw1 = ops.grouped_linear_bwd(dy, x, w, gr.offsets, want_dx=False)
+    assert none is None and none1 is None and torch.equal(dx, dx1) and torch.equal(dw, dw1)
+    for g, a, b in gr.spans:
+        if b > a:
+            product(dx[a:b], dy[a:b], w[g].T, "dx")
+            product(dw[g], x[a:b].T, dy[a:b], "dw")
+        else:
+            assert float(dw[g].abs().max()) == 0
+
+
+@pytest.mark.parametrize("m,k,n", [(411, 700, 72), (428, 333, 432), (64, 2000, 512), (100, 100, 3000), (129, 64, 64)])
+def test_few_tiles(ops, m, k, n):
+    """one group with fewer tiles than SMs: narrower ones"""
+    gr = Groups([m])
+    x, w = mat(m, k, 53), weights(1, k, n, 54)
+    product(ops.grouped_linear_fwd(x, w, gr.offsets), x, w[0], "y")
+    w1 = weights(1, k, 2 * n, 55, std=2.0 / math.sqrt(k))
+    h, a = ops.grouped_ffn_fwd(x, w1, gr.offsets, want_a=True)
+    ffn_check(h, a, x, w1[0], "silu", "gated")
+
+
 def test_more_groups_than_rows(ops):
     G, k, n = 5000, 40, 24
     counts = [0] * G
