@@ -52,7 +52,9 @@ using namespace dense;
 constexpr int ACC_COLS = 256;                   // TMEM columns of an accumulator
 constexpr int NACC = 2;
 constexpr int HALF_BYTES = 128 * TK * 2;        // one CTA's 128 rows of an operand per stage
-constexpr int MAX_STAGES = 10;
+// six of 32 KB; eight of 18 KB where rows are few (32 experts' gated projections, 7,168 x
+// 2 * 2,048, a row each: 259 us, with six or ten 263 and 267)
+constexpr int MAX_STAGES = 8;
 constexpr int SMEM_WORK = 14 * HALF_BYTES;      // stages, then the epilogue's boxes
 constexpr int OFF_BAR = SMEM_WORK;              // full[S], empty[S], tfull[A], tempty[A], xfull[4], xempty[4], drain
 constexpr int NBAR = 2 * MAX_STAGES + 2 * NACC + 9;
@@ -390,18 +392,16 @@ template <bool GLU, int ACT, int BOXES>
 __device__ __forceinline__ bool store_rows(const Place& pl, const Params& p, const CUtensorMap* tmY,
                                            const CUtensorMap* tmA, const CUtensorMap* tmA2, uint32_t tmem_base,
                                            Cursor& cur, int64_t& t, Ring& acc) {
-    constexpr int EPI_STAGE = 2048 * BOXES + (GLU ? 4096 : 0);      // GLU: gate's way to up
     Tile ti;
     const int lane = pl.lane, ew = pl.warp - 4, quarter = ew & 3, half = ew >> 2;
     const uint32_t lane_base = tmem_base + ((uint32_t)(quarter * 32) << 16);
-    const uint32_t stage = smem_u32(pl.smem + SMEM_WORK - (EPI_WARPS - ew) * EPI_STAGE);
+    const uint32_t stage = smem_u32(pl.smem + SMEM_WORK - (EPI_WARPS - ew) * 2048 * BOXES);
     Out<BOXES> out{stage, lane, 0u};
     // GLU: lanes 0..63 hold gate columns, 64..127 the up columns of the same h;
     // the gate warp hands act(gate) in fp32 to the up warp two quarters on
     const bool gate = GLU && quarter < 2;
     const int pair = (quarter & 1) + 2 * half;
-    const uint32_t to_up = smem_u32(pl.smem + SMEM_WORK - (EPI_WARPS - (quarter & 1) - 4 * half) * EPI_STAGE + 4096) +
-                           16u * lane;
+    const uint32_t to_up = smem_u32(pl.smem + SMEM_WORK - EPI_WARPS * 2048 * BOXES - (4 - pair) * 4096) + 16u * lane;
     uint32_t handed = 0;
     bool ok = true;
     for (; ok && cur.find(p, t, lane, ti); t += pl.step) {
@@ -515,7 +515,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         multiply_rows<W_MN>(pl, p, tmem_base, cur, t, ring, acc);
         products_end(pl, p, ring);
     } else if (pl.warp >= 4) {
-        store_rows<GLU, ACT, 2>(pl, p, &tmY, &tmA, &tmA2, tmem_base, cur, t, acc);
+        store_rows<GLU, ACT, GLU ? 1 : 2>(pl, p, &tmY, &tmA, &tmA2, tmem_base, cur, t, acc);
         stores_end(pl.lane);
     }
     tear_down(pl, tmem_base);
@@ -973,7 +973,8 @@ static moe_status_t product_rows(const Mat& x, const Mat& w, Params p, cudaStrea
     MOE_REQUIRE(g_max_clusters > 0, MOE_ERR_NOT_INITIALIZED);
     const moe_status_t st = plan_rows<GLU>(p);
     if (st != MOE_OK) return st;
-    p.stages = std::min(MAX_STAGES, (SMEM_WORK - EPI_WARPS * (GLU ? 8192 : 4096)) / p.stage_bytes);
+    // eight warps' boxes (GLU: half as many, and four gate warps' way to up)
+    p.stages = std::min(MAX_STAGES, (SMEM_WORK - EPI_WARPS * 4096) / p.stage_bytes);
     CUtensorMap tmW, tmX[4], tmY, tmA, tmA2;
     bool ok = make_bf16_map3(&tmW, w.p, p.G, w.rows, w.cols, w.ld, w.gs, W_MN ? TK : 128) && rows_maps(tmX, &tmY, x, p);
     tmA = tmA2 = tmY;
