@@ -922,11 +922,26 @@ def _size_groups(fn, x, w):
     _need(fn, isinstance(x, torch.Tensor) and x.dim() == 2 and isinstance(w, torch.Tensor) and w.dim() == 3)
 
 
-def grouped_linear_fwd(x, w, offsets, rows=None, y=None, err=None, stream=None):
+def grouped_workspace_size(G: int) -> int:
+    """Bytes of the workspace `ws` of the calls over G groups: none, as each
+    CTA pair works out its tiles from the offsets; -1 for a G that they refuse."""
+    return 0 if 1 <= G <= 65536 else -1
+
+
+def _groups_ws(fn, ws, x):
+    """ws as for the dense operators' calls: bytes on x's device."""
+    _need(fn, isinstance(ws, torch.Tensor) and isinstance(x, torch.Tensor) and ws.dtype == torch.uint8 and
+          ws.device == x.device)
+
+
+def grouped_linear_fwd(x, w, offsets, rows=None, y=None, err=None, stream=None, ws=None):
     """y[r] = x[r] w[g] for the rows r of every group g (bf16; w [G, K, N]):
     offsets[g] .. offsets[g + 1], or rows[g] of them (int32 device tensors).
-    Rows of no group are not written.  See include/moe.h.  Returns y."""
+    Rows of no group are not written.  ws may be left out: it needs no bytes
+    (grouped_workspace_size).  See include/moe.h.  Returns y."""
     fn = "grouped_linear_fwd"
+    if ws is not None:
+        _groups_ws(fn, ws, x)
     if y is None:
         _size_groups(fn, x, w)
         y = _new_rows(x.shape[0], w.shape[2], torch.bfloat16, x, stream)
@@ -937,10 +952,12 @@ def grouped_linear_fwd(x, w, offsets, rows=None, y=None, err=None, stream=None):
 
 
 def grouped_linear_bwd(dy, x, w, offsets, rows=None, want_dx=True, want_dw=True, dx=None, dw=None,
-                       dw_dtype=torch.bfloat16, err=None, stream=None):
+                       dw_dtype=torch.bfloat16, err=None, stream=None, ws=None):
     """Gradients of grouped_linear_fwd: dx and dw [G, K, N] (bfloat16 or float32),
-    those that are wanted or given.  See include/moe.h.  Returns (dx, dw)."""
+    those that are wanted or given; ws as there.  See include/moe.h.  Returns (dx, dw)."""
     fn = "grouped_linear_bwd"
+    if ws is not None:
+        _groups_ws(fn, ws, x)
     if (want_dx and dx is None) or (want_dw and dw is None):
         _size_groups(fn, x, w)
         if want_dx and dx is None:
@@ -953,11 +970,14 @@ def grouped_linear_bwd(dy, x, w, offsets, rows=None, want_dx=True, want_dw=True,
     return dx, dw
 
 
-def grouped_ffn_fwd(x, w1, offsets, rows=None, act="silu", h=None, a=None, want_a=False, err=None, stream=None):
+def grouped_ffn_fwd(x, w1, offsets, rows=None, act="silu", h=None, a=None, want_a=False, err=None, stream=None,
+                    ws=None):
     """[gate | up] = x[r] w1[g], h = act(gate) * up for the rows r of every group
-    g in one kernel (bf16; w1 [G, d, 2f]).  See include/moe.h.  Returns h, or
-    (h, a) when a = [gate | up] is asked for."""
+    g in one kernel (bf16; w1 [G, d, 2f]); ws as for grouped_linear_fwd.  See
+    include/moe.h.  Returns h, or (h, a) when a = [gate | up] is asked for."""
     fn = "grouped_ffn_fwd"
+    if ws is not None:
+        _groups_ws(fn, ws, x)
     if h is None or (want_a and a is None):
         _size_groups(fn, x, w1)
         M, f2 = x.shape[0], w1.shape[2]
@@ -970,11 +990,13 @@ def grouped_ffn_fwd(x, w1, offsets, rows=None, act="silu", h=None, a=None, want_
 
 
 def grouped_ffn_bwd(dh, a, x, w1, offsets, rows=None, act="silu", want_dx=True, want_dw=True, dx=None, dw1=None, da=None,
-                    dw_dtype=torch.bfloat16, err=None, stream=None):
+                    dw_dtype=torch.bfloat16, err=None, stream=None, ws=None):
     """Gradients of grouped_ffn_fwd from the kept a: dx and dw1 (bfloat16 or
-    float32); da [M, 2f] is written on the way (may be a itself).  See
-    include/moe.h.  Returns (dx, dw1)."""
+    float32); da [M, 2f] is written on the way (may be a itself); ws as for
+    grouped_linear_fwd.  See include/moe.h.  Returns (dx, dw1)."""
     fn = "grouped_ffn_bwd"
+    if ws is not None:
+        _groups_ws(fn, ws, x)
     if da is None or (want_dx and dx is None) or (want_dw and dw1 is None):
         _size_groups(fn, x, w1)
         da = da if da is not None else _new_rows(x.shape[0], w1.shape[2], torch.bfloat16, x, stream)
