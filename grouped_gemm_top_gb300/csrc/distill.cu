@@ -11,7 +11,8 @@
 // sum is s_rest: loss gains rest (log rest - log(s_rest / s)) and the other
 // tokens' dx lose dloss tau rest e_i / s_rest.  s_rest is summed over those
 // tokens themselves (a bit per token says which were kept): as s - sum of the
-// kept it would be lost where the student is sure of them.
+// kept it would be lost where the student is sure of them.  Its terms are relative to
+// the others' own maximum: relative to max x they would all be zero 87 tau below it.
 //
 // Loss and gradient together read the logits once: a row's parts lie in the
 // shared memory of a cluster's CTAs, whose maxima and sums are exchanged
@@ -59,7 +60,7 @@ struct Params {
     const float* lse;         // teacher's, or NULL
     const float* dloss;
     float* loss;
-    float* stats;             // [M, 3]: max x, s, s_rest; BWD: read
+    float* stats;             // [M, 3]: see put_stats; BWD: read
     int64_t M;
     int V, k;
     float tau, inv_tau, c;    // c = log2(e) / tau
@@ -73,7 +74,7 @@ struct Teacher {
     float mass, rest, p_sum;        // mass = sum p + rest
     float fit, x_ref, t_lse;        // sum p ((t - max t) - (x - x_ref) / tau); log-sum-exp of t - max t
     float top_max, top_sum;         // of the kept tokens in this CTA's part
-    float dloss, m, s, s_rest;      // of the row (BWD: what the forward pass kept)
+    float dloss, stats[3];          // of the row (BWD: what the forward pass kept)
     int some;                       // 0: no teacher, loss and gradient are zero
 };
 
@@ -92,7 +93,7 @@ struct Smem {
 };
 struct Fixed {
     unsigned long long bar[6];
-    float4 mail[2][MAX_C];          // max, s, s_rest of the cluster's parts
+    float4 mail[2][MAX_C];          // of the cluster's parts, see Sums: m, s, or kept m, s, the others' m, s
     float2 warp_part[2][8];
     Teacher teacher[2];
     int abort_flag;
@@ -313,7 +314,7 @@ __device__ __forceinline__ float warp_sum(float v) {
 struct Ahead {
     int i[4];
     uint32_t t[4];
-    float lse, dloss, m, s, s_rest;
+    float lse, dloss, stats[3];
 };
 template <int MODE, bool TAIL>
 __device__ __forceinline__ void load_tokens(const Params& p, int64_t row, int j0, int lane, Ahead& a) {
@@ -330,7 +331,8 @@ __device__ __forceinline__ void load_tokens(const Params& p, int64_t row, int j0
     if (row < p.M && j0 == 0) {
         if (TAIL) a.lse = p.lse[row];
         if (MODE != FWD) a.dloss = p.dloss[row];
-        if (MODE == BWD) a.m = p.stats[3 * row], a.s = p.stats[3 * row + 1], a.s_rest = p.stats[3 * row + 2];
+        if (MODE == BWD)
+            for (int i = 0; i < 3; ++i) a.stats[i] = p.stats[3 * row + i];
     }
 }
 // of the tokens in this CTA's part; the first CTA, which works out the loss, of all
@@ -385,7 +387,10 @@ __device__ __forceinline__ void teacher_row(const Params& p, const Smem& sm, Tea
             t_max = fmaxf(t_max, t);
         }
     }
-    if (lane == 0 && MODE != FWD) out.dloss = ah.dloss, out.m = ah.m, out.s = ah.s, out.s_rest = ah.s_rest;
+    if (lane == 0 && MODE != FWD) {
+        out.dloss = ah.dloss;
+        for (int i = 0; i < 3; ++i) out.stats[i] = ah.stats[i];
+    }
     const float row_lse = ah.lse;
     load_tokens<MODE, TAIL>(p, next, 0, lane, ah);
     any = __any_sync(0xFFFFFFFFu, any);
@@ -467,14 +472,61 @@ __device__ __forceinline__ void clear_bits(const Params& p, const Smem& sm, int 
     __syncwarp();
 }
 
-// The row's loss, and what the backward pass needs, from the sums over it.
+// Sums over a row of exp((x - maximum) / tau): over all tokens, and over those that were
+// not kept with a maximum of their own (TAIL).
+struct Sums {
+    float m, s, m_rest, s_rest;
+};
+// the sums from those of the kept tokens and of the others
+__device__ __forceinline__ Sums joined(float m_top, float s_top, float m_rest, float s_rest, float c) {
+    const float m = fmaxf(m_top, m_rest), ref = finite_max(m);
+    return {m, s_top * e_of(m_top, ref, c) + s_rest * e_of(m_rest, ref, c), m_rest, s_rest};
+}
+
+// What the loss and the gradient go by.  The others' part of q, q_rest, counts as none
+// below e^-700: a maximum of the type's lowest value is a mask.  Below e^-40 the
+// student is `sure`: the others' gradient is then that of rest alone (what mass
+// adds to it, q_rest / rest of it, is less than a rounding as rest is at least 2^-24),
+// taken relative to their own maximum, so that rest / s_rest does not overflow.
+constexpr float kNoRest = -700.f, kSure = -40.f;
+struct View {
+    float m, s;               // maximum and sum, for the kept tokens (not sure: for all)
+    float m_rest, s_rest;     // for the others; s_rest = 0: none; not sure: relative to m
+    float log_rest;           // log q_rest
+    bool sure;
+};
 template <bool TAIL>
-__device__ __forceinline__ void write_loss(const Params& p, int64_t row, const Teacher& te, float m, float s,
-                                           float s_rest) {
-    if (p.stats) p.stats[3 * row] = m, p.stats[3 * row + 1] = s, p.stats[3 * row + 2] = s_rest;
+__device__ __forceinline__ View view_of(const Params& p, const Sums& r) {
+    View v{r.m, r.s, r.m, r.s, 0.f, false};
+    if (TAIL) {
+        v.log_rest = (r.m_rest - r.m) * p.inv_tau + logf(r.s_rest) - logf(r.s);
+        const bool some = r.s_rest > 0.f && v.log_rest >= kNoRest;
+        v.sure = some && v.log_rest < kSure;
+        v.m_rest = v.sure ? r.m_rest : r.m;
+        v.s_rest = !some ? 0.f : (v.sure ? r.s_rest : r.s_rest * e_of(r.m_rest, finite_max(r.m), p.c));
+    }
+    return v;
+}
+// The view in three numbers: m, s, s_rest, or, of a student who is sure, the kept
+// tokens' log-sum-exp (tau of it, in the logits' scale), minus s_rest, m_rest.
+__device__ __forceinline__ void put_stats(const Params& p, float* out, const View& v) {
+    out[0] = v.sure ? v.m + p.tau * logf(v.s) : v.m;
+    out[1] = v.sure ? -v.s_rest : v.s;
+    out[2] = v.sure ? v.m_rest : v.s_rest;
+}
+template <bool TAIL>
+__device__ __forceinline__ View view_of_stats(const float* st) {
+    if (TAIL && st[1] < 0.f) return {st[0], 1.f, st[2], -st[1], 0.f, true};
+    return {st[0], st[1], st[0], st[2], 0.f, false};
+}
+
+// The row's loss, and what the backward pass needs.
+template <bool TAIL>
+__device__ __forceinline__ void write_loss(const Params& p, int64_t row, const Teacher& te, const View& v) {
+    if (p.stats) put_stats(p, p.stats + 3 * row, v);
     if (p.loss) {
-        float loss = te.fit + te.p_sum * ((finite_max(m) - te.x_ref) * p.inv_tau + logf(s) - te.t_lse);
-        if (TAIL && te.rest > 0.f && s_rest > 0.f) loss += te.rest * (logf(te.rest) - logf(s_rest / s));
+        float loss = te.fit + te.p_sum * ((finite_max(v.m) - te.x_ref) * p.inv_tau + logf(v.s) - te.t_lse);
+        if (TAIL && te.rest > 0.f && v.s_rest > 0.f) loss += te.rest * (logf(te.rest) - v.log_rest);
         p.loss[row] = te.some ? loss * p.tau * p.tau : 0.f;
     }
 }
@@ -488,16 +540,17 @@ struct Slope {
     f2 neg2, f2_all, c2;
     bool zero, vec;
     T* dx;      // element 0 of the part
-    __device__ __forceinline__ Slope(const Params& p, const Part& pt, const Teacher& te, int64_t row, float m, float s,
-                                     float s_rest) {
+    __device__ __forceinline__ Slope(const Params& p, const Part& pt, const Teacher& te, int64_t row, const View& v) {
         g = te.dloss * p.tau;
         zero = !te.some || g == 0.f;
-        const bool with_rest = TAIL && te.rest > 0.f && s_rest > 0.f;
+        const bool with_rest = TAIL && te.rest > 0.f && v.s_rest > 0.f;
         const float mass = with_rest ? te.mass : te.p_sum;
-        f_top = g * (mass / s);
-        const float f_all = with_rest ? g * (mass / s - te.rest / s_rest) : f_top;
-        ref = finite_max(m), c = p.c;
-        neg2 = pack(-ref, -ref), f2_all = pack(f_all, f_all), c2 = pack(c, c);
+        f_top = g * (mass / v.s);
+        const bool alone = with_rest && v.sure;      // the others have rest alone
+        const float f_all = with_rest ? g * ((alone ? 0.f : mass / v.s) - te.rest / v.s_rest) : f_top;
+        ref = finite_max(v.m), c = p.c;
+        const float ref_all = alone ? v.m_rest : ref;
+        neg2 = pack(-ref_all, -ref_all), f2_all = pack(f_all, f_all), c2 = pack(c, c);
         dx = static_cast<T*>(p.dx) + row * p.lddx - pt.head + (int64_t)pt.g0 * E;
         vec = (reinterpret_cast<uintptr_t>(dx) & 15) == 0;
     }
@@ -568,16 +621,19 @@ __global__ void __launch_bounds__(32 * W + 32, W == 8 ? 3 : 10) k_distill(const 
     const int64_t row0 = blockIdx.x / C, step = gridDim.x / C;
 
     // the row's maximum and sums from the parts'
-    auto gather_mail = [&](int b, float& m, float& s, float& s_rest) {
-        m = -INFINITY, s = 0.f, s_rest = 0.f;
-        for (int i = 0; i < (int)C; ++i) m = fmaxf(m, fx.mail[b][i].x);
-        const float ref = finite_max(m);
+    auto gather_mail = [&](int b) {
+        float m = -INFINITY, m_rest = -INFINITY, s = 0.f, s_rest = 0.f;
+        for (int i = 0; i < (int)C; ++i) {
+            m = fmaxf(m, fx.mail[b][i].x);
+            if (TAIL) m_rest = fmaxf(m_rest, fx.mail[b][i].z);
+        }
+        const float ref = finite_max(m), ref_rest = finite_max(m_rest);
         for (int i = 0; i < (int)C; ++i) {
             const float4 v = fx.mail[b][i];
-            const float f = e_of(v.x, ref, p.c);
-            s += v.y * f;
-            s_rest += v.z * f;
+            s += v.y * e_of(v.x, ref, p.c);
+            if (TAIL) s_rest += v.w * e_of(v.z, ref_rest, p.c);
         }
+        return TAIL ? joined(m, s, m_rest, s_rest, p.c) : Sums{m, s, m, s};
     };
     if (warp == W) {
         // ---------------------------------------------- teacher, a row ahead ----
@@ -637,7 +693,7 @@ __global__ void __launch_bounds__(32 * W + 32, W == 8 ? 3 : 10) k_distill(const 
             const Teacher& te = fx.teacher[b];
             // which of a unit's tokens were kept has to be known before the sums
             if (TAIL || MODE == BWD) ok = ok && mbar_wait(tfull(b), buf_phase, p, abort_flag);
-            float m = 0.f, s = 1.f, s_rest = 1.f;
+            View view{0.f, 1.f, 0.f, 1.f, 0.f, false};
             if constexpr (MODE != BWD) {
                 // -------------------------------- maximum and sum ----
                 const uint8_t* bits = sm.bits(b);
@@ -686,13 +742,13 @@ __global__ void __launch_bounds__(32 * W + 32, W == 8 ? 3 : 10) k_distill(const 
                 if (warp == 0) {      // this CTA's sums, to every CTA that goes on with them
                     if (!TAIL) ok = ok && mbar_wait(tfull(b), buf_phase, p, abort_flag);
                     const float2* part = fx.warp_part[it & 1];
-                    float cm = te.top_max, rest = 0.f;
+                    float cm = -INFINITY, cs = 0.f;
 #pragma unroll
                     for (int w = 0; w < W; ++w) cm = fmaxf(cm, part[w].x);
                     const float ref = finite_max(cm);
 #pragma unroll
-                    for (int w = 0; w < W; ++w) rest += part[w].y * e_of(part[w].x, ref, p.c);
-                    const float all = TAIL ? rest + te.top_sum * e_of(te.top_max, ref, p.c) : rest;
+                    for (int w = 0; w < W; ++w) cs += part[w].y * e_of(part[w].x, ref, p.c);
+                    const float4 v = TAIL ? make_float4(te.top_max, te.top_sum, cm, cs) : make_float4(cm, cs, 0.f, 0.f);
                     // the bytes themselves count on the barriers: a release at cluster scope
                     // would wait for every store of this warp, 1 to 2 us a row
                     if (lane == 0 && ok) mbar_expect_tx(xbar(b), 16u * C);
@@ -700,31 +756,28 @@ __global__ void __launch_bounds__(32 * W + 32, W == 8 ? 3 : 10) k_distill(const 
                         asm volatile(
                             "st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(
                                 mapa(smem_u32(&fx.mail[b][rank]), (uint32_t)lane)),
-                            "f"(cm), "f"(all), "f"(rest), "f"(0.f), "r"(mapa(xbar(b), (uint32_t)lane))
+                            "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w), "r"(mapa(xbar(b), (uint32_t)lane))
                             : "memory");
                 }
                 if (MODE == FWD) {      // the other warps go on to the next row
                     if (warp == 0) {
                         ok = __all_sync(0xFFFFFFFFu, ok && mbar_wait(xbar(b), buf_phase, p, abort_flag));
-                        if (rank == 0 && lane == 0 && ok) {
-                            gather_mail(b, m, s, s_rest);
-                            write_loss<TAIL>(p, row, te, m, s, s_rest);
-                        }
+                        if (rank == 0 && lane == 0 && ok) write_loss<TAIL>(p, row, te, view_of<TAIL>(p, gather_mail(b)));
                         __syncwarp();
                         if (lane == 0) mbar_arrive(tempty(b));
                     }
                 } else {
                     if (!TAIL) ok = ok && mbar_wait(tfull(b), buf_phase, p, abort_flag);
                     ok = ok && mbar_wait(xbar(b), buf_phase, p, abort_flag);
-                    gather_mail(b, m, s, s_rest);
-                    if (rank == 0 && threadIdx.x == 0 && ok) write_loss<TAIL>(p, row, te, m, s, s_rest);
+                    view = view_of<TAIL>(p, gather_mail(b));
+                    if (rank == 0 && threadIdx.x == 0 && ok) write_loss<TAIL>(p, row, te, view);
                 }
             } else {
-                m = te.m, s = te.s, s_rest = te.s_rest;
+                view = view_of_stats<TAIL>(te.stats);
             }
             if constexpr (MODE != FWD) {
                 // ------------------------------------------ gradient ----
-                const Slope<T, TAIL> slope(p, pt, te, row, m, s, s_rest);
+                const Slope<T, TAIL> slope(p, pt, te, row, view);
 #pragma unroll 1
                 for (int c0 = 0, ch = 0; STREAM ? c0 < p.part : ch < CHUNKS; c0 += p.chunk, ++ch) {
                     if (STREAM) wait_group(CHUNKS - 1);
@@ -791,7 +844,7 @@ __global__ void __launch_bounds__(32, kWarpPerSm) k_distill_warp(const Params p)
         teacher_row<T, MODE, TAIL>(p, sm, te, 0, row, row + step, 0u, lane, ah);
         wait_group(1);
         const uint8_t* rows = smem + 16 * buf * p.part;
-        float m, s, s_rest;
+        View view;
         if constexpr (MODE != BWD) {
             Sum sum;
 #pragma unroll 2
@@ -802,17 +855,14 @@ __global__ void __launch_bounds__(32, kWarpPerSm) k_distill_warp(const Params p)
                 if (out) leave_out<E>(v, out);
                 sum.add<T, 1>(&v, p.c);
             }
-            m = warp_max(sum.m);
-            if (TAIL) m = fmaxf(m, te.top_max);
-            const float ref = finite_max(m);
-            s_rest = warp_sum(sum.total() * e_of(sum.m, ref, p.c));
-            s = TAIL ? s_rest + te.top_sum * e_of(te.top_max, ref, p.c) : s_rest;
-            if (lane == 0) write_loss<TAIL>(p, row, te, m, s, s_rest);
+            const float m = warp_max(sum.m), s = warp_sum(sum.total() * e_of(sum.m, finite_max(m), p.c));
+            view = view_of<TAIL>(p, TAIL ? joined(te.top_max, te.top_sum, m, s, p.c) : Sums{m, s, m, s});
+            if (lane == 0) write_loss<TAIL>(p, row, te, view);
         } else {
-            m = te.m, s = te.s, s_rest = te.s_rest;
+            view = view_of_stats<TAIL>(te.stats);
         }
         if constexpr (MODE != FWD) {
-            const Slope<T, TAIL> slope(p, pt, te, row, m, s, s_rest);
+            const Slope<T, TAIL> slope(p, pt, te, row, view);
             slope.units(pt, rows, lane, pt.n, 32);
             __syncwarp();      // what the other lanes stored is there
             slope.kept(p, pt, sm, 0, lane, 32);
