@@ -73,6 +73,7 @@ struct Params {
 struct Teacher {
     float mass, rest, p_sum;        // mass = sum p + rest
     float fit, x_ref, t_lse;        // sum p ((t - max t) - (x - x_ref) / tau); log-sum-exp of t - max t
+    float again;                    // tokens of this CTA's part that occur several times: what the loss gains, P log P - sum p log p
     float top_max, top_sum;         // of the kept tokens in this CTA's part
     float dloss, stats[3];          // of the row (BWD: what the forward pass kept)
     int some;                       // 0: no teacher, loss and gradient are zero
@@ -93,6 +94,7 @@ struct Smem {
 };
 struct Fixed {
     unsigned long long bar[6];
+    float again[2][MAX_C];          // (the first CTA's) of the cluster's parts
     float4 mail[2][MAX_C];          // of the cluster's parts, see Sums: m, s, or kept m, s, the others' m, s
     float2 warp_part[2][8];
     Teacher teacher[2];
@@ -348,6 +350,8 @@ __device__ __forceinline__ void load_logits(const Params& p, int64_t row, uint32
     }
 }
 
+__device__ __forceinline__ float p_log_p(float p) { return p == 0.f ? 0.f : p * logf(p); }
+
 // The teacher's row (one warp): probabilities, what the loss needs of them,
 // and, of the tokens in this CTA's part, their bits, sums and logits.
 template <typename T, int MODE, bool TAIL>
@@ -375,7 +379,7 @@ __device__ __forceinline__ void teacher_row(const Params& p, const Smem& sm, Tea
             if (ok) {
                 any = true;
                 const int u = i + pt.head, g = u / E - pt.g0;
-                if (g >= 0 && g < pt.n && (TAIL || MODE != FWD)) {
+                if (g >= 0 && g < pt.n) {
                     const uint32_t bit = 1u << (8 * (g & 3) + u % E);
                     dup |= (atomicOr(words + (g >> 2), bit) & bit) != 0;
                 }
@@ -420,20 +424,32 @@ __device__ __forceinline__ void teacher_row(const Params& p, const Smem& sm, Tea
     }
     warp_sum2(mass, fit);
     __syncwarp();
+    float again = 0.f;
     if (dup) {      // the first of several holds the sum of their probabilities
         for (int j = lane; j < p.k; j += 32) {
             const int cj = col[j];
             if (cj == -1) continue;
             bool first = true;
-            float q = pr[j];
+            int others = 0;
+            float q = pr[j], apart = MODE != BWD ? p_log_p(q) : 0.f;
             for (int i = 0; i < p.k; ++i) {
                 if (i == j || col[i] == -1 || (col[i] & 0x7FFFFFFF) != cj) continue;
-                if (i < j) first = false;
-                else q += pr[i];
+                if (i < j) {
+                    first = false;
+                } else {
+                    q += pr[i], ++others;
+                    if (MODE != BWD) apart += p_log_p(pr[i]);
+                }
             }
-            if (first) pr[j] = q;
-            else col[j] = cj | (int)0x80000000;
+            if (first) {
+                pr[j] = q;
+                const int g = (cj + pt.head) / E - pt.g0;
+                if (MODE != BWD && others > 0 && g >= 0 && g < pt.n) again += p_log_p(q) - apart;
+            } else {
+                col[j] = cj | (int)0x80000000;
+            }
         }
+        if (MODE != BWD) again = warp_sum(again);
         __syncwarp();
     }
     float top_max = -INFINITY, top_sum = 0.f;
@@ -453,7 +469,7 @@ __device__ __forceinline__ void teacher_row(const Params& p, const Smem& sm, Tea
         out.rest = TAIL && some ? fmaxf(1.f - mass, 0.f) : 0.f;
         out.p_sum = mass;
         out.mass = mass + out.rest;
-        out.fit = fit, out.x_ref = x_ref, out.t_lse = t_lse;
+        out.fit = fit, out.x_ref = x_ref, out.t_lse = t_lse, out.again = again;
         out.top_max = top_max, out.top_sum = top_sum;
         out.some = some;
     }
@@ -522,10 +538,11 @@ __device__ __forceinline__ View view_of_stats(const float* st) {
 
 // The row's loss, and what the backward pass needs.
 template <bool TAIL>
-__device__ __forceinline__ void write_loss(const Params& p, int64_t row, const Teacher& te, const View& v) {
+__device__ __forceinline__ void write_loss(const Params& p, int64_t row, const Teacher& te, const View& v,
+                                           float again) {
     if (p.stats) put_stats(p, p.stats + 3 * row, v);
     if (p.loss) {
-        float loss = te.fit + te.p_sum * ((finite_max(v.m) - te.x_ref) * p.inv_tau + logf(v.s) - te.t_lse);
+        float loss = te.fit + again + te.p_sum * ((finite_max(v.m) - te.x_ref) * p.inv_tau + logf(v.s) - te.t_lse);
         if (TAIL && te.rest > 0.f && v.s_rest > 0.f) loss += te.rest * (logf(te.rest) - v.log_rest);
         p.loss[row] = te.some ? loss * p.tau * p.tau : 0.f;
     }
@@ -635,19 +652,22 @@ __global__ void __launch_bounds__(32 * W + 32, W == 8 ? 3 : 10) k_distill(const 
         }
         return TAIL ? joined(m, s, m_rest, s_rest, p.c) : Sums{m, s, m, s};
     };
+    auto gather_again = [&](int b) {
+        float sum = 0.f;
+        for (int i = 0; i < (int)C; ++i) sum += fx.again[b][i];
+        return sum;
+    };
     if (warp == W) {
         // ---------------------------------------------- teacher, a row ahead ----
-        if (TAIL || MODE != FWD) {
-            for (int i = lane; i < bits_bytes(p.part) / 2; i += 32) reinterpret_cast<uint32_t*>(sm.bits(0))[i] = 0u;
-            __syncwarp();
-        }
+        for (int i = lane; i < bits_bytes(p.part) / 2; i += 32) reinterpret_cast<uint32_t*>(sm.bits(0))[i] = 0u;
+        __syncwarp();
         int it = 0;
         Ahead ah = {};
         load_tokens<MODE, TAIL>(p, row0, 0, lane, ah);
         for (int64_t row = row0; row < p.M; row += step, ++it) {
             const int b = it & 1;
             if (!__all_sync(0xFFFFFFFFu, mbar_wait(tempty(b), (uint32_t)(it >> 1 & 1) ^ 1u, p, abort_flag))) break;
-            if (it >= 2 && (TAIL || MODE != FWD)) clear_bits<T>(p, sm, b, part_of<T>(p, row - 2 * step, rank), lane);
+            if (it >= 2) clear_bits<T>(p, sm, b, part_of<T>(p, row - 2 * step, rank), lane);
             teacher_row<T, MODE, TAIL>(p, sm, fx.teacher[b], b, row, row + step, rank, lane, ah);
             if (lane == 0) mbar_arrive(tfull(b));
         }
@@ -751,7 +771,14 @@ __global__ void __launch_bounds__(32 * W + 32, W == 8 ? 3 : 10) k_distill(const 
                     const float4 v = TAIL ? make_float4(te.top_max, te.top_sum, cm, cs) : make_float4(cm, cs, 0.f, 0.f);
                     // the bytes themselves count on the barriers: a release at cluster scope
                     // would wait for every store of this warp, 1 to 2 us a row
-                    if (lane == 0 && ok) mbar_expect_tx(xbar(b), 16u * C);
+                    if (lane == 0 && ok) {
+                        mbar_expect_tx(xbar(b), (rank == 0 ? 20u : 16u) * C);
+                        asm volatile(
+                            "st.async.shared::cluster.mbarrier::complete_tx::bytes.f32 [%0], %1, [%2];" ::"r"(
+                                mapa(smem_u32(&fx.again[b][rank]), 0u)),
+                            "f"(te.again), "r"(mapa(xbar(b), 0u))
+                            : "memory");
+                    }
                     if (lane < (int)C && ok)
                         asm volatile(
                             "st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(
@@ -762,7 +789,8 @@ __global__ void __launch_bounds__(32 * W + 32, W == 8 ? 3 : 10) k_distill(const 
                 if (MODE == FWD) {      // the other warps go on to the next row
                     if (warp == 0) {
                         ok = __all_sync(0xFFFFFFFFu, ok && mbar_wait(xbar(b), buf_phase, p, abort_flag));
-                        if (rank == 0 && lane == 0 && ok) write_loss<TAIL>(p, row, te, view_of<TAIL>(p, gather_mail(b)));
+                        if (rank == 0 && lane == 0 && ok)
+                            write_loss<TAIL>(p, row, te, view_of<TAIL>(p, gather_mail(b)), gather_again(b));
                         __syncwarp();
                         if (lane == 0) mbar_arrive(tempty(b));
                     }
@@ -770,7 +798,7 @@ __global__ void __launch_bounds__(32 * W + 32, W == 8 ? 3 : 10) k_distill(const 
                     if (!TAIL) ok = ok && mbar_wait(tfull(b), buf_phase, p, abort_flag);
                     ok = ok && mbar_wait(xbar(b), buf_phase, p, abort_flag);
                     view = view_of<TAIL>(p, gather_mail(b));
-                    if (rank == 0 && threadIdx.x == 0 && ok) write_loss<TAIL>(p, row, te, view);
+                    if (rank == 0 && threadIdx.x == 0 && ok) write_loss<TAIL>(p, row, te, view, gather_again(b));
                 }
             } else {
                 view = view_of_stats<TAIL>(te.stats);
@@ -857,7 +885,7 @@ __global__ void __launch_bounds__(32, kWarpPerSm) k_distill_warp(const Params p)
             }
             const float m = warp_max(sum.m), s = warp_sum(sum.total() * e_of(sum.m, finite_max(m), p.c));
             view = view_of<TAIL>(p, TAIL ? joined(te.top_max, te.top_sum, m, s, p.c) : Sums{m, s, m, s});
-            if (lane == 0) write_loss<TAIL>(p, row, te, view);
+            if (lane == 0) write_loss<TAIL>(p, row, te, view, te.again);
         } else {
             view = view_of_stats<TAIL>(te.stats);
         }
@@ -868,7 +896,7 @@ __global__ void __launch_bounds__(32, kWarpPerSm) k_distill_warp(const Params p)
             slope.kept(p, pt, sm, 0, lane, 32);
         }
         __syncwarp();
-        if (TAIL || MODE != FWD) clear_bits<T>(p, sm, 0, pt, lane);
+        clear_bits<T>(p, sm, 0, pt, lane);
     }
     wait_group(0);
 }

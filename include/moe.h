@@ -1067,7 +1067,7 @@ MOE_API moe_status_t grouped_ffn_bwd(const void* dh, int64_t lddh, const void* a
  * teacher_lse, with none above -inf) has loss 0 and gradient 0: padding, or a
  * masked token.  An idx of V or more is taken as not kept and puts
  * MOE_ERR_BAD_INDEX in err.  A token that occurs several times in a row has the sum
- * of its probabilities.  Terms with p = 0 are 0; a rest without student tokens
+ * of its probabilities, in the loss as in the gradient.  Terms with p = 0 are 0; a rest without student tokens
  * of any probability (q_rest below e^-700: all are -inf or of the type's lowest value, or
  * as good as that) is dropped.  dloss = 0 gives a gradient of zeros whatever
  * the row's logits are.  Infinities and NaN otherwise show in the results as the

@@ -21,9 +21,9 @@ def distill(x, idx, t, teacher_lse=None, tau=1.0, dloss=None):
         logq = z - np.logaddexp.reduce(z)
         target = np.zeros(V)
         np.add.at(target, at, p)
-        for pj, i in zip(p, at):
-            if pj > 0:
-                loss[r] += pj * (np.log(pj) - logq[i])
+        for i in np.unique(at):              # a token that occurs several times has the sum of its probabilities
+            if target[i] > 0:
+                loss[r] += target[i] * (np.log(target[i]) - logq[i])
         if teacher_lse is not None:
             others = np.exp(logq)
             others[at] = 0.0
