@@ -786,9 +786,10 @@ __global__ void __launch_bounds__(32 * W + 32, W == 8 ? 3 : 10) k_distill(const 
                             "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w), "r"(mapa(xbar(b), (uint32_t)lane))
                             : "memory");
                 }
+                // (the peers' mail is read after a wait that acquires at cluster scope)
                 if (MODE == FWD) {      // the other warps go on to the next row
                     if (warp == 0) {
-                        ok = __all_sync(0xFFFFFFFFu, ok && mbar_wait(xbar(b), buf_phase, p, abort_flag));
+                        ok = __all_sync(0xFFFFFFFFu, ok && mbar_wait_cluster(xbar(b), buf_phase, p, abort_flag));
                         if (rank == 0 && lane == 0 && ok)
                             write_loss<TAIL>(p, row, te, view_of<TAIL>(p, gather_mail(b)), gather_again(b));
                         __syncwarp();
@@ -796,7 +797,7 @@ __global__ void __launch_bounds__(32 * W + 32, W == 8 ? 3 : 10) k_distill(const 
                     }
                 } else {
                     if (!TAIL) ok = ok && mbar_wait(tfull(b), buf_phase, p, abort_flag);
-                    ok = ok && mbar_wait(xbar(b), buf_phase, p, abort_flag);
+                    ok = ok && mbar_wait_cluster(xbar(b), buf_phase, p, abort_flag);
                     view = view_of<TAIL>(p, gather_mail(b));
                     if (rank == 0 && threadIdx.x == 0 && ok) write_loss<TAIL>(p, row, te, view, gather_again(b));
                 }
