@@ -5,7 +5,6 @@
 
 namespace moe {
 
-static constexpr int kMaxDevices = 64;
 static int g_sm_count[kMaxDevices] = {0};
 static bool g_init[kMaxDevices] = {false};
 static std::mutex g_mu;

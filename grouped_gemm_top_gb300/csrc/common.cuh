@@ -6,6 +6,7 @@
 #include <stdint.h>
 
 #include "moe.h"
+#include "per_device.cuh"
 
 namespace moe {
 

@@ -1083,7 +1083,11 @@ __global__ void __launch_bounds__(256) k_act_bwd(const __nv_bfloat16* __restrict
 
 // ----------------------------------------------------------------- host ----
 
-static int g_max_clusters[kMaxSplits] = {0, 0, 0, 0};      // clusters of 2, 4, 6, 8 CTAs that run at a time
+struct MaxClusters {
+    int n[kMaxSplits];      // clusters of 2, 4, 6, 8 CTAs that run at a time
+};
+static PerDevice<MaxClusters> g_max_clusters;
+static int* max_clusters() { return g_max_clusters.here().n; }
 
 // attr: room for two (the cluster, and the early start described at
 // wait_for_previous_kernels)
@@ -1135,7 +1139,7 @@ static cudaError_t set_attributes() {
         cudaLaunchAttribute attr[2];
         cudaLaunchConfig_t cfg = launch_cfg(1024, i + 1, nullptr, attr);
         const cudaError_t e =
-            cudaOccupancyMaxActiveClusters(&g_max_clusters[i], k_dense_pair<false, true, EPI_PLAIN, 0>, &cfg);
+            cudaOccupancyMaxActiveClusters(&max_clusters()[i], k_dense_pair<false, true, EPI_PLAIN, 0>, &cfg);
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;
@@ -1237,10 +1241,11 @@ static bool make_maps(CUtensorMap* tmA, CUtensorMap* tmB, CUtensorMap* tmY, cons
 
 template <bool A_MN, bool B_MN, int EPI, int ACT>
 static moe_status_t product(const Mat& a, const Mat& b, Params p, cudaStream_t s) {
-    MOE_REQUIRE(g_max_clusters[0] > 0, MOE_ERR_NOT_INITIALIZED);
+    const int* most = max_clusters();
+    MOE_REQUIRE(most[0] > 0, MOE_ERR_NOT_INITIALIZED);
     p.m_tiles = (int)((p.M + TM - 1) / TM);
     p.nk = (int)((p.K + TK - 1) / TK);
-    const Choice c = choose(p.m_tiles, p.N, p.nk, EPI == EPI_GLU, g_max_clusters);
+    const Choice c = choose(p.m_tiles, p.N, p.nk, EPI == EPI_GLU, most);
     p.splits = c.splits;
     set_width(p, c.bn, stage_size(B_MN, c.bn), EPI == EPI_GLU);
     CUtensorMap tmA, tmB, tmY, tmZ, tmZ2;
@@ -1252,7 +1257,7 @@ static moe_status_t product(const Mat& a, const Mat& b, Params p, cudaStream_t s
                     MOE_ERR_CUDA);
     const int64_t tiles = (int64_t)p.m_tiles * p.n_tiles;
     MOE_REQUIRE(tiles <= 0x3FFFFFFF, MOE_ERR_UNSUPPORTED);
-    const int clusters = (int)(p.splits > 1 ? tiles : std::min<int64_t>(tiles, g_max_clusters[0]));
+    const int clusters = (int)(p.splits > 1 ? tiles : std::min<int64_t>(tiles, most[0]));
     cudaLaunchAttribute attr[2];
     cudaLaunchConfig_t cfg = launch_cfg(clusters, p.splits, s, attr);
     if (cudaLaunchKernelEx(&cfg, k_dense_pair<A_MN, B_MN, EPI, ACT>, tmA, tmB, tmY, tmZ, tmZ2, p) != cudaSuccess)
@@ -1276,7 +1281,7 @@ static moe_status_t product_both(const Mat& x, const Mat& w, const Mat& dz, Para
     const int64_t tiles = (int64_t)p.m_tiles * p.n_tiles + (int64_t)q.m_tiles * q.n_tiles;
     MOE_REQUIRE(tiles <= 0x3FFFFFFF, MOE_ERR_UNSUPPORTED);
     cudaLaunchAttribute attr[2];
-    cudaLaunchConfig_t cfg = launch_cfg((int)std::min<int64_t>(tiles, g_max_clusters[0]), 1, s, attr);
+    cudaLaunchConfig_t cfg = launch_cfg((int)std::min<int64_t>(tiles, max_clusters()[0]), 1, s, attr);
     if (cudaLaunchKernelEx(&cfg, k_dense_both<EPI_W>, tmA, tmB, tmY, tmA2, tmB2, tmY2, p, q) != cudaSuccess)
         return MOE_ERR_CUDA;
     MOE_CHECK_LAUNCH();
@@ -1417,10 +1422,11 @@ static moe_status_t gradients(const void* dz, int64_t lddz, const void* x, int64
     q.M = K, q.N = N, q.K = M, q.act = MOE_ACT_NONE, q.y = dw, q.ldy = lddw, q.err = err;
     const bool few = few_rows(M, N);
     if (dx && dw && !few) {
-        MOE_REQUIRE(g_max_clusters[0] > 0, MOE_ERR_NOT_INITIALIZED);
+        const int* most = max_clusters();
+        MOE_REQUIRE(most[0] > 0, MOE_ERR_NOT_INITIALIZED);
         p.m_tiles = (int)((M + TM - 1) / TM), p.nk = (N + TK - 1) / TK;
         q.m_tiles = (int)((K + TM - 1) / TM), q.nk = (int)((M + TK - 1) / TK);
-        const Choice c = choose_both(p.m_tiles, p.N, p.nk, q.m_tiles, q.N, q.nk, g_max_clusters);
+        const Choice c = choose_both(p.m_tiles, p.N, p.nk, q.m_tiles, q.N, q.nk, most);
         if (c.bn > 0)
             return f32 ? product_both<EPI_F32>(mx, mw, mz, p, q, c.bn, s)
                        : product_both<EPI_PLAIN>(mx, mw, mz, p, q, c.bn, s);
@@ -1557,7 +1563,7 @@ extern "C" moe_status_t moe_selftest_dense_plan(int product, int64_t M, int64_t 
     MOE_REQUIRE(M >= 1 && N >= 1 && K >= 1, MOE_ERR_INVALID_ARG);
     MOE_REQUIRE(M <= 0x7FFFFF00LL && size_ok(N) && size_ok(K), MOE_ERR_UNSUPPORTED);
     *plan = {};
-    const int* slots = clusters ? clusters : g_max_clusters;
+    const int* slots = clusters ? clusters : max_clusters();
     const int sms = clusters ? 2 * clusters[0] : device_sm_count();
     const bool glu = product == MOE_DENSE_GATED;
     const int nk = (int)((K + TK - 1) / TK);

@@ -912,7 +912,10 @@ __global__ void __launch_bounds__(32, kWarpPerSm) k_distill_warp(const Params p)
 
 constexpr int kPerSm = 3, kNarrowPerSm = 10;      // CTAs of an SM, by registers
 constexpr int kSmemSm = 233472;                   // shared memory of an SM, 1 KB of it the system's per CTA
-static int g_clusters[2][4][kPerSm];              // that run at a time: wide CTAs or not; of 1, 2, 4, 8; CTAs an SM
+struct Clusters {                                 // that run at a time: wide CTAs or not; of 1, 2, 4, 8; CTAs an SM
+    int n[2][4][kPerSm];
+};
+static PerDevice<Clusters> g_clusters;
 static size_t smem_of(int per_sm) { return kSmemSm / per_sm / 128 * 128 - 1024; }
 
 static cudaLaunchConfig_t launch_cfg(int64_t clusters, int C, bool wide, size_t smem, cudaStream_t stream,
@@ -943,13 +946,14 @@ static cudaError_t set_attributes() {
     }
     MOE_DISTILL_INSTANCES(X)
 #undef X
+    Clusters& at = g_clusters.here();
     for (int wide = 0; wide < 2; ++wide)
         for (int c = 0; c < 4; ++c)
             for (int n = 1; n <= (wide ? kPerSm : 1); ++n) {
                 cudaLaunchAttribute attr[2];
                 const cudaLaunchConfig_t cfg = launch_cfg(1024, 1 << c, wide, wide ? smem_of(n) : smem_of(kNarrowPerSm), nullptr, attr);
                 const cudaError_t e = cudaOccupancyMaxActiveClusters(
-                    &g_clusters[wide][c][n - 1],
+                    &at.n[wide][c][n - 1],
                     wide ? k_distill<__nv_bfloat16, BOTH, true, 8> : k_distill<__nv_bfloat16, BOTH, true, 2>, &cfg);
                 if (e != cudaSuccess) return e;
             }
@@ -1008,6 +1012,7 @@ struct Spread {
 };
 static Spread spread(int64_t M, int V, int elem, int k, int mode, int sms) {
     const int E = 16 / elem, units = (E - 1 + V + E - 1) / E;
+    const Clusters& at = g_clusters.here();
     Spread best{};
     double least = 1e300;
     for (int c = 0; c < 4; ++c) {
@@ -1024,7 +1029,7 @@ static Spread spread(int64_t M, int V, int elem, int k, int mode, int sms) {
         s.per_sm = s.wide ? kPerSm : kNarrowPerSm;
         while (s.per_sm > 1 && s.smem > smem_of(s.per_sm)) --s.per_sm;
         const int64_t slots =
-            s.wide ? g_clusters[1][c][s.per_sm - 1] : (int64_t)g_clusters[0][c][0] * s.per_sm / kNarrowPerSm;
+            s.wide ? at.n[1][c][s.per_sm - 1] : (int64_t)at.n[0][c][0] * s.per_sm / kNarrowPerSm;
         s.clusters = std::min<int64_t>(M, std::max<int64_t>(1, slots));
         const double ctas = std::max(2., std::min<double>(s.per_sm, (double)s.clusters * s.C / sms));
         const double cost = (double)((M + s.clusters - 1) / s.clusters) *

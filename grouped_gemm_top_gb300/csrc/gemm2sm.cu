@@ -466,7 +466,10 @@ __global__ void __launch_bounds__(THREADS, 1)
 }  // namespace sm2
 }  // namespace gg
 
-static int g_max_clusters[3] = {0, 0, 0};   // [N = 128, N = 256, N = 224]
+struct MaxClusters {
+    int n[3];      // [N = 128, N = 256, N = 224]
+};
+static PerDevice<MaxClusters> g_max_clusters;
 
 template <int BN>
 static cudaLaunchConfig_t launch_cfg(int clusters, cudaStream_t stream, cudaLaunchAttribute* attr) {
@@ -506,9 +509,10 @@ static cudaError_t set_attr_2sm(int* max_clusters) {
 }
 
 cudaError_t gemm_set_attributes_2sm() {
-    cudaError_t e = set_attr_2sm<128>(&g_max_clusters[0]);
+    int* n = g_max_clusters.here().n;
+    cudaError_t e = set_attr_2sm<128>(&n[0]);
     if (e != cudaSuccess) return e;
-    e = set_attr_2sm<256>(&g_max_clusters[1]);
+    e = set_attr_2sm<256>(&n[1]);
     if (e != cudaSuccess) return e;
     e = cudaFuncSetAttribute(gg::sm2::k_grouped_gemm_2sm<224, MOE_EPI_NONE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              gg::sm2::C2<224>::SMEM_BYTES);
@@ -516,7 +520,7 @@ cudaError_t gemm_set_attributes_2sm() {
     {
         cudaLaunchAttribute attr[1];
         cudaLaunchConfig_t cfg = launch_cfg<224>(1024, nullptr, attr);
-        e = cudaOccupancyMaxActiveClusters(&g_max_clusters[2], gg::sm2::k_grouped_gemm_2sm<224, MOE_EPI_NONE>, &cfg);
+        e = cudaOccupancyMaxActiveClusters(&n[2], gg::sm2::k_grouped_gemm_2sm<224, MOE_EPI_NONE>, &cfg);
         if (e != cudaSuccess) return e;
     }
     const cudaError_t es[] = {
@@ -545,7 +549,7 @@ cudaError_t gemm_launch_2sm_nvf4(int epilogue, const CUtensorMap& tmA, const CUt
                               p);
 }
 
-int gemm_max_clusters_2sm(int bn) { return g_max_clusters[bn == 256 ? 1 : (bn == 224 ? 2 : 0)]; }
+int gemm_max_clusters_2sm(int bn) { return g_max_clusters.here().n[bn == 256 ? 1 : (bn == 224 ? 2 : 0)]; }
 
 template <int BN>
 static cudaError_t launch_2sm(int epilogue, const CUtensorMap& tmA, const CUtensorMap& tmB, const CUtensorMap& tmSFA,

@@ -896,7 +896,8 @@ __global__ void __launch_bounds__(256) k_glu_rows(const __nv_bfloat16* __restric
 
 // ----------------------------------------------------------------- host ----
 
-static int g_max_clusters = 0;      // CTA pairs that run at a time
+static PerDevice<int> g_max_clusters;      // CTA pairs that run at a time
+static int max_clusters() { return g_max_clusters.here(); }
 
 static cudaLaunchConfig_t launch_cfg(int64_t pairs, cudaStream_t stream, cudaLaunchAttribute* attr) {
     cudaLaunchConfig_t cfg = {};
@@ -932,7 +933,7 @@ static cudaError_t set_attributes() {
     }
     cudaLaunchAttribute attr[2];
     cudaLaunchConfig_t cfg = launch_cfg(1024, nullptr, attr);
-    return cudaOccupancyMaxActiveClusters(&g_max_clusters, k_wgrad<false>, &cfg);
+    return cudaOccupancyMaxActiveClusters(&g_max_clusters.here(), k_wgrad<false>, &cfg);
 }
 
 struct Mat {
@@ -950,7 +951,8 @@ static moe_status_t plan_rows(Params& p) {
     // Where even M rows in one group give fewer tiles than half of the pairs, tiles of
     // fewer rows: a step of 64 rows takes half the time of one of 256 (428 rows, 1,589 x 432: 8.8 us, with
     // 256 rows 13.0; gated 411 rows, 3,713 x 2 * 72: 18.1 and 27.6).
-    while (p.n_max > 64 && (p.M + p.n_max - 1) / p.n_max * p.col_tiles * 2 <= g_max_clusters)
+    const int most = max_clusters();
+    while (p.n_max > 64 && (p.M + p.n_max - 1) / p.n_max * p.col_tiles * 2 <= most)
         p.n_max = (p.n_max / 2 + 31) / 32 * 32;
     int box = 16;      // rows of x per CTA that a stage has room for
     while (2 * box < p.n_max) box *= 2;
@@ -970,7 +972,7 @@ static bool rows_maps(CUtensorMap* tmX, CUtensorMap* tmY, const Mat& x, const Pa
 // D = x op(W) of every group; D's columns are W's (W_MN) or its rows.
 template <bool W_MN, bool GLU, int ACT>
 static moe_status_t product_rows(const Mat& x, const Mat& w, Params p, cudaStream_t s) {
-    MOE_REQUIRE(g_max_clusters > 0, MOE_ERR_NOT_INITIALIZED);
+    MOE_REQUIRE(max_clusters() > 0, MOE_ERR_NOT_INITIALIZED);
     const moe_status_t st = plan_rows<GLU>(p);
     if (st != MOE_OK) return st;
     // eight warps' boxes (GLU: half as many, and four gate warps' way to up)
@@ -983,7 +985,7 @@ static moe_status_t product_rows(const Mat& x, const Mat& w, Params p, cudaStrea
              make_store_map(&tmA2, p.a + p.N, p.M, p.N, p.lda, false);
     MOE_REQUIRE(ok, MOE_ERR_CUDA);
     cudaLaunchAttribute attr[2];
-    cudaLaunchConfig_t cfg = launch_cfg(std::min<int64_t>(p.max_tiles, g_max_clusters), s, attr);
+    cudaLaunchConfig_t cfg = launch_cfg(std::min<int64_t>(p.max_tiles, max_clusters()), s, attr);
     if (cudaLaunchKernelEx(&cfg, k_rows<W_MN, GLU, ACT>, tmW, tmX[0], tmX[1], tmX[2], tmX[3], tmY, tmA, tmA2, p) !=
         cudaSuccess)
         return MOE_ERR_CUDA;
@@ -1010,7 +1012,7 @@ static int wgrad_width(int64_t tiles256, int N, double nk, int slots) {
 }
 static moe_status_t plan_wgrad(Params& p) {
     p.m_tiles = (p.K + TM - 1) / TM;
-    p.bn = wgrad_width((int64_t)p.G * p.m_tiles, p.N, (double)p.M / p.G / TK, g_max_clusters);
+    p.bn = wgrad_width((int64_t)p.G * p.m_tiles, p.N, (double)p.M / p.G / TK, max_clusters());
     p.col_tiles = (p.N + p.bn - 1) / p.bn;
     p.max_tiles = (int64_t)p.G * p.m_tiles * p.col_tiles;
     p.stage_bytes = HALF_BYTES + (p.bn / 2 + 63) / 64 * (HALF_BYTES / 2);
@@ -1027,7 +1029,7 @@ static bool wgrad_maps(CUtensorMap* tmX, CUtensorMap* tmDY, CUtensorMap* tmD, co
 
 // D_g [K, N] = x^T dy of every group
 static moe_status_t product_wgrad(const Mat& x, const Mat& dy, Params p, bool f32, cudaStream_t s) {
-    MOE_REQUIRE(g_max_clusters > 0, MOE_ERR_NOT_INITIALIZED);
+    MOE_REQUIRE(max_clusters() > 0, MOE_ERR_NOT_INITIALIZED);
     const size_t size = f32 ? 4 : 2;
     if (p.M == 0) {
         const bool joined = p.gsy == p.K * p.ldy;      // one matrix of G K rows
@@ -1043,7 +1045,7 @@ static moe_status_t product_wgrad(const Mat& x, const Mat& dy, Params p, bool f3
     CUtensorMap tmX, tmDY, tmD;
     MOE_REQUIRE(wgrad_maps(&tmX, &tmDY, &tmD, x, dy, p, f32), MOE_ERR_CUDA);
     cudaLaunchAttribute attr[2];
-    cudaLaunchConfig_t cfg = launch_cfg(std::min<int64_t>(p.max_tiles, g_max_clusters), s, attr);
+    cudaLaunchConfig_t cfg = launch_cfg(std::min<int64_t>(p.max_tiles, max_clusters()), s, attr);
     const cudaError_t e = f32 ? cudaLaunchKernelEx(&cfg, k_wgrad<true>, tmX, tmDY, tmD, p)
                               : cudaLaunchKernelEx(&cfg, k_wgrad<false>, tmX, tmDY, tmD, p);
     if (e != cudaSuccess) return MOE_ERR_CUDA;
@@ -1054,7 +1056,7 @@ static moe_status_t product_wgrad(const Mat& x, const Mat& dy, Params p, bool f3
 // dx = dz W^T (p) and dW = x^T dz (q) in one launch
 static moe_status_t product_both(const Mat& dz, const Mat& x, const Mat& w, Params p, Params q, bool f32,
                                  cudaStream_t s) {
-    MOE_REQUIRE(g_max_clusters > 0, MOE_ERR_NOT_INITIALIZED);
+    MOE_REQUIRE(max_clusters() > 0, MOE_ERR_NOT_INITIALIZED);
     moe_status_t st = plan_rows<false>(p);
     if (st == MOE_OK) st = plan_wgrad(q);
     if (st != MOE_OK) return st;
@@ -1065,7 +1067,7 @@ static moe_status_t product_both(const Mat& dz, const Mat& x, const Mat& w, Para
                     wgrad_maps(&tmX, &tmDY, &tmD, x, dz, q, f32),
                 MOE_ERR_CUDA);
     cudaLaunchAttribute attr[2];
-    cudaLaunchConfig_t cfg = launch_cfg(std::min<int64_t>(p.max_tiles + q.max_tiles, g_max_clusters), s, attr);
+    cudaLaunchConfig_t cfg = launch_cfg(std::min<int64_t>(p.max_tiles + q.max_tiles, max_clusters()), s, attr);
     const cudaError_t e =
         f32 ? cudaLaunchKernelEx(&cfg, k_both<true>, tmW, tmZ[0], tmZ[1], tmZ[2], tmZ[3], tmDX, tmX, tmDY, tmD, p, q)
             : cudaLaunchKernelEx(&cfg, k_both<false>, tmW, tmZ[0], tmZ[1], tmZ[2], tmZ[3], tmDX, tmX, tmDY, tmD, p, q);
@@ -1100,7 +1102,7 @@ static moe_status_t gradients(const Mat& dz, const Mat& x, const Mat& w, const P
     // 7,168: 1.85 ms, 1.90 in one; 8,192 x 4,096 x 7,168 551 us, 567): up to about 1,000 steps of
     // 256 x 256 x 64 a pair.
     const double steps = 2. * groups.M * K * N / (256. * 256. * 64.);
-    if (dx && dw && groups.M > 0 && steps < 1000. * g_max_clusters) return product_both(dz, x, w, p, q, f32, s);
+    if (dx && dw && groups.M > 0 && steps < 1000. * max_clusters()) return product_both(dz, x, w, p, q, f32, s);
     if (dx && groups.M > 0) {
         const moe_status_t st = product_rows<false, false, 0>(dz, w, p, s);
         if (st != MOE_OK) return st;
