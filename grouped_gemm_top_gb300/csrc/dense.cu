@@ -1539,6 +1539,7 @@ extern "C" moe_status_t gated_ffn_bwd(const void* dh, int64_t lddh, const void* 
     ldx = stride_of(M, d, ldx), lddx = stride_of(M, d, lddx), ldw = stride_of(d, f2, ldw);
     lddw = stride_of(d, f2, lddw);
     MOE_REQUIRE(M == 0 || (dh && a && da && (!dx || w1) && (!dw1 || x)), MOE_ERR_INVALID_ARG);
+    MOE_REQUIRE(M == 0 || da != a || ldda == lda, MOE_ERR_INVALID_ARG);      // in place: row by row
     MOE_REQUIRE(row_ok(dh, lddh) && row_ok(a, lda) && row_ok(da, ldda) &&
                     (!dx || (row_ok(w1, ldw) && row_ok(dx, lddx))) &&
                     (!dw1 || (row_ok(x, ldx) && row_ok(dw1, lddw))),

@@ -1214,6 +1214,7 @@ extern "C" moe_status_t grouped_ffn_bwd(const void* dh, int64_t lddh, const void
     lddh = stride_of(M, f, lddh), lda = stride_of(M, f2, lda), ldda = stride_of(M, f2, ldda);
     ldx = stride_of(M, d, ldx), lddx = stride_of(M, d, lddx), ldw = stride_of(d, f2, ldw), lddw = stride_of(d, f2, lddw);
     gsw = group_stride_of(G, d, ldw, gsw), gsdw = group_stride_of(G, d, lddw, gsdw);
+    MOE_REQUIRE(M == 0 || da != a || ldda == lda, MOE_ERR_INVALID_ARG);      // in place: row by row
     MOE_REQUIRE(row_ok(dh, lddh) && row_ok(a, lda) && row_ok(da, ldda) &&
                     (!dx || (row_ok(w1, ldw) && gsw % 8 == 0 && row_ok(dx, lddx))) &&
                     (!dw1 || (row_ok(x, ldx) && row_ok(dw1, lddw) && gsdw % 8 == 0)) && grouped::groups_ok(offsets, rows),

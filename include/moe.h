@@ -917,7 +917,7 @@ MOE_API moe_status_t gated_ffn_fwd(const void* x, int64_t ldx, const void* w1, i
 /*
  * gated_ffn_bwd -- da = [dh up act'(gate) | dh act(gate)] from the forward
  * call's a, dx = da w1^T, dw1 = x^T da.  da [M, 2f] is written (bf16, the
- * operand type of the two products) and may be a itself; dx [M, d] and dw1 [d, 2f] (dw_type) may each
+ * operand type of the two products) and may be a itself (same stride); dx [M, d] and dw1 [d, 2f] (dw_type) may each
  * be NULL.  M = 0 writes zeros to dw1.
  */
 MOE_API moe_status_t gated_ffn_bwd(const void* dh, int64_t lddh, const void* a, int64_t lda, const void* x,
@@ -1035,7 +1035,7 @@ MOE_API moe_status_t adamw_step(void* plan, int tensors, int64_t tiles, int p_ty
  *   in one kernel; W1_g [d, 2f], f % 8 == 0; a [M, 2f] = [gate | up] or NULL (kept for
  *   the backward pass).
  * grouped_ffn_bwd     da = [dh up act'(gate) | dh act(gate)] (bf16, the operand of the
- *   two products; may be a itself), dx = da W1_g^T, dW1_g = x_g^T da_g.
+ *   two products; may be a itself, same stride), dx = da W1_g^T, dW1_g = x_g^T da_g.
  */
 MOE_API moe_status_t grouped_linear_fwd(const void* x, int64_t ldx, const void* w, int64_t ldw, int64_t gsw,
                                         const int32_t* offsets, const int32_t* rows, int G, int64_t M, int N, int64_t K,
