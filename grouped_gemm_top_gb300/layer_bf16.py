@@ -39,7 +39,11 @@ class MoELayerBF16:
         self.gofs, self.slot_of, self.row_id = z((E + 1,), torch.int32), z((T, k), torch.int32), z((M,), torch.int32)
         self.ws_route = z((ops.moe_route_workspace_size(T, E),), torch.uint8)
         self.ws_perm = z((ops.moe_permute_workspace_size(T, E),), torch.uint8)
-        self.x_perm, self.a, self.h, self.y_perm, self.out = z((M, d)), z((M, 2 * f)), z((M, f)), z((M, d)), z((T, d))
+        self.x_perm, self.h, self.y_perm, self.out = z((M, d)), z((M, f)), z((M, d)), z((T, d))
+        # [gate | up], and their gradient (apart, so that backward_ can be repeated); a is the one
+        # that was written last, by forward_ or backward_
+        self.gate_up, self.da = z((M, 2 * f)), z((M, 2 * f))
+        self.a = self.gate_up
         self.dy_perm, self.dh, self.dx_perm, self.dx = z((M, d)), z((M, f)), z((M, d)), z((T, d))
         self.dw, self.dlogits = z((T, k), torch.float32), z((T, E), torch.float32)
         self.W1 = self.W2 = None
@@ -71,7 +75,8 @@ class MoELayerBF16:
                            self.offsets, self.ws_route, err)
         ops.moe_permute(self.x, self.topk_idx, self.E, self.row_cap, self.gofs, self.slot_of, self.row_id, self.x_perm,
                         True, self.ws_perm, err)
-        ops.grouped_ffn_fwd(self.x_perm, self.W1, self.gofs, self.counts, h=self.h, a=self.a, err=err)
+        self.a = self.gate_up
+        ops.grouped_ffn_fwd(self.x_perm, self.W1, self.gofs, self.counts, h=self.h, a=self.gate_up, err=err)
         ops.grouped_linear_fwd(self.h, self.W2, self.gofs, self.counts, y=self.y_perm, err=err)
         ops.moe_unpermute_combine(self.y_perm, self.slot_of, self.topk_w, self.out, err)
 
@@ -80,9 +85,9 @@ class MoELayerBF16:
         ops.moe_combine_bwd(self.dout, self.y_perm, self.slot_of, self.topk_w, self.row_id, self.gofs, self.E,
                             self.dy_perm, self.dw, err)
         ops.grouped_linear_bwd(self.dy_perm, self.h, self.W2, self.gofs, self.counts, dx=self.dh, dw=self.dW2, err=err)
-        # da takes a's place: nothing reads a afterwards
-        ops.grouped_ffn_bwd(self.dh, self.a, self.x_perm, self.W1, self.gofs, self.counts, dx=self.dx_perm,
-                            dw1=self.dW1, da=self.a, err=err)
+        self.a = self.da
+        ops.grouped_ffn_bwd(self.dh, self.gate_up, self.x_perm, self.W1, self.gofs, self.counts, dx=self.dx_perm,
+                            dw1=self.dW1, da=self.da, err=err)
         ops.moe_route_bwd(self.logits, self.topk_idx, self.dw, self.score, self.normalize, self.dlogits, err)
         if not self.router:
             ops.moe_unpermute_combine(self.dx_perm, self.slot_of, None, self.dx, err)
