@@ -18,11 +18,27 @@ from . import ops
 _SCORES = {"softmax": ops.MOE_SCORE_SOFTMAX, "sigmoid": ops.MOE_SCORE_SIGMOID}
 
 
+def _as_operand(name, w, shape, device):
+    """w as the grouped products read it where it lies, or a ValueError."""
+    ok = (isinstance(w, torch.Tensor) and w.shape == shape and w.dtype == torch.bfloat16 and w.device == device and
+          w.data_ptr() % 16 == 0)
+    if ok:
+        G, K, N = shape
+        gs, ld, one = w.stride()
+        ok = (one == 1 or N == 1) and (K == 1 or (ld >= N and ld % 8 == 0))
+        ok = ok and (G == 1 or (gs >= (K - 1) * ld + N and gs % 8 == 0))
+    if not ok:
+        raise ValueError(f"{name}: bfloat16 {tuple(shape)} on {device}, rows at multiples of 16 bytes")
+    return w
+
+
 class MoELayerBF16:
     def __init__(self, T, d, E, k, f, score="softmax", normalize=True, device="cuda:0", router=False):
         """T tokens of width d (d % 8 == 0), E experts of width f (f % 8 == 0),
         top-k.  router: logits = x W_r (T % 128 == 0, E % 8 == 0), with its
         gradients, as in MoELayer."""
+        if d % 8 or f % 8:
+            raise ValueError("16-bit products: d % 8, f % 8")
         self.T, self.d, self.E, self.k, self.f = T, d, E, k, f
         self.score, self.normalize = _SCORES[score], bool(normalize)
         self.device = torch.device(device)
@@ -57,11 +73,10 @@ class MoELayerBF16:
             self.dx_r, self.dWr = z((T, d), torch.float32), z((d, E), torch.float32)
 
     def set_weights(self, W1, W2):
-        """bf16 W1 [E, d, 2f] and W2 [E, f, d]; they stay the caller's, and
-        the steps read them where they lie."""
-        if W1.shape != self.dW1.shape or W2.shape != self.dW2.shape:
-            raise ValueError(f"W1 {tuple(W1.shape)}, W2 {tuple(W2.shape)}")
-        self.W1, self.W2 = W1, W2
+        """bf16 W1 [E, d, 2f] and W2 [E, f, d], rows at multiples of 16 bytes;
+        they stay the caller's, and the steps read them where they lie."""
+        W1 = _as_operand("W1", W1, self.dW1.shape, self.dW1.device)
+        self.W1, self.W2 = W1, _as_operand("W2", W2, self.dW2.shape, self.dW2.device)
 
     def set_router_weights(self, Wr):
         self.Wr.copy_(Wr)
