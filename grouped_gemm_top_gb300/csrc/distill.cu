@@ -94,8 +94,8 @@ struct Smem {
 };
 struct Fixed {
     unsigned long long bar[6];
-    float again[2][MAX_C];          // (the first CTA's) of the cluster's parts
-    float4 mail[2][MAX_C];          // of the cluster's parts, see Sums: m, s, or kept m, s, the others' m, s
+    float4 mail[2][MAX_C];          // of the cluster's parts, see Sums: m, s, again, or (TAIL) kept m, s, the others' m, s
+    float again[2][MAX_C];          // TAIL: the first CTA's, of the others' parts
     float2 warp_part[2][8];
     Teacher teacher[2];
     int abort_flag;
@@ -350,6 +350,12 @@ __device__ __forceinline__ void load_logits(const Params& p, int64_t row, uint32
     }
 }
 
+// Whether the teacher's tokens set bits: where only repeated ones are looked for, up to 32
+// compare themselves with one another (16,384 x 4,096, loss alone: 43.6 us, 44.6 by bits).
+template <int MODE, bool TAIL>
+__device__ __forceinline__ bool by_bits(const Params& p) {
+    return TAIL || MODE != FWD || p.k > 32;
+}
 __device__ __forceinline__ float p_log_p(float p) { return p == 0.f ? 0.f : p * logf(p); }
 
 // The teacher's row (one warp): probabilities, what the loss needs of them,
@@ -363,6 +369,7 @@ __device__ __forceinline__ void teacher_row(const Params& p, const Smem& sm, Tea
     float *pr = sm.p(b), *xs = sm.x(b);
     uint32_t* words = reinterpret_cast<uint32_t*>(sm.bits(b));
     const float inv_tau = p.inv_tau;
+    const bool bits = by_bits<MODE, TAIL>(p);
     bool any = false, dup = false;
     float t_max = -INFINITY, x_max = -INFINITY;
     for (int j0 = 0; j0 < p.k; j0 += 128) {
@@ -379,7 +386,7 @@ __device__ __forceinline__ void teacher_row(const Params& p, const Smem& sm, Tea
             if (ok) {
                 any = true;
                 const int u = i + pt.head, g = u / E - pt.g0;
-                if (g >= 0 && g < pt.n) {
+                if (bits && g >= 0 && g < pt.n) {
                     const uint32_t bit = 1u << (8 * (g & 3) + u % E);
                     dup |= (atomicOr(words + (g >> 2), bit) & bit) != 0;
                 }
@@ -390,6 +397,10 @@ __device__ __forceinline__ void teacher_row(const Params& p, const Smem& sm, Tea
             xs[j] = x[q];
             t_max = fmaxf(t_max, t);
         }
+    }
+    if (!bits) {
+        const int i = ah.i[0];
+        dup = __popc(__match_any_sync(0xFFFFFFFFu, i >= 0 && i < p.V ? i : -1 - lane)) > 1;
     }
     if (lane == 0 && MODE != FWD) {
         out.dloss = ah.dloss;
@@ -499,29 +510,24 @@ __device__ __forceinline__ Sums joined(float m_top, float s_top, float m_rest, f
     return {m, s_top * e_of(m_top, ref, c) + s_rest * e_of(m_rest, ref, c), m_rest, s_rest};
 }
 
-// What the loss and the gradient go by.  The others' part of q, q_rest, counts as none
-// below e^-700: a maximum of the type's lowest value is a mask.  Below e^-40 the
-// student is `sure`: the others' gradient is then that of rest alone (what mass
-// adds to it, q_rest / rest of it, is less than a rounding as rest is at least 2^-24),
-// taken relative to their own maximum, so that rest / s_rest does not overflow.
-constexpr float kNoRest = -700.f, kSure = -40.f;
+// What the loss and the gradient go by.  Others whose largest logit lies more than 700 tau
+// below max x count as none: a maximum of the type's lowest value is a mask.  From
+// 50 tau on the student is `sure`: the others' gradient is then that of rest alone (what
+// mass adds to it, q_rest / rest of it, is less than a rounding: V e^-50, and rest is at
+// least 2^-24), taken relative to their own maximum, so that rest / s_rest does not
+// overflow.
+constexpr float kNone = -700.f * kLog2e, kSure = -50.f * kLog2e;
 struct View {
     float m, s;               // maximum and sum, for the kept tokens (not sure: for all)
     float m_rest, s_rest;     // for the others; s_rest = 0: none; not sure: relative to m
-    float log_rest;           // log q_rest
     bool sure;
 };
 template <bool TAIL>
 __device__ __forceinline__ View view_of(const Params& p, const Sums& r) {
-    View v{r.m, r.s, r.m, r.s, 0.f, false};
-    if (TAIL) {
-        v.log_rest = (r.m_rest - r.m) * p.inv_tau + logf(r.s_rest) - logf(r.s);
-        const bool some = r.s_rest > 0.f && v.log_rest >= kNoRest;
-        v.sure = some && v.log_rest < kSure;
-        v.m_rest = v.sure ? r.m_rest : r.m;
-        v.s_rest = !some ? 0.f : (v.sure ? r.s_rest : r.s_rest * e_of(r.m_rest, finite_max(r.m), p.c));
-    }
-    return v;
+    if (!TAIL) return {r.m, r.s, r.m, r.s, false};
+    const float below = (r.m_rest - finite_max(r.m)) * p.c;
+    if (below < kSure && below >= kNone) return {r.m, r.s, r.m_rest, r.s_rest, true};
+    return {r.m, r.s, r.m, r.s_rest * ex2(below), false};
 }
 // The view in three numbers: m, s, s_rest, or, of a student who is sure, the kept
 // tokens' log-sum-exp (tau of it, in the logits' scale), minus s_rest, m_rest.
@@ -532,8 +538,8 @@ __device__ __forceinline__ void put_stats(const Params& p, float* out, const Vie
 }
 template <bool TAIL>
 __device__ __forceinline__ View view_of_stats(const float* st) {
-    if (TAIL && st[1] < 0.f) return {st[0], 1.f, st[2], -st[1], 0.f, true};
-    return {st[0], st[1], st[0], st[2], 0.f, false};
+    if (TAIL && st[1] < 0.f) return {st[0], 1.f, st[2], -st[1], true};
+    return {st[0], st[1], st[0], st[2], false};
 }
 
 // The row's loss, and what the backward pass needs.
@@ -542,8 +548,12 @@ __device__ __forceinline__ void write_loss(const Params& p, int64_t row, const T
                                            float again) {
     if (p.stats) put_stats(p, p.stats + 3 * row, v);
     if (p.loss) {
-        float loss = te.fit + again + te.p_sum * ((finite_max(v.m) - te.x_ref) * p.inv_tau + logf(v.s) - te.t_lse);
-        if (TAIL && te.rest > 0.f && v.s_rest > 0.f) loss += te.rest * (logf(te.rest) - v.log_rest);
+        const float log_s = logf(v.s);
+        float loss = te.fit + again + te.p_sum * ((finite_max(v.m) - te.x_ref) * p.inv_tau + log_s - te.t_lse);
+        if (TAIL && te.rest > 0.f && v.s_rest > 0.f) {
+            const float log_rest = (v.sure ? (v.m_rest - v.m) * p.inv_tau : 0.f) + logf(v.s_rest) - log_s;      // log q_rest
+            loss += te.rest * (logf(te.rest) - log_rest);
+        }
         p.loss[row] = te.some ? loss * p.tau * p.tau : 0.f;
     }
 }
@@ -653,21 +663,28 @@ __global__ void __launch_bounds__(32 * W + 32, W == 8 ? 3 : 10) k_distill(const 
         return TAIL ? joined(m, s, m_rest, s_rest, p.c) : Sums{m, s, m, s};
     };
     auto gather_again = [&](int b) {
-        float sum = 0.f;
-        for (int i = 0; i < (int)C; ++i) sum += fx.again[b][i];
+        float sum = fx.teacher[b].again;      // the first CTA's own
+        for (int i = 1; i < (int)C; ++i) sum += TAIL ? fx.again[b][i] : fx.mail[b][i].z;
         return sum;
+    };
+    // (what peers sent is read behind a wait that acquires at cluster scope)
+    auto wait_mail = [&](int b, uint32_t phase) {
+        return C > 1 ? mbar_wait_cluster(xbar(b), phase, p, abort_flag) : mbar_wait(xbar(b), phase, p, abort_flag);
     };
     if (warp == W) {
         // ---------------------------------------------- teacher, a row ahead ----
-        for (int i = lane; i < bits_bytes(p.part) / 2; i += 32) reinterpret_cast<uint32_t*>(sm.bits(0))[i] = 0u;
-        __syncwarp();
+        const bool bits = by_bits<MODE, TAIL>(p);
+        if (bits) {
+            for (int i = lane; i < bits_bytes(p.part) / 2; i += 32) reinterpret_cast<uint32_t*>(sm.bits(0))[i] = 0u;
+            __syncwarp();
+        }
         int it = 0;
         Ahead ah = {};
         load_tokens<MODE, TAIL>(p, row0, 0, lane, ah);
         for (int64_t row = row0; row < p.M; row += step, ++it) {
             const int b = it & 1;
             if (!__all_sync(0xFFFFFFFFu, mbar_wait(tempty(b), (uint32_t)(it >> 1 & 1) ^ 1u, p, abort_flag))) break;
-            if (it >= 2) clear_bits<T>(p, sm, b, part_of<T>(p, row - 2 * step, rank), lane);
+            if (it >= 2 && bits) clear_bits<T>(p, sm, b, part_of<T>(p, row - 2 * step, rank), lane);
             teacher_row<T, MODE, TAIL>(p, sm, fx.teacher[b], b, row, row + step, rank, lane, ah);
             if (lane == 0) mbar_arrive(tfull(b));
         }
@@ -713,7 +730,7 @@ __global__ void __launch_bounds__(32 * W + 32, W == 8 ? 3 : 10) k_distill(const 
             const Teacher& te = fx.teacher[b];
             // which of a unit's tokens were kept has to be known before the sums
             if (TAIL || MODE == BWD) ok = ok && mbar_wait(tfull(b), buf_phase, p, abort_flag);
-            View view{0.f, 1.f, 0.f, 1.f, 0.f, false};
+            View view{0.f, 1.f, 0.f, 1.f, false};
             if constexpr (MODE != BWD) {
                 // -------------------------------- maximum and sum ----
                 const uint8_t* bits = sm.bits(b);
@@ -768,12 +785,12 @@ __global__ void __launch_bounds__(32 * W + 32, W == 8 ? 3 : 10) k_distill(const 
                     const float ref = finite_max(cm);
 #pragma unroll
                     for (int w = 0; w < W; ++w) cs += part[w].y * e_of(part[w].x, ref, p.c);
-                    const float4 v = TAIL ? make_float4(te.top_max, te.top_sum, cm, cs) : make_float4(cm, cs, 0.f, 0.f);
+                    const float4 v = TAIL ? make_float4(te.top_max, te.top_sum, cm, cs) : make_float4(cm, cs, te.again, 0.f);
                     // the bytes themselves count on the barriers: a release at cluster scope
                     // would wait for every store of this warp, 1 to 2 us a row
                     if (lane == 0 && ok) {
-                        mbar_expect_tx(xbar(b), (rank == 0 ? 20u : 16u) * C);
-                        asm volatile(
+                        mbar_expect_tx(xbar(b), 16u * C + (TAIL && rank == 0 ? 4u * (C - 1u) : 0u));
+                        if (TAIL && rank > 0) asm volatile(
                             "st.async.shared::cluster.mbarrier::complete_tx::bytes.f32 [%0], %1, [%2];" ::"r"(
                                 mapa(smem_u32(&fx.again[b][rank]), 0u)),
                             "f"(te.again), "r"(mapa(xbar(b), 0u))
@@ -786,10 +803,9 @@ __global__ void __launch_bounds__(32 * W + 32, W == 8 ? 3 : 10) k_distill(const 
                             "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w), "r"(mapa(xbar(b), (uint32_t)lane))
                             : "memory");
                 }
-                // (the peers' mail is read after a wait that acquires at cluster scope)
                 if (MODE == FWD) {      // the other warps go on to the next row
                     if (warp == 0) {
-                        ok = __all_sync(0xFFFFFFFFu, ok && mbar_wait_cluster(xbar(b), buf_phase, p, abort_flag));
+                        ok = __all_sync(0xFFFFFFFFu, ok && wait_mail(b, buf_phase));
                         if (rank == 0 && lane == 0 && ok)
                             write_loss<TAIL>(p, row, te, view_of<TAIL>(p, gather_mail(b)), gather_again(b));
                         __syncwarp();
@@ -797,7 +813,7 @@ __global__ void __launch_bounds__(32 * W + 32, W == 8 ? 3 : 10) k_distill(const 
                     }
                 } else {
                     if (!TAIL) ok = ok && mbar_wait(tfull(b), buf_phase, p, abort_flag);
-                    ok = ok && mbar_wait_cluster(xbar(b), buf_phase, p, abort_flag);
+                    ok = ok && wait_mail(b, buf_phase);
                     view = view_of<TAIL>(p, gather_mail(b));
                     if (rank == 0 && threadIdx.x == 0 && ok) write_loss<TAIL>(p, row, te, view, gather_again(b));
                 }
@@ -897,7 +913,7 @@ __global__ void __launch_bounds__(32, kWarpPerSm) k_distill_warp(const Params p)
             slope.kept(p, pt, sm, 0, lane, 32);
         }
         __syncwarp();
-        clear_bits<T>(p, sm, 0, pt, lane);
+        if (by_bits<MODE, TAIL>(p)) clear_bits<T>(p, sm, 0, pt, lane);
     }
     wait_group(0);
 }

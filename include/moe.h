@@ -1068,8 +1068,8 @@ MOE_API moe_status_t grouped_ffn_bwd(const void* dh, int64_t lddh, const void* a
  * masked token.  An idx of V or more is taken as not kept and puts
  * MOE_ERR_BAD_INDEX in err.  A token that occurs several times in a row has the sum
  * of its probabilities, in the loss as in the gradient.  Terms with p = 0 are 0; a rest without student tokens
- * of any probability (q_rest below e^-700: all are -inf or of the type's lowest value, or
- * as good as that) is dropped.  dloss = 0 gives a gradient of zeros whatever
+ * of any probability (all of them more than 700 tau below max x, such as -inf or the
+ * type's lowest value) is dropped.  dloss = 0 gives a gradient of zeros whatever
  * the row's logits are.  Infinities and NaN otherwise show in the results as the
  * formulas have them.
  *   x      x_type, any row stride and element-aligned address (16-byte units
@@ -1079,9 +1079,9 @@ MOE_API moe_status_t grouped_ffn_bwd(const void* dh, int64_t lddh, const void* a
  *   loss [M], dloss [M] fp32 (dloss: gradient of the row's loss, a row's weight).
  *   stats [M, 3] fp32: what the backward pass needs of the forward pass: max x, and
  *          sums of exp((x - max x) / tau) over all tokens and over those not kept
- *          (all, without teacher_lse).  Where q_rest is below e^-40: tau times the
- *          log-sum-exp of x / tau, minus the sum over those not kept relative to
- *          their own maximum, and that maximum.
+ *          (all, without teacher_lse).  Where those not kept are more than 50 tau
+ *          below max x: tau times the log-sum-exp of x / tau, minus the sum over
+ *          those not kept relative to their own maximum, and that maximum.
  *   tau    1e-6 .. 1e6.  V up to 720,882 (bf16), 360,442 (fp32).
  * All sums are fp32.  distill_loss_fwd writes loss and stats, those that are
  * not NULL; distill_loss_bwd dx from stats; distill_loss loss (may be NULL) and dx
