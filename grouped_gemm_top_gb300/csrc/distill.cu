@@ -27,7 +27,7 @@
 // another's loads.  (Bulk copies by one thread were no faster.)  Warp W works on
 // the teacher's tokens a row ahead.  All waits are bounded.
 // Bound by the memory for large vocabularies (a plain copy 6.8 TB/s): 8,192 x 129,280 bf16
-// loss 322 us (6.6 TB/s), loss and gradient 734 us (5.8; 58 % of the issue slots, the rest of
+// loss 322 us (6.6 TB/s), loss and gradient 733 us (5.8; 62 % of the issue slots, the rest of
 // the gap is the chain of a row's sums through the cluster, three CTAs an SM in turn),
 // gradient of 2,048 rows 172 us (6.2), loss of 4,099 x 50,257 fp32 137 us (6.0); by that chain
 // for small ones; 5.5 us for 4 x 32,000.
@@ -853,7 +853,7 @@ __global__ void __launch_bounds__(32 * W + 32, W == 8 ? 3 : 10) k_distill(const 
 // Small vocabularies: one warp does all of a row, the next row's logits on
 // their way meanwhile, and up to 28 rows are under way on an SM.  The chain of a
 // row's sums, which bounds them, has no barrier in it (16,384 x 1,000 bf16, loss and
-// gradient: 29 us, 54 by three warps with 10 rows an SM; 2,500 columns 58 and 75).
+// gradient: 27 us, 54 by three warps with 10 rows an SM; 2,500 columns 56 and 75).
 constexpr int kWarpPerSm = 28;
 template <typename T, int MODE, bool TAIL>
 __global__ void __launch_bounds__(32, kWarpPerSm) k_distill_warp(const Params p) {
@@ -1013,13 +1013,15 @@ static bool warps_do(int64_t M, int V, bool f32, int sms) {
 
 // How a call is spread: CTAs of a cluster (they share a row), 288 threads each
 // or, for small parts, 96, of which three times as many rows are under way on
-// an SM (16,384 x 4,096 bf16, loss and gradient: 80 us, 149 with 288; 8,000 columns 107
-// and 179, 16,000 240 and 231), and clusters, no more than run at a time, so that rows are
+// an SM (16,384 x 4,096 bf16, loss and gradient: 75 us, 149 with 288; 8,000 columns 103
+// and 179, 16,000 240 and 229), and clusters, no more than run at a time, so that rows are
 // dealt out evenly.  Of the sizes of clusters the one with the shortest
 // time by this count, in ns: a 16-byte unit takes an SM 0.36 to read at the
 // memory's rate and as much to write, shared by its CTAs (one alone gets no more
 // than half of it), and a row 700 besides for the chain of its sums (800 more where they
-// go through the cluster), 600 for the gradient alone.
+// go through the cluster), 600 for the gradient alone.  The count ranks the
+// sizes; where a row's chain is not covered it is below what is measured (loss and
+// gradient of 16,384 rows: 8,000 columns 87 and 103 us, 16,000 181 and 229).
 struct Spread {
     int C, part, chunk, held, per_sm;
     bool wide;

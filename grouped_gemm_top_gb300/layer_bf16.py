@@ -6,7 +6,10 @@ groups' real rows out of the padded layout:
     y_perm = h W2,         out = combine(y_perm)
 
 For fine-tuning and for teachers in 16 bits, and as a reference for the MXFP8
-layer.  Same buffers and calls as MoELayer where they mean the same; the step
+layer.  Buffers and calls that it has in common with MoELayer mean the same; it
+has no shared experts, row capacity of its own or steps from host inputs, its gate
+is silu, and the forward pass always keeps what the backward pass needs (for
+decoding call ops.grouped_ffn_fwd and grouped_linear_fwd themselves).  The step
 allocates nothing, never synchronises and can be captured in a CUDA graph.  The
 weights are read where they lie: nothing is derived from them."""
 from __future__ import annotations
