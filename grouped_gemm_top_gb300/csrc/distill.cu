@@ -668,9 +668,7 @@ __global__ void __launch_bounds__(32 * W + 32, W == 8 ? 3 : 10) k_distill(const 
         return sum;
     };
     // (what peers sent is read behind a wait that acquires at cluster scope)
-    auto wait_mail = [&](int b, uint32_t phase) {
-        return C > 1 ? mbar_wait_cluster(xbar(b), phase, p, abort_flag) : mbar_wait(xbar(b), phase, p, abort_flag);
-    };
+    auto wait_mail = [&](int b, uint32_t phase) { return mbar_wait_cluster(xbar(b), phase, p, abort_flag); };
     if (warp == W) {
         // ---------------------------------------------- teacher, a row ahead ----
         const bool bits = by_bits<MODE, TAIL>(p);
@@ -1013,7 +1011,7 @@ static bool warps_do(int64_t M, int V, bool f32, int sms) {
 
 // How a call is spread: CTAs of a cluster (they share a row), 288 threads each
 // or, for small parts, 96, of which three times as many rows are under way on
-// an SM (16,384 x 4,096 bf16, loss and gradient: 75 us, 149 with 288; 8,000 columns 103
+// an SM (16,384 x 4,096 bf16, loss and gradient: 75 us, 149 with 288; 8,000 columns 101
 // and 179, 16,000 240 and 229), and clusters, no more than run at a time, so that rows are
 // dealt out evenly.  Of the sizes of clusters the one with the shortest
 // time by this count, in ns: a 16-byte unit takes an SM 0.36 to read at the
@@ -1021,7 +1019,7 @@ static bool warps_do(int64_t M, int V, bool f32, int sms) {
 // than half of it), and a row 700 besides for the chain of its sums (800 more where they
 // go through the cluster), 600 for the gradient alone.  The count ranks the
 // sizes; where a row's chain is not covered it is below what is measured (loss and
-// gradient of 16,384 rows: 8,000 columns 87 and 103 us, 16,000 181 and 229).
+// gradient of 16,384 rows: 8,000 columns 87 and 101 us, 16,000 181 and 229).
 struct Spread {
     int C, part, chunk, held, per_sm;
     bool wide;
